@@ -35,6 +35,14 @@ class Params(ctypes.Structure):
 
 PP = ctypes.POINTER(Params)
 
+
+class Pages(ctypes.Structure):
+    _fields_ = [("pool", P), ("layer_bytes", I64), ("table", P), ("ref", P)] + [
+        (n, ctypes.c_int) for n in ("layers", "n_pages", "page_size", "max_seqs", "max_pages")]
+
+
+GP = ctypes.POINTER(Pages)
+
 SIGNATURES = {
     "csa2_default_params": (None, [PP]),
     "csa2_version": (I32, []),
@@ -57,6 +65,15 @@ SIGNATURES = {
     "csa2_sparse_attn_layers_part": (I32, [PP, I32, I32, I32, I32, P, P, P, P, P, P, P, P, P, P]),
     "csa2_sparse_attn_layers_split": (I32, [PP, I32, I32, P, P, P, P, P, P, P, P, P, SZ, P, P]),
     "csa2_sparse_attn_layers_split_workspace_size": (SZ, [PP, I32, I32]),
+    "csa2_rope": (I32, [PP, I32, I32, I64, I32, I32, I32, I32, P, I64, I64, P, I64, I64, P, P]),
+    "csa2_page_workspace_size": (SZ, [GP]),
+    "csa2_page_reserve": (I32, [PP, GP, I32, P, P, P, P, SZ, P, P]),
+    "csa2_page_release": (I32, [PP, GP, I32, P, P, I32, I32, P, P]),
+    "csa2_page_fork": (I32, [PP, GP, I32, P, P, P, P, SZ, P, P]),
+    "csa2_page_compact": (I32, [PP, GP, P, P, SZ, P, P]),
+    "csa2_page_write": (I32, [PP, GP, I32, I64, P, I32, I64, P, P, P, P]),
+    "csa2_paged_attn_workspace_size": (SZ, [PP, GP, I32]),
+    "csa2_paged_attn": (I32, [PP, GP, I32, I32, P, I64, I64, P, P, P, I32, I32, P, P, SZ, P, P]),
     "csa2_fp4_mma_peak": (I32, [I32, I32, P, P]),
 }
 

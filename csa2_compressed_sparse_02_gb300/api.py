@@ -17,10 +17,11 @@ from dataclasses import dataclass
 
 import torch
 
-from ._lib import Csa2Error, Params, check, lib  # noqa: F401
+from ._lib import Csa2Error, Pages, Params, check, lib  # noqa: F401
 
 F32, NVFP4, E4M3, BF16 = 0, 1, 2, 3
 WIN_RING, WIN_LINEAR = 0, 1
+ROPE_PAIRS, ROPE_HALF = 0, 1
 D, H, HI, DI, W, BLK, KB, KP = 512, 64, 32, 128, 128, 8, 2048, 512
 KEY_TILE, KEY_TILE_BYTES = 128, 9216
 
@@ -206,6 +207,170 @@ def sparse_attn_noalloc(params, q, sink, win_ptrs, n_tokens, comp_ptrs, comp_sca
         _stream(stream)), "sparse_attn_noalloc")
 
 
+# --------------------------------------------------------------------------- paged cache
+# These calls check what the pointers stand for (types, shapes, devices, strides) before
+# they hand them on; everything else is checked by the library.
+_FORMATS = {torch.bfloat16: BF16, torch.float32: F32}
+
+
+def _fail(what):
+    raise Csa2Error(what)
+
+
+def _on(device, **tensors):
+    """All tensors on `device`, which is made the current one by the caller's `with`."""
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            _fail("%s is on %s, the call's other tensors on %s" % (name, t.device, device))
+
+
+def _i32(name, t, n):
+    if t.dtype != torch.int32 or t.dim() != 1 or t.numel() != n or not (n <= 1 or t.stride(0) == 1):
+        _fail("%s must be a contiguous int32 tensor of %d elements" % (name, n))
+    return t.data_ptr()
+
+
+def _status(t):
+    if t is None:
+        return None
+    if t.dtype != torch.int32 or t.numel() < 1:
+        _fail("dev_status must be an int32 tensor")
+    return t.data_ptr()
+
+
+class _Call:
+    """The device of a call's tensors as the current one, and the stream it runs on."""
+
+    def __init__(self, device, stream):
+        if device.type != "cuda":
+            _fail("expected a CUDA tensor")
+        self.index, self.stream, self.back = device.index, stream, None
+
+    def __enter__(self):
+        now = torch.cuda.current_device()
+        if now != self.index:
+            self.back = now
+            torch.cuda.set_device(self.index)
+        s = torch.cuda.current_stream() if self.stream is None else self.stream
+        return s.cuda_stream
+
+    def __exit__(self, *exc):
+        if self.back is not None:
+            torch.cuda.set_device(self.back)
+
+
+def rope(params, x, pos, out=None, layout=ROPE_PAIRS, first=-1, inverse=False, stream=None):
+    """Rotary embedding (csa2_rope): x [N, heads, channels] bf16 or fp32 with contiguous
+    channels, pos [N] int32; out as x (None: a new tensor; x itself: in place).
+    inverse=True turns back, which is also the gradient of the call. Returns out."""
+    if x.dim() != 3 or x.dtype not in _FORMATS:
+        _fail("rope: x must be [N, heads, channels], bf16 or fp32")
+    if out is None:
+        out = torch.empty_like(x, memory_format=torch.contiguous_format)
+    if out.shape != x.shape or out.dtype != x.dtype:
+        _fail("rope: out must have x's shape and type")
+    N, heads, ch = x.shape
+    if N == 0 or heads == 0:
+        return out
+    xs, os_ = x.stride(), out.stride()
+    if (xs[2] != 1 or os_[2] != 1) and ch > 1:
+        _fail("rope: the channels of x and out must be contiguous")
+    _on(x.device, out=out, pos=pos)
+    with _Call(x.device, stream) as s:
+        check(lib().csa2_rope(ctypes.byref(params), layout, int(inverse), N, heads, ch, first,
+                              _FORMATS[x.dtype], x.data_ptr(), xs[0], xs[1], out.data_ptr(), os_[0],
+                              os_[1], _i32("pos", pos, N), s), "rope")
+    return out
+
+
+def page_reserve(params, cache, seq, n_from, n_to, dev_status=None, stream=None):
+    """Give sequences seq [N] the pages of positions n_from .. n_to-1 (csa2_page_reserve)."""
+    N, ws = seq.numel(), cache.workspace
+    _on(cache.device, seq=seq, n_from=n_from, n_to=n_to, dev_status=dev_status)
+    with _Call(cache.device, stream) as s:
+        check(lib().csa2_page_reserve(
+            ctypes.byref(params), cache.ref_c, N, _i32("seq", seq, N), _i32("n_from", n_from, N),
+            _i32("n_to", n_to, N), ws.data_ptr(), ws.numel(), _status(dev_status), s), "page_reserve")
+
+
+def page_release(params, cache, seq, n_tokens=None, window=0, n_first=0, dev_status=None, stream=None):
+    """Let go of every page of sequences seq [N], or with n_tokens [N] of those that no later
+    token sees through window and n_first (csa2_page_release)."""
+    N = seq.numel()
+    _on(cache.device, seq=seq, n_tokens=n_tokens, dev_status=dev_status)
+    with _Call(cache.device, stream) as s:
+        check(lib().csa2_page_release(
+            ctypes.byref(params), cache.ref_c, N, _i32("seq", seq, N),
+            None if n_tokens is None else _i32("n_tokens", n_tokens, N), window, n_first,
+            _status(dev_status), s), "page_release")
+
+
+def page_fork(params, cache, parent, child, n_tokens, dev_status=None, stream=None):
+    """child[i] continues the first n_tokens[i] positions of parent[i] (csa2_page_fork)."""
+    N, ws = child.numel(), cache.workspace
+    _on(cache.device, parent=parent, child=child, n_tokens=n_tokens, dev_status=dev_status)
+    with _Call(cache.device, stream) as s:
+        check(lib().csa2_page_fork(
+            ctypes.byref(params), cache.ref_c, N, _i32("parent", parent, N), _i32("child", child, N),
+            _i32("n_tokens", n_tokens, N), ws.data_ptr(), ws.numel(), _status(dev_status), s), "page_fork")
+
+
+def page_compact(params, cache, n_used=None, dev_status=None, stream=None):
+    """Move the used pages to the front of the pool (csa2_page_compact); n_used [1] int32
+    receives their number."""
+    ws = cache.workspace
+    _on(cache.device, n_used=n_used, dev_status=dev_status)
+    with _Call(cache.device, stream) as s:
+        check(lib().csa2_page_compact(
+            ctypes.byref(params), cache.ref_c, None if n_used is None else _i32("n_used", n_used, 1),
+            ws.data_ptr(), ws.numel(), _status(dev_status), s), "page_compact")
+
+
+def page_write(params, cache, layer, x, seq, pos, dev_status=None, stream=None):
+    """Write rows x [N, 512] (fp32 or bf16) as positions pos [N] of sequences seq [N]
+    (csa2_page_write), turned first when params.rope_dim > 0."""
+    if x.dim() != 2 or x.shape[1] != D or x.dtype not in _FORMATS or x.stride(1) != 1:
+        _fail("page_write: x must be [N, %d], bf16 or fp32, with contiguous rows" % D)
+    N = x.shape[0]
+    _on(cache.device, x=x, seq=seq, pos=pos, dev_status=dev_status)
+    with _Call(cache.device, stream) as s:
+        check(lib().csa2_page_write(
+            ctypes.byref(params), cache.ref_c, layer, N, x.data_ptr(), _FORMATS[x.dtype], x.stride(0),
+            _i32("seq", seq, N), _i32("pos", pos, N), _status(dev_status), s), "page_write")
+
+
+def paged_attn_workspace(params, cache, B):
+    """Workspace tensor of paged_attn for batches of up to B sequences."""
+    with _Call(cache.device, None):
+        n = lib().csa2_paged_attn_workspace_size(ctypes.byref(params), cache.ref_c, B)
+    return torch.empty(max(int(n), 256), dtype=torch.uint8, device=cache.device)
+
+
+def paged_attn(params, cache, layer, q, sink, seq, n_tokens, out, workspace, window=0, n_first=0,
+               dev_status=None, stream=None):
+    """Attention of one new token per sequence over a layer's pages (csa2_paged_attn):
+    q [B, heads, 512] bf16 with contiguous channels, sink [heads] fp32 or None, seq [B] int32
+    or None (row b of the table), n_tokens [B] int32, out [B, heads, 512] bf16. A window of 0
+    sees everything; n_first positions stay visible before it."""
+    if q.dim() != 3 or q.dtype != torch.bfloat16 or q.shape[2] != D or q.stride(2) != 1:
+        _fail("paged_attn: q must be [B, heads, %d] bf16 with contiguous channels" % D)
+    B, heads = q.shape[0], q.shape[1]
+    if heads != params.heads:
+        _fail("paged_attn: q has %d heads, the parameters say %d" % (heads, params.heads))
+    if out.shape != q.shape or out.dtype != torch.bfloat16 or not out.is_contiguous():
+        _fail("paged_attn: out must be contiguous bf16 of q's shape")
+    if sink is not None and (sink.dtype != torch.float32 or sink.numel() != heads or not sink.is_contiguous()):
+        _fail("paged_attn: sink must be %d contiguous fp32 values" % heads)
+    _on(cache.device, q=q, sink=sink, seq=seq, n_tokens=n_tokens, out=out, workspace=workspace,
+        dev_status=dev_status)
+    with _Call(cache.device, stream) as s:
+        check(lib().csa2_paged_attn(
+            ctypes.byref(params), cache.ref_c, layer, B, q.data_ptr(), q.stride(0), q.stride(1),
+            None if sink is None else sink.data_ptr(), None if seq is None else _i32("seq", seq, B),
+            _i32("n_tokens", n_tokens, B), window, n_first, out.data_ptr(), workspace.data_ptr(),
+            workspace.numel() * workspace.element_size(), _status(dev_status), s), "paged_attn")
+
+
 def fp4_mma_peak(ctas, iters, dev_status=None, stream=None):
     """Enqueue the FP4 tensor-core rate measurement (csa2_fp4_mma_peak): ctas x iters
     MMA pairs of 2 x 128 x 128 x 128 flop each. The caller times it."""
@@ -284,6 +449,43 @@ class IndexKeyCache:
         p0 = torch.tensor([pos0], dtype=torch.int64, device=self.device)
         index_keys_write(params, vals[None], scales[None], p0, self.ptrs[b:b + 1],
                          self.cap[b:b + 1], dev_status, stream)
+
+
+class PagedCache:
+    """A cache in pages (csa2_pages): the pool of `layers` layers, the page table and the
+    counts, allocated here from sizes, or the caller's own tensors. pool [layers, n_pages,
+    page_size, 512] of bf16 or float8_e4m3fn (params.kv_format), table [max_seqs, max_pages]
+    and ref [n_pages] int32; a page of a layer is contiguous. Holds the scratch of the page
+    calls too, so calls on one cache are ordered: one stream, or events between streams."""
+
+    def __init__(self, params, n_pages=0, page_size=0, max_seqs=0, max_pages=0, layers=1,
+                 device="cuda", pool=None, table=None, ref=None):
+        types = {BF16: torch.bfloat16, E4M3: torch.float8_e4m3fn}
+        if params.kv_format not in types:
+            _fail("PagedCache: pages hold BF16 or E4M3 rows")
+        dt = types[params.kv_format]
+        if pool is None:
+            pool = torch.zeros(layers, n_pages, page_size, D, dtype=torch.int8 if dt.itemsize == 1
+                               else torch.int16, device=device).view(dt)
+        if table is None:
+            table = torch.full((max_seqs, max_pages), -1, dtype=torch.int32, device=pool.device)
+        if ref is None:
+            ref = torch.zeros(pool.shape[1], dtype=torch.int32, device=pool.device)
+        if pool.dim() != 4 or pool.shape[3] != D or pool.dtype != dt or (
+                pool.stride()[1:] != (pool.shape[2] * D, D, 1)):
+            _fail("PagedCache: pool must be [layers, n_pages, page_size, %d] of %s with contiguous layers" % (D, dt))
+        if table.dim() != 2 or table.dtype != torch.int32 or not table.is_contiguous():
+            _fail("PagedCache: table must be contiguous int32 [max_seqs, max_pages]")
+        _i32("ref", ref, pool.shape[1])
+        self.device = pool.device
+        _on(self.device, table=table, ref=ref)
+        self.pool, self.table, self.ref = pool, table, ref
+        self.c = Pages(pool.data_ptr(), pool.stride(0) * pool.element_size(), table.data_ptr(),
+                       ref.data_ptr(), pool.shape[0], pool.shape[1], pool.shape[2], table.shape[0],
+                       table.shape[1])
+        self.ref_c = ctypes.byref(self.c)
+        n = lib().csa2_page_workspace_size(self.ref_c)
+        self.workspace = torch.empty(max(int(n), 256), dtype=torch.uint8, device=self.device)
 
 
 def n_blocks(n: int) -> int:

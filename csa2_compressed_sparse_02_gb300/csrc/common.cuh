@@ -55,6 +55,9 @@ cudaError_t preload_select();
 cudaError_t preload_attn();
 cudaError_t preload_attn_tc();
 cudaError_t preload_peak();
+cudaError_t preload_rope();
+cudaError_t preload_pages();
+cudaError_t preload_paged_attn();
 
 // Single-layer sparse attention (csa2_sparse_attn, quantised formats) on the
 // tcgen05 kernel of sparse_attn_tc.cu with the even split schedule; the

@@ -61,6 +61,7 @@ extern "C" {
 #define CSA2_DEV_BAD_LENGTH 2  /* a sequence length beyond the stated capacity, or < 0 */
 #define CSA2_DEV_TIMEOUT 4     /* a pipeline wait gave up (the kernel returned early) */
 #define CSA2_DEV_BAD_ALIGN 8   /* a per-sequence buffer base is misaligned (its rows read as empty) */
+#define CSA2_DEV_NO_PAGE 16    /* the pool has no free page left: the entry stays -1 */
 
 /* ---- formats ---- */
 #define CSA2_F32 0   /* fp32 */
@@ -503,6 +504,159 @@ int csa2_sparse_attn_noalloc(const csa2_params* p, int B,
                              const void* const* comp, const uint8_t* const* comp_scales,
                              const int32_t* idx, void* out,
                              int32_t* dev_status, void* stream);
+
+/*
+ * csa2_rope — rotary embedding of N rows x heads (queries and window tokens before the
+ * path, outputs after it: K = V carries the rotation, so an output is turned back by its
+ * own position). The frequencies are those of csa2_params (rope_dim, rope_theta and the
+ * YaRN settings; rope_factor 1 is the plain embedding, and betas above every pair's turns
+ * divide all positions by the factor). Channels first .. first + rope_dim - 1 of each head
+ * turn by angle pos[n] * theta_i:
+ *   (a, b) -> (a cos - b sin, a sin + b cos), inverse != 0: by minus the angle, which is
+ *   also the gradient (dx = the inverse of dy);
+ *   CSA2_ROPE_PAIRS: a, b = channels first + 2i, first + 2i + 1;
+ *   CSA2_ROPE_HALF:  a, b = channels first + i, first + rope_dim/2 + i.
+ * The other channels are copied. Angles are reduced in fp64; sines, cosines and the
+ * products are fp32, rounded once to the output's type.
+ *   x, out  format CSA2_BF16 or CSA2_F32; element (n, h, c) at n*row + h*head + c (strides
+ *           in elements; the channels are contiguous). out may be x itself (same strides:
+ *           only the rotated channels are touched) and must not overlap it otherwise.
+ *   pos     [N] int32, device; a row with pos < 0 (padding) is left as it is in out.
+ *   first   first rotated channel, or -1 for the last rope_dim channels.
+ * Constraints: 2 <= rope_dim <= 512, even, first + rope_dim <= head_dim <= 4096; heads <= 4096.
+ */
+#define CSA2_ROPE_PAIRS 0
+#define CSA2_ROPE_HALF 1
+int csa2_rope(const csa2_params* p, int layout, int inverse, int64_t N, int heads, int head_dim,
+              int first, int format, const void* x, int64_t x_row, int64_t x_head,
+              void* out, int64_t out_row, int64_t out_head, const int32_t* pos, void* stream);
+
+/*
+ * A cache in pages: latents of `layers` layers for up to max_seqs sequences, with one page
+ * table for all layers. Position t of sequence s is row t % page_size of page
+ * table[s][t / page_size]; layer l's page g starts at pool + l*layer_bytes +
+ * g*page_size*row bytes, its rows follow each other. A row is D bf16 (p->kv_format
+ * CSA2_BF16, 1024 bytes) or D E4M3 values (CSA2_E4M3, 512 bytes).
+ * ref[g] counts the table entries that hold page g: 0 = free, above 1 = shared. Every
+ * device array belongs to the caller, who starts with ref all 0 and table all -1.
+ * The calls below change table and ref; on one cache they must be ordered (one stream or
+ * events), with each other and with the calls that read it.
+ */
+typedef struct csa2_pages {
+    void* pool;          /* device, 16-byte aligned */
+    int64_t layer_bytes; /* multiple of 16, at least n_pages*page_size*row bytes */
+    int32_t* table;      /* [max_seqs, max_pages] int32, device: page of each page_size positions, -1 = none */
+    int32_t* ref;        /* [n_pages] int32, device, 16-byte aligned */
+    int layers;
+    int n_pages;
+    int page_size;       /* positions a page holds: a multiple of 8, 8 .. 1024 */
+    int max_seqs;
+    int max_pages;       /* pages a sequence can hold */
+} csa2_pages;
+
+/* Bytes of scratch csa2_page_reserve, _fork and _compact need (contents arbitrary,
+ * 256-byte aligned; calls that share it are ordered as those on the cache are). */
+size_t csa2_page_workspace_size(const csa2_pages* c);
+
+/*
+ * csa2_page_reserve — give N sequences the pages of positions n_from[i] .. n_to[i]-1
+ * that their tables lack. Entries are filled in the order of (i, position), each with the
+ * lowest-numbered free page; entries that hold a page keep it. When no page is left the
+ * entry stays -1 and CSA2_DEV_NO_PAGE is set.
+ *   seq, n_from, n_to [N] int32, device. seq[i] < 0 skips i. A sequence past max_seqs or
+ *   listed before sets CSA2_DEV_BAD_INDEX, a length below 0 or beyond max_pages pages
+ *   CSA2_DEV_BAD_LENGTH, and i is skipped. N <= max(max_seqs, 1024).
+ */
+int csa2_page_reserve(const csa2_params* p, const csa2_pages* c, int N, const int32_t* seq,
+                      const int32_t* n_from, const int32_t* n_to, void* workspace, size_t ws_bytes,
+                      int32_t* dev_status, void* stream);
+
+/*
+ * csa2_page_release — let go of pages of N sequences: their entries become -1 and the
+ * pages' counts fall by one (a page with count 0 is free).
+ *   n_tokens NULL: every page. Else the pages that no later token of a sequence with
+ *   n_tokens[i] positions sees through `window` and `n_first` (csa2_paged_attn): those
+ *   wholly within [n_first, n_tokens[i] - window).
+ *   seq as in csa2_page_reserve (a sequence listed twice is released once).
+ */
+int csa2_page_release(const csa2_params* p, const csa2_pages* c, int N, const int32_t* seq,
+                      const int32_t* n_tokens, int window, int n_first, int32_t* dev_status,
+                      void* stream);
+
+/*
+ * csa2_page_fork — sequence child[i] continues the first n_tokens[i] positions of
+ * parent[i]: it shares the parent's full pages (their counts rise by one) and gets its own
+ * copy of the rows in the page that is only partly filled, in every layer. That page is the
+ * lowest-numbered free one, in the order of i; without one its entry is -1
+ * (CSA2_DEV_NO_PAGE). The rest of the child's row becomes -1. Pages that the child's row
+ * held before lose one count after the new pages are taken.
+ *   parent, child, n_tokens [N] int32, device; a parent may appear often. A child that
+ *   appears twice or is a parent too, or a sequence out of range, sets
+ *   CSA2_DEV_BAD_INDEX; n_tokens[i] outside [0, max_pages*page_size] CSA2_DEV_BAD_LENGTH;
+ *   that fork is skipped. child[i] < 0 skips i. N <= max(max_seqs, 1024), at most 65535.
+ */
+int csa2_page_fork(const csa2_params* p, const csa2_pages* c, int N, const int32_t* parent,
+                   const int32_t* child, const int32_t* n_tokens, void* workspace,
+                   size_t ws_bytes, int32_t* dev_status, void* stream);
+
+/*
+ * csa2_page_compact — move the pages in use into the first pages of the pool: with n of
+ * them, the i-th used page at or above n goes to the i-th free page below n, in every
+ * layer, and tables and counts follow. Afterwards pages n .. n_pages-1 are free and their
+ * memory can be given back.
+ *   n_used [1] int32 out, device: n (may be NULL). Table entries that name no page of the
+ *   pool are left and set CSA2_DEV_BAD_INDEX.
+ */
+int csa2_page_compact(const csa2_params* p, const csa2_pages* c, int32_t* n_used, void* workspace,
+                      size_t ws_bytes, int32_t* dev_status, void* stream);
+
+/*
+ * csa2_page_write — write N rows into one layer's pages: row i is position pos[i] of
+ * sequence seq[i]. With p->rope_dim > 0 its last rope_dim channels are turned first, in
+ * adjacent pairs, by the angles of pos[i] (csa2_rope's arithmetic). Values are rounded to
+ * nearest even (E4M3: saturating, as the window's).
+ *   x [N, D], x_format CSA2_F32 or CSA2_BF16, rows x_row elements apart.
+ *   seq, pos [N] int32, device. seq[i] < 0 is padding and skipped. A position past
+ *   max_pages pages (or < 0) sets CSA2_DEV_BAD_LENGTH, a sequence out of range or an entry
+ *   without a page CSA2_DEV_BAD_INDEX; the row is skipped. Rows of one call must go to
+ *   different places, and not into a shared page (reserve and fork hand out none).
+ * Constraints: D == 512; rope_dim a multiple of 4; x 16-byte aligned, x_row*size too.
+ */
+int csa2_page_write(const csa2_params* p, const csa2_pages* c, int layer, int64_t N,
+                    const void* x, int x_format, int64_t x_row, const int32_t* seq,
+                    const int32_t* pos, int32_t* dev_status, void* stream);
+
+/* Bytes of scratch csa2_paged_attn needs for B queries on the current device. */
+size_t csa2_paged_attn_workspace_size(const csa2_params* p, const csa2_pages* c, int B);
+
+/*
+ * csa2_paged_attn — dense attention of one new token per sequence over one layer's pages,
+ * with K = V = the stored latent and a sink logit in the denominator as in
+ * csa2_sparse_attn. The query of a sequence with T = n_tokens[b] positions (its own row
+ * among them) sees position t < T if window <= 0, t >= T - window or t < n_first:
+ *   z_t = softmax_scale * q_h . k_t;  o_h = sum_t e^{z_t} k_t / (e^{sink_h} + sum_t e^{z_t}).
+ * A sequence that sees nothing gets zeros. Rows and pages that are not seen are not used,
+ * whatever they hold; their table entries may be -1.
+ *   q    element (b, h, c) at b*q_seq + h*q_head + c, bf16, strides in elements (multiples
+ *        of 8);  out [B, heads, D] bf16, contiguous;  both 16-byte aligned
+ *   sink [heads] fp32, or NULL for none (all -infinity)
+ *   seq  [B] int32, device: the sequences' rows of the table (NULL: row b); the same one
+ *        may appear often. seq[b] < 0 is padding: its output is left as it is.
+ *   n_tokens [B] int32, device
+ *   A length below 0 or beyond max_pages pages sets CSA2_DEV_BAD_LENGTH (nothing, or the
+ *   first max_pages pages are seen), a sequence out of range (nothing is seen) or a seen
+ *   position without a page (not seen) CSA2_DEV_BAD_INDEX.
+ *   workspace: csa2_paged_attn_workspace_size bytes, 256-byte aligned, contents
+ *   arbitrary; calls that share it must be ordered (one stream or events).
+ * The (sequence, 128 positions) tiles of the batch are cut into one range of equal length
+ * per CTA (one per SM, or p->max_ctas); a second kernel joins the sequences that were cut,
+ * in the order of their positions, so results do not vary from run to run.
+ * Constraints: 1 <= heads <= 64, D == 512, kv_format BF16 or E4M3, q_format BF16, B <= 65535.
+ */
+int csa2_paged_attn(const csa2_params* p, const csa2_pages* c, int layer, int B,
+                    const void* q, int64_t q_seq, int64_t q_head, const float* sink,
+                    const int32_t* seq, const int32_t* n_tokens, int window, int n_first,
+                    void* out, void* workspace, size_t ws_bytes, int32_t* dev_status, void* stream);
 
 /*
  * csa2_fp4_mma_peak — measurement aid, no counterpart in the pages: the rate of
