@@ -7,6 +7,8 @@
 // A sequence within one range is finished there; one that ranges cut leaves a partial result
 // per piece (unnormalised O, running maximum m and sum l of each head), and k_paged_join
 // joins them in order: o = sum_i O_i 2^{m_i - M} / (2^{sink - M} + sum_i l_i 2^{m_i - M}).
+#include <cuda.h>
+
 #include <climits>
 
 #include "pages.cuh"
@@ -35,6 +37,7 @@ struct Args {
     int32_t* dev_status;
     float scale_log2;
     int ctas;         // of the attention kernel (the join needs its ranges)
+    int box_rows;     // rows of a copied box: divides 128 and the page size
 };
 
 __host__ __device__ inline int64_t part_floats(int heads) { return (int64_t)heads * (kD + 2); }
@@ -142,126 +145,596 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
-// ---------------------------------------------------------------- one CTA's pieces
-constexpr int kThreads = 256;
-constexpr int kStep = 16;  // positions taken at a time
-struct Shared {
-    float kv[kStep][kD + 1];
-    float z[kMaxHeads][kStep];
-    Range range;
+// ---------------------------------------------------------------- shapes
+// kBf16: bf16 pages, the products in bf16; else E4M3 pages, decoded (exactly) into f16.
+// NH: the heads, rounded up to the 16, 32 or 64 columns of the MMAs.
+template <bool kBf16, int NH>
+struct Shape {
+    static constexpr int kSoftWarps = kBf16 && NH >= 32 ? 16 : 8;
+    static constexpr int kGroups = kSoftWarps / 4;  // of heads: one per four lane quarters
+    static constexpr int NC = NH / kGroups;         // heads of a softmax warp
+    static constexpr int kMmaWarp = kSoftWarps;
+    static constexpr int kProd0 = kSoftWarps + 1;   // first producer warp
+    static constexpr int kProdWarps = kBf16 ? 4 : 8;
+    static constexpr int kQueryWarps = kBf16 ? 3 : 8;  // of them, those that stage the query
+    static constexpr int kThreads = 32 * (kProd0 + kProdWarps);
+    // Pairs of 64-channel chunks of a tile in the ring: a tile has 4; what the query leaves
+    // of shared memory lets the next tile's first pairs arrive early.
+    static constexpr int kPairs = NH == 64 ? 4 : NH == 32 ? 5 : 6;
+    static constexpr uint32_t kColS = 4 * NH;  // TMEM: O^T 4 x NH columns, then S^T
+    static constexpr uint32_t kFmt = kBf16 ? 1u : 0u;
+    // D fp32, A and B bf16 or f16, N = NH, M = 128; S: both K-major; PV: A MN-major
+    static constexpr uint32_t kIdescS =
+        (1u << 4) | (kFmt << 7) | (kFmt << 10) | ((uint32_t)(NH >> 3) << 17) | ((128u >> 4) << 24);
+    static constexpr uint32_t kIdescPV = kIdescS | (1u << 15);
 };
 
-__device__ __forceinline__ float e4m3_at(const uint8_t* p) { return e4m3_value(*p); }
-
+constexpr uint32_t kChunk = 128 * 128;  // 128 positions x 64 channels of 16 bits, 128-byte swizzle
+constexpr uint32_t kTmemCols = 512;     // one CTA an SM (shared memory), so it takes them all
+constexpr float kLazyMax = 8.0f;        // log2 of the largest P before the maximum moves
+// P = 2^(x - m + kLift): f16 holds small P as multiples of 2^-24, so they are lifted as far
+// as its range allows (8 + 7 < 16), which puts that step at 2^-31 of the largest weight.
 template <bool kBf16>
-__global__ void __launch_bounds__(kThreads) k_paged_attn(Args a) {
-    extern __shared__ uint8_t raw[];
-    Shared& sh = *reinterpret_cast<Shared*>(raw);
-    grid_dep_wait();
-    plan(a, &sh.range);
-    const int tid = threadIdx.x;
-    const int h = tid >> 2, part = tid & 3;  // O of head h, channels part + 4 i
-    int64_t at = sh.range.at;
-    const int64_t end = sh.range.end;
-    int b = sh.range.b, j = sh.range.j;
-    bool opens = true;
-    while (at < end) {
-        const View v = view_of(a, b, false);
-        if (j >= v.tiles) {
+constexpr float kLift = kBf16 ? 0.f : 7.f;
+
+template <bool kBf16, int NH>
+struct Shared {
+    using S = Shape<kBf16, NH>;
+    uint8_t kv[S::kPairs][2][kChunk];  // A operand of both products
+    uint8_t q[8][NH * 128];            // B operand of S: heads x 64 channels a chunk, K-major
+    uint8_t p[2][NH * 128];            // B operand of PV: heads x 64 positions a chunk, K-major
+    float col_scale[2][kMaxHeads];     // E4M3: per-head logit factor, by piece parity
+    float red_max[4][kMaxHeads];
+    float red_sum[4][kMaxHeads];
+    uint8_t row_ok[2][kTile];          // by tile parity: the row holds a position that is seen
+    // q_full: two barriers, so that a producer can publish the next piece's query before a
+    // softmax warp has waited on this one (a one-tile piece needs no softmax before its S ends)
+    uint64_t q_full[2], q_empty, s_full, p_full, o_full, drain;
+    uint64_t full[S::kPairs], empty[S::kPairs];
+    uint64_t max_bar[S::kGroups], sum_bar[S::kGroups];
+    Range range;
+    uint32_t tmem_base;
+    int abort;
+};
+
+// ---------------------------------------------------------------- a CTA's pieces
+struct Piece {
+    View v;
+    int b, j0, j1;
+    bool opens;  // the CTA's range begins with it
+    __device__ __forceinline__ bool whole() const { return j0 == 0 && j1 == v.tiles; }
+};
+struct Pieces {
+    int64_t at, end;
+    int b, j;
+    bool opens;
+    __device__ __forceinline__ explicit Pieces(const Range& r) : at(r.at), end(r.end), b(r.b), j(r.j), opens(true) {}
+    __device__ __forceinline__ bool next(const Args& a, Piece& p) {
+        while (at < end) {
+            p.v = view_of(a, b, false);
+            if (j < p.v.tiles) {
+                p.b = b;
+                p.j0 = j;
+                p.j1 = (int)min((int64_t)p.v.tiles, j + (end - at));
+                p.opens = opens;
+                opens = false;
+                at += p.j1 - j;
+                j = p.j1;
+                return true;
+            }
             ++b;
             j = 0;
-            continue;
         }
-        const int j1 = (int)min((int64_t)v.tiles, j + (end - at));
-        const int32_t* table = a.g.table + (int64_t)v.row * a.g.max_pages;
-        float o[kD / 4];
+        return false;
+    }
+};
+
+// The page that holds position t (which is seen) of table row `table`; -1 and a status bit
+// where there is none.
+__device__ __forceinline__ int page_of(const Args& a, const int32_t* table, uint32_t t) {
+    const int page = table[t / (uint32_t)a.g.page_size];
+    if (page >= 0 && page < a.g.n_pages) return page;
+    raise_status(a.dev_status, CSA2_DEV_BAD_INDEX);
+    return -1;
+}
+
+__device__ __forceinline__ uint32_t sw128(int row, int unit) { return (uint32_t)(row * 128 + ((unit ^ (row & 7)) << 4)); }
+
+// ---------------------------------------------------------------- bf16 producers
+// One warp copies the tile's rows, box by box (rows of one page, 64 channels), straight into
+// the swizzled operand; boxes that hold nothing seen are left out.
+template <int NH>
+__device__ void tma_role(Shared<true, NH>& sh, const Args& a, const CUtensorMap* tmap, int lane, volatile int* abort) {
+    constexpr int kPairs = Shape<true, NH>::kPairs;
+    const uint32_t ps = a.g.page_size;
+    Pieces it(sh.range);
+    Piece pc;
+    int g = 0, gt = 0;  // pairs and tiles so far
+    bool gave_up = false;
+    while (!gave_up && it.next(a, pc)) {
+        const int32_t* table = a.g.table + (int64_t)pc.v.row * a.g.max_pages;
+        for (int j = pc.j0; j < pc.j1 && !gave_up; ++j, ++gt) {
+            const int64_t t0 = pc.v.start(j);
+            uint32_t rows[4];
 #pragma unroll
-        for (int i = 0; i < kD / 4; ++i) o[i] = 0.f;
-        float m = -INFINITY, l = 0.f;
-        for (int jj = j; jj < j1; ++jj) {
-            const int64_t t0 = v.start(jj);
-            for (int s = 0; s < kTile; s += kStep) {
-                __syncthreads();
-                for (int e = tid; e < kStep * kD; e += kThreads) {
-                    const int r = e / kD, c = e % kD;
-                    const int64_t t = t0 + s + r;
-                    float x = 0.f;
-                    if (v.sees(t)) {
-                        const int page = table[t / a.g.page_size];
-                        if (page >= 0 && page < a.g.n_pages) {
-                            const uint8_t* row = a.base + page * a.g.page_bytes() + (t % a.g.page_size) * a.g.row_bytes;
-                            x = kBf16 ? __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(row)[c]) : e4m3_at(row + c);
-                        } else if (c == 0) {
-                            raise_status(a.dev_status, CSA2_DEV_BAD_INDEX);
-                        }
-                    }
-                    sh.kv[r][c] = x;
+            for (int w = 0; w < 4; ++w) {
+                const int64_t t = t0 + 32 * w + lane;
+                const bool ok = pc.v.sees(t) && page_of(a, table, (uint32_t)t) >= 0;
+                rows[w] = __ballot_sync(0xffffffffu, ok);
+            }
+            // lane i has box i: box_rows divides 128 and the page size, so a box lies in a page
+            const int first = lane * a.box_rows;
+            bool mine = false;
+            int y = 0;
+            if (first < kTile) {
+                const uint32_t m = a.box_rows >= 32 ? 0xffffffffu : ((1u << a.box_rows) - 1u) << (first & 31);
+                for (int w = first >> 5; w <= (first + a.box_rows - 1) >> 5; ++w) mine |= (rows[w] & m) != 0;
+                if (mine) {
+                    const uint32_t t = (uint32_t)t0 + first;
+                    y = table[t / ps] * (int)ps + (int)(t % ps);
                 }
-                __syncthreads();
-                for (int e = tid; e < a.heads * kStep; e += kThreads) {
-                    const int hh = e / kStep, r = e % kStep;
-                    const int64_t t = t0 + s + r;
-                    bool ok = v.sees(t);
-                    if (ok) {
-                        const int page = table[t / a.g.page_size];
-                        ok = page >= 0 && page < a.g.n_pages;
-                    }
-                    float z = -INFINITY;
-                    if (ok) {
-                        const __nv_bfloat16* q = a.q + b * a.q_seq + hh * a.q_head;
-                        z = 0.f;
-                        for (int c = 0; c < kD; ++c) z = fmaf(__bfloat162float(q[c]), sh.kv[r][c], z);
-                        z *= a.scale_log2;
-                    }
-                    sh.z[hh][r] = z;
+            }
+            const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, mine)) * a.box_rows * 256u;
+            for (int pr = 0; pr < 4; ++pr, ++g) {
+                const int slot = g % kPairs;
+                if (g >= kPairs && !mbar_wait(&sh.empty[slot], (uint32_t)((g / kPairs - 1) & 1), abort)) gave_up = true;
+                if (__any_sync(0xffffffffu, gave_up)) {
+                    gave_up = true;
+                    break;
                 }
-                __syncthreads();
-                if (h < a.heads) {
-                    float mx = m;
-                    for (int r = 0; r < kStep; ++r) mx = fmaxf(mx, sh.z[h][r]);
-                    if (mx != m) {
-                        const float f = m == -INFINITY ? 0.f : ex2(m - mx);
-                        l *= f;
-#pragma unroll
-                        for (int i = 0; i < kD / 4; ++i) o[i] *= f;
-                        m = mx;
-                    }
-                    for (int r = 0; r < kStep; ++r) {
-                        const float z = sh.z[h][r];
-                        if (z == -INFINITY) continue;
-                        const float p = ex2(z - m);
-                        l += p;
-#pragma unroll
-                        for (int i = 0; i < kD / 4; ++i) o[i] = fmaf(p, sh.kv[r][part + 4 * i], o[i]);
-                    }
+                if (pr == 0)
+                    *reinterpret_cast<uint32_t*>(&sh.row_ok[gt & 1][4 * lane]) =
+                        ((rows[lane >> 3] >> (4 * (lane & 7))) & 15u) * 0x00204081u & 0x01010101u;
+                __syncwarp();
+                if (lane == 0) mbar_arrive_expect_tx(&sh.full[slot], bytes);
+                __syncwarp();
+                if (mine) {
+                    const uint32_t dst = smem_u32(sh.kv[slot][0]) + first * 128;
+                    tma_g2s_2d(dst, tmap, 128 * pr, y, &sh.full[slot]);
+                    tma_g2s_2d(dst + kChunk, tmap, 128 * pr + 64, y, &sh.full[slot]);
                 }
             }
         }
-        if (h < a.heads) {
-            if (j == 0 && j1 == v.tiles) {
-                const float s2 = a.sink ? a.sink[h] * kLog2e : -INFINITY;
-                const float M = fmaxf(m, s2);
-                const float f = m == -INFINITY ? 0.f : ex2(m - M);
-                const float den = l * f + (s2 == -INFINITY ? 0.f : ex2(s2 - M));
-                __nv_bfloat16* out = a.out + ((int64_t)b * a.heads + h) * kD;
-#pragma unroll
-                for (int i = 0; i < kD / 4; ++i)
-                    out[part + 4 * i] = __float2bfloat16_rn(den == 0.f ? 0.f : o[i] * f / den);
-            } else {
-                float* p = part_of(a, blockIdx.x, opens ? 0 : 1);
-#pragma unroll
-                for (int i = 0; i < kD / 4; ++i) p[(int64_t)h * kD + part + 4 * i] = o[i];
-                if (part == 0) {
-                    p[(int64_t)a.heads * kD + h] = m;
-                    p[(int64_t)a.heads * (kD + 1) + h] = l;
-                }
-            }
+    }
+    // whatever ended the loop, no copy of this CTA outlives it
+    for (int s = max(0, g - kPairs); s < g; ++s) mbar_wait_drain(&sh.full[s % kPairs], (uint32_t)((s / kPairs) & 1));
+}
+
+template <int NH>
+__device__ void query_role(Shared<true, NH>& sh, const Args& a, int pt, int lane, volatile int* abort) {
+    constexpr int kStagers = 32 * Shape<true, NH>::kQueryWarps;
+    Pieces pi(sh.range);
+    Piece pc;
+    for (int it = 0; pi.next(a, pc); ++it) {
+        if (it > 0 && !mbar_wait(&sh.q_empty, (uint32_t)((it - 1) & 1), abort)) return;
+        __syncwarp();
+        const __nv_bfloat16* q = a.q + pc.b * a.q_seq;
+        for (int i = pt; i < NH * 64; i += kStagers) {
+            const int h = i >> 6, u = i & 63;
+            cp_async_16(smem_u32(sh.q[u >> 3]) + sw128(h, u & 7), q + (h < a.heads ? h * a.q_head + 8 * u : 0), h < a.heads);
         }
-        at += j1 - j;
-        j = j1;
-        opens = false;
+        cp_async_wait_all();
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.q_full[it & 1]);
     }
 }
+
+// ---------------------------------------------------------------- E4M3 producers
+__device__ __forceinline__ void e4m3x4_to_h2x2(uint32_t w, uint32_t* o) {
+    asm("{\n .reg .b16 lo, hi;\n mov.b32 {lo, hi}, %2;\n"
+        " cvt.rn.f16x2.e4m3x2 %0, lo;\n cvt.rn.f16x2.e4m3x2 %1, hi;\n}"
+        : "=r"(o[0]), "=r"(o[1])
+        : "r"(w));
+}
+
+__device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// Eight warps: thread (r, hf) has row r of every tile and chunk 2 pr + hf of each pair. The
+// next tile's bytes of a pair are requested as soon as this tile's are decoded.
+template <int NH>
+__device__ void decode_role(Shared<false, NH>& sh, const Args& a, int pt, int lane, volatile int* abort) {
+    constexpr int kPairs = Shape<false, NH>::kPairs;
+    const int pw = pt >> 5, r = pt >> 1, hf = pt & 1;
+    const uint32_t ps = a.g.page_size;
+    Pieces pi(sh.range);
+    Piece pc, nx;
+    bool has = pi.next(a, pc), has_nx = has && pi.next(a, nx);
+    if (!has) return;
+    // this thread's bytes of tile j of a piece: its row's half, or NULL where nothing is seen
+    auto row_of = [&](const Piece& p, int j) -> const uint4* {
+        const int64_t t = p.v.start(j) + r;
+        if (!p.v.sees(t)) return nullptr;
+        const int page = page_of(a, a.g.table + (int64_t)p.v.row * a.g.max_pages, (uint32_t)t);
+        if (page < 0) return nullptr;
+        return reinterpret_cast<const uint4*>(a.base + page * a.g.page_bytes() + (int64_t)((uint32_t)t % ps) * kD + 64 * hf);
+    };
+    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+    uint4 raw[4][4];
+    const uint4* cur = row_of(pc, pc.j0);
+#pragma unroll
+    for (int pr = 0; pr < 4; ++pr)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) raw[pr][k] = cur ? __ldg(cur + 8 * pr + k) : zero;
+    int g = 0, gt = 0;
+    for (int it = 0; has; ++it) {
+        // ---- query: warp pw stages heads pw, pw + 8, ...; lane = channels 16 lane .. + 15
+        if (it > 0 && !mbar_wait(&sh.q_empty, (uint32_t)((it - 1) & 1), abort)) return;
+        __syncwarp();
+#pragma unroll 1
+        for (int h = pw; h < NH; h += 8) {
+            uint4 w2[2] = {zero, zero};
+            if (h < a.heads) {
+                const uint4* src = reinterpret_cast<const uint4*>(a.q + pc.b * a.q_seq + h * a.q_head) + 2 * lane;
+                w2[0] = __ldg(src);
+                w2[1] = __ldg(src + 1);
+            }
+            const uint32_t w[8] = {w2[0].x, w2[0].y, w2[0].z, w2[0].w, w2[1].x, w2[1].y, w2[1].z, w2[1].w};
+            float mx = 0.f;
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(w[k] << 16)), fabsf(__uint_as_float(w[k] & 0xffff0000u))));
+#pragma unroll
+            for (int o = 16; o >= 1; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+            // times 2^s with the head's largest |q| in [2^14, 2^15): f16 then keeps bf16's 8
+            // bits of everything above 2^-24 of it; the factor goes into the logit scale
+            int s = 14 - ((int)((__float_as_uint(mx) >> 23) & 0xffu) - 127);
+            s = max(-126, min(126, s));
+            const float two_s = __uint_as_float((uint32_t)(s + 127) << 23);
+            uint32_t hq[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                hq[k] = pack_h2(__uint_as_float(w[k] << 16) * two_s, __uint_as_float(w[k] & 0xffff0000u) * two_s);
+            uint8_t* row = sh.q[lane >> 2];
+            const int u0 = (lane & 3) * 2;
+            *reinterpret_cast<uint4*>(row + sw128(h, u0)) = make_uint4(hq[0], hq[1], hq[2], hq[3]);
+            *reinterpret_cast<uint4*>(row + sw128(h, u0 + 1)) = make_uint4(hq[4], hq[5], hq[6], hq[7]);
+            if (lane == 0) sh.col_scale[it & 1][h] = a.scale_log2 * __uint_as_float((uint32_t)(127 - s) << 23);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.q_full[it & 1]);
+        for (int j = pc.j0; j < pc.j1; ++j, ++gt) {
+            const uint4* nxt = j + 1 < pc.j1 ? row_of(pc, j + 1) : has_nx ? row_of(nx, nx.j0) : nullptr;
+#pragma unroll
+            for (int pr = 0; pr < 4; ++pr, ++g) {
+                const int slot = g % kPairs;
+                if (g >= kPairs && !mbar_wait(&sh.empty[slot], (uint32_t)((g / kPairs - 1) & 1), abort)) return;
+                if (pr == 0 && hf == 0) sh.row_ok[gt & 1][r] = cur != nullptr;
+                uint8_t* dst = sh.kv[slot][hf];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    uint32_t o[8];
+                    e4m3x4_to_h2x2(raw[pr][k].x, &o[0]);
+                    e4m3x4_to_h2x2(raw[pr][k].y, &o[2]);
+                    e4m3x4_to_h2x2(raw[pr][k].z, &o[4]);
+                    e4m3x4_to_h2x2(raw[pr][k].w, &o[6]);
+                    *reinterpret_cast<uint4*>(dst + sw128(r, 2 * k)) = make_uint4(o[0], o[1], o[2], o[3]);
+                    *reinterpret_cast<uint4*>(dst + sw128(r, 2 * k + 1)) = make_uint4(o[4], o[5], o[6], o[7]);
+                }
+#pragma unroll
+                for (int k = 0; k < 4; ++k) raw[pr][k] = nxt ? __ldg(nxt + 8 * pr + k) : zero;
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh.full[slot]);
+            }
+            cur = nxt;
+        }
+        pc = nx;
+        has = has_nx;
+        has_nx = has && pi.next(a, nx);
+    }
+}
+
+// ---------------------------------------------------------------- MMA issuer
+template <bool kBf16, int NH>
+__device__ void mma_role(Shared<kBf16, NH>& sh, const Args& a, uint32_t tmem, volatile int* abort) {
+    using S = Shape<kBf16, NH>;
+    const uint64_t dK = smem_desc(smem_u32(sh.kv[0][0]), 16, 1024, kLayoutSw128);
+    const uint64_t dQ = smem_desc(smem_u32(sh.q[0]), 16, 1024, kLayoutSw128);
+    const uint64_t dV = smem_desc(smem_u32(sh.kv[0][0]), kChunk, 1024, kLayoutSw128);
+    const uint64_t dP = smem_desc(smem_u32(sh.p[0]), 16, 1024, kLayoutSw128);
+    Pieces pi(sh.range);
+    Piece pc;
+    int g = 0, gt = 0;
+    for (int it = 0; pi.next(a, pc); ++it) {
+        if (!mbar_wait(&sh.q_full[it & 1], (uint32_t)((it >> 1) & 1), abort)) return;
+        tc_fence_after();
+        for (int j = pc.j0; j < pc.j1; ++j, ++gt, g += 4) {
+            // S^T = K . Q^T over the 512 channels, pair by pair as they land
+#pragma unroll
+            for (int pr = 0; pr < 4; ++pr) {
+                const int slot = (g + pr) % S::kPairs;
+                if (!mbar_wait(&sh.full[slot], (uint32_t)(((g + pr) / S::kPairs) & 1), abort)) return;
+                tc_fence_after();
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        mma_f16(tmem + S::kColS, dK + (((2 * slot + c) * kChunk + 32 * k) >> 4),
+                                dQ + (((2 * pr + c) * NH * 128 + 32 * k) >> 4), S::kIdescS, (pr | c | k) != 0);
+            }
+            tc_commit(&sh.s_full);
+            if (j == pc.j1 - 1) tc_commit(&sh.q_empty);
+            // O^T += V^T . P^T, 128 channels (one pair) at a time
+            if (!mbar_wait(&sh.p_full, (uint32_t)(gt & 1), abort)) return;
+            tc_fence_after();
+#pragma unroll
+            for (int mb = 0; mb < 4; ++mb) {
+                const int slot = (g + mb) % S::kPairs;
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    mma_f16(tmem + NH * mb, dV + ((2 * slot * kChunk + k * 2048) >> 4),
+                            dP + (((k >> 2) * NH * 128 + 32 * (k & 3)) >> 4), S::kIdescPV, j != pc.j0 || k != 0);
+                tc_commit(&sh.empty[slot]);
+            }
+        }
+        tc_commit(&sh.o_full);
+    }
+}
+
+// ---------------------------------------------------------------- softmax and epilogue
+template <int NC>
+__device__ __forceinline__ void tmem_ld(uint32_t at, uint32_t* r) {
+    if constexpr (NC == 32) tmem_ld_32x32b_x32(at, r);
+    else if constexpr (NC == 16) tmem_ld_32x32b_x16(at, r);
+    else tmem_ld_32x32b_x8(at, r);
+}
+template <int NC>
+__device__ __forceinline__ void tmem_st(uint32_t at, const uint32_t* r) {
+    if constexpr (NC == 32) tmem_st_32x32b_x32(at, r);
+    else if constexpr (NC == 16) tmem_st_32x32b_x16(at, r);
+    else tmem_st_32x32b_x8(at, r);
+}
+
+// Sums NC per-head values over the warp's 32 lanes; lane i returns head i mod NC.
+template <int NC>
+__device__ __forceinline__ float warp_sum(float* v, int lane) {
+#pragma unroll
+    for (int o = NC / 2; o >= 1; o >>= 1) {
+        const bool up = (lane & o) != 0;
+#pragma unroll
+        for (int i = 0; i < o; ++i) {
+            const float keep = up ? v[i + o] : v[i], give = up ? v[i] : v[i + o];
+            v[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+        }
+    }
+    float s = v[0];
+#pragma unroll
+    for (int o = NC; o < 32; o <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    return s;
+}
+
+__device__ __forceinline__ float warp_max(float v) {
+    float r;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;\n" : "=f"(r) : "f"(v));
+    return r;
+}
+
+// Warp (qd, cg): positions 32 qd + lane of the tile, heads cg NC .. + NC - 1. Logits are in
+// the log2 domain. The running maximum is lazy: it moves only when a tile would push P above
+// 2^8, and then those heads' columns of O are rescaled in TMEM.
+template <bool kBf16, int NH>
+__device__ void softmax_role(Shared<kBf16, NH>& sh, const Args& a, uint32_t tmem, int warp, int lane,
+                             volatile int* abort) {
+    using S = Shape<kBf16, NH>;
+    constexpr int NC = S::NC;
+    const int qd = warp & 3, cg = warp >> 2, h0 = cg * NC, mine = lane & (NC - 1);
+    const int r = 32 * qd + lane;
+    const uint32_t tl = tmem + ((uint32_t)(32 * qd) << 16);
+    // P of this position: row h of its chunk, byte (unit ^ (h & 7)) * 16 + 2 (r mod 8)
+    uint8_t* const prow = sh.p[r >> 6] + 2 * (r & 7);
+    const int punit = (r & 63) >> 3;
+    const float sink2 = a.sink && h0 + mine < a.heads ? a.sink[h0 + mine] * kLog2e : -INFINITY;
+    Pieces pi(sh.range);
+    Piece pc;
+    int g = 0, gt = 0;
+    for (int it = 0; pi.next(a, pc); ++it) {
+        if (!mbar_wait(&sh.q_full[it & 1], (uint32_t)((it >> 1) & 1), abort)) return;
+        float m_run = -INFINITY;  // running maximum of head h0 + mine
+        float lpart[NC];          // this row's share of the sum of P
+#pragma unroll
+        for (int i = 0; i < NC; ++i) lpart[i] = 0.f;
+        for (int j = pc.j0; j < pc.j1; ++j, ++gt, g += 4) {
+            if (!mbar_wait(&sh.s_full, (uint32_t)(gt & 1), abort)) return;
+            // (complete already: orders the read of row_ok after the producer's write)
+            if (!mbar_wait(&sh.full[g % S::kPairs], (uint32_t)((g / S::kPairs) & 1), abort)) return;
+            tc_fence_after();
+            const bool ok = sh.row_ok[gt & 1][r] != 0;
+            float x[NC];
+            {
+                uint32_t sv[NC];
+                tmem_ld<NC>(tl + S::kColS + h0, sv);
+#pragma unroll
+                for (int i = 0; i < NC; ++i) {
+                    const float c = kBf16 ? a.scale_log2 : sh.col_scale[it & 1][h0 + i];
+                    x[i] = ok ? __uint_as_float(sv[i]) * c : -INFINITY;
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < NC; i += 4) {
+                const float4 m4 = make_float4(warp_max(x[i]), warp_max(x[i + 1]), warp_max(x[i + 2]), warp_max(x[i + 3]));
+                if (lane == 0) *reinterpret_cast<float4*>(&sh.red_max[qd][h0 + i]) = m4;
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.max_bar[cg]);
+            if constexpr (kBf16) {
+                // Rows that are not seen came with the box or are left from another tile:
+                // whatever they hold (NaN among it) must not meet P = 0 in the product. S has
+                // read them, PV has not.
+                if (!ok) {
+#pragma unroll 1
+                    for (int c = cg * (8 / S::kGroups); c < (cg + 1) * (8 / S::kGroups); ++c) {
+                        uint4* z = reinterpret_cast<uint4*>(sh.kv[(g + (c >> 1)) % S::kPairs][c & 1] + r * 128);
+#pragma unroll
+                        for (int u = 0; u < 8; ++u) z[u] = make_uint4(0u, 0u, 0u, 0u);
+                    }
+                }
+            }
+            if (!mbar_wait(&sh.max_bar[cg], (uint32_t)(gt & 1), abort)) return;
+            const float tm = fmaxf(fmaxf(sh.red_max[0][h0 + mine], sh.red_max[1][h0 + mine]),
+                                   fmaxf(sh.red_max[2][h0 + mine], sh.red_max[3][h0 + mine]));
+            const float m_new = tm > m_run + kLazyMax ? tm : m_run;
+            const float alpha = (m_new != m_run && m_run != -INFINITY) ? ex2(m_run - m_new) : 1.f;
+            const bool rescale = __any_sync(0xffffffffu, alpha != 1.f);
+            m_run = m_new;
+            const float mfix = m_run == -INFINITY ? 0.f : m_run - kLift<kBf16>;
+            if (rescale) {
+#pragma unroll
+                for (int i = 0; i < NC; ++i) lpart[i] *= __shfl_sync(0xffffffffu, alpha, i);
+            }
+            // P = 2^(x - m) (lifted), rounded to the matrix type; the sum takes the rounded values, so
+            // the weights of a row add up to one whatever the rounding does
+#pragma unroll
+            for (int i = 0; i < NC; ++i) {
+                const float p = ex2(x[i] - __shfl_sync(0xffffffffu, mfix, i));
+                uint16_t bits;
+                if constexpr (kBf16) {
+                    bits = __bfloat16_as_ushort(__float2bfloat16_rn(p));
+                    lpart[i] += __uint_as_float((uint32_t)bits << 16);
+                } else {
+                    const __half ph = __float2half_rn(p);
+                    bits = __half_as_ushort(ph);
+                    lpart[i] += __half2float(ph);
+                }
+                const int h = h0 + i;
+                *reinterpret_cast<uint16_t*>(prow + h * 128 + ((punit ^ (h & 7)) << 4)) = bits;
+            }
+            if (rescale) {  // O holds the tiles before this one (S was issued after them)
+#pragma unroll 1
+                for (int mb = 0; mb < 4; ++mb) {
+                    uint32_t ov[NC];
+                    tmem_ld<NC>(tl + NH * mb + h0, ov);
+#pragma unroll
+                    for (int i = 0; i < NC; ++i)
+                        ov[i] = __float_as_uint(__uint_as_float(ov[i]) * __shfl_sync(0xffffffffu, alpha, i));
+                    tmem_st<NC>(tl + NH * mb + h0, ov);
+                }
+                tmem_wait_st();
+            }
+            fence_proxy_async_smem();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.p_full);
+        }
+        if (!mbar_wait(&sh.o_full, (uint32_t)(it & 1), abort)) return;
+        tc_fence_after();
+        sh.red_sum[qd][h0 + mine] = warp_sum<NC>(lpart, lane);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.sum_bar[cg]);
+        if (!mbar_wait(&sh.sum_bar[cg], (uint32_t)(it & 1), abort)) return;
+        const float l = (sh.red_sum[0][h0 + mine] + sh.red_sum[1][h0 + mine]) +
+                        (sh.red_sum[2][h0 + mine] + sh.red_sum[3][h0 + mine]);
+        m_run -= kLift<kBf16>;  // what P and O are relative to
+        // lane = channel 128 mb + 32 qd + lane of NC heads: for each head the warp stores 32
+        // neighbouring values
+        if (pc.whole()) {
+            const float M = fmaxf(m_run, sink2);
+            const float f = m_run == -INFINITY ? 0.f : ex2(m_run - M);
+            const float den = l * f + (sink2 == -INFINITY ? 0.f : ex2(sink2 - M));
+            const float w = den == 0.f ? 0.f : f / den;
+            __nv_bfloat16* out = a.out + ((int64_t)pc.b * a.heads + h0) * kD + r;
+#pragma unroll 1
+            for (int mb = 0; mb < 4; ++mb) {
+                uint32_t ov[NC];
+                tmem_ld<NC>(tl + NH * mb + h0, ov);
+#pragma unroll
+                for (int i = 0; i < NC; ++i) {
+                    const float wi = __shfl_sync(0xffffffffu, w, i);
+                    if (h0 + i < a.heads)
+                        out[(int64_t)i * kD + 128 * mb] = __float2bfloat16_rn(wi == 0.f ? 0.f : __uint_as_float(ov[i]) * wi);
+                }
+            }
+        } else {
+            float* part = part_of(a, blockIdx.x, pc.opens ? 0 : 1);
+            if (qd == 0 && lane < NC && h0 + lane < a.heads) {
+                part[(int64_t)a.heads * kD + h0 + lane] = m_run;
+                part[(int64_t)a.heads * (kD + 1) + h0 + lane] = l;
+            }
+#pragma unroll 1
+            for (int mb = 0; mb < 4; ++mb) {
+                uint32_t ov[NC];
+                tmem_ld<NC>(tl + NH * mb + h0, ov);
+#pragma unroll
+                for (int i = 0; i < NC; ++i)
+                    if (h0 + i < a.heads) part[(int64_t)(h0 + i) * kD + 128 * mb + r] = __uint_as_float(ov[i]);
+            }
+        }
+        tc_fence_before();
+    }
+}
+
+template <bool kBf16, int NH>
+__global__ void __launch_bounds__(Shape<kBf16, NH>::kThreads, 1)
+k_paged_attn(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap tmap) {
+    using S = Shape<kBf16, NH>;
+    extern __shared__ uint8_t raw[];
+    auto& sh = *reinterpret_cast<Shared<kBf16, NH>*>(raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u));
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    volatile int* abort = &sh.abort;
+    if (tid == 0) {
+        mbar_init(&sh.q_full[0], S::kQueryWarps);
+        mbar_init(&sh.q_full[1], S::kQueryWarps);
+        mbar_init(&sh.q_empty, 1);
+        mbar_init(&sh.s_full, 1);
+        mbar_init(&sh.p_full, S::kSoftWarps);
+        mbar_init(&sh.o_full, 1);
+        mbar_init(&sh.drain, 1);
+        for (int i = 0; i < S::kPairs; ++i) {
+            mbar_init(&sh.full[i], kBf16 ? 1 : S::kProdWarps);
+            mbar_init(&sh.empty[i], 1);
+        }
+        for (int i = 0; i < S::kGroups; ++i) {
+            mbar_init(&sh.max_bar[i], 4);
+            mbar_init(&sh.sum_bar[i], 4);
+        }
+        sh.abort = 0;
+        fence_mbar_init();
+    }
+    if (warp == S::kMmaWarp) {
+        tmem_alloc(&sh.tmem_base, kTmemCols);
+        tmem_relinquish();
+    }
+    // a programmatic launch: only the setup above may overlap the kernel ahead
+    grid_dep_wait();
+    tc_fence_before();
+    plan(a, &sh.range);  // ends with a CTA barrier
+    tc_fence_after();
+    const uint32_t tmem = sh.tmem_base;
+    if (warp < S::kSoftWarps) {
+        softmax_role<kBf16, NH>(sh, a, tmem, warp, lane, abort);
+    } else if (warp == S::kMmaWarp) {
+        if (lane == 0) {
+            mma_role<kBf16, NH>(sh, a, tmem, abort);
+            // every MMA issued must finish before TMEM and shared memory are released
+            tc_commit(&sh.drain);
+            if (!mbar_wait_drain(&sh.drain, 0)) *abort = 1;
+        }
+    } else if constexpr (kBf16) {
+        if (warp == S::kProd0) tma_role<NH>(sh, a, &tmap, lane, abort);
+        else query_role<NH>(sh, a, tid - 32 * (S::kProd0 + 1), lane, abort);
+    } else {
+        decode_role<NH>(sh, a, tid - 32 * S::kProd0, lane, abort);
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (tid == 0 && sh.abort) raise_status(a.dev_status, CSA2_DEV_TIMEOUT);
+    if (warp == S::kMmaWarp) {
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc(tmem, kTmemCols);
+    }
+}
+
+template <bool kBf16, int NH>
+constexpr int smem_bytes() {
+    return (int)sizeof(Shared<kBf16, NH>) + 1024;
+}
+static_assert(smem_bytes<true, 64>() <= 232448 && smem_bytes<true, 32>() <= 232448 && smem_bytes<true, 16>() <= 232448,
+              "shared memory of a CTA");
 
 // ---------------------------------------------------------------- join
 // One warp per (sequence, head), lane = 16 channels in four groups of four. Sequences that
@@ -329,6 +802,38 @@ int grid_of(const csa2_params* p) {
     return p->max_ctas > 0 && p->max_ctas < n ? p->max_ctas : n;
 }
 
+// The layer's rows as a 2-d tensor map, whose boxes are box_rows rows x 64 channels laid out
+// in the 128-byte swizzle of the MMA operands. The driver's encoder is looked up once.
+int encode_rows(const Args& a, CUtensorMap* m) {
+    using Encode = decltype(&cuTensorMapEncodeTiled);
+    static Encode encode = [] {
+        void* f = nullptr;
+        cudaDriverEntryPointQueryResult r;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &r) != cudaSuccess ||
+            r != cudaDriverEntryPointSuccess)
+            f = nullptr;
+        return reinterpret_cast<Encode>(f);
+    }();
+    if (!encode) return fail(CSA2_ERR_CUDA, "paged_attn: the driver has no cuTensorMapEncodeTiled");
+    const cuuint64_t dims[2] = {kD, (cuuint64_t)a.g.n_pages * a.g.page_size};
+    const cuuint64_t strides[1] = {2 * kD};
+    const cuuint32_t box[2] = {64, (cuuint32_t)a.box_rows}, steps[2] = {1, 1};
+    if (encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<uint8_t*>(a.base), dims, strides, box, steps,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+        return fail(CSA2_ERR_CUDA, "paged_attn: tensor map of the pool");
+    return CSA2_OK;
+}
+
+template <bool kBf16, int NH>
+int launch_attn(const Args& a, const CUtensorMap& m, cudaLaunchConfig_t* cfg) {
+    cfg->gridDim = dim3(a.ctas);
+    cfg->blockDim = dim3(Shape<kBf16, NH>::kThreads);
+    cfg->dynamicSmemBytes = smem_bytes<kBf16, NH>();
+    cudaLaunchKernelEx(cfg, k_paged_attn<kBf16, NH>, a, m);
+    return check_launch("paged_attn");
+}
+
 int64_t prefix_bytes(int64_t B) { return (8 * (B + 1) + 255) & ~(int64_t)255; }
 
 int64_t ws_need(int B, int heads, int ctas) { return prefix_bytes(B) + 2 * (int64_t)ctas * part_floats(heads) * 4; }
@@ -336,8 +841,12 @@ int64_t ws_need(int B, int heads, int ctas) { return prefix_bytes(B) + 2 * (int6
 }  // namespace
 
 cudaError_t preload_paged_attn() {
-    cudaError_t (*l[])() = {[] { return preload_kernel(k_paged_attn<true>, (int)sizeof(Shared)); },
-                            [] { return preload_kernel(k_paged_attn<false>, (int)sizeof(Shared)); },
+    cudaError_t (*l[])() = {[] { return preload_kernel(k_paged_attn<true, 64>, smem_bytes<true, 64>()); },
+                            [] { return preload_kernel(k_paged_attn<true, 32>, smem_bytes<true, 32>()); },
+                            [] { return preload_kernel(k_paged_attn<true, 16>, smem_bytes<true, 16>()); },
+                            [] { return preload_kernel(k_paged_attn<false, 64>, smem_bytes<false, 64>()); },
+                            [] { return preload_kernel(k_paged_attn<false, 32>, smem_bytes<false, 32>()); },
+                            [] { return preload_kernel(k_paged_attn<false, 16>, smem_bytes<false, 16>()); },
                             [] { return preload_kernel(k_paged_join); }};
     for (auto f : l)
         if (const cudaError_t e = f()) return e;
@@ -394,19 +903,29 @@ extern "C" int csa2_paged_attn(const csa2_params* p, const csa2_pages* c, int la
     a.dev_status = dev_status;
     a.scale_log2 = p->softmax_scale * kLog2e;
     a.ctas = ctas;
+    a.box_rows = a.g.page_size & -a.g.page_size;
+    if (a.box_rows > kTile) a.box_rows = kTile;
+    CUtensorMap rows = {};
+    if (p->kv_format == CSA2_BF16)
+        if (const int rc = encode_rows(a, &rows)) return rc;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(ctas);
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = sizeof(Shared);
     cfg.stream = static_cast<cudaStream_t>(stream);
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (p->kv_format == CSA2_BF16) cudaLaunchKernelEx(&cfg, k_paged_attn<true>, a);
-    else cudaLaunchKernelEx(&cfg, k_paged_attn<false>, a);
-    if (const int rc = check_launch("paged_attn")) return rc;
+    // The fewest columns that hold the heads: the query then leaves more of shared memory to
+    // the rows, and the softmax and the operand reads shrink with it.
+    int rc;
+    if (p->kv_format == CSA2_BF16) {
+        rc = p->heads > 32 ? launch_attn<true, 64>(a, rows, &cfg)
+             : p->heads > 16 ? launch_attn<true, 32>(a, rows, &cfg) : launch_attn<true, 16>(a, rows, &cfg);
+    } else {
+        rc = p->heads > 32 ? launch_attn<false, 64>(a, rows, &cfg)
+             : p->heads > 16 ? launch_attn<false, 32>(a, rows, &cfg) : launch_attn<false, 16>(a, rows, &cfg);
+    }
+    if (rc) return rc;
     cfg.gridDim = dim3(B, (p->heads + kJoinWarps - 1) / kJoinWarps);
     cfg.blockDim = dim3(32 * kJoinWarps);
     cfg.dynamicSmemBytes = 0;
