@@ -40,46 +40,57 @@ struct Args {
     int box_rows;     // rows of a copied box: divides 128 and the page size
 };
 
-__host__ __device__ inline int64_t part_floats(int heads) { return (int64_t)heads * (kD + 2); }
+// O [heads][512], then m [heads] and l [heads]; a multiple of four, as the join reads float4
+__host__ __device__ inline int64_t part_floats(int heads) { return ((int64_t)heads * (kD + 2) + 3) & ~(int64_t)3; }
 
 // What sequence b of the call sees: positions [0, nf) and [lo, T), in `tiles` tiles.
 struct View {
-    int64_t T, lo, nf;
-    int row;  // of the table; < 0: padding
+    uint32_t T, lo, nf;  // below 2^31
+    int row;             // of the table; < 0: padding
     int first_tiles, lo_tile, tiles;
-    __device__ __forceinline__ bool sees(int64_t t) const { return t < T && (t >= lo || t < nf); }
-    __device__ __forceinline__ int64_t start(int j) const {
-        return (int64_t)(j < first_tiles ? j : lo_tile + j - first_tiles) * kTile;
+    __device__ __forceinline__ bool sees(uint32_t t) const { return t < T && (t >= lo || t < nf); }
+    __device__ __forceinline__ uint32_t start(int j) const {
+        return (uint32_t)(j < first_tiles ? j : lo_tile + j - first_tiles) * kTile;
     }
 };
 
 __device__ __forceinline__ View view_of(const Args& a, int b, bool report) {
     View v;
     v.row = a.seq ? a.seq[b] : b;
-    v.T = v.row < 0 ? 0 : a.n_tokens[b];
+    int T = v.row < 0 ? 0 : a.n_tokens[b];
     if (v.row >= a.g.max_seqs) {
         if (report) raise_status(a.dev_status, CSA2_DEV_BAD_INDEX);
-        v.T = 0;
+        T = 0;
     }
-    if (v.T < 0 || v.T > a.g.max_len()) {
+    if (T < 0 || T > a.g.max_len()) {
         if (report) raise_status(a.dev_status, CSA2_DEV_BAD_LENGTH);
-        v.T = v.T < 0 ? 0 : a.g.max_len();
+        T = T < 0 ? 0 : (int)a.g.max_len();
     }
-    v.lo = a.window > 0 ? max((int64_t)0, v.T - a.window) : 0;
-    v.nf = min((int64_t)max(a.n_first, 0), v.lo);
-    v.lo_tile = (int)(v.lo / kTile);
-    v.first_tiles = min((int)((v.nf + kTile - 1) / kTile), v.lo_tile);
-    v.tiles = v.first_tiles + (int)((v.T + kTile - 1) / kTile) - v.lo_tile;
+    const int lo = a.window > 0 ? max(0, T - a.window) : 0, nf = min(max(a.n_first, 0), lo);
+    v.T = T;
+    v.lo = lo;
+    v.nf = nf;
+    v.lo_tile = lo / kTile;
+    v.first_tiles = min(nf / kTile + (nf % kTile != 0), v.lo_tile);
+    v.tiles = v.first_tiles + T / kTile + (T % kTile != 0) - v.lo_tile;
     return v;
 }
 
-// Items [range(c), range(c + 1)) of `total` belong to CTA c of n.
-__device__ __forceinline__ int64_t range_of(int64_t total, int c, int n) { return total * c / n; }
-
-// Fewer items than CTAs leave some ranges empty.
-__device__ __forceinline__ bool holds(int64_t total, int c, int n) {
-    return range_of(total, c, n) < range_of(total, c + 1, n);
-}
+// The ranges: n = min(CTAs, items) of them, the first `total % n` one item longer.
+struct Cut {
+    int64_t base;
+    int n, rem;
+    __device__ __forceinline__ Cut(int64_t total, int ctas) {
+        n = (int)min((int64_t)ctas, total);
+        base = n ? total / n : 0;
+        rem = n ? (int)(total - base * n) : 0;
+    }
+    __device__ __forceinline__ int64_t at(int c) const { return c * base + min(c, rem); }  // c = 0 .. n
+    __device__ __forceinline__ int holder(int64_t item) const {
+        const int64_t big = rem * (base + 1);
+        return (int)(item < big ? item / (base + 1) : rem + (item - big) / base);
+    }
+};
 
 // The partial result of a piece of CTA c: slot 0 if the piece opens the CTA's range, else 1.
 __device__ __forceinline__ float* part_of(const Args& a, int c, int slot) {
@@ -90,14 +101,14 @@ __device__ __forceinline__ float* part_of(const Args& a, int c, int slot) {
 // leaves every sequence's first item in a.prefix for the join. Called by the whole CTA
 // (a multiple of 32 threads, at most 1,024).
 struct Range {
-    int64_t total, at, end;
+    int64_t items;
     int b, j;
 };
 __device__ void plan(const Args& a, Range* sh) {
     __shared__ int64_t warp_sum[32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
     const bool lead = blockIdx.x == 0;
-    int64_t total = 0;
+    int64_t total = 0, at = 0, end = 0;
     for (int pass = 0; pass < 2; ++pass) {  // the sum of all items, then the place of this range
         int64_t before = 0;
         for (int b0 = 0; b0 < a.B; b0 += blockDim.x) {
@@ -119,7 +130,6 @@ __device__ void plan(const Args& a, Range* sh) {
             __syncthreads();
             here += inc - n;
             if (pass == 1 && b < a.B) {
-                const int64_t at = range_of(total, blockIdx.x, a.ctas);
                 if (at >= here && at < here + n) {
                     sh->b = b;
                     sh->j = (int)(at - here);
@@ -128,12 +138,16 @@ __device__ void plan(const Args& a, Range* sh) {
             }
             before += all;
         }
-        total = before;
+        if (pass == 0) {
+            total = before;
+            const Cut cut(total, a.ctas);
+            const int c = min((int)blockIdx.x, cut.n);
+            at = cut.at(c);
+            end = cut.at(min(c + 1, cut.n));
+        }
     }
     if (tid == 0) {
-        sh->total = total;
-        sh->at = range_of(total, blockIdx.x, a.ctas);
-        sh->end = range_of(total, blockIdx.x + 1, a.ctas);
+        sh->items = end - at;
         if (lead) a.prefix[a.B] = total;
     }
     __syncthreads();
@@ -205,20 +219,20 @@ struct Piece {
     __device__ __forceinline__ bool whole() const { return j0 == 0 && j1 == v.tiles; }
 };
 struct Pieces {
-    int64_t at, end;
+    int64_t left;  // items
     int b, j;
     bool opens;
-    __device__ __forceinline__ explicit Pieces(const Range& r) : at(r.at), end(r.end), b(r.b), j(r.j), opens(true) {}
+    __device__ __forceinline__ explicit Pieces(const Range& r) : left(r.items), b(r.b), j(r.j), opens(true) {}
     __device__ __forceinline__ bool next(const Args& a, Piece& p) {
-        while (at < end) {
+        while (left > 0) {
             p.v = view_of(a, b, false);
             if (j < p.v.tiles) {
                 p.b = b;
                 p.j0 = j;
-                p.j1 = (int)min((int64_t)p.v.tiles, j + (end - at));
+                p.j1 = (int)min((int64_t)p.v.tiles, j + left);
                 p.opens = opens;
                 opens = false;
-                at += p.j1 - j;
+                left -= p.j1 - j;
                 j = p.j1;
                 return true;
             }
@@ -226,6 +240,20 @@ struct Pieces {
             j = 0;
         }
         return false;
+    }
+};
+
+// The same range tile by tile.
+struct Tiles {
+    Pieces it;
+    Piece pc;
+    int j;
+    __device__ __forceinline__ explicit Tiles(const Range& r) : it(r), j(0) { pc.j1 = 0; }
+    __device__ __forceinline__ bool next(const Args& a) {
+        if (++j < pc.j1) return true;
+        if (!it.next(a, pc)) return false;
+        j = pc.j0;
+        return true;
     }
 };
 
@@ -240,61 +268,86 @@ __device__ __forceinline__ int page_of(const Args& a, const int32_t* table, uint
 
 __device__ __forceinline__ uint32_t sw128(int row, int unit) { return (uint32_t)(row * 128 + ((unit ^ (row & 7)) << 4)); }
 
+__device__ __forceinline__ float warp_max(float v) {
+    float r;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;\n" : "=f"(r) : "f"(v));
+    return r;
+}
+
 // ---------------------------------------------------------------- bf16 producers
 // One warp copies the tile's rows, box by box (rows of one page, 64 channels), straight into
 // the swizzled operand; boxes that hold nothing seen are left out.
+struct Boxes {
+    uint32_t rows[4];  // the tile's rows that hold a seen position
+    bool mine;         // this lane's box is copied: rows 'first' on, the pool's row y on
+    int y;
+};
+__device__ __forceinline__ Boxes boxes_of(const Args& a, const Tiles& t, int lane) {
+    Boxes x;
+    const uint32_t ps = a.g.page_size, t0 = t.pc.v.start(t.j);
+    const int32_t* table = a.g.table + (int64_t)t.pc.v.row * a.g.max_pages;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+        const uint32_t p = t0 + 32 * w + lane;
+        x.rows[w] = __ballot_sync(0xffffffffu, t.pc.v.sees(p) && page_of(a, table, p) >= 0);
+    }
+    // lane i has box i: box_rows divides 128 and the page size, so a box lies in one page
+    const int first = lane * a.box_rows;
+    x.mine = false;
+    x.y = 0;
+    if (first < kTile) {
+        const uint32_t m = a.box_rows >= 32 ? 0xffffffffu : ((1u << a.box_rows) - 1u) << (first & 31);
+#pragma unroll
+        for (int w = 0; w < 4; ++w)
+            if (w >= first >> 5 && w <= (first + a.box_rows - 1) >> 5) x.mine |= (x.rows[w] & m) != 0;
+        if (x.mine) x.y = table[(t0 + first) / ps] * (int)ps + (int)((t0 + first) % ps);
+    }
+    return x;
+}
+
 template <int NH>
 __device__ void tma_role(Shared<true, NH>& sh, const Args& a, const CUtensorMap* tmap, int lane, volatile int* abort) {
     constexpr int kPairs = Shape<true, NH>::kPairs;
-    const uint32_t ps = a.g.page_size;
-    Pieces it(sh.range);
-    Piece pc;
-    int g = 0, gt = 0;  // pairs and tiles so far
-    bool gave_up = false;
-    while (!gave_up && it.next(a, pc)) {
-        const int32_t* table = a.g.table + (int64_t)pc.v.row * a.g.max_pages;
-        for (int j = pc.j0; j < pc.j1 && !gave_up; ++j, ++gt) {
-            const int64_t t0 = pc.v.start(j);
-            uint32_t rows[4];
+    const uint32_t dst0 = smem_u32(sh.kv[0][0]) + lane * a.box_rows * 128;
+    Tiles it(sh.range);
+    int g = 0;  // pairs so far
+    bool has = it.next(a), gave_up = false;
+    Boxes cur, nxt;
+    if (has) cur = boxes_of(a, it, lane);
+    for (int gt = 0; has && !gave_up; ++gt) {
+        // The ring holds little more than a tile, and it stands still between a tile's S and
+        // its PV: the next tile comes into L2 meanwhile, so that the refill is short.
+        const bool has_nx = it.next(a);
+        if (has_nx) {
+            nxt = boxes_of(a, it, lane);
+            if (nxt.mine)
 #pragma unroll
-            for (int w = 0; w < 4; ++w) {
-                const int64_t t = t0 + 32 * w + lane;
-                const bool ok = pc.v.sees(t) && page_of(a, table, (uint32_t)t) >= 0;
-                rows[w] = __ballot_sync(0xffffffffu, ok);
+                for (int c = 0; c < 8; ++c) tma_prefetch_2d(tmap, 64 * c, nxt.y);
+        }
+        const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, cur.mine)) * a.box_rows * 256u;
+        for (int pr = 0; pr < 4; ++pr, ++g) {
+            const int slot = g % kPairs;
+            if (g >= kPairs && !mbar_wait(&sh.empty[slot], (uint32_t)((g / kPairs - 1) & 1), abort)) gave_up = true;
+            if (__any_sync(0xffffffffu, gave_up)) {
+                gave_up = true;
+                break;
             }
-            // lane i has box i: box_rows divides 128 and the page size, so a box lies in a page
-            const int first = lane * a.box_rows;
-            bool mine = false;
-            int y = 0;
-            if (first < kTile) {
-                const uint32_t m = a.box_rows >= 32 ? 0xffffffffu : ((1u << a.box_rows) - 1u) << (first & 31);
-                for (int w = first >> 5; w <= (first + a.box_rows - 1) >> 5; ++w) mine |= (rows[w] & m) != 0;
-                if (mine) {
-                    const uint32_t t = (uint32_t)t0 + first;
-                    y = table[t / ps] * (int)ps + (int)(t % ps);
-                }
+            if (pr == 0) {  // four rows a lane: their bits to bytes
+                const uint32_t w = lane < 16 ? (lane < 8 ? cur.rows[0] : cur.rows[1]) : lane < 24 ? cur.rows[2] : cur.rows[3];
+                *reinterpret_cast<uint32_t*>(&sh.row_ok[gt & 1][4 * lane]) =
+                    (((w >> (4 * (lane & 7))) & 15u) * 0x00204081u) & 0x01010101u;
             }
-            const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, mine)) * a.box_rows * 256u;
-            for (int pr = 0; pr < 4; ++pr, ++g) {
-                const int slot = g % kPairs;
-                if (g >= kPairs && !mbar_wait(&sh.empty[slot], (uint32_t)((g / kPairs - 1) & 1), abort)) gave_up = true;
-                if (__any_sync(0xffffffffu, gave_up)) {
-                    gave_up = true;
-                    break;
-                }
-                if (pr == 0)
-                    *reinterpret_cast<uint32_t*>(&sh.row_ok[gt & 1][4 * lane]) =
-                        ((rows[lane >> 3] >> (4 * (lane & 7))) & 15u) * 0x00204081u & 0x01010101u;
-                __syncwarp();
-                if (lane == 0) mbar_arrive_expect_tx(&sh.full[slot], bytes);
-                __syncwarp();
-                if (mine) {
-                    const uint32_t dst = smem_u32(sh.kv[slot][0]) + first * 128;
-                    tma_g2s_2d(dst, tmap, 128 * pr, y, &sh.full[slot]);
-                    tma_g2s_2d(dst + kChunk, tmap, 128 * pr + 64, y, &sh.full[slot]);
-                }
+            __syncwarp();
+            if (lane == 0) mbar_arrive_expect_tx(&sh.full[slot], bytes);
+            __syncwarp();
+            if (cur.mine) {
+                const uint32_t dst = dst0 + 2 * slot * kChunk;
+                tma_g2s_2d(dst, tmap, 128 * pr, cur.y, &sh.full[slot]);
+                tma_g2s_2d(dst + kChunk, tmap, 128 * pr + 64, cur.y, &sh.full[slot]);
             }
         }
+        cur = nxt;
+        has = has_nx;
     }
     // whatever ended the loop, no copy of this CTA outlives it
     for (int s = max(0, g - kPairs); s < g; ++s) mbar_wait_drain(&sh.full[s % kPairs], (uint32_t)((s / kPairs) & 1));
@@ -334,37 +387,36 @@ __device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
 }
 
 // Eight warps: thread (r, hf) has row r of every tile and chunk 2 pr + hf of each pair. The
-// next tile's bytes of a pair are requested as soon as this tile's are decoded.
+// bytes of two pairs are on their way while one is decoded.
 template <int NH>
 __device__ void decode_role(Shared<false, NH>& sh, const Args& a, int pt, int lane, volatile int* abort) {
     constexpr int kPairs = Shape<false, NH>::kPairs;
     const int pw = pt >> 5, r = pt >> 1, hf = pt & 1;
     const uint32_t ps = a.g.page_size;
-    Pieces pi(sh.range);
-    Piece pc, nx;
-    bool has = pi.next(a, pc), has_nx = has && pi.next(a, nx);
-    if (!has) return;
-    // this thread's bytes of tile j of a piece: its row's half, or NULL where nothing is seen
-    auto row_of = [&](const Piece& p, int j) -> const uint4* {
-        const int64_t t = p.v.start(j) + r;
-        if (!p.v.sees(t)) return nullptr;
-        const int page = page_of(a, a.g.table + (int64_t)p.v.row * a.g.max_pages, (uint32_t)t);
+    // this thread's bytes of the tile the cursor is at: its row's half, or NULL where nothing is seen
+    Tiles ahead(sh.range);
+    auto row_of = [&]() -> const uint4* {
+        const uint32_t t = ahead.pc.v.start(ahead.j) + r;
+        if (!ahead.pc.v.sees(t)) return nullptr;
+        const int page = page_of(a, a.g.table + (int64_t)ahead.pc.v.row * a.g.max_pages, t);
         if (page < 0) return nullptr;
-        return reinterpret_cast<const uint4*>(a.base + page * a.g.page_bytes() + (int64_t)((uint32_t)t % ps) * kD + 64 * hf);
+        return reinterpret_cast<const uint4*>(a.base + page * a.g.page_bytes() + (int64_t)(t % ps) * kD + 64 * hf);
     };
     const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-    uint4 raw[4][4];
-    const uint4* cur = row_of(pc, pc.j0);
+    uint4 raw[2][4];
+    const uint4* cur = ahead.next(a) ? row_of() : nullptr;
 #pragma unroll
-    for (int pr = 0; pr < 4; ++pr)
+    for (int pr = 0; pr < 2; ++pr)
 #pragma unroll
         for (int k = 0; k < 4; ++k) raw[pr][k] = cur ? __ldg(cur + 8 * pr + k) : zero;
+    Pieces pi(sh.range);
+    Piece pc;
     int g = 0, gt = 0;
-    for (int it = 0; has; ++it) {
+    for (int it = 0; pi.next(a, pc); ++it) {
         // ---- query: warp pw stages heads pw, pw + 8, ...; lane = channels 16 lane .. + 15
         if (it > 0 && !mbar_wait(&sh.q_empty, (uint32_t)((it - 1) & 1), abort)) return;
         __syncwarp();
-#pragma unroll 1
+#pragma unroll 2
         for (int h = pw; h < NH; h += 8) {
             uint4 w2[2] = {zero, zero};
             if (h < a.heads) {
@@ -377,8 +429,7 @@ __device__ void decode_role(Shared<false, NH>& sh, const Args& a, int pt, int la
 #pragma unroll
             for (int k = 0; k < 8; ++k)
                 mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(w[k] << 16)), fabsf(__uint_as_float(w[k] & 0xffff0000u))));
-#pragma unroll
-            for (int o = 16; o >= 1; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+            mx = warp_max(mx);
             // times 2^s with the head's largest |q| in [2^14, 2^15): f16 then keeps bf16's 8
             // bits of everything above 2^-24 of it; the factor goes into the logit scale
             int s = 14 - ((int)((__float_as_uint(mx) >> 23) & 0xffu) - 127);
@@ -397,8 +448,8 @@ __device__ void decode_role(Shared<false, NH>& sh, const Args& a, int pt, int la
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.q_full[it & 1]);
-        for (int j = pc.j0; j < pc.j1; ++j, ++gt) {
-            const uint4* nxt = j + 1 < pc.j1 ? row_of(pc, j + 1) : has_nx ? row_of(nx, nx.j0) : nullptr;
+        for (int n = pc.j1 - pc.j0; n > 0; --n, ++gt) {
+            const uint4* nxt = ahead.next(a) ? row_of() : nullptr;
 #pragma unroll
             for (int pr = 0; pr < 4; ++pr, ++g) {
                 const int slot = g % kPairs;
@@ -408,24 +459,22 @@ __device__ void decode_role(Shared<false, NH>& sh, const Args& a, int pt, int la
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     uint32_t o[8];
-                    e4m3x4_to_h2x2(raw[pr][k].x, &o[0]);
-                    e4m3x4_to_h2x2(raw[pr][k].y, &o[2]);
-                    e4m3x4_to_h2x2(raw[pr][k].z, &o[4]);
-                    e4m3x4_to_h2x2(raw[pr][k].w, &o[6]);
+                    e4m3x4_to_h2x2(raw[pr & 1][k].x, &o[0]);
+                    e4m3x4_to_h2x2(raw[pr & 1][k].y, &o[2]);
+                    e4m3x4_to_h2x2(raw[pr & 1][k].z, &o[4]);
+                    e4m3x4_to_h2x2(raw[pr & 1][k].w, &o[6]);
                     *reinterpret_cast<uint4*>(dst + sw128(r, 2 * k)) = make_uint4(o[0], o[1], o[2], o[3]);
                     *reinterpret_cast<uint4*>(dst + sw128(r, 2 * k + 1)) = make_uint4(o[4], o[5], o[6], o[7]);
                 }
+                const uint4* src = pr < 2 ? cur : nxt;
 #pragma unroll
-                for (int k = 0; k < 4; ++k) raw[pr][k] = nxt ? __ldg(nxt + 8 * pr + k) : zero;
+                for (int k = 0; k < 4; ++k) raw[pr & 1][k] = src ? __ldg(src + 8 * ((pr + 2) & 3) + k) : zero;
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sh.full[slot]);
             }
             cur = nxt;
         }
-        pc = nx;
-        has = has_nx;
-        has_nx = has && pi.next(a, nx);
     }
 }
 
@@ -506,12 +555,6 @@ __device__ __forceinline__ float warp_sum(float* v, int lane) {
 #pragma unroll
     for (int o = NC; o < 32; o <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
     return s;
-}
-
-__device__ __forceinline__ float warp_max(float v) {
-    float r;
-    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;\n" : "=f"(r) : "f"(v));
-    return r;
 }
 
 // Warp (qd, cg): positions 32 qd + lane of the tile, heads cg NC .. + NC - 1. Logits are in
@@ -752,17 +795,14 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_paged_join(Args a) {
             for (int k = 0; k < 4; ++k) *reinterpret_cast<uint2*>(out + 128 * k) = make_uint2(0u, 0u);
         return;
     }
-    int c0 = (int)(s * a.ctas / total);  // the CTA whose range holds item s
-    while (range_of(total, c0 + 1, a.ctas) <= s) ++c0;
-    int c1 = c0;
-    while (range_of(total, c1 + 1, a.ctas) < e) ++c1;
+    const Cut cut(total, a.ctas);
+    const int c0 = cut.holder(s), c1 = cut.holder(e - 1);
     if (c0 == c1) return;
     const float s2 = a.sink ? a.sink[h] * kLog2e : -INFINITY;
     const int64_t mo = (int64_t)a.heads * kD + h, lo = mo + a.heads;
-    const int slot0 = range_of(total, c0, a.ctas) == s ? 0 : 1;
+    const int slot0 = cut.at(c0) == s ? 0 : 1;
     float M = s2;
-    for (int c = c0 + lane; c <= c1; c += 32)
-        if (holds(total, c, a.ctas)) M = fmaxf(M, part_of(a, c, c == c0 ? slot0 : 0)[mo]);
+    for (int c = c0 + lane; c <= c1; c += 32) M = fmaxf(M, part_of(a, c, c == c0 ? slot0 : 0)[mo]);
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
     float den = s2 == -INFINITY ? 0.f : ex2(s2 - M);
@@ -770,7 +810,6 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_paged_join(Args a) {
 #pragma unroll
     for (int k = 0; k < 4; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int c = c0; c <= c1; ++c) {
-        if (!holds(total, c, a.ctas)) continue;
         const float* p = part_of(a, c, c == c0 ? slot0 : 0);
         const float m = p[mo];
         const float f = m == -INFINITY ? 0.f : ex2(m - M);

@@ -205,6 +205,12 @@ __device__ __forceinline__ void tma_g2s_2d(uint32_t smem_dst, const void* tmap, 
         : "memory");
 }
 
+// The same box into L2 only.
+__device__ __forceinline__ void tma_prefetch_2d(const void* tmap, int x, int y) {
+    asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];\n" ::"l"(tmap), "r"(x), "r"(y)
+                 : "memory");
+}
+
 // 16 bytes global -> shared by the calling thread, zeros when !pred (nothing is read then).
 __device__ __forceinline__ void cp_async_16(uint32_t smem_dst, const void* gsrc, bool pred) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(smem_dst), "l"(gsrc),
