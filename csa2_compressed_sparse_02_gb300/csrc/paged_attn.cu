@@ -177,10 +177,17 @@ struct Shape {
     static constexpr int kPairs = NH == 64 ? 4 : NH == 32 ? 5 : 6;
     static constexpr uint32_t kColS = 4 * NH;  // TMEM: O^T 4 x NH columns, then S^T
     static constexpr uint32_t kFmt = kBf16 ? 1u : 0u;
-    // D fp32, A and B bf16 or f16, N = NH, M = 128; S: both K-major; PV: A MN-major
+    // D fp32, A and B bf16 or f16, N = NH, M = 128; S: both K-major, PV: both MN-major
     static constexpr uint32_t kIdescS =
         (1u << 4) | (kFmt << 7) | (kFmt << 10) | ((uint32_t)(NH >> 3) << 17) | ((128u >> 4) << 24);
-    static constexpr uint32_t kIdescPV = kIdescS | (1u << 15);
+    static constexpr uint32_t kIdescPV = kIdescS | (1u << 15) | (1u << 16);
+    // P: a row of NH heads per position, swizzled over its own width (128, 64 or 32 bytes)
+    static constexpr uint32_t kPRow = 2 * NH;
+    static constexpr uint32_t kPLayout = NH == 64 ? kLayoutSw128 : NH == 32 ? kLayoutSw64 : kLayoutSw32;
+    __device__ static __forceinline__ uint32_t p_unit(int row, int unit) {  // byte of 16-byte unit `unit`
+        const int x = NH == 64 ? row & 7 : NH == 32 ? (row >> 1) & 3 : (row >> 2) & 1;
+        return row * kPRow + ((unit ^ x) << 4);
+    }
 };
 
 constexpr uint32_t kChunk = 128 * 128;  // 128 positions x 64 channels of 16 bits, 128-byte swizzle
@@ -196,16 +203,18 @@ struct Shared {
     using S = Shape<kBf16, NH>;
     uint8_t kv[S::kPairs][2][kChunk];  // A operand of both products
     uint8_t q[8][NH * 128];            // B operand of S: heads x 64 channels a chunk, K-major
-    uint8_t p[2][NH * 128];            // B operand of PV: heads x 64 positions a chunk, K-major
+    uint8_t p[kTile * 2 * NH];         // B operand of PV: positions x heads, MN-major
     float col_scale[2][kMaxHeads];     // E4M3: per-head logit factor, by piece parity
     float red_max[4][kMaxHeads];
+    float m_sub[4][kMaxHeads];         // per lane quarter: what its logits are reduced by
+    int moved[S::kGroups];             // the last tile whose maximum had to move
     float red_sum[4][kMaxHeads];
     uint8_t row_ok[2][kTile];          // by tile parity: the row holds a position that is seen
     // q_full: two barriers, so that a producer can publish the next piece's query before a
     // softmax warp has waited on this one (a one-tile piece needs no softmax before its S ends)
     uint64_t q_full[2], q_empty, s_full, p_full, o_full, drain;
     uint64_t full[S::kPairs], empty[S::kPairs];
-    uint64_t max_bar[S::kGroups], sum_bar[S::kGroups];
+    uint64_t agree_bar[S::kGroups], max_bar[S::kGroups], sum_bar[S::kGroups];
     Range range;
     uint32_t tmem_base;
     int abort;
@@ -485,7 +494,7 @@ __device__ void mma_role(Shared<kBf16, NH>& sh, const Args& a, uint32_t tmem, vo
     const uint64_t dK = smem_desc(smem_u32(sh.kv[0][0]), 16, 1024, kLayoutSw128);
     const uint64_t dQ = smem_desc(smem_u32(sh.q[0]), 16, 1024, kLayoutSw128);
     const uint64_t dV = smem_desc(smem_u32(sh.kv[0][0]), kChunk, 1024, kLayoutSw128);
-    const uint64_t dP = smem_desc(smem_u32(sh.p[0]), 16, 1024, kLayoutSw128);
+    const uint64_t dP = smem_desc(smem_u32(sh.p), 1024, 8 * S::kPRow, S::kPLayout);
     Pieces pi(sh.range);
     Piece pc;
     int g = 0, gt = 0;
@@ -517,7 +526,7 @@ __device__ void mma_role(Shared<kBf16, NH>& sh, const Args& a, uint32_t tmem, vo
 #pragma unroll
                 for (int k = 0; k < 8; ++k)
                     mma_f16(tmem + NH * mb, dV + ((2 * slot * kChunk + k * 2048) >> 4),
-                            dP + (((k >> 2) * NH * 128 + 32 * (k & 3)) >> 4), S::kIdescPV, j != pc.j0 || k != 0);
+                            dP + ((k * 16 * S::kPRow) >> 4), S::kIdescPV, j != pc.j0 || k != 0);
                 tc_commit(&sh.empty[slot]);
             }
         }
@@ -558,23 +567,68 @@ __device__ __forceinline__ float warp_sum(float* v, int lane) {
 }
 
 // Warp (qd, cg): positions 32 qd + lane of the tile, heads cg NC .. + NC - 1. Logits are in
-// the log2 domain. The running maximum is lazy: it moves only when a tile would push P above
-// 2^8, and then those heads' columns of O are rescaled in TMEM.
+// the log2 domain.
+//
+// The running maximum is lazy: it moves only when a tile would push P above 2^kLazyMax. A
+// tile therefore needs no maximum of its own as long as its logits stay below that: the warp
+// takes P from the maximum it has, and the four warps of a head group only agree that none of
+// them saw a larger logit (2,080 -> 900 cycles from S to P against finding each tile's
+// maximum). Where one did, or at a piece's first tile, the maxima are found and exchanged,
+// and the heads' columns of O are rescaled in TMEM.
 template <bool kBf16, int NH>
 __device__ void softmax_role(Shared<kBf16, NH>& sh, const Args& a, uint32_t tmem, int warp, int lane,
                              volatile int* abort) {
     using S = Shape<kBf16, NH>;
     constexpr int NC = S::NC;
+    constexpr float kNone = -3.0e38f;  // m_sub before any logit: whatever is finite exceeds it
     const int qd = warp & 3, cg = warp >> 2, h0 = cg * NC, mine = lane & (NC - 1);
     const int r = 32 * qd + lane;
     const uint32_t tl = tmem + ((uint32_t)(32 * qd) << 16);
-    // P of this position: row h of its chunk, byte (unit ^ (h & 7)) * 16 + 2 (r mod 8)
-    uint8_t* const prow = sh.p[r >> 6] + 2 * (r & 7);
-    const int punit = (r & 63) >> 3;
     const float sink2 = a.sink && h0 + mine < a.heads ? a.sink[h0 + mine] * kLog2e : -INFINITY;
+    float* const m_sub = &sh.m_sub[qd][h0];
+    // x[i] = logit i of this row less `sub` (NULL: nothing), -infinity where nothing is seen
+    auto logits = [&](float* x, const float* sub, int it, bool ok) {
+        uint32_t sv[NC];
+        tmem_ld<NC>(tl + S::kColS + h0, sv);
+#pragma unroll
+        for (int i = 0; i < NC; i += 4) {
+            float4 c = make_float4(a.scale_log2, a.scale_log2, a.scale_log2, a.scale_log2);
+            if constexpr (!kBf16) c = *reinterpret_cast<const float4*>(&sh.col_scale[it & 1][h0 + i]);
+            const float4 m = sub ? *reinterpret_cast<const float4*>(sub + i) : make_float4(0.f, 0.f, 0.f, 0.f);
+            x[i] = ok ? fmaf(__uint_as_float(sv[i]), c.x, -m.x) : -INFINITY;
+            x[i + 1] = ok ? fmaf(__uint_as_float(sv[i + 1]), c.y, -m.y) : -INFINITY;
+            x[i + 2] = ok ? fmaf(__uint_as_float(sv[i + 2]), c.z, -m.z) : -INFINITY;
+            x[i + 3] = ok ? fmaf(__uint_as_float(sv[i + 3]), c.w, -m.w) : -INFINITY;
+        }
+    };
+    // x -> P = 2^x rounded to the matrix type, into the operand; x becomes the rounded values:
+    // the sums take these, so a row's weights add up to one whatever the rounding does
+    auto weights = [&](float* x) {
+#pragma unroll
+        for (int u = 0; u < NC / 8; ++u) {
+            uint32_t w[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                float& p = x[8 * u + 2 * k];
+                float& q = x[8 * u + 2 * k + 1];
+                if constexpr (kBf16) {
+                    const __nv_bfloat162 v = __floats2bfloat162_rn(ex2(p), ex2(q));
+                    w[k] = *reinterpret_cast<const uint32_t*>(&v);
+                    p = __uint_as_float(w[k] << 16);
+                    q = __uint_as_float(w[k] & 0xffff0000u);
+                } else {
+                    const __half2 v = __floats2half2_rn(ex2(p), ex2(q));
+                    w[k] = *reinterpret_cast<const uint32_t*>(&v);
+                    p = __low2float(v);
+                    q = __high2float(v);
+                }
+            }
+            *reinterpret_cast<uint4*>(sh.p + S::p_unit(r, h0 / 8 + u)) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+    };
     Pieces pi(sh.range);
     Piece pc;
-    int g = 0, gt = 0;
+    int g = 0, gt = 0, agreed = 0, moves = 0;
     for (int it = 0; pi.next(a, pc); ++it) {
         if (!mbar_wait(&sh.q_full[it & 1], (uint32_t)((it >> 1) & 1), abort)) return;
         float m_run = -INFINITY;  // running maximum of head h0 + mine
@@ -587,23 +641,6 @@ __device__ void softmax_role(Shared<kBf16, NH>& sh, const Args& a, uint32_t tmem
             if (!mbar_wait(&sh.full[g % S::kPairs], (uint32_t)((g / S::kPairs) & 1), abort)) return;
             tc_fence_after();
             const bool ok = sh.row_ok[gt & 1][r] != 0;
-            float x[NC];
-            {
-                uint32_t sv[NC];
-                tmem_ld<NC>(tl + S::kColS + h0, sv);
-#pragma unroll
-                for (int i = 0; i < NC; ++i) {
-                    const float c = kBf16 ? a.scale_log2 : sh.col_scale[it & 1][h0 + i];
-                    x[i] = ok ? __uint_as_float(sv[i]) * c : -INFINITY;
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < NC; i += 4) {
-                const float4 m4 = make_float4(warp_max(x[i]), warp_max(x[i + 1]), warp_max(x[i + 2]), warp_max(x[i + 3]));
-                if (lane == 0) *reinterpret_cast<float4*>(&sh.red_max[qd][h0 + i]) = m4;
-            }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sh.max_bar[cg]);
             if constexpr (kBf16) {
                 // Rows that are not seen came with the box or are left from another tile:
                 // whatever they hold (NaN among it) must not meet P = 0 in the product. S has
@@ -617,46 +654,60 @@ __device__ void softmax_role(Shared<kBf16, NH>& sh, const Args& a, uint32_t tmem
                     }
                 }
             }
-            if (!mbar_wait(&sh.max_bar[cg], (uint32_t)(gt & 1), abort)) return;
-            const float tm = fmaxf(fmaxf(sh.red_max[0][h0 + mine], sh.red_max[1][h0 + mine]),
-                                   fmaxf(sh.red_max[2][h0 + mine], sh.red_max[3][h0 + mine]));
-            const float m_new = tm > m_run + kLazyMax ? tm : m_run;
-            const float alpha = (m_new != m_run && m_run != -INFINITY) ? ex2(m_run - m_new) : 1.f;
-            const bool rescale = __any_sync(0xffffffffu, alpha != 1.f);
-            m_run = m_new;
-            const float mfix = m_run == -INFINITY ? 0.f : m_run - kLift<kBf16>;
-            if (rescale) {
+            bool move = j == pc.j0;
+            if (!move) {
+                float x[NC];
+                logits(x, m_sub, it, ok);
+                bool over = false;
 #pragma unroll
-                for (int i = 0; i < NC; ++i) lpart[i] *= __shfl_sync(0xffffffffu, alpha, i);
-            }
-            // P = 2^(x - m) (lifted), rounded to the matrix type; the sum takes the rounded values, so
-            // the weights of a row add up to one whatever the rounding does
+                for (int i = 0; i < NC; ++i) over |= x[i] > kLazyMax + kLift<kBf16>;
+                if (__any_sync(0xffffffffu, over) && lane == 0) sh.moved[cg] = gt;
+                weights(x);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh.agree_bar[cg]);
+                if (!mbar_wait(&sh.agree_bar[cg], (uint32_t)(agreed++ & 1), abort)) return;
+                move = *(volatile int*)&sh.moved[cg] == gt;
+                if (!move) {
 #pragma unroll
-            for (int i = 0; i < NC; ++i) {
-                const float p = ex2(x[i] - __shfl_sync(0xffffffffu, mfix, i));
-                uint16_t bits;
-                if constexpr (kBf16) {
-                    bits = __bfloat16_as_ushort(__float2bfloat16_rn(p));
-                    lpart[i] += __uint_as_float((uint32_t)bits << 16);
-                } else {
-                    const __half ph = __float2half_rn(p);
-                    bits = __half_as_ushort(ph);
-                    lpart[i] += __half2float(ph);
+                    for (int i = 0; i < NC; ++i) lpart[i] += x[i];
                 }
-                const int h = h0 + i;
-                *reinterpret_cast<uint16_t*>(prow + h * 128 + ((punit ^ (h & 7)) << 4)) = bits;
             }
-            if (rescale) {  // O holds the tiles before this one (S was issued after them)
+            if (move) {
+                float x[NC];
+                logits(x, nullptr, it, ok);
+#pragma unroll
+                for (int i = 0; i < NC; i += 4) {
+                    const float4 m4 = make_float4(warp_max(x[i]), warp_max(x[i + 1]), warp_max(x[i + 2]), warp_max(x[i + 3]));
+                    if (lane == 0) *reinterpret_cast<float4*>(&sh.red_max[qd][h0 + i]) = m4;
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh.max_bar[cg]);
+                if (!mbar_wait(&sh.max_bar[cg], (uint32_t)(moves++ & 1), abort)) return;
+                const float tm = fmaxf(fmaxf(sh.red_max[0][h0 + mine], sh.red_max[1][h0 + mine]),
+                                       fmaxf(sh.red_max[2][h0 + mine], sh.red_max[3][h0 + mine]));
+                const float m_new = tm > m_run + kLazyMax ? tm : m_run;
+                const float alpha = (m_new != m_run && m_run != -INFINITY) ? ex2(m_run - m_new) : 1.f;
+                const bool rescale = __any_sync(0xffffffffu, alpha != 1.f);
+                m_run = m_new;
+                __syncwarp();
+                if (lane < NC) m_sub[lane] = m_run == -INFINITY ? kNone : m_run - kLift<kBf16>;
+                __syncwarp();
+                logits(x, m_sub, it, ok);
+                weights(x);
+#pragma unroll
+                for (int i = 0; i < NC; ++i) lpart[i] = fmaf(lpart[i], __shfl_sync(0xffffffffu, alpha, i), x[i]);
+                if (rescale) {  // O holds the tiles before this one (S was issued after them)
 #pragma unroll 1
-                for (int mb = 0; mb < 4; ++mb) {
-                    uint32_t ov[NC];
-                    tmem_ld<NC>(tl + NH * mb + h0, ov);
+                    for (int mb = 0; mb < 4; ++mb) {
+                        uint32_t ov[NC];
+                        tmem_ld<NC>(tl + NH * mb + h0, ov);
 #pragma unroll
-                    for (int i = 0; i < NC; ++i)
-                        ov[i] = __float_as_uint(__uint_as_float(ov[i]) * __shfl_sync(0xffffffffu, alpha, i));
-                    tmem_st<NC>(tl + NH * mb + h0, ov);
+                        for (int i = 0; i < NC; ++i)
+                            ov[i] = __float_as_uint(__uint_as_float(ov[i]) * __shfl_sync(0xffffffffu, alpha, i));
+                        tmem_st<NC>(tl + NH * mb + h0, ov);
+                    }
+                    tmem_wait_st();
                 }
-                tmem_wait_st();
             }
             fence_proxy_async_smem();
             tc_fence_before();
@@ -731,7 +782,9 @@ k_paged_attn(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap
             mbar_init(&sh.empty[i], 1);
         }
         for (int i = 0; i < S::kGroups; ++i) {
+            mbar_init(&sh.agree_bar[i], 4);
             mbar_init(&sh.max_bar[i], 4);
+            sh.moved[i] = -1;
             mbar_init(&sh.sum_bar[i], 4);
         }
         sh.abort = 0;
