@@ -488,6 +488,8 @@ __device__ void decode_role(Shared<false, NH>& sh, const Args& a, int pt, int la
 }
 
 // ---------------------------------------------------------------- MMA issuer
+// The whole warp walks the tiles and one elected lane issues: the operands' descriptors are
+// then the warp's (uniform registers), not a thread's that every MMA would have to move there.
 template <bool kBf16, int NH>
 __device__ void mma_role(Shared<kBf16, NH>& sh, const Args& a, uint32_t tmem, volatile int* abort) {
     using S = Shape<kBf16, NH>;
@@ -497,40 +499,56 @@ __device__ void mma_role(Shared<kBf16, NH>& sh, const Args& a, uint32_t tmem, vo
     const uint64_t dP = smem_desc(smem_u32(sh.p), 1024, 8 * S::kPRow, S::kPLayout);
     Pieces pi(sh.range);
     Piece pc;
-    int g = 0, gt = 0;
+    int gt = 0, slot0 = 0;   // tiles so far; slot of the tile's first pair and its phase
+    uint32_t phase0 = 0;
     for (int it = 0; pi.next(a, pc); ++it) {
-        if (!mbar_wait(&sh.q_full[it & 1], (uint32_t)((it >> 1) & 1), abort)) return;
+        if (!mbar_wait_warp(&sh.q_full[it & 1], (uint32_t)((it >> 1) & 1), abort)) return;
         tc_fence_after();
-        for (int j = pc.j0; j < pc.j1; ++j, ++gt, g += 4) {
+        for (int j = pc.j0; j < pc.j1; ++j, ++gt) {
             // S^T = K . Q^T over the 512 channels, pair by pair as they land
+            int slot = slot0;
+            uint32_t phase = phase0;
 #pragma unroll
             for (int pr = 0; pr < 4; ++pr) {
-                const int slot = (g + pr) % S::kPairs;
-                if (!mbar_wait(&sh.full[slot], (uint32_t)(((g + pr) / S::kPairs) & 1), abort)) return;
+                if (!mbar_wait_warp(&sh.full[slot], phase, abort)) return;
                 tc_fence_after();
+                if (elect_one()) {
 #pragma unroll
-                for (int c = 0; c < 2; ++c)
+                    for (int c = 0; c < 2; ++c)
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        mma_f16(tmem + S::kColS, dK + (((2 * slot + c) * kChunk + 32 * k) >> 4),
-                                dQ + (((2 * pr + c) * NH * 128 + 32 * k) >> 4), S::kIdescS, (pr | c | k) != 0);
+                        for (int k = 0; k < 4; ++k)
+                            mma_f16(tmem + S::kColS, dK + (((2 * slot + c) * kChunk + 32 * k) >> 4),
+                                    dQ + (((2 * pr + c) * NH * 128 + 32 * k) >> 4), S::kIdescS, (pr | c | k) != 0);
+                }
+                __syncwarp();
+                if (++slot == S::kPairs) slot = 0, phase ^= 1u;
             }
-            tc_commit(&sh.s_full);
-            if (j == pc.j1 - 1) tc_commit(&sh.q_empty);
+            if (elect_one()) {
+                tc_commit(&sh.s_full);
+                if (j == pc.j1 - 1) tc_commit(&sh.q_empty);
+            }
+            __syncwarp();
             // O^T += V^T . P^T, 128 channels (one pair) at a time
-            if (!mbar_wait(&sh.p_full, (uint32_t)(gt & 1), abort)) return;
+            if (!mbar_wait_warp(&sh.p_full, (uint32_t)(gt & 1), abort)) return;
             tc_fence_after();
+            slot = slot0;
 #pragma unroll
             for (int mb = 0; mb < 4; ++mb) {
-                const int slot = (g + mb) % S::kPairs;
+                if (elect_one()) {
 #pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    mma_f16(tmem + NH * mb, dV + ((2 * slot * kChunk + k * 2048) >> 4),
-                            dP + ((k * 16 * S::kPRow) >> 4), S::kIdescPV, j != pc.j0 || k != 0);
-                tc_commit(&sh.empty[slot]);
+                    for (int k = 0; k < 8; ++k)
+                        mma_f16(tmem + NH * mb, dV + ((2 * slot * kChunk + k * 2048) >> 4),
+                                dP + ((k * 16 * S::kPRow) >> 4), S::kIdescPV, j != pc.j0 || k != 0);
+                    tc_commit(&sh.empty[slot]);
+                }
+                __syncwarp();
+                if (++slot == S::kPairs) slot = 0;
             }
+            slot0 = slot;
+            phase0 = phase;
         }
-        tc_commit(&sh.o_full);
+        if (elect_one()) tc_commit(&sh.o_full);
+        __syncwarp();
     }
 }
 
@@ -803,12 +821,11 @@ k_paged_attn(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap
     if (warp < S::kSoftWarps) {
         softmax_role<kBf16, NH>(sh, a, tmem, warp, lane, abort);
     } else if (warp == S::kMmaWarp) {
-        if (lane == 0) {
-            mma_role<kBf16, NH>(sh, a, tmem, abort);
-            // every MMA issued must finish before TMEM and shared memory are released
-            tc_commit(&sh.drain);
-            if (!mbar_wait_drain(&sh.drain, 0)) *abort = 1;
-        }
+        mma_role<kBf16, NH>(sh, a, tmem, abort);
+        // every MMA issued must finish before TMEM and shared memory are released
+        __syncwarp();
+        if (elect_one()) tc_commit(&sh.drain);
+        if (!mbar_wait_drain(&sh.drain, 0)) *abort = 1;
     } else if constexpr (kBf16) {
         if (warp == S::kProd0) tma_role<NH>(sh, a, &tmap, lane, abort);
         else query_role<NH>(sh, a, tid - 32 * (S::kProd0 + 1), lane, abort);

@@ -55,6 +55,12 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volati
     return false;
 }
 
+// mbar_wait by a whole warp that goes on together: false in every lane if any gave up.
+__device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort) {
+    const bool ok = mbar_wait(bar, parity, abort);
+    return __all_sync(0xffffffffu, ok);
+}
+
 // try_wait with a suspend-time hint: a waiting thread sleeps until the phase
 // completes (or the hint runs out) instead of polling, which leaves the issue
 // slots to the warps doing work. Bounded by the global timer: after about two
