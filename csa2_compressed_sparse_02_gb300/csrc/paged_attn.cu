@@ -318,21 +318,18 @@ template <int NH>
 __device__ void tma_role(Shared<true, NH>& sh, const Args& a, const CUtensorMap* tmap, int lane, volatile int* abort) {
     constexpr int kPairs = Shape<true, NH>::kPairs;
     const uint32_t dst0 = smem_u32(sh.kv[0][0]) + lane * a.box_rows * 128;
+    const int box_bytes = a.box_rows * a.g.row_bytes;
     Tiles it(sh.range);
     int g = 0;  // pairs so far
     bool has = it.next(a), gave_up = false;
     Boxes cur, nxt;
     if (has) cur = boxes_of(a, it, lane);
+    bool has_nx = has && it.next(a);
+    if (has_nx) {
+        nxt = boxes_of(a, it, lane);
+        if (nxt.mine) bulk_prefetch_l2(a.base + (int64_t)nxt.y * a.g.row_bytes, box_bytes);
+    }
     for (int gt = 0; has && !gave_up; ++gt) {
-        // The ring holds little more than a tile, and it stands still between a tile's S and
-        // its PV: the next tile comes into L2 meanwhile, so that the refill is short.
-        const bool has_nx = it.next(a);
-        if (has_nx) {
-            nxt = boxes_of(a, it, lane);
-            if (nxt.mine)
-#pragma unroll
-                for (int c = 0; c < 8; ++c) tma_prefetch_2d(tmap, 64 * c, nxt.y);
-        }
         const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, cur.mine)) * a.box_rows * 256u;
         for (int pr = 0; pr < 4; ++pr, ++g) {
             const int slot = g % kPairs;
@@ -355,8 +352,16 @@ __device__ void tma_role(Shared<true, NH>& sh, const Args& a, const CUtensorMap*
                 tma_g2s_2d(dst + kChunk, tmap, 128 * pr + 64, cur.y, &sh.full[slot]);
             }
         }
+        // The ring holds little more than a tile and stands still between a tile's S and its
+        // PV. The tile after the next comes into L2 meanwhile, so that HBM does not stand still
+        // too and the refill is short.
         cur = nxt;
         has = has_nx;
+        has_nx = has && it.next(a);
+        if (has_nx) {
+            nxt = boxes_of(a, it, lane);
+            if (nxt.mine) bulk_prefetch_l2(a.base + (int64_t)nxt.y * a.g.row_bytes, box_bytes);
+        }
     }
     // whatever ended the loop, no copy of this CTA outlives it
     for (int s = max(0, g - kPairs); s < g; ++s) mbar_wait_drain(&sh.full[s % kPairs], (uint32_t)((s / kPairs) & 1));

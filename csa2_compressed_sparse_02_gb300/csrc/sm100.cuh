@@ -211,10 +211,9 @@ __device__ __forceinline__ void tma_g2s_2d(uint32_t smem_dst, const void* tmap, 
         : "memory");
 }
 
-// The same box into L2 only.
-__device__ __forceinline__ void tma_prefetch_2d(const void* tmap, int x, int y) {
-    asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];\n" ::"l"(tmap), "r"(x), "r"(y)
-                 : "memory");
+// Consecutive bytes into L2 only; address and size are multiples of 16.
+__device__ __forceinline__ void bulk_prefetch_l2(const void* gsrc, uint32_t bytes) {
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;\n" ::"l"(gsrc), "r"(bytes) : "memory");
 }
 
 // 16 bytes global -> shared by the calling thread, zeros when !pred (nothing is read then).
