@@ -108,42 +108,53 @@ __device__ void plan(const Args& a, Range* sh) {
     __shared__ int64_t warp_sum[32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
     const bool lead = blockIdx.x == 0;
-    int64_t total = 0, at = 0, end = 0;
-    for (int pass = 0; pass < 2; ++pass) {  // the sum of all items, then the place of this range
-        int64_t before = 0;
-        for (int b0 = 0; b0 < a.B; b0 += blockDim.x) {
-            const int b = b0 + tid;
-            const int64_t n = b < a.B ? view_of(a, b, lead && pass == 0).tiles : 0;
-            int64_t inc = n;
+    // Exclusive sum of n over the CTA, and the sum of all.
+    auto scan = [&](int64_t n, int64_t* all) {
+        int64_t inc = n;
 #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int64_t up = __shfl_up_sync(0xffffffffu, inc, o);
-                if (lane >= o) inc += up;
-            }
-            if (lane == 31) warp_sum[warp] = inc;
-            __syncthreads();
-            int64_t here = before, all = 0;
-            for (int w = 0; w < warps; ++w) {
-                if (w < warp) here += warp_sum[w];
-                all += warp_sum[w];
-            }
-            __syncthreads();
-            here += inc - n;
-            if (pass == 1 && b < a.B) {
-                if (at >= here && at < here + n) {
-                    sh->b = b;
-                    sh->j = (int)(at - here);
-                }
-                if (lead) a.prefix[b] = here;
-            }
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t up = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += up;
+        }
+        if (lane == 31) warp_sum[warp] = inc;
+        __syncthreads();
+        const int64_t w = lane < warps ? warp_sum[lane] : 0;
+        int64_t before = lane < warp ? w : 0, sum = w;
+#pragma unroll
+        for (int o = 16; o >= 1; o >>= 1) {
+            before += __shfl_xor_sync(0xffffffffu, before, o);
+            sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        }
+        __syncthreads();
+        *all = sum;
+        return before + inc - n;
+    };
+    // The first sweep finds the total; a batch of at most a CTA's threads needs no second.
+    int64_t total = 0, n = 0, here = 0;
+    for (int b0 = 0; b0 < a.B; b0 += blockDim.x) {
+        n = b0 + tid < a.B ? view_of(a, b0 + tid, lead).tiles : 0;
+        int64_t all;
+        here = total + scan(n, &all);
+        total += all;
+    }
+    const Cut cut(total, a.ctas);
+    const int c = min((int)blockIdx.x, cut.n);
+    const int64_t at = cut.at(c), end = cut.at(min(c + 1, cut.n));
+    int64_t before = 0;
+    for (int b0 = 0; b0 < a.B; b0 += blockDim.x) {
+        const int b = b0 + tid;
+        if (a.B > (int)blockDim.x) {
+            n = b < a.B ? view_of(a, b, false).tiles : 0;
+            int64_t all;
+            here = before + scan(n, &all);
             before += all;
         }
-        if (pass == 0) {
-            total = before;
-            const Cut cut(total, a.ctas);
-            const int c = min((int)blockIdx.x, cut.n);
-            at = cut.at(c);
-            end = cut.at(min(c + 1, cut.n));
+        if (b < a.B) {
+            if (at >= here && at < here + n) {
+                sh->b = b;
+                sh->j = (int)(at - here);
+            }
+            if (lead) a.prefix[b] = here;
         }
     }
     if (tid == 0) {
@@ -207,14 +218,14 @@ struct Shared {
     float col_scale[2][kMaxHeads];     // E4M3: per-head logit factor, by piece parity
     float red_max[4][kMaxHeads];
     float m_sub[4][kMaxHeads];         // per lane quarter: what its logits are reduced by
-    int moved[S::kGroups];             // the last tile whose maximum had to move
+    int moved[4];                      // per head group: the last tile whose maximum had to move
     float red_sum[4][kMaxHeads];
     uint8_t row_ok[2][kTile];          // by tile parity: the row holds a position that is seen
     // q_full: two barriers, so that a producer can publish the next piece's query before a
     // softmax warp has waited on this one (a one-tile piece needs no softmax before its S ends)
     uint64_t q_full[2], q_empty, s_full, p_full, o_full, drain;
     uint64_t full[S::kPairs], empty[S::kPairs];
-    uint64_t agree_bar[S::kGroups], max_bar[S::kGroups], sum_bar[S::kGroups];
+    uint64_t p_again, max_bar[S::kGroups], sum_bar[S::kGroups];
     Range range;
     uint32_t tmem_base;
     int abort;
@@ -492,6 +503,16 @@ __device__ void decode_role(Shared<false, NH>& sh, const Args& a, int pt, int la
     }
 }
 
+// Whether a head group's maximum moved at tile gt (read after p_full of that tile).
+template <bool kBf16, int NH>
+__device__ __forceinline__ bool any_moved(Shared<kBf16, NH>& sh, int gt) {
+    const volatile int* m = sh.moved;
+    bool any = m[0] == gt;
+#pragma unroll
+    for (int i = 1; i < Shape<kBf16, NH>::kGroups; ++i) any |= m[i] == gt;
+    return any;
+}
+
 // ---------------------------------------------------------------- MMA issuer
 // The whole warp walks the tiles and one elected lane issues: the operands' descriptors are
 // then the warp's (uniform registers), not a thread's that every MMA would have to move there.
@@ -504,7 +525,7 @@ __device__ void mma_role(Shared<kBf16, NH>& sh, const Args& a, uint32_t tmem, vo
     const uint64_t dP = smem_desc(smem_u32(sh.p), 1024, 8 * S::kPRow, S::kPLayout);
     Pieces pi(sh.range);
     Piece pc;
-    int gt = 0, slot0 = 0;   // tiles so far; slot of the tile's first pair and its phase
+    int gt = 0, again = 0, slot0 = 0;  // tiles so far, those whose P came twice; slot of the tile's first pair and its phase
     uint32_t phase0 = 0;
     for (int it = 0; pi.next(a, pc); ++it) {
         if (!mbar_wait_warp(&sh.q_full[it & 1], (uint32_t)((it >> 1) & 1), abort)) return;
@@ -535,6 +556,7 @@ __device__ void mma_role(Shared<kBf16, NH>& sh, const Args& a, uint32_t tmem, vo
             __syncwarp();
             // O^T += V^T . P^T, 128 channels (one pair) at a time
             if (!mbar_wait_warp(&sh.p_full, (uint32_t)(gt & 1), abort)) return;
+            if (any_moved(sh, gt) && !mbar_wait_warp(&sh.p_again, (uint32_t)(again++ & 1), abort)) return;
             tc_fence_after();
             slot = slot0;
 #pragma unroll
@@ -596,7 +618,8 @@ __device__ __forceinline__ float warp_sum(float* v, int lane) {
 // tile therefore needs no maximum of its own as long as its logits stay below that: the warp
 // takes P from the maximum it has, and the four warps of a head group only agree that none of
 // them saw a larger logit (2,080 -> 900 cycles from S to P against finding each tile's
-// maximum). Where one did, or at a piece's first tile, the maxima are found and exchanged,
+// maximum). The agreement rides on the barrier that hands P to the MMAs: an issuer that finds
+// a group's mark set waits for that group's second P. Where one did, or at a piece's first tile, the maxima are found and exchanged,
 // and the heads' columns of O are rescaled in TMEM.
 template <bool kBf16, int NH>
 __device__ void softmax_role(Shared<kBf16, NH>& sh, const Args& a, uint32_t tmem, int warp, int lane,
@@ -651,7 +674,7 @@ __device__ void softmax_role(Shared<kBf16, NH>& sh, const Args& a, uint32_t tmem
     };
     Pieces pi(sh.range);
     Piece pc;
-    int g = 0, gt = 0, agreed = 0, moves = 0;
+    int g = 0, gt = 0, moves = 0;
     for (int it = 0; pi.next(a, pc); ++it) {
         if (!mbar_wait(&sh.q_full[it & 1], (uint32_t)((it >> 1) & 1), abort)) return;
         float m_run = -INFINITY;  // running maximum of head h0 + mine
@@ -677,18 +700,23 @@ __device__ void softmax_role(Shared<kBf16, NH>& sh, const Args& a, uint32_t tmem
                     }
                 }
             }
-            bool move = j == pc.j0;
-            if (!move) {
+            const bool opens = j == pc.j0;
+            bool move = opens, any = false;
+            if (!opens) {
                 float x[NC];
                 logits(x, m_sub, it, ok);
                 bool over = false;
 #pragma unroll
                 for (int i = 0; i < NC; ++i) over |= x[i] > kLazyMax + kLift<kBf16>;
-                if (__any_sync(0xffffffffu, over) && lane == 0) sh.moved[cg] = gt;
+                if (__any_sync(0xffffffffu, over) && lane == 0) *(volatile int*)&sh.moved[cg] = gt;
                 weights(x);
+                fence_proxy_async_smem();
+                tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&sh.agree_bar[cg]);
-                if (!mbar_wait(&sh.agree_bar[cg], (uint32_t)(agreed++ & 1), abort)) return;
+                if (lane == 0) mbar_arrive(&sh.p_full);
+                // the MMA issuer goes on with this P unless a group found a larger logit
+                if (!mbar_wait(&sh.p_full, (uint32_t)(gt & 1), abort)) return;
+                any = any_moved(sh, gt);
                 move = *(volatile int*)&sh.moved[cg] == gt;
                 if (!move) {
 #pragma unroll
@@ -696,6 +724,7 @@ __device__ void softmax_role(Shared<kBf16, NH>& sh, const Args& a, uint32_t tmem
                 }
             }
             if (move) {
+                tc_fence_after();
                 float x[NC];
                 logits(x, nullptr, it, ok);
 #pragma unroll
@@ -731,11 +760,15 @@ __device__ void softmax_role(Shared<kBf16, NH>& sh, const Args& a, uint32_t tmem
                     }
                     tmem_wait_st();
                 }
+                fence_proxy_async_smem();
+                tc_fence_before();
+                __syncwarp();
             }
-            fence_proxy_async_smem();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sh.p_full);
+            if (opens) {
+                if (lane == 0) mbar_arrive(&sh.p_full);
+            } else if (any) {
+                if (lane == 0) mbar_arrive(&sh.p_again);
+            }
         }
         if (!mbar_wait(&sh.o_full, (uint32_t)(it & 1), abort)) return;
         tc_fence_after();
@@ -798,6 +831,7 @@ k_paged_attn(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap
         mbar_init(&sh.q_empty, 1);
         mbar_init(&sh.s_full, 1);
         mbar_init(&sh.p_full, S::kSoftWarps);
+        mbar_init(&sh.p_again, S::kSoftWarps);
         mbar_init(&sh.o_full, 1);
         mbar_init(&sh.drain, 1);
         for (int i = 0; i < S::kPairs; ++i) {
@@ -805,11 +839,11 @@ k_paged_attn(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap
             mbar_init(&sh.empty[i], 1);
         }
         for (int i = 0; i < S::kGroups; ++i) {
-            mbar_init(&sh.agree_bar[i], 4);
             mbar_init(&sh.max_bar[i], 4);
-            sh.moved[i] = -1;
+
             mbar_init(&sh.sum_bar[i], 4);
         }
+        for (int i = 0; i < 4; ++i) sh.moved[i] = -1;
         sh.abort = 0;
         fence_mbar_init();
     }
@@ -817,7 +851,9 @@ k_paged_attn(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap
         tmem_alloc(&sh.tmem_base, kTmemCols);
         tmem_relinquish();
     }
-    // a programmatic launch: only the setup above may overlap the kernel ahead
+    // a programmatic launch: only the setup above may overlap the kernel ahead; the join's
+    // CTAs may be placed from now on, and wait for this grid's end
+    grid_dep_launch_dependents();
     grid_dep_wait();
     tc_fence_before();
     plan(a, &sh.range);  // ends with a CTA barrier
@@ -858,7 +894,7 @@ static_assert(smem_bytes<true, 64>() <= 232448 && smem_bytes<true, 32>() <= 2324
 // One warp per (sequence, head), lane = 16 channels in four groups of four. Sequences that
 // no range boundary cuts were finished by the attention kernel; those that see nothing get
 // their zeros here.
-constexpr int kJoinWarps = 8;
+constexpr int kJoinWarps = 4;
 __global__ void __launch_bounds__(32 * kJoinWarps) k_paged_join(Args a) {
     grid_dep_wait();
     const int lane = threadIdx.x & 31, b = blockIdx.x, h = blockIdx.y * kJoinWarps + (threadIdx.x >> 5);
