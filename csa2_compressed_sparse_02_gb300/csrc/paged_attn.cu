@@ -37,7 +37,8 @@ struct Args {
     int32_t* dev_status;
     float scale_log2;
     int ctas;         // of the attention kernel (the join needs its ranges)
-    int box_rows;     // rows of a copied box: divides 128 and the page size
+    int box_rows;     // rows of a copied box, 2^box_shift: divides 128 and the page size
+    int box_shift;
 };
 
 // O [heads][512], then m [heads] and l [heads]; a multiple of four, as the join reads float4
@@ -56,8 +57,9 @@ struct View {
 
 __device__ __forceinline__ View view_of(const Args& a, int b, bool report) {
     View v;
+    int T = a.n_tokens[b];  // (the two loads do not wait for each other)
     v.row = a.seq ? a.seq[b] : b;
-    int T = v.row < 0 ? 0 : a.n_tokens[b];
+    if (v.row < 0) T = 0;
     if (v.row >= a.g.max_seqs) {
         if (report) raise_status(a.dev_status, CSA2_DEV_BAD_INDEX);
         T = 0;
@@ -180,8 +182,8 @@ struct Shape {
     static constexpr int NC = NH / kGroups;         // heads of a softmax warp
     static constexpr int kMmaWarp = kSoftWarps;
     static constexpr int kProd0 = kSoftWarps + 1;   // first producer warp
-    static constexpr int kProdWarps = kBf16 ? 4 : 8;
-    static constexpr int kQueryWarps = kBf16 ? 3 : 8;  // of them, those that stage the query
+    static constexpr int kProdWarps = kBf16 ? 5 : 8;
+    static constexpr int kQueryWarps = kBf16 ? 4 : 8;  // of them, those that stage the query
     static constexpr int kThreads = 32 * (kProd0 + kProdWarps);
     // Pairs of 64-channel chunks of a tile in the ring: a tile has 4; what the query leaves
     // of shared memory lets the next tile's first pairs arrive early.
@@ -299,28 +301,28 @@ __device__ __forceinline__ float warp_max(float v) {
 // the swizzled operand; boxes that hold nothing seen are left out.
 struct Boxes {
     uint32_t rows[4];  // the tile's rows that hold a seen position
-    bool mine;         // this lane's box is copied: rows 'first' on, the pool's row y on
+    bool mine;         // this lane's box is copied: it begins at the pool's row y
     int y;
 };
 __device__ __forceinline__ Boxes boxes_of(const Args& a, const Tiles& t, int lane) {
     Boxes x;
-    const uint32_t ps = a.g.page_size, t0 = t.pc.v.start(t.j);
-    const int32_t* table = a.g.table + (int64_t)t.pc.v.row * a.g.max_pages;
-#pragma unroll
-    for (int w = 0; w < 4; ++w) {
-        const uint32_t p = t0 + 32 * w + lane;
-        x.rows[w] = __ballot_sync(0xffffffffu, t.pc.v.sees(p) && page_of(a, table, p) >= 0);
-    }
+    const View& v = t.pc.v;
+    const uint32_t ps = a.g.page_size, t0 = v.start(t.j), br = a.box_rows;
     // lane i has box i: box_rows divides 128 and the page size, so a box lies in one page
-    const int first = lane * a.box_rows;
+    const uint32_t p = t0 + lane * br;
+    const bool any = lane * br < kTile && (p < v.nf || (p < v.T && p + br > v.lo));
     x.mine = false;
     x.y = 0;
-    if (first < kTile) {
-        const uint32_t m = a.box_rows >= 32 ? 0xffffffffu : ((1u << a.box_rows) - 1u) << (first & 31);
+    if (any) {
+        const int page = page_of(a, a.g.table + (int64_t)v.row * a.g.max_pages, p);
+        x.mine = page >= 0;
+        x.y = page * (int)ps + (int)(p % ps);
+    }
+    const uint32_t held = __ballot_sync(0xffffffffu, x.mine);
 #pragma unroll
-        for (int w = 0; w < 4; ++w)
-            if (w >= first >> 5 && w <= (first + a.box_rows - 1) >> 5) x.mine |= (x.rows[w] & m) != 0;
-        if (x.mine) x.y = table[(t0 + first) / ps] * (int)ps + (int)((t0 + first) % ps);
+    for (int w = 0; w < 4; ++w) {
+        const uint32_t row = 32 * w + lane;
+        x.rows[w] = __ballot_sync(0xffffffffu, v.sees(t0 + row) && ((held >> (row >> a.box_shift)) & 1u));
     }
     return x;
 }
@@ -381,16 +383,18 @@ __device__ void tma_role(Shared<true, NH>& sh, const Args& a, const CUtensorMap*
 template <int NH>
 __device__ void query_role(Shared<true, NH>& sh, const Args& a, int pt, int lane, volatile int* abort) {
     constexpr int kStagers = 32 * Shape<true, NH>::kQueryWarps;
+    static_assert(kStagers == 128, "a thread stages unit pt mod 64 of every other head");
+    const int u = pt & 63, hb = pt >> 6;
     Pieces pi(sh.range);
     Piece pc;
     for (int it = 0; pi.next(a, pc); ++it) {
         if (it > 0 && !mbar_wait(&sh.q_empty, (uint32_t)((it - 1) & 1), abort)) return;
         __syncwarp();
-        const __nv_bfloat16* q = a.q + pc.b * a.q_seq;
-        for (int i = pt; i < NH * 64; i += kStagers) {
-            const int h = i >> 6, u = i & 63;
-            cp_async_16(smem_u32(sh.q[u >> 3]) + sw128(h, u & 7), q + (h < a.heads ? h * a.q_head + 8 * u : 0), h < a.heads);
-        }
+        const __nv_bfloat16* src = a.q + pc.b * a.q_seq + hb * a.q_head + 8 * u;
+        const uint32_t dst = smem_u32(sh.q[u >> 3]);
+#pragma unroll 4
+        for (int h = hb; h < NH; h += 2, src += 2 * a.q_head)
+            cp_async_16(dst + sw128(h, u & 7), h < a.heads ? src : a.q, h < a.heads);
         cp_async_wait_all();
         fence_proxy_async_smem();
         __syncwarp();
@@ -696,7 +700,7 @@ __device__ void softmax_role(Shared<kBf16, NH>& sh, const Args& a, uint32_t tmem
                     for (int c = cg * (8 / S::kGroups); c < (cg + 1) * (8 / S::kGroups); ++c) {
                         uint4* z = reinterpret_cast<uint4*>(sh.kv[(g + (c >> 1)) % S::kPairs][c & 1] + r * 128);
 #pragma unroll
-                        for (int u = 0; u < 8; ++u) z[u] = make_uint4(0u, 0u, 0u, 0u);
+                        for (int u = 0; u < 8; ++u) z[(u + lane) & 7] = make_uint4(0u, 0u, 0u, 0u);  // all banks
                     }
                 }
             }
@@ -920,18 +924,29 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_paged_join(Args a) {
     float4 acc[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int c = c0; c <= c1; ++c) {
-        const float* p = part_of(a, c, c == c0 ? slot0 : 0);
-        const float m = p[mo];
-        const float f = m == -INFINITY ? 0.f : ex2(m - M);
-        den = fmaf(p[lo], f, den);
+    for (int b0 = c0; b0 <= c1; b0 += 32) {  // 32 pieces at a time, lane = piece for the factors
+        const int c = b0 + lane;
+        float f = 0.f, l = 0.f;
+        if (c <= c1) {
+            const float* p = part_of(a, c, c == c0 ? slot0 : 0);
+            const float m = p[mo];
+            f = m == -INFINITY ? 0.f : ex2(m - M);
+            l = p[lo] * f;
+        }
+        const int n = min(32, c1 - b0 + 1);
+#pragma unroll 4
+        for (int i = 0; i < n; ++i) {
+            const float fi = __shfl_sync(0xffffffffu, f, i);
+            den += __shfl_sync(0xffffffffu, l, i);
+            const float* p = part_of(a, b0 + i, b0 + i == c0 ? slot0 : 0) + (int64_t)h * kD + 4 * lane;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const float4 v = *reinterpret_cast<const float4*>(p + (int64_t)h * kD + 4 * lane + 128 * k);
-            acc[k].x = fmaf(v.x, f, acc[k].x);
-            acc[k].y = fmaf(v.y, f, acc[k].y);
-            acc[k].z = fmaf(v.z, f, acc[k].z);
-            acc[k].w = fmaf(v.w, f, acc[k].w);
+            for (int k = 0; k < 4; ++k) {
+                const float4 v = __ldcg(reinterpret_cast<const float4*>(p + 128 * k));
+                acc[k].x = fmaf(v.x, fi, acc[k].x);
+                acc[k].y = fmaf(v.y, fi, acc[k].y);
+                acc[k].z = fmaf(v.z, fi, acc[k].z);
+                acc[k].w = fmaf(v.w, fi, acc[k].w);
+            }
         }
     }
     const float inv = den == 0.f ? 0.f : 1.f / den;
@@ -1055,6 +1070,7 @@ extern "C" int csa2_paged_attn(const csa2_params* p, const csa2_pages* c, int la
     a.ctas = ctas;
     a.box_rows = a.g.page_size & -a.g.page_size;
     if (a.box_rows > kTile) a.box_rows = kTile;
+    while ((1 << a.box_shift) < a.box_rows) ++a.box_shift;
     CUtensorMap rows = {};
     if (p->kv_format == CSA2_BF16)
         if (const int rc = encode_rows(a, &rows)) return rc;
