@@ -209,140 +209,127 @@ def sparse_attn_noalloc(params, q, sink, win_ptrs, n_tokens, comp_ptrs, comp_sca
 
 # --------------------------------------------------------------------------- paged cache
 # These calls check what the pointers stand for (types, shapes, devices, strides) before
-# they hand them on; everything else is checked by the library.
+# they hand them on; everything else is checked by the library. A decode step's kernels run
+# for a few microseconds each, so the checks are kept to what costs tenths of one.
 _FORMATS = {torch.bfloat16: BF16, torch.float32: F32}
+_raw_stream = torch._C._cuda_getCurrentRawStream  # of a device index, without a Stream object
 
 
 def _fail(what):
     raise Csa2Error(what)
 
 
-def _on(device, **tensors):
-    """All tensors on `device`, which is made the current one by the caller's `with`."""
-    for name, t in tensors.items():
-        if t is not None and t.device != device:
-            _fail("%s is on %s, the call's other tensors on %s" % (name, t.device, device))
-
-
-def _i32(name, t, n):
-    if t.dtype != torch.int32 or t.dim() != 1 or t.numel() != n or not (n <= 1 or t.stride(0) == 1):
+def _i32(name, t, n, index):
+    """Address of a contiguous int32 tensor of n elements on device `index`."""
+    if t.dtype is not torch.int32 or t.numel() != n or not t.is_contiguous():
         _fail("%s must be a contiguous int32 tensor of %d elements" % (name, n))
+    if t.get_device() != index:
+        _fail("%s is on %s, the call's other tensors on cuda:%d" % (name, t.device, index))
     return t.data_ptr()
 
 
-def _status(t):
+def _at(name, t, index):
+    if t.get_device() != index:
+        _fail("%s is on %s, the call's other tensors on cuda:%d" % (name, t.device, index))
+    return t.data_ptr()
+
+
+def _status(t, index):
     if t is None:
         return None
-    if t.dtype != torch.int32 or t.numel() < 1:
+    if t.dtype is not torch.int32 or t.numel() < 1:
         _fail("dev_status must be an int32 tensor")
-    return t.data_ptr()
+    return _at("dev_status", t, index)
 
 
-class _Call:
-    """The device of a call's tensors as the current one, and the stream it runs on."""
-
-    def __init__(self, device, stream):
-        if device.type != "cuda":
-            _fail("expected a CUDA tensor")
-        self.index, self.stream, self.back = device.index, stream, None
-
-    def __enter__(self):
-        now = torch.cuda.current_device()
-        if now != self.index:
-            self.back = now
-            torch.cuda.set_device(self.index)
-        s = torch.cuda.current_stream() if self.stream is None else self.stream
-        return s.cuda_stream
-
-    def __exit__(self, *exc):
-        if self.back is not None:
-            torch.cuda.set_device(self.back)
+def _run(name, index, stream, fn, *args):
+    """fn(*args, stream) with device `index` current, on `stream` or the device's current one."""
+    if index < 0:
+        _fail("expected a CUDA tensor")
+    if torch.cuda.current_device() != index:
+        with torch.cuda.device(index):
+            return _run(name, index, stream, fn, *args)
+    rc = fn(*args, _raw_stream(index) if stream is None else stream.cuda_stream)
+    if rc:
+        check(rc, name)
 
 
 def rope(params, x, pos, out=None, layout=ROPE_PAIRS, first=-1, inverse=False, stream=None):
     """Rotary embedding (csa2_rope): x [N, heads, channels] bf16 or fp32 with contiguous
     channels, pos [N] int32; out as x (None: a new tensor; x itself: in place).
     inverse=True turns back, which is also the gradient of the call. Returns out."""
-    if x.dim() != 3 or x.dtype not in _FORMATS:
+    dt = x.dtype
+    if x.dim() != 3 or dt not in _FORMATS:
         _fail("rope: x must be [N, heads, channels], bf16 or fp32")
     if out is None:
         out = torch.empty_like(x, memory_format=torch.contiguous_format)
-    if out.shape != x.shape or out.dtype != x.dtype:
+    N, heads, ch = shape = x.shape
+    if out.shape != shape or out.dtype is not dt:
         _fail("rope: out must have x's shape and type")
-    N, heads, ch = x.shape
     if N == 0 or heads == 0:
         return out
     xs, os_ = x.stride(), out.stride()
     if (xs[2] != 1 or os_[2] != 1) and ch > 1:
         _fail("rope: the channels of x and out must be contiguous")
-    _on(x.device, out=out, pos=pos)
-    with _Call(x.device, stream) as s:
-        check(lib().csa2_rope(ctypes.byref(params), layout, int(inverse), N, heads, ch, first,
-                              _FORMATS[x.dtype], x.data_ptr(), xs[0], xs[1], out.data_ptr(), os_[0],
-                              os_[1], _i32("pos", pos, N), s), "rope")
+    dev = x.get_device()
+    _run("rope", dev, stream, lib().csa2_rope, params, layout, int(inverse), N, heads, ch, first,
+         _FORMATS[dt], x.data_ptr(), xs[0], xs[1], _at("out", out, dev), os_[0], os_[1],
+         _i32("pos", pos, N, dev))
     return out
 
 
 def page_reserve(params, cache, seq, n_from, n_to, dev_status=None, stream=None):
     """Give sequences seq [N] the pages of positions n_from .. n_to-1 (csa2_page_reserve)."""
-    N, ws = seq.numel(), cache.workspace
-    _on(cache.device, seq=seq, n_from=n_from, n_to=n_to, dev_status=dev_status)
-    with _Call(cache.device, stream) as s:
-        check(lib().csa2_page_reserve(
-            ctypes.byref(params), cache.ref_c, N, _i32("seq", seq, N), _i32("n_from", n_from, N),
-            _i32("n_to", n_to, N), ws.data_ptr(), ws.numel(), _status(dev_status), s), "page_reserve")
+    N, dev = seq.numel(), cache.index
+    _run("page_reserve", dev, stream, lib().csa2_page_reserve, params, cache.c, N,
+         _i32("seq", seq, N, dev), _i32("n_from", n_from, N, dev), _i32("n_to", n_to, N, dev),
+         cache.ws_ptr, cache.ws_bytes, _status(dev_status, dev))
 
 
 def page_release(params, cache, seq, n_tokens=None, window=0, n_first=0, dev_status=None, stream=None):
     """Let go of every page of sequences seq [N], or with n_tokens [N] of those that no later
     token sees through window and n_first (csa2_page_release)."""
-    N = seq.numel()
-    _on(cache.device, seq=seq, n_tokens=n_tokens, dev_status=dev_status)
-    with _Call(cache.device, stream) as s:
-        check(lib().csa2_page_release(
-            ctypes.byref(params), cache.ref_c, N, _i32("seq", seq, N),
-            None if n_tokens is None else _i32("n_tokens", n_tokens, N), window, n_first,
-            _status(dev_status), s), "page_release")
+    N, dev = seq.numel(), cache.index
+    _run("page_release", dev, stream, lib().csa2_page_release, params, cache.c, N,
+         _i32("seq", seq, N, dev), None if n_tokens is None else _i32("n_tokens", n_tokens, N, dev),
+         window, n_first, _status(dev_status, dev))
 
 
 def page_fork(params, cache, parent, child, n_tokens, dev_status=None, stream=None):
     """child[i] continues the first n_tokens[i] positions of parent[i] (csa2_page_fork)."""
-    N, ws = child.numel(), cache.workspace
-    _on(cache.device, parent=parent, child=child, n_tokens=n_tokens, dev_status=dev_status)
-    with _Call(cache.device, stream) as s:
-        check(lib().csa2_page_fork(
-            ctypes.byref(params), cache.ref_c, N, _i32("parent", parent, N), _i32("child", child, N),
-            _i32("n_tokens", n_tokens, N), ws.data_ptr(), ws.numel(), _status(dev_status), s), "page_fork")
+    N, dev = child.numel(), cache.index
+    _run("page_fork", dev, stream, lib().csa2_page_fork, params, cache.c, N,
+         _i32("parent", parent, N, dev), _i32("child", child, N, dev),
+         _i32("n_tokens", n_tokens, N, dev), cache.ws_ptr, cache.ws_bytes, _status(dev_status, dev))
 
 
 def page_compact(params, cache, n_used=None, dev_status=None, stream=None):
     """Move the used pages to the front of the pool (csa2_page_compact); n_used [1] int32
     receives their number."""
-    ws = cache.workspace
-    _on(cache.device, n_used=n_used, dev_status=dev_status)
-    with _Call(cache.device, stream) as s:
-        check(lib().csa2_page_compact(
-            ctypes.byref(params), cache.ref_c, None if n_used is None else _i32("n_used", n_used, 1),
-            ws.data_ptr(), ws.numel(), _status(dev_status), s), "page_compact")
+    dev = cache.index
+    _run("page_compact", dev, stream, lib().csa2_page_compact, params, cache.c,
+         None if n_used is None else _i32("n_used", n_used, 1, dev), cache.ws_ptr, cache.ws_bytes,
+         _status(dev_status, dev))
 
 
 def page_write(params, cache, layer, x, seq, pos, dev_status=None, stream=None):
     """Write rows x [N, 512] (fp32 or bf16) as positions pos [N] of sequences seq [N]
     (csa2_page_write), turned first when params.rope_dim > 0."""
-    if x.dim() != 2 or x.shape[1] != D or x.dtype not in _FORMATS or x.stride(1) != 1:
+    dt = x.dtype
+    if x.dim() != 2 or x.shape[1] != D or dt not in _FORMATS or x.stride(1) != 1:
         _fail("page_write: x must be [N, %d], bf16 or fp32, with contiguous rows" % D)
-    N = x.shape[0]
-    _on(cache.device, x=x, seq=seq, pos=pos, dev_status=dev_status)
-    with _Call(cache.device, stream) as s:
-        check(lib().csa2_page_write(
-            ctypes.byref(params), cache.ref_c, layer, N, x.data_ptr(), _FORMATS[x.dtype], x.stride(0),
-            _i32("seq", seq, N), _i32("pos", pos, N), _status(dev_status), s), "page_write")
+    N, dev = x.shape[0], cache.index
+    _run("page_write", dev, stream, lib().csa2_page_write, params, cache.c, layer, N,
+         _at("x", x, dev), _FORMATS[dt], x.stride(0), _i32("seq", seq, N, dev),
+         _i32("pos", pos, N, dev), _status(dev_status, dev))
 
 
 def paged_attn_workspace(params, cache, B):
     """Workspace tensor of paged_attn for batches of up to B sequences."""
-    with _Call(cache.device, None):
-        n = lib().csa2_paged_attn_workspace_size(ctypes.byref(params), cache.ref_c, B)
+    if cache.index < 0:
+        _fail("expected a CUDA tensor")
+    with torch.cuda.device(cache.index):
+        n = lib().csa2_paged_attn_workspace_size(params, cache.c, B)
     return torch.empty(max(int(n), 256), dtype=torch.uint8, device=cache.device)
 
 
@@ -352,23 +339,22 @@ def paged_attn(params, cache, layer, q, sink, seq, n_tokens, out, workspace, win
     q [B, heads, 512] bf16 with contiguous channels, sink [heads] fp32 or None, seq [B] int32
     or None (row b of the table), n_tokens [B] int32, out [B, heads, 512] bf16. A window of 0
     sees everything; n_first positions stay visible before it."""
-    if q.dim() != 3 or q.dtype != torch.bfloat16 or q.shape[2] != D or q.stride(2) != 1:
+    shape = q.shape
+    if len(shape) != 3 or q.dtype is not torch.bfloat16 or shape[2] != D or q.stride(2) != 1:
         _fail("paged_attn: q must be [B, heads, %d] bf16 with contiguous channels" % D)
-    B, heads = q.shape[0], q.shape[1]
+    B, heads, _ = shape
     if heads != params.heads:
         _fail("paged_attn: q has %d heads, the parameters say %d" % (heads, params.heads))
-    if out.shape != q.shape or out.dtype != torch.bfloat16 or not out.is_contiguous():
+    if out.shape != shape or out.dtype is not torch.bfloat16 or not out.is_contiguous():
         _fail("paged_attn: out must be contiguous bf16 of q's shape")
-    if sink is not None and (sink.dtype != torch.float32 or sink.numel() != heads or not sink.is_contiguous()):
+    if sink is not None and (sink.dtype is not torch.float32 or sink.numel() != heads or not sink.is_contiguous()):
         _fail("paged_attn: sink must be %d contiguous fp32 values" % heads)
-    _on(cache.device, q=q, sink=sink, seq=seq, n_tokens=n_tokens, out=out, workspace=workspace,
-        dev_status=dev_status)
-    with _Call(cache.device, stream) as s:
-        check(lib().csa2_paged_attn(
-            ctypes.byref(params), cache.ref_c, layer, B, q.data_ptr(), q.stride(0), q.stride(1),
-            None if sink is None else sink.data_ptr(), None if seq is None else _i32("seq", seq, B),
-            _i32("n_tokens", n_tokens, B), window, n_first, out.data_ptr(), workspace.data_ptr(),
-            workspace.numel() * workspace.element_size(), _status(dev_status), s), "paged_attn")
+    dev = cache.index
+    _run("paged_attn", dev, stream, lib().csa2_paged_attn, params, cache.c, layer, B,
+         _at("q", q, dev), q.stride(0), q.stride(1), None if sink is None else _at("sink", sink, dev),
+         None if seq is None else _i32("seq", seq, B, dev), _i32("n_tokens", n_tokens, B, dev),
+         window, n_first, _at("out", out, dev), _at("workspace", workspace, dev), workspace.nbytes,
+         _status(dev_status, dev))
 
 
 def fp4_mma_peak(ctas, iters, dev_status=None, stream=None):
@@ -476,16 +462,16 @@ class PagedCache:
             _fail("PagedCache: pool must be [layers, n_pages, page_size, %d] of %s with contiguous layers" % (D, dt))
         if table.dim() != 2 or table.dtype != torch.int32 or not table.is_contiguous():
             _fail("PagedCache: table must be contiguous int32 [max_seqs, max_pages]")
-        _i32("ref", ref, pool.shape[1])
-        self.device = pool.device
-        _on(self.device, table=table, ref=ref)
+        _i32("ref", ref, pool.shape[1], pool.get_device())
+        _at("table", table, pool.get_device())
+        self.device, self.index = pool.device, pool.get_device()
         self.pool, self.table, self.ref = pool, table, ref
         self.c = Pages(pool.data_ptr(), pool.stride(0) * pool.element_size(), table.data_ptr(),
                        ref.data_ptr(), pool.shape[0], pool.shape[1], pool.shape[2], table.shape[0],
                        table.shape[1])
-        self.ref_c = ctypes.byref(self.c)
-        n = lib().csa2_page_workspace_size(self.ref_c)
+        n = lib().csa2_page_workspace_size(self.c)
         self.workspace = torch.empty(max(int(n), 256), dtype=torch.uint8, device=self.device)
+        self.ws_ptr, self.ws_bytes = self.workspace.data_ptr(), self.workspace.numel()
 
 
 def n_blocks(n: int) -> int:

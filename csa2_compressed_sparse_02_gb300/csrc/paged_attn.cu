@@ -9,6 +9,7 @@
 // joins them in order: o = sum_i O_i 2^{m_i - M} / (2^{sink - M} + sum_i l_i 2^{m_i - M}).
 #include <cuda.h>
 
+#include <atomic>
 #include <climits>
 
 #include "pages.cuh"
@@ -445,40 +446,52 @@ __device__ void decode_role(Shared<false, NH>& sh, const Args& a, int pt, int la
         // ---- query: warp pw stages heads pw, pw + 8, ...; lane = channels 16 lane .. + 15
         if (it > 0 && !mbar_wait(&sh.q_empty, (uint32_t)((it - 1) & 1), abort)) return;
         __syncwarp();
-#pragma unroll 2
-        for (int h = pw; h < NH; h += 8) {
-            uint4 w2[2] = {zero, zero};
-            if (h < a.heads) {
+        constexpr int kAtOnce = NH / 8 < 4 ? NH / 8 : 4;  // heads whose loads are in flight together
+#pragma unroll 1
+        for (int h1 = pw; h1 < NH; h1 += 8 * kAtOnce) {
+            uint4 w2[kAtOnce][2];
+#pragma unroll
+            for (int i = 0; i < kAtOnce; ++i) {
+                const int h = h1 + 8 * i;
                 const uint4* src = reinterpret_cast<const uint4*>(a.q + pc.b * a.q_seq + h * a.q_head) + 2 * lane;
-                w2[0] = __ldg(src);
-                w2[1] = __ldg(src + 1);
+                w2[i][0] = h < a.heads ? __ldg(src) : zero;
+                w2[i][1] = h < a.heads ? __ldg(src + 1) : zero;
             }
-            const uint32_t w[8] = {w2[0].x, w2[0].y, w2[0].z, w2[0].w, w2[1].x, w2[1].y, w2[1].z, w2[1].w};
-            float mx = 0.f;
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-                mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(w[k] << 16)), fabsf(__uint_as_float(w[k] & 0xffff0000u))));
-            mx = warp_max(mx);
-            // times 2^s with the head's largest |q| in [2^14, 2^15): f16 then keeps bf16's 8
-            // bits of everything above 2^-24 of it; the factor goes into the logit scale
-            int s = 14 - ((int)((__float_as_uint(mx) >> 23) & 0xffu) - 127);
-            s = max(-126, min(126, s));
-            const float two_s = __uint_as_float((uint32_t)(s + 127) << 23);
-            uint32_t hq[8];
+            for (int i = 0; i < kAtOnce; ++i) {
+                const int h = h1 + 8 * i;
+                const uint32_t w[8] = {w2[i][0].x, w2[i][0].y, w2[i][0].z, w2[i][0].w,
+                                       w2[i][1].x, w2[i][1].y, w2[i][1].z, w2[i][1].w};
+                float mx = 0.f;
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-                hq[k] = pack_h2(__uint_as_float(w[k] << 16) * two_s, __uint_as_float(w[k] & 0xffff0000u) * two_s);
-            uint8_t* row = sh.q[lane >> 2];
-            const int u0 = (lane & 3) * 2;
-            *reinterpret_cast<uint4*>(row + sw128(h, u0)) = make_uint4(hq[0], hq[1], hq[2], hq[3]);
-            *reinterpret_cast<uint4*>(row + sw128(h, u0 + 1)) = make_uint4(hq[4], hq[5], hq[6], hq[7]);
-            if (lane == 0) sh.col_scale[it & 1][h] = a.scale_log2 * __uint_as_float((uint32_t)(127 - s) << 23);
+                for (int k = 0; k < 8; ++k)
+                    mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(w[k] << 16)), fabsf(__uint_as_float(w[k] & 0xffff0000u))));
+                mx = warp_max(mx);
+                // times 2^s with the head's largest |q| in [2^14, 2^15): f16 then keeps bf16's 8
+                // bits of everything above 2^-24 of it; the factor goes into the logit scale
+                int s = 14 - ((int)((__float_as_uint(mx) >> 23) & 0xffu) - 127);
+                s = max(-126, min(126, s));
+                const float two_s = __uint_as_float((uint32_t)(s + 127) << 23);
+                uint32_t hq[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    hq[k] = pack_h2(__uint_as_float(w[k] << 16) * two_s, __uint_as_float(w[k] & 0xffff0000u) * two_s);
+                uint8_t* row = sh.q[lane >> 2];
+                const int u0 = (lane & 3) * 2;
+                *reinterpret_cast<uint4*>(row + sw128(h, u0)) = make_uint4(hq[0], hq[1], hq[2], hq[3]);
+                *reinterpret_cast<uint4*>(row + sw128(h, u0 + 1)) = make_uint4(hq[4], hq[5], hq[6], hq[7]);
+                if (lane == 0) sh.col_scale[it & 1][h] = a.scale_log2 * __uint_as_float((uint32_t)(127 - s) << 23);
+            }
         }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.q_full[it & 1]);
         for (int n = pc.j1 - pc.j0; n > 0; --n, ++gt) {
             const uint4* nxt = ahead.next(a) ? row_of() : nullptr;
+            if (nxt) {  // its lines into L2: the loads below then wait for that only
+                prefetch_l2(reinterpret_cast<const uint8_t*>(nxt) + (hf ? 192 : 0));
+                prefetch_l2(reinterpret_cast<const uint8_t*>(nxt) + (hf ? 320 : 128));
+            }
 #pragma unroll
             for (int pr = 0; pr < 4; ++pr, ++g) {
                 const int slot = g % kPairs;
@@ -895,19 +908,17 @@ static_assert(smem_bytes<true, 64>() <= 232448 && smem_bytes<true, 32>() <= 2324
               "shared memory of a CTA");
 
 // ---------------------------------------------------------------- join
-// One warp per (sequence, head), lane = 16 channels in four groups of four. Sequences that
+// One CTA per (sequence, head), a warp per 128 channels, lane = four of them. Sequences that
 // no range boundary cuts were finished by the attention kernel; those that see nothing get
-// their zeros here.
-constexpr int kJoinWarps = 4;
-__global__ void __launch_bounds__(32 * kJoinWarps) k_paged_join(Args a) {
+// their zeros here. Eight pieces' values are requested before the first is used.
+constexpr int kJoinThreads = 128;
+__global__ void __launch_bounds__(kJoinThreads) k_paged_join(Args a) {
     grid_dep_wait();
-    const int lane = threadIdx.x & 31, b = blockIdx.x, h = blockIdx.y * kJoinWarps + (threadIdx.x >> 5);
-    if (h >= a.heads) return;
+    const int lane = threadIdx.x & 31, b = blockIdx.x, h = blockIdx.y;
     const int64_t total = a.prefix[a.B], s = a.prefix[b], e = a.prefix[b + 1];
-    __nv_bfloat16* out = a.out + ((int64_t)b * a.heads + h) * kD + 4 * lane;
+    __nv_bfloat16* out = a.out + ((int64_t)b * a.heads + h) * kD + 4 * threadIdx.x;
     if (s == e) {
-        if (!a.seq || a.seq[b] >= 0)
-            for (int k = 0; k < 4; ++k) *reinterpret_cast<uint2*>(out + 128 * k) = make_uint2(0u, 0u);
+        if (!a.seq || a.seq[b] >= 0) *reinterpret_cast<uint2*>(out) = make_uint2(0u, 0u);
         return;
     }
     const Cut cut(total, a.ctas);
@@ -921,11 +932,9 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_paged_join(Args a) {
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
     float den = s2 == -INFINITY ? 0.f : ex2(s2 - M);
-    float4 acc[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int b0 = c0; b0 <= c1; b0 += 32) {  // 32 pieces at a time, lane = piece for the factors
-        const int c = b0 + lane;
+        const int c = b0 + lane, n = min(32, c1 - b0 + 1);
         float f = 0.f, l = 0.f;
         if (c <= c1) {
             const float* p = part_of(a, c, c == c0 ? slot0 : 0);
@@ -933,37 +942,45 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_paged_join(Args a) {
             f = m == -INFINITY ? 0.f : ex2(m - M);
             l = p[lo] * f;
         }
-        const int n = min(32, c1 - b0 + 1);
-#pragma unroll 4
-        for (int i = 0; i < n; ++i) {
-            const float fi = __shfl_sync(0xffffffffu, f, i);
-            den += __shfl_sync(0xffffffffu, l, i);
-            const float* p = part_of(a, b0 + i, b0 + i == c0 ? slot0 : 0) + (int64_t)h * kD + 4 * lane;
+        for (int i0 = 0; i0 < n; i0 += 8) {
+            float4 v[8];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const float4 v = __ldcg(reinterpret_cast<const float4*>(p + 128 * k));
-                acc[k].x = fmaf(v.x, fi, acc[k].x);
-                acc[k].y = fmaf(v.y, fi, acc[k].y);
-                acc[k].z = fmaf(v.z, fi, acc[k].z);
-                acc[k].w = fmaf(v.w, fi, acc[k].w);
-            }
+            for (int i = 0; i < 8; ++i)
+                if (i0 + i < n) {
+                    const int ci = b0 + i0 + i;
+                    v[i] = __ldcg(reinterpret_cast<const float4*>(part_of(a, ci, ci == c0 ? slot0 : 0) +
+                                                                  (int64_t)h * kD) + threadIdx.x);
+                }
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (i0 + i < n) {
+                    const float fi = __shfl_sync(0xffffffffu, f, i0 + i);
+                    den += __shfl_sync(0xffffffffu, l, i0 + i);
+                    acc.x = fmaf(v[i].x, fi, acc.x);
+                    acc.y = fmaf(v[i].y, fi, acc.y);
+                    acc.z = fmaf(v[i].z, fi, acc.z);
+                    acc.w = fmaf(v[i].w, fi, acc.w);
+                }
         }
     }
     const float inv = den == 0.f ? 0.f : 1.f / den;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        const __nv_bfloat162 x = __floats2bfloat162_rn(acc[k].x * inv, acc[k].y * inv);
-        const __nv_bfloat162 y = __floats2bfloat162_rn(acc[k].z * inv, acc[k].w * inv);
-        *reinterpret_cast<uint2*>(out + 128 * k) =
-            make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
-    }
+    const __nv_bfloat162 x = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
+    const __nv_bfloat162 y = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
+    *reinterpret_cast<uint2*>(out) =
+        make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
 }
 
+// CTAs of the attention kernel on the current device: one per SM (asked for once a device),
+// at most max_ctas. 0: no device.
 int grid_of(const csa2_params* p) {
-    int dev = 0, n = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-        return 0;
+    static std::atomic<int> sms[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) return 0;
+    int n = dev < 64 ? sms[dev].load(std::memory_order_relaxed) : 0;
+    if (!n) {
+        if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+        if (dev < 64) sms[dev].store(n, std::memory_order_relaxed);
+    }
     return p->max_ctas > 0 && p->max_ctas < n ? p->max_ctas : n;
 }
 
@@ -1092,8 +1109,8 @@ extern "C" int csa2_paged_attn(const csa2_params* p, const csa2_pages* c, int la
              : p->heads > 16 ? launch_attn<false, 32>(a, rows, &cfg) : launch_attn<false, 16>(a, rows, &cfg);
     }
     if (rc) return rc;
-    cfg.gridDim = dim3(B, (p->heads + kJoinWarps - 1) / kJoinWarps);
-    cfg.blockDim = dim3(32 * kJoinWarps);
+    cfg.gridDim = dim3(B, p->heads);
+    cfg.blockDim = dim3(kJoinThreads);
     cfg.dynamicSmemBytes = 0;
     cudaLaunchKernelEx(&cfg, k_paged_join, a);
     return check_launch("paged_attn: join");

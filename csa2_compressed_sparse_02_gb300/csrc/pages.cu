@@ -626,8 +626,7 @@ extern "C" int csa2_page_write(const csa2_params* p, const csa2_pages* c, int la
     if (!aligned16(x) || x_row % (x_format == CSA2_F32 ? 4 : 8))
         return fail(CSA2_ERR_ALIGN, "page_write: rows of x must be 16-byte aligned");
     if (const int rc = ensure_loaded()) return rc;
-    RopeTable tab;
-    rope_table(p, p->rope_dim, &tab);
+    const RopeTable& tab = rope_table(p, p->rope_dim);
     const dim3 grid((unsigned)((N + kWriteWarps - 1) / kWriteWarps));
     const int th = 32 * kWriteWarps;
     const bool bf = p->kv_format == CSA2_BF16;

@@ -222,8 +222,7 @@ extern "C" int csa2_rope(const csa2_params* p, int layout, int inverse, int64_t 
     if (x == out && (x_row != out_row || x_head != out_head))
         return fail(CSA2_ERR_INVALID_ARG, "rope: in place, x and out must have the same strides");
     if (const int rc = ensure_loaded()) return rc;
-    RopeTable tab;
-    rope_table(p, rot, &tab);
+    const RopeTable& tab = rope_table(p, rot);
     Args a = {};
     a.x = x;
     a.out = out;

@@ -17,8 +17,24 @@ struct RopeTable {
     double turns[kRopeMaxPairs];
 };
 
-inline void rope_table(const csa2_params* p, int dim, RopeTable* t) {
+// Built once per thread and setting (a program rarely alternates between two): the powers of
+// 32 pairs take about a microsecond, as long as the launch.
+inline const RopeTable& rope_table(const csa2_params* p, int dim) {
+    struct Built {
+        RopeTable t;
+        float theta, factor, orig_len, fast, slow;
+    };
+    static thread_local Built last = {};
+    if (last.t.dim == dim && last.theta == p->rope_theta && last.factor == p->rope_factor &&
+        last.orig_len == p->rope_orig_len && last.fast == p->rope_beta_fast && last.slow == p->rope_beta_slow)
+        return last.t;
+    RopeTable* t = &last.t;
     t->dim = dim;
+    last.theta = p->rope_theta;
+    last.factor = p->rope_factor;
+    last.orig_len = p->rope_orig_len;
+    last.fast = p->rope_beta_fast;
+    last.slow = p->rope_beta_slow;
     for (int i = 0; i < dim / 2; ++i) {
         const double f = std::pow((double)p->rope_theta, -(double)(2 * i) / (double)dim) * 0.15915494309189535;
         const double r = (double)p->rope_orig_len * f;  // turns over the original context
@@ -28,6 +44,7 @@ inline void rope_table(const csa2_params* p, int dim, RopeTable* t) {
         else keep = (r - p->rope_beta_slow) / ((double)p->rope_beta_fast - (double)p->rope_beta_slow);
         t->turns[i] = f * keep + (f / (double)p->rope_factor) * (1.0 - keep);
     }
+    return last.t;
 }
 
 inline bool rope_settings_ok(const csa2_params* p) {
