@@ -182,10 +182,10 @@ struct Shape {
     static constexpr int kGroups = kSoftWarps / 4;  // of heads: one per four lane quarters
     static constexpr int NC = NH / kGroups;         // heads of a softmax warp
     static constexpr int kMmaWarp = kSoftWarps;
-    static constexpr int kProd0 = kSoftWarps + 1;   // first producer warp
-    static constexpr int kProdWarps = kBf16 ? 5 : 8;
-    static constexpr int kQueryWarps = kBf16 ? 4 : 8;  // of them, those that stage the query
-    static constexpr int kThreads = 32 * (kProd0 + kProdWarps);
+    static constexpr int kTmaWarp = kSoftWarps + 1;
+    static constexpr int kHelp0 = kSoftWarps + 2;       // first of the warps that stage the query
+    static constexpr int kHelpWarps = kBf16 ? 4 : 8;    // and, for E4M3, decode the rows
+    static constexpr int kThreads = 32 * (kHelp0 + kHelpWarps);
     // Pairs of 64-channel chunks of a tile in the ring: a tile has 4; what the query leaves
     // of shared memory lets the next tile's first pairs arrive early.
     static constexpr int kPairs = NH == 64 ? 4 : NH == 32 ? 5 : 6;
@@ -228,6 +228,7 @@ struct Shared {
     // softmax warp has waited on this one (a one-tile piece needs no softmax before its S ends)
     uint64_t q_full[2], q_empty, s_full, p_full, o_full, drain;
     uint64_t full[S::kPairs], empty[S::kPairs];
+    uint64_t raw_full[S::kPairs];      // E4M3: the bytes have landed, full: they are decoded
     uint64_t p_again, max_bar[S::kGroups], sum_bar[S::kGroups];
     Range range;
     uint32_t tmem_base;
@@ -297,9 +298,9 @@ __device__ __forceinline__ float warp_max(float v) {
     return r;
 }
 
-// ---------------------------------------------------------------- bf16 producers
-// One warp copies the tile's rows, box by box (rows of one page, 64 channels), straight into
-// the swizzled operand; boxes that hold nothing seen are left out.
+// ---------------------------------------------------------------- producers
+// One warp copies the tile's rows box by box (rows of one page): bf16 straight into the
+// swizzled operand. Boxes that hold nothing seen are left out.
 struct Boxes {
     uint32_t rows[4];  // the tile's rows that hold a seen position
     bool mine;         // this lane's box is copied: it begins at the pool's row y
@@ -328,10 +329,14 @@ __device__ __forceinline__ Boxes boxes_of(const Args& a, const Tiles& t, int lan
     return x;
 }
 
-template <int NH>
-__device__ void tma_role(Shared<true, NH>& sh, const Args& a, const CUtensorMap* tmap, int lane, volatile int* abort) {
-    constexpr int kPairs = Shape<true, NH>::kPairs;
-    const uint32_t dst0 = smem_u32(sh.kv[0][0]) + lane * a.box_rows * 128;
+template <bool kBf16, int NH>
+__device__ void tma_role(Shared<kBf16, NH>& sh, const Args& a, const CUtensorMap* tmap, int lane, volatile int* abort) {
+    constexpr int kPairs = Shape<kBf16, NH>::kPairs;
+    // bf16: two boxes of 64 channels, in the operand's place; E4M3: one of 128, its bytes in
+    // the place of the pair's second chunk
+    constexpr uint32_t kRowBytes = kBf16 ? 256 : 128;
+    uint64_t* const landed = kBf16 ? sh.full : sh.raw_full;
+    const uint32_t dst0 = smem_u32(sh.kv[0][kBf16 ? 0 : 1]) + lane * a.box_rows * 128;
     const int box_bytes = a.box_rows * a.g.row_bytes;
     Tiles it(sh.range);
     int g = 0;  // pairs so far
@@ -344,7 +349,7 @@ __device__ void tma_role(Shared<true, NH>& sh, const Args& a, const CUtensorMap*
         if (nxt.mine) bulk_prefetch_l2(a.base + (int64_t)nxt.y * a.g.row_bytes, box_bytes);
     }
     for (int gt = 0; has && !gave_up; ++gt) {
-        const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, cur.mine)) * a.box_rows * 256u;
+        const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, cur.mine)) * a.box_rows * kRowBytes;
         for (int pr = 0; pr < 4; ++pr, ++g) {
             const int slot = g % kPairs;
             if (g >= kPairs && !mbar_wait(&sh.empty[slot], (uint32_t)((g / kPairs - 1) & 1), abort)) gave_up = true;
@@ -358,12 +363,12 @@ __device__ void tma_role(Shared<true, NH>& sh, const Args& a, const CUtensorMap*
                     (((w >> (4 * (lane & 7))) & 15u) * 0x00204081u) & 0x01010101u;
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive_expect_tx(&sh.full[slot], bytes);
+            if (lane == 0) mbar_arrive_expect_tx(&landed[slot], bytes);
             __syncwarp();
             if (cur.mine) {
                 const uint32_t dst = dst0 + 2 * slot * kChunk;
-                tma_g2s_2d(dst, tmap, 128 * pr, cur.y, &sh.full[slot]);
-                tma_g2s_2d(dst + kChunk, tmap, 128 * pr + 64, cur.y, &sh.full[slot]);
+                tma_g2s_2d(dst, tmap, 128 * pr, cur.y, &landed[slot]);
+                if constexpr (kBf16) tma_g2s_2d(dst + kChunk, tmap, 128 * pr + 64, cur.y, &landed[slot]);
             }
         }
         // The ring holds little more than a tile and stands still between a tile's S and its
@@ -378,12 +383,12 @@ __device__ void tma_role(Shared<true, NH>& sh, const Args& a, const CUtensorMap*
         }
     }
     // whatever ended the loop, no copy of this CTA outlives it
-    for (int s = max(0, g - kPairs); s < g; ++s) mbar_wait_drain(&sh.full[s % kPairs], (uint32_t)((s / kPairs) & 1));
+    for (int s = max(0, g - kPairs); s < g; ++s) mbar_wait_drain(&landed[s % kPairs], (uint32_t)((s / kPairs) & 1));
 }
 
 template <int NH>
 __device__ void query_role(Shared<true, NH>& sh, const Args& a, int pt, int lane, volatile int* abort) {
-    constexpr int kStagers = 32 * Shape<true, NH>::kQueryWarps;
+    constexpr int kStagers = 32 * Shape<true, NH>::kHelpWarps;
     static_assert(kStagers == 128, "a thread stages unit pt mod 64 of every other head");
     const int u = pt & 63, hb = pt >> 6;
     Pieces pi(sh.range);
@@ -416,33 +421,19 @@ __device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
     return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// Eight warps: thread (r, hf) has row r of every tile and chunk 2 pr + hf of each pair. The
-// bytes of two pairs are on their way while one is decoded.
+// Eight warps, 16 rows of every tile each. The 128 bytes of a row that become a pair of chunks
+// lie where its 128 bytes of the second chunk will be: a warp reads its rows, then writes both
+// chunks over them, so the raw bytes take no room of their own.
 template <int NH>
 __device__ void decode_role(Shared<false, NH>& sh, const Args& a, int pt, int lane, volatile int* abort) {
     constexpr int kPairs = Shape<false, NH>::kPairs;
-    const int pw = pt >> 5, r = pt >> 1, hf = pt & 1;
-    const uint32_t ps = a.g.page_size;
-    // this thread's bytes of the tile the cursor is at: its row's half, or NULL where nothing is seen
-    Tiles ahead(sh.range);
-    auto row_of = [&]() -> const uint4* {
-        const uint32_t t = ahead.pc.v.start(ahead.j) + r;
-        if (!ahead.pc.v.sees(t)) return nullptr;
-        const int page = page_of(a, a.g.table + (int64_t)ahead.pc.v.row * a.g.max_pages, t);
-        if (page < 0) return nullptr;
-        return reinterpret_cast<const uint4*>(a.base + page * a.g.page_bytes() + (int64_t)(t % ps) * kD + 64 * hf);
-    };
-    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-    uint4 raw[2][4];
-    const uint4* cur = ahead.next(a) ? row_of() : nullptr;
-#pragma unroll
-    for (int pr = 0; pr < 2; ++pr)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) raw[pr][k] = cur ? __ldg(cur + 8 * pr + k) : zero;
+    const int pw = pt >> 5, sub = lane >> 3, un = lane & 7;  // lane: unit un of rows 4 k + sub
     Pieces pi(sh.range);
-    Piece pc;
-    int g = 0, gt = 0;
-    for (int it = 0; pi.next(a, pc); ++it) {
+    int gt = 0, slot = 0;
+    uint32_t phase = 0;
+    for (int it = 0;; ++it) {
+        Piece pc;
+        if (!pi.next(a, pc)) break;
         // ---- query: warp pw stages heads pw, pw + 8, ...; lane = channels 16 lane .. + 15
         if (it > 0 && !mbar_wait(&sh.q_empty, (uint32_t)((it - 1) & 1), abort)) return;
         __syncwarp();
@@ -454,8 +445,8 @@ __device__ void decode_role(Shared<false, NH>& sh, const Args& a, int pt, int la
             for (int i = 0; i < kAtOnce; ++i) {
                 const int h = h1 + 8 * i;
                 const uint4* src = reinterpret_cast<const uint4*>(a.q + pc.b * a.q_seq + h * a.q_head) + 2 * lane;
-                w2[i][0] = h < a.heads ? __ldg(src) : zero;
-                w2[i][1] = h < a.heads ? __ldg(src + 1) : zero;
+                w2[i][0] = w2[i][1] = make_uint4(0u, 0u, 0u, 0u);
+                if (h < a.heads) w2[i][0] = __ldg(src), w2[i][1] = __ldg(src + 1);
             }
 #pragma unroll
             for (int i = 0; i < kAtOnce; ++i) {
@@ -487,35 +478,37 @@ __device__ void decode_role(Shared<false, NH>& sh, const Args& a, int pt, int la
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.q_full[it & 1]);
         for (int n = pc.j1 - pc.j0; n > 0; --n, ++gt) {
-            const uint4* nxt = ahead.next(a) ? row_of() : nullptr;
-            if (nxt) {  // its lines into L2: the loads below then wait for that only
-                prefetch_l2(reinterpret_cast<const uint8_t*>(nxt) + (hf ? 192 : 0));
-                prefetch_l2(reinterpret_cast<const uint8_t*>(nxt) + (hf ? 320 : 128));
-            }
+#pragma unroll 1
+            for (int pr = 0; pr < 4; ++pr) {
+                if (!mbar_wait(&sh.raw_full[slot], phase, abort)) return;
+                uint8_t* rows = sh.kv[slot][1] + 16 * pw * 128;
+                uint4 raw[4];
 #pragma unroll
-            for (int pr = 0; pr < 4; ++pr, ++g) {
-                const int slot = g % kPairs;
-                if (g >= kPairs && !mbar_wait(&sh.empty[slot], (uint32_t)((g / kPairs - 1) & 1), abort)) return;
-                if (pr == 0 && hf == 0) sh.row_ok[gt & 1][r] = cur != nullptr;
-                uint8_t* dst = sh.kv[slot][hf];
+                for (int k = 0; k < 4; ++k) {  // a row that is not seen becomes zeros, whatever is there
+                    raw[k] = *reinterpret_cast<const uint4*>(rows + (4 * k + sub) * 128 + 16 * un);
+                    if (!sh.row_ok[gt & 1][16 * pw + 4 * k + sub]) raw[k] = make_uint4(0u, 0u, 0u, 0u);
+                }
+                __syncwarp();  // every lane has its bytes: they may be overwritten
+                uint8_t* dst = sh.kv[slot][un >> 2];
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     uint32_t o[8];
-                    e4m3x4_to_h2x2(raw[pr & 1][k].x, &o[0]);
-                    e4m3x4_to_h2x2(raw[pr & 1][k].y, &o[2]);
-                    e4m3x4_to_h2x2(raw[pr & 1][k].z, &o[4]);
-                    e4m3x4_to_h2x2(raw[pr & 1][k].w, &o[6]);
-                    *reinterpret_cast<uint4*>(dst + sw128(r, 2 * k)) = make_uint4(o[0], o[1], o[2], o[3]);
-                    *reinterpret_cast<uint4*>(dst + sw128(r, 2 * k + 1)) = make_uint4(o[4], o[5], o[6], o[7]);
+                    e4m3x4_to_h2x2(raw[k].x, &o[0]);
+                    e4m3x4_to_h2x2(raw[k].y, &o[2]);
+                    e4m3x4_to_h2x2(raw[k].z, &o[4]);
+                    e4m3x4_to_h2x2(raw[k].w, &o[6]);
+                    // the second chunk's lanes store their odd unit first: a row's eight lanes then
+                    // hit all banks
+                    const int r = 16 * pw + 4 * k + sub, u0 = 2 * (un & 3), odd = un >> 2;
+                    const uint4 lo = make_uint4(o[0], o[1], o[2], o[3]), hi = make_uint4(o[4], o[5], o[6], o[7]);
+                    *reinterpret_cast<uint4*>(dst + sw128(r, u0 + odd)) = odd ? hi : lo;
+                    *reinterpret_cast<uint4*>(dst + sw128(r, u0 + 1 - odd)) = odd ? lo : hi;
                 }
-                const uint4* src = pr < 2 ? cur : nxt;
-#pragma unroll
-                for (int k = 0; k < 4; ++k) raw[pr & 1][k] = src ? __ldg(src + 8 * ((pr + 2) & 3) + k) : zero;
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sh.full[slot]);
+                if (++slot == kPairs) slot = 0, phase ^= 1u;
             }
-            cur = nxt;
         }
     }
 }
@@ -843,8 +836,8 @@ k_paged_attn(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     volatile int* abort = &sh.abort;
     if (tid == 0) {
-        mbar_init(&sh.q_full[0], S::kQueryWarps);
-        mbar_init(&sh.q_full[1], S::kQueryWarps);
+        mbar_init(&sh.q_full[0], S::kHelpWarps);
+        mbar_init(&sh.q_full[1], S::kHelpWarps);
         mbar_init(&sh.q_empty, 1);
         mbar_init(&sh.s_full, 1);
         mbar_init(&sh.p_full, S::kSoftWarps);
@@ -852,7 +845,8 @@ k_paged_attn(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap
         mbar_init(&sh.o_full, 1);
         mbar_init(&sh.drain, 1);
         for (int i = 0; i < S::kPairs; ++i) {
-            mbar_init(&sh.full[i], kBf16 ? 1 : S::kProdWarps);
+            mbar_init(&sh.full[i], kBf16 ? 1 : S::kHelpWarps);
+            mbar_init(&sh.raw_full[i], 1);
             mbar_init(&sh.empty[i], 1);
         }
         for (int i = 0; i < S::kGroups; ++i) {
@@ -884,11 +878,12 @@ k_paged_attn(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap
         __syncwarp();
         if (elect_one()) tc_commit(&sh.drain);
         if (!mbar_wait_drain(&sh.drain, 0)) *abort = 1;
+    } else if (warp == S::kTmaWarp) {
+        tma_role<kBf16, NH>(sh, a, &tmap, lane, abort);
     } else if constexpr (kBf16) {
-        if (warp == S::kProd0) tma_role<NH>(sh, a, &tmap, lane, abort);
-        else query_role<NH>(sh, a, tid - 32 * (S::kProd0 + 1), lane, abort);
+        query_role<NH>(sh, a, tid - 32 * S::kHelp0, lane, abort);
     } else {
-        decode_role<NH>(sh, a, tid - 32 * S::kProd0, lane, abort);
+        decode_role<NH>(sh, a, tid - 32 * S::kHelp0, lane, abort);
     }
     tc_fence_before();
     __syncthreads();
@@ -984,8 +979,9 @@ int grid_of(const csa2_params* p) {
     return p->max_ctas > 0 && p->max_ctas < n ? p->max_ctas : n;
 }
 
-// The layer's rows as a 2-d tensor map, whose boxes are box_rows rows x 64 channels laid out
-// in the 128-byte swizzle of the MMA operands. The driver's encoder is looked up once.
+// The layer's rows as a 2-d tensor map, whose boxes are box_rows rows x 128 bytes: of bf16 laid
+// out in the 128-byte swizzle of the MMA operands, of E4M3 (which is decoded) as they are. The
+// driver's encoder is looked up once.
 int encode_rows(const Args& a, CUtensorMap* m) {
     using Encode = decltype(&cuTensorMapEncodeTiled);
     static Encode encode = [] {
@@ -997,11 +993,13 @@ int encode_rows(const Args& a, CUtensorMap* m) {
         return reinterpret_cast<Encode>(f);
     }();
     if (!encode) return fail(CSA2_ERR_CUDA, "paged_attn: the driver has no cuTensorMapEncodeTiled");
+    const bool bf16 = a.g.row_bytes == 2 * kD;
     const cuuint64_t dims[2] = {kD, (cuuint64_t)a.g.n_pages * a.g.page_size};
-    const cuuint64_t strides[1] = {2 * kD};
-    const cuuint32_t box[2] = {64, (cuuint32_t)a.box_rows}, steps[2] = {1, 1};
-    if (encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<uint8_t*>(a.base), dims, strides, box, steps,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+    const cuuint64_t strides[1] = {(cuuint64_t)a.g.row_bytes};
+    const cuuint32_t box[2] = {bf16 ? 64u : 128u, (cuuint32_t)a.box_rows}, steps[2] = {1, 1};
+    if (encode(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 2,
+               const_cast<uint8_t*>(a.base), dims, strides, box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               bf16 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
         return fail(CSA2_ERR_CUDA, "paged_attn: tensor map of the pool");
     return CSA2_OK;
@@ -1089,8 +1087,7 @@ extern "C" int csa2_paged_attn(const csa2_params* p, const csa2_pages* c, int la
     if (a.box_rows > kTile) a.box_rows = kTile;
     while ((1 << a.box_shift) < a.box_rows) ++a.box_shift;
     CUtensorMap rows = {};
-    if (p->kv_format == CSA2_BF16)
-        if (const int rc = encode_rows(a, &rows)) return rc;
+    if (const int rc = encode_rows(a, &rows)) return rc;
     cudaLaunchConfig_t cfg = {};
     cfg.stream = static_cast<cudaStream_t>(stream);
     cudaLaunchAttribute attr[1];
