@@ -421,13 +421,15 @@ __device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
     return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// Eight warps, 16 rows of every tile each. The 128 bytes of a row that become a pair of chunks
-// lie where its 128 bytes of the second chunk will be: a warp reads its rows, then writes both
-// chunks over them, so the raw bytes take no room of their own.
+// Two groups of four warps take a tile's pairs in turn (a pair is one chain of waits, loads,
+// stores and a fence, so two run side by side), a warp 32 rows. The 128 bytes of a row that
+// become a pair of chunks lie where its 128 bytes of the second chunk will be: a warp reads its
+// rows, then writes both chunks over them, so the raw bytes take no room of their own.
 template <int NH>
 __device__ void decode_role(Shared<false, NH>& sh, const Args& a, int pt, int lane, volatile int* abort) {
     constexpr int kPairs = Shape<false, NH>::kPairs;
     const int pw = pt >> 5, sub = lane >> 3, un = lane & 7;  // lane: unit un of rows 4 k + sub
+    const int row0 = 32 * (pw & 3), group = pw >> 2;
     Pieces pi(sh.range);
     int gt = 0, slot = 0;
     uint32_t phase = 0;
@@ -480,33 +482,36 @@ __device__ void decode_role(Shared<false, NH>& sh, const Args& a, int pt, int la
         for (int n = pc.j1 - pc.j0; n > 0; --n, ++gt) {
 #pragma unroll 1
             for (int pr = 0; pr < 4; ++pr) {
-                if (!mbar_wait(&sh.raw_full[slot], phase, abort)) return;
-                uint8_t* rows = sh.kv[slot][1] + 16 * pw * 128;
-                uint4 raw[4];
+                if ((pr & 1) == group) {
+                    if (!mbar_wait(&sh.raw_full[slot], phase, abort)) return;
+                    uint8_t* rows = sh.kv[slot][1] + row0 * 128;
+                    const uint8_t* ok = &sh.row_ok[gt & 1][row0 + sub];
+                    uint4 raw[8];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {  // a row that is not seen becomes zeros, whatever is there
-                    raw[k] = *reinterpret_cast<const uint4*>(rows + (4 * k + sub) * 128 + 16 * un);
-                    if (!sh.row_ok[gt & 1][16 * pw + 4 * k + sub]) raw[k] = make_uint4(0u, 0u, 0u, 0u);
-                }
-                __syncwarp();  // every lane has its bytes: they may be overwritten
-                uint8_t* dst = sh.kv[slot][un >> 2];
+                    for (int k = 0; k < 8; ++k) {  // a row that is not seen becomes zeros, whatever is there
+                        raw[k] = *reinterpret_cast<const uint4*>(rows + (4 * k + sub) * 128 + 16 * un);
+                        if (!ok[4 * k]) raw[k] = make_uint4(0u, 0u, 0u, 0u);
+                    }
+                    __syncwarp();  // every lane has its bytes: they may be overwritten
+                    uint8_t* dst = sh.kv[slot][un >> 2];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    uint32_t o[8];
-                    e4m3x4_to_h2x2(raw[k].x, &o[0]);
-                    e4m3x4_to_h2x2(raw[k].y, &o[2]);
-                    e4m3x4_to_h2x2(raw[k].z, &o[4]);
-                    e4m3x4_to_h2x2(raw[k].w, &o[6]);
-                    // the second chunk's lanes store their odd unit first: a row's eight lanes then
-                    // hit all banks
-                    const int r = 16 * pw + 4 * k + sub, u0 = 2 * (un & 3), odd = un >> 2;
-                    const uint4 lo = make_uint4(o[0], o[1], o[2], o[3]), hi = make_uint4(o[4], o[5], o[6], o[7]);
-                    *reinterpret_cast<uint4*>(dst + sw128(r, u0 + odd)) = odd ? hi : lo;
-                    *reinterpret_cast<uint4*>(dst + sw128(r, u0 + 1 - odd)) = odd ? lo : hi;
+                    for (int k = 0; k < 8; ++k) {
+                        uint32_t o[8];
+                        e4m3x4_to_h2x2(raw[k].x, &o[0]);
+                        e4m3x4_to_h2x2(raw[k].y, &o[2]);
+                        e4m3x4_to_h2x2(raw[k].z, &o[4]);
+                        e4m3x4_to_h2x2(raw[k].w, &o[6]);
+                        // the second chunk's lanes store their odd unit first: a row's eight lanes
+                        // then hit all banks
+                        const int r = row0 + 4 * k + sub, u0 = 2 * (un & 3), odd = un >> 2;
+                        const uint4 lo = make_uint4(o[0], o[1], o[2], o[3]), hi = make_uint4(o[4], o[5], o[6], o[7]);
+                        *reinterpret_cast<uint4*>(dst + sw128(r, u0 + odd)) = odd ? hi : lo;
+                        *reinterpret_cast<uint4*>(dst + sw128(r, u0 + 1 - odd)) = odd ? lo : hi;
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sh.full[slot]);
                 }
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sh.full[slot]);
                 if (++slot == kPairs) slot = 0, phase ^= 1u;
             }
         }
@@ -845,7 +850,7 @@ k_paged_attn(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap
         mbar_init(&sh.o_full, 1);
         mbar_init(&sh.drain, 1);
         for (int i = 0; i < S::kPairs; ++i) {
-            mbar_init(&sh.full[i], kBf16 ? 1 : S::kHelpWarps);
+            mbar_init(&sh.full[i], kBf16 ? 1 : S::kHelpWarps / 2);
             mbar_init(&sh.raw_full[i], 1);
             mbar_init(&sh.empty[i], 1);
         }
