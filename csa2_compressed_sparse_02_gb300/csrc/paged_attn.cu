@@ -908,61 +908,81 @@ static_assert(smem_bytes<true, 64>() <= 232448 && smem_bytes<true, 32>() <= 2324
               "shared memory of a CTA");
 
 // ---------------------------------------------------------------- join
-// One CTA per (sequence, head), a warp per 128 channels, lane = four of them. Sequences that
-// no range boundary cuts were finished by the attention kernel; those that see nothing get
-// their zeros here. Eight pieces' values are requested before the first is used.
+// One CTA per (sequence, head), a thread per four channels; with G groups of 128 threads,
+// group i takes every G-th piece and the groups' sums are added in order. Sequences that no
+// range boundary cuts were finished by the attention kernel; those that see nothing get their
+// zeros here. A chain of three round trips bounds it (the items, the pieces' values and
+// maxima, the output): up to eight pieces' values are requested together, before the weights
+// they will get are known.
 constexpr int kJoinThreads = 128;
-__global__ void __launch_bounds__(kJoinThreads) k_paged_join(Args a) {
+constexpr int kJoinBatch = 8;
+template <int G>
+__global__ void __launch_bounds__(kJoinThreads * G, 8 / G) k_paged_join(Args a) {
+    __shared__ float4 sums[G > 1 ? G - 1 : 1][kJoinThreads];
+    __shared__ float dens[G];
     grid_dep_wait();
-    const int lane = threadIdx.x & 31, b = blockIdx.x, h = blockIdx.y;
+    const int lane = threadIdx.x & 31, ch = threadIdx.x % kJoinThreads, grp = threadIdx.x / kJoinThreads;
+    const int b = blockIdx.x, h = blockIdx.y;
     const int64_t total = a.prefix[a.B], s = a.prefix[b], e = a.prefix[b + 1];
-    __nv_bfloat16* out = a.out + ((int64_t)b * a.heads + h) * kD + 4 * threadIdx.x;
+    const float s2 = a.sink ? a.sink[h] * kLog2e : -INFINITY;
+    __nv_bfloat16* out = a.out + ((int64_t)b * a.heads + h) * kD + 4 * ch;
     if (s == e) {
-        if (!a.seq || a.seq[b] >= 0) *reinterpret_cast<uint2*>(out) = make_uint2(0u, 0u);
+        if (grp == 0 && (!a.seq || a.seq[b] >= 0)) *reinterpret_cast<uint2*>(out) = make_uint2(0u, 0u);
         return;
     }
     const Cut cut(total, a.ctas);
     const int c0 = cut.holder(s), c1 = cut.holder(e - 1);
     if (c0 == c1) return;
-    const float s2 = a.sink ? a.sink[h] * kLog2e : -INFINITY;
     const int64_t mo = (int64_t)a.heads * kD + h, lo = mo + a.heads;
     const int slot0 = cut.at(c0) == s ? 0 : 1;
-    float M = s2;
-    for (int c = c0 + lane; c <= c1; c += 32) M = fmaxf(M, part_of(a, c, c == c0 ? slot0 : 0)[mo]);
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    float den = s2 == -INFINITY ? 0.f : ex2(s2 - M);
+    auto piece = [&](int c) { return part_of(a, c, c == c0 ? slot0 : 0); };
+    // this group's pieces c0 + grp + G i, i < n; lane = piece for the maxima of all
+    const int n = c1 - c0 >= grp ? (c1 - c0 - grp) / G + 1 : 0;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int b0 = c0; b0 <= c1; b0 += 32) {  // 32 pieces at a time, lane = piece for the factors
-        const int c = b0 + lane, n = min(32, c1 - b0 + 1);
-        float f = 0.f, l = 0.f;
-        if (c <= c1) {
-            const float* p = part_of(a, c, c == c0 ? slot0 : 0);
-            const float m = p[mo];
-            f = m == -INFINITY ? 0.f : ex2(m - M);
-            l = p[lo] * f;
+    float den = 0.f, M = s2;
+    for (int i0 = 0; i0 < n || i0 == 0; i0 += kJoinBatch) {
+        float4 v[kJoinBatch];
+        float m[kJoinBatch], l[kJoinBatch];
+#pragma unroll
+        for (int i = 0; i < kJoinBatch; ++i)
+            if (i0 + i < n) {
+                const float* p = piece(c0 + grp + G * (i0 + i));
+                v[i] = __ldcg(reinterpret_cast<const float4*>(p + (int64_t)h * kD) + ch);
+                m[i] = __ldcg(p + mo);
+                l[i] = __ldcg(p + lo);
+            }
+        if (i0 == 0) {  // the maximum over all pieces
+            for (int c = c0 + lane; c <= c1; c += 32) M = fmaxf(M, piece(c)[mo]);
+#pragma unroll
+            for (int o = 16; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
         }
-        for (int i0 = 0; i0 < n; i0 += 8) {
-            float4 v[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (i0 + i < n) {
-                    const int ci = b0 + i0 + i;
-                    v[i] = __ldcg(reinterpret_cast<const float4*>(part_of(a, ci, ci == c0 ? slot0 : 0) +
-                                                                  (int64_t)h * kD) + threadIdx.x);
-                }
+        for (int i = 0; i < kJoinBatch; ++i)
+            if (i0 + i < n) {
+                const float f = m[i] == -INFINITY ? 0.f : ex2(m[i] - M);
+                den = fmaf(l[i], f, den);
+                acc.x = fmaf(v[i].x, f, acc.x);
+                acc.y = fmaf(v[i].y, f, acc.y);
+                acc.z = fmaf(v[i].z, f, acc.z);
+                acc.w = fmaf(v[i].w, f, acc.w);
+            }
+    }
+    if constexpr (G > 1) {
+        if (grp > 0) sums[grp - 1][ch] = acc;
+        if (ch == 0) dens[grp] = den;
+        __syncthreads();
+        if (grp > 0) return;
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (i0 + i < n) {
-                    const float fi = __shfl_sync(0xffffffffu, f, i0 + i);
-                    den += __shfl_sync(0xffffffffu, l, i0 + i);
-                    acc.x = fmaf(v[i].x, fi, acc.x);
-                    acc.y = fmaf(v[i].y, fi, acc.y);
-                    acc.z = fmaf(v[i].z, fi, acc.z);
-                    acc.w = fmaf(v[i].w, fi, acc.w);
-                }
+        for (int i = 1; i < G; ++i) {
+            const float4 v = sums[i - 1][ch];
+            acc.x += v.x;
+            acc.y += v.y;
+            acc.z += v.z;
+            acc.w += v.w;
+            den += dens[i];
         }
     }
+    den += s2 == -INFINITY ? 0.f : ex2(s2 - M);
     const float inv = den == 0.f ? 0.f : 1.f / den;
     const __nv_bfloat162 x = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
     const __nv_bfloat162 y = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
@@ -1032,7 +1052,8 @@ cudaError_t preload_paged_attn() {
                             [] { return preload_kernel(k_paged_attn<false, 64>, smem_bytes<false, 64>()); },
                             [] { return preload_kernel(k_paged_attn<false, 32>, smem_bytes<false, 32>()); },
                             [] { return preload_kernel(k_paged_attn<false, 16>, smem_bytes<false, 16>()); },
-                            [] { return preload_kernel(k_paged_join); }};
+                            [] { return preload_kernel(k_paged_join<1>); },
+                            [] { return preload_kernel(k_paged_join<4>); }};
     for (auto f : l)
         if (const cudaError_t e = f()) return e;
     return cudaSuccess;
@@ -1111,9 +1132,14 @@ extern "C" int csa2_paged_attn(const csa2_params* p, const csa2_pages* c, int la
              : p->heads > 16 ? launch_attn<false, 32>(a, rows, &cfg) : launch_attn<false, 16>(a, rows, &cfg);
     }
     if (rc) return rc;
+    // A sequence is cut into about ctas / B pieces. Four groups of threads share them where
+    // that is more than one group requests at once (two sequences of 131,072, 76 pieces each:
+    // KJOIN4 against KJOIN1 us); where it is not, three groups would have nothing to do.
+    const bool wide = ctas / B > kJoinBatch;
     cfg.gridDim = dim3(B, p->heads);
-    cfg.blockDim = dim3(kJoinThreads);
+    cfg.blockDim = dim3(wide ? 4 * kJoinThreads : kJoinThreads);
     cfg.dynamicSmemBytes = 0;
-    cudaLaunchKernelEx(&cfg, k_paged_join, a);
+    if (wide) cudaLaunchKernelEx(&cfg, k_paged_join<4>, a);
+    else cudaLaunchKernelEx(&cfg, k_paged_join<1>, a);
     return check_launch("paged_attn: join");
 }

@@ -1,16 +1,15 @@
 // csa2_rope: rotary embedding of rows x heads, either pair layout, part of the head, both
 // directions. A pair (a, b) turns by the angle of its row: (a cos - b sin, a sin + b cos).
 //
-// Bound by memory: each channel is read once and written once. A row's sines and cosines
-// (fp64 angle reduction) are computed once per CTA into shared memory and serve all its
-// heads; the loads of the first batch are issued before that, so their latency covers it.
+// Bound by memory: each channel is read once and written once. A row's sines and cosines are
+// computed once per CTA into shared memory and serve all its heads; the loads of the CTA's
+// first units are issued before that, so their latency covers it.
 #include "rope.cuh"
 
 namespace csa2 {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kBatch = 4;        // units a thread holds in registers at once
 constexpr int kMaxTable = 2048;  // pairs in shared memory (16 KB)
 
 struct Args {
@@ -35,6 +34,22 @@ struct alignas(sizeof(T) * V) Vec {
     T v[V];
 };
 
+// A vector, read or written once: 16 bytes stream past the caches.
+template <typename T, int V>
+__device__ __forceinline__ Vec<T, V> ld_vec(const T* p) {
+    if constexpr (sizeof(T) * V == 16) {
+        const uint4 u = __ldcs(reinterpret_cast<const uint4*>(p));
+        return *reinterpret_cast<const Vec<T, V>*>(&u);
+    } else {
+        return *reinterpret_cast<const Vec<T, V>*>(p);
+    }
+}
+template <typename T, int V>
+__device__ __forceinline__ void st_vec(T* p, const Vec<T, V>& v) {
+    if constexpr (sizeof(T) * V == 16) __stcs(reinterpret_cast<uint4*>(p), *reinterpret_cast<const uint4*>(&v));
+    else *reinterpret_cast<Vec<T, V>*>(p) = v;
+}
+
 __device__ __forceinline__ float to_f(float v) { return v; }
 __device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
 __device__ __forceinline__ void from_f(float f, float& o) { o = f; }
@@ -43,10 +58,50 @@ __device__ __forceinline__ void from_f(float f, __nv_bfloat16& o) { o = __float2
 // A unit is V channels that are copied, or rotated channels: with kTwo the two vectors of
 // V channels that hold V pairs' a and b (the half layout, or single channels of adjacent
 // pairs where vectors do not fit), without it one vector of V/2 adjacent pairs.
+struct Unit {
+    int64_t row;  // of the call; -1: past the end
+    int head, ch; // first channel
+    int second;   // kTwo: distance of the second vector
+    int pair;     // first pair's entry in the CTA's table; -1: copied
+};
+template <int V, bool kTwo>
+__device__ __forceinline__ Unit unit_of(const Args& a, int dim, uint32_t n, uint32_t total, int64_t row0,
+                                        int head0, int heads) {
+    Unit x;
+    x.row = -1;
+    if (n >= total) return x;
+    const uint32_t rh = div_magic(n, a.units_magic), u = n - rh * a.units;
+    const uint32_t r = div_magic(rh, a.heads_magic), h = rh - r * heads;
+    const int pairs = dim / 2;
+    x.row = row0 + r;
+    x.head = head0 + h;
+    x.second = 0;
+    if (u < (uint32_t)a.rot_units) {
+        if (!kTwo) {
+            x.ch = a.first + u * V;
+            x.pair = r * pairs + u * (V / 2);
+        } else if (a.half) {
+            x.ch = a.first + u * V;
+            x.second = pairs;
+            x.pair = r * pairs + u * V;
+        } else {
+            x.ch = a.first + 2 * u;
+            x.second = 1;
+            x.pair = r * pairs + u;
+        }
+    } else {
+        x.ch = (u - a.rot_units) * V;
+        if (x.ch >= a.first) x.ch += dim;
+        x.pair = -1;
+    }
+    return x;
+}
+
 template <typename T, int V, bool kTwo>
 __global__ void __launch_bounds__(kThreads)
 k_rope(const __grid_constant__ Args a, const __grid_constant__ RopeTable tab) {
     using VT = Vec<T, V>;
+    constexpr int kBatch = kTwo ? 4 : 8;  // units a thread holds in registers at once
     __shared__ float2 cs[kMaxTable];
     const int tid = threadIdx.x;
     const int64_t row0 = (int64_t)blockIdx.x * a.rows_cta;
@@ -58,43 +113,15 @@ k_rope(const __grid_constant__ Args a, const __grid_constant__ RopeTable tab) {
     const T* x = static_cast<const T*>(a.x);
     T* out = static_cast<T*>(a.out);
     bool ready = false;
-    for (uint32_t base = 0; base < total; base += kThreads * kBatch) {
-        VT va[kBatch], vb[kBatch];
-        int64_t oa[kBatch];   // offset in out of the unit's first vector
-        int ob[kBatch];       // second vector (kTwo), relative
-        int at[kBatch];       // first pair's entry in cs; -1: copied; -2: nothing to do
+    for (uint32_t base = tid; base - tid < total; base += kThreads * kBatch) {
+        VT va[kBatch], vb[kTwo ? kBatch : 1];
 #pragma unroll
         for (int k = 0; k < kBatch; ++k) {
-            const uint32_t n = base + k * kThreads + tid;
-            at[k] = -2;
-            if (n >= total) continue;
-            const uint32_t rh = div_magic(n, a.units_magic), u = n - rh * a.units;
-            const uint32_t r = div_magic(rh, a.heads_magic), h = rh - r * heads;
-            if (a.pos[row0 + r] < 0) continue;
-            int ch;
-            ob[k] = 0;
-            if (u < (uint32_t)a.rot_units) {
-                if (!kTwo) {
-                    ch = a.first + u * V;
-                    at[k] = r * pairs + u * (V / 2);
-                } else if (a.half) {
-                    ch = a.first + u * V;
-                    ob[k] = pairs;
-                    at[k] = r * pairs + u * V;
-                } else {
-                    ch = a.first + 2 * u;
-                    ob[k] = 1;
-                    at[k] = r * pairs + u;
-                }
-            } else {
-                ch = (u - a.rot_units) * V;
-                if (ch >= a.first) ch += tab.dim;
-                at[k] = -1;
-            }
-            const T* src = x + (row0 + r) * a.x_row + (int64_t)(head0 + h) * a.x_head + ch;
-            oa[k] = (row0 + r) * a.out_row + (int64_t)(head0 + h) * a.out_head + ch;
-            va[k] = *reinterpret_cast<const VT*>(src);
-            if (kTwo && at[k] >= 0) vb[k] = *reinterpret_cast<const VT*>(src + ob[k]);
+            const Unit u = unit_of<V, kTwo>(a, tab.dim, base + k * kThreads, total, row0, head0, heads);
+            if (u.row < 0) continue;
+            const T* src = x + u.row * a.x_row + (int64_t)u.head * a.x_head + u.ch;
+            va[k] = ld_vec<T, V>(src);
+            if (kTwo && u.pair >= 0) vb[kTwo ? k : 0] = ld_vec<T, V>(src + u.second);
         }
         if (!ready) {
             for (int i = tid; i < rows * pairs; i += kThreads) {
@@ -108,28 +135,30 @@ k_rope(const __grid_constant__ Args a, const __grid_constant__ RopeTable tab) {
         }
 #pragma unroll
         for (int k = 0; k < kBatch; ++k) {
-            if (at[k] == -2) continue;
-            if (at[k] >= 0) {
+            const Unit u = unit_of<V, kTwo>(a, tab.dim, base + k * kThreads, total, row0, head0, heads);
+            if (u.row < 0 || a.pos[u.row] < 0) continue;  // a padding row is left as it is
+            T* dst = out + u.row * a.out_row + (int64_t)u.head * a.out_head + u.ch;
+            if (u.pair >= 0) {
                 if constexpr (kTwo) {
 #pragma unroll
                     for (int i = 0; i < V; ++i) {
-                        const float2 c = cs[at[k] + i];
+                        const float2 c = cs[u.pair + i];
                         const float p = to_f(va[k].v[i]), q = to_f(vb[k].v[i]);
                         from_f(p * c.x - q * c.y, va[k].v[i]);
                         from_f(p * c.y + q * c.x, vb[k].v[i]);
                     }
-                    *reinterpret_cast<VT*>(out + oa[k] + ob[k]) = vb[k];
+                    st_vec<T, V>(dst + u.second, vb[k]);
                 } else {
 #pragma unroll
                     for (int i = 0; i < V / 2; ++i) {
-                        const float2 c = cs[at[k] + i];
+                        const float2 c = cs[u.pair + i];
                         const float p = to_f(va[k].v[2 * i]), q = to_f(va[k].v[2 * i + 1]);
                         from_f(p * c.x - q * c.y, va[k].v[2 * i]);
                         from_f(p * c.y + q * c.x, va[k].v[2 * i + 1]);
                     }
                 }
             }
-            *reinterpret_cast<VT*>(out + oa[k]) = va[k];
+            st_vec<T, V>(dst, va[k]);
         }
     }
 }

@@ -10,11 +10,12 @@ namespace csa2 {
 
 constexpr int kRopeMaxPairs = 256;
 
-// Turns (angle / 2 pi) a position adds to pair i: the YaRN frequency (Peng et al. 2023,
-// NTK-by-parts) of base^(-2i/dim), in fp64 as the Compressor's. A kernel argument (2 KB).
+// Turns (angle / 2 pi) a position adds to pair i, in units of 2^-64: the YaRN frequency (Peng
+// et al. 2023, NTK-by-parts) of base^(-2i/dim), computed in fp64 as the Compressor's. Whole
+// turns drop out, as positions are integers. A kernel argument (2 KB).
 struct RopeTable {
     int dim;  // rotated channels; 0: no rotation
-    double turns[kRopeMaxPairs];
+    uint64_t turns[kRopeMaxPairs];
 };
 
 // Built once per thread and setting (a program rarely alternates between two): the powers of
@@ -42,7 +43,10 @@ inline const RopeTable& rope_table(const csa2_params* p, int dim) {
         if (r > p->rope_beta_fast) keep = 1.0;
         else if (r < p->rope_beta_slow) keep = 0.0;
         else keep = (r - p->rope_beta_slow) / ((double)p->rope_beta_fast - (double)p->rope_beta_slow);
-        t->turns[i] = f * keep + (f / (double)p->rope_factor) * (1.0 - keep);
+        const double turns = f * keep + (f / (double)p->rope_factor) * (1.0 - keep);
+        // the fraction in two halves: fp64 holds 53 bits of it, all of which are kept
+        const double hi = (turns - std::floor(turns)) * 4294967296.0, whole = std::floor(hi);
+        t->turns[i] = ((uint64_t)whole << 32) + (uint64_t)((hi - whole) * 4294967296.0);
     }
     return last.t;
 }
@@ -52,20 +56,19 @@ inline bool rope_settings_ok(const csa2_params* p) {
            p->rope_beta_fast > p->rope_beta_slow;
 }
 
-// Cosine and sine of `pos` positions at `turns` a position. The whole quarter turns are
-// taken off in fp64 (a product of about 2^-53 relative error: 2e-11 turns at a million
-// positions); what is left, at most an eighth of a turn, keeps 24 bits in fp32.
-__device__ __forceinline__ float2 rope_cs(double turns, int pos) {
-    const double t = turns * (double)pos;
-    const double quarters = rint(4.0 * t);
+// Cosine and sine of `pos` positions at `turns` a position. The product is exact modulo whole
+// turns in 64-bit integers (GB300's fp64 rate, two lanes a cycle and SM, would bound the
+// kernels here: 19 us against 11 for 16,004 rows of csa2_page_write). The quarter turns are
+// taken off; the rest, at most an eighth of a turn, keeps 32 bits behind the point (2^-33 turns
+// off) and 24 bits in fp32.
+__device__ __forceinline__ float2 rope_cs(uint64_t turns, int pos) {
+    const uint64_t t = turns * (uint64_t)(uint32_t)pos;
+    const uint32_t quarters = (uint32_t)((t + (1ull << 61)) >> 62);
+    const int rest = (int)((t - ((uint64_t)quarters << 62)) >> 32);
     float s, c;
-    sincospif(2.0f * (float)fma(-0.25, quarters, t), &s, &c);
-    switch ((int)(__double2ll_rn(quarters) & 3)) {
-        case 0: return make_float2(c, s);
-        case 1: return make_float2(-s, c);
-        case 2: return make_float2(-c, -s);
-        default: return make_float2(s, -c);
-    }
+    sincospif((float)rest * 0x1p-31f, &s, &c);
+    const float a = quarters & 1u ? s : c, b = quarters & 1u ? c : s;  // |cos|, |sin| by quarter
+    return make_float2(quarters == 1u || quarters == 2u ? -a : a, quarters & 2u ? -b : b);
 }
 
 }  // namespace csa2
