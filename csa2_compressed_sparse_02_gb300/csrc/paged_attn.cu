@@ -1,12 +1,15 @@
 // csa2_paged_attn: dense attention of one new token per sequence over a paged cache of
 // latents (K = V), with a window, first tokens that stay visible and a sink logit.
 //
-// Schedule. The positions a sequence sees lie in tiles of 128 (its first tokens' tiles, then
-// those from the window's start to its end). The (sequence, tile) items of the whole batch
-// are cut into one contiguous range of equal length per CTA, from the lengths on the device.
-// A sequence within one range is finished there; one that ranges cut leaves a partial result
-// per piece (unnormalised O, running maximum m and sum l of each head), and k_paged_join
-// joins them in order: o = sum_i O_i 2^{m_i - M} / (2^{sink - M} + sum_i l_i 2^{m_i - M}).
+// Schedule, from the lengths on the device. The positions a sequence sees lie in tiles of 128
+// (its first tokens' tiles, then those from the window's start to its end).
+//  - At most as many sequences as CTAs: sequence b is cut into ceil(tiles_b / L) pieces of
+//    equal length, one CTA each, with the smallest L whose pieces fit the CTAs.
+//  - More sequences: the (sequence, tile) items of the batch are cut into one contiguous
+//    range of equal length per CTA.
+// A sequence in one piece is finished by its CTA; of a cut one every piece leaves a partial
+// result (unnormalised O, running maximum m and sum l of each head), and k_paged_join joins
+// them in order: o = sum_i O_i 2^{m_i - M} / (2^{sink - M} + sum_i l_i 2^{m_i - M}).
 #include <cuda.h>
 
 #include <atomic>
@@ -33,11 +36,11 @@ struct Args {
     const int32_t* seq;
     const int32_t* n_tokens;
     __nv_bfloat16* out;
-    int64_t* prefix;  // workspace: items before each sequence [B + 1]
+    int2* pieces;     // workspace: of each sequence the CTAs of its first and last piece [B]
     float* part;      // workspace: two partial results per CTA
     int32_t* dev_status;
     float scale_log2;
-    int ctas;         // of the attention kernel (the join needs its ranges)
+    int ctas;         // of the attention kernel
     int box_rows;     // rows of a copied box, 2^box_shift: divides 128 and the page size
     int box_shift;
 };
@@ -100,15 +103,27 @@ __device__ __forceinline__ float* part_of(const Args& a, int c, int slot) {
     return a.part + (2 * (int64_t)c + slot) * part_floats(a.heads);
 }
 
-// This CTA's range of items, and the sequence and tile its first item belongs to; CTA 0
-// leaves every sequence's first item in a.prefix for the join. Called by the whole CTA
-// (a multiple of 32 threads, at most 1,024).
+// What a CTA has to do: `items` tiles from tile j of sequence b on.
 struct Range {
     int64_t items;
     int b, j;
 };
+
+// A sequence's first and last CTA for the join, packed into an int2: y < x where nothing is
+// seen; the sign of x says that its first piece does not open its CTA's range.
+__device__ __forceinline__ int2 pieces_of(int c0, int c1, bool opens) {
+    return make_int2(opens ? c0 : c0 | (int)0x80000000, c1);
+}
+
+constexpr int kPlanWarps = 32;  // at most
+constexpr int kPlanSeqs = 255;  // sequences the first schedule plans for
+
+// This CTA's range, from the lengths of all sequences; CTA 0 leaves every sequence's pieces in
+// a.pieces. Called by the whole CTA (a multiple of 32 threads, at most 1,024).
 __device__ void plan(const Args& a, Range* sh) {
-    __shared__ int64_t warp_sum[32];
+    __shared__ int64_t warp_sum[kPlanWarps];
+    __shared__ int tiles[kPlanSeqs];
+    __shared__ int fits[kPlanWarps];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
     const bool lead = blockIdx.x == 0;
     // Exclusive sum of n over the CTA, and the sum of all.
@@ -132,37 +147,78 @@ __device__ void plan(const Args& a, Range* sh) {
         *all = sum;
         return before + inc - n;
     };
-    // The first sweep finds the total; a batch of at most a CTA's threads needs no second.
-    int64_t total = 0, n = 0, here = 0;
-    for (int b0 = 0; b0 < a.B; b0 += blockDim.x) {
-        n = b0 + tid < a.B ? view_of(a, b0 + tid, lead).tiles : 0;
-        int64_t all;
-        here = total + scan(n, &all);
-        total += all;
-    }
-    const Cut cut(total, a.ctas);
-    const int c = min((int)blockIdx.x, cut.n);
-    const int64_t at = cut.at(c), end = cut.at(min(c + 1, cut.n));
-    int64_t before = 0;
+    if (tid == 0) sh->items = 0;
+    int64_t total = 0;
+    const bool single = a.B <= a.ctas && a.B <= kPlanSeqs;
     for (int b0 = 0; b0 < a.B; b0 += blockDim.x) {
         const int b = b0 + tid;
-        if (a.B > (int)blockDim.x) {
-            n = b < a.B ? view_of(a, b, false).tiles : 0;
-            int64_t all;
-            here = before + scan(n, &all);
-            before += all;
+        const int n = b < a.B ? view_of(a, b, lead).tiles : 0;
+        if (single && b < a.B) tiles[b] = n;
+        int64_t all;
+        scan(n, &all);
+        total += all;
+    }
+    if (single) {
+        // The smallest L with sum_b ceil(tiles_b / L) <= CTAs: at least total / CTAs, and
+        // total / (CTAs - B) is enough, as rounding up adds less than one a sequence. Every warp
+        // tries one value a round. (total < 2^32: at most 255 sequences of 2^24 tiles.)
+        const uint32_t all = (uint32_t)total, ctas = a.ctas, spare = ctas - a.B;
+        uint32_t lo = max(1u, (all + ctas - 1) / ctas);                       // L >= lo
+        uint32_t hi = max(lo, spare ? (all + spare - 1) / spare : all);       // L <= hi
+        while (lo < hi) {
+            const uint32_t step = (hi - lo + warps - 1) / warps, cand = lo + step * warp;
+            bool ok = true;  // hi fits
+            if (cand < hi) {
+                uint32_t n = 0;
+                for (int b = lane; b < a.B; b += 32) n += ((uint32_t)tiles[b] + cand - 1) / cand;
+                ok = __reduce_add_sync(0xffffffffu, n) <= ctas;
+            }
+            if (lane == 0) fits[warp] = ok;
+            __syncthreads();
+            const uint32_t good = __ballot_sync(0xffffffffu, lane < warps && fits[lane]);
+            __syncthreads();
+            // the first warp whose value fits: L is at most its value, and above the one before
+            const uint32_t w = good ? __ffs(good) - 1 : warps;
+            hi = min(hi, lo + step * w);
+            if (w > 0) lo = min(hi, lo + step * (w - 1) + 1);
         }
-        if (b < a.B) {
+        const int L = (int)lo;
+        int64_t at = 0;  // CTAs before the sequences of this sweep
+        for (int b0 = 0; b0 < a.B; b0 += blockDim.x) {
+            const int b = b0 + tid;
+            const int t = b < a.B ? tiles[b] : 0, k = (t + L - 1) / L;
+            int64_t all;
+            const int64_t first = at + scan(k, &all);
+            at += all;
+            const int64_t i = (int64_t)blockIdx.x - first;
+            if (i >= 0 && i < k) {
+                sh->b = b;
+                sh->j = (int)(t * i / k);
+                sh->items = t * (i + 1) / k - t * i / k;
+            }
+            if (lead && b < a.B) a.pieces[b] = pieces_of((int)first, (int)first + k - 1, true);
+        }
+    } else {
+        const Cut cut(total, a.ctas);
+        const int c = min((int)blockIdx.x, cut.n);
+        const int64_t at = cut.at(c), end = cut.at(min(c + 1, cut.n));
+        int64_t before = 0;
+        for (int b0 = 0; b0 < a.B; b0 += blockDim.x) {
+            const int b = b0 + tid;
+            const int64_t n = b < a.B ? view_of(a, b, false).tiles : 0;
+            int64_t all;
+            const int64_t here = before + scan(n, &all);
+            before += all;
             if (at >= here && at < here + n) {
                 sh->b = b;
                 sh->j = (int)(at - here);
+                sh->items = end - at;
             }
-            if (lead) a.prefix[b] = here;
+            if (lead && b < a.B) {
+                const int c0 = n ? cut.holder(here) : 0;
+                a.pieces[b] = n ? pieces_of(c0, cut.holder(here + n - 1), cut.at(c0) == here) : make_int2(0, -1);
+            }
         }
-    }
-    if (tid == 0) {
-        sh->items = end - at;
-        if (lead) a.prefix[a.B] = total;
     }
     __syncthreads();
 }
@@ -904,77 +960,92 @@ template <bool kBf16, int NH>
 constexpr int smem_bytes() {
     return (int)sizeof(Shared<kBf16, NH>) + 1024;
 }
-static_assert(smem_bytes<true, 64>() <= 232448 && smem_bytes<true, 32>() <= 232448 && smem_bytes<true, 16>() <= 232448,
+// (plan() has 4,480 bytes of its own)
+static_assert(smem_bytes<true, 64>() <= 227840 && smem_bytes<true, 32>() <= 227840 && smem_bytes<true, 16>() <= 227840 &&
+                  smem_bytes<false, 64>() <= 227840 && smem_bytes<false, 32>() <= 227840 && smem_bytes<false, 16>() <= 227840,
               "shared memory of a CTA");
 
 // ---------------------------------------------------------------- join
-// One CTA per (sequence, head), a thread per four channels; with G groups of 128 threads,
-// group i takes every G-th piece and the groups' sums are added in order. Sequences that no
-// range boundary cuts were finished by the attention kernel; those that see nothing get their
-// zeros here. A chain of three round trips bounds it (the items, the pieces' values and
-// maxima, the output): up to eight pieces' values are requested together, before the weights
-// they will get are known.
-constexpr int kJoinThreads = 128;
+// A thread has four channels of a (sequence, head) and, with G groups of threads, every G-th
+// piece; the groups' sums are added in order. Sequences in one piece were finished by the
+// attention kernel; those that see nothing get their zeros here. A chain of three round trips
+// bounds it (the pieces, their values and maxima, the output): up to eight pieces' values are
+// requested together, before the weights they will get are known.
+//   narrow: one CTA of 128 threads per (sequence, head), one group;
+//   wide: four CTAs, of 32 channels' threads x 16 groups each.
 constexpr int kJoinBatch = 8;
-template <int G>
-__global__ void __launch_bounds__(kJoinThreads * G, 8 / G) k_paged_join(Args a) {
-    __shared__ float4 sums[G > 1 ? G - 1 : 1][kJoinThreads];
+template <bool kWide>
+struct Join {
+    static constexpr int kLanes = kWide ? 32 : 128, kGroups = kWide ? 16 : 1, kThreads = kLanes * kGroups;
+};
+template <bool kWide>
+__global__ void __launch_bounds__(Join<kWide>::kThreads) k_paged_join(Args a) {
+    constexpr int kLanes = Join<kWide>::kLanes, G = Join<kWide>::kGroups;
+    __shared__ float4 sums[G][kWide ? kLanes : 1];
     __shared__ float dens[G];
     grid_dep_wait();
-    const int lane = threadIdx.x & 31, ch = threadIdx.x % kJoinThreads, grp = threadIdx.x / kJoinThreads;
+    const int lane = threadIdx.x & 31, grp = kWide ? threadIdx.x / kLanes : 0;
+    const int ch = kWide ? blockIdx.z * kLanes + lane : threadIdx.x;
     const int b = blockIdx.x, h = blockIdx.y;
-    const int64_t total = a.prefix[a.B], s = a.prefix[b], e = a.prefix[b + 1];
+    const int2 span = a.pieces[b];
     const float s2 = a.sink ? a.sink[h] * kLog2e : -INFINITY;
     __nv_bfloat16* out = a.out + ((int64_t)b * a.heads + h) * kD + 4 * ch;
-    if (s == e) {
+    const int c0 = span.x & 0x7fffffff, c1 = span.y, slot0 = span.x < 0 ? 1 : 0;
+    if (c1 < c0) {
         if (grp == 0 && (!a.seq || a.seq[b] >= 0)) *reinterpret_cast<uint2*>(out) = make_uint2(0u, 0u);
         return;
     }
-    const Cut cut(total, a.ctas);
-    const int c0 = cut.holder(s), c1 = cut.holder(e - 1);
     if (c0 == c1) return;
     const int64_t mo = (int64_t)a.heads * kD + h, lo = mo + a.heads;
-    const int slot0 = cut.at(c0) == s ? 0 : 1;
     auto piece = [&](int c) { return part_of(a, c, c == c0 ? slot0 : 0); };
-    // this group's pieces c0 + grp + G i, i < n; lane = piece for the maxima of all
-    const int n = c1 - c0 >= grp ? (c1 - c0 - grp) / G + 1 : 0;
+    const int n = c1 - c0 >= grp ? (c1 - c0 - grp) / G + 1 : 0;  // this group's: c0 + grp + G i
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    float den = 0.f, M = s2;
+    float den = 0.f, M = s2, f = 0.f, l = 0.f;  // f, l: of the piece i0 + lane of 32
     for (int i0 = 0; i0 < n || i0 == 0; i0 += kJoinBatch) {
         float4 v[kJoinBatch];
-        float m[kJoinBatch], l[kJoinBatch];
 #pragma unroll
         for (int i = 0; i < kJoinBatch; ++i)
-            if (i0 + i < n) {
-                const float* p = piece(c0 + grp + G * (i0 + i));
-                v[i] = __ldcg(reinterpret_cast<const float4*>(p + (int64_t)h * kD) + ch);
-                m[i] = __ldcg(p + mo);
-                l[i] = __ldcg(p + lo);
+            if (i0 + i < n)
+                v[i] = __ldcg(reinterpret_cast<const float4*>(piece(c0 + grp + G * (i0 + i)) + (int64_t)h * kD) + ch);
+        if ((i0 & 31) == 0) {
+            float m = -INFINITY;
+            if (i0 + lane < n) {
+                const float* p = piece(c0 + grp + G * (i0 + lane));
+                m = __ldcg(p + mo);
+                l = __ldcg(p + lo);
             }
-        if (i0 == 0) {  // the maximum over all pieces
-            for (int c = c0 + lane; c <= c1; c += 32) M = fmaxf(M, piece(c)[mo]);
+            if (i0 == 0) {  // the maximum over all pieces
+                for (int c = c0 + lane; c <= c1; c += 256) {
+                    float t[8];
 #pragma unroll
-            for (int o = 16; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+                    for (int k = 0; k < 8; ++k) t[k] = c + 32 * k <= c1 ? __ldcg(piece(c + 32 * k) + mo) : -INFINITY;
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) M = fmaxf(M, t[k]);
+                }
+#pragma unroll
+                for (int o = 16; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+            }
+            f = m == -INFINITY ? 0.f : ex2(m - M);
         }
 #pragma unroll
         for (int i = 0; i < kJoinBatch; ++i)
             if (i0 + i < n) {
-                const float f = m[i] == -INFINITY ? 0.f : ex2(m[i] - M);
-                den = fmaf(l[i], f, den);
-                acc.x = fmaf(v[i].x, f, acc.x);
-                acc.y = fmaf(v[i].y, f, acc.y);
-                acc.z = fmaf(v[i].z, f, acc.z);
-                acc.w = fmaf(v[i].w, f, acc.w);
+                const float w = __shfl_sync(0xffffffffu, f, (i0 + i) & 31);
+                den = fmaf(__shfl_sync(0xffffffffu, l, (i0 + i) & 31), w, den);
+                acc.x = fmaf(v[i].x, w, acc.x);
+                acc.y = fmaf(v[i].y, w, acc.y);
+                acc.z = fmaf(v[i].z, w, acc.z);
+                acc.w = fmaf(v[i].w, w, acc.w);
             }
     }
-    if constexpr (G > 1) {
-        if (grp > 0) sums[grp - 1][ch] = acc;
-        if (ch == 0) dens[grp] = den;
+    if constexpr (kWide) {
+        sums[grp][lane] = acc;
+        if (lane == 0) dens[grp] = den;
         __syncthreads();
         if (grp > 0) return;
 #pragma unroll
         for (int i = 1; i < G; ++i) {
-            const float4 v = sums[i - 1][ch];
+            const float4 v = sums[i][lane];
             acc.x += v.x;
             acc.y += v.y;
             acc.z += v.z;
@@ -1039,9 +1110,9 @@ int launch_attn(const Args& a, const CUtensorMap& m, cudaLaunchConfig_t* cfg) {
     return check_launch("paged_attn");
 }
 
-int64_t prefix_bytes(int64_t B) { return (8 * (B + 1) + 255) & ~(int64_t)255; }
+int64_t pieces_bytes(int64_t B) { return (8 * B + 255) & ~(int64_t)255; }
 
-int64_t ws_need(int B, int heads, int ctas) { return prefix_bytes(B) + 2 * (int64_t)ctas * part_floats(heads) * 4; }
+int64_t ws_need(int B, int heads, int ctas) { return pieces_bytes(B) + 2 * (int64_t)ctas * part_floats(heads) * 4; }
 
 }  // namespace
 
@@ -1052,8 +1123,8 @@ cudaError_t preload_paged_attn() {
                             [] { return preload_kernel(k_paged_attn<false, 64>, smem_bytes<false, 64>()); },
                             [] { return preload_kernel(k_paged_attn<false, 32>, smem_bytes<false, 32>()); },
                             [] { return preload_kernel(k_paged_attn<false, 16>, smem_bytes<false, 16>()); },
-                            [] { return preload_kernel(k_paged_join<1>); },
-                            [] { return preload_kernel(k_paged_join<4>); }};
+                            [] { return preload_kernel(k_paged_join<false>); },
+                            [] { return preload_kernel(k_paged_join<true>); }};
     for (auto f : l)
         if (const cudaError_t e = f()) return e;
     return cudaSuccess;
@@ -1104,8 +1175,8 @@ extern "C" int csa2_paged_attn(const csa2_params* p, const csa2_pages* c, int la
     a.seq = seq;
     a.n_tokens = n_tokens;
     a.out = static_cast<__nv_bfloat16*>(out);
-    a.prefix = static_cast<int64_t*>(workspace);
-    a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + prefix_bytes(B));
+    a.pieces = static_cast<int2*>(workspace);
+    a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + pieces_bytes(B));
     a.dev_status = dev_status;
     a.scale_log2 = p->softmax_scale * kLog2e;
     a.ctas = ctas;
@@ -1132,14 +1203,14 @@ extern "C" int csa2_paged_attn(const csa2_params* p, const csa2_pages* c, int la
              : p->heads > 16 ? launch_attn<false, 32>(a, rows, &cfg) : launch_attn<false, 16>(a, rows, &cfg);
     }
     if (rc) return rc;
-    // A sequence is cut into about ctas / B pieces. Four groups of threads share them where
-    // that is more than one group requests at once (two sequences of 131,072, 76 pieces each:
-    // KJOIN4 against KJOIN1 us); where it is not, three groups would have nothing to do.
-    const bool wide = ctas / B > kJoinBatch;
-    cfg.gridDim = dim3(B, p->heads);
-    cfg.blockDim = dim3(wide ? 4 * kJoinThreads : kJoinThreads);
+    // A sequence is cut into about ctas / B pieces, which a narrow thread requests eight at a
+    // time. Measured (64 heads): 2 sequences of 131,072 (76 pieces) 77 us wide, 87 narrow; 8 of
+    // 8,192 (16 pieces) 46 wide, 36 narrow.
+    const bool wide = ctas / B > 32;
+    cfg.gridDim = dim3(B, p->heads, wide ? kD / (4 * Join<true>::kLanes) : 1);
+    cfg.blockDim = dim3(wide ? Join<true>::kThreads : Join<false>::kThreads);
     cfg.dynamicSmemBytes = 0;
-    if (wide) cudaLaunchKernelEx(&cfg, k_paged_join<4>, a);
-    else cudaLaunchKernelEx(&cfg, k_paged_join<1>, a);
+    if (wide) cudaLaunchKernelEx(&cfg, k_paged_join<true>, a);
+    else cudaLaunchKernelEx(&cfg, k_paged_join<false>, a);
     return check_launch("paged_attn: join");
 }
