@@ -52,28 +52,28 @@ constexpr int kCopy = 256;       // threads of a copying CTA
 constexpr int kSlice = 32768;    // bytes a copying CTA moves at a time
 constexpr int kWriteWarps = 8;   // rows a CTA of k_page_write takes
 constexpr int kOffsets = 1024;   // list entries whose offsets fit in shared memory
+constexpr int kOwners = 4096;    // sequences whose owners do
+constexpr int kFresh = 1024;     // free pages that do
 
 // Scratch (256-byte aligned): offsets of reserve [longest list + 1] int64; then int32:
-// owner [max_seqs], parent marks [max_seqs], new pages [longest list], and three lists of
-// n_pages. A list of sequences may be as long as there are sequences, or 1,024 with padding.
+// owner [max_seqs], new pages [longest list], and three lists of n_pages. A list of sequences may be as long as there are sequences, or 1,024 with padding.
 struct Scratch {
     int64_t* offset;
-    int32_t *owner, *mark, *fresh, *list, *list2, *map;
-    int32_t* count;  // [0]: moves planned by compact
+    int32_t *owner, *fresh, *list, *list2, *map;
+    int32_t* count;  // compact: pages to move, pages in use
 };
 
 int64_t longest_list(int64_t max_seqs) { return max_seqs > kOffsets ? max_seqs : kOffsets; }
 
 int64_t scratch_bytes(int64_t max_seqs, int64_t n_pages) {
-    return 8 * (longest_list(max_seqs) + 1) + 4 * (2 * max_seqs + longest_list(max_seqs) + 3 * n_pages + 1);
+    return 8 * (longest_list(max_seqs) + 1) + 4 * (max_seqs + longest_list(max_seqs) + 3 * n_pages + 2);
 }
 
 Scratch scratch_of(void* ws, const Pages& g) {
     Scratch s;
     s.offset = static_cast<int64_t*>(ws);
     s.owner = reinterpret_cast<int32_t*>(s.offset + longest_list(g.max_seqs) + 1);
-    s.mark = s.owner + g.max_seqs;
-    s.fresh = s.mark + g.max_seqs;
+    s.fresh = s.owner + g.max_seqs;
     s.list = s.fresh + longest_list(g.max_seqs);
     s.list2 = s.list + g.n_pages;
     s.map = s.list2 + g.n_pages;
@@ -118,9 +118,10 @@ __device__ __forceinline__ int4 ref4(const Pages& g, int64_t at) {
 }
 
 // The `want` lowest free pages into list[], by the whole CTA; returns how many there are.
-__device__ int lowest_free(const Pages& g, int64_t want, int32_t* list) {
+// `first` holds the counts of pages 4 tid .. + 3, requested by the caller ahead of time.
+__device__ int lowest_free(const Pages& g, int64_t want, int32_t* list, int4 first) {
     int64_t have = 0;
-    int4 v = ref4(g, 4 * (int64_t)threadIdx.x);
+    int4 v = first;
     for (int64_t base = 0; base < g.n_pages && have < want; base += 4 * kPlan) {
         const int64_t at = base + 4 * (int64_t)threadIdx.x;
         const int4 nx = ref4(g, at + 4 * kPlan);  // the next round's, on its way during this one
@@ -146,13 +147,16 @@ __global__ void __launch_bounds__(kPlan)
 k_page_reserve(Pages g, int N, const int32_t* seq, const int32_t* n_from,
                const int32_t* n_to, Scratch ws, int32_t* dev_status) {
     __shared__ int64_t off_s[kOffsets + 1];
+    __shared__ int32_t owner_s[kOwners], list_s[kFresh];
     sm100::grid_dep_wait();
     const int tid = threadIdx.x;
+    const int4 first_ref = ref4(g, 4 * (int64_t)tid);
+    int32_t* owner = g.max_seqs <= kOwners ? owner_s : ws.owner;
     for (int i = tid; i < N; i += kPlan)
-        if (seq[i] >= 0 && seq[i] < g.max_seqs) ws.owner[seq[i]] = INT_MAX;
+        if (seq[i] >= 0 && seq[i] < g.max_seqs) owner[seq[i]] = INT_MAX;
     __syncthreads();
     for (int i = tid; i < N; i += kPlan)
-        if (seq[i] >= 0 && seq[i] < g.max_seqs) atomicMin(&ws.owner[seq[i]], i);
+        if (seq[i] >= 0 && seq[i] < g.max_seqs) atomicMin(&owner[seq[i]], i);
     __syncthreads();
     int64_t* off = N <= kOffsets ? off_s : ws.offset;
     int64_t entries = 0;
@@ -161,7 +165,7 @@ k_page_reserve(Pages g, int N, const int32_t* seq, const int32_t* n_from,
         int64_t n = 0;
         if (i < N && seq[i] >= 0) {
             const int s = seq[i], a = n_from[i], e = n_to[i];
-            if (s >= g.max_seqs || ws.owner[s] != i) raise_status(dev_status, CSA2_DEV_BAD_INDEX);
+            if (s >= g.max_seqs || owner[s] != i) raise_status(dev_status, CSA2_DEV_BAD_INDEX);
             else if (a < 0 || e > g.max_len()) raise_status(dev_status, CSA2_DEV_BAD_LENGTH);
             else if (e > a) n = ((int64_t)e + g.page_size - 1) / g.page_size - a / g.page_size;
         }
@@ -171,7 +175,8 @@ k_page_reserve(Pages g, int N, const int32_t* seq, const int32_t* n_from,
         entries += total;
     }
     if (tid == 0) off[N] = entries;
-    const int free = lowest_free(g, entries, ws.list);  // ends with a CTA barrier
+    int32_t* list = entries <= kFresh ? list_s : ws.list;
+    const int free = lowest_free(g, entries, list, first_ref);  // ends with a CTA barrier
     int taken = 0;
     for (int64_t e0 = 0; e0 < entries; e0 += kPlan) {
         const int64_t e = e0 + tid;
@@ -190,7 +195,7 @@ k_page_reserve(Pages g, int N, const int32_t* seq, const int32_t* n_from,
         const int k = taken + block_scan(entry ? 1 : 0, &total);
         if (entry) {
             if (k < free) {
-                const int32_t page = ws.list[k];
+                const int32_t page = list[k];
                 *entry = page;
                 g.ref[page] = 1;
             } else {
@@ -240,18 +245,21 @@ k_fork_plan(Pages g, int N, const int32_t* parent, const int32_t* child,
             const int32_t* n_tokens, Scratch ws, int32_t* dev_status) {
     sm100::grid_dep_wait();
     sm100::grid_dep_launch_dependents();
+    __shared__ int32_t owner_s[kOwners], list_s[kFresh];
     const int tid = threadIdx.x;
+    const int4 first_ref = ref4(g, 4 * (int64_t)tid);
+    int32_t* owner = g.max_seqs <= kOwners ? owner_s : ws.owner;
     for (int i = tid; i < N; i += kPlan) {
         const int c = child[i], p = parent[i];
-        if (c >= 0 && c < g.max_seqs) ws.owner[c] = INT_MAX, ws.mark[c] = 0;
-        if (p >= 0 && p < g.max_seqs) ws.mark[p] = 0;
+        if (c >= 0 && c < g.max_seqs) owner[c] = INT_MAX;
+        if (p >= 0 && p < g.max_seqs) owner[p] = INT_MAX;
     }
     __syncthreads();
-    for (int i = tid; i < N; i += kPlan) {
+    for (int i = tid; i < N; i += kPlan) {  // a child's owner is its first fork; a parent's is -1
         const int c = child[i], p = parent[i];
         if (c < 0) continue;
-        if (c < g.max_seqs) atomicMin(&ws.owner[c], i);
-        if (p >= 0 && p < g.max_seqs) ws.mark[p] = 1;
+        if (c < g.max_seqs) atomicMin(&owner[c], i);
+        if (p >= 0 && p < g.max_seqs) atomicMin(&owner[p], -1);
     }
     __syncthreads();
     int copies = 0;
@@ -261,7 +269,7 @@ k_fork_plan(Pages g, int N, const int32_t* parent, const int32_t* child,
         if (i < N && child[i] >= 0) {
             const int c = child[i], p = parent[i];
             const int64_t T = n_tokens[i];
-            if (c >= g.max_seqs || p < 0 || p >= g.max_seqs || ws.owner[c] != i || ws.mark[c]) {
+            if (c >= g.max_seqs || p < 0 || p >= g.max_seqs || owner[c] != i) {
                 raise_status(dev_status, CSA2_DEV_BAD_INDEX);
             } else if (T < 0 || T > g.max_len()) {
                 raise_status(dev_status, CSA2_DEV_BAD_LENGTH);
@@ -279,13 +287,14 @@ k_fork_plan(Pages g, int N, const int32_t* parent, const int32_t* child,
         if (i < N) ws.fresh[i] = state == 1 ? k : state;
         copies += total;
     }
-    const int free = lowest_free(g, copies, ws.list);
+    int32_t* list = copies <= kFresh ? list_s : ws.list;
+    const int free = lowest_free(g, copies, list, first_ref);
     for (int i = tid; i < N; i += kPlan) {
         const int k = ws.fresh[i];
         if (k < 0) continue;
         if (k < free) {
-            ws.fresh[i] = ws.list[k];
-            g.ref[ws.list[k]] = 1;
+            ws.fresh[i] = list[k];
+            g.ref[list[k]] = 1;
         } else {
             ws.fresh[i] = -1;
             raise_status(dev_status, CSA2_DEV_NO_PAGE);
@@ -347,66 +356,76 @@ k_fork_copy(Pages g, int slices, const int32_t* parent, const int32_t* child,
 }
 
 // ---------------------------------------------------------------- compact
+// Sixteen neighbouring pages a thread: 16,384 a sweep, whose counts stay in registers where
+// one sweep holds the pool.
+constexpr int kSweep = 16 * kPlan;
+
+// Bits 0..15: which of pages at .. at + 15 are used.
+__device__ __forceinline__ uint32_t used16(const Pages& g, int64_t at) {
+    int4 v[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) v[q] = ref4(g, at + 4 * q);
+    uint32_t bits = 0;
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+        bits |= ((v[q].x > 0 ? 1u : 0u) | (v[q].y > 0 ? 2u : 0u) | (v[q].z > 0 ? 4u : 0u) | (v[q].w > 0 ? 8u : 0u)) << (4 * q);
+    const int64_t in = g.n_pages - at;  // ref4 reads pages past the end as used
+    return in >= 16 ? bits : in <= 0 ? 0u : bits & ((1u << in) - 1u);
+}
+
 __global__ void __launch_bounds__(kPlan)
 k_compact_plan(Pages g, Scratch ws, int32_t* n_used) {
     sm100::grid_dep_wait();
     sm100::grid_dep_launch_dependents();
     const int tid = threadIdx.x;
+    uint32_t bits = 0;
     int mine = 0;
-    for (int64_t at = 4 * (int64_t)tid; at < g.n_pages; at += 4 * kPlan) {
-        const int4 v = ref4(g, at);
-        const int in = (int)min((int64_t)4, g.n_pages - at);
-        mine += (v.x > 0) + (in > 1 && v.y > 0) + (in > 2 && v.z > 0) + (in > 3 && v.w > 0);
+    for (int64_t base = 0; base < g.n_pages; base += kSweep) {
+        bits = used16(g, base + 16 * (int64_t)tid);
+        mine += __popc(bits);
     }
     int used;
     block_scan(mine, &used);
     int from = 0, to = 0;  // pages to move so far, free pages below `used` so far
-    int4 v = ref4(g, 4 * (int64_t)tid);
-    for (int64_t base = 0; base < g.n_pages; base += 4 * kPlan) {
-        const int64_t at = base + 4 * (int64_t)tid;
-        const int4 nx = ref4(g, at + 4 * kPlan);
-        const int c[4] = {v.x, v.y, v.z, v.w};
-        int n = 0;  // moves in the low half, free places in the high half (at most 4,096 each)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const int64_t page = at + k;
-            if (page >= g.n_pages) continue;
-            if (page < used) n += c[k] <= 0 ? 1 << 16 : 0;
-            else n += c[k] > 0 ? 1 : 0;
-        }
-        int total;
-        const int before = block_scan(n, &total);
+    for (int64_t base = 0; base < g.n_pages; base += kSweep) {
+        const int64_t at = base + 16 * (int64_t)tid;
+        if (g.n_pages > kSweep) bits = used16(g, at);
+        const int64_t below = min(max((int64_t)used - at, (int64_t)0), (int64_t)16);  // of the 16, pages < used
+        const int64_t in = min(max((int64_t)g.n_pages - at, (int64_t)0), (int64_t)16);
+        const uint32_t low = (1u << below) - 1u, all = (1u << in) - 1u;
+        uint32_t gaps = ~bits & low & all, moves = bits & ~low & all;
+        int total;  // moves in the low half, gaps in the high half (at most 16,384 each)
+        const int before = block_scan(__popc(moves) | __popc(gaps) << 16, &total);
         int f = from + (before & 0xffff), t = to + (before >> 16);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const int64_t page = at + k;
-            if (page >= g.n_pages) continue;
-            ws.map[page] = (int32_t)page;
-            if (page < used) {
-                if (c[k] <= 0) ws.list2[t++] = (int32_t)page;
-            } else if (c[k] > 0) {
-                ws.list[f++] = (int32_t)page;
-            }
+        for (; gaps; gaps &= gaps - 1) ws.list2[t++] = (int32_t)at + __ffs(gaps) - 1;
+        for (; moves; moves &= moves - 1) ws.list[f++] = (int32_t)at + __ffs(moves) - 1;
+        for (uint32_t idle = ~bits & ~low & all; idle; idle &= idle - 1) {  // nothing to follow
+            const int32_t page = (int32_t)at + __ffs(idle) - 1;
+            ws.map[page] = page;
         }
         from += total & 0xffff;
         to += total >> 16;
-        v = nx;
     }
     __syncthreads();
-    for (int i = tid; i < from; i += kPlan) {
-        const int32_t a = ws.list[i], b = ws.list2[i];
-        ws.map[a] = b;
-        g.ref[b] = g.ref[a];
-        g.ref[a] = 0;
+    // (map[] is filled from page `used` on: pages below it stay)
+    for (int i0 = tid; i0 < from; i0 += 8 * kPlan) {
+        int32_t a[8], b[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (i0 + k * kPlan < from) a[k] = ws.list[i0 + k * kPlan], b[k] = ws.list2[i0 + k * kPlan];
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (i0 + k * kPlan < from) ws.map[a[k]] = b[k];
     }
     if (tid == 0) {
-        *ws.count = from;
+        ws.count[0] = from;
+        ws.count[1] = used;
         if (n_used) *n_used = used;
     }
 }
 
-// Moves the planned pages (from above the used count to below it: no move reads what
-// another writes) and renames the table's entries.
+// Moves the planned pages and their counts (from above the used count to below it: no move
+// reads what another writes) and renames the table's entries.
 __global__ void __launch_bounds__(kCopy)
 k_compact_move(Pages g, Scratch ws, int32_t* dev_status) {
     sm100::grid_dep_wait();
@@ -420,10 +439,16 @@ k_compact_move(Pages g, Scratch ws, int32_t* dev_status) {
         copy_bytes(base + ws.list2[i] * g.page_bytes() + at, base + ws.list[i] * g.page_bytes() + at,
                    min((int64_t)kSlice, g.page_bytes() - at));
     }
+    for (int i = blockIdx.x * kCopy + threadIdx.x; i < ws.count[0]; i += gridDim.x * kCopy) {
+        const int32_t a = ws.list[i];
+        g.ref[ws.list2[i]] = g.ref[a];
+        g.ref[a] = 0;
+    }
+    const int used = ws.count[1];
     const int64_t entries = (int64_t)g.max_seqs * g.max_pages;
     for (int64_t e = (int64_t)blockIdx.x * kCopy + threadIdx.x; e < entries; e += (int64_t)gridDim.x * kCopy) {
         const int32_t page = g.table[e];
-        if (page < 0) continue;
+        if (page < used) continue;
         if (page < g.n_pages) g.table[e] = ws.map[page];
         else raise_status(dev_status, CSA2_DEV_BAD_INDEX);
     }
