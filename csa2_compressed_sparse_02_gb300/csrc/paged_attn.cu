@@ -118,109 +118,127 @@ __device__ __forceinline__ int2 pieces_of(int c0, int c1, bool opens) {
 constexpr int kPlanWarps = 32;  // at most
 constexpr int kPlanSeqs = 255;  // sequences the first schedule plans for
 
-// This CTA's range, from the lengths of all sequences; CTA 0 leaves every sequence's pieces in
-// a.pieces. Called by the whole CTA (a multiple of 32 threads, at most 1,024).
-__device__ void plan(const Args& a, Range* sh) {
-    __shared__ int64_t warp_sum[kPlanWarps];
-    __shared__ int tiles[kPlanSeqs];
+// Sum over the warp, and with it the sum over the lanes before this one.
+__device__ __forceinline__ uint32_t warp_scan(uint32_t v, int lane) {
+    uint32_t inc = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t up = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += up;
+    }
+    return inc - v;
+}
+
+// At most as many sequences as CTAs (and kPlanSeqs: one a thread).
+__device__ void plan_pieces(const Args& a, Range* sh) {
+    __shared__ uint32_t warp_sum[2][kPlanWarps];
+    __shared__ uint32_t tiles[kPlanSeqs];
     __shared__ int fits[kPlanWarps];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
     const bool lead = blockIdx.x == 0;
-    // Exclusive sum of n over the CTA, and the sum of all.
-    auto scan = [&](int64_t n, int64_t* all) {
-        int64_t inc = n;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int64_t up = __shfl_up_sync(0xffffffffu, inc, o);
-            if (lane >= o) inc += up;
+    const uint32_t t = tid < a.B ? view_of(a, tid, lead).tiles : 0;
+    if (tid < a.B) tiles[tid] = t;
+    const uint32_t mine = __reduce_add_sync(0xffffffffu, t);
+    if (lane == 0) warp_sum[0][warp] = mine;
+    if (tid == 0) sh->items = 0;
+    __syncthreads();
+    // (below 2^32: 255 sequences of at most 2^24 tiles)
+    const uint32_t all = __reduce_add_sync(0xffffffffu, lane < warps ? warp_sum[0][lane] : 0u);
+    // The smallest L with sum_b ceil(tiles_b / L) <= CTAs: at least all / CTAs, and
+    // all / (CTAs - B) is enough, as rounding up adds less than one a sequence. Every warp
+    // tries one value a round.
+    const uint32_t ctas = a.ctas, spare = ctas - a.B;
+    uint32_t lo = max(1u, (uint32_t)(((uint64_t)all + ctas - 1) / ctas));                   // L >= lo
+    uint32_t hi = max(lo, spare ? (uint32_t)(((uint64_t)all + spare - 1) / spare) : all);   // L <= hi
+    while (lo < hi) {
+        const uint32_t step = (hi - lo + warps - 1) / warps;
+        const uint64_t cand = lo + (uint64_t)step * warp;
+        bool ok = true;  // hi fits
+        if (cand < hi) {
+            uint32_t n = 0;
+            for (int b = lane; b < a.B; b += 32) n += (tiles[b] + (uint32_t)cand - 1) / (uint32_t)cand;
+            ok = __reduce_add_sync(0xffffffffu, n) <= ctas;
         }
-        if (lane == 31) warp_sum[warp] = inc;
+        if (lane == 0) fits[warp] = ok;
+        __syncthreads();
+        const uint32_t good = __ballot_sync(0xffffffffu, lane < warps && fits[lane]);
+        __syncthreads();
+        // the first warp whose value fits: L is at most its value, and above the one before
+        const uint32_t w = good ? __ffs(good) - 1 : warps;
+        hi = (uint32_t)min((uint64_t)hi, lo + (uint64_t)step * w);
+        if (w > 0) lo = (uint32_t)min((uint64_t)hi, lo + (uint64_t)step * (w - 1) + 1);
+    }
+    const uint32_t k = (t + lo - 1) / lo;
+    uint32_t first = warp_scan(k, lane);
+    if (lane == 31) warp_sum[1][warp] = first + k;
+    __syncthreads();
+    first += __reduce_add_sync(0xffffffffu, lane < warp ? warp_sum[1][lane] : 0u);
+    const int64_t i = (int64_t)blockIdx.x - first;
+    if (i >= 0 && i < k) {
+        sh->b = tid;
+        sh->j = (int)(t * i / k);
+        sh->items = t * (i + 1) / k - t * i / k;
+    }
+    if (lead && tid < a.B) a.pieces[tid] = pieces_of((int)first, (int)(first + k) - 1, true);
+    __syncthreads();
+}
+
+// More sequences than that: equal ranges of all items.
+__device__ void plan_ranges(const Args& a, Range* sh) {
+    __shared__ int64_t warp_sum[kPlanWarps];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
+    const bool lead = blockIdx.x == 0;
+    // Exclusive sum over the CTA of n < 2^25, and the sum of all.
+    auto scan = [&](uint32_t n, int64_t* all) {
+        const uint32_t before = warp_scan(n, lane);
+        if (lane == 31) warp_sum[warp] = before + n;
         __syncthreads();
         const int64_t w = lane < warps ? warp_sum[lane] : 0;
-        int64_t before = lane < warp ? w : 0, sum = w;
+        int64_t warps_before = lane < warp ? w : 0, sum = w;
 #pragma unroll
         for (int o = 16; o >= 1; o >>= 1) {
-            before += __shfl_xor_sync(0xffffffffu, before, o);
+            warps_before += __shfl_xor_sync(0xffffffffu, warps_before, o);
             sum += __shfl_xor_sync(0xffffffffu, sum, o);
         }
         __syncthreads();
         *all = sum;
-        return before + inc - n;
+        return warps_before + before;
     };
     if (tid == 0) sh->items = 0;
     int64_t total = 0;
-    const bool single = a.B <= a.ctas && a.B <= kPlanSeqs;
     for (int b0 = 0; b0 < a.B; b0 += blockDim.x) {
-        const int b = b0 + tid;
-        const int n = b < a.B ? view_of(a, b, lead).tiles : 0;
-        if (single && b < a.B) tiles[b] = n;
         int64_t all;
-        scan(n, &all);
+        scan(b0 + tid < a.B ? view_of(a, b0 + tid, lead).tiles : 0, &all);
         total += all;
     }
-    if (single) {
-        // The smallest L with sum_b ceil(tiles_b / L) <= CTAs: at least total / CTAs, and
-        // total / (CTAs - B) is enough, as rounding up adds less than one a sequence. Every warp
-        // tries one value a round. (total < 2^32: at most 255 sequences of 2^24 tiles.)
-        const uint32_t all = (uint32_t)total, ctas = a.ctas, spare = ctas - a.B;
-        uint32_t lo = max(1u, (all + ctas - 1) / ctas);                       // L >= lo
-        uint32_t hi = max(lo, spare ? (all + spare - 1) / spare : all);       // L <= hi
-        while (lo < hi) {
-            const uint32_t step = (hi - lo + warps - 1) / warps, cand = lo + step * warp;
-            bool ok = true;  // hi fits
-            if (cand < hi) {
-                uint32_t n = 0;
-                for (int b = lane; b < a.B; b += 32) n += ((uint32_t)tiles[b] + cand - 1) / cand;
-                ok = __reduce_add_sync(0xffffffffu, n) <= ctas;
-            }
-            if (lane == 0) fits[warp] = ok;
-            __syncthreads();
-            const uint32_t good = __ballot_sync(0xffffffffu, lane < warps && fits[lane]);
-            __syncthreads();
-            // the first warp whose value fits: L is at most its value, and above the one before
-            const uint32_t w = good ? __ffs(good) - 1 : warps;
-            hi = min(hi, lo + step * w);
-            if (w > 0) lo = min(hi, lo + step * (w - 1) + 1);
+    const Cut cut(total, a.ctas);
+    const int c = min((int)blockIdx.x, cut.n);
+    const int64_t at = cut.at(c), end = cut.at(min(c + 1, cut.n));
+    int64_t before = 0;
+    for (int b0 = 0; b0 < a.B; b0 += blockDim.x) {
+        const int b = b0 + tid;
+        const uint32_t n = b < a.B ? view_of(a, b, false).tiles : 0;
+        int64_t all;
+        const int64_t here = before + scan(n, &all);
+        before += all;
+        if (at >= here && at < here + n) {
+            sh->b = b;
+            sh->j = (int)(at - here);
+            sh->items = end - at;
         }
-        const int L = (int)lo;
-        int64_t at = 0;  // CTAs before the sequences of this sweep
-        for (int b0 = 0; b0 < a.B; b0 += blockDim.x) {
-            const int b = b0 + tid;
-            const int t = b < a.B ? tiles[b] : 0, k = (t + L - 1) / L;
-            int64_t all;
-            const int64_t first = at + scan(k, &all);
-            at += all;
-            const int64_t i = (int64_t)blockIdx.x - first;
-            if (i >= 0 && i < k) {
-                sh->b = b;
-                sh->j = (int)(t * i / k);
-                sh->items = t * (i + 1) / k - t * i / k;
-            }
-            if (lead && b < a.B) a.pieces[b] = pieces_of((int)first, (int)first + k - 1, true);
-        }
-    } else {
-        const Cut cut(total, a.ctas);
-        const int c = min((int)blockIdx.x, cut.n);
-        const int64_t at = cut.at(c), end = cut.at(min(c + 1, cut.n));
-        int64_t before = 0;
-        for (int b0 = 0; b0 < a.B; b0 += blockDim.x) {
-            const int b = b0 + tid;
-            const int64_t n = b < a.B ? view_of(a, b, false).tiles : 0;
-            int64_t all;
-            const int64_t here = before + scan(n, &all);
-            before += all;
-            if (at >= here && at < here + n) {
-                sh->b = b;
-                sh->j = (int)(at - here);
-                sh->items = end - at;
-            }
-            if (lead && b < a.B) {
-                const int c0 = n ? cut.holder(here) : 0;
-                a.pieces[b] = n ? pieces_of(c0, cut.holder(here + n - 1), cut.at(c0) == here) : make_int2(0, -1);
-            }
+        if (lead && b < a.B) {
+            const int c0 = n ? cut.holder(here) : 0;
+            a.pieces[b] = n ? pieces_of(c0, cut.holder(here + n - 1), cut.at(c0) == here) : make_int2(0, -1);
         }
     }
     __syncthreads();
+}
+
+// This CTA's range, from the lengths of all sequences; CTA 0 leaves every sequence's pieces in
+// a.pieces. Called by the whole CTA (a multiple of 32 threads, 256 to 1,024).
+__device__ void plan(const Args& a, Range* sh) {
+    if (a.B <= a.ctas && a.B <= kPlanSeqs) plan_pieces(a, sh);
+    else plan_ranges(a, sh);
 }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -399,11 +417,12 @@ __device__ void tma_role(Shared<kBf16, NH>& sh, const Args& a, const CUtensorMap
     bool has = it.next(a), gave_up = false;
     Boxes cur, nxt;
     if (has) cur = boxes_of(a, it, lane);
-    bool has_nx = has && it.next(a);
-    if (has_nx) {
-        nxt = boxes_of(a, it, lane);
-        if (nxt.mine) bulk_prefetch_l2(a.base + (int64_t)nxt.y * a.g.row_bytes, box_bytes);
-    }
+    bool has_nx = false;
+    auto look_ahead = [&]() -> Boxes {
+        const Boxes x = boxes_of(a, it, lane);
+        if (x.mine) bulk_prefetch_l2(a.base + (int64_t)x.y * a.g.row_bytes, box_bytes);
+        return x;
+    };
     for (int gt = 0; has && !gave_up; ++gt) {
         const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, cur.mine)) * a.box_rows * kRowBytes;
         for (int pr = 0; pr < 4; ++pr, ++g) {
@@ -428,15 +447,16 @@ __device__ void tma_role(Shared<kBf16, NH>& sh, const Args& a, const CUtensorMap
             }
         }
         // The ring holds little more than a tile and stands still between a tile's S and its
-        // PV. The tile after the next comes into L2 meanwhile, so that HBM does not stand still
-        // too and the refill is short.
+        // PV. The tile after the next comes into L2 meanwhile (both at the first), so that HBM
+        // does not stand still too and the refill is short.
+        if (gt == 0) {
+            has_nx = it.next(a);
+            if (has_nx) nxt = look_ahead();
+        }
         cur = nxt;
         has = has_nx;
         has_nx = has && it.next(a);
-        if (has_nx) {
-            nxt = boxes_of(a, it, lane);
-            if (nxt.mine) bulk_prefetch_l2(a.base + (int64_t)nxt.y * a.g.row_bytes, box_bytes);
-        }
+        if (has_nx) nxt = look_ahead();
     }
     // whatever ended the loop, no copy of this CTA outlives it
     for (int s = max(0, g - kPairs); s < g; ++s) mbar_wait_drain(&landed[s % kPairs], (uint32_t)((s / kPairs) & 1));
