@@ -994,6 +994,7 @@ static_assert(smem_bytes<true, 64>() <= 227840 && smem_bytes<true, 32>() <= 2278
 //   narrow: one CTA of 128 threads per (sequence, head), one group;
 //   wide: four CTAs, of 32 channels' threads x 16 groups each.
 constexpr int kJoinBatch = 8;
+constexpr int kMaxCtas = 256;  // of the attention kernel: a sequence has at most as many pieces
 template <bool kWide>
 struct Join {
     static constexpr int kLanes = kWide ? 32 : 128, kGroups = kWide ? 16 : 1, kThreads = kLanes * kGroups;
@@ -1002,7 +1003,7 @@ template <bool kWide>
 __global__ void __launch_bounds__(Join<kWide>::kThreads) k_paged_join(Args a) {
     constexpr int kLanes = Join<kWide>::kLanes, G = Join<kWide>::kGroups;
     __shared__ float4 sums[G][kWide ? kLanes : 1];
-    __shared__ float dens[G];
+    __shared__ float dens[G], m_s[kMaxCtas], l_s[kMaxCtas];
     grid_dep_wait();
     const int lane = threadIdx.x & 31, grp = kWide ? threadIdx.x / kLanes : 0;
     const int ch = kWide ? blockIdx.z * kLanes + lane : threadIdx.x;
@@ -1020,38 +1021,30 @@ __global__ void __launch_bounds__(Join<kWide>::kThreads) k_paged_join(Args a) {
     auto piece = [&](int c) { return part_of(a, c, c == c0 ? slot0 : 0); };
     const int n = c1 - c0 >= grp ? (c1 - c0 - grp) / G + 1 : 0;  // this group's: c0 + grp + G i
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    float den = 0.f, M = s2, f = 0.f, l = 0.f;  // f, l: of the piece i0 + lane of 32
+    float den = 0.f, M = s2;
     for (int i0 = 0; i0 < n || i0 == 0; i0 += kJoinBatch) {
         float4 v[kJoinBatch];
 #pragma unroll
         for (int i = 0; i < kJoinBatch; ++i)
             if (i0 + i < n)
                 v[i] = __ldcg(reinterpret_cast<const float4*>(piece(c0 + grp + G * (i0 + i)) + (int64_t)h * kD) + ch);
-        if ((i0 & 31) == 0) {
-            float m = -INFINITY;
-            if (i0 + lane < n) {
-                const float* p = piece(c0 + grp + G * (i0 + lane));
-                m = __ldcg(p + mo);
-                l = __ldcg(p + lo);
+        if (i0 == 0) {  // every piece's maximum and sum, once a CTA
+            for (int c = threadIdx.x; c <= c1 - c0; c += Join<kWide>::kThreads) {
+                const float* p = piece(c0 + c);
+                m_s[c] = __ldcg(p + mo);
+                l_s[c] = __ldcg(p + lo);
             }
-            if (i0 == 0) {  // the maximum over all pieces
-                for (int c = c0 + lane; c <= c1; c += 256) {
-                    float t[8];
+            __syncthreads();
+            for (int c = lane; c <= c1 - c0; c += 32) M = fmaxf(M, m_s[c]);
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) t[k] = c + 32 * k <= c1 ? __ldcg(piece(c + 32 * k) + mo) : -INFINITY;
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) M = fmaxf(M, t[k]);
-                }
-#pragma unroll
-                for (int o = 16; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-            }
-            f = m == -INFINITY ? 0.f : ex2(m - M);
+            for (int o = 16; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
         }
 #pragma unroll
         for (int i = 0; i < kJoinBatch; ++i)
             if (i0 + i < n) {
-                const float w = __shfl_sync(0xffffffffu, f, (i0 + i) & 31);
-                den = fmaf(__shfl_sync(0xffffffffu, l, (i0 + i) & 31), w, den);
+                const int c = grp + G * (i0 + i);
+                const float m = m_s[c], w = m == -INFINITY ? 0.f : ex2(m - M);
+                den = fmaf(l_s[c], w, den);
                 acc.x = fmaf(v[i].x, w, acc.x);
                 acc.y = fmaf(v[i].y, w, acc.y);
                 acc.z = fmaf(v[i].z, w, acc.z);
@@ -1092,6 +1085,7 @@ int grid_of(const csa2_params* p) {
         if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
         if (dev < 64) sms[dev].store(n, std::memory_order_relaxed);
     }
+    if (n > kMaxCtas) n = kMaxCtas;
     return p->max_ctas > 0 && p->max_ctas < n ? p->max_ctas : n;
 }
 
