@@ -80,6 +80,6 @@ extern "C" int csa2_trace_attach(int32_t* record) {
     return CSA2_OK;
 }
 
-extern "C" int csa2_version(void) { return 300; }
+extern "C" int csa2_version(void) { return 400; }
 
 extern "C" const char* csa2_last_error(void) { return csa2::g_last_error.c_str(); }

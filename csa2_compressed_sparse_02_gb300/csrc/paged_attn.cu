@@ -1218,8 +1218,8 @@ extern "C" int csa2_paged_attn(const csa2_params* p, const csa2_pages* c, int la
     }
     if (rc) return rc;
     // A sequence is cut into about ctas / B pieces, which a narrow thread requests eight at a
-    // time. Measured (64 heads): 2 sequences of 131,072 (76 pieces) 77 us wide, 87 narrow; 8 of
-    // 8,192 (16 pieces) 46 wide, 36 narrow.
+    // time. Measured (64 heads, bf16): 1 sequence of 32,768 (128 pieces) 25 us wide, 43 narrow;
+    // 2 of 131,072 (74 each) 74 and 80; 8 of 8,192 (16 each) 47 and 32.
     const bool wide = ctas / B > 32;
     cfg.gridDim = dim3(B, p->heads, wide ? kD / (4 * Join<true>::kLanes) : 1);
     cfg.blockDim = dim3(wide ? Join<true>::kThreads : Join<false>::kThreads);

@@ -644,7 +644,7 @@ extern "C" int csa2_page_write(const csa2_params* p, const csa2_pages* c, int la
         return fail(CSA2_ERR_UNSUPPORTED, "page_write: rope_dim must be a multiple of 4 in [0, 512]");
     if (p->rope_dim > 0 && !rope_settings_ok(p))
         return fail(CSA2_ERR_INVALID_ARG,
-                    "page_write: rope needs theta, factor, orig_len > 0 and beta_fast > beta_slow");
+                    "page_write: rope needs finite settings, theta, factor, orig_len > 0 and beta_fast > beta_slow");
     if (N > (int64_t)INT_MAX * kWriteWarps) return fail(CSA2_ERR_UNSUPPORTED, "page_write: too many rows");
     if (N == 0) return CSA2_OK;
     if (!x || !seq || !pos) return fail(CSA2_ERR_INVALID_ARG, "page_write: NULL buffer");

@@ -241,13 +241,15 @@ extern "C" int csa2_rope(const csa2_params* p, int layout, int inverse, int64_t 
     if (first < 0 || first > head_dim - rot)
         return fail(CSA2_ERR_INVALID_ARG, "rope: the rotated channels must lie within the head");
     if (!rope_settings_ok(p))
-        return fail(CSA2_ERR_INVALID_ARG, "rope: needs theta, factor, orig_len > 0 and beta_fast > beta_slow");
+        return fail(CSA2_ERR_INVALID_ARG, "rope: needs finite settings, theta, factor, orig_len > 0 and beta_fast > beta_slow");
     if (N > ((int64_t)1 << 31) - 1) return fail(CSA2_ERR_UNSUPPORTED, "rope: more than 2^31 - 1 rows");
     if (N == 0 || heads == 0) return CSA2_OK;
     if (!x || !out || !pos) return fail(CSA2_ERR_INVALID_ARG, "rope: NULL buffer");
     const uintptr_t es = format == CSA2_BF16 ? 2 : 4;
     if (reinterpret_cast<uintptr_t>(x) % es || reinterpret_cast<uintptr_t>(out) % es)
         return fail(CSA2_ERR_ALIGN, "rope: x and out must be aligned to their element");
+    if ((N > 1 && out_row == 0) || (heads > 1 && out_head == 0))
+        return fail(CSA2_ERR_INVALID_ARG, "rope: rows or heads of out overlap");
     if (x == out && (x_row != out_row || x_head != out_head))
         return fail(CSA2_ERR_INVALID_ARG, "rope: in place, x and out must have the same strides");
     if (const int rc = ensure_loaded()) return rc;

@@ -3,6 +3,7 @@
 #pragma once
 
 #include <cmath>
+#include <initializer_list>
 
 #include "common.cuh"
 
@@ -52,6 +53,8 @@ inline const RopeTable& rope_table(const csa2_params* p, int dim) {
 }
 
 inline bool rope_settings_ok(const csa2_params* p) {
+    for (float v : {p->rope_theta, p->rope_factor, p->rope_orig_len, p->rope_beta_fast, p->rope_beta_slow})
+        if (!std::isfinite(v)) return false;
     return p->rope_theta > 0.f && p->rope_factor > 0.f && p->rope_orig_len > 0.f &&
            p->rope_beta_fast > p->rope_beta_slow;
 }

@@ -516,11 +516,12 @@ int csa2_sparse_attn_noalloc(const csa2_params* p, int B,
  *   also the gradient (dx = the inverse of dy);
  *   CSA2_ROPE_PAIRS: a, b = channels first + 2i, first + 2i + 1;
  *   CSA2_ROPE_HALF:  a, b = channels first + i, first + rope_dim/2 + i.
- * The other channels are copied. Angles are reduced in fp64; sines, cosines and the
- * products are fp32, rounded once to the output's type.
+ * The other channels are copied. Angles are reduced in 64-bit integers (exact modulo
+ * whole turns); sines, cosines and the products are fp32, rounded once to the output's type.
  *   x, out  format CSA2_BF16 or CSA2_F32; element (n, h, c) at n*row + h*head + c (strides
  *           in elements; the channels are contiguous). out may be x itself (same strides:
- *           only the rotated channels are touched) and must not overlap it otherwise.
+ *           only the rotated channels are touched) and must not overlap it, or itself,
+ *           otherwise.
  *   pos     [N] int32, device; a row with pos < 0 (padding) is left as it is in out.
  *   first   first rotated channel, or -1 for the last rope_dim channels.
  * Constraints: 2 <= rope_dim <= 512, even, first + rope_dim <= head_dim <= 4096; heads <= 4096.
@@ -638,7 +639,7 @@ size_t csa2_paged_attn_workspace_size(const csa2_params* p, const csa2_pages* c,
  * A sequence that sees nothing gets zeros. Rows and pages that are not seen are not used,
  * whatever they hold; their table entries may be -1.
  *   q    element (b, h, c) at b*q_seq + h*q_head + c, bf16, strides in elements (multiples
- *        of 8);  out [B, heads, D] bf16, contiguous;  both 16-byte aligned
+ *        of 8);  out [B, heads, D] bf16, contiguous, not overlapping q;  both 16-byte aligned
  *   sink [heads] fp32, or NULL for none (all -infinity)
  *   seq  [B] int32, device: the sequences' rows of the table (NULL: row b); the same one
  *        may appear often. seq[b] < 0 is padding: its output is left as it is.
@@ -648,8 +649,12 @@ size_t csa2_paged_attn_workspace_size(const csa2_params* p, const csa2_pages* c,
  *   position without a page (not seen) CSA2_DEV_BAD_INDEX.
  *   workspace: csa2_paged_attn_workspace_size bytes, 256-byte aligned, contents
  *   arbitrary; calls that share it must be ordered (one stream or events).
- * The (sequence, 128 positions) tiles of the batch are cut into one range of equal length
- * per CTA (one per SM, or p->max_ctas); a second kernel joins the sequences that were cut,
+ * On the 5th-generation tensor cores: bf16 pages as bf16 operands, E4M3 pages decoded
+ * exactly into f16 (the query scaled per head by a power of two); fp32 logits, sums and
+ * accumulators; the weights e^z are rounded to the operands' type, in numerator and
+ * denominator alike. A batch of at most as many sequences as CTAs (one per SM, or
+ * p->max_ctas) is cut into pieces of nearly equal length, one per CTA; a larger one into
+ * equal ranges of tiles of 128 positions. A second kernel joins the sequences that were cut,
  * in the order of their positions, so results do not vary from run to run.
  * Constraints: 1 <= heads <= 64, D == 512, kv_format BF16 or E4M3, q_format BF16, B <= 65535.
  */

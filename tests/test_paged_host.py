@@ -48,11 +48,14 @@ def test_rope_refusals(L):
         assert rope(L, params(rope_dim=dim), dim=1024) == UNSUPPORTED, dim
     assert rope(L, p, dim=62) == UNSUPPORTED and rope(L, p, dim=4100) == UNSUPPORTED
     assert rope(L, p, first=65) == INVALID and rope(L, p, first=-2) == INVALID
-    for over in (dict(rope_theta=0.0), dict(rope_factor=-1.0), dict(rope_beta_fast=1.0)):
+    for over in (dict(rope_theta=0.0), dict(rope_factor=-1.0), dict(rope_beta_fast=1.0),
+                 dict(rope_theta=float("inf")), dict(rope_factor=float("nan")),
+                 dict(rope_beta_slow=-float("inf"))):
         assert rope(L, params(rope_dim=64, **over)) == INVALID, over
     assert rope(L, p, x=None) == INVALID and rope(L, p, pos=None) == INVALID
     assert rope(L, p, x=A + 1) == ALIGN and rope(L, p, fmt=api.F32, out=A + 2) == ALIGN
     assert rope(L, p, out=A, orow=1024) == INVALID  # in place with other strides
+    assert rope(L, p, orow=0) == INVALID and rope(L, p, oh=0) == INVALID  # out over itself
     assert rope(L, p, N=0, x=None, out=None, pos=None) == 0 and rope(L, p, heads=0) == 0
     assert L.csa2_rope(None, 0, 0, 1, 1, 64, -1, api.BF16, A, 64, 64, A, 64, 64, A, None) == INVALID
 
