@@ -1,6 +1,20 @@
 // csa2_paged_attn: dense attention of one new token per sequence over a paged cache of
 // latents (K = V), with a window, first tokens that stay visible and a sink logit.
 //
+// Per tile of 128 positions, with the positions as the MMA's M (tcgen05, fp32 in TMEM):
+//   S^T[128 x heads] = K_tile[128 x 512] . Q^T,   P = 2^(S - m),   O^T[512 x heads] += V_tile^T . P^T
+// The tile is the A operand of both products, from one copy in shared memory: bf16 pages are
+// copied into the swizzled operand as they are, E4M3 pages are decoded into f16 there.
+//
+// What bounds it. HBM: a position is 1,024 bytes in bf16 (512 in E4M3), read once (134.68 MB
+// of DRAM reads for two sequences of 65,536). Shared memory: a tile of 64 heads moves 530 KB
+// through it in bf16 (128 in, 192 for each product, P), 4.1k cycles at 128 bytes a cycle; and
+// as one tile and the query fill it (208 KB), a tile's softmax stands between its two products,
+// about 1.2k cycles in which nothing else can run. 16 sequences of 131,072 with 64 heads:
+// 383 us, 5.6 TB/s (0.83 of the measured copy rate); with every page in L2 331 us, 5.3k cycles
+// a tile. E4M3, the same contexts: 428 us; the bytes pass twice more (copied, read, written
+// decoded: 656 KB a tile), 7.3k cycles a tile.
+//
 // Schedule, from the lengths on the device. The positions a sequence sees lie in tiles of 128
 // (its first tokens' tiles, then those from the window's start to its end).
 //  - At most as many sequences as CTAs: sequence b is cut into ceil(tiles_b / L) pieces of
@@ -605,8 +619,12 @@ __device__ __forceinline__ bool any_moved(Shared<kBf16, NH>& sh, int gt) {
 }
 
 // ---------------------------------------------------------------- MMA issuer
-// The whole warp walks the tiles and one elected lane issues: the operands' descriptors are
-// then the warp's (uniform registers), not a thread's that every MMA would have to move there.
+// The whole warp walks the tiles and one elected lane issues; what the descriptors are made
+// from is broadcast from a lane first. Both let them live in the warp's uniform registers,
+// where the MMA takes them from: issued by a thread that had left its warp, an MMA followed
+// the one before by 75 to 80 cycles, so by 61 to 64. (Alone, M = 128 MMAs from shared memory
+// follow by 40 cycles at N = 16 and 49 at N = 64; here the copies of the next rows share
+// shared memory with them.)
 template <bool kBf16, int NH>
 __device__ void mma_role(Shared<kBf16, NH>& sh, const Args& a, uint32_t tmem, volatile int* abort) {
     using S = Shape<kBf16, NH>;
@@ -629,12 +647,13 @@ __device__ void mma_role(Shared<kBf16, NH>& sh, const Args& a, uint32_t tmem, vo
             for (int pr = 0; pr < 4; ++pr) {
                 if (!mbar_wait_warp(&sh.full[slot], phase, abort)) return;
                 tc_fence_after();
+                const uint64_t dKs = dK + ((2 * (uint32_t)__shfl_sync(0xffffffffu, slot, 0) * kChunk) >> 4);
                 if (elect_one()) {
 #pragma unroll
                     for (int c = 0; c < 2; ++c)
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
-                            mma_f16(tmem + S::kColS, dK + (((2 * slot + c) * kChunk + 32 * k) >> 4),
+                            mma_f16(tmem + S::kColS, dKs + ((c * kChunk + 32 * k) >> 4),
                                     dQ + (((2 * pr + c) * NH * 128 + 32 * k) >> 4), S::kIdescS, (pr | c | k) != 0);
                 }
                 __syncwarp();
@@ -650,13 +669,15 @@ __device__ void mma_role(Shared<kBf16, NH>& sh, const Args& a, uint32_t tmem, vo
             if (any_moved(sh, gt) && !mbar_wait_warp(&sh.p_again, (uint32_t)(again++ & 1), abort)) return;
             tc_fence_after();
             slot = slot0;
+            const uint32_t more = __shfl_sync(0xffffffffu, j != pc.j0 ? 1u : 0u, 0);
 #pragma unroll
             for (int mb = 0; mb < 4; ++mb) {
+                const uint64_t dVs = dV + ((2 * (uint32_t)__shfl_sync(0xffffffffu, slot, 0) * kChunk) >> 4);
                 if (elect_one()) {
 #pragma unroll
                     for (int k = 0; k < 8; ++k)
-                        mma_f16(tmem + NH * mb, dV + ((2 * slot * kChunk + k * 2048) >> 4),
-                                dP + ((k * 16 * S::kPRow) >> 4), S::kIdescPV, j != pc.j0 || k != 0);
+                        mma_f16(tmem + NH * mb, dVs + ((k * 2048) >> 4),
+                                dP + ((k * 16 * S::kPRow) >> 4), S::kIdescPV, k == 0 ? more : 1u);
                     tc_commit(&sh.empty[slot]);
                 }
                 __syncwarp();
@@ -950,7 +971,7 @@ k_paged_attn(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap
     tc_fence_before();
     plan(a, &sh.range);  // ends with a CTA barrier
     tc_fence_after();
-    const uint32_t tmem = sh.tmem_base;
+    const uint32_t tmem = __shfl_sync(0xffffffffu, sh.tmem_base, 0);
     if (warp < S::kSoftWarps) {
         softmax_role<kBf16, NH>(sh, a, tmem, warp, lane, abort);
     } else if (warp == S::kMmaWarp) {
