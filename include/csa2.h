@@ -653,8 +653,8 @@ size_t csa2_paged_attn_workspace_size(const csa2_params* p, const csa2_pages* c,
  * exactly into f16 (the query scaled per head by a power of two); fp32 logits, sums and
  * accumulators; the weights e^z are rounded to the operands' type, in numerator and
  * denominator alike. A batch of at most as many sequences as CTAs (one per SM, or
- * p->max_ctas) is cut into pieces of nearly equal length, one per CTA; a larger one into
- * equal ranges of tiles of 128 positions. A second kernel joins the sequences that were cut,
+ * p->max_ctas) is cut into pieces of nearly equal length, one per CTA, where that leaves few
+ * CTAs idle; else into equal ranges of tiles of 128 positions. A second kernel joins the sequences that were cut,
  * in the order of their positions, so results do not vary from run to run.
  * Constraints: 1 <= heads <= 64, D == 512, kv_format BF16 or E4M3, q_format BF16, B <= 65535.
  */

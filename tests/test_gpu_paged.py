@@ -494,6 +494,45 @@ def test_attention_window_and_first_tokens(kv, heads, window, first):
     assert_attn(out, attn64(p, c, 0, q, sink, np.arange(len(T)), T, window, first), kv)
 
 
+@pytest.mark.parametrize("seed", range(24))
+def test_attention_random_batches(seed):
+    """Batches of both schedules (at most as many sequences as CTAs, and more), any page size,
+    head count, window and grid, empty sequences and padding among them."""
+    rng = np.random.default_rng(1000 + seed)
+    kv = [api.BF16, api.E4M3][seed % 2]
+    B = int(rng.choice([1, 2, 3, 9, 40, 153, 300]))
+    top = int(min(4000, 30000 // B))
+    T = rng.integers(0, top + 1, B) * (rng.random(B) < 0.9)
+    T[0] = top
+    heads, ps = int(rng.integers(1, 65)), 8 * int(rng.choice([1, 2, 3, 4, 7, 8, 16, 20, 32, 128]))
+    window = int(rng.choice([0, 1, rng.integers(1, top + 200), 128, 256]))
+    first = int(rng.choice([0, 1, 100, 128, 300])) if window else 0
+    p, c, q, sink = filled(kv, heads, T, ps, seed=seed, window=window, first=first)
+    p.max_ctas = int(rng.choice([0, 0, 1, 2, 7, 41, 150]))
+    rows = rng.permutation(B)
+    rows[rng.random(B) < 0.1] = -1
+    st = torch.zeros(1, dtype=torch.int32, device=DEV)
+    lens = np.where(rows >= 0, T[np.maximum(rows, 0)], 17)
+    out = attend(p, c, q, sink, rows, lens, window, first, st=st)
+    assert st.item() == 0
+    live = rows >= 0
+    assert torch.all(out[torch.from_numpy(~live).to(DEV)] == 9)
+    if live.any():
+        o, A, dz, F = attn64(p, c, 0, q, sink, rows, lens, window, first)
+        if np.linalg.norm(o[live]) > 0:
+            assert_attn(out[torch.from_numpy(live).to(DEV)], (o[live], A[live], dz, F[live]), kv)
+
+
+@pytest.mark.parametrize("kv", [api.BF16, api.E4M3], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("ctas,B", [(1, 1), (2, 2), (3, 3), (4, 3), (3, 4), (152, 151), (0, 160)])
+def test_attention_one_piece_or_ranges_at_the_border(kv, ctas, B):
+    T = [700 + 37 * (b % 5) for b in range(B)]
+    p, c, q, sink = filled(kv, 40, T, 32, seed=ctas + B)
+    p.max_ctas = ctas
+    out = attend(p, c, q, sink, None, T)
+    assert_attn(out, attn64(p, c, 0, q, sink, np.arange(B), T, 0, 0), kv)
+
+
 @pytest.mark.parametrize("kv", [api.BF16, api.E4M3], ids=["bf16", "e4m3"])
 def test_attention_long_and_split(kv):
     """One sequence over every CTA, and a few that share them unevenly; the same bytes in
@@ -683,6 +722,50 @@ def test_a_dense_layer_decodes_forks_and_compacts(kv):
     used = c.table[c.table >= 0]
     counts = torch.bincount(used.long(), minlength=64)
     assert torch.equal(counts.int(), c.ref)
+
+
+@pytest.mark.parametrize("kv", [api.BF16, api.E4M3], ids=["bf16", "e4m3"])
+def test_offsets_past_32_bits_and_positions_past_a_million(kv):
+    """Pages beyond 4 GB of a pool and beyond a layer's 4 GB, held at the far end of a long
+    table: written, forked, attended through a window, compacted to the front."""
+    n_pages = 70_001 if kv == api.BF16 else 140_001
+    ps, T, W, F = 64, 1_000_003, 300, 5
+    p = api.default_params(kv_format=kv, heads=16)
+    c = api.PagedCache(p, n_pages, ps, 3, 16_000, layers=2, device=DEV)
+    assert c.pool[0].numel() * c.pool.element_size() > 1 << 32
+    st = torch.zeros(1, dtype=torch.int32, device=DEV)
+    c.ref[:n_pages - 9] = 1  # taken by others: the lowest free page is far out
+    at = np.concatenate([np.arange(F), np.arange(T - W, T)])
+    api.page_reserve(p, c, i32([1]), i32([0]), i32([F]), st)
+    api.page_reserve(p, c, i32([1]), i32([T - W]), i32([T]), st)
+    held = c.table[1][c.table[1] >= 0]
+    assert st.item() == 0 and held.min().item() == n_pages - 9
+    assert held.numel() == 1 + 6  # page 0, and 15,620 (from 999,703) to 15,625 (to 1,000,002)
+    x = randn(len(at), D, seed=3)
+    for layer in (0, 1):
+        api.page_write(p, c, layer, x * (layer + 1), i32(np.ones(len(at))), i32(at), st)
+    api.page_fork(p, c, i32([1]), i32([2]), i32([T]), st)
+    q, sink = randn(1, 16, D, seed=4, dtype=torch.bfloat16), randn(16, seed=5)
+    k64 = {}
+    for layer in (0, 1):
+        rows = (x * (layer + 1)).to(dtype_of(kv)).double().cpu().numpy()
+        z = q[0].double().cpu().numpy() @ rows.T * float(p.softmax_scale)
+        sk = sink.double().cpu().numpy()[:, None]
+        e, es = np.exp(z - z.max()), np.exp(sk - z.max())
+        den = e.sum(1, keepdims=True) + es
+        o = e @ rows / den
+        k64[layer] = (o[None], (e @ np.abs(rows) / den)[None], 512 * 2.0 ** -24 * 40, np.abs(rows).sum(0)[None] + len(at) * np.abs(o)[None])
+    for row in (1, 2):
+        for layer in (0, 1):
+            assert_attn(attend(p, c, q, sink, [row], [T], W, F, layer=layer, st=st), k64[layer], kv)
+    c.ref[:n_pages - 9] = 0
+    n = torch.zeros(1, dtype=torch.int32, device=DEV)
+    api.page_compact(p, c, n, st)
+    # those 7, and the fork's copy of the last, which holds 3 rows
+    assert n.item() == 8 and c.table.max().item() == 7 and st.item() == 0
+    for row in (1, 2):
+        for layer in (0, 1):
+            assert_attn(attend(p, c, q, sink, [row], [T], W, F, layer=layer, st=st), k64[layer], kv)
 
 
 def test_two_streams_with_workspaces_of_their_own():
