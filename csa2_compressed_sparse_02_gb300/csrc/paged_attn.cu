@@ -1031,7 +1031,7 @@ struct Join {
     static constexpr int kLanes = kWide ? 32 : 128, kGroups = kWide ? 16 : 1, kThreads = kLanes * kGroups;
 };
 template <bool kWide>
-__global__ void __launch_bounds__(Join<kWide>::kThreads) k_paged_join(Args a) {
+__global__ void __launch_bounds__(Join<kWide>::kThreads, 1) k_paged_join(Args a) {
     constexpr int kLanes = Join<kWide>::kLanes, G = Join<kWide>::kGroups;
     __shared__ float4 sums[G][kWide ? kLanes : 1];
     __shared__ float dens[G], m_s[kMaxCtas], l_s[kMaxCtas];
