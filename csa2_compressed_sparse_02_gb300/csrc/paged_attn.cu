@@ -10,10 +10,10 @@
 // of DRAM reads for two sequences of 65,536). Shared memory: a tile of 64 heads moves 530 KB
 // through it in bf16 (128 in, 192 for each product, P), 4.1k cycles at 128 bytes a cycle; and
 // as one tile and the query fill it (208 KB), a tile's softmax stands between its two products,
-// about 1.2k cycles in which nothing else can run. 16 sequences of 131,072 with 64 heads:
-// 383 us, 5.6 TB/s (0.83 of the measured copy rate); with every page in L2 331 us, 5.3k cycles
-// a tile. E4M3, the same contexts: 428 us; the bytes pass twice more (copied, read, written
-// decoded: 656 KB a tile), 7.3k cycles a tile.
+// about 1.2k cycles in which nothing else can run. 16 sequences of 131,072 in bf16: 331 us with
+// 16 heads (6.5 TB/s, 0.96 of the measured copy rate), 390 with 64 (5.5 TB/s, 0.81; 331 with
+// every page in L2, 5.3k cycles a tile). In E4M3 with 64 heads 419 us: the bytes pass twice
+// more (copied, read, written decoded: 656 KB a tile).
 //
 // Schedule, from the lengths on the device. The positions a sequence sees lie in tiles of 128
 // (its first tokens' tiles, then those from the window's start to its end).
@@ -472,7 +472,8 @@ __device__ void tma_role(Shared<kBf16, NH>& sh, const Args& a, const CUtensorMap
         }
         // The ring holds little more than a tile and stands still between a tile's S and its
         // PV. The tile after the next comes into L2 meanwhile (both at the first), so that HBM
-        // does not stand still too and the refill is short.
+        // does not stand still too and the refill is short. (16 sequences of 131,072: 394 us;
+        // the next tile only 409, three tiles ahead 483.)
         if (gt == 0) {
             has_nx = it.next(a);
             if (has_nx) nxt = look_ahead();
