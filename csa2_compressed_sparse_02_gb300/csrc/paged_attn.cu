@@ -285,8 +285,11 @@ struct Shape {
     static constexpr int kHelpWarps = kBf16 ? 4 : 8;    // and, for E4M3, decode the rows
     static constexpr int kThreads = 32 * (kHelp0 + kHelpWarps);
     // Pairs of 64-channel chunks of a tile in the ring: a tile has 4; what the query leaves
-    // of shared memory lets the next tile's first pairs arrive early.
-    static constexpr int kPairs = NH == 64 ? 4 : NH == 32 ? 5 : 6;
+    // of shared memory lets the next tile's first pairs arrive early. An even number for E4M3,
+    // so that a pair's place always belongs to the same group of decoding warps: a group that
+    // skipped a phase of its barrier could take the one before for it.
+    static constexpr int kPairs = NH == 64 ? 4 : NH == 32 ? (kBf16 ? 5 : 4) : 6;
+    static_assert(kBf16 || kPairs % 2 == 0, "see above");
     static constexpr uint32_t kColS = 4 * NH;  // TMEM: O^T 4 x NH columns, then S^T
     static constexpr uint32_t kFmt = kBf16 ? 1u : 0u;
     // D fp32, A and B bf16 or f16, N = NH, M = 128; S: both K-major, PV: both MN-major
@@ -583,7 +586,7 @@ __device__ void decode_role(Shared<false, NH>& sh, const Args& a, int pt, int la
         for (int n = pc.j1 - pc.j0; n > 0; --n, ++gt) {
 #pragma unroll 1
             for (int pr = 0; pr < 4; ++pr) {
-                if ((pr & 1) == group) {
+                if ((pr & 1) == group) {  // (= slot & 1)
                     if (!mbar_wait(&sh.raw_full[slot], phase, abort)) return;
                     uint8_t* rows = sh.kv[slot][1] + row0 * 128;
                     const uint8_t* ok = &sh.row_ok[gt & 1][row0 + sub];
@@ -645,7 +648,8 @@ __device__ void mma_role(Shared<kBf16, NH>& sh, const Args& a, uint32_t tmem, vo
     const uint64_t dP = smem_desc(smem_u32(sh.p), 1024, 8 * S::kPRow, S::kPLayout);
     Pieces pi(sh.range);
     Piece pc;
-    int gt = 0, again = 0, slot0 = 0;  // tiles so far, those whose P came twice; slot of the tile's first pair and its phase
+    int gt = 0, again = 0;  // tiles so far, those whose P came twice
+    int slot0 = 0;          // slot of the tile's first pair, and its phase
     uint32_t phase0 = 0;
     for (int it = 0; pi.next(a, pc); ++it) {
         if (!mbar_wait_warp(&sh.q_full[it & 1], (uint32_t)((it >> 1) & 1), abort)) return;
@@ -740,10 +744,10 @@ __device__ __forceinline__ float warp_sum(float* v, int lane) {
 // The running maximum is lazy: it moves only when a tile would push P above 2^kLazyMax. A
 // tile therefore needs no maximum of its own as long as its logits stay below that: the warp
 // takes P from the maximum it has, and the four warps of a head group only agree that none of
-// them saw a larger logit (2,080 -> 900 cycles from S to P against finding each tile's
+// them saw a larger logit (2,080 -> 850 cycles from S to P against finding each tile's
 // maximum). The agreement rides on the barrier that hands P to the MMAs: an issuer that finds
-// a group's mark set waits for that group's second P. Where one did, or at a piece's first tile, the maxima are found and exchanged,
-// and the heads' columns of O are rescaled in TMEM.
+// a group's mark set waits for that group's second P. Where one is set, or at a piece's first
+// tile, the maxima are found and exchanged, and the heads' columns of O rescaled in TMEM.
 template <bool kBf16, int NH>
 __device__ void softmax_role(Shared<kBf16, NH>& sh, const Args& a, uint32_t tmem, int warp, int lane,
                              volatile int* abort) {
