@@ -285,11 +285,8 @@ struct Shape {
     static constexpr int kHelpWarps = kBf16 ? 4 : 8;    // and, for E4M3, decode the rows
     static constexpr int kThreads = 32 * (kHelp0 + kHelpWarps);
     // Pairs of 64-channel chunks of a tile in the ring: a tile has 4; what the query leaves
-    // of shared memory lets the next tile's first pairs arrive early. An even number for E4M3,
-    // so that a pair's place always belongs to the same group of decoding warps: a group that
-    // skipped a phase of its barrier could take the one before for it.
-    static constexpr int kPairs = NH == 64 ? 4 : NH == 32 ? (kBf16 ? 5 : 4) : 6;
-    static_assert(kBf16 || kPairs % 2 == 0, "see above");
+    // of shared memory lets the next tile's first pairs arrive early.
+    static constexpr int kPairs = NH == 64 ? 4 : NH == 32 ? 5 : 6;
     static constexpr uint32_t kColS = 4 * NH;  // TMEM: O^T 4 x NH columns, then S^T
     static constexpr uint32_t kFmt = kBf16 ? 1u : 0u;
     // D fp32, A and B bf16 or f16, N = NH, M = 128; S: both K-major, PV: both MN-major
@@ -525,8 +522,10 @@ __device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
     return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// Two groups of four warps take a tile's pairs in turn (a pair is one chain of waits, loads,
-// stores and a fence, so two run side by side), a warp 32 rows. The 128 bytes of a row that
+// Two groups of four warps take the pairs in turn (a pair is one chain of waits, loads, stores
+// and a fence, so two run side by side), a warp 32 rows. A place in the ring always has the
+// same group: one that skipped a phase of the place's barrier could take the phase before for
+// the one it waits for. The 128 bytes of a row that
 // become a pair of chunks lie where its 128 bytes of the second chunk will be: a warp reads its
 // rows, then writes both chunks over them, so the raw bytes take no room of their own.
 template <int NH>
@@ -586,7 +585,7 @@ __device__ void decode_role(Shared<false, NH>& sh, const Args& a, int pt, int la
         for (int n = pc.j1 - pc.j0; n > 0; --n, ++gt) {
 #pragma unroll 1
             for (int pr = 0; pr < 4; ++pr) {
-                if ((pr & 1) == group) {  // (= slot & 1)
+                if ((slot & 1) == group) {
                     if (!mbar_wait(&sh.raw_full[slot], phase, abort)) return;
                     uint8_t* rows = sh.kv[slot][1] + row0 * 128;
                     const uint8_t* ok = &sh.row_ok[gt & 1][row0 + sub];
