@@ -276,7 +276,7 @@ __device__ __forceinline__ float ex2(float x) {
 // NH: the heads, rounded up to the 16, 32 or 64 columns of the MMAs.
 template <bool kBf16, int NH>
 struct Shape {
-    static constexpr int kSoftWarps = kBf16 && NH >= 32 ? 16 : 8;
+    static constexpr int kSoftWarps = 8;            // (16 of them: 361 us for the 64-head case above, 8: 347)
     static constexpr int kGroups = kSoftWarps / 4;  // of heads: one per four lane quarters
     static constexpr int NC = NH / kGroups;         // heads of a softmax warp
     static constexpr int kMmaWarp = kSoftWarps;
@@ -436,6 +436,7 @@ __device__ void tma_role(Shared<kBf16, NH>& sh, const Args& a, const CUtensorMap
     uint64_t* const landed = kBf16 ? sh.full : sh.raw_full;
     const uint32_t dst0 = smem_u32(sh.kv[0][kBf16 ? 0 : 1]) + lane * a.box_rows * 128;
     const int box_bytes = a.box_rows * a.g.row_bytes;
+    const uint64_t once = l2_policy_evict_first();
     Tiles it(sh.range);
     int g = 0;  // pairs so far
     bool has = it.next(a), gave_up = false;
@@ -466,14 +467,16 @@ __device__ void tma_role(Shared<kBf16, NH>& sh, const Args& a, const CUtensorMap
             __syncwarp();
             if (cur.mine) {
                 const uint32_t dst = dst0 + 2 * slot * kChunk;
-                tma_g2s_2d(dst, tmap, 128 * pr, cur.y, &landed[slot]);
-                if constexpr (kBf16) tma_g2s_2d(dst + kChunk, tmap, 128 * pr + 64, cur.y, &landed[slot]);
+                tma_g2s_2d_hint(dst, tmap, 128 * pr, cur.y, &landed[slot], once);
+                if constexpr (kBf16) tma_g2s_2d_hint(dst + kChunk, tmap, 128 * pr + 64, cur.y, &landed[slot], once);
             }
         }
         // The ring holds little more than a tile and stands still between a tile's S and its
         // PV. The tile after the next comes into L2 meanwhile (both at the first), so that HBM
-        // does not stand still too and the refill is short. (16 sequences of 131,072: 394 us;
-        // the next tile only 409, three tiles ahead 483.)
+        // does not stand still too and the refill is short. What has been copied goes first
+        // when L2 makes room, and copies ask for their own lines only, so that it is never what
+        // waits there. (16 sequences of 131,072, 64 heads: 361 us, the next tile alone 418,
+        // three ahead 379; without the hint 393; with it, but copies widened to 256 bytes, 414.)
         if (gt == 0) {
             has_nx = it.next(a);
             if (has_nx) nxt = look_ahead();
@@ -1144,7 +1147,7 @@ int encode_rows(const Args& a, CUtensorMap* m) {
     const cuuint32_t box[2] = {bf16 ? 64u : 128u, (cuuint32_t)a.box_rows}, steps[2] = {1, 1};
     if (encode(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 2,
                const_cast<uint8_t*>(a.base), dims, strides, box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
-               bf16 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               bf16 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_NONE,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
         return fail(CSA2_ERR_CUDA, "paged_attn: tensor map of the pool");
     return CSA2_OK;

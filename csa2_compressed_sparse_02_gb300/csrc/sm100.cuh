@@ -202,12 +202,13 @@ __device__ __forceinline__ void bulk_g2s_hint(void* smem_dst, const void* gsrc, 
 }
 
 // Tiled copy of a box of a 2-d tensor map (an address in the kernel's parameters) to shared
-// memory; x * element size must be a multiple of 16 bytes.
-__device__ __forceinline__ void tma_g2s_2d(uint32_t smem_dst, const void* tmap, int x, int y, uint64_t* bar) {
+// memory, with an L2 policy for its lines; x * element size must be a multiple of 16 bytes.
+__device__ __forceinline__ void tma_g2s_2d_hint(uint32_t smem_dst, const void* tmap, int x, int y, uint64_t* bar,
+                                                uint64_t policy) {
     asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], "
-        "[%1, {%2, %3}], [%4];\n" ::"r"(smem_dst),
-        "l"(tmap), "r"(x), "r"(y), "r"(smem_u32(bar))
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint [%0], "
+        "[%1, {%2, %3}], [%4], %5;\n" ::"r"(smem_dst),
+        "l"(tmap), "r"(x), "r"(y), "r"(smem_u32(bar)), "l"(policy)
         : "memory");
 }
 
