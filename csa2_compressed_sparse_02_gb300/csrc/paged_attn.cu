@@ -443,9 +443,14 @@ __device__ void tma_role(Shared<kBf16, NH>& sh, const Args& a, const CUtensorMap
     Boxes cur, nxt;
     if (has) cur = boxes_of(a, it, lane);
     bool has_nx = false;
-    auto look_ahead = [&]() -> Boxes {
+    // With few bf16 tiles the requests ahead only hold up the other CTAs' first ones: pieces of
+    // 11 or 12 tiles (48 windows of 4,096, 16 heads) 45 us without, 49 with them; of 4 (8
+    // sequences of 8,192) 30 and 32; of 14 (32 of 8,192, 64 heads) 75 and 71. (E4M3, 9 tiles:
+    // 54 and 53.)
+    const bool ahead = !kBf16 || sh.range.items > 12;
+    auto look_ahead = [&](bool request) -> Boxes {
         const Boxes x = boxes_of(a, it, lane);
-        if (x.mine) bulk_prefetch_l2(a.base + (int64_t)x.y * a.g.row_bytes, box_bytes);
+        if (request && x.mine) bulk_prefetch_l2(a.base + (int64_t)x.y * a.g.row_bytes, box_bytes);
         return x;
     };
     for (int gt = 0; has && !gave_up; ++gt) {
@@ -475,16 +480,17 @@ __device__ void tma_role(Shared<kBf16, NH>& sh, const Args& a, const CUtensorMap
         // PV. The tile after the next comes into L2 meanwhile (both at the first), so that HBM
         // does not stand still too and the refill is short. What has been copied goes first
         // when L2 makes room, and copies ask for their own lines only, so that it is never what
-        // waits there. (16 sequences of 131,072, 64 heads: 361 us, the next tile alone 418,
-        // three ahead 379; without the hint 393; with it, but copies widened to 256 bytes, 414.)
+        // waits there. (16 sequences of 131,072, 64 heads, with 16 softmax warps: 361 us, three
+        // tiles ahead 379, none 418; without the hint 393; with it, but copies widened to 256
+        // bytes, 414.)
         if (gt == 0) {
             has_nx = it.next(a);
-            if (has_nx) nxt = look_ahead();
+            if (has_nx) nxt = look_ahead(true);
         }
         cur = nxt;
         has = has_nx;
         has_nx = has && it.next(a);
-        if (has_nx) nxt = look_ahead();
+        if (has_nx) nxt = look_ahead(ahead);
     }
     // whatever ended the loop, no copy of this CTA outlives it
     for (int s = max(0, g - kPairs); s < g; ++s) mbar_wait_drain(&landed[s % kPairs], (uint32_t)((s / kPairs) & 1));
