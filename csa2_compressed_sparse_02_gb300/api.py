@@ -213,10 +213,15 @@ def sparse_attn_noalloc(params, q, sink, win_ptrs, n_tokens, comp_ptrs, comp_sca
 # for a few microseconds each, so the checks are kept to what costs tenths of one.
 _FORMATS = {torch.bfloat16: BF16, torch.float32: F32}
 _raw_stream = torch._C._cuda_getCurrentRawStream  # of a device index, without a Stream object
+_current_device = torch._C._cuda_getDevice
 
 
 def _fail(what):
     raise Csa2Error(what)
+
+
+def _elsewhere(name, t, index):
+    _fail("%s is on %s, the call's other tensors on cuda:%d" % (name, t.device, index))
 
 
 def _i32(name, t, n, index):
@@ -224,13 +229,13 @@ def _i32(name, t, n, index):
     if t.dtype is not torch.int32 or t.numel() != n or not t.is_contiguous():
         _fail("%s must be a contiguous int32 tensor of %d elements" % (name, n))
     if t.get_device() != index:
-        _fail("%s is on %s, the call's other tensors on cuda:%d" % (name, t.device, index))
+        _elsewhere(name, t, index)
     return t.data_ptr()
 
 
 def _at(name, t, index):
     if t.get_device() != index:
-        _fail("%s is on %s, the call's other tensors on cuda:%d" % (name, t.device, index))
+        _elsewhere(name, t, index)
     return t.data_ptr()
 
 
@@ -246,7 +251,7 @@ def _run(name, index, stream, fn, *args):
     """fn(*args, stream) with device `index` current, on `stream` or the device's current one."""
     if index < 0:
         _fail("expected a CUDA tensor")
-    if torch.cuda.current_device() != index:
+    if _current_device() != index:
         with torch.cuda.device(index):
             return _run(name, index, stream, fn, *args)
     rc = fn(*args, _raw_stream(index) if stream is None else stream.cuda_stream)
@@ -258,23 +263,24 @@ def rope(params, x, pos, out=None, layout=ROPE_PAIRS, first=-1, inverse=False, s
     """Rotary embedding (csa2_rope): x [N, heads, channels] bf16 or fp32 with contiguous
     channels, pos [N] int32; out as x (None: a new tensor; x itself: in place).
     inverse=True turns back, which is also the gradient of the call. Returns out."""
-    dt = x.dtype
-    if x.dim() != 3 or dt not in _FORMATS:
+    dt, shape = x.dtype, x.shape
+    fmt = _FORMATS.get(dt)
+    if fmt is None or len(shape) != 3:
         _fail("rope: x must be [N, heads, channels], bf16 or fp32")
     if out is None:
         out = torch.empty_like(x, memory_format=torch.contiguous_format)
-    N, heads, ch = shape = x.shape
-    if out.shape != shape or out.dtype is not dt:
+    elif out.shape != shape or out.dtype is not dt:
         _fail("rope: out must have x's shape and type")
+    N, heads, ch = shape
     if N == 0 or heads == 0:
         return out
-    xs, os_ = x.stride(), out.stride()
-    if (xs[2] != 1 or os_[2] != 1) and ch > 1:
+    x0, x1, x2 = x.stride()
+    o0, o1, o2 = out.stride()
+    if (x2 != 1 or o2 != 1) and ch > 1:
         _fail("rope: the channels of x and out must be contiguous")
     dev = x.get_device()
-    _run("rope", dev, stream, lib().csa2_rope, params, layout, int(inverse), N, heads, ch, first,
-         _FORMATS[dt], x.data_ptr(), xs[0], xs[1], _at("out", out, dev), os_[0], os_[1],
-         _i32("pos", pos, N, dev))
+    _run("rope", dev, stream, lib().csa2_rope, params, layout, 1 if inverse else 0, N, heads, ch,
+         first, fmt, x.data_ptr(), x0, x1, _at("out", out, dev), o0, o1, _i32("pos", pos, N, dev))
     return out
 
 

@@ -10,9 +10,9 @@
 // of DRAM reads for two sequences of 65,536). Shared memory: a tile of 64 heads moves 530 KB
 // through it in bf16 (128 in, 192 for each product, P), 4.1k cycles at 128 bytes a cycle; and
 // as one tile and the query fill it (208 KB), a tile's softmax stands between its two products,
-// about 1.2k cycles in which nothing else can run. 16 sequences of 131,072 in bf16: 331 us with
-// 16 heads (6.5 TB/s, 0.96 of the measured copy rate), 390 with 64 (5.5 TB/s, 0.81; 331 with
-// every page in L2, 5.3k cycles a tile). In E4M3 with 64 heads 419 us: the bytes pass twice
+// about 1.2k cycles in which nothing else can run. 16 sequences of 131,072 in bf16: 322 us with
+// 16 heads (6.7 TB/s, 0.98 of the measured copy rate), 347 with 64 (6.2 TB/s, 0.91; 330 with
+// every page in L2, 5.3k cycles a tile). In E4M3 with 64 heads 415 us: the bytes pass twice
 // more (copied, read, written decoded: 656 KB a tile).
 //
 // Schedule, from the lengths on the device. The positions a sequence sees lie in tiles of 128
