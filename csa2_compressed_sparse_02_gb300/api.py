@@ -269,6 +269,8 @@ def rope(params, x, pos, out=None, layout=ROPE_PAIRS, first=-1, inverse=False, s
         _fail("rope: x must be [N, heads, channels], bf16 or fp32")
     if out is None:
         out = torch.empty_like(x, memory_format=torch.contiguous_format)
+        if stream is not None and x.get_device() >= 0:
+            out.record_stream(stream)
     elif out.shape != shape or out.dtype is not dt:
         _fail("rope: out must have x's shape and type")
     N, heads, ch = shape
@@ -282,6 +284,12 @@ def rope(params, x, pos, out=None, layout=ROPE_PAIRS, first=-1, inverse=False, s
     _run("rope", dev, stream, lib().csa2_rope, params, layout, 1 if inverse else 0, N, heads, ch,
          first, fmt, x.data_ptr(), x0, x1, _at("out", out, dev), o0, o1, _i32("pos", pos, N, dev))
     return out
+
+
+def _rows_of(params, cache):
+    """The pool's rows are params.kv_format (a wider one would read past its end)."""
+    if params.kv_format != cache.kv_format:
+        _fail("the cache holds rows of another format than params.kv_format")
 
 
 def page_reserve(params, cache, seq, n_from, n_to, dev_status=None, stream=None):
@@ -303,6 +311,7 @@ def page_release(params, cache, seq, n_tokens=None, window=0, n_first=0, dev_sta
 
 def page_fork(params, cache, parent, child, n_tokens, dev_status=None, stream=None):
     """child[i] continues the first n_tokens[i] positions of parent[i] (csa2_page_fork)."""
+    _rows_of(params, cache)
     N, dev = child.numel(), cache.index
     _run("page_fork", dev, stream, lib().csa2_page_fork, params, cache.c, N,
          _i32("parent", parent, N, dev), _i32("child", child, N, dev),
@@ -312,6 +321,7 @@ def page_fork(params, cache, parent, child, n_tokens, dev_status=None, stream=No
 def page_compact(params, cache, n_used=None, dev_status=None, stream=None):
     """Move the used pages to the front of the pool (csa2_page_compact); n_used [1] int32
     receives their number."""
+    _rows_of(params, cache)
     dev = cache.index
     _run("page_compact", dev, stream, lib().csa2_page_compact, params, cache.c,
          None if n_used is None else _i32("n_used", n_used, 1, dev), cache.ws_ptr, cache.ws_bytes,
@@ -324,6 +334,7 @@ def page_write(params, cache, layer, x, seq, pos, dev_status=None, stream=None):
     dt = x.dtype
     if x.dim() != 2 or x.shape[1] != D or dt not in _FORMATS or x.stride(1) != 1:
         _fail("page_write: x must be [N, %d], bf16 or fp32, with contiguous rows" % D)
+    _rows_of(params, cache)
     N, dev = x.shape[0], cache.index
     _run("page_write", dev, stream, lib().csa2_page_write, params, cache.c, layer, N,
          _at("x", x, dev), _FORMATS[dt], x.stride(0), _i32("seq", seq, N, dev),
@@ -355,6 +366,7 @@ def paged_attn(params, cache, layer, q, sink, seq, n_tokens, out, workspace, win
         _fail("paged_attn: out must be contiguous bf16 of q's shape")
     if sink is not None and (sink.dtype is not torch.float32 or sink.numel() != heads or not sink.is_contiguous()):
         _fail("paged_attn: sink must be %d contiguous fp32 values" % heads)
+    _rows_of(params, cache)
     dev = cache.index
     _run("paged_attn", dev, stream, lib().csa2_paged_attn, params, cache.c, layer, B,
          _at("q", q, dev), q.stride(0), q.stride(1), None if sink is None else _at("sink", sink, dev),
@@ -448,7 +460,8 @@ class PagedCache:
     counts, allocated here from sizes, or the caller's own tensors. pool [layers, n_pages,
     page_size, 512] of bf16 or float8_e4m3fn (params.kv_format), table [max_seqs, max_pages]
     and ref [n_pages] int32; a page of a layer is contiguous. Holds the scratch of the page
-    calls too, so calls on one cache are ordered: one stream, or events between streams."""
+    calls too, so calls on one cache are ordered: one stream, or events between streams. The
+    tensors' contents are the state; the tensors themselves stay (c holds their addresses)."""
 
     def __init__(self, params, n_pages=0, page_size=0, max_seqs=0, max_pages=0, layers=1,
                  device="cuda", pool=None, table=None, ref=None):
@@ -470,7 +483,7 @@ class PagedCache:
             _fail("PagedCache: table must be contiguous int32 [max_seqs, max_pages]")
         _i32("ref", ref, pool.shape[1], pool.get_device())
         _at("table", table, pool.get_device())
-        self.device, self.index = pool.device, pool.get_device()
+        self.device, self.index, self.kv_format = pool.device, pool.get_device(), params.kv_format
         self.pool, self.table, self.ref = pool, table, ref
         self.c = Pages(pool.data_ptr(), pool.stride(0) * pool.element_size(), table.data_ptr(),
                        ref.data_ptr(), pool.shape[0], pool.shape[1], pool.shape[2], table.shape[0],

@@ -1212,6 +1212,8 @@ extern "C" int csa2_paged_attn(const csa2_params* p, const csa2_pages* c, int la
     if (B == 0) return CSA2_OK;
     if (!seq && B > a.g.max_seqs) return fail(CSA2_ERR_INVALID_ARG, "paged_attn: B beyond max_seqs needs seq");
     if (!q || !n_tokens || !out || !workspace) return fail(CSA2_ERR_INVALID_ARG, "paged_attn: NULL buffer");
+    if (B == 1) q_seq = 0;  // strides that nothing is stepped by
+    if (p->heads == 1) q_head = 0;
     if (!aligned16(q) || !aligned16(out) || q_seq % 8 || q_head % 8)
         return fail(CSA2_ERR_ALIGN, "paged_attn: q's heads and out must be 16-byte aligned");
     if (reinterpret_cast<uintptr_t>(workspace) & 255u)
@@ -1261,10 +1263,16 @@ extern "C" int csa2_paged_attn(const csa2_params* p, const csa2_pages* c, int la
              : p->heads > 16 ? launch_attn<false, 32>(a, rows, &cfg) : launch_attn<false, 16>(a, rows, &cfg);
     }
     if (rc) return rc;
-    // A sequence is cut into about ctas / B pieces, which a narrow thread requests eight at a
-    // time. Measured (64 heads, bf16): 1 sequence of 32,768 (128 pieces) 25 us wide, 43 narrow;
-    // 2 of 131,072 (74 each) 74 and 80; 8 of 8,192 (16 each) 47 and 32.
-    const bool wide = ctas / B > 32;
+    // A sequence is cut into about ctas / B pieces, at most one a tile, which a narrow thread
+    // requests eight at a time. Measured (64 heads, bf16): 1 sequence of 32,768 (128 pieces) 25
+    // us wide, 43 narrow; 2 of 131,072 (74 each) 74 and 80; 8 of 8,192 (16 each) 47 and 32; 1 of
+    // 200 (2) 14.7 and 13.3.
+    int64_t tiles = a.g.max_len() / kTile + 1;
+    if (window > 0) {
+        const int64_t seen = window / kTile + 2 + (n_first > 0 ? n_first / kTile + 1 : 0);
+        if (seen < tiles) tiles = seen;
+    }
+    const bool wide = ctas / B > 32 && tiles > 32;
     cfg.gridDim = dim3(B, p->heads, wide ? kD / (4 * Join<true>::kLanes) : 1);
     cfg.blockDim = dim3(wide ? Join<true>::kThreads : Join<false>::kThreads);
     cfg.dynamicSmemBytes = 0;

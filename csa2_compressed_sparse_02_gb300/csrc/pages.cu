@@ -648,6 +648,7 @@ extern "C" int csa2_page_write(const csa2_params* p, const csa2_pages* c, int la
     if (N > (int64_t)INT_MAX * kWriteWarps) return fail(CSA2_ERR_UNSUPPORTED, "page_write: too many rows");
     if (N == 0) return CSA2_OK;
     if (!x || !seq || !pos) return fail(CSA2_ERR_INVALID_ARG, "page_write: NULL buffer");
+    if (N == 1) x_row = 0;  // not stepped by
     if (!aligned16(x) || x_row % (x_format == CSA2_F32 ? 4 : 8))
         return fail(CSA2_ERR_ALIGN, "page_write: rows of x must be 16-byte aligned");
     if (const int rc = ensure_loaded()) return rc;

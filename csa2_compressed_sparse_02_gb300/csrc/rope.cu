@@ -248,6 +248,8 @@ extern "C" int csa2_rope(const csa2_params* p, int layout, int inverse, int64_t 
     const uintptr_t es = format == CSA2_BF16 ? 2 : 4;
     if (reinterpret_cast<uintptr_t>(x) % es || reinterpret_cast<uintptr_t>(out) % es)
         return fail(CSA2_ERR_ALIGN, "rope: x and out must be aligned to their element");
+    if (N == 1) x_row = out_row = 0;  // strides that nothing is stepped by
+    if (heads == 1) x_head = out_head = 0;
     if ((N > 1 && out_row == 0) || (heads > 1 && out_head == 0))
         return fail(CSA2_ERR_INVALID_ARG, "rope: rows or heads of out overlap");
     if (x == out && (x_row != out_row || x_head != out_head))

@@ -783,6 +783,27 @@ def test_two_streams_with_workspaces_of_their_own():
     assert torch.equal(outs[0], alone) and torch.equal(outs[1], alone)
 
 
+def test_strides_of_single_rows_and_heads_do_not_count():
+    """A single sequence, head or row cut out of tensors with odd strides, and a side stream."""
+    p, c, q, sink = filled(api.BF16, 1, [300], 16, seed=61)
+    odd = torch.zeros(1, 1, 512, dtype=torch.bfloat16, device=DEV).as_strided((1, 1, 512), (513, 517, 1))
+    odd.copy_(q)
+    assert torch.equal(attend(p, c, odd, sink, None, [300]), attend(p, c, q, sink, None, [300]))
+    x = randn(1, D, seed=62)
+    p2, c2 = api.default_params(kv_format=api.BF16), api.PagedCache(p, 2, 16, 1, 2, device=DEV)
+    api.page_reserve(p2, c2, i32([0]), i32([0]), i32([1]))
+    api.page_write(p2, c2, 0, x.as_strided((1, D), (D + 1, 1)), i32([0]), i32([0]))
+    assert torch.equal(c2.pool[0, c2.table[0, 0].item(), 0], x[0].bfloat16())
+    p3 = api.default_params(rope_dim=64)
+    side, y = torch.cuda.Stream(), randn(1, 1, D, seed=63)
+    ref = api.rope(p3, y, i32([7]))
+    pos = i32([7])
+    side.wait_stream(torch.cuda.current_stream())
+    got = api.rope(p3, y.as_strided((1, 1, D), (D + 3, D + 1, 1)), pos, stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    assert torch.equal(got, ref)
+
+
 def test_calls_name_what_they_refuse():
     p, c, q, sink = filled(api.BF16, 8, [20], 16, seed=51)
     small = torch.empty(256, dtype=torch.uint8, device=DEV)

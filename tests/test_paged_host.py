@@ -149,6 +149,13 @@ def test_binding_refuses_tensors_the_pointers_would_not_stand_for():
     with pytest.raises(api.Csa2Error, match="BF16 or E4M3"):
         api.PagedCache(api.default_params(), pool=pool, table=table, ref=ref)
     c = api.PagedCache(p, pool=pool, table=table, ref=ref)
+    e4m3, j = params(kv_format=api.E4M3), torch.zeros(1, dtype=torch.int32)
+    for call in (lambda: api.page_fork(e4m3, c, j, j, j), lambda: api.page_compact(e4m3, c),
+                 lambda: api.page_write(e4m3, c, 0, torch.zeros(1, 512), j, j),
+                 lambda: api.paged_attn(e4m3, c, 0, torch.zeros(1, 64, 512, dtype=torch.bfloat16), None, j, j,
+                                        torch.zeros(1, 64, 512, dtype=torch.bfloat16), j)):
+        with pytest.raises(api.Csa2Error, match="another format"):
+            call()
     i = torch.zeros(2, dtype=torch.int32)
     q = torch.zeros(2, 64, 512, dtype=torch.bfloat16)
     for k in (dict(q=q.float()), dict(q=q[:, :, :256]), dict(q=q[:, :32]), dict(out=q.float()),
