@@ -56,7 +56,8 @@ constexpr int kOwners = 4096;    // sequences whose owners do
 constexpr int kFresh = 1024;     // free pages that do
 
 // Scratch (256-byte aligned): offsets of reserve [longest list + 1] int64; then int32:
-// owner [max_seqs], new pages [longest list], and three lists of n_pages. A list of sequences may be as long as there are sequences, or 1,024 with padding.
+// owner [max_seqs], new pages [longest list], and three lists of n_pages. A list of sequences
+// may be as long as there are sequences, or 1,024 with padding.
 struct Scratch {
     int64_t* offset;
     int32_t *owner, *fresh, *list, *list2, *map;

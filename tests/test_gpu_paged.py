@@ -301,7 +301,9 @@ def cache_of(kv, n_pages, ps, seqs, wide, layers=1, seed=0):
 
 @pytest.mark.parametrize("kv,n_pages,ps,seqs,wide,layers", [
     (api.BF16, 40, 8, 6, 9, 2), (api.E4M3, 5000, 16, 40, 300, 1), (api.E4M3, 4099, 8, 70, 120, 3),
-    (api.BF16, 1, 64, 1, 1, 1), (api.BF16, 9, 48, 1100, 3, 1)])
+    (api.BF16, 1, 64, 1, 1, 1), (api.BF16, 9, 48, 1100, 3, 1),
+    # more sequences, entries to fill and pages than the planning kernels keep on chip
+    (api.E4M3, 9001, 8, 5000, 2, 1), (api.E4M3, 33_333, 8, 300, 400, 1)])
 def test_page_table_calls_follow_the_model(kv, n_pages, ps, seqs, wide, layers):
     """A random run of reserve, fork, release (whole and behind a window) and compact,
     shared and exhausted pools included, compared after each call."""
@@ -313,7 +315,8 @@ def test_page_table_calls_follow_the_model(kv, n_pages, ps, seqs, wide, layers):
         some = rng.permutation(seqs)[:int(rng.integers(1, seqs + 1))]
         kind = ["reserve", "reserve", "fork", "window", "release", "compact"][step % 6]
         if kind == "reserve":
-            to = np.minimum(T[some] + rng.integers(0, 2 * ps + 1, len(some)), wide * ps)
+            more = wide * ps // 2 if wide == 400 else 2 * ps
+            to = np.minimum(T[some] + rng.integers(0, more + 1, len(some)), wide * ps)
             api.page_reserve(p, c, i32(some), i32(T[some]), i32(to), st)
             m.reserve(some, T[some], to)
             T[some] = to
