@@ -3,17 +3,20 @@
 //
 // Per tile of 128 positions, with the positions as the MMA's M (tcgen05, fp32 in TMEM):
 //   S^T[128 x heads] = K_tile[128 x 512] . Q^T,   P = 2^(S - m),   O^T[512 x heads] += V_tile^T . P^T
-// The tile is the A operand of both products, from one copy in shared memory: bf16 pages are
-// copied into the swizzled operand as they are, E4M3 pages are decoded into f16 there.
+// The tile is the A operand of both products, from one copy in shared memory, in the pages' own
+// type: bf16 MMAs, or 8-bit ones for E4M3, whose other operands come in 8-bit parts (see Shape).
 //
 // What bounds it. HBM: a position is 1,024 bytes in bf16 (512 in E4M3), read once (134.68 MB
 // of DRAM reads for two sequences of 65,536). Shared memory: a tile of 64 heads moves 530 KB
 // through it in bf16 (128 in, 192 for each product, P), 4.1k cycles at 128 bytes a cycle; and
 // as one tile and the query fill it (208 KB), a tile's softmax stands between its two products,
-// about 1.2k cycles in which nothing else can run. 16 sequences of 131,072 in bf16: 322 us with
-// 16 heads (6.7 TB/s, 0.98 of the measured copy rate), 347 with 64 (6.2 TB/s, 0.91; 330 with
-// every page in L2, 5.3k cycles a tile). In E4M3 with 64 heads 415 us: the bytes pass twice
-// more (copied, read, written decoded: 656 KB a tile).
+// about 1.2k cycles in which nothing else can run. 16 sequences of 131,072 in bf16: 324 us with
+// 16 heads (6.6 TB/s, 0.98 of the measured copy rate), 352 with 64 (6.1 TB/s, 0.90; 330 with
+// every page in L2, 5.3k cycles a tile). E4M3: 291 us with 64 heads, 213 with up to 32 (3.7 and
+// 5.0 TB/s; the rows decoded into f16 operands instead: 419 and 346). The MMAs, 64 a tile, take
+// 3.4k of its 5.0k cycles with 64 heads: two tiles fit beside the query's two parts and P's
+// three, and a place that PV frees is filled 1.5k to 2k cycles later, so the tensor cores wait
+// now for the softmax, now for the copy.
 //
 // Schedule, from the lengths on the device. The positions a sequence sees lie in tiles of 128
 // (its first tokens' tiles, then those from the window's start to its end).
@@ -146,8 +149,8 @@ __device__ __forceinline__ uint32_t warp_scan(uint32_t v, int lane) {
 // One piece per CTA leaves CTAs idle where the sequences do not divide well; equal ranges do
 // not, but give most CTAs a second piece, whose query, first tile and partial result cost about
 // a tile. Measured on 152 CTAs, pieces (tiles of the longest) against ranges: 100 sequences of
-// 3 tiles 26 us (3) and 33 (2); 20 of 18 on average 28 (3) and 31 (3); 32 of 64 in E4M3 79 (16)
-// and 72 (14); 100 of 63 205 (63) and 173 (42).
+// 3 tiles 26 us (3) and 33 (2); 20 of 18 on average 28 (3) and 31 (3); 32 of 64 in E4M3 63 (16)
+// and 62 (14); 100 of 63 205 (63) and 173 (42).
 constexpr uint32_t kSecondPiece = 1;
 
 // At most as many sequences as CTAs (and kPlanSeqs: one a thread). False, with nothing
@@ -272,61 +275,78 @@ __device__ __forceinline__ float ex2(float x) {
 }
 
 // ---------------------------------------------------------------- shapes
-// kBf16: bf16 pages, the products in bf16; else E4M3 pages, decoded (exactly) into f16.
-// NH: the heads, rounded up to the 16, 32 or 64 columns of the MMAs.
+// kBf16: bf16 pages, the products in bf16. Else E4M3 pages, whose bytes are the operand as they
+// are; what meets them is split into 8-bit parts that add up to it:
+//   q 2^s = hi + 2^-5 lo, both E4M3, as 2 NH columns of S (they hold bf16's 8 bits);
+//   P in f16 = three parts in E5M2, one product each into the same O. Each part takes the
+//   nearest three bits of what is left: of a value in [1, 2) that is 2^-3, 2^-7, then nothing.
+// NH: the heads, rounded up to the columns of the MMAs (bf16 16, 32 or 64, E4M3 32 or 64).
 template <bool kBf16, int NH>
 struct Shape {
-    static constexpr int kSoftWarps = 8;            // (16 of them: 361 us for the 64-head case above, 8: 347)
+    static constexpr int kSoftWarps = 8;            // (16 of them: 361 us for the 64-head case above in bf16, 8: 347)
     static constexpr int kGroups = kSoftWarps / 4;  // of heads: one per four lane quarters
     static constexpr int NC = NH / kGroups;         // heads of a softmax warp
     static constexpr int kMmaWarp = kSoftWarps;
     static constexpr int kTmaWarp = kSoftWarps + 1;
-    static constexpr int kHelp0 = kSoftWarps + 2;       // first of the warps that stage the query
-    static constexpr int kHelpWarps = kBf16 ? 4 : 8;    // and, for E4M3, decode the rows
+    static constexpr int kHelp0 = kSoftWarps + 2;   // first of the warps that stage the query
+    static constexpr int kHelpWarps = kBf16 ? 4 : 6;
     static constexpr int kThreads = 32 * (kHelp0 + kHelpWarps);
-    // Pairs of 64-channel chunks of a tile in the ring: a tile has 4; what the query leaves
-    // of shared memory lets the next tile's first pairs arrive early.
-    static constexpr int kPairs = NH == 64 ? 4 : NH == 32 ? 5 : 6;
-    static constexpr uint32_t kColS = 4 * NH;  // TMEM: O^T 4 x NH columns, then S^T
-    static constexpr uint32_t kFmt = kBf16 ? 1u : 0u;
-    // D fp32, A and B bf16 or f16, N = NH, M = 128; S: both K-major, PV: both MN-major
-    static constexpr uint32_t kIdescS =
-        (1u << 4) | (kFmt << 7) | (kFmt << 10) | ((uint32_t)(NH >> 3) << 17) | ((128u >> 4) << 24);
-    static constexpr uint32_t kIdescPV = kIdescS | (1u << 15) | (1u << 16);
+    // The ring's places hold 128 channels of a tile's positions each, so a tile has 4: what the
+    // query and P leave of shared memory. bf16: a tile and the next one's first places. E4M3: two
+    // tiles (64 heads) or two and a half.
+    static constexpr int kPairs = kBf16 ? (NH == 64 ? 4 : NH == 32 ? 5 : 6) : NH == 64 ? 8 : 10;
+    static constexpr int kChunks = kBf16 ? 2 : 1;   // of 128 bytes a row in a place
+    static constexpr int kQRows = kBf16 ? NH : 2 * NH;
+    static constexpr int kQChunks = kBf16 ? 8 : 4;
+    static constexpr int kParts = kBf16 ? 1 : 3;    // of P
+    static constexpr uint32_t kColS = 4 * NH;  // TMEM: O^T 4 x NH columns, then S^T (E4M3: two of them)
+    // D fp32, N = NH (S of E4M3: its two parts), M = 128; S: both K-major, PV: both MN-major.
+    // Types: bf16 1, E4M3 0, E5M2 1 (a kind of MMA each)
+    static constexpr uint32_t kIdesc = (1u << 4) | ((128u >> 4) << 24);
+    static constexpr uint32_t kIdescS = kIdesc | ((uint32_t)(kQRows >> 3) << 17) | (kBf16 ? (1u << 7) | (1u << 10) : 0u);
+    static constexpr uint32_t kIdescPV =
+        kIdesc | ((uint32_t)(NH >> 3) << 17) | (kBf16 ? 1u << 7 : 0u) | (1u << 10) | (1u << 15) | (1u << 16);
     // P: a row of NH heads per position, swizzled over its own width (128, 64 or 32 bytes)
-    static constexpr uint32_t kPRow = 2 * NH;
-    static constexpr uint32_t kPLayout = NH == 64 ? kLayoutSw128 : NH == 32 ? kLayoutSw64 : kLayoutSw32;
+    static constexpr uint32_t kPRow = (kBf16 ? 2 : 1) * NH;
+    static constexpr uint32_t kPLayout = kPRow == 128 ? kLayoutSw128 : kPRow == 64 ? kLayoutSw64 : kLayoutSw32;
     __device__ static __forceinline__ uint32_t p_unit(int row, int unit) {  // byte of 16-byte unit `unit`
-        const int x = NH == 64 ? row & 7 : NH == 32 ? (row >> 1) & 3 : (row >> 2) & 1;
+        const int x = kPRow == 128 ? row & 7 : kPRow == 64 ? (row >> 1) & 3 : (row >> 2) & 1;
         return row * kPRow + ((unit ^ x) << 4);
     }
+    // P = 2^(x - m + kLift), x - m <= kLazyMax before the maximum has to move. E5M2 ends at
+    // 1.75 x 2^15 and holds small values as multiples of 2^-16, half a step off at most: with
+    // the largest weight at 2^9 or more, 2^-26 of it. (A kLazyMax of 3 would make that 2^-29, but
+    // logits of a standard deviation of 3 in log2 then move the maximum in 4 of the first 8 tiles,
+    // with 6 in 2.)
+    static constexpr float kLazyMax = kBf16 ? 8.0f : 6.0f;
+    static constexpr float kLift = kBf16 ? 0.f : 9.f;
 };
 
-constexpr uint32_t kChunk = 128 * 128;  // 128 positions x 64 channels of 16 bits, 128-byte swizzle
+constexpr uint32_t kChunk = 128 * 128;  // 128 positions x 128 bytes, 128-byte swizzle
 constexpr uint32_t kTmemCols = 512;     // one CTA an SM (shared memory), so it takes them all
-constexpr float kLazyMax = 8.0f;        // log2 of the largest P before the maximum moves
-// P = 2^(x - m + kLift): f16 holds small P as multiples of 2^-24, so they are lifted as far
-// as its range allows (8 + 7 < 16), which puts that step at 2^-31 of the largest weight.
-template <bool kBf16>
-constexpr float kLift = kBf16 ? 0.f : 7.f;
 
 template <bool kBf16, int NH>
 struct Shared {
     using S = Shape<kBf16, NH>;
-    uint8_t kv[S::kPairs][2][kChunk];  // A operand of both products
-    uint8_t q[8][NH * 128];            // B operand of S: heads x 64 channels a chunk, K-major
-    uint8_t p[kTile * 2 * NH];         // B operand of PV: positions x heads, MN-major
+    uint8_t kv[S::kPairs][S::kChunks][kChunk];        // A operand of both products
+    uint8_t q[S::kQChunks][S::kQRows * 128];          // B operand of S: heads x 128 bytes of channels a chunk, K-major
+    uint8_t p[S::kParts][kTile * S::kPRow];           // B operand of PV: positions x heads, MN-major
     float col_scale[2][kMaxHeads];     // E4M3: per-head logit factor, by piece parity
     float red_max[4][kMaxHeads];
     float m_sub[4][kMaxHeads];         // per lane quarter: what its logits are reduced by
-    int moved[4];                      // per head group: the last tile whose maximum had to move
+    alignas(8) int moved[2];           // per head group: the last tile whose maximum had to move
     float red_sum[4][kMaxHeads];
-    uint8_t row_ok[2][kTile];          // by tile parity: the row holds a position that is seen
+    // by tile mod 4: the row holds a position that is seen. (The ring holds less than three
+    // tiles, and a place comes free after PV, so tile gt + 4 begins after the softmax of gt.)
+    uint8_t row_ok[4][kTile];
     // q_full: two barriers, so that a producer can publish the next piece's query before a
     // softmax warp has waited on this one (a one-tile piece needs no softmax before its S ends)
-    uint64_t q_full[2], q_empty, s_full, p_full, o_full, drain;
+    uint64_t q_full[2], q_empty, p_full, o_full, drain;
+    // bf16 the first; E4M3 by tile parity, as S of tile gt + 1 may end before a warp has waited
+    // on that of gt
+    uint64_t s_full[2];
+    uint64_t pv_done;                  // E4M3: P may be written again, and O rescaled
     uint64_t full[S::kPairs], empty[S::kPairs];
-    uint64_t raw_full[S::kPairs];      // E4M3: the bytes have landed, full: they are decoded
     uint64_t p_again, max_bar[S::kGroups], sum_bar[S::kGroups];
     Range range;
     uint32_t tmem_base;
@@ -430,11 +450,8 @@ __device__ __forceinline__ Boxes boxes_of(const Args& a, const Tiles& t, int lan
 template <bool kBf16, int NH>
 __device__ void tma_role(Shared<kBf16, NH>& sh, const Args& a, const CUtensorMap* tmap, int lane, volatile int* abort) {
     constexpr int kPairs = Shape<kBf16, NH>::kPairs;
-    // bf16: two boxes of 64 channels, in the operand's place; E4M3: one of 128, its bytes in
-    // the place of the pair's second chunk
-    constexpr uint32_t kRowBytes = kBf16 ? 256 : 128;
-    uint64_t* const landed = kBf16 ? sh.full : sh.raw_full;
-    const uint32_t dst0 = smem_u32(sh.kv[0][kBf16 ? 0 : 1]) + lane * a.box_rows * 128;
+    constexpr int kChunks = Shape<kBf16, NH>::kChunks;  // boxes of 128 bytes a row: 64 channels in bf16
+    const uint32_t dst0 = smem_u32(sh.kv[0][0]) + lane * a.box_rows * 128;
     const int box_bytes = a.box_rows * a.g.row_bytes;
     const uint64_t once = l2_policy_evict_first();
     Tiles it(sh.range);
@@ -443,18 +460,18 @@ __device__ void tma_role(Shared<kBf16, NH>& sh, const Args& a, const CUtensorMap
     Boxes cur, nxt;
     if (has) cur = boxes_of(a, it, lane);
     bool has_nx = false;
-    // With few bf16 tiles the requests ahead only hold up the other CTAs' first ones: pieces of
-    // 11 or 12 tiles (48 windows of 4,096, 16 heads) 45 us without, 49 with them; of 4 (8
-    // sequences of 8,192) 30 and 32; of 14 (32 of 8,192, 64 heads) 75 and 71. (E4M3, 9 tiles:
-    // 54 and 53.)
-    const bool ahead = !kBf16 || sh.range.items > 12;
+    // With few tiles the requests ahead only hold up the other CTAs' first ones: pieces of 11 or
+    // 12 tiles (48 windows of 4,096, 16 heads) 45 us without, 49 with them; of 4 (8 sequences of
+    // 8,192) 30 and 32; of 14 (32 of 8,192, 64 heads) 75 and 71. E4M3: of 4 tiles 31 and 33, of 9
+    // (32 ragged sequences) 46 and 47, of 108 with 32 heads 252 and 213.
+    const bool ahead = sh.range.items > 12;
     auto look_ahead = [&](bool request) -> Boxes {
         const Boxes x = boxes_of(a, it, lane);
         if (request && x.mine) bulk_prefetch_l2(a.base + (int64_t)x.y * a.g.row_bytes, box_bytes);
         return x;
     };
     for (int gt = 0; has && !gave_up; ++gt) {
-        const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, cur.mine)) * a.box_rows * kRowBytes;
+        const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, cur.mine)) * a.box_rows * 128 * kChunks;
         for (int pr = 0; pr < 4; ++pr, ++g) {
             const int slot = g % kPairs;
             if (g >= kPairs && !mbar_wait(&sh.empty[slot], (uint32_t)((g / kPairs - 1) & 1), abort)) gave_up = true;
@@ -464,16 +481,16 @@ __device__ void tma_role(Shared<kBf16, NH>& sh, const Args& a, const CUtensorMap
             }
             if (pr == 0) {  // four rows a lane: their bits to bytes
                 const uint32_t w = lane < 16 ? (lane < 8 ? cur.rows[0] : cur.rows[1]) : lane < 24 ? cur.rows[2] : cur.rows[3];
-                *reinterpret_cast<uint32_t*>(&sh.row_ok[gt & 1][4 * lane]) =
+                *reinterpret_cast<uint32_t*>(&sh.row_ok[gt & 3][4 * lane]) =
                     (((w >> (4 * (lane & 7))) & 15u) * 0x00204081u) & 0x01010101u;
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive_expect_tx(&landed[slot], bytes);
+            if (lane == 0) mbar_arrive_expect_tx(&sh.full[slot], bytes);
             __syncwarp();
             if (cur.mine) {
-                const uint32_t dst = dst0 + 2 * slot * kChunk;
-                tma_g2s_2d_hint(dst, tmap, 128 * pr, cur.y, &landed[slot], once);
-                if constexpr (kBf16) tma_g2s_2d_hint(dst + kChunk, tmap, 128 * pr + 64, cur.y, &landed[slot], once);
+                const uint32_t dst = dst0 + kChunks * slot * kChunk;
+                tma_g2s_2d_hint(dst, tmap, 128 * pr, cur.y, &sh.full[slot], once);
+                if constexpr (kBf16) tma_g2s_2d_hint(dst + kChunk, tmap, 128 * pr + 64, cur.y, &sh.full[slot], once);
             }
         }
         // The ring holds little more than a tile and stands still between a tile's S and its
@@ -493,7 +510,7 @@ __device__ void tma_role(Shared<kBf16, NH>& sh, const Args& a, const CUtensorMap
         if (has_nx) nxt = look_ahead(ahead);
     }
     // whatever ended the loop, no copy of this CTA outlives it
-    for (int s = max(0, g - kPairs); s < g; ++s) mbar_wait_drain(&landed[s % kPairs], (uint32_t)((s / kPairs) & 1));
+    for (int s = max(0, g - kPairs); s < g; ++s) mbar_wait_drain(&sh.full[s % kPairs], (uint32_t)((s / kPairs) & 1));
 }
 
 template <int NH>
@@ -518,53 +535,44 @@ __device__ void query_role(Shared<true, NH>& sh, const Args& a, int pt, int lane
     }
 }
 
-// ---------------------------------------------------------------- E4M3 producers
-__device__ __forceinline__ void e4m3x4_to_h2x2(uint32_t w, uint32_t* o) {
-    asm("{\n .reg .b16 lo, hi;\n mov.b32 {lo, hi}, %2;\n"
-        " cvt.rn.f16x2.e4m3x2 %0, lo;\n cvt.rn.f16x2.e4m3x2 %1, hi;\n}"
-        : "=r"(o[0]), "=r"(o[1])
-        : "r"(w));
+// E4M3: a warp takes a head, a lane 16 of its channels. The head's values times 2^s, with the
+// largest |q| in [2^7, 2^8): hi holds 4 bits, what is left is at most 2^-5 of 2^8 and lo = 2^5
+// times it holds the other 4, exactly down to 2^-14 of the largest, to 2^-22 of it below. The
+// factor goes into the logit scale. E4M3 has no infinity: one in the query becomes NaN.
+__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;\n" : "=h"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ float2 e4m3x2_to_float2(uint32_t v) {
+    uint32_t h;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;\n" : "=r"(h) : "h"((uint16_t)v));
+    return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
 
-__device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
-    const __half2 h = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&h);
-}
-
-// Two groups of four warps take the pairs in turn (a pair is one chain of waits, loads, stores
-// and a fence, so two run side by side), a warp 32 rows. A place in the ring always has the
-// same group: one that skipped a phase of the place's barrier could take the phase before for
-// the one it waits for. The 128 bytes of a row that
-// become a pair of chunks lie where its 128 bytes of the second chunk will be: a warp reads its
-// rows, then writes both chunks over them, so the raw bytes take no room of their own.
 template <int NH>
-__device__ void decode_role(Shared<false, NH>& sh, const Args& a, int pt, int lane, volatile int* abort) {
-    constexpr int kPairs = Shape<false, NH>::kPairs;
-    const int pw = pt >> 5, sub = lane >> 3, un = lane & 7;  // lane: unit un of rows 4 k + sub
-    const int row0 = 32 * (pw & 3), group = pw >> 2;
+__device__ void query_role(Shared<false, NH>& sh, const Args& a, int pt, int lane, volatile int* abort) {
+    constexpr int kWarps = Shape<false, NH>::kHelpWarps, kAtOnce = 4;  // heads whose loads are in flight together
+    const int pw = pt >> 5;
     Pieces pi(sh.range);
-    int gt = 0, slot = 0;
-    uint32_t phase = 0;
-    for (int it = 0;; ++it) {
-        Piece pc;
-        if (!pi.next(a, pc)) break;
-        // ---- query: warp pw stages heads pw, pw + 8, ...; lane = channels 16 lane .. + 15
+    Piece pc;
+    for (int it = 0; pi.next(a, pc); ++it) {
         if (it > 0 && !mbar_wait(&sh.q_empty, (uint32_t)((it - 1) & 1), abort)) return;
         __syncwarp();
-        constexpr int kAtOnce = NH / 8 < 4 ? NH / 8 : 4;  // heads whose loads are in flight together
 #pragma unroll 1
-        for (int h1 = pw; h1 < NH; h1 += 8 * kAtOnce) {
+        for (int h1 = pw; h1 < NH; h1 += kWarps * kAtOnce) {
             uint4 w2[kAtOnce][2];
 #pragma unroll
             for (int i = 0; i < kAtOnce; ++i) {
-                const int h = h1 + 8 * i;
+                const int h = h1 + kWarps * i;
                 const uint4* src = reinterpret_cast<const uint4*>(a.q + pc.b * a.q_seq + h * a.q_head) + 2 * lane;
                 w2[i][0] = w2[i][1] = make_uint4(0u, 0u, 0u, 0u);
                 if (h < a.heads) w2[i][0] = __ldg(src), w2[i][1] = __ldg(src + 1);
             }
 #pragma unroll
             for (int i = 0; i < kAtOnce; ++i) {
-                const int h = h1 + 8 * i;
+                const int h = h1 + kWarps * i;
+                if (h >= NH) break;
                 const uint32_t w[8] = {w2[i][0].x, w2[i][0].y, w2[i][0].z, w2[i][0].w,
                                        w2[i][1].x, w2[i][1].y, w2[i][1].z, w2[i][1].w};
                 float mx = 0.f;
@@ -572,72 +580,38 @@ __device__ void decode_role(Shared<false, NH>& sh, const Args& a, int pt, int la
                 for (int k = 0; k < 8; ++k)
                     mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(w[k] << 16)), fabsf(__uint_as_float(w[k] & 0xffff0000u))));
                 mx = warp_max(mx);
-                // times 2^s with the head's largest |q| in [2^14, 2^15): f16 then keeps bf16's 8
-                // bits of everything above 2^-24 of it; the factor goes into the logit scale
-                int s = 14 - ((int)((__float_as_uint(mx) >> 23) & 0xffu) - 127);
+                int s = 7 - ((int)((__float_as_uint(mx) >> 23) & 0xffu) - 127);
                 s = max(-126, min(126, s));
                 const float two_s = __uint_as_float((uint32_t)(s + 127) << 23);
-                uint32_t hq[8];
+                uint32_t hi[4] = {}, lo[4] = {};
 #pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    hq[k] = pack_h2(__uint_as_float(w[k] << 16) * two_s, __uint_as_float(w[k] & 0xffff0000u) * two_s);
-                uint8_t* row = sh.q[lane >> 2];
-                const int u0 = (lane & 3) * 2;
-                *reinterpret_cast<uint4*>(row + sw128(h, u0)) = make_uint4(hq[0], hq[1], hq[2], hq[3]);
-                *reinterpret_cast<uint4*>(row + sw128(h, u0 + 1)) = make_uint4(hq[4], hq[5], hq[6], hq[7]);
+                for (int k = 0; k < 8; ++k) {
+                    float x = __uint_as_float(w[k] << 16) * two_s, y = __uint_as_float(w[k] & 0xffff0000u) * two_s;
+                    x = fmaf(x, 0.f, x);  // infinity to NaN
+                    y = fmaf(y, 0.f, y);
+                    const uint32_t xy = e4m3x2(x, y);
+                    const float2 got = e4m3x2_to_float2(xy);
+                    hi[k >> 1] |= xy << (16 * (k & 1));
+                    lo[k >> 1] |= e4m3x2(32.f * (x - got.x), 32.f * (y - got.y)) << (16 * (k & 1));
+                }
+                uint8_t* q = sh.q[lane >> 3];
+                *reinterpret_cast<uint4*>(q + sw128(h, lane & 7)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                *reinterpret_cast<uint4*>(q + sw128(NH + h, lane & 7)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                 if (lane == 0) sh.col_scale[it & 1][h] = a.scale_log2 * __uint_as_float((uint32_t)(127 - s) << 23);
             }
         }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.q_full[it & 1]);
-        for (int n = pc.j1 - pc.j0; n > 0; --n, ++gt) {
-#pragma unroll 1
-            for (int pr = 0; pr < 4; ++pr) {
-                if ((slot & 1) == group) {
-                    if (!mbar_wait(&sh.raw_full[slot], phase, abort)) return;
-                    uint8_t* rows = sh.kv[slot][1] + row0 * 128;
-                    const uint8_t* ok = &sh.row_ok[gt & 1][row0 + sub];
-                    uint4 raw[8];
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) {  // a row that is not seen becomes zeros, whatever is there
-                        raw[k] = *reinterpret_cast<const uint4*>(rows + (4 * k + sub) * 128 + 16 * un);
-                        if (!ok[4 * k]) raw[k] = make_uint4(0u, 0u, 0u, 0u);
-                    }
-                    __syncwarp();  // every lane has its bytes: they may be overwritten
-                    uint8_t* dst = sh.kv[slot][un >> 2];
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        uint32_t o[8];
-                        e4m3x4_to_h2x2(raw[k].x, &o[0]);
-                        e4m3x4_to_h2x2(raw[k].y, &o[2]);
-                        e4m3x4_to_h2x2(raw[k].z, &o[4]);
-                        e4m3x4_to_h2x2(raw[k].w, &o[6]);
-                        // the second chunk's lanes store their odd unit first: a row's eight lanes
-                        // then hit all banks
-                        const int r = row0 + 4 * k + sub, u0 = 2 * (un & 3), odd = un >> 2;
-                        const uint4 lo = make_uint4(o[0], o[1], o[2], o[3]), hi = make_uint4(o[4], o[5], o[6], o[7]);
-                        *reinterpret_cast<uint4*>(dst + sw128(r, u0 + odd)) = odd ? hi : lo;
-                        *reinterpret_cast<uint4*>(dst + sw128(r, u0 + 1 - odd)) = odd ? lo : hi;
-                    }
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&sh.full[slot]);
-                }
-                if (++slot == kPairs) slot = 0, phase ^= 1u;
-            }
-        }
     }
 }
 
 // Whether a head group's maximum moved at tile gt (read after p_full of that tile).
 template <bool kBf16, int NH>
 __device__ __forceinline__ bool any_moved(Shared<kBf16, NH>& sh, int gt) {
-    const volatile int* m = sh.moved;
-    bool any = m[0] == gt;
-#pragma unroll
-    for (int i = 1; i < Shape<kBf16, NH>::kGroups; ++i) any |= m[i] == gt;
-    return any;
+    static_assert(Shape<kBf16, NH>::kGroups == 2, "a mark each");
+    const long long m = *reinterpret_cast<const volatile long long*>(sh.moved);
+    return (int)m == gt || (int)(m >> 32) == gt;
 }
 
 // ---------------------------------------------------------------- MMA issuer
@@ -647,13 +621,13 @@ __device__ __forceinline__ bool any_moved(Shared<kBf16, NH>& sh, int gt) {
 // the one before by 75 to 80 cycles, so by 61 to 64. (Alone, M = 128 MMAs from shared memory
 // follow by 40 cycles at N = 16 and 49 at N = 64; here the copies of the next rows share
 // shared memory with them.)
-template <bool kBf16, int NH>
-__device__ void mma_role(Shared<kBf16, NH>& sh, const Args& a, uint32_t tmem, volatile int* abort) {
-    using S = Shape<kBf16, NH>;
+template <int NH>
+__device__ void mma_role(Shared<true, NH>& sh, const Args& a, uint32_t tmem, int, volatile int* abort) {
+    using S = Shape<true, NH>;
     const uint64_t dK = smem_desc(smem_u32(sh.kv[0][0]), 16, 1024, kLayoutSw128);
     const uint64_t dQ = smem_desc(smem_u32(sh.q[0]), 16, 1024, kLayoutSw128);
     const uint64_t dV = smem_desc(smem_u32(sh.kv[0][0]), kChunk, 1024, kLayoutSw128);
-    const uint64_t dP = smem_desc(smem_u32(sh.p), 1024, 8 * S::kPRow, S::kPLayout);
+    const uint64_t dP = smem_desc(smem_u32(sh.p[0]), 1024, 8 * S::kPRow, S::kPLayout);
     Pieces pi(sh.range);
     Piece pc;
     int gt = 0, again = 0;  // tiles so far, those whose P came twice
@@ -683,7 +657,7 @@ __device__ void mma_role(Shared<kBf16, NH>& sh, const Args& a, uint32_t tmem, vo
                 if (++slot == S::kPairs) slot = 0, phase ^= 1u;
             }
             if (elect_one()) {
-                tc_commit(&sh.s_full);
+                tc_commit(&sh.s_full[0]);
                 if (j == pc.j1 - 1) tc_commit(&sh.q_empty);
             }
             __syncwarp();
@@ -711,6 +685,97 @@ __device__ void mma_role(Shared<kBf16, NH>& sh, const Args& a, uint32_t tmem, vo
         }
         if (elect_one()) tc_commit(&sh.o_full);
         __syncwarp();
+    }
+}
+
+// E4M3: S of the next tile may come before PV of this one (within a piece: the next one's query
+// comes after this one's last S), so that the tensor cores have it to do while the softmax runs.
+// S of gt + 1 takes the columns of gt - 1, whose softmax has ended: PV of gt - 1 came after its P.
+// Where the ring holds two tiles only, the next one's last rows land when PV of the tile before
+// has long ended, and this one's P is often ready first: whichever is, goes first (64 heads, 16 x
+// 131,072: 291 us, S always first 314). With half a tile more S always first is better (214, 221).
+// The MMAs are short (28 to 65 cycles), so what stands between them counts: a product's are issued
+// in one go, after one look at all the barriers it needs (32 heads: 214 us, place by place 245).
+// The three MMAs of P's parts share V in the tensor core's collector (114 cycles, 149 without).
+template <int NH>
+__device__ void mma_role(Shared<false, NH>& sh, const Args& a, uint32_t tmem, int lane, volatile int* abort) {
+    using S = Shape<false, NH>;
+    const uint64_t dK = smem_desc(smem_u32(sh.kv[0][0]), 16, 1024, kLayoutSw128);
+    const uint64_t dQ = smem_desc(smem_u32(sh.q[0]), 16, 1024, kLayoutSw128);
+    const uint64_t dV = smem_desc(smem_u32(sh.kv[0][0]), kChunk, 1024, kLayoutSw128);
+    const uint64_t dP = smem_desc(smem_u32(sh.p[0]), 1024, 8 * S::kPRow, S::kPLayout);
+    Pieces pi(sh.range);
+    Piece pc;
+    int gt = 0, again = 0;  // tiles whose PV has been issued, those whose P came twice
+    int slot = 0, pv_slot = 0;  // first place of the next S and PV
+    uint32_t phase = 0;
+    // a descriptor's step to place i of a tile that begins at place `from`
+    auto place = [&](int from, int i) {
+        const int x = from + i < S::kPairs ? from + i : from + i - S::kPairs;
+        return (uint64_t)__shfl_sync(0xffffffffu, (uint32_t)x * (kChunk >> 4), 0);
+    };
+    // the barrier, and its phase, of the next S's place that this lane looks at
+    auto landing = [&] { return &sh.full[slot + (lane & 3) < S::kPairs ? slot + (lane & 3) : slot + (lane & 3) - S::kPairs]; };
+    auto landing_phase = [&] { return phase ^ (uint32_t)(slot + (lane & 3) >= S::kPairs); };
+    auto scores = [&](int tile, bool last) {
+        const uint32_t at = tmem + S::kColS + (uint32_t)__shfl_sync(0xffffffffu, tile & 1, 0) * S::kQRows;
+        const uint64_t k[4] = {dK + place(slot, 0), dK + place(slot, 1), dK + place(slot, 2), dK + place(slot, 3)};
+        if (!mbar_wait_warp(landing(), landing_phase(), abort)) return false;
+        tc_fence_after();
+        if (elect_one()) {
+#pragma unroll
+            for (int pr = 0; pr < 4; ++pr)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    mma_f8(at, k[pr] + ((32 * i) >> 4), dQ + ((pr * S::kQRows * 128 + 32 * i) >> 4), S::kIdescS, (pr | i) != 0);
+            tc_commit(&sh.s_full[tile & 1]);
+            if (last) tc_commit(&sh.q_empty);
+        }
+        __syncwarp();
+        if ((slot += 4) >= S::kPairs) slot -= S::kPairs, phase ^= 1u;
+        return true;
+    };
+    for (int it = 0; pi.next(a, pc); ++it) {
+        if (!mbar_wait_warp(&sh.q_full[it & 1], (uint32_t)((it >> 1) & 1), abort)) return;
+        tc_fence_after();
+        bool ahead = false;  // S of this tile has been issued
+        for (int j = pc.j0; j < pc.j1; ++j, ++gt) {
+            if (!ahead && !scores(gt, j + 1 == pc.j1)) return;
+            ahead = false;
+            const uint64_t v[4] = {dV + place(pv_slot, 0), dV + place(pv_slot, 1), dV + place(pv_slot, 2), dV + place(pv_slot, 3)};
+            const uint32_t more = __shfl_sync(0xffffffffu, j != pc.j0 ? 1u : 0u, 0);
+            if (j + 1 < pc.j1 && S::kPairs > 8) {
+                ahead = true;
+                if (!scores(gt + 1, j + 2 == pc.j1)) return;
+            } else if (j + 1 < pc.j1) {
+                const int first = mbar_wait_either_warp(lane < 4 ? landing() : &sh.p_full,
+                                                        lane < 4 ? landing_phase() : (uint32_t)(gt & 1), lane, 4, abort);
+                if (!first) return;
+                ahead = first == 1;
+                if (ahead && !scores(gt + 1, j + 2 == pc.j1)) return;
+            }
+            if ((ahead || j + 1 == pc.j1) && !mbar_wait_warp(&sh.p_full, (uint32_t)(gt & 1), abort)) return;
+            if (any_moved(sh, gt) && !mbar_wait_warp(&sh.p_again, (uint32_t)(again++ & 1), abort)) return;
+            tc_fence_after();
+            if (elect_one()) {
+#pragma unroll
+                for (int mb = 0; mb < 4; ++mb) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {  // 32 positions and the three parts of their P
+                        const uint64_t vi = v[mb] + ((i * 32 * 128) >> 4), wi = dP + ((i * 32 * S::kPRow) >> 4);
+                        constexpr uint32_t kPart = (kTile * S::kPRow) >> 4;
+                        mma_f8<Collector::kFill>(tmem + NH * mb, vi, wi, S::kIdescPV, i == 0 ? more : 1u);
+                        mma_f8<Collector::kUse>(tmem + NH * mb, vi, wi + kPart, S::kIdescPV, 1u);
+                        mma_f8<Collector::kLast>(tmem + NH * mb, vi, wi + 2 * kPart, S::kIdescPV, 1u);
+                    }
+                    tc_commit(&sh.empty[pv_slot + mb < S::kPairs ? pv_slot + mb : pv_slot + mb - S::kPairs]);
+                }
+                tc_commit(&sh.pv_done);
+                if (j + 1 == pc.j1) tc_commit(&sh.o_full);
+            }
+            __syncwarp();
+            if ((pv_slot += 4) >= S::kPairs) pv_slot -= S::kPairs;
+        }
     }
 }
 
@@ -746,6 +811,19 @@ __device__ __forceinline__ float warp_sum(float* v, int lane) {
     return s;
 }
 
+__device__ __forceinline__ uint32_t h2_sub(uint32_t x, uint32_t y) {
+    const __half2 d = __hsub2(*reinterpret_cast<const __half2*>(&x), *reinterpret_cast<const __half2*>(&y));
+    return *reinterpret_cast<const uint32_t*>(&d);
+}
+__device__ __forceinline__ uint32_t h2x2_to_e5m2x4(uint32_t x, uint32_t y) {
+    uint32_t r;
+    asm("{\n .reg .b16 lo, hi;\n cvt.rn.satfinite.e5m2x2.f16x2 lo, %1;\n cvt.rn.satfinite.e5m2x2.f16x2 hi, %2;\n"
+        " mov.b32 %0, {lo, hi};\n}"
+        : "=r"(r)
+        : "r"(x), "r"(y));
+    return r;
+}
+
 // Warp (qd, cg): positions 32 qd + lane of the tile, heads cg NC .. + NC - 1. Logits are in
 // the log2 domain.
 //
@@ -767,45 +845,85 @@ __device__ void softmax_role(Shared<kBf16, NH>& sh, const Args& a, uint32_t tmem
     const uint32_t tl = tmem + ((uint32_t)(32 * qd) << 16);
     const float sink2 = a.sink && h0 + mine < a.heads ? a.sink[h0 + mine] * kLog2e : -INFINITY;
     float* const m_sub = &sh.m_sub[qd][h0];
-    // x[i] = logit i of this row less `sub` (NULL: nothing), -infinity where nothing is seen
-    auto logits = [&](float* x, const float* sub, int it, bool ok) {
+    // x[i] = logit i of this row (`less`: what m_sub holds), -infinity where nothing is seen
+    auto logits = [&](float* x, bool less, int it, int gt, bool ok) {
         uint32_t sv[NC];
-        tmem_ld<NC>(tl + S::kColS + h0, sv);
+        if constexpr (kBf16) {
+            tmem_ld<NC>(tl + S::kColS + h0, sv);
+        } else {
+            const uint32_t at = tl + S::kColS + (gt & 1) * S::kQRows + h0;
+            uint32_t lo[NC];
+            tmem_ld<NC>(at, sv);
+            tmem_ld<NC>(at + NH, lo);
+#pragma unroll
+            for (int i = 0; i < NC; ++i)
+                sv[i] = __float_as_uint(fmaf(__uint_as_float(lo[i]), 0.03125f, __uint_as_float(sv[i])));
+        }
 #pragma unroll
         for (int i = 0; i < NC; i += 4) {
             float4 c = make_float4(a.scale_log2, a.scale_log2, a.scale_log2, a.scale_log2);
             if constexpr (!kBf16) c = *reinterpret_cast<const float4*>(&sh.col_scale[it & 1][h0 + i]);
-            const float4 m = sub ? *reinterpret_cast<const float4*>(sub + i) : make_float4(0.f, 0.f, 0.f, 0.f);
+            const float4 m = less ? *reinterpret_cast<const float4*>(m_sub + i) : make_float4(0.f, 0.f, 0.f, 0.f);
             x[i] = ok ? fmaf(__uint_as_float(sv[i]), c.x, -m.x) : -INFINITY;
             x[i + 1] = ok ? fmaf(__uint_as_float(sv[i + 1]), c.y, -m.y) : -INFINITY;
             x[i + 2] = ok ? fmaf(__uint_as_float(sv[i + 2]), c.z, -m.z) : -INFINITY;
             x[i + 3] = ok ? fmaf(__uint_as_float(sv[i + 3]), c.w, -m.w) : -INFINITY;
         }
     };
-    // x -> P = 2^x rounded to the matrix type, into the operand; x becomes the rounded values:
-    // the sums take these, so a row's weights add up to one whatever the rounding does
-    auto weights = [&](float* x) {
+    // P = 2^x, rounded to bf16 or f16, into the operand. The sums take the rounded values, so a
+    // row's weights add up to one whatever the rounding does: bf16 leaves them in x, E4M3, whose
+    // parts need the registers, in pairs in w.
+    auto weights = [&](float* x, uint32_t* w, int gt) {
+        if constexpr (kBf16) {
 #pragma unroll
-        for (int u = 0; u < NC / 8; ++u) {
-            uint32_t w[4];
+            for (int u = 0; u < NC / 8; ++u) {
+                uint32_t o[4];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                float& p = x[8 * u + 2 * k];
-                float& q = x[8 * u + 2 * k + 1];
-                if constexpr (kBf16) {
+                for (int k = 0; k < 4; ++k) {
+                    float& p = x[8 * u + 2 * k];
+                    float& q = x[8 * u + 2 * k + 1];
                     const __nv_bfloat162 v = __floats2bfloat162_rn(ex2(p), ex2(q));
-                    w[k] = *reinterpret_cast<const uint32_t*>(&v);
-                    p = __uint_as_float(w[k] << 16);
-                    q = __uint_as_float(w[k] & 0xffff0000u);
-                } else {
-                    const __half2 v = __floats2half2_rn(ex2(p), ex2(q));
-                    w[k] = *reinterpret_cast<const uint32_t*>(&v);
-                    p = __low2float(v);
-                    q = __high2float(v);
+                    o[k] = *reinterpret_cast<const uint32_t*>(&v);
+                    p = __uint_as_float(o[k] << 16);
+                    q = __uint_as_float(o[k] & 0xffff0000u);
                 }
+                *reinterpret_cast<uint4*>(sh.p[0] + S::p_unit(r, h0 / 8 + u)) = make_uint4(o[0], o[1], o[2], o[3]);
             }
-            *reinterpret_cast<uint4*>(sh.p + S::p_unit(r, h0 / 8 + u)) = make_uint4(w[0], w[1], w[2], w[3]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < NC / 2; ++i) {
+                const __half2 v = __floats2half2_rn(ex2(x[2 * i]), ex2(x[2 * i + 1]));
+                w[i] = *reinterpret_cast<const uint32_t*>(&v);
+            }
+            // E5M2 is the upper byte of f16. A NaN loses itself in the first two parts' rounding
+            // and stays what is left of them, so the last part holds it.
+            uint32_t o[3][NC / 4];
+#pragma unroll
+            for (int k = 0; k < NC / 4; ++k) {
+                uint32_t x0 = w[2 * k], x1 = w[2 * k + 1];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const uint32_t p0 = (x0 + 0x00800080u) & 0xff00ff00u, p1 = (x1 + 0x00800080u) & 0xff00ff00u;
+                    o[i][k] = __byte_perm(p0, p1, 0x7531);
+                    x0 = h2_sub(x0, p0);
+                    x1 = h2_sub(x1, p1);
+                }
+                o[2][k] = h2x2_to_e5m2x4(x0, x1);
+            }
+            if (gt > 0 && !mbar_wait(&sh.pv_done, (uint32_t)((gt - 1) & 1), abort)) return false;
+#pragma unroll
+            for (int i = 0; i < 3; ++i)
+#pragma unroll
+                for (int u = 0; u < NC / 16; ++u)
+                    *reinterpret_cast<uint4*>(sh.p[i] + S::p_unit(r, h0 / 16 + u)) =
+                        make_uint4(o[i][4 * u], o[i][4 * u + 1], o[i][4 * u + 2], o[i][4 * u + 3]);
         }
+        return true;
+    };
+    auto value = [](const float* x, const uint32_t* w, int i) {
+        if constexpr (kBf16) return x[i];
+        const __half2 v = *reinterpret_cast<const __half2*>(&w[i >> 1]);
+        return i & 1 ? __high2float(v) : __low2float(v);
     };
     Pieces pi(sh.range);
     Piece pc;
@@ -817,34 +935,37 @@ __device__ void softmax_role(Shared<kBf16, NH>& sh, const Args& a, uint32_t tmem
 #pragma unroll
         for (int i = 0; i < NC; ++i) lpart[i] = 0.f;
         for (int j = pc.j0; j < pc.j1; ++j, ++gt, g += 4) {
-            if (!mbar_wait(&sh.s_full, (uint32_t)(gt & 1), abort)) return;
+            if (!mbar_wait(&sh.s_full[kBf16 ? 0 : gt & 1], (uint32_t)((kBf16 ? gt : gt >> 1) & 1), abort)) return;
             // (complete already: orders the read of row_ok after the producer's write)
             if (!mbar_wait(&sh.full[g % S::kPairs], (uint32_t)((g / S::kPairs) & 1), abort)) return;
             tc_fence_after();
-            const bool ok = sh.row_ok[gt & 1][r] != 0;
-            if constexpr (kBf16) {
-                // Rows that are not seen came with the box or are left from another tile:
-                // whatever they hold (NaN among it) must not meet P = 0 in the product. S has
-                // read them, PV has not.
-                if (!ok) {
+            const bool ok = sh.row_ok[gt & 3][r] != 0;
+            // Rows that are not seen came with the box or are left from another tile: whatever
+            // they hold (NaN among it) must not meet P = 0 in the product. S has read them, PV
+            // has not.
+            if (!ok) {
+                constexpr int kAll = 4 * S::kChunks, kMine = kAll / S::kGroups;
 #pragma unroll 1
-                    for (int c = cg * (8 / S::kGroups); c < (cg + 1) * (8 / S::kGroups); ++c) {
-                        uint4* z = reinterpret_cast<uint4*>(sh.kv[(g + (c >> 1)) % S::kPairs][c & 1] + r * 128);
+                for (int c = cg * kMine; c < (cg + 1) * kMine; ++c) {
+                    uint4* z = reinterpret_cast<uint4*>(sh.kv[(g + c / S::kChunks) % S::kPairs][c % S::kChunks] + r * 128);
 #pragma unroll
-                        for (int u = 0; u < 8; ++u) z[(u + lane) & 7] = make_uint4(0u, 0u, 0u, 0u);  // all banks
-                    }
+                    for (int u = 0; u < 8; ++u) z[(u + lane) & 7] = make_uint4(0u, 0u, 0u, 0u);  // all banks
                 }
             }
             const bool opens = j == pc.j0;
             bool move = opens, any = false;
             if (!opens) {
                 float x[NC];
-                logits(x, m_sub, it, ok);
+                logits(x, true, it, gt, ok);
                 bool over = false;
 #pragma unroll
-                for (int i = 0; i < NC; ++i) over |= x[i] > kLazyMax + kLift<kBf16>;
-                if (__any_sync(0xffffffffu, over) && lane == 0) *(volatile int*)&sh.moved[cg] = gt;
-                weights(x);
+                for (int i = 0; i < NC; ++i) over |= x[i] > S::kLazyMax + S::kLift;
+                over = __any_sync(0xffffffffu, over) && lane == 0;
+                if (kBf16 && over) *(volatile int*)&sh.moved[cg] = gt;
+                uint32_t w[NC / 2];
+                if (!weights(x, w, gt)) return;
+                // (E4M3: after PV of the tile before, whose marks everyone has read by then)
+                if (!kBf16 && over) *(volatile int*)&sh.moved[cg] = gt;
                 fence_proxy_async_smem();
                 tc_fence_before();
                 __syncwarp();
@@ -855,13 +976,13 @@ __device__ void softmax_role(Shared<kBf16, NH>& sh, const Args& a, uint32_t tmem
                 move = *(volatile int*)&sh.moved[cg] == gt;
                 if (!move) {
 #pragma unroll
-                    for (int i = 0; i < NC; ++i) lpart[i] += x[i];
+                    for (int i = 0; i < NC; ++i) lpart[i] += value(x, w, i);
                 }
             }
             if (move) {
                 tc_fence_after();
                 float x[NC];
-                logits(x, nullptr, it, ok);
+                logits(x, false, it, gt, ok);
 #pragma unroll
                 for (int i = 0; i < NC; i += 4) {
                     const float4 m4 = make_float4(warp_max(x[i]), warp_max(x[i + 1]), warp_max(x[i + 2]), warp_max(x[i + 3]));
@@ -872,18 +993,32 @@ __device__ void softmax_role(Shared<kBf16, NH>& sh, const Args& a, uint32_t tmem
                 if (!mbar_wait(&sh.max_bar[cg], (uint32_t)(moves++ & 1), abort)) return;
                 const float tm = fmaxf(fmaxf(sh.red_max[0][h0 + mine], sh.red_max[1][h0 + mine]),
                                        fmaxf(sh.red_max[2][h0 + mine], sh.red_max[3][h0 + mine]));
-                const float m_new = tm > m_run + kLazyMax ? tm : m_run;
+                const float m_new = tm > m_run + S::kLazyMax ? tm : m_run;
                 const float alpha = (m_new != m_run && m_run != -INFINITY) ? ex2(m_run - m_new) : 1.f;
                 const bool rescale = __any_sync(0xffffffffu, alpha != 1.f);
                 m_run = m_new;
                 __syncwarp();
-                if (lane < NC) m_sub[lane] = m_run == -INFINITY ? kNone : m_run - kLift<kBf16>;
+                if (lane < NC) m_sub[lane] = m_run == -INFINITY ? kNone : m_run - S::kLift;
                 __syncwarp();
-                logits(x, m_sub, it, ok);
-                weights(x);
+                // (bf16 reads them again: kept until here they spill, 357 us against 351 for 64 heads
+                // and 16 x 131,072; with two reads a logit, E4M3 gains a microsecond by keeping them)
+                if constexpr (kBf16) {
+                    logits(x, true, it, gt, ok);
+                } else {
 #pragma unroll
-                for (int i = 0; i < NC; ++i) lpart[i] = fmaf(lpart[i], __shfl_sync(0xffffffffu, alpha, i), x[i]);
-                if (rescale) {  // O holds the tiles before this one (S was issued after them)
+                    for (int i = 0; i < NC; i += 4) {
+                        const float4 m = *reinterpret_cast<const float4*>(m_sub + i);
+                        x[i] -= m.x;
+                        x[i + 1] -= m.y;
+                        x[i + 2] -= m.z;
+                        x[i + 3] -= m.w;
+                    }
+                }
+                uint32_t w[NC / 2];
+                if (!weights(x, w, gt)) return;
+#pragma unroll
+                for (int i = 0; i < NC; ++i) lpart[i] = fmaf(lpart[i], __shfl_sync(0xffffffffu, alpha, i), value(x, w, i));
+                if (rescale) {  // O holds the tiles before this one: their PV has ended
 #pragma unroll 1
                     for (int mb = 0; mb < 4; ++mb) {
                         uint32_t ov[NC];
@@ -913,7 +1048,7 @@ __device__ void softmax_role(Shared<kBf16, NH>& sh, const Args& a, uint32_t tmem
         if (!mbar_wait(&sh.sum_bar[cg], (uint32_t)(it & 1), abort)) return;
         const float l = (sh.red_sum[0][h0 + mine] + sh.red_sum[1][h0 + mine]) +
                         (sh.red_sum[2][h0 + mine] + sh.red_sum[3][h0 + mine]);
-        m_run -= kLift<kBf16>;  // what P and O are relative to
+        m_run -= S::kLift;  // what P and O are relative to
         // lane = channel 128 mb + 32 qd + lane of NC heads: for each head the warp stores 32
         // neighbouring values
         if (pc.whole()) {
@@ -964,22 +1099,22 @@ k_paged_attn(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap
         mbar_init(&sh.q_full[0], S::kHelpWarps);
         mbar_init(&sh.q_full[1], S::kHelpWarps);
         mbar_init(&sh.q_empty, 1);
-        mbar_init(&sh.s_full, 1);
+        mbar_init(&sh.s_full[0], 1);
+        mbar_init(&sh.s_full[1], 1);
+        mbar_init(&sh.pv_done, 1);
         mbar_init(&sh.p_full, S::kSoftWarps);
         mbar_init(&sh.p_again, S::kSoftWarps);
         mbar_init(&sh.o_full, 1);
         mbar_init(&sh.drain, 1);
         for (int i = 0; i < S::kPairs; ++i) {
-            mbar_init(&sh.full[i], kBf16 ? 1 : S::kHelpWarps / 2);
-            mbar_init(&sh.raw_full[i], 1);
+            mbar_init(&sh.full[i], 1);
             mbar_init(&sh.empty[i], 1);
         }
         for (int i = 0; i < S::kGroups; ++i) {
             mbar_init(&sh.max_bar[i], 4);
-
             mbar_init(&sh.sum_bar[i], 4);
         }
-        for (int i = 0; i < 4; ++i) sh.moved[i] = -1;
+        sh.moved[0] = sh.moved[1] = -1;
         sh.abort = 0;
         fence_mbar_init();
     }
@@ -998,17 +1133,15 @@ k_paged_attn(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap
     if (warp < S::kSoftWarps) {
         softmax_role<kBf16, NH>(sh, a, tmem, warp, lane, abort);
     } else if (warp == S::kMmaWarp) {
-        mma_role<kBf16, NH>(sh, a, tmem, abort);
+        mma_role<NH>(sh, a, tmem, lane, abort);
         // every MMA issued must finish before TMEM and shared memory are released
         __syncwarp();
         if (elect_one()) tc_commit(&sh.drain);
         if (!mbar_wait_drain(&sh.drain, 0)) *abort = 1;
     } else if (warp == S::kTmaWarp) {
         tma_role<kBf16, NH>(sh, a, &tmap, lane, abort);
-    } else if constexpr (kBf16) {
-        query_role<NH>(sh, a, tid - 32 * S::kHelp0, lane, abort);
     } else {
-        decode_role<NH>(sh, a, tid - 32 * S::kHelp0, lane, abort);
+        query_role<NH>(sh, a, tid - 32 * S::kHelp0, lane, abort);
     }
     tc_fence_before();
     __syncthreads();
@@ -1026,7 +1159,7 @@ constexpr int smem_bytes() {
 }
 // (plan() has 4,480 bytes of its own)
 static_assert(smem_bytes<true, 64>() <= 227840 && smem_bytes<true, 32>() <= 227840 && smem_bytes<true, 16>() <= 227840 &&
-                  smem_bytes<false, 64>() <= 227840 && smem_bytes<false, 32>() <= 227840 && smem_bytes<false, 16>() <= 227840,
+                  smem_bytes<false, 64>() <= 227840 && smem_bytes<false, 32>() <= 227840,
               "shared memory of a CTA");
 
 // ---------------------------------------------------------------- join
@@ -1133,9 +1266,8 @@ int grid_of(const csa2_params* p) {
     return p->max_ctas > 0 && p->max_ctas < n ? p->max_ctas : n;
 }
 
-// The layer's rows as a 2-d tensor map, whose boxes are box_rows rows x 128 bytes: of bf16 laid
-// out in the 128-byte swizzle of the MMA operands, of E4M3 (which is decoded) as they are. The
-// driver's encoder is looked up once.
+// The layer's rows as a 2-d tensor map, whose boxes are box_rows rows x 128 bytes, laid out in
+// the 128-byte swizzle of the MMA operands. The driver's encoder is looked up once.
 int encode_rows(const Args& a, CUtensorMap* m) {
     using Encode = decltype(&cuTensorMapEncodeTiled);
     static Encode encode = [] {
@@ -1153,7 +1285,7 @@ int encode_rows(const Args& a, CUtensorMap* m) {
     const cuuint32_t box[2] = {bf16 ? 64u : 128u, (cuuint32_t)a.box_rows}, steps[2] = {1, 1};
     if (encode(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 2,
                const_cast<uint8_t*>(a.base), dims, strides, box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
-               bf16 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
         return fail(CSA2_ERR_CUDA, "paged_attn: tensor map of the pool");
     return CSA2_OK;
@@ -1180,7 +1312,6 @@ cudaError_t preload_paged_attn() {
                             [] { return preload_kernel(k_paged_attn<true, 16>, smem_bytes<true, 16>()); },
                             [] { return preload_kernel(k_paged_attn<false, 64>, smem_bytes<false, 64>()); },
                             [] { return preload_kernel(k_paged_attn<false, 32>, smem_bytes<false, 32>()); },
-                            [] { return preload_kernel(k_paged_attn<false, 16>, smem_bytes<false, 16>()); },
                             [] { return preload_kernel(k_paged_join<false>); },
                             [] { return preload_kernel(k_paged_join<true>); }};
     for (auto f : l)
@@ -1259,8 +1390,7 @@ extern "C" int csa2_paged_attn(const csa2_params* p, const csa2_pages* c, int la
         rc = p->heads > 32 ? launch_attn<true, 64>(a, rows, &cfg)
              : p->heads > 16 ? launch_attn<true, 32>(a, rows, &cfg) : launch_attn<true, 16>(a, rows, &cfg);
     } else {
-        rc = p->heads > 32 ? launch_attn<false, 64>(a, rows, &cfg)
-             : p->heads > 16 ? launch_attn<false, 32>(a, rows, &cfg) : launch_attn<false, 16>(a, rows, &cfg);
+        rc = p->heads > 32 ? launch_attn<false, 64>(a, rows, &cfg) : launch_attn<false, 32>(a, rows, &cfg);
     }
     if (rc) return rc;
     // A sequence is cut into about ctas / B pieces, at most one a tile, which a narrow thread

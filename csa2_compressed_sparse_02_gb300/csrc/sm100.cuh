@@ -43,6 +43,18 @@ __device__ __forceinline__ bool mbar_try_wait(uint64_t* bar, uint32_t parity) {
 // a second on any load this library generates.
 constexpr uint32_t kSpinLimit = 1u << 22;
 
+// Whether the phase with the given parity has completed, without a wait.
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+        " selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
 // Waits for the phase with the given parity to complete. Returns false when it
 // gave up (after kSpinLimit tries) or when another role already raised *abort;
 // a give-up raises *abort.
@@ -59,6 +71,21 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volati
 __device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort) {
     const bool ok = mbar_wait(bar, parity, abort);
     return __all_sync(0xffffffffu, ok);
+}
+
+// A warp waits on a barrier of each lane's own: 1 once the phases of all lanes below `split` have
+// completed, 2 once those of all others have (1 if both), 0 if it gave up.
+__device__ __forceinline__ int mbar_wait_either_warp(uint64_t* bar, uint32_t parity, int lane, int split,
+                                                     volatile int* abort) {
+    const uint32_t first = (1u << split) - 1u;
+    for (uint32_t i = 0; i < kSpinLimit; ++i) {
+        const uint32_t done = __ballot_sync(0xffffffffu, mbar_test(bar, parity));
+        if ((done & first) == first) return 1;
+        if ((done | first) == 0xffffffffu) return 2;
+        if ((i & 255u) == 255u && __any_sync(0xffffffffu, *abort != 0)) return 0;
+    }
+    *abort = 1;
+    return 0;
 }
 
 // try_wait with a suspend-time hint: a waiting thread sleeps until the phase
@@ -308,6 +335,24 @@ __device__ __forceinline__ void mma_f16(uint32_t d_tmem, uint64_t adesc, uint64_
         " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
         "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
         : "memory");
+}
+
+// The 8-bit types, which the descriptor names for A and B each; K = 32. The form with a
+// collector's name says what becomes of A: MMAs in a row that share it read it once.
+enum class Collector { kDiscard, kFill, kUse, kLast };
+template <Collector kA = Collector::kDiscard>
+__device__ __forceinline__ void mma_f8(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                       uint32_t accumulate) {
+#define CSA2_MMA_F8(collector)                                                                       \
+    asm volatile(                                                                                    \
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"                                                \
+        " tcgen05.mma.cta_group::1.kind::f8f6f4.collector::a::" collector " [%0], %1, %2, %3, p;\n}\n" \
+        ::"r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate) : "memory")
+    if constexpr (kA == Collector::kFill) CSA2_MMA_F8("fill");
+    else if constexpr (kA == Collector::kUse) CSA2_MMA_F8("use");
+    else if constexpr (kA == Collector::kLast) CSA2_MMA_F8("lastuse");
+    else CSA2_MMA_F8("discard");
+#undef CSA2_MMA_F8
 }
 
 // Arrive on an mbarrier once every tcgen05 operation this thread issued so far completes.

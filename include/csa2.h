@@ -649,10 +649,12 @@ size_t csa2_paged_attn_workspace_size(const csa2_params* p, const csa2_pages* c,
  *   position without a page (not seen) CSA2_DEV_BAD_INDEX.
  *   workspace: csa2_paged_attn_workspace_size bytes, 256-byte aligned, contents
  *   arbitrary; calls that share it must be ordered (one stream or events).
- * On the 5th-generation tensor cores: bf16 pages as bf16 operands, E4M3 pages decoded
- * exactly into f16 (the query scaled per head by a power of two); fp32 logits, sums and
- * accumulators; the weights e^z are rounded to the operands' type, in numerator and
- * denominator alike. A batch of at most as many sequences as CTAs (one per SM, or
+ * On the 5th-generation tensor cores, the pages as they are; fp32 logits, sums and
+ * accumulators. The weights e^z are rounded to bf16, for E4M3 pages to f16, in numerator and
+ * denominator alike. With E4M3 pages f16 weights are exact sums of three E5M2 values (multiples
+ * of 2^-25 of the largest at least, below that to the nearest one), and a query is the sum of
+ * two E4M3 values under a power of two per head: exact down to 2^-14 of the head's largest
+ * value, to 2^-22 of it below; a head whose query holds an infinity gives NaN. A batch of at most as many sequences as CTAs (one per SM, or
  * p->max_ctas) is cut into pieces of nearly equal length, one per CTA, where that leaves few
  * CTAs idle; else into equal ranges of tiles of 128 positions. A second kernel joins the sequences that were cut,
  * in the order of their positions, so results do not vary from run to run.

@@ -10,8 +10,8 @@ each: below 4 * 2^-24 (|a| + |b|) in all, then the output's own rounding.
 Attention: p is rounded to the pages' matrix type (u_p: bf16 2^-8, for E4M3 pages f16 2^-11)
 in numerator and denominator alike, so o moves by at most 2 u_p A with A = sum p |v| / den,
 and by 2 dz A for logits that are dz off; fp32 sums of 512 products give dz <= 512 * 2^-24 *
-scale * sum |q||k|, in practice far less; ex2.approx adds 2^-22. The output's rounding comes
-on top. Over many values the roundings are independent: each contributes at most u / sqrt(3)
+scale * sum |q||k|, in practice far less; with E4M3 pages two E4M3 parts of the query leave
+2^-22 of a head's largest |q| besides; ex2.approx adds 2^-22. The output's rounding comes on top. Over many values the roundings are independent: each contributes at most u / sqrt(3)
 in the mean square, so the relative error in the 2-norm stays below
 sqrt(2) * 2^-8 / sqrt(3) = 3.2e-3; 4e-3 is asked for."""
 import math
@@ -398,7 +398,8 @@ def attn64(p, c, layer, q, sink, rows, T, window, first):
             continue
         qb = q[b].double().cpu().numpy()
         z = qb @ k.T * float(p.softmax_scale)
-        dz = max(dz, float((np.abs(qb) @ np.abs(k).T).max()) * float(p.softmax_scale) * 512 * 2.0 ** -24)
+        dq = 2.0 ** -22 * np.abs(qb).max(1, keepdims=True) if p.kv_format == api.E4M3 else 0.0
+        dz = max(dz, float(((np.abs(qb) * 512 * 2.0 ** -24 + dq) @ np.abs(k).T).max()) * float(p.softmax_scale))
         s = np.full((H, 1), -np.inf) if sink is None else sink.double().cpu().numpy()[:, None]
         mx = np.maximum(z.max(1, keepdims=True), s)
         e = np.exp(z - mx)
@@ -413,10 +414,10 @@ def assert_attn(got, ref, kv):
     g = got.double().cpu().numpy()
     u_p = 2.0 ** -8 if kv == api.BF16 else 2.0 ** -11
     # weights below fp32's normals (2^-126 of the largest) count as 0: at most 2,100
-    # positions of |v| < 2^5 here, so 2^-109 in all. f16 holds weights below its normals as
-    # multiples of 2^-24, half a step off at most, when the largest is 2^7 or more: 2^-32 of
-    # the sum of weights each, in the numerator (times |v|) and the denominator (times |o|).
-    step = 0.0 if kv == api.BF16 else 2.0 ** -32
+    # positions of |v| < 2^5 here, so 2^-109 in all. The three E5M2 parts of an f16 weight hold
+    # it exactly, but for multiples of 2^-16, half a step off at most, when the largest weight
+    # is 2^9 or more: 2^-26 of the sum of weights each, in the numerator (times |v|).
+    step = 0.0 if kv == api.BF16 else 2.0 ** -26
     over = np.abs(g - o) - (2.0 ** -8 * np.abs(o) + (2 * u_p + 2 * dz + 2.0 ** -20) * A + step * F + 2.0 ** -109)
     assert over.max(initial=0) <= 0, over.max()
     n = np.linalg.norm(o)
@@ -650,6 +651,53 @@ def test_attention_nan_that_is_seen_reaches_the_output():
     c.pool[0, c.table[1, 3].item(), 5, 100] = float("nan")
     out = attend(p, c, q, sink, None, [200, 200])
     assert torch.isfinite(out[0]).all() and torch.isnan(out[1]).all()
+
+
+@pytest.mark.parametrize("heads", [5, 16, 64])
+def test_attention_e4m3_queries_of_a_wide_range(heads):
+    """The query's two E4M3 parts: channels down to 2^-18 of a head's largest, heads from 2^-40 on."""
+    p, c, q, sink = filled(api.E4M3, heads, [700, 129], 16, seed=35)
+    g = torch.Generator(device=DEV).manual_seed(36)
+    q = q.float() * torch.exp2(-torch.randint(0, 19, q.shape, generator=g, device=DEV).float())
+    q = (q * torch.exp2(torch.randint(-40, 4, q.shape[:2], generator=g, device=DEV).float())[..., None]).bfloat16()
+    assert_attn(attend(p, c, q, sink, None, [700, 129]), attn64(p, c, 0, q, sink, [0, 1], [700, 129], 0, 0), api.E4M3)
+
+
+@pytest.mark.parametrize("heads", [16, 64])
+@pytest.mark.parametrize("low,high", [(-16.0, 0.0), (-11.0, -10.0), (-6.0, -5.0)])
+def test_attention_e4m3_long_tails(low, high, heads):
+    """One position far above the others, whose weights reach below the smallest part of P:
+    sums of 16-bit weights in 8-bit parts. The peak comes late, so the maximum moves."""
+    T = 2049
+    p, c, q, sink = filled(api.E4M3, heads, [T], 64, seed=37)
+    g = torch.Generator(device=DEV).manual_seed(38)
+    k0 = torch.rand(T, generator=g, device=DEV) * (high - low) + low
+    k0[T - 300] = 0
+    t = torch.arange(T, device=DEV)
+    pool = c.pool[0].float()
+    pool[c.table[0, t // 64].long(), t % 64, 0] = k0
+    c.pool[0].copy_(pool.to(dtype_of(api.E4M3)))
+    q = torch.zeros_like(q)
+    q[..., 0] = 32
+    sink = torch.full_like(sink, -100.0)
+    assert_attn(attend(p, c, q, sink, None, [T]), attn64(p, c, 0, q, sink, [0], [T], 0, 0), api.E4M3)
+
+
+@pytest.mark.parametrize("heads", [16, 64])
+def test_attention_e4m3_nan_and_infinity(heads):
+    """A NaN that is seen reaches every head of its sequence; an infinite query its head only."""
+    p, c, q, sink = filled(api.E4M3, heads, [300, 200], 16, seed=39)
+    ref = attend(p, c, q, sink, None, [300, 200])
+    q2 = q.clone()
+    q2[1, 3, 100] = float("inf")
+    out = attend(p, c, q2, sink, None, [300, 200])
+    assert out[1, 3].isnan().all()
+    out[1, 3] = ref[1, 3]
+    assert torch.equal(out, ref)
+    pool = c.pool[0].view(torch.uint8)
+    pool[c.table[0, 150 // 16].long(), 150 % 16, 7] = 0x7F
+    out = attend(p, c, q, sink, None, [300, 200])
+    assert out[0].isnan().all() and torch.equal(out[1], ref[1])
 
 
 def test_attention_wide_values_of_bf16():
