@@ -78,7 +78,7 @@ __device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, v
 __device__ __forceinline__ int mbar_wait_either_warp(uint64_t* bar, uint32_t parity, int lane, int split,
                                                      volatile int* abort) {
     const uint32_t first = (1u << split) - 1u;
-    for (uint32_t i = 0; i < kSpinLimit; ++i) {
+    for (uint32_t i = 0; i < 8 * kSpinLimit; ++i) {  // (a test does not sleep, as a try may)
         const uint32_t done = __ballot_sync(0xffffffffu, mbar_test(bar, parity));
         if ((done & first) == first) return 1;
         if ((done | first) == 0xffffffffu) return 2;
