@@ -815,6 +815,7 @@ __device__ __forceinline__ uint32_t h2_sub(uint32_t x, uint32_t y) {
     const __half2 d = __hsub2(*reinterpret_cast<const __half2*>(&x), *reinterpret_cast<const __half2*>(&y));
     return *reinterpret_cast<const uint32_t*>(&d);
 }
+// Four E5M2 of halves (x.lo, x.hi, y.lo, y.hi); E5M2 is the upper byte of f16.
 __device__ __forceinline__ uint32_t h2x2_to_e5m2x4(uint32_t x, uint32_t y) {
     uint32_t r;
     asm("{\n .reg .b16 lo, hi;\n cvt.rn.satfinite.e5m2x2.f16x2 lo, %1;\n cvt.rn.satfinite.e5m2x2.f16x2 hi, %2;\n"
@@ -870,9 +871,10 @@ __device__ void softmax_role(Shared<kBf16, NH>& sh, const Args& a, uint32_t tmem
             x[i + 3] = ok ? fmaf(__uint_as_float(sv[i + 3]), c.w, -m.w) : -INFINITY;
         }
     };
-    // P = 2^x, rounded to bf16 or f16, into the operand. The sums take the rounded values, so a
-    // row's weights add up to one whatever the rounding does: bf16 leaves them in x, E4M3, whose
-    // parts need the registers, in pairs in w.
+    // P = 2^x, rounded to bf16 or f16, into the operand. The sums take the values that the product
+    // multiplies (E4M3: what the three parts add up to, so without what is left of a weight below
+    // the last part's steps), so a row's weights add up to one whatever the rounding does: bf16
+    // leaves them in x, E4M3, whose parts need the registers, in pairs in w.
     auto weights = [&](float* x, uint32_t* w, int gt) {
         if constexpr (kBf16) {
 #pragma unroll
@@ -895,8 +897,9 @@ __device__ void softmax_role(Shared<kBf16, NH>& sh, const Args& a, uint32_t tmem
                 const __half2 v = __floats2half2_rn(ex2(x[2 * i]), ex2(x[2 * i + 1]));
                 w[i] = *reinterpret_cast<const uint32_t*>(&v);
             }
-            // E5M2 is the upper byte of f16. A NaN loses itself in the first two parts' rounding
-            // and stays what is left of them, so the last part holds it.
+            // A NaN loses itself in the first two parts' rounding and stays what is left of them, so
+            // the last part holds it. What that one leaves out is at most half its step, and what
+            // it leaves of w a multiple of 2^-16 that f16 holds: both differences are exact.
             uint32_t o[3][NC / 4];
 #pragma unroll
             for (int k = 0; k < NC / 4; ++k) {
@@ -909,6 +912,8 @@ __device__ void softmax_role(Shared<kBf16, NH>& sh, const Args& a, uint32_t tmem
                     x1 = h2_sub(x1, p1);
                 }
                 o[2][k] = h2x2_to_e5m2x4(x0, x1);
+                w[2 * k] = h2_sub(w[2 * k], h2_sub(x0, __byte_perm(o[2][k], 0u, 0x1404)));
+                w[2 * k + 1] = h2_sub(w[2 * k + 1], h2_sub(x1, __byte_perm(o[2][k], 0u, 0x3424)));
             }
             if (gt > 0 && !mbar_wait(&sh.pv_done, (uint32_t)((gt - 1) & 1), abort)) return false;
 #pragma unroll

@@ -683,6 +683,40 @@ def test_attention_e4m3_long_tails(low, high, heads):
     assert_attn(attend(p, c, q, sink, None, [T]), attn64(p, c, 0, q, sink, [0], [T], 0, 0), api.E4M3)
 
 
+def one_peak(kv, T, drop, heads, at, ctas=1):
+    """(params, cache, q, the output in 64 bits [512]) of a sequence in which position `at` weighs 1
+    and every other one 2^-drop, by CTAs that hold all of it or a share each. Channel 0 sets the
+    logits, channel 1 is one everywhere, 2 and 3 are +-1 but zero at the peak, the rest random."""
+    ps = 64
+    n = -(-T // ps)
+    p = api.default_params(kv_format=kv, heads=heads)
+    p.max_ctas, p.softmax_scale = ctas, drop * math.log(2) / 512
+    rows = randn(64, D, seed=T % 1000).to(dtype_of(kv)).bfloat16().repeat(n, 1)
+    rows[:, 0], rows[:, 1], rows[:, 2], rows[:, 3] = -16, 1, 1, -1
+    rows[at] = 0
+    rows[at, 1] = 1
+    c = api.PagedCache(p, pool=rows.to(dtype_of(kv)).view(1, n, ps, D), device=DEV,
+                       table=i32(np.arange(n)[None]), ref=i32(np.ones(n)))
+    total = torch.zeros(D, dtype=torch.float64, device=DEV)
+    for i in range(0, T, 1 << 16):
+        total += rows[i:min(T, i + (1 << 16))].double().sum(0)
+    w, peak = 2.0 ** -drop, rows[at].double()
+    q = torch.zeros(1, heads, D, dtype=torch.bfloat16, device=DEV)
+    q[..., 0] = 32
+    return p, c, q, (peak + w * (total - peak)) / (1 + w * (T - 1))
+
+
+@pytest.mark.parametrize("heads", [16, 64])
+@pytest.mark.parametrize("T", [300_000, 1_000_000])
+def test_attention_e4m3_weights_below_the_parts_add_up_to_one(heads, T):
+    """What the three parts of a weight leave out is left out of the sum too: a channel that is one
+    everywhere comes out as one (whatever is off by less than 2^-9 rounds to it), although 0.4 and
+    1.4 % of the weight lie below the last part's steps at these lengths."""
+    p, c, q, _ = one_peak(api.E4M3, T, 26.1, heads, at=5)
+    out = attend(p, c, q, None, None, [T])
+    assert torch.all(out[..., 1] == 1), out[..., 1].min()
+
+
 @pytest.mark.parametrize("heads", [16, 64])
 def test_attention_e4m3_nan_and_infinity(heads):
     """A NaN that is seen reaches every head of its sequence; an infinite query its head only."""
