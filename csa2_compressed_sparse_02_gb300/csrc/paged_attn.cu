@@ -315,11 +315,18 @@ struct Shape {
     }
     // P = 2^(x - m + kLift), x - m <= kLazyMax before the maximum has to move. E5M2 ends at
     // 1.75 x 2^15 and holds small values as multiples of 2^-16, half a step off at most: with
-    // the largest weight at 2^9 or more, 2^-26 of it. (A kLazyMax of 3 would make that 2^-29, but
+    // the largest weight at 2^9 or more, 2^-26 of it (see kRun). (A kLazyMax of 3 would make that 2^-29, but
     // logits of a standard deviation of 3 in log2 then move the maximum in 4 of the first 8 tiles,
     // with 6 in 2.)
     static constexpr float kLazyMax = kBf16 ? 8.0f : 6.0f;
     static constexpr float kLift = kBf16 ? 0.f : 9.f;
+    // Tiles that add up in TMEM under one maximum; those that follow start anew, and what came
+    // before is added in fp32 (add it up in one, and 2^-26.1 of a weight among them loses a million
+    // positions, 1.4 % of the weight). Of 16,384 positions at most 2^-12 of the weight lies below the
+    // parts' steps, whatever the length. An end costs about 12 us with 64 heads and 8 with 32, for
+    // the partial result through L2 and a pipeline that starts again: 16 x 131,072, 108 tiles a
+    // CTA, 293 us with runs of 128, 305 of 64, 318 of 36.
+    static constexpr int kRun = kBf16 ? INT_MAX : 128;
 };
 
 constexpr uint32_t kChunk = 128 * 128;  // 128 positions x 128 bytes, 128-byte swizzle
@@ -336,6 +343,7 @@ struct Shared {
     float m_sub[4][kMaxHeads];         // per lane quarter: what its logits are reduced by
     alignas(8) int moved[2];           // per head group: the last tile whose maximum had to move
     float red_sum[4][kMaxHeads];
+    float2 before[4][NH];              // E4M3: maximum and sum of the piece up to this run, per lane quarter
     // by tile mod 4: the row holds a position that is seen. (The ring holds less than three
     // tiles, and a place comes free after PV, so tile gt + 4 begins after the softmax of gt.)
     uint8_t row_ok[4][kTile];
@@ -354,32 +362,37 @@ struct Shared {
 };
 
 // ---------------------------------------------------------------- a CTA's pieces
+// Tiles j0 .. j1 - 1 of sequence b: at most `most` of the CTA's piece of it.
 struct Piece {
+    // the CTA's range begins with the piece; the piece is the whole sequence; this begins, ends it
+    enum { kOpens = 1, kWhole = 2, kBegins = 4, kEnds = 8 };
     View v;
     int b, j0, j1;
-    bool opens;  // the CTA's range begins with it
-    __device__ __forceinline__ bool whole() const { return j0 == 0 && j1 == v.tiles; }
+    uint32_t is;  // which of these
 };
 struct Pieces {
     int64_t left;  // items
-    int b, j;
+    int b, from, j, most;
     bool opens;
-    __device__ __forceinline__ explicit Pieces(const Range& r) : left(r.items), b(r.b), j(r.j), opens(true) {}
+    __device__ __forceinline__ Pieces(const Range& r, int most)
+        : left(r.items), b(r.b), from(r.j), j(r.j), most(most), opens(true) {}
     __device__ __forceinline__ bool next(const Args& a, Piece& p) {
         while (left > 0) {
             p.v = view_of(a, b, false);
             if (j < p.v.tiles) {
+                const int to = (int)min((int64_t)p.v.tiles, j + left);
                 p.b = b;
                 p.j0 = j;
-                p.j1 = (int)min((int64_t)p.v.tiles, j + left);
-                p.opens = opens;
-                opens = false;
+                p.j1 = to - j > most ? j + most : to;
+                p.is = (opens ? Piece::kOpens : 0u) | (from == 0 && to == p.v.tiles ? Piece::kWhole : 0u) |
+                       (j == from ? Piece::kBegins : 0u) | (p.j1 == to ? Piece::kEnds : 0u);
                 left -= p.j1 - j;
                 j = p.j1;
                 return true;
             }
             ++b;
-            j = 0;
+            from = j = 0;
+            opens = false;
         }
         return false;
     }
@@ -390,7 +403,7 @@ struct Tiles {
     Pieces it;
     Piece pc;
     int j;
-    __device__ __forceinline__ explicit Tiles(const Range& r) : it(r), j(0) { pc.j1 = 0; }
+    __device__ __forceinline__ explicit Tiles(const Range& r) : it(r, INT_MAX), j(0) { pc.j1 = 0; }
     __device__ __forceinline__ bool next(const Args& a) {
         if (++j < pc.j1) return true;
         if (!it.next(a, pc)) return false;
@@ -518,7 +531,7 @@ __device__ void query_role(Shared<true, NH>& sh, const Args& a, int pt, int lane
     constexpr int kStagers = 32 * Shape<true, NH>::kHelpWarps;
     static_assert(kStagers == 128, "a thread stages unit pt mod 64 of every other head");
     const int u = pt & 63, hb = pt >> 6;
-    Pieces pi(sh.range);
+    Pieces pi(sh.range, Shape<true, NH>::kRun);
     Piece pc;
     for (int it = 0; pi.next(a, pc); ++it) {
         if (it > 0 && !mbar_wait(&sh.q_empty, (uint32_t)((it - 1) & 1), abort)) return;
@@ -554,7 +567,7 @@ template <int NH>
 __device__ void query_role(Shared<false, NH>& sh, const Args& a, int pt, int lane, volatile int* abort) {
     constexpr int kWarps = Shape<false, NH>::kHelpWarps, kAtOnce = 4;  // heads whose loads are in flight together
     const int pw = pt >> 5;
-    Pieces pi(sh.range);
+    Pieces pi(sh.range, Shape<false, NH>::kRun);
     Piece pc;
     for (int it = 0; pi.next(a, pc); ++it) {
         if (it > 0 && !mbar_wait(&sh.q_empty, (uint32_t)((it - 1) & 1), abort)) return;
@@ -628,7 +641,7 @@ __device__ void mma_role(Shared<true, NH>& sh, const Args& a, uint32_t tmem, int
     const uint64_t dQ = smem_desc(smem_u32(sh.q[0]), 16, 1024, kLayoutSw128);
     const uint64_t dV = smem_desc(smem_u32(sh.kv[0][0]), kChunk, 1024, kLayoutSw128);
     const uint64_t dP = smem_desc(smem_u32(sh.p[0]), 1024, 8 * S::kPRow, S::kPLayout);
-    Pieces pi(sh.range);
+    Pieces pi(sh.range, S::kRun);
     Piece pc;
     int gt = 0, again = 0;  // tiles so far, those whose P came twice
     int slot0 = 0;          // slot of the tile's first pair, and its phase
@@ -704,7 +717,7 @@ __device__ void mma_role(Shared<false, NH>& sh, const Args& a, uint32_t tmem, in
     const uint64_t dQ = smem_desc(smem_u32(sh.q[0]), 16, 1024, kLayoutSw128);
     const uint64_t dV = smem_desc(smem_u32(sh.kv[0][0]), kChunk, 1024, kLayoutSw128);
     const uint64_t dP = smem_desc(smem_u32(sh.p[0]), 1024, 8 * S::kPRow, S::kPLayout);
-    Pieces pi(sh.range);
+    Pieces pi(sh.range, S::kRun);
     Piece pc;
     int gt = 0, again = 0;  // tiles whose PV has been issued, those whose P came twice
     int slot = 0, pv_slot = 0;  // first place of the next S and PV
@@ -930,7 +943,7 @@ __device__ void softmax_role(Shared<kBf16, NH>& sh, const Args& a, uint32_t tmem
         const __half2 v = *reinterpret_cast<const __half2*>(&w[i >> 1]);
         return i & 1 ? __high2float(v) : __low2float(v);
     };
-    Pieces pi(sh.range);
+    Pieces pi(sh.range, S::kRun);
     Piece pc;
     int g = 0, gt = 0, moves = 0;
     for (int it = 0; pi.next(a, pc); ++it) {
@@ -1051,12 +1064,45 @@ __device__ void softmax_role(Shared<kBf16, NH>& sh, const Args& a, uint32_t tmem
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.sum_bar[cg]);
         if (!mbar_wait(&sh.sum_bar[cg], (uint32_t)(it & 1), abort)) return;
-        const float l = (sh.red_sum[0][h0 + mine] + sh.red_sum[1][h0 + mine]) +
-                        (sh.red_sum[2][h0 + mine] + sh.red_sum[3][h0 + mine]);
+        float l = (sh.red_sum[0][h0 + mine] + sh.red_sum[1][h0 + mine]) +
+                  (sh.red_sum[2][h0 + mine] + sh.red_sum[3][h0 + mine]);
         m_run -= S::kLift;  // what P and O are relative to
+        float* part = part_of(a, blockIdx.x, pc.is & Piece::kOpens ? 0 : 1);
+        if constexpr (S::kRun != INT_MAX) {
+            if (!(pc.is & Piece::kBegins)) {
+                // What came before of the piece is added in TMEM: its O stands in part (written by
+                // this thread), its maximum and sum in sh.before.
+                const float2 ml = sh.before[qd][h0 + mine];
+                const float M = fmaxf(ml.x, m_run);
+                const float was = ml.x == -INFINITY ? 0.f : ex2(ml.x - M);
+                const float now = m_run == -INFINITY ? 0.f : ex2(m_run - M);
+                l = fmaf(ml.y, was, l * now);
+                m_run = M;
+                constexpr int kAtOnce = NC < 16 ? NC : 16;  // heads whose loads are in flight together
+#pragma unroll 1
+                for (int n = 0; n < 4 * NC; n += kAtOnce) {
+                    const int mb = n / NC, i0 = n % NC;
+                    const float* src = part + (int64_t)(h0 + i0) * kD + 128 * mb + r;
+                    float x[kAtOnce];
+                    uint32_t ov[kAtOnce];
+#pragma unroll
+                    for (int i = 0; i < kAtOnce; ++i) x[i] = h0 + i0 + i < a.heads ? src[i * kD] : 0.f;
+                    tmem_ld<kAtOnce>(tl + NH * mb + h0 + i0, ov);
+#pragma unroll
+                    for (int i = 0; i < kAtOnce; ++i)
+                        ov[i] = __float_as_uint(fmaf(x[i], __shfl_sync(0xffffffffu, was, i0 + i),
+                                                     __uint_as_float(ov[i]) * __shfl_sync(0xffffffffu, now, i0 + i)));
+                    tmem_st<kAtOnce>(tl + NH * mb + h0 + i0, ov);
+                }
+                tmem_wait_st();
+            }
+            __syncwarp();
+            if (!(pc.is & Piece::kEnds) && lane < NC) sh.before[qd][h0 + lane] = make_float2(m_run, l);
+            __syncwarp();
+        }
         // lane = channel 128 mb + 32 qd + lane of NC heads: for each head the warp stores 32
         // neighbouring values
-        if (pc.whole()) {
+        if ((pc.is & (Piece::kWhole | Piece::kEnds)) == (Piece::kWhole | Piece::kEnds)) {
             const float M = fmaxf(m_run, sink2);
             const float f = m_run == -INFINITY ? 0.f : ex2(m_run - M);
             const float den = l * f + (sink2 == -INFINITY ? 0.f : ex2(sink2 - M));
@@ -1074,7 +1120,6 @@ __device__ void softmax_role(Shared<kBf16, NH>& sh, const Args& a, uint32_t tmem
                 }
             }
         } else {
-            float* part = part_of(a, blockIdx.x, pc.opens ? 0 : 1);
             if (qd == 0 && lane < NC && h0 + lane < a.heads) {
                 part[(int64_t)a.heads * kD + h0 + lane] = m_run;
                 part[(int64_t)a.heads * (kD + 1) + h0 + lane] = l;
@@ -1162,9 +1207,10 @@ template <bool kBf16, int NH>
 constexpr int smem_bytes() {
     return (int)sizeof(Shared<kBf16, NH>) + 1024;
 }
-// (plan() has 4,480 bytes of its own)
-static_assert(smem_bytes<true, 64>() <= 227840 && smem_bytes<true, 32>() <= 227840 && smem_bytes<true, 16>() <= 227840 &&
-                  smem_bytes<false, 64>() <= 227840 && smem_bytes<false, 32>() <= 227840,
+// (227 KB, of which plan() has 1,664 bytes)
+template <bool kBf16, int NH>
+constexpr bool kFits = smem_bytes<kBf16, NH>() <= 227 * 1024 - 1664;
+static_assert(kFits<true, 64> && kFits<true, 32> && kFits<true, 16> && kFits<false, 64> && kFits<false, 32>,
               "shared memory of a CTA");
 
 // ---------------------------------------------------------------- join

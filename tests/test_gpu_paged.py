@@ -684,9 +684,10 @@ def test_attention_e4m3_long_tails(low, high, heads):
 
 
 def one_peak(kv, T, drop, heads, at, ctas=1):
-    """(params, cache, q, the output in 64 bits [512]) of a sequence in which position `at` weighs 1
-    and every other one 2^-drop, by CTAs that hold all of it or a share each. Channel 0 sets the
-    logits, channel 1 is one everywhere, 2 and 3 are +-1 but zero at the peak, the rest random."""
+    """(params, cache, q, o, A, V) of a sequence in which position `at` weighs 1 and every other one
+    2^-drop, for `ctas` CTAs: the output in 64 bits, sum w |v| / den and max |v| [512]. Channel 0
+    sets the logits, channel 1 is one everywhere, 2 and 3 are +-1 but zero at the peak, the rest
+    random."""
     ps = 64
     n = -(-T // ps)
     p = api.default_params(kv_format=kv, heads=heads)
@@ -697,13 +698,16 @@ def one_peak(kv, T, drop, heads, at, ctas=1):
     rows[at, 1] = 1
     c = api.PagedCache(p, pool=rows.to(dtype_of(kv)).view(1, n, ps, D), device=DEV,
                        table=i32(np.arange(n)[None]), ref=i32(np.ones(n)))
-    total = torch.zeros(D, dtype=torch.float64, device=DEV)
+    total, size = torch.zeros(2, D, dtype=torch.float64, device=DEV)
     for i in range(0, T, 1 << 16):
-        total += rows[i:min(T, i + (1 << 16))].double().sum(0)
+        part = rows[i:min(T, i + (1 << 16))].double()
+        total += part.sum(0)
+        size += part.abs().sum(0)
     w, peak = 2.0 ** -drop, rows[at].double()
     q = torch.zeros(1, heads, D, dtype=torch.bfloat16, device=DEV)
     q[..., 0] = 32
-    return p, c, q, (peak + w * (total - peak)) / (1 + w * (T - 1))
+    o, A = ((x + w * (y - x)) / (1 + w * (T - 1)) for x, y in ((peak, total), (peak.abs(), size)))
+    return p, c, q, o, A, rows.abs().amax(0).double()
 
 
 @pytest.mark.parametrize("heads", [16, 64])
@@ -712,9 +716,50 @@ def test_attention_e4m3_weights_below_the_parts_add_up_to_one(heads, T):
     """What the three parts of a weight leave out is left out of the sum too: a channel that is one
     everywhere comes out as one (whatever is off by less than 2^-9 rounds to it), although 0.4 and
     1.4 % of the weight lie below the last part's steps at these lengths."""
-    p, c, q, _ = one_peak(api.E4M3, T, 26.1, heads, at=5)
+    p, c, q = one_peak(api.E4M3, T, 26.1, heads, at=5)[:3]
     out = attend(p, c, q, None, None, [T])
     assert torch.all(out[..., 1] == 1), out[..., 1].min()
+
+
+def assert_one_peak(got, o, A, V, drop, u_p, lost):
+    """A bound that does not grow with the length. Relative to A: the rounding of the weights (u_p,
+    numerator and denominator alike), of their logits (four fp32 roundings of `drop` in log2, times
+    ln 2, in both) and ex2 (2^-22, in both); and for the 16,384 positions that meet in one
+    accumulator a product's alignment to it, 2^-25 for each of at most three parts, and 2^-23 for
+    each sum of at least 16 products: below 2^-23 a position, 2^-9. `lost` of the largest weight for
+    each of them, which the parts leave out, in numerator (times |v|) and denominator. Then the
+    output's rounding."""
+    tol = (2 * u_p + 8 * drop * 2.0 ** -24 + 2.0 ** -21 + 2.0 ** -9) * A + 2.0 ** 14 * lost * (V + o.abs())
+    over = (got.double() - o).abs() - (tol + 2.0 ** -8 * (o.abs() + tol))
+    assert over.max().item() <= 0, (over.max().item(), over.argmax().item() % D)
+
+
+@pytest.mark.parametrize("heads", [16, 64])
+@pytest.mark.parametrize("T,ctas,at", [(300_000, 1, 5), (300_000, 2, 299_000), (1_000_000, 1, 9), (1_000_000, 3, 700_000)])
+@pytest.mark.parametrize("drop", [24.4, 25.4, 26.1, 28.0])
+def test_attention_e4m3_tails_of_long_contexts(drop, T, ctas, at, heads):
+    """Weights about the steps of a weight's last part and below, whose share grows with the length:
+    one position above a million others, many of them to a CTA."""
+    p, c, q, o, A, V = one_peak(api.E4M3, T, drop, heads, at, ctas)
+    assert_one_peak(attend(p, c, q, None, None, [T]), o, A, V, drop, 2.0 ** -11, 2.0 ** -26)
+
+
+@pytest.mark.parametrize("kv", [api.BF16, api.E4M3], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("ctas,T,window,first", [
+    (1, [40_000], 0, 0), (1, [16_384, 16_385, 32_768, 100, 32_897], 0, 0), (2, [60_000, 5, 34_000, 0, 17_000], 0, 0),
+    (3, [90_000, 21_000], 0, 0), (2, [70_000], 40_000, 9000), (2, [17_500] * 4, 17_000, 3)])
+@pytest.mark.parametrize("heads", [3, 33, 64])
+def test_attention_long_pieces(kv, heads, ctas, T, window, first):
+    """More tiles to a CTA than meet in one accumulator, in sequences that are cut and in whole
+    ones, first, in the middle and last of a CTA's range; the same bytes in every run."""
+    p, c, q, sink = filled(kv, heads, T, 64, seed=heads + ctas, window=window, first=first)
+    p.max_ctas = ctas
+    st = torch.zeros(1, dtype=torch.int32, device=DEV)
+    ws = torch.full_like(api.paged_attn_workspace(p, c, len(T)), 0xFF)  # NaN, wherever it is read unwritten
+    out = attend(p, c, q, sink, None, T, window, first, st=st, ws=ws)
+    assert st.item() == 0
+    assert_attn(out, attn64(p, c, 0, q, sink, np.arange(len(T)), T, window, first), kv)
+    assert torch.equal(attend(p, c, q, sink, None, T, window, first, st=st, ws=ws), out)
 
 
 @pytest.mark.parametrize("heads", [16, 64])
