@@ -321,12 +321,14 @@ struct Shape {
     static constexpr float kLazyMax = kBf16 ? 8.0f : 6.0f;
     static constexpr float kLift = kBf16 ? 0.f : 9.f;
     // Tiles that add up in TMEM under one maximum; those that follow start anew, and what came
-    // before is added in fp32 (add it up in one, and 2^-26.1 of a weight among them loses a million
-    // positions, 1.4 % of the weight). Of 16,384 positions at most 2^-12 of the weight lies below the
-    // parts' steps, whatever the length. An end costs about 12 us with 64 heads and 8 with 32, for
-    // the partial result through L2 and a pipeline that starts again: 16 x 131,072, 108 tiles a
-    // CTA, 293 us with runs of 128, 305 of 64, 318 of 36.
-    static constexpr int kRun = kBf16 ? INT_MAX : 128;
+    // before is added in fp32. The tensor cores align each product to the accumulator and leave out
+    // what lies below 2^-25 of it, and E4M3's parts end at 2^-26: with a million positions at
+    // 2^-26.1 of one before them in one accumulator, their 1.4 % of the weight were lost. Of
+    // 16,384 positions it is at most 2^-11 (E4M3 another 2^-12), whatever the length. An end costs
+    // 12 to 15 us with 64 heads and 6 with up to 32, for the partial result through L2 and a
+    // pipeline that starts again: 16 x 131,072, 108 tiles a CTA, in E4M3 293 us with runs of 128,
+    // 305 of 64, 318 of 36, in bf16 355 and 370.
+    static constexpr int kRun = 128;
 };
 
 constexpr uint32_t kChunk = 128 * 128;  // 128 positions x 128 bytes, 128-byte swizzle
@@ -343,7 +345,7 @@ struct Shared {
     float m_sub[4][kMaxHeads];         // per lane quarter: what its logits are reduced by
     alignas(8) int moved[2];           // per head group: the last tile whose maximum had to move
     float red_sum[4][kMaxHeads];
-    float2 before[4][NH];              // E4M3: maximum and sum of the piece up to this run, per lane quarter
+    float2 before[4][NH];              // maximum and sum of the piece up to this run, per lane quarter
     // by tile mod 4: the row holds a position that is seen. (The ring holds less than three
     // tiles, and a place comes free after PV, so tile gt + 4 begins after the softmax of gt.)
     uint8_t row_ok[4][kTile];
@@ -1068,38 +1070,36 @@ __device__ void softmax_role(Shared<kBf16, NH>& sh, const Args& a, uint32_t tmem
                   (sh.red_sum[2][h0 + mine] + sh.red_sum[3][h0 + mine]);
         m_run -= S::kLift;  // what P and O are relative to
         float* part = part_of(a, blockIdx.x, pc.is & Piece::kOpens ? 0 : 1);
-        if constexpr (S::kRun != INT_MAX) {
-            if (!(pc.is & Piece::kBegins)) {
-                // What came before of the piece is added in TMEM: its O stands in part (written by
-                // this thread), its maximum and sum in sh.before.
-                const float2 ml = sh.before[qd][h0 + mine];
-                const float M = fmaxf(ml.x, m_run);
-                const float was = ml.x == -INFINITY ? 0.f : ex2(ml.x - M);
-                const float now = m_run == -INFINITY ? 0.f : ex2(m_run - M);
-                l = fmaf(ml.y, was, l * now);
-                m_run = M;
-                constexpr int kAtOnce = NC < 16 ? NC : 16;  // heads whose loads are in flight together
+        if (!(pc.is & Piece::kBegins)) {
+            // What came before of the piece is added in TMEM: its O stands in part (written by
+            // this thread), its maximum and sum in sh.before.
+            const float2 ml = sh.before[qd][h0 + mine];
+            const float M = fmaxf(ml.x, m_run);
+            const float was = ml.x == -INFINITY ? 0.f : ex2(ml.x - M);
+            const float now = m_run == -INFINITY ? 0.f : ex2(m_run - M);
+            l = fmaf(ml.y, was, l * now);
+            m_run = M;
+            constexpr int kAtOnce = NC < 16 ? NC : 16;  // heads whose loads are in flight together
 #pragma unroll 1
-                for (int n = 0; n < 4 * NC; n += kAtOnce) {
-                    const int mb = n / NC, i0 = n % NC;
-                    const float* src = part + (int64_t)(h0 + i0) * kD + 128 * mb + r;
-                    float x[kAtOnce];
-                    uint32_t ov[kAtOnce];
+            for (int n = 0; n < 4 * NC; n += kAtOnce) {
+                const int mb = n / NC, i0 = n % NC;
+                const float* src = part + (int64_t)(h0 + i0) * kD + 128 * mb + r;
+                float x[kAtOnce];
+                uint32_t ov[kAtOnce];
 #pragma unroll
-                    for (int i = 0; i < kAtOnce; ++i) x[i] = h0 + i0 + i < a.heads ? src[i * kD] : 0.f;
-                    tmem_ld<kAtOnce>(tl + NH * mb + h0 + i0, ov);
+                for (int i = 0; i < kAtOnce; ++i) x[i] = h0 + i0 + i < a.heads ? src[i * kD] : 0.f;
+                tmem_ld<kAtOnce>(tl + NH * mb + h0 + i0, ov);
 #pragma unroll
-                    for (int i = 0; i < kAtOnce; ++i)
-                        ov[i] = __float_as_uint(fmaf(x[i], __shfl_sync(0xffffffffu, was, i0 + i),
-                                                     __uint_as_float(ov[i]) * __shfl_sync(0xffffffffu, now, i0 + i)));
-                    tmem_st<kAtOnce>(tl + NH * mb + h0 + i0, ov);
-                }
-                tmem_wait_st();
+                for (int i = 0; i < kAtOnce; ++i)
+                    ov[i] = __float_as_uint(fmaf(x[i], __shfl_sync(0xffffffffu, was, i0 + i),
+                                                 __uint_as_float(ov[i]) * __shfl_sync(0xffffffffu, now, i0 + i)));
+                tmem_st<kAtOnce>(tl + NH * mb + h0 + i0, ov);
             }
-            __syncwarp();
-            if (!(pc.is & Piece::kEnds) && lane < NC) sh.before[qd][h0 + lane] = make_float2(m_run, l);
-            __syncwarp();
+            tmem_wait_st();
         }
+        __syncwarp();
+        if (!(pc.is & Piece::kEnds) && lane < NC) sh.before[qd][h0 + lane] = make_float2(m_run, l);
+        __syncwarp();
         // lane = channel 128 mb + 32 qd + lane of NC heads: for each head the warp stores 32
         // neighbouring values
         if ((pc.is & (Piece::kWhole | Piece::kEnds)) == (Piece::kWhole | Piece::kEnds)) {

@@ -684,10 +684,10 @@ def test_attention_e4m3_long_tails(low, high, heads):
 
 
 def one_peak(kv, T, drop, heads, at, ctas=1):
-    """(params, cache, q, o, A, V) of a sequence in which position `at` weighs 1 and every other one
-    2^-drop, for `ctas` CTAs: the output in 64 bits, sum w |v| / den and max |v| [512]. Channel 0
-    sets the logits, channel 1 is one everywhere, 2 and 3 are +-1 but zero at the peak, the rest
-    random."""
+    """(params, cache, q, ref) of a sequence in which position `at` weighs 1 and every other one
+    2^-drop, for `ctas` CTAs. ref: the output in 64 bits, sum w |v| / den, that of the others alone,
+    and max |v| [512], then the others' share of the weight. Channel 0 sets the logits, channel 1 is
+    one everywhere, 2 and 3 are +-1 but zero at the peak, the rest random."""
     ps = 64
     n = -(-T // ps)
     p = api.default_params(kv_format=kv, heads=heads)
@@ -706,8 +706,9 @@ def one_peak(kv, T, drop, heads, at, ctas=1):
     w, peak = 2.0 ** -drop, rows[at].double()
     q = torch.zeros(1, heads, D, dtype=torch.bfloat16, device=DEV)
     q[..., 0] = 32
-    o, A = ((x + w * (y - x)) / (1 + w * (T - 1)) for x, y in ((peak, total), (peak.abs(), size)))
-    return p, c, q, o, A, rows.abs().amax(0).double()
+    den, others = 1 + w * (T - 1), w * (size - peak.abs())
+    return p, c, q, ((peak + w * (total - peak)) / den, (peak.abs() + others) / den, others / den,
+                     rows.abs().amax(0).double(), 1 - 1 / den)
 
 
 @pytest.mark.parametrize("heads", [16, 64])
@@ -716,20 +717,22 @@ def test_attention_e4m3_weights_below_the_parts_add_up_to_one(heads, T):
     """What the three parts of a weight leave out is left out of the sum too: a channel that is one
     everywhere comes out as one (whatever is off by less than 2^-9 rounds to it), although 0.4 and
     1.4 % of the weight lie below the last part's steps at these lengths."""
-    p, c, q = one_peak(api.E4M3, T, 26.1, heads, at=5)[:3]
+    p, c, q, _ = one_peak(api.E4M3, T, 26.1, heads, at=5)
     out = attend(p, c, q, None, None, [T])
     assert torch.all(out[..., 1] == 1), out[..., 1].min()
 
 
-def assert_one_peak(got, o, A, V, drop, u_p, lost):
-    """A bound that does not grow with the length. Relative to A: the rounding of the weights (u_p,
-    numerator and denominator alike), of their logits (four fp32 roundings of `drop` in log2, times
-    ln 2, in both) and ex2 (2^-22, in both); and for the 16,384 positions that meet in one
+def assert_one_peak(got, ref, drop, u_p, lost):
+    """A bound that does not grow with the length. The peak's weight is a power of two; the others
+    are off by their rounding u_p, that of their logits (four fp32 roundings of `drop` in log2, times
+    ln 2) and ex2's 2^-22, in numerator and denominator. For the 16,384 positions that meet in one
     accumulator a product's alignment to it, 2^-25 for each of at most three parts, and 2^-23 for
-    each sum of at least 16 products: below 2^-23 a position, 2^-9. `lost` of the largest weight for
-    each of them, which the parts leave out, in numerator (times |v|) and denominator. Then the
-    output's rounding."""
-    tol = (2 * u_p + 8 * drop * 2.0 ** -24 + 2.0 ** -21 + 2.0 ** -9) * A + 2.0 ** 14 * lost * (V + o.abs())
+    each sum of at least 16 products: below 2^-23 a position, 2^-9 of the whole. `lost` of the
+    largest weight for each of them, which the parts leave out, in numerator (times |v|) and
+    denominator. Then the output's rounding."""
+    o, A, others, V, share = ref
+    tol = (u_p + 4 * drop * 2.0 ** -24 + 2.0 ** -22) * (others + share * o.abs())
+    tol = tol + 2.0 ** -9 * A + 2.0 ** 14 * lost * (V + o.abs())
     over = (got.double() - o).abs() - (tol + 2.0 ** -8 * (o.abs() + tol))
     assert over.max().item() <= 0, (over.max().item(), over.argmax().item() % D)
 
@@ -740,8 +743,20 @@ def assert_one_peak(got, o, A, V, drop, u_p, lost):
 def test_attention_e4m3_tails_of_long_contexts(drop, T, ctas, at, heads):
     """Weights about the steps of a weight's last part and below, whose share grows with the length:
     one position above a million others, many of them to a CTA."""
-    p, c, q, o, A, V = one_peak(api.E4M3, T, drop, heads, at, ctas)
-    assert_one_peak(attend(p, c, q, None, None, [T]), o, A, V, drop, 2.0 ** -11, 2.0 ** -26)
+    p, c, q, ref = one_peak(api.E4M3, T, drop, heads, at, ctas)
+    assert_one_peak(attend(p, c, q, None, None, [T]), ref, drop, 2.0 ** -11, 2.0 ** -26)
+
+
+@pytest.mark.parametrize("heads", [16, 64])
+@pytest.mark.parametrize("ctas,at", [(1, 9), (1, 999_990), (3, 700_000)])
+@pytest.mark.parametrize("drop", [24.5, 25.4, 26.1, 28.0])
+def test_attention_bf16_tails_of_long_contexts(drop, ctas, at, heads):
+    """bf16 weights have no steps to fall below, but the tensor cores align each product to the
+    accumulator: of 2^-25.4 beside one nothing is left, so a CTA that added a million of them to
+    one accumulator lost their 2.2 %."""
+    p, c, q, ref = one_peak(api.BF16, 1_000_000, drop, heads, at, ctas)
+    out = attend(p, c, q, None, None, [1_000_000])
+    assert_one_peak(out, ref, drop, 2.0 ** -8, 0.0)
 
 
 @pytest.mark.parametrize("kv", [api.BF16, api.E4M3], ids=["bf16", "e4m3"])
