@@ -259,6 +259,19 @@ def _run(name, index, stream, fn, *args):
         check(rc, name)
 
 
+def _new_like(x, stream):
+    """An uninitialised tensor as x that a call on `stream` (None: the current one) writes. It
+    comes from that stream's memory: a block that the current stream has let go of may still be
+    in use by what is queued there. Letting go of it waits for the current stream too, where the
+    caller is likely to read it."""
+    if stream is None or x.get_device() < 0:
+        return torch.empty_like(x, memory_format=torch.contiguous_format)
+    with torch.cuda.stream(stream):
+        out = torch.empty_like(x, memory_format=torch.contiguous_format)
+    out.record_stream(torch.cuda.current_stream(x.device))
+    return out
+
+
 def rope(params, x, pos, out=None, layout=ROPE_PAIRS, first=-1, inverse=False, stream=None):
     """Rotary embedding (csa2_rope): x [N, heads, channels] bf16 or fp32 with contiguous
     channels, pos [N] int32; out as x (None: a new tensor; x itself: in place).
@@ -268,9 +281,7 @@ def rope(params, x, pos, out=None, layout=ROPE_PAIRS, first=-1, inverse=False, s
     if fmt is None or len(shape) != 3:
         _fail("rope: x must be [N, heads, channels], bf16 or fp32")
     if out is None:
-        out = torch.empty_like(x, memory_format=torch.contiguous_format)
-        if stream is not None and x.get_device() >= 0:
-            out.record_stream(stream)
+        out = _new_like(x, stream)
     elif out.shape != shape or out.dtype is not dt:
         _fail("rope: out must have x's shape and type")
     N, heads, ch = shape

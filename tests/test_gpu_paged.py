@@ -949,6 +949,28 @@ def test_strides_of_single_rows_and_heads_do_not_count():
     assert torch.equal(got, ref)
 
 
+def test_a_new_tensor_on_a_side_stream_is_not_in_use_elsewhere():
+    """The current stream lets go of a block that work queued there has still to write; a call on a
+    side stream that waits for none of it must not get that block for its output."""
+    p, side = api.default_params(rope_dim=64), torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        x = torch.randn(4096, 8, 128, device=DEV)
+        pos = torch.arange(4096, dtype=torch.int32, device=DEV)
+        ref = api.rope(p, x, pos)
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    block = torch.empty_like(x)
+    torch.cuda._sleep(1)
+    block.fill_(1)  # (the kernels are loaded: nothing below waits for the device)
+    torch.cuda.synchronize()
+    torch.cuda._sleep(200_000_000)  # about a tenth of a second
+    block.fill_(7)
+    del block
+    got = api.rope(p, x, pos, stream=side)
+    torch.cuda.synchronize()
+    assert torch.equal(got, ref)
+
+
 def test_calls_name_what_they_refuse():
     p, c, q, sink = filled(api.BF16, 8, [20], 16, seed=51)
     small = torch.empty(256, dtype=torch.uint8, device=DEV)
