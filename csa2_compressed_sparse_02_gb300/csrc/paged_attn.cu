@@ -431,6 +431,9 @@ __device__ __forceinline__ float warp_max(float v) {
     return r;
 }
 
+// Every wait is decided by its whole warp: what follows one holds shuffles and TMEM accesses of all
+// 32 lanes, for which the others would wait forever if one had given up and left alone.
+
 // ---------------------------------------------------------------- producers
 // One warp copies the tile's rows box by box (rows of one page): bf16 straight into the
 // swizzled operand. Boxes that hold nothing seen are left out.
@@ -489,11 +492,8 @@ __device__ void tma_role(Shared<kBf16, NH>& sh, const Args& a, const CUtensorMap
         const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, cur.mine)) * a.box_rows * 128 * kChunks;
         for (int pr = 0; pr < 4; ++pr, ++g) {
             const int slot = g % kPairs;
-            if (g >= kPairs && !mbar_wait(&sh.empty[slot], (uint32_t)((g / kPairs - 1) & 1), abort)) gave_up = true;
-            if (__any_sync(0xffffffffu, gave_up)) {
-                gave_up = true;
-                break;
-            }
+            gave_up = g >= kPairs && !mbar_wait_warp(&sh.empty[slot], (uint32_t)((g / kPairs - 1) & 1), abort);
+            if (gave_up) break;
             if (pr == 0) {  // four rows a lane: their bits to bytes
                 const uint32_t w = lane < 16 ? (lane < 8 ? cur.rows[0] : cur.rows[1]) : lane < 24 ? cur.rows[2] : cur.rows[3];
                 *reinterpret_cast<uint32_t*>(&sh.row_ok[gt & 3][4 * lane]) =
@@ -536,8 +536,7 @@ __device__ void query_role(Shared<true, NH>& sh, const Args& a, int pt, int lane
     Pieces pi(sh.range, Shape<true, NH>::kRun);
     Piece pc;
     for (int it = 0; pi.next(a, pc); ++it) {
-        if (it > 0 && !mbar_wait(&sh.q_empty, (uint32_t)((it - 1) & 1), abort)) return;
-        __syncwarp();
+        if (it > 0 && !mbar_wait_warp(&sh.q_empty, (uint32_t)((it - 1) & 1), abort)) return;
         const __nv_bfloat16* src = a.q + pc.b * a.q_seq + hb * a.q_head + 8 * u;
         const uint32_t dst = smem_u32(sh.q[u >> 3]);
 #pragma unroll 4
@@ -572,8 +571,7 @@ __device__ void query_role(Shared<false, NH>& sh, const Args& a, int pt, int lan
     Pieces pi(sh.range, Shape<false, NH>::kRun);
     Piece pc;
     for (int it = 0; pi.next(a, pc); ++it) {
-        if (it > 0 && !mbar_wait(&sh.q_empty, (uint32_t)((it - 1) & 1), abort)) return;
-        __syncwarp();
+        if (it > 0 && !mbar_wait_warp(&sh.q_empty, (uint32_t)((it - 1) & 1), abort)) return;
 #pragma unroll 1
         for (int h1 = pw; h1 < NH; h1 += kWarps * kAtOnce) {
             uint4 w2[kAtOnce][2];
@@ -930,7 +928,7 @@ __device__ void softmax_role(Shared<kBf16, NH>& sh, const Args& a, uint32_t tmem
                 w[2 * k] = h2_sub(w[2 * k], h2_sub(x0, __byte_perm(o[2][k], 0u, 0x1404)));
                 w[2 * k + 1] = h2_sub(w[2 * k + 1], h2_sub(x1, __byte_perm(o[2][k], 0u, 0x3424)));
             }
-            if (gt > 0 && !mbar_wait(&sh.pv_done, (uint32_t)((gt - 1) & 1), abort)) return false;
+            if (gt > 0 && !mbar_wait_warp(&sh.pv_done, (uint32_t)((gt - 1) & 1), abort)) return false;
 #pragma unroll
             for (int i = 0; i < 3; ++i)
 #pragma unroll
@@ -949,15 +947,15 @@ __device__ void softmax_role(Shared<kBf16, NH>& sh, const Args& a, uint32_t tmem
     Piece pc;
     int g = 0, gt = 0, moves = 0;
     for (int it = 0; pi.next(a, pc); ++it) {
-        if (!mbar_wait(&sh.q_full[it & 1], (uint32_t)((it >> 1) & 1), abort)) return;
+        if (!mbar_wait_warp(&sh.q_full[it & 1], (uint32_t)((it >> 1) & 1), abort)) return;
         float m_run = -INFINITY;  // running maximum of head h0 + mine
         float lpart[NC];          // this row's share of the sum of P
 #pragma unroll
         for (int i = 0; i < NC; ++i) lpart[i] = 0.f;
         for (int j = pc.j0; j < pc.j1; ++j, ++gt, g += 4) {
-            if (!mbar_wait(&sh.s_full[kBf16 ? 0 : gt & 1], (uint32_t)((kBf16 ? gt : gt >> 1) & 1), abort)) return;
+            if (!mbar_wait_warp(&sh.s_full[kBf16 ? 0 : gt & 1], (uint32_t)((kBf16 ? gt : gt >> 1) & 1), abort)) return;
             // (complete already: orders the read of row_ok after the producer's write)
-            if (!mbar_wait(&sh.full[g % S::kPairs], (uint32_t)((g / S::kPairs) & 1), abort)) return;
+            if (!mbar_wait_warp(&sh.full[g % S::kPairs], (uint32_t)((g / S::kPairs) & 1), abort)) return;
             tc_fence_after();
             const bool ok = sh.row_ok[gt & 3][r] != 0;
             // Rows that are not seen came with the box or are left from another tile: whatever
@@ -991,7 +989,7 @@ __device__ void softmax_role(Shared<kBf16, NH>& sh, const Args& a, uint32_t tmem
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sh.p_full);
                 // the MMA issuer goes on with this P unless a group found a larger logit
-                if (!mbar_wait(&sh.p_full, (uint32_t)(gt & 1), abort)) return;
+                if (!mbar_wait_warp(&sh.p_full, (uint32_t)(gt & 1), abort)) return;
                 any = any_moved(sh, gt);
                 move = *(volatile int*)&sh.moved[cg] == gt;
                 if (!move) {
@@ -1010,7 +1008,7 @@ __device__ void softmax_role(Shared<kBf16, NH>& sh, const Args& a, uint32_t tmem
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sh.max_bar[cg]);
-                if (!mbar_wait(&sh.max_bar[cg], (uint32_t)(moves++ & 1), abort)) return;
+                if (!mbar_wait_warp(&sh.max_bar[cg], (uint32_t)(moves++ & 1), abort)) return;
                 const float tm = fmaxf(fmaxf(sh.red_max[0][h0 + mine], sh.red_max[1][h0 + mine]),
                                        fmaxf(sh.red_max[2][h0 + mine], sh.red_max[3][h0 + mine]));
                 const float m_new = tm > m_run + S::kLazyMax ? tm : m_run;
@@ -1060,12 +1058,12 @@ __device__ void softmax_role(Shared<kBf16, NH>& sh, const Args& a, uint32_t tmem
                 if (lane == 0) mbar_arrive(&sh.p_again);
             }
         }
-        if (!mbar_wait(&sh.o_full, (uint32_t)(it & 1), abort)) return;
+        if (!mbar_wait_warp(&sh.o_full, (uint32_t)(it & 1), abort)) return;
         tc_fence_after();
         sh.red_sum[qd][h0 + mine] = warp_sum<NC>(lpart, lane);
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.sum_bar[cg]);
-        if (!mbar_wait(&sh.sum_bar[cg], (uint32_t)(it & 1), abort)) return;
+        if (!mbar_wait_warp(&sh.sum_bar[cg], (uint32_t)(it & 1), abort)) return;
         float l = (sh.red_sum[0][h0 + mine] + sh.red_sum[1][h0 + mine]) +
                   (sh.red_sum[2][h0 + mine] + sh.red_sum[3][h0 + mine]);
         m_run -= S::kLift;  // what P and O are relative to

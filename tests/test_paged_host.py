@@ -2,6 +2,7 @@
 refuse before anything is enqueued. The buffers are host memory, never dereferenced."""
 import ctypes
 import os
+import re
 
 import pytest
 import torch
@@ -171,3 +172,20 @@ def test_binding_refuses_tensors_the_pointers_would_not_stand_for():
                  lambda j: api.paged_attn(p, c, 0, q, None, j, i, torch.empty_like(q), i)):
         with pytest.raises(api.Csa2Error, match="CUDA"):  # nothing is enqueued for host tensors
             call(i)
+
+
+def test_waits_of_the_attention_kernel_are_decided_by_the_warp():
+    """A bounded wait can give up lane by lane. The roles go on with shuffles, votes and TMEM
+    accesses of the whole warp, so a lane that left alone would leave the others waiting without a
+    bound. By the source: every wait of a role votes, and none of a lane's own is left."""
+    csrc = os.path.join(os.path.dirname(_lib.LIB_PATH), "csrc")
+    code = {n: re.sub(r"//[^\n]*", "", open(os.path.join(csrc, n)).read()) for n in ("paged_attn.cu", "sm100.cuh")}
+    waits = re.findall(r"\bmbar_(?:try_)?(?:wait|test)\w*(?=\()", code["paged_attn.cu"])
+    # (a drain is the last thing a role does)
+    assert set(waits) == {"mbar_wait_warp", "mbar_wait_either_warp", "mbar_wait_drain"}
+    for name in ("mbar_wait_warp", "mbar_wait_either_warp"):
+        body = code["sm100.cuh"].split(name + "(", 1)[1].split("\n}\n", 1)[0]
+        tries = [line for line in body.split("\n") if "mbar_t" in line or "mbar_wait" in line]
+        assert tries and all(re.search(r"__(all|ballot)_sync\(0xffffffffu", line) for line in tries), name
+        returns = [line for line in body.split("\n") if "*abort" in line and "return" in line]
+        assert returns and all("__any_sync(0xffffffffu" in line for line in returns), name
