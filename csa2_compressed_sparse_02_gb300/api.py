@@ -212,8 +212,11 @@ def sparse_attn_noalloc(params, q, sink, win_ptrs, n_tokens, comp_ptrs, comp_sca
 # they hand them on; everything else is checked by the library. A decode step's kernels run
 # for a few microseconds each, so the checks are kept to what costs tenths of one.
 _FORMATS = {torch.bfloat16: BF16, torch.float32: F32}
-_raw_stream = torch._C._cuda_getCurrentRawStream  # of a device index, without a Stream object
-_current_device = torch._C._cuda_getDevice
+# Of a device index, without a Stream object. A torch built without CUDA has neither: the module
+# still imports there, for what needs no device.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _fail(what):

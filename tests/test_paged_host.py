@@ -3,6 +3,8 @@ refuse before anything is enqueued. The buffers are host memory, never dereferen
 import ctypes
 import os
 import re
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -189,3 +191,25 @@ def test_waits_of_the_attention_kernel_are_decided_by_the_warp():
         assert tries and all(re.search(r"__(all|ballot)_sync\(0xffffffffu", line) for line in tries), name
         returns = [line for line in body.split("\n") if "*abort" in line and "return" in line]
         assert returns and all("__any_sync(0xffffffffu" in line for line in returns), name
+
+
+def test_import_with_a_torch_built_without_cuda(L):
+    """Such a torch lacks the private calls of the fast path; the module imports, and what needs no
+    device works."""
+    code = """
+import torch
+for name in ("_cuda_getCurrentRawStream", "_cuda_getDevice"):
+    if hasattr(torch._C, name):
+        delattr(torch._C, name)
+from csa2_compressed_sparse_02_gb300 import api
+p = api.default_params(rope_dim=16)
+try:
+    api.rope(p, torch.zeros(2, 1, 16), torch.zeros(2, dtype=torch.int32))
+except api.Csa2Error as e:
+    assert "CUDA tensor" in str(e)
+else:
+    raise SystemExit("a host tensor was taken")
+"""
+    root = os.path.dirname(os.path.dirname(_lib.LIB_PATH))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr
