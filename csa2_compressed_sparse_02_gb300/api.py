@@ -21,7 +21,7 @@ from ._lib import Csa2Error, Pages, Params, check, lib  # noqa: F401
 
 F32, NVFP4, E4M3, BF16 = 0, 1, 2, 3
 WIN_RING, WIN_LINEAR = 0, 1
-ROPE_PAIRS, ROPE_HALF = 0, 1
+ROPE_PAIRS, ROPE_HALF, ROPE_CLEAR = 0, 1, 16
 D, H, HI, DI, W, BLK, KB, KP = 512, 64, 32, 128, 128, 8, 2048, 512
 KEY_TILE, KEY_TILE_BYTES = 128, 9216
 
@@ -278,6 +278,7 @@ def _new_like(x, stream):
 def rope(params, x, pos, out=None, layout=ROPE_PAIRS, first=-1, inverse=False, stream=None):
     """Rotary embedding (csa2_rope): x [N, heads, channels] bf16 or fp32 with contiguous
     channels, pos [N] int32; out as x (None: a new tensor; x itself: in place).
+    A row with pos < 0 is padding: zeros in a new tensor, left as it is in a given one.
     inverse=True turns back, which is also the gradient of the call. Returns out."""
     dt, shape = x.dtype, x.shape
     fmt = _FORMATS.get(dt)
@@ -285,6 +286,7 @@ def rope(params, x, pos, out=None, layout=ROPE_PAIRS, first=-1, inverse=False, s
         _fail("rope: x must be [N, heads, channels], bf16 or fp32")
     if out is None:
         out = _new_like(x, stream)
+        layout |= ROPE_CLEAR
     elif out.shape != shape or out.dtype is not dt:
         _fail("rope: out must have x's shape and type")
     N, heads, ch = shape

@@ -18,6 +18,7 @@ struct Args {
     const int32_t* pos;
     int64_t N, x_row, x_head, out_row, out_head;
     int heads, first, half;  // half: CSA2_ROPE_HALF
+    int clear;               // padding becomes zeros instead of being left as it is
     int rows_cta, heads_cta;
     int units, rot_units;    // per (row, head): units of work, the rotated ones first
     uint32_t units_magic, heads_magic;
@@ -136,7 +137,12 @@ k_rope(const __grid_constant__ Args a, const __grid_constant__ RopeTable tab) {
 #pragma unroll
         for (int k = 0; k < kBatch; ++k) {
             const Unit u = unit_of<V, kTwo>(a, tab.dim, base + k * kThreads, total, row0, head0, heads);
-            if (u.row < 0 || a.pos[u.row] < 0) continue;  // a padding row is left as it is
+            if (u.row < 0) continue;
+            if (a.pos[u.row] < 0) {  // padding
+                if (!a.clear) continue;
+                va[k] = VT{};
+                if constexpr (kTwo) vb[k] = VT{};
+            }
             T* dst = out + u.row * a.out_row + (int64_t)u.head * a.out_head + u.ch;
             if (u.pair >= 0) {
                 if constexpr (kTwo) {
@@ -228,6 +234,8 @@ extern "C" int csa2_rope(const csa2_params* p, int layout, int inverse, int64_t 
                          int64_t x_head, void* out, int64_t out_row, int64_t out_head,
                          const int32_t* pos, void* stream) {
     CSA2_CHECK_PARAMS(p);
+    const bool clear = (layout & CSA2_ROPE_CLEAR) != 0;
+    layout &= ~CSA2_ROPE_CLEAR;
     if (N < 0 || heads < 0) return fail(CSA2_ERR_INVALID_ARG, "rope: negative size");
     if (layout != CSA2_ROPE_PAIRS && layout != CSA2_ROPE_HALF)
         return fail(CSA2_ERR_UNSUPPORTED, "rope: layout must be PAIRS or HALF");
@@ -252,6 +260,7 @@ extern "C" int csa2_rope(const csa2_params* p, int layout, int inverse, int64_t 
     if (heads == 1) x_head = out_head = 0;
     if ((N > 1 && out_row == 0) || (heads > 1 && out_head == 0))
         return fail(CSA2_ERR_INVALID_ARG, "rope: rows or heads of out overlap");
+    if (x == out && clear) return fail(CSA2_ERR_INVALID_ARG, "rope: in place, padding stays as it is");
     if (x == out && (x_row != out_row || x_head != out_head))
         return fail(CSA2_ERR_INVALID_ARG, "rope: in place, x and out must have the same strides");
     if (const int rc = ensure_loaded()) return rc;
@@ -268,6 +277,7 @@ extern "C" int csa2_rope(const csa2_params* p, int layout, int inverse, int64_t 
     a.heads = heads;
     a.first = first;
     a.half = layout == CSA2_ROPE_HALF;
+    a.clear = clear;
     a.sign = inverse ? -1.f : 1.f;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const bool pl = layout == CSA2_ROPE_PAIRS;

@@ -522,12 +522,14 @@ int csa2_sparse_attn_noalloc(const csa2_params* p, int B,
  *           in elements; the channels are contiguous). out may be x itself (same strides:
  *           only the rotated channels are touched) and must not overlap it, or itself,
  *           otherwise.
- *   pos     [N] int32, device; a row with pos < 0 (padding) is left as it is in out.
+ *   pos     [N] int32, device; a row with pos < 0 (padding) is left as it is in out, with
+ *           CSA2_ROPE_CLEAR added to layout all its channels become zero (not in place).
  *   first   first rotated channel, or -1 for the last rope_dim channels.
  * Constraints: 2 <= rope_dim <= 512, even, first + rope_dim <= head_dim <= 4096; heads <= 4096.
  */
 #define CSA2_ROPE_PAIRS 0
 #define CSA2_ROPE_HALF 1
+#define CSA2_ROPE_CLEAR 16
 int csa2_rope(const csa2_params* p, int layout, int inverse, int64_t N, int heads, int head_dim,
               int first, int format, const void* x, int64_t x_row, int64_t x_head,
               void* out, int64_t out_row, int64_t out_head, const int32_t* pos, void* stream);

@@ -112,6 +112,31 @@ def test_rope_strided_views_padding_and_settings(layout, off):
         assert torch.all(dst[:, 5] == 7) and torch.all(dst[:, :, :4] == 7) and torch.equal(wide, before)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("layout", [api.ROPE_PAIRS, api.ROPE_HALF])
+@pytest.mark.parametrize("C,dim,first", [(128, 64, -1), (50, 20, 3), (64, 64, 0)])
+def test_rope_padding_of_a_new_tensor_is_zero(dtype, layout, C, dim, first):
+    """Not whatever its memory held: here NaN, which a block of the same size had before. Padded rows
+    of x may be NaN themselves."""
+    p = api.default_params(rope_dim=dim)
+    x, pos = randn(300, 5, C, seed=C, dtype=dtype), np.arange(300) * 7
+    pos[[0, 7, 8, 250, 299]] = -1
+    pad = torch.from_numpy(pos < 0).to(DEV)
+    x[7] = float("nan")
+    where, ref = i32(pos), torch.full_like(x, 5)
+    api.rope(p, x, where, out=ref, layout=layout, first=first)
+    assert torch.all(ref[pad] == 5)
+    for inverse in (False, True):
+        torch.cuda.synchronize()
+        torch.cuda.empty_cache()
+        block = torch.full_like(x, float("nan"))
+        del block
+        y = api.rope(p, x, where, layout=layout, first=first, inverse=inverse)
+        assert torch.all(y[pad] == 0)
+        if not inverse:
+            assert torch.equal(y[~pad], ref[~pad])
+
+
 @pytest.mark.parametrize("layout", [api.ROPE_PAIRS, api.ROPE_HALF])
 def test_rope_inverse_is_the_gradient(layout):
     """<dy, J x'> = <J^T dy, x'> with J^T the inverse call, and differences of the call."""

@@ -63,6 +63,12 @@ def test_rope_refusals(L):
     assert L.csa2_rope(None, 0, 0, 1, 1, 64, -1, api.BF16, A, 64, 64, A, 64, 64, A, None) == INVALID
 
 
+def test_rope_in_place_keeps_its_padding(L):
+    assert rope(L, params(rope_dim=64), layout=16, out=A) == INVALID
+    for layout in (18, 32, 3, -1):
+        assert rope(L, params(rope_dim=64), layout=layout) == UNSUPPORTED, layout
+
+
 def calls(L, p, c, ws=A, n=1 << 30):
     """Every call on a cache, with sound arguments of its own."""
     p, c = ctypes.byref(p), ctypes.byref(c) if c is not None else None
