@@ -10,13 +10,14 @@
 // of DRAM reads for two sequences of 65,536). Shared memory: a tile of 64 heads moves 530 KB
 // through it in bf16 (128 in, 192 for each product, P), 4.1k cycles at 128 bytes a cycle; and
 // as one tile and the query fill it (208 KB), a tile's softmax stands between its two products,
-// about 1.2k cycles in which nothing else can run. 16 sequences of 131,072 in bf16: 324 us with
-// 16 heads (6.6 TB/s, 0.98 of the measured copy rate), 352 with 64 (6.1 TB/s, 0.90; 330 with
-// every page in L2, 5.3k cycles a tile). E4M3: 291 us with 64 heads, 213 with up to 32 (3.7 and
-// 5.0 TB/s; the rows decoded into f16 operands instead: 419 and 346). The MMAs, 64 a tile, take
+// about 1.2k cycles in which nothing else can run. 16 sequences of 131,072 in bf16: 326 us with
+// 16 heads (6.6 TB/s, 0.97 of the measured copy rate), 354 with 64 (6.1 TB/s, 0.90; 330 with
+// every page in L2, 5.3k cycles a tile). E4M3: 289 us with 64 heads, 209 with up to 32 (3.7 and
+// 5.1 TB/s; the rows decoded into f16 operands instead: 419 and 346). The MMAs, 64 a tile, take
 // 3.4k of its 5.0k cycles with 64 heads: two tiles fit beside the query's two parts and P's
 // three, and a place that PV frees is filled 1.5k to 2k cycles later, so the tensor cores wait
-// now for the softmax, now for the copy.
+// now for the softmax, now for the copy. The builds with 64 heads use all 128 registers a thread
+// and spill a little beside them: 24 bytes in bf16, 52 in E4M3.
 //
 // Schedule, from the lengths on the device. The positions a sequence sees lie in tiles of 128
 // (its first tokens' tiles, then those from the window's start to its end).
@@ -26,7 +27,8 @@
 //    batch are cut into one contiguous range of equal length per CTA.
 // A sequence in one piece is finished by its CTA; of a cut one every piece leaves a partial
 // result (unnormalised O, running maximum m and sum l of each head), and k_paged_join joins
-// them in order: o = sum_i O_i 2^{m_i - M} / (2^{sink - M} + sum_i l_i 2^{m_i - M}).
+// them in order: o = sum_i O_i 2^{m_i - M} / (2^{sink - M} + sum_i l_i 2^{m_i - M}). Within a CTA
+// the runs of a long piece (see Shape::kRun) are joined by the same rule.
 #include <cuda.h>
 
 #include <atomic>

@@ -62,8 +62,8 @@ inline bool rope_settings_ok(const csa2_params* p) {
 // Cosine and sine of `pos` positions at `turns` a position. The product is exact modulo whole
 // turns in 64-bit integers (GB300's fp64 rate, two lanes a cycle and SM, would bound the
 // kernels here: 19 us against 11 for 16,004 rows of csa2_page_write). The quarter turns are
-// taken off; the rest, at most an eighth of a turn, keeps 32 bits behind the point (2^-33 turns
-// off) and 24 bits in fp32.
+// taken off; the rest, at most an eighth of a turn, keeps 32 bits behind the point (cut off there:
+// up to 2^-32 turns low) and 24 bits in fp32.
 __device__ __forceinline__ float2 rope_cs(uint64_t turns, int pos) {
     const uint64_t t = turns * (uint64_t)(uint32_t)pos;
     const uint32_t quarters = (uint32_t)((t + (1ull << 61)) >> 62);

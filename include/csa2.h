@@ -657,8 +657,9 @@ size_t csa2_paged_attn_workspace_size(const csa2_params* p, const csa2_pages* c,
  * are multiples of 2^-25 of the largest, else the nearest such multiple, again in both. The
  * tensor cores leave out of a product what lies below 2^-25 of its accumulator. At most 16,384
  * positions are added up so, and longer pieces joined from such runs in fp32: of a long tail at
- * most 2^-11 of the weight is lost (E4M3 2^-11 + 2^-12), whatever the length. A query is the sum of two E4M3 values under a power of two per head: exact down to 2^-14 of the head's
- * largest value, to 2^-22 of it below; a head whose query holds an infinity gives NaN.
+ * most 2^-11 of the weight is lost (E4M3 2^-11 + 2^-12), whatever the length. With E4M3 pages a
+ * query is the sum of two E4M3 values under a power of two per head: exact down to 2^-14 of the
+ * head's largest value, to 2^-22 of it below; a head whose query holds an infinity gives NaN.
  * A batch of at most as many sequences as CTAs (one per SM, or p->max_ctas) is cut into pieces
  * of nearly equal length, one per CTA, where that leaves few CTAs idle; else into equal ranges
  * of tiles of 128 positions. A second kernel joins the sequences that were cut, in the order of
