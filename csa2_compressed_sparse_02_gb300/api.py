@@ -267,11 +267,12 @@ def _new_like(x, stream):
     comes from that stream's memory: a block that the current stream has let go of may still be
     in use by what is queued there. Letting go of it waits for the current stream too, where the
     caller is likely to read it."""
-    if stream is None or x.get_device() < 0:
+    here = None if stream is None or x.get_device() < 0 else torch.cuda.current_stream(x.device)
+    if here is None or here == stream:
         return torch.empty_like(x, memory_format=torch.contiguous_format)
     with torch.cuda.stream(stream):
         out = torch.empty_like(x, memory_format=torch.contiguous_format)
-    out.record_stream(torch.cuda.current_stream(x.device))
+    out.record_stream(here)
     return out
 
 
