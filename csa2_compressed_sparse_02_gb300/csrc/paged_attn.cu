@@ -317,16 +317,17 @@ struct Shape {
     }
     // P = 2^(x - m + kLift), x - m <= kLazyMax before the maximum has to move. E5M2 ends at
     // 1.75 x 2^15 and holds small values as multiples of 2^-16, half a step off at most: with
-    // the largest weight at 2^9 or more, 2^-26 of it (see kRun). (A kLazyMax of 3 would make that 2^-29, but
-    // logits of a standard deviation of 3 in log2 then move the maximum in 4 of the first 8 tiles,
-    // with 6 in 2.)
+    // the largest weight at 2^9 or more, 2^-26 of it (see kRun). (A kLazyMax of 3 would make that
+    // 2^-29, but logits of a standard deviation of 3 in log2 then move the maximum in 4 of the first
+    // 8 tiles, with 6 in 2.)
     static constexpr float kLazyMax = kBf16 ? 8.0f : 6.0f;
     static constexpr float kLift = kBf16 ? 0.f : 9.f;
     // Tiles that add up in TMEM under one maximum; those that follow start anew, and what came
     // before is added in fp32. The tensor cores align each product to the accumulator and leave out
     // what lies below 2^-25 of it, and E4M3's parts end at 2^-26: with a million positions at
     // 2^-26.1 of one before them in one accumulator, their 1.4 % of the weight were lost. Of
-    // 16,384 positions it is at most 2^-11 (E4M3 another 2^-12), whatever the length. An end costs
+    // 16,384 positions it is below 2^-10 in bf16 (2^-25 a product and 2^-23 a sum of 16 of them) and
+    // below 2^-9 in E4M3 (three products, and 2^-26 of the parts), whatever the length. An end costs
     // 12 to 15 us with 64 heads and 6 with up to 32, for the partial result through L2 and a
     // pipeline that starts again: 16 x 131,072, 108 tiles a CTA, in E4M3 293 us with runs of 128,
     // 305 of 64, 318 of 36, in bf16 355 and 370.

@@ -656,8 +656,8 @@ size_t csa2_paged_attn_workspace_size(const csa2_params* p, const csa2_pages* c,
  * denominator alike. With E4M3 pages f16 weights are sums of three E5M2 values: exact where they
  * are multiples of 2^-25 of the largest, else the nearest such multiple, again in both. The
  * tensor cores leave out of a product what lies below 2^-25 of its accumulator. At most 16,384
- * positions are added up so, and longer pieces joined from such runs in fp32: of a long tail at
- * most 2^-11 of the weight is lost (E4M3 2^-11 + 2^-12), whatever the length. With E4M3 pages a
+ * positions are added up so, and longer pieces joined from such runs in fp32: of a long tail
+ * less than 2^-9 of the weight is lost, whatever the length. With E4M3 pages a
  * query is the sum of two E4M3 values under a power of two per head: exact down to 2^-14 of the
  * head's largest value, to 2^-22 of it below; a head whose query holds an infinity gives NaN.
  * A batch of at most as many sequences as CTAs (one per SM, or p->max_ctas) is cut into pieces
