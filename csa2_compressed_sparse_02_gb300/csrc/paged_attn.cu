@@ -29,21 +29,19 @@
 // result (unnormalised O, running maximum m and sum l of each head), and k_paged_join joins
 // them in order: o = sum_i O_i 2^{m_i - M} / (2^{sink - M} + sum_i l_i 2^{m_i - M}). Within a CTA
 // the runs of a long piece (see Shape::kRun) are joined by the same rule.
-#include <cuda.h>
-
-#include <atomic>
 #include <climits>
 
+#include "attn.cuh"
 #include "pages.cuh"
 #include "sm100.cuh"
 
 namespace csa2 {
 namespace {
 using namespace sm100;
+using namespace attn;
 
 constexpr int kTile = 128;
 constexpr int kMaxHeads = 64;
-constexpr float kLog2e = 1.4426950408889634f;
 
 struct Args {
     Pages g;
@@ -101,22 +99,6 @@ __device__ __forceinline__ View view_of(const Args& a, int b, bool report) {
     return v;
 }
 
-// The ranges: n = min(CTAs, items) of them, the first `total % n` one item longer.
-struct Cut {
-    int64_t base;
-    int n, rem;
-    __device__ __forceinline__ Cut(int64_t total, int ctas) {
-        n = (int)min((int64_t)ctas, total);
-        base = n ? total / n : 0;
-        rem = n ? (int)(total - base * n) : 0;
-    }
-    __device__ __forceinline__ int64_t at(int c) const { return c * base + min(c, rem); }  // c = 0 .. n
-    __device__ __forceinline__ int holder(int64_t item) const {
-        const int64_t big = rem * (base + 1);
-        return (int)(item < big ? item / (base + 1) : rem + (item - big) / base);
-    }
-};
-
 // The partial result of a piece of CTA c: slot 0 if the piece opens the CTA's range, else 1.
 __device__ __forceinline__ float* part_of(const Args& a, int c, int slot) {
     return a.part + (2 * (int64_t)c + slot) * part_floats(a.heads);
@@ -136,17 +118,6 @@ __device__ __forceinline__ int2 pieces_of(int c0, int c1, bool opens) {
 
 constexpr int kPlanWarps = 32;  // at most
 constexpr int kPlanSeqs = 255;  // sequences the first schedule plans for
-
-// Sum over the warp, and with it the sum over the lanes before this one.
-__device__ __forceinline__ uint32_t warp_scan(uint32_t v, int lane) {
-    uint32_t inc = v;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t up = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += up;
-    }
-    return inc - v;
-}
 
 // One piece per CTA leaves CTAs idle where the sequences do not divide well; equal ranges do
 // not, but give most CTAs a second piece, whose query, first tile and partial result cost about
@@ -268,12 +239,6 @@ __device__ void plan_ranges(const Args& a, Range* sh) {
 __device__ void plan(const Args& a, Range* sh) {
     if (a.B <= a.ctas && a.B <= kPlanSeqs && plan_pieces(a, sh)) return;
     plan_ranges(a, sh);
-}
-
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
-    return y;
 }
 
 // ---------------------------------------------------------------- shapes
@@ -426,14 +391,6 @@ __device__ __forceinline__ int page_of(const Args& a, const int32_t* table, uint
     return -1;
 }
 
-__device__ __forceinline__ uint32_t sw128(int row, int unit) { return (uint32_t)(row * 128 + ((unit ^ (row & 7)) << 4)); }
-
-__device__ __forceinline__ float warp_max(float v) {
-    float r;
-    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;\n" : "=f"(r) : "f"(v));
-    return r;
-}
-
 // Every wait is decided by its whole warp: what follows one holds shuffles and TMEM accesses of all
 // 32 lanes, for which the others would wait forever if one had given up and left alone.
 
@@ -556,17 +513,6 @@ __device__ void query_role(Shared<true, NH>& sh, const Args& a, int pt, int lane
 // largest |q| in [2^7, 2^8): hi holds 4 bits, what is left is at most 2^-5 of 2^8 and lo = 2^5
 // times it holds the other 4, exactly down to 2^-14 of the largest, to 2^-22 of it below. The
 // factor goes into the logit scale. E4M3 has no infinity: one in the query becomes NaN.
-__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
-    uint16_t r;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;\n" : "=h"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-__device__ __forceinline__ float2 e4m3x2_to_float2(uint32_t v) {
-    uint32_t h;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;\n" : "=r"(h) : "h"((uint16_t)v));
-    return __half22float2(*reinterpret_cast<const __half2*>(&h));
-}
-
 template <int NH>
 __device__ void query_role(Shared<false, NH>& sh, const Args& a, int pt, int lane, volatile int* abort) {
     constexpr int kWarps = Shape<false, NH>::kHelpWarps, kAtOnce = 4;  // heads whose loads are in flight together
@@ -825,20 +771,6 @@ __device__ __forceinline__ float warp_sum(float* v, int lane) {
 #pragma unroll
     for (int o = NC; o < 32; o <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
     return s;
-}
-
-__device__ __forceinline__ uint32_t h2_sub(uint32_t x, uint32_t y) {
-    const __half2 d = __hsub2(*reinterpret_cast<const __half2*>(&x), *reinterpret_cast<const __half2*>(&y));
-    return *reinterpret_cast<const uint32_t*>(&d);
-}
-// Four E5M2 of halves (x.lo, x.hi, y.lo, y.hi); E5M2 is the upper byte of f16.
-__device__ __forceinline__ uint32_t h2x2_to_e5m2x4(uint32_t x, uint32_t y) {
-    uint32_t r;
-    asm("{\n .reg .b16 lo, hi;\n cvt.rn.satfinite.e5m2x2.f16x2 lo, %1;\n cvt.rn.satfinite.e5m2x2.f16x2 hi, %2;\n"
-        " mov.b32 %0, {lo, hi};\n}"
-        : "=r"(r)
-        : "r"(x), "r"(y));
-    return r;
 }
 
 // Warp (qd, cg): positions 32 qd + lane of the tile, heads cg NC .. + NC - 1. Logits are in
@@ -1303,44 +1235,10 @@ __global__ void __launch_bounds__(Join<kWide>::kThreads, 1) k_paged_join(Args a)
         make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
 }
 
-// CTAs of the attention kernel on the current device: one per SM (asked for once a device),
-// at most max_ctas. 0: no device.
+// CTAs of the attention kernel on the current device: one per SM, at most max_ctas. 0: no device.
 int grid_of(const csa2_params* p) {
-    static std::atomic<int> sms[64];
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) return 0;
-    int n = dev < 64 ? sms[dev].load(std::memory_order_relaxed) : 0;
-    if (!n) {
-        if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
-        if (dev < 64) sms[dev].store(n, std::memory_order_relaxed);
-    }
-    if (n > kMaxCtas) n = kMaxCtas;
+    const int n = min(sm_count(), kMaxCtas);
     return p->max_ctas > 0 && p->max_ctas < n ? p->max_ctas : n;
-}
-
-// The layer's rows as a 2-d tensor map, whose boxes are box_rows rows x 128 bytes, laid out in
-// the 128-byte swizzle of the MMA operands. The driver's encoder is looked up once.
-int encode_rows(const Args& a, CUtensorMap* m) {
-    using Encode = decltype(&cuTensorMapEncodeTiled);
-    static Encode encode = [] {
-        void* f = nullptr;
-        cudaDriverEntryPointQueryResult r;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &r) != cudaSuccess ||
-            r != cudaDriverEntryPointSuccess)
-            f = nullptr;
-        return reinterpret_cast<Encode>(f);
-    }();
-    if (!encode) return fail(CSA2_ERR_CUDA, "paged_attn: the driver has no cuTensorMapEncodeTiled");
-    const bool bf16 = a.g.row_bytes == 2 * kD;
-    const cuuint64_t dims[2] = {kD, (cuuint64_t)a.g.n_pages * a.g.page_size};
-    const cuuint64_t strides[1] = {(cuuint64_t)a.g.row_bytes};
-    const cuuint32_t box[2] = {bf16 ? 64u : 128u, (cuuint32_t)a.box_rows}, steps[2] = {1, 1};
-    if (encode(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 2,
-               const_cast<uint8_t*>(a.base), dims, strides, box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
-               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
-               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-        return fail(CSA2_ERR_CUDA, "paged_attn: tensor map of the pool");
-    return CSA2_OK;
 }
 
 template <bool kBf16, int NH>
@@ -1427,7 +1325,7 @@ extern "C" int csa2_paged_attn(const csa2_params* p, const csa2_pages* c, int la
     if (a.box_rows > kTile) a.box_rows = kTile;
     while ((1 << a.box_shift) < a.box_rows) ++a.box_shift;
     CUtensorMap rows = {};
-    if (const int rc = encode_rows(a, &rows)) return rc;
+    if (const int rc = encode_rows("paged_attn", a.g, a.base, a.box_rows, &rows)) return rc;
     cudaLaunchConfig_t cfg = {};
     cfg.stream = static_cast<cudaStream_t>(stream);
     cudaLaunchAttribute attr[1];
