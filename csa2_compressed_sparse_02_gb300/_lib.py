@@ -74,6 +74,8 @@ SIGNATURES = {
     "csa2_page_write": (I32, [PP, GP, I32, I64, P, I32, I64, P, P, P, P]),
     "csa2_paged_attn_workspace_size": (SZ, [PP, GP, I32]),
     "csa2_paged_attn": (I32, [PP, GP, I32, I32, P, I64, I64, P, P, P, I32, I32, P, P, SZ, P, P]),
+    "csa2_paged_attn_shared_workspace_size": (SZ, [PP, GP, I32]),
+    "csa2_paged_attn_shared": (I32, [PP, GP, I32, I32, P, I64, I64, P, P, P, P, P, P, P, P, SZ, P, P]),
     "csa2_fp4_mma_peak": (I32, [I32, I32, P, P]),
 }
 

@@ -392,6 +392,40 @@ def paged_attn(params, cache, layer, q, sink, seq, n_tokens, out, workspace, win
          _status(dev_status, dev))
 
 
+def paged_attn_shared_workspace(params, cache, B):
+    """Workspace tensor of paged_attn_shared, for batches of any size."""
+    if cache.index < 0:
+        _fail("expected a CUDA tensor")
+    with torch.cuda.device(cache.index):
+        n = lib().csa2_paged_attn_shared_workspace_size(params, cache.c, B)
+    return torch.empty(max(int(n), 256), dtype=torch.uint8, device=cache.device)
+
+
+def paged_attn_shared(params, cache, layer, q, sink, seq, n_tokens, groups, out, workspace,
+                      dev_status=None, stream=None):
+    """paged_attn (without a window) of a batch whose sequences share prefixes as `groups`
+    (PrefixGroups) says: each shared position is read once for its group
+    (csa2_paged_attn_shared)."""
+    shape = q.shape
+    if len(shape) != 3 or q.dtype is not torch.bfloat16 or shape[2] != D or q.stride(2) != 1:
+        _fail("paged_attn_shared: q must be [B, heads, %d] bf16 with contiguous channels" % D)
+    B, heads, _ = shape
+    if heads != params.heads:
+        _fail("paged_attn_shared: q has %d heads, the parameters say %d" % (heads, params.heads))
+    if out.shape != shape or out.dtype is not torch.bfloat16 or not out.is_contiguous():
+        _fail("paged_attn_shared: out must be contiguous bf16 of q's shape")
+    if sink is not None and (sink.dtype is not torch.float32 or sink.numel() != heads or not sink.is_contiguous()):
+        _fail("paged_attn_shared: sink must be %d contiguous fp32 values" % heads)
+    _rows_of(params, cache)
+    dev = cache.index
+    _run("paged_attn_shared", dev, stream, lib().csa2_paged_attn_shared, params, cache.c, layer, B,
+         _at("q", q, dev), q.stride(0), q.stride(1), None if sink is None else _at("sink", sink, dev),
+         None if seq is None else _i32("seq", seq, B, dev), _i32("n_tokens", n_tokens, B, dev),
+         _i32("groups.order", groups.order, B, dev), _i32("groups.first", groups.first, B, dev),
+         _i32("groups.shared", groups.shared, B, dev), _at("out", out, dev), _at("workspace", workspace, dev),
+         workspace.nbytes, _status(dev_status, dev))
+
+
 def fp4_mma_peak(ctas, iters, dev_status=None, stream=None):
     """Enqueue the FP4 tensor-core rate measurement (csa2_fp4_mma_peak): ctas x iters
     MMA pairs of 2 x 128 x 128 x 128 flop each. The caller times it."""
@@ -508,6 +542,22 @@ class PagedCache:
         n = lib().csa2_page_workspace_size(self.c)
         self.workspace = torch.empty(max(int(n), 256), dtype=torch.uint8, device=self.device)
         self.ws_ptr, self.ws_bytes = self.workspace.data_ptr(), self.workspace.numel()
+
+
+class PrefixGroups:
+    """Which sequences of a batch share leading positions (csa2_prefix_groups): order, first and
+    shared [B] int32, allocated here for B sequences or the caller's own. Slot i of the batch's
+    order is sequence order[i]; its group begins at slot first[i] and shares shared[i] positions."""
+
+    def __init__(self, B=0, device="cuda", order=None, first=None, shared=None):
+        given = [t for t in (order, first, shared) if t is not None]
+        if len(given) not in (0, 3):
+            _fail("PrefixGroups: order, first and shared come together")
+        if not given:
+            order, first, shared = torch.empty(3, B, dtype=torch.int32, device=device).unbind(0)
+        for name, t in (("order", order), ("first", first), ("shared", shared)):
+            _i32(name, t, order.numel(), order.get_device())
+        self.order, self.first, self.shared = order, first, shared
 
 
 def n_blocks(n: int) -> int:

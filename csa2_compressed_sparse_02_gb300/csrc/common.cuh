@@ -58,6 +58,7 @@ cudaError_t preload_peak();
 cudaError_t preload_rope();
 cudaError_t preload_pages();
 cudaError_t preload_paged_attn();
+cudaError_t preload_paged_shared();
 
 // Single-layer sparse attention (csa2_sparse_attn, quantised formats) on the
 // tcgen05 kernel of sparse_attn_tc.cu with the even split schedule; the

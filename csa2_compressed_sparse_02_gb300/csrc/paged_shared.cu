@@ -1,0 +1,1182 @@
+// csa2_paged_attn_shared: csa2_paged_attn for a batch in which groups of sequences share their
+// leading positions. The rows of a group's sequences (a row: a head of a sequence) meet a shared
+// position together, so it is read once for up to 128 rows.
+//
+// A unit is up to 128 rows of one group: floor(128 / heads) sequences. It walks the tiles of 128
+// positions of the shared prefix, which all its rows see, then those of each sequence's own
+// positions, which only that sequence's rows see (the others' weights are zero there). With the
+// rows as the MMA's M, over a pair of CTAs (tcgen05, cta_group::2, fp32 in TMEM):
+//   S[128 x 128] = Q . K_tile^T,   P = 2^(S - m),   O[128 x 512] += P . V_tile
+// CTA c of the pair has rows 64 c .. 64 c + 63 of Q, S, P and O. The pair shares the other operand:
+// for S, CTA c brings positions 64 c .. + 63 with all their channels; for PV all 128 positions with
+// channels 256 h + 128 c .. + 127 of both halves h. These are two copies of the tile's bytes (an
+// operand's place in shared memory holds the same positions or channels in both CTAs, which differ
+// between the two products), so a CTA streams 1,024 bytes a position in bf16, and each place of the
+// ring comes free as soon as its own product has read it.
+#include <climits>
+
+#include "attn.cuh"
+#include "pages.cuh"
+#include "sm100.cuh"
+
+namespace csa2 {
+namespace {
+using namespace sm100;
+using namespace attn;
+
+constexpr int kTile = 128;      // positions
+constexpr int kRows = 128;      // of a unit
+constexpr int kMine = 64;       // of them a CTA's
+constexpr int kMaxHeads = 64;
+constexpr int kMaxPairs = 128;
+
+struct Args {
+    Pages g;
+    const uint8_t* base;  // the layer's first page
+    int B, heads, members;  // sequences a unit holds: kRows / heads
+    int64_t q_seq, q_head;
+    const __nv_bfloat16* q;
+    const float* sink;
+    const int32_t *seq, *n_tokens, *order, *first, *shared;
+    __nv_bfloat16* out;
+    int4* ends;       // workspace: of each pair, how its range ends and with which unit [pairs]
+    float* part;      // workspace: two partial results per pair
+    int32_t* dev_status;
+    float scale_log2;
+    int pairs;
+    int box_rows;     // rows of a copied box: a power of two, divides 64 and the page size
+};
+
+// How a pair's range ends: its last unit goes on behind it; is its only one; and began before it.
+enum { kCut = 1, kSingle = 2, kThrough = 4 };
+
+// A partial result: O as [512 / 4][128 rows] float4, then m [128] and l [128].
+constexpr int kPartFloats = kRows * (kD + 2);
+
+__device__ __forceinline__ float* part_of(const Args& a, int pair, int slot) {
+    return a.part + (2 * (int64_t)pair + slot) * kPartFloats;
+}
+
+// ---------------------------------------------------------------- the batch
+// Slot i of the order: sequence b of the call with T positions in row `row` of the table (T = 0:
+// nothing to see), in the group that begins at slot f and shares `sh` positions, which are read
+// through row `prow`.
+struct Slot {
+    int b, T, row, f, sh, prow;
+};
+
+__device__ __forceinline__ int row_of(const Args& a, int b, bool report) {
+    if (b < 0 || b >= a.B) {
+        if (report) raise_status(a.dev_status, CSA2_DEV_BAD_INDEX);
+        return -1;
+    }
+    const int row = a.seq ? a.seq[b] : b;
+    if (row < a.g.max_seqs) return row;
+    if (report) raise_status(a.dev_status, CSA2_DEV_BAD_INDEX);
+    return -1;
+}
+
+__device__ __forceinline__ int length_of(const Args& a, int64_t n, bool report) {
+    if (n >= 0 && n <= a.g.max_len()) return (int)n;
+    if (report) raise_status(a.dev_status, CSA2_DEV_BAD_LENGTH);
+    return n < 0 ? 0 : (int)a.g.max_len();
+}
+
+// The slot where i's group begins.
+__device__ __forceinline__ int first_of(const Args& a, int i, bool report) {
+    const int f = a.first[i];
+    if (f >= 0 && f <= i) return f;
+    if (report) raise_status(a.dev_status, CSA2_DEV_BAD_INDEX);
+    return i;
+}
+
+__device__ __forceinline__ Slot slot_of(const Args& a, int i, bool report) {
+    Slot s;
+    s.b = a.order[i];
+    s.f = first_of(a, i, report);
+    s.sh = length_of(a, a.shared[s.f], report && s.f == i);
+    s.row = row_of(a, s.b, report);
+    s.T = s.row < 0 ? 0 : length_of(a, a.n_tokens[s.b], report);
+    s.prow = row_of(a, a.order[s.f], false);
+    return s;
+}
+
+// The slot where the unit of slot i begins.
+__device__ __forceinline__ int unit_of(const Args& a, int i, int f) { return i - (i - f) % a.members; }
+
+__device__ __forceinline__ int tiles_of(int n) { return n / kTile + (n % kTile != 0); }
+
+// Tiles that slot i brings: the prefix's, if its unit begins with it, and its own positions'.
+__device__ __forceinline__ int prefix_tiles(const Args& a, const Slot& s, int i) {
+    return unit_of(a, i, s.f) == i ? tiles_of(s.sh) : 0;
+}
+__device__ __forceinline__ int own_tiles(const Slot& s) { return s.T > s.sh ? tiles_of(s.T) - s.sh / kTile : 0; }
+
+// ---------------------------------------------------------------- schedule
+// The batch's tiles, unit after unit, are cut into one contiguous range of equal length a pair.
+struct Range {
+    int64_t items;
+    int i, j;          // it begins with tile j of slot i
+    bool cont, cut;    // its first unit began before it; its last one ends behind it
+};
+
+struct PlanShared {
+    int64_t warp_sum[32];
+    long long begin, end;  // where the first tile's unit begins, and the last one's ends
+    Range range;
+};
+
+// Called by the whole CTA.
+__device__ void plan(const Args& a, PlanShared& sh, int pair) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
+    // Exclusive sum over the CTA of n < 2^26, and the sum of all.
+    auto scan = [&](uint32_t n, int64_t* all) {
+        const uint32_t before = warp_scan(n, lane);
+        if (lane == 31) sh.warp_sum[warp] = (int64_t)before + n;
+        __syncthreads();
+        const int64_t w = lane < warps ? sh.warp_sum[lane] : 0;
+        int64_t warps_before = lane < warp ? w : 0, sum = w;
+#pragma unroll
+        for (int o = 16; o >= 1; o >>= 1) {
+            warps_before += __shfl_xor_sync(0xffffffffu, warps_before, o);
+            sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        }
+        __syncthreads();
+        *all = sum;
+        return warps_before + before;
+    };
+    auto items_of = [&](int i, bool report, bool* head) -> uint32_t {
+        *head = false;
+        if (i >= a.B) return 0;
+        const Slot s = slot_of(a, i, report);
+        *head = unit_of(a, i, s.f) == i;
+        return (uint32_t)prefix_tiles(a, s, i) + own_tiles(s);
+    };
+    int64_t total = 0, all;
+    uint32_t n = 0;
+    bool head = false;
+    for (int i0 = 0; i0 < a.B; i0 += blockDim.x) {
+        n = items_of(i0 + tid, blockIdx.x == 0, &head);
+        scan(n, &all);
+        total += all;
+    }
+    const Cut ranges(total, a.pairs);
+    const int c = min(pair, ranges.n);
+    const int64_t at = ranges.at(c), end = ranges.at(min(c + 1, ranges.n));
+    if (tid == 0) {
+        sh.range.items = end - at;
+        sh.range.i = sh.range.j = 0;
+        sh.begin = 0;
+        sh.end = total;
+    }
+    __syncthreads();
+    int64_t before = 0;
+    for (int i0 = 0; i0 < a.B; i0 += blockDim.x) {
+        const int i = i0 + tid;
+        if (a.B > (int)blockDim.x) n = items_of(i, false, &head);
+        const int64_t here = before + scan(n, &all);
+        before += all;
+        if (at >= here && at < here + n) {
+            sh.range.i = i;
+            sh.range.j = (int)(at - here);
+        }
+        if (head && here <= at) atomicMax(&sh.begin, (long long)here);
+        if (head && here >= end) atomicMin(&sh.end, (long long)here);
+    }
+    __syncthreads();
+    if (tid == 0) {
+        sh.range.cont = sh.begin < at;
+        sh.range.cut = sh.end > end;
+    }
+    __syncthreads();
+}
+
+// A range tile by tile, by a whole warp: each lane holds one of 32 neighbouring slots.
+struct Tile {
+    int t0, lo, hi;  // positions t0 .. t0 + 127, of which [lo, hi) are seen
+    int row;         // of the table
+    int k;           // the sequence of the unit that sees it, -1: all
+    int u0, f;       // first slot of its unit and of its group
+};
+struct Walk {
+    const Args& a;
+    int64_t left;
+    int i, j, base;
+    Slot mine, s;  // of lane's slot, of slot i
+    int pre, items;
+    __device__ __forceinline__ Walk(const Args& a, const Range& r)
+        : a(a), left(r.items), i(r.i), j(r.j), base(-1) {
+        if (left > 0) enter();
+    }
+    __device__ __forceinline__ void enter() {
+        if ((i & ~31) != base) {
+            base = i & ~31;
+            const int at = base + (threadIdx.x & 31);
+            mine = at < a.B ? slot_of(a, at, false) : Slot{0, 0, -1, at, 0, -1};
+        }
+        const int l = i & 31;
+        s.T = __shfl_sync(0xffffffffu, mine.T, l);
+        s.row = __shfl_sync(0xffffffffu, mine.row, l);
+        s.f = __shfl_sync(0xffffffffu, mine.f, l);
+        s.sh = __shfl_sync(0xffffffffu, mine.sh, l);
+        s.prow = __shfl_sync(0xffffffffu, mine.prow, l);
+        pre = prefix_tiles(a, s, i);
+        items = pre + own_tiles(s);
+    }
+    __device__ __forceinline__ bool next(Tile& t) {
+        if (left <= 0) return false;
+        while (j >= items) {
+            ++i;
+            j = 0;
+            enter();
+        }
+        const bool own = j >= pre;
+        t.u0 = unit_of(a, i, s.f);
+        t.f = s.f;
+        t.t0 = kTile * (own ? s.sh / kTile + j - pre : j);
+        t.lo = own ? s.sh : 0;
+        t.hi = own ? s.T : s.sh;
+        t.row = own ? s.row : s.prow;
+        t.k = own ? i - t.u0 : -1;
+        ++j;
+        --left;
+        return true;
+    }
+};
+
+// What a row of a unit stands for: head `h` of sequence b (-1: nothing), which sees T positions.
+struct Row {
+    int b, h, k, T;
+};
+__device__ __forceinline__ Row row_info(const Args& a, int u0, int f, int r) {
+    Row x;
+    x.k = r / a.heads;
+    x.h = r - x.k * a.heads;
+    x.b = -1;
+    x.T = 0;
+    const int i = u0 + x.k;
+    if (x.k >= a.members || i >= a.B || first_of(a, i, false) != f) return x;
+    const int b = a.order[i];
+    if (b < 0 || b >= a.B) return x;
+    const int row = a.seq ? a.seq[b] : b;
+    if (row < 0) return x;  // padding: its output is left as it is
+    x.b = b;
+    if (row < a.g.max_seqs) x.T = length_of(a, a.n_tokens[b], false);
+    return x;
+}
+
+// ---------------------------------------------------------------- shapes
+// kBf16: bf16 pages, the products in bf16. Else E4M3 pages, whose bytes are the operand as they
+// are; what meets them is split into 8-bit parts that add up to it:
+//   q 2^s = hi + lo, both E4M3, with the largest |q| 2^s of a row in [2^7, 2^8): bf16's 8 bits
+//   down to 2^-10 of the largest, to 2^-18 of it below; both products into the same S;
+//   P in f16 = three parts in E5M2, each the nearest three bits of what is left.
+template <bool kBf16>
+struct Shape {
+    static constexpr int kSoftWarps = 8;
+    static constexpr int kMmaWarp = 8, kTmaWarp = 9, kHelp0 = 10, kHelpWarps = 4;
+    static constexpr int kThreads = 32 * (kHelp0 + kHelpWarps);
+    static constexpr uint32_t kChunk = kMine * 128;            // 64 rows x 128 bytes, 128-byte swizzle
+    static constexpr uint32_t kPlace = kBf16 ? 2 * kChunk : kChunk;  // 64 positions x 128 channels
+    static constexpr int kPlaces = kBf16 ? 8 : 16;
+    static constexpr uint32_t kIdesc = (1u << 4) | ((128u >> 4) << 24);  // D fp32, M = 128 over the pair
+    // N = 128 positions, both K-major; N = 256 channels, B MN-major. Types: bf16 1, E4M3 0, E5M2 1
+    static constexpr uint32_t kIdescS = kIdesc | ((128u >> 3) << 17) | (kBf16 ? (1u << 7) | (1u << 10) : 0u);
+    static constexpr uint32_t kIdescPV = kIdesc | ((256u >> 3) << 17) | (1u << 16) | (1u << 7) | (kBf16 ? 1u << 10 : 0u);
+    // P = 2^(x - m + kLift), and m moves only where P would pass 2^(kLazyMax + kLift). E5M2 ends at
+    // 1.75 x 2^15 and holds small values as multiples of 2^-16.
+    static constexpr float kLazyMax = kBf16 ? 8.f : 6.f;
+    static constexpr float kLift = kBf16 ? 0.f : 9.f;
+    // Tiles that add up in TMEM under one maximum (see csa2_paged_attn: of a long tail less than 2^-9
+    // of the weight is lost); what came before is added in fp32.
+    static constexpr int kRun = 128;
+};
+constexpr uint32_t kColO = 0, kColS = 256;  // TMEM: O 2 x 128 columns, S 2 x 64
+constexpr uint32_t kTmemCols = 512;         // one CTA an SM, so it takes them all
+
+constexpr int kInfos = 8;
+struct alignas(16) Info {
+    enum {
+        kFirst = 1, kLast = 2,    // of a run of at most kRun tiles
+        kBegins = 4, kEnds = 8,   // the run begins, ends what this pair has of the unit
+        kOpens = 16,              // which opens the pair's range
+        kWhole = 32,              // and is all of the unit (set with kEnds)
+        kStop = 64                // no tile: the range is done
+    };
+    int t0, lo, hi, k, u0, f, flags, pad;
+    uint32_t ok[4];  // the positions whose page exists
+};
+
+template <bool kBf16>
+struct Shared {
+    using S = Shape<kBf16>;
+    uint8_t ring[S::kPlaces][S::kPlace];
+    uint8_t q[8 * S::kChunk];
+    uint8_t p[(kBf16 ? 2 : 3) * S::kChunk];  // bf16: 64 positions each; E4M3: 128, a part each
+    float red_max[2][4][kMine];
+    float red_sum[4][kMine];
+    float row_scale[2][kMine];  // E4M3: logit factor, by run parity
+    Info info[kInfos];
+    uint64_t full[S::kPlaces], empty[S::kPlaces];
+    uint64_t peer_full[S::kPlaces];  // the even CTA's: the odd one's place is full
+    uint64_t info_full[kInfos];
+    uint64_t s_full[2], p_full, pv_done;
+    uint64_t q_full[2];   // the even CTA's: both CTAs' rows are staged; by run parity
+    uint64_t q_here[2];   // this CTA's are
+    uint64_t q_empty;
+    uint64_t max_bar[2], sum_bar[2];
+    uint64_t drain;
+    PlanShared plan;
+    uint32_t tmem_base;
+    int abort;
+};
+
+// An arrive on the even CTA's barrier, from either CTA of the pair.
+__device__ __forceinline__ void arrive_lead(uint64_t* bar, uint32_t rank) {
+    if (rank == 0) mbar_arrive(bar);
+    else mbar_arrive_cluster(mapa_shared(smem_u32(bar), 0));
+}
+
+// ---------------------------------------------------------------- copies
+// One warp walks the range, tells the other roles of each tile, and copies it box by box (rows of
+// one page). Boxes that hold nothing seen are copied from behind the pool's last row, which reads
+// as zeros: P is zero for them, and 0 x whatever the place held before might be NaN.
+// The places in order: K of a run's first tile; then, for each tile, K of the next one and V of it.
+template <bool kBf16>
+__device__ void tma_role(Shared<kBf16>& sh, const Args& a, const CUtensorMap* tmap, int lane, int rank, int pair,
+                         volatile int* abort) {
+    using S = Shape<kBf16>;
+    const int br = a.box_rows, ps = a.g.page_size, behind = a.g.n_pages * ps;
+    const int pos = lane * br;  // of this lane's box in the tile
+    const Range range = sh.plan.range;
+    Walk walk(a, range);
+    Tile cur = {}, nxt = {};
+    bool has = walk.next(cur), has_nx = has && walk.next(nxt);
+    int gt = 0, g = 0;  // tiles told of, places filled
+    int run = 0, runs = 0, pieces = 0;
+    auto tell = [&](const Tile& t, bool more) {  // returns the pool's row where this lane's box begins
+        const bool ends = !more || nxt.u0 != t.u0 || nxt.f != t.f;
+        const bool last = ends || run == S::kRun - 1;
+        int y = behind;
+        bool there = false;
+        if (pos < kTile && t.t0 + pos < t.hi && t.t0 + pos + br > t.lo) {
+            const int at = t.t0 + pos, page = t.row < 0 ? -1 : a.g.table[(int64_t)t.row * a.g.max_pages + at / ps];
+            there = page >= 0 && page < a.g.n_pages;
+            if (there) y = page * ps + at % ps;
+            else if (rank == 0) raise_status(a.dev_status, CSA2_DEV_BAD_INDEX);
+        }
+        const uint32_t held = __ballot_sync(0xffffffffu, there);
+        Info& o = sh.info[gt % kInfos];
+        if (lane < 4) {
+            uint32_t ok = 0;
+            for (int p = 0; p < 32; p += 8)  // (a box has at least eight rows)
+                if ((held >> ((32 * lane + p) / br)) & 1u) ok |= 0xffu << p;
+            o.ok[lane] = ok;
+        }
+        if (lane == 0) {
+            o.t0 = t.t0;
+            o.lo = t.lo;
+            o.hi = t.hi;
+            o.k = t.k;
+            o.u0 = t.u0;
+            o.f = t.f;
+            o.flags = (run == 0 ? Info::kFirst : 0) | (last ? Info::kLast : 0) | (runs == 0 ? Info::kBegins : 0) |
+                      (ends ? Info::kEnds : 0) | (pieces == 0 ? Info::kOpens : 0) |
+                      (ends && !(pieces == 0 && range.cont) && !(!more && range.cut) ? Info::kWhole : 0);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.info_full[gt % kInfos]);
+        ++gt;
+        ++run;
+        if (last) run = 0, ++runs;
+        if (ends) runs = 0, ++pieces;
+        return y;
+    };
+    const uint32_t ring = smem_u32(sh.ring[0]);
+    auto fill = [&](int y, int first, int x) {  // 64 positions from `first` of the tile, 128 channels from x
+        const int slot = g % S::kPlaces;
+        if (g >= S::kPlaces && !mbar_wait_warp(&sh.empty[slot], (uint32_t)((g / S::kPlaces - 1) & 1), abort)) return false;
+        if (lane == 0) mbar_arrive_expect_tx(&sh.full[slot], S::kPlace);
+        __syncwarp();
+        if (pos >= first && pos < first + kMine) {
+            const uint32_t dst = ring + slot * S::kPlace + (pos - first) * 128;
+            tma_g2s_2d(dst, tmap, x, y, &sh.full[slot]);
+            if constexpr (kBf16) tma_g2s_2d(dst + S::kChunk, tmap, x + 64, y, &sh.full[slot]);
+        }
+        ++g;
+        return true;
+    };
+    auto keys = [&](int y) {
+        for (int d = 0; d < 4; ++d)
+            if (!fill(y, kMine * rank, 128 * d)) return false;
+        return true;
+    };
+    auto values = [&](int y) {
+        for (int h = 0; h < 2; ++h)
+            for (int p = 0; p < 2; ++p)
+                if (!fill(y, kMine * p, 256 * h + 128 * rank)) return false;
+        return true;
+    };
+    int y = 0, y_nx = 0;
+    bool good = true, last = false;
+    Tile end = {};
+    if (has) {
+        y = tell(cur, has_nx);
+        last = run == 0;
+        good = keys(y);
+    }
+    while (has && good) {
+        const bool was_last = last, more = has_nx;
+        end = cur;
+        if (more) {
+            cur = nxt;
+            has_nx = walk.next(nxt);
+            y_nx = tell(cur, has_nx);
+            last = run == 0;
+        }
+        good = (was_last || keys(y_nx)) && values(y) && (!was_last || !more || keys(y_nx));
+        y = y_nx;
+        has = more;
+    }
+    if (lane == 0) {
+        sh.info[gt % kInfos].flags = Info::kStop;
+        mbar_arrive(&sh.info_full[gt % kInfos]);
+        // for the join: the unit that the range ends with, and whether it is cut there and before
+        if (rank == 0) {
+            const bool any = range.items > 0;
+            a.ends[pair] = make_int4(any ? (range.cut ? kCut : 0) | (pieces == 1 ? kSingle : 0) |
+                                               (pieces == 1 && range.cont ? kThrough : 0) : 0, end.u0, end.f, 0);
+        }
+    }
+    __syncwarp();
+    // whatever ended the loop, no copy of this CTA outlives it
+    for (int s = max(0, g - S::kPlaces); s < g; ++s)
+        mbar_wait_drain(&sh.full[s % S::kPlaces], (uint32_t)((s / S::kPlaces) & 1));
+}
+
+// ---------------------------------------------------------------- queries
+// Four warps stage this CTA's rows of the unit, once a run: warp w rows 16 w .. 16 w + 15.
+template <bool kBf16>
+__device__ void query_role(Shared<kBf16>& sh, const Args& a, int warp, int lane, int rank, volatile int* abort) {
+    using S = Shape<kBf16>;
+    constexpr int kEach = kMine / S::kHelpWarps;
+    Walk walk(a, sh.plan.range);
+    Tile t;
+    int it = 0, run = 0, u0 = -1, f = -1;
+    while (walk.next(t)) {
+        if (t.u0 == u0 && t.f == f && run < S::kRun) {
+            ++run;
+            continue;
+        }
+        u0 = t.u0;
+        f = t.f;
+        run = 1;
+        if (it > 0 && !mbar_wait_warp(&sh.q_empty, (uint32_t)((it - 1) & 1), abort)) return;
+        const Row mine = row_info(a, u0, f, kMine * rank + kEach * warp + (lane & (kEach - 1)));
+#pragma unroll 4
+        for (int i = 0; i < kEach; ++i) {
+            const int r = kEach * warp + i;
+            const int b = __shfl_sync(0xffffffffu, mine.b, i), h = __shfl_sync(0xffffffffu, mine.h, i);
+            const __nv_bfloat16* src = a.q + (b < 0 ? 0 : b * a.q_seq + h * a.q_head);
+            if constexpr (kBf16) {
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const int u = lane + 32 * x;
+                    cp_async_16(smem_u32(sh.q) + (u >> 3) * S::kChunk + sw128(r, u & 7), src + 8 * u, b >= 0);
+                }
+            } else {
+                uint4 w2[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
+                if (b >= 0) {
+                    w2[0] = __ldg(reinterpret_cast<const uint4*>(src) + 2 * lane);
+                    w2[1] = __ldg(reinterpret_cast<const uint4*>(src) + 2 * lane + 1);
+                }
+                const uint32_t w[8] = {w2[0].x, w2[0].y, w2[0].z, w2[0].w, w2[1].x, w2[1].y, w2[1].z, w2[1].w};
+                float mx = 0.f;
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(w[k] << 16)), fabsf(__uint_as_float(w[k] & 0xffff0000u))));
+                mx = warp_max(mx);
+                int s = 7 - ((int)((__float_as_uint(mx) >> 23) & 0xffu) - 127);
+                s = max(-126, min(126, s));
+                const float two_s = __uint_as_float((uint32_t)(s + 127) << 23);
+                uint32_t hi[4] = {}, lo[4] = {};
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    float x = __uint_as_float(w[k] << 16) * two_s, y = __uint_as_float(w[k] & 0xffff0000u) * two_s;
+                    x = fmaf(x, 0.f, x);  // infinity to NaN: E4M3 has none
+                    y = fmaf(y, 0.f, y);
+                    const uint32_t xy = e4m3x2(x, y);
+                    const float2 got = e4m3x2_to_float2(xy);
+                    hi[k >> 1] |= xy << (16 * (k & 1));
+                    lo[k >> 1] |= e4m3x2(x - got.x, y - got.y) << (16 * (k & 1));
+                }
+                uint8_t* q = sh.q + (lane >> 3) * S::kChunk + sw128(r, lane & 7);
+                *reinterpret_cast<uint4*>(q) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                *reinterpret_cast<uint4*>(q + 4 * S::kChunk) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                if (lane == 0) sh.row_scale[it & 1][r] = a.scale_log2 * __uint_as_float((uint32_t)(127 - s) << 23);
+            }
+        }
+        if constexpr (kBf16) cp_async_wait_all();
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+            mbar_arrive(&sh.q_here[it & 1]);
+            arrive_lead(&sh.q_full[it & 1], rank);
+        }
+        ++it;
+    }
+}
+
+// ---------------------------------------------------------------- MMAs
+// The even CTA's warp issues the pair's MMAs: S of a tile, then S of the next one before PV of this,
+// so that the tensor cores work while the softmax runs. The odd CTA's passes on that its places are
+// full.
+template <bool kBf16>
+__device__ void mma_role(Shared<kBf16>& sh, uint32_t tmem, volatile int* abort) {
+    using S = Shape<kBf16>;
+    const uint64_t dQ = smem_desc(smem_u32(sh.q), 16, 1024, kLayoutSw128);
+    const uint64_t dP = smem_desc(smem_u32(sh.p), 16, 1024, kLayoutSw128);
+    const uint64_t dK = smem_desc(smem_u32(sh.ring[0]), 16, 1024, kLayoutSw128);
+    const uint64_t dV = smem_desc(smem_u32(sh.ring[0]), S::kChunk, 1024, kLayoutSw128);
+    int slot = 0, it = 0;
+    uint32_t phase = 0;
+    auto landed = [&]() {
+        if (!mbar_wait_warp(&sh.full[slot], phase, abort)) return false;
+        if (!mbar_wait_cluster_warp(&sh.peer_full[slot], phase, abort)) return false;
+        tc_fence_after();
+        return true;
+    };
+    auto place = [&]() { return (uint64_t)__shfl_sync(0xffffffffu, (uint32_t)slot * (S::kPlace >> 4), 0); };
+    auto used = [&]() {
+        if (++slot == S::kPlaces) slot = 0, phase ^= 1u;
+    };
+    auto scores = [&](int gt, bool last) {
+        const uint32_t at = tmem + kColS + (uint32_t)__shfl_sync(0xffffffffu, gt & 1, 0) * 64u;
+#pragma unroll
+        for (int d = 0; d < 4; ++d) {
+            if (!landed()) return false;
+            const uint64_t k = dK + place();
+            if (elect_one()) {
+                if constexpr (kBf16) {
+#pragma unroll
+                    for (int c = 0; c < 2; ++c)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            mma_f16_pair(at, dQ + (((2 * d + c) * S::kChunk + 32 * i) >> 4),
+                                         k + ((c * S::kChunk + 32 * i) >> 4), S::kIdescS, (d | c | i) != 0);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+#pragma unroll
+                        for (int part = 0; part < 2; ++part)
+                            mma_f8_pair(at, dQ + (((4 * part + d) * S::kChunk + 32 * i) >> 4), k + ((32 * i) >> 4),
+                                        S::kIdescS, (d | i | part) != 0);
+                }
+                tc_commit_pair(&sh.empty[slot]);
+                if (d == 3) tc_commit_pair(&sh.s_full[gt & 1]);
+                if (d == 3 && last) tc_commit_pair(&sh.q_empty);
+            }
+            __syncwarp();
+            used();
+        }
+        return true;
+    };
+    auto flags_of = [&](int gt) -> int {  // -1: gave up
+        if (!mbar_wait_warp(&sh.info_full[gt % kInfos], (uint32_t)((gt / kInfos) & 1), abort)) return -1;
+        return *(volatile int*)&sh.info[gt % kInfos].flags;
+    };
+    int flags = flags_of(0);
+    for (int gt = 0; flags >= 0 && !(flags & Info::kStop); ++gt) {
+        if (flags & Info::kFirst) {
+            if (!mbar_wait_cluster_warp(&sh.q_full[it & 1], (uint32_t)((it >> 1) & 1), abort)) return;
+            tc_fence_after();
+            ++it;
+            if (!scores(gt, flags & Info::kLast)) return;
+        }
+        const int next = flags_of(gt + 1);
+        if (next < 0) return;
+        if (!(flags & Info::kLast) && !scores(gt + 1, next & Info::kLast)) return;
+        if (!mbar_wait_cluster_warp(&sh.p_full, (uint32_t)(gt & 1), abort)) return;
+        tc_fence_after();
+        const uint32_t more = __shfl_sync(0xffffffffu, flags & Info::kFirst ? 0u : 1u, 0);
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+                if (!landed()) return;
+                const uint64_t v = dV + place();
+                if (elect_one()) {
+                    if constexpr (kBf16) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            mma_f16_pair(tmem + kColO + 128 * h, dP + ((p * S::kChunk + 32 * i) >> 4),
+                                         v + ((2048 * i) >> 4), S::kIdescPV, (p | i) == 0 ? more : 1u);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 2; ++i)
+#pragma unroll
+                            for (int part = 0; part < 3; ++part)
+                                mma_f8_pair(tmem + kColO + 128 * h, dP + ((part * S::kChunk + 64 * p + 32 * i) >> 4),
+                                            v + ((4096 * i) >> 4), S::kIdescPV, (p | i | part) == 0 ? more : 1u);
+                    }
+                    tc_commit_pair(&sh.empty[slot]);
+                    if ((h & p) == 1) tc_commit_pair(&sh.pv_done);
+                }
+                __syncwarp();
+                used();
+            }
+        flags = next;
+    }
+}
+
+template <bool kBf16>
+__device__ void relay_role(Shared<kBf16>& sh, int lane, volatile int* abort) {
+    using S = Shape<kBf16>;
+    int slot = 0;
+    uint32_t phase = 0;
+    for (int gt = 0;; ++gt) {
+        if (!mbar_wait_warp(&sh.info_full[gt % kInfos], (uint32_t)((gt / kInfos) & 1), abort)) return;
+        if (*(volatile int*)&sh.info[gt % kInfos].flags & Info::kStop) return;
+        for (int i = 0; i < 8; ++i) {  // (a tile has eight places)
+            if (!mbar_wait_warp(&sh.full[slot], phase, abort)) return;
+            fence_proxy_async_smem();
+            if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&sh.peer_full[slot]), 0));
+            __syncwarp();
+            if (++slot == S::kPlaces) slot = 0, phase ^= 1u;
+        }
+    }
+}
+
+// ---------------------------------------------------------------- softmax and epilogue
+// Makes zeros of what is not finite of positions 32 quarter + (the bits of `which`) in this CTA's
+// places of V of tile gt. Called by a warp when PV of the tile before is done.
+template <bool kBf16>
+__device__ __noinline__ bool finite_values(Shared<kBf16>& sh, uint32_t which, int gt, int flags, int quarter, int lane,
+                                           volatile int* abort) {
+    using S = Shape<kBf16>;
+    // places filled before them: four a tile for V and for K, K of the next tile of the run among them
+    const int v0 = 8 * gt + (flags & Info::kLast ? 4 : 8);
+    uint8_t* at[2];
+    for (int h = 0; h < 2; ++h) {
+        const int g = v0 + 2 * h + (quarter >> 1), slot = g % S::kPlaces;
+        // (what the place held before has been used: this is the phase that its barrier is in)
+        if (!mbar_wait_warp(&sh.full[slot], (uint32_t)((g / S::kPlaces) & 1), abort)) return false;
+        at[h] = sh.ring[slot];
+    }
+    constexpr int kUnits = kBf16 ? 32 : 16;  // of 16 bytes: 128 channels in each half
+    if (lane < kUnits) {
+        const int h = lane / (kUnits / 2), u = lane % (kUnits / 2);
+        uint8_t* const from = (h ? at[1] : at[0]) + (u >> 3) * S::kChunk + (u & 7) * 16 + 32 * (quarter & 1) * 128;
+        for (; which; which &= which - 1) {
+            uint4* const x = reinterpret_cast<uint4*>(from + (__ffs(which) - 1) * 128);
+            uint32_t v[4] = {x->x, x->y, x->z, x->w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if constexpr (kBf16) {
+                    if ((v[i] & 0x7f80u) == 0x7f80u) v[i] &= 0xffff0000u;
+                    if ((v[i] & 0x7f800000u) == 0x7f800000u) v[i] &= 0x0000ffffu;
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 32; k += 8)
+                        if (((v[i] >> k) & 0x7fu) == 0x7fu) v[i] &= ~(0xffu << k);
+                }
+            }
+            *x = make_uint4(v[0], v[1], v[2], v[3]);
+        }
+    }
+    return true;
+}
+
+// Warp (qd, ch): rows 32 (qd & 1) + lane of this CTA, positions 64 (qd >> 1) + 32 ch .. + 31 of the
+// tile: lane quarter qd of TMEM, whose upper half holds the same rows' other 64 positions. Logits
+// are in the log2 domain. A row's four threads agree on its maximum through shared memory; it is
+// lazy, and where it moves the row's part of O is rescaled in TMEM.
+template <bool kBf16>
+__device__ void softmax_role(Shared<kBf16>& sh, const Args& a, uint32_t tmem, int warp, int lane, int rank, int pair,
+                             volatile int* abort) {
+    using S = Shape<kBf16>;
+    const int qd = warp & 3, ch = warp >> 2, grp = qd & 1, quarter = 2 * (qd >> 1) + ch;
+    const int r = 32 * grp + lane;                 // of this CTA's rows
+    const int p0 = 32 * quarter;                   // first position
+    const uint32_t tl = tmem + ((uint32_t)(32 * qd) << 16);
+    float m = -INFINITY, l = 0.f, c = a.scale_log2;
+    float m_was = -INFINITY, l_was = 0.f;          // of the piece up to this run
+    Row row = {-1, 0, 0, 0};
+    int runs = 0;
+    for (int gt = 0;; ++gt) {
+        if (!mbar_wait_warp(&sh.info_full[gt % kInfos], (uint32_t)((gt / kInfos) & 1), abort)) return;
+        const Info& in = sh.info[gt % kInfos];
+        const int flags = in.flags;
+        if (flags & Info::kStop) return;
+        if (flags & Info::kFirst) {
+            row = row_info(a, in.u0, in.f, kMine * rank + r);
+            m = -INFINITY;
+            l = 0.f;
+            if constexpr (!kBf16) {
+                if (!mbar_wait_warp(&sh.q_here[runs & 1], (uint32_t)((runs >> 1) & 1), abort)) return;
+                c = sh.row_scale[runs & 1][r];
+            }
+            ++runs;
+        }
+        // the positions of this thread that its row sees; rows that stand for nothing see everything
+        uint32_t seen = ~0u;
+        if (row.b >= 0) {
+            const int lo = max(0, min(32, in.lo - in.t0 - p0));
+            const int hi = in.k >= 0 && in.k != row.k ? 0 : max(0, min(32, min(in.hi, row.T) - in.t0 - p0));
+            seen = in.ok[quarter] & (hi == 32 ? ~0u : (1u << hi) - 1u) & (lo == 32 ? 0u : ~0u << lo);
+        }
+        const bool all = __all_sync(0xffffffffu, seen == ~0u);
+        if (!mbar_wait_warp(&sh.s_full[gt & 1], (uint32_t)((gt >> 1) & 1), abort)) return;
+        tc_fence_after();
+        uint32_t sv[32];
+        tmem_ld_32x32b_x32(tl + kColS + 64 * (gt & 1) + 32 * ch, sv);
+        float x[32], odd = 0.f, odd2 = 0.f;  // 0, or NaN where a product is not finite
+#pragma unroll
+        for (int i = 0; i < 32; i += 2) {
+            odd = fmaf(__uint_as_float(sv[i]), 0.f, odd);
+            odd2 = fmaf(__uint_as_float(sv[i + 1]), 0.f, odd2);
+        }
+        const bool bad = __any_sync(0xffffffffu, !(odd + odd2 == 0.f));
+        uint32_t which = 0;  // positions whose products are not finite
+        if (bad) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) which |= (uint32_t)((sv[i] & 0x7f800000u) == 0x7f800000u) << i;
+            which = __reduce_or_sync(0xffffffffu, which);
+        }
+#pragma unroll
+        for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(sv[i]) * c;
+        if (!all) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) x[i] = (seen >> i) & 1u ? x[i] : -INFINITY;
+        }
+        float top = x[0];
+#pragma unroll
+        for (int i = 1; i < 32; ++i) top = fmaxf(top, x[i]);
+        sh.red_max[gt & 1][quarter][r] = top;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.max_bar[grp]);
+        if (!mbar_wait_warp(&sh.max_bar[grp], (uint32_t)(gt & 1), abort)) return;
+        top = fmaxf(fmaxf(sh.red_max[gt & 1][0][r], sh.red_max[gt & 1][1][r]),
+                    fmaxf(sh.red_max[gt & 1][2][r], sh.red_max[gt & 1][3][r]));
+        float alpha = 1.f;
+        if (top > m + S::kLazyMax || (flags & Info::kFirst)) {
+            if (m != -INFINITY) alpha = ex2(m - top);
+            m = top;
+        }
+        const float sub = m == -INFINITY ? 0.f : m - S::kLift;
+        // P, rounded; the sum takes the values that the product multiplies
+        uint32_t w[16], part[kBf16 ? 1 : 3][8];
+        float sum = 0.f, sum2 = 0.f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const float e0 = ex2(x[2 * i] - sub), e1 = ex2(x[2 * i + 1] - sub);
+            if constexpr (kBf16) {
+                const __nv_bfloat162 v = __floats2bfloat162_rn(e0, e1);
+                w[i] = *reinterpret_cast<const uint32_t*>(&v);
+                sum += __uint_as_float(w[i] << 16);
+                sum2 += __uint_as_float(w[i] & 0xffff0000u);
+            } else {
+                const __half2 v = __floats2half2_rn(e0, e1);
+                w[i] = *reinterpret_cast<const uint32_t*>(&v);
+            }
+        }
+        if constexpr (!kBf16) {
+            // A NaN loses itself in the first two parts' rounding and stays what is left of them, so the
+            // last part holds it. What that one leaves out is at most half its step, and what it leaves of
+            // w f16 holds: both differences are exact.
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                uint32_t x0 = w[2 * k], x1 = w[2 * k + 1];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const uint32_t q0 = (x0 + 0x00800080u) & 0xff00ff00u, q1 = (x1 + 0x00800080u) & 0xff00ff00u;
+                    part[i][k] = __byte_perm(q0, q1, 0x7531);
+                    x0 = h2_sub(x0, q0);
+                    x1 = h2_sub(x1, q1);
+                }
+                part[2][k] = h2x2_to_e5m2x4(x0, x1);
+                const uint32_t v0 = h2_sub(w[2 * k], h2_sub(x0, __byte_perm(part[2][k], 0u, 0x1404)));
+                const uint32_t v1 = h2_sub(w[2 * k + 1], h2_sub(x1, __byte_perm(part[2][k], 0u, 0x3424)));
+                const float2 f0 = __half22float2(*reinterpret_cast<const __half2*>(&v0));
+                const float2 f1 = __half22float2(*reinterpret_cast<const __half2*>(&v1));
+                sum += f0.x + f0.y;
+                sum2 += f1.x + f1.y;
+            }
+        }
+        l = fmaf(l, alpha, sum + sum2);
+        // after PV of the tile before P may be written again, and O rescaled
+        if (!(flags & Info::kFirst) && !mbar_wait_warp(&sh.pv_done, (uint32_t)((gt - 1) & 1), abort)) return;
+        if (__any_sync(0xffffffffu, alpha != 1.f)) {
+            tc_fence_after();
+#pragma unroll 1
+            for (int n = 0; n < 128; n += 32) {
+                uint32_t ov[32];
+                tmem_ld_32x32b_x32(tl + kColO + 128 * ch + n, ov);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) ov[i] = __float_as_uint(__uint_as_float(ov[i]) * alpha);
+                tmem_st_32x32b_x32(tl + kColO + 128 * ch + n, ov);
+            }
+            tmem_wait_st();
+        }
+        if constexpr (kBf16) {
+            uint8_t* dst = sh.p + (qd >> 1) * S::kChunk;
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                *reinterpret_cast<uint4*>(dst + sw128(r, 4 * ch + u)) = make_uint4(w[4 * u], w[4 * u + 1], w[4 * u + 2], w[4 * u + 3]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 3; ++i)
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+                    *reinterpret_cast<uint4*>(sh.p + i * S::kChunk + sw128(r, 2 * quarter + u)) =
+                        make_uint4(part[i][4 * u], part[i][4 * u + 1], part[i][4 * u + 2], part[i][4 * u + 3]);
+        }
+        // A weight of zero takes nothing from a position, unless that is not finite: rows that do not see
+        // a position must not notice what it holds. Its products with the queries tell. What is not finite
+        // of it becomes zero for PV; the rows that see it have NaN (or, of -infinity, zero) weights.
+        if (which && !finite_values(sh, which, gt, flags, quarter, lane, abort)) return;
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) arrive_lead(&sh.p_full, rank);
+        if (!(flags & Info::kLast)) continue;
+
+        // ---- the run's end: this thread has 128 channels of its row, 256 ch + 128 (qd >> 1) and on
+        if (!mbar_wait_warp(&sh.pv_done, (uint32_t)(gt & 1), abort)) return;
+        tc_fence_after();
+        sh.red_sum[quarter][r] = l;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.sum_bar[grp]);
+        if (!mbar_wait_warp(&sh.sum_bar[grp], (uint32_t)((runs - 1) & 1), abort)) return;
+        float total = (sh.red_sum[0][r] + sh.red_sum[1][r]) + (sh.red_sum[2][r] + sh.red_sum[3][r]);
+        float top_of = m - S::kLift;  // what P and O are relative to
+        float was = 0.f, now = 1.f;
+        if (!(flags & Info::kBegins)) {
+            const float M = fmaxf(m_was, top_of);
+            was = m_was == -INFINITY ? 0.f : ex2(m_was - M);
+            now = top_of == -INFINITY ? 0.f : ex2(top_of - M);
+            total = fmaf(l_was, was, total * now);
+            top_of = M;
+        }
+        m_was = top_of;
+        l_was = total;
+        const bool done = (flags & (Info::kEnds | Info::kWhole)) == (Info::kEnds | Info::kWhole);
+        float scale = 1.f;
+        if (done) {
+            const float sink2 = a.sink && row.b >= 0 ? a.sink[row.h] * kLog2e : -INFINITY;
+            const float M = fmaxf(top_of, sink2);
+            const float f = top_of == -INFINITY ? 0.f : ex2(top_of - M);
+            const float den = total * f + (sink2 == -INFINITY ? 0.f : ex2(sink2 - M));
+            scale = den == 0.f ? 0.f : f / den;
+        }
+        const int R = kMine * rank + r, d0 = 256 * ch + 128 * (qd >> 1);
+        float* const slot = part_of(a, pair, flags & Info::kOpens ? 0 : 1);
+        float4* const kept = reinterpret_cast<float4*>(slot) + (d0 / 4) * kRows + R;
+        __nv_bfloat16* const out = a.out + ((int64_t)max(row.b, 0) * a.heads + row.h) * kD + d0;
+#pragma unroll 1
+        for (int n = 0; n < 128; n += 32) {
+            float4 before[8];
+            if (!(flags & Info::kBegins)) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) before[i] = row.b >= 0 ? kept[(n / 4 + i) * kRows] : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+            uint32_t ov[32];
+            tmem_ld_32x32b_x32(tl + kColO + 128 * ch + n, ov);
+            float o[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = __uint_as_float(ov[i]);
+            if (!(flags & Info::kBegins)) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    o[4 * i] = fmaf(before[i].x, was, o[4 * i] * now);
+                    o[4 * i + 1] = fmaf(before[i].y, was, o[4 * i + 1] * now);
+                    o[4 * i + 2] = fmaf(before[i].z, was, o[4 * i + 2] * now);
+                    o[4 * i + 3] = fmaf(before[i].w, was, o[4 * i + 3] * now);
+                }
+            }
+            if (row.b < 0) continue;
+            if (done) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    uint32_t v[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const float2 y = make_float2(o[8 * i + 2 * k], o[8 * i + 2 * k + 1]);
+                        const __nv_bfloat162 b2 = __floats2bfloat162_rn(scale == 0.f ? 0.f : y.x * scale, scale == 0.f ? 0.f : y.y * scale);
+                        v[k] = *reinterpret_cast<const uint32_t*>(&b2);
+                    }
+                    *reinterpret_cast<uint4*>(out + n + 8 * i) = make_uint4(v[0], v[1], v[2], v[3]);
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    kept[(n / 4 + i) * kRows] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+            }
+        }
+        if (!done && quarter == 0 && row.b >= 0) {
+            slot[kRows * kD + R] = top_of;
+            slot[kRows * (kD + 1) + R] = total;
+        }
+        tc_fence_before();
+    }
+}
+
+template <bool kBf16>
+__global__ void __launch_bounds__(Shape<kBf16>::kThreads, 1)
+k_paged_shared(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap tmap) {
+    using S = Shape<kBf16>;
+    extern __shared__ uint8_t raw[];
+    auto& sh = *reinterpret_cast<Shared<kBf16>*>(raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u));
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+    const int rank = (int)cluster_ctarank(), pair = blockIdx.x >> 1;
+    volatile int* abort = &sh.abort;
+    if (tid == 0) {
+        for (int i = 0; i < S::kPlaces; ++i) {
+            mbar_init(&sh.full[i], 1);
+            mbar_init(&sh.empty[i], 1);
+            mbar_init(&sh.peer_full[i], 1);
+        }
+        for (int i = 0; i < kInfos; ++i) mbar_init(&sh.info_full[i], 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sh.s_full[i], 1);
+            mbar_init(&sh.q_full[i], 2 * S::kHelpWarps);
+            mbar_init(&sh.q_here[i], S::kHelpWarps);
+            mbar_init(&sh.max_bar[i], 4);
+            mbar_init(&sh.sum_bar[i], 4);
+        }
+        mbar_init(&sh.p_full, 2 * S::kSoftWarps);
+        mbar_init(&sh.pv_done, 1);
+        mbar_init(&sh.q_empty, 1);
+        mbar_init(&sh.drain, 1);
+        sh.abort = 0;
+        fence_mbar_init();
+    }
+    if (warp == S::kMmaWarp) tmem_alloc_pair(&sh.tmem_base, kTmemCols);
+    // a programmatic launch: only the setup above may overlap the kernel ahead
+    grid_dep_launch_dependents();
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync_all();  // the other CTA's barriers are there
+    tc_fence_after();
+    grid_dep_wait();
+    plan(a, sh.plan, pair);  // ends with a CTA barrier
+    const uint32_t tmem = __shfl_sync(0xffffffffu, sh.tmem_base, 0);
+    if (warp < S::kSoftWarps) {
+        softmax_role<kBf16>(sh, a, tmem, warp, lane, rank, pair, abort);
+    } else if (warp == S::kMmaWarp) {
+        if (rank == 0) {
+            mma_role<kBf16>(sh, tmem, abort);
+            // every MMA issued must finish before TMEM and shared memory are released
+            __syncwarp();
+            if (elect_one()) tc_commit_pair(&sh.drain);
+            if (!mbar_wait_drain(&sh.drain, 0)) *abort = 1;
+        } else {
+            relay_role<kBf16>(sh, lane, abort);
+        }
+    } else if (warp == S::kTmaWarp) {
+        tma_role<kBf16>(sh, a, &tmap, lane, rank, pair, abort);
+    } else {
+        query_role<kBf16>(sh, a, warp - S::kHelp0, lane, rank, abort);
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync_all();  // nothing of the pair is in flight
+    if (tid == 0 && sh.abort) raise_status(a.dev_status, CSA2_DEV_TIMEOUT);
+    if (warp == S::kMmaWarp) {
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc_pair(tmem, kTmemCols);
+    }
+    cluster_sync_all();
+}
+
+template <bool kBf16>
+constexpr int smem_bytes() {
+    return (int)sizeof(Shared<kBf16>) + 1024;
+}
+static_assert(smem_bytes<true>() <= 227 * 1024 && smem_bytes<false>() <= 227 * 1024, "shared memory of a CTA");
+
+// ---------------------------------------------------------------- join
+// The units that the ranges cut: o = sum_i O_i 2^(m_i - M) / (2^(sink - M) + sum_i l_i 2^(m_i - M)) over the
+// pairs' partial results in order. A thread has four channels of a row; an item is 8 channels of a
+// unit's 128 rows. What sees nothing and had no unit gets its zeros here.
+constexpr int kJoinThreads = 256;
+constexpr int kJoinItems = kD / 8;  // of a unit
+constexpr int kJoinBatch = 8;
+
+__global__ void __launch_bounds__(kJoinThreads) k_shared_join(const __grid_constant__ Args a) {
+    __shared__ int4 ends[kMaxPairs];
+    __shared__ int starts[kMaxPairs], units;
+    grid_dep_wait();
+    const int tid = threadIdx.x, lane = tid & 31;
+    for (int c = tid; c < a.pairs; c += kJoinThreads) ends[c] = a.ends[c];
+    for (int b = blockIdx.x * (kJoinThreads / 32) + (tid >> 5); b < a.B; b += gridDim.x * (kJoinThreads / 32)) {
+        const int row = a.seq ? a.seq[b] : b;
+        if (row < 0 || (row < a.g.max_seqs && length_of(a, a.n_tokens[b], false) > 0)) continue;
+        uint4* out = reinterpret_cast<uint4*>(a.out + (int64_t)b * a.heads * kD);
+        for (int u = lane; u < a.heads * (kD / 8); u += 32) out[u] = make_uint4(0u, 0u, 0u, 0u);
+    }
+    __syncthreads();
+    if (tid == 0) {
+        int n = 0;
+        for (int c = 0; c + 1 < a.pairs; ++c)
+            if ((ends[c].x & kCut) && !(ends[c].x & kThrough)) starts[n++] = c;
+        units = n;
+    }
+    __syncthreads();
+    const int R = tid & (kRows - 1);
+    for (int item = blockIdx.x; item < units * kJoinItems; item += gridDim.x) {
+        const int c0 = starts[item / kJoinItems], cg = 2 * (item % kJoinItems) + (tid >> 7);
+        const int4 u = ends[c0];
+        const Row row = row_info(a, u.y, u.z, R);
+        if (row.b < 0) continue;
+        int n = 2;  // pieces: c0's last one, then the others' first ones
+        while (c0 + n < a.pairs && (ends[c0 + n - 1].x & (kCut | kThrough)) == (kCut | kThrough)) ++n;
+        auto piece = [&](int i) { return part_of(a, c0 + i, i == 0 && !(u.x & kSingle) ? 1 : 0); };
+        const float s2 = a.sink ? a.sink[row.h] * kLog2e : -INFINITY;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        float den = 0.f, M = s2;
+        for (int i0 = 0; i0 < n; i0 += kJoinBatch) {
+            float m[kJoinBatch];
+#pragma unroll
+            for (int i = 0; i < kJoinBatch; ++i) m[i] = i0 + i < n ? __ldcg(piece(i0 + i) + kRows * kD + R) : -INFINITY;
+#pragma unroll
+            for (int i = 0; i < kJoinBatch; ++i) M = fmaxf(M, m[i]);
+        }
+        for (int i0 = 0; i0 < n; i0 += kJoinBatch) {
+            float4 v[kJoinBatch];
+            float m[kJoinBatch], l[kJoinBatch];
+#pragma unroll
+            for (int i = 0; i < kJoinBatch; ++i) {
+                if (i0 + i >= n) continue;
+                const float* p = piece(i0 + i);
+                v[i] = __ldcg(reinterpret_cast<const float4*>(p) + cg * kRows + R);
+                m[i] = __ldcg(p + kRows * kD + R);
+                l[i] = __ldcg(p + kRows * (kD + 1) + R);
+            }
+#pragma unroll
+            for (int i = 0; i < kJoinBatch; ++i) {
+                if (i0 + i >= n) continue;
+                const float w = m[i] == -INFINITY ? 0.f : ex2(m[i] - M);
+                den = fmaf(l[i], w, den);
+                acc.x = fmaf(v[i].x, w, acc.x);
+                acc.y = fmaf(v[i].y, w, acc.y);
+                acc.z = fmaf(v[i].z, w, acc.z);
+                acc.w = fmaf(v[i].w, w, acc.w);
+            }
+        }
+        den += s2 == -INFINITY ? 0.f : ex2(s2 - M);
+        const float inv = den == 0.f ? 0.f : 1.f / den;
+        const __nv_bfloat162 x = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
+        const __nv_bfloat162 y = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
+        *reinterpret_cast<uint2*>(a.out + ((int64_t)row.b * a.heads + row.h) * kD + 4 * cg) =
+            make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
+    }
+}
+
+// CTA pairs on the current device: one CTA per SM, at most max_ctas (but one pair). 0: no device.
+int pairs_of(const csa2_params* p) {
+    int n = sm_count();
+    if (n <= 0) return 0;
+    if (p->max_ctas > 0 && p->max_ctas < n) n = p->max_ctas;
+    return n < 2 ? 1 : n / 2 < kMaxPairs ? n / 2 : kMaxPairs;
+}
+
+int64_t ends_bytes(int pairs) { return ((int64_t)pairs * (int)sizeof(int4) + 255) & ~(int64_t)255; }
+int64_t ws_need(int pairs) { return ends_bytes(pairs) + 2 * (int64_t)pairs * kPartFloats * 4; }
+
+}  // namespace
+
+cudaError_t preload_paged_shared() {
+    cudaError_t (*l[])() = {[] { return preload_kernel(k_paged_shared<true>, smem_bytes<true>()); },
+                            [] { return preload_kernel(k_paged_shared<false>, smem_bytes<false>()); },
+                            [] { return preload_kernel(k_shared_join); }};
+    for (auto f : l)
+        if (const cudaError_t e = f()) return e;
+    return cudaSuccess;
+}
+
+}  // namespace csa2
+
+using namespace csa2;
+
+extern "C" size_t csa2_paged_attn_shared_workspace_size(const csa2_params* p, const csa2_pages* c, int B) {
+    if (!p || !c || B <= 0 || p->heads < 1 || p->heads > kMaxHeads) return 0;
+    const int pairs = pairs_of(p);
+    return pairs > 0 ? (size_t)ws_need(pairs) : 0;
+}
+
+extern "C" int csa2_paged_attn_shared(const csa2_params* p, const csa2_pages* c, int layer, int B, const void* q,
+                                      int64_t q_seq, int64_t q_head, const float* sink, const int32_t* seq,
+                                      const int32_t* n_tokens, const int32_t* order, const int32_t* first,
+                                      const int32_t* shared, void* out, void* workspace, size_t ws_bytes,
+                                      int32_t* dev_status, void* stream) {
+    Args a = {};
+    if (const int rc = check_pages("paged_attn_shared", p, c, &a.g)) return rc;
+    if (B < 0 || layer < 0 || layer >= a.g.layers)
+        return fail(CSA2_ERR_INVALID_ARG, "paged_attn_shared: negative size or layer out of range");
+    if (p->heads < 1 || p->heads > kMaxHeads || p->q_format != CSA2_BF16)
+        return fail(CSA2_ERR_UNSUPPORTED, "paged_attn_shared: built for 1 .. 64 heads, BF16 queries");
+    if (B > 65535) return fail(CSA2_ERR_UNSUPPORTED, "paged_attn_shared: at most 65535 sequences");
+    if (B == 0) return CSA2_OK;
+    if (!seq && B > a.g.max_seqs) return fail(CSA2_ERR_INVALID_ARG, "paged_attn_shared: B beyond max_seqs needs seq");
+    if (!q || !n_tokens || !order || !first || !shared || !out || !workspace)
+        return fail(CSA2_ERR_INVALID_ARG, "paged_attn_shared: NULL buffer");
+    if (B == 1) q_seq = 0;  // strides that nothing is stepped by
+    if (p->heads == 1) q_head = 0;
+    if (!aligned16(q) || !aligned16(out) || q_seq % 8 || q_head % 8)
+        return fail(CSA2_ERR_ALIGN, "paged_attn_shared: q's heads and out must be 16-byte aligned");
+    if (reinterpret_cast<uintptr_t>(workspace) & 255u)
+        return fail(CSA2_ERR_ALIGN, "paged_attn_shared: workspace must be 256-byte aligned");
+    if (const int rc = ensure_loaded()) return rc;
+    const int pairs = pairs_of(p);
+    if (pairs <= 0) return check_launch("paged_attn_shared: device");
+    if ((int64_t)ws_bytes < ws_need(pairs))
+        return fail(CSA2_ERR_SHAPE, "paged_attn_shared: workspace smaller than csa2_paged_attn_shared_workspace_size");
+    a.base = a.g.pool + layer * a.g.layer_bytes;
+    a.B = B;
+    a.heads = p->heads;
+    a.members = kRows / p->heads;
+    a.q_seq = q_seq;
+    a.q_head = q_head;
+    a.q = static_cast<const __nv_bfloat16*>(q);
+    a.sink = sink;
+    a.seq = seq;
+    a.n_tokens = n_tokens;
+    a.order = order;
+    a.first = first;
+    a.shared = shared;
+    a.out = static_cast<__nv_bfloat16*>(out);
+    a.ends = static_cast<int4*>(workspace);
+    a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + ends_bytes(pairs));
+    a.dev_status = dev_status;
+    a.scale_log2 = p->softmax_scale * kLog2e;
+    a.pairs = pairs;
+    a.box_rows = a.g.page_size & -a.g.page_size;
+    if (a.box_rows > kMine) a.box_rows = kMine;
+    CUtensorMap rows = {};
+    if (const int rc = encode_rows("paged_attn_shared", a.g, a.base, a.box_rows, &rows)) return rc;
+    const bool bf16 = p->kv_format == CSA2_BF16;
+    cudaLaunchConfig_t cfg = {};
+    cfg.stream = static_cast<cudaStream_t>(stream);
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = 2;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    cfg.gridDim = dim3(2 * pairs);
+    cfg.blockDim = dim3(bf16 ? Shape<true>::kThreads : Shape<false>::kThreads);
+    cfg.dynamicSmemBytes = bf16 ? smem_bytes<true>() : smem_bytes<false>();
+    if (bf16) cudaLaunchKernelEx(&cfg, k_paged_shared<true>, a, rows);
+    else cudaLaunchKernelEx(&cfg, k_paged_shared<false>, a, rows);
+    if (const int rc = check_launch("paged_attn_shared")) return rc;
+    cfg.numAttrs = 1;
+    cfg.gridDim = dim3(pairs > 1 ? 16 * pairs : 8);
+    cfg.blockDim = dim3(kJoinThreads);
+    cfg.dynamicSmemBytes = 0;
+    cudaLaunchKernelEx(&cfg, k_shared_join, a);
+    return check_launch("paged_attn_shared: join");
+}

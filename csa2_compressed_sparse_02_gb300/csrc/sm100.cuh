@@ -194,6 +194,15 @@ __device__ __forceinline__ bool mbar_try_wait_acq_cluster(uint64_t* bar, uint32_
         : "memory");
     return ok != 0;
 }
+// mbar_wait_warp for such a phase.
+__device__ __forceinline__ bool mbar_wait_cluster_warp(uint64_t* bar, uint32_t parity, volatile int* abort) {
+    for (uint32_t i = 0; i < kSpinLimit; ++i) {
+        if (__all_sync(0xffffffffu, mbar_try_wait_acq_cluster(bar, parity))) return true;
+        if ((i & 255u) == 255u && __any_sync(0xffffffffu, *abort != 0)) return false;
+    }
+    *abort = 1;
+    return false;
+}
 // Bounded wait for a phase whose arrivals come from other CTAs of the cluster.
 __device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity) {
     for (uint32_t i = 0; i < kSpinLimit; ++i)
@@ -243,6 +252,15 @@ __device__ __forceinline__ void tma_g2s_2d_hint(uint32_t smem_dst, const void* t
         "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint [%0], "
         "[%1, {%2, %3}], [%4], %5;\n" ::"r"(smem_dst),
         "l"(tmap), "r"(x), "r"(y), "r"(smem_u32(bar)), "l"(policy)
+        : "memory");
+}
+
+// The same without a policy.
+__device__ __forceinline__ void tma_g2s_2d(uint32_t smem_dst, const void* tmap, int x, int y, uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];\n" ::"r"(
+            smem_dst),
+        "l"(tmap), "r"(x), "r"(y), "r"(smem_u32(bar))
         : "memory");
 }
 
@@ -507,6 +525,50 @@ __device__ __forceinline__ void tmem_st_32x32b_x8(uint32_t taddr, const uint32_t
 __device__ __forceinline__ void tmem_wait_st() {
     __syncwarp();  // .sync.aligned: the whole warp, converged
     asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory");
+}
+
+// ---- CTA pairs (cta_group::2): two CTAs of a cluster whose ranks differ in the last bit run one
+// MMA. The even one issues it; the descriptors name the same offsets in both. With M = 128 each
+// CTA's A holds 64 of D's rows and its B one half of D's columns; a CTA's own rows come out in its
+// TMEM, columns 0 .. N/2 - 1 in lanes 0 .. 63 and the others in lanes 64 .. 127. Measured: 32
+// cycles at N = 128 and 64 at N = 256 (K = 16 of bf16, K = 32 of 8-bit types), the full rate.
+// A kernel that uses them allocates and frees its TMEM with them too, a warp in each CTA.
+__device__ __forceinline__ void tmem_alloc_pair(uint32_t* smem_slot, uint32_t ncols) {
+    __syncwarp();  // .sync.aligned: the whole warp, converged
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(smem_u32(smem_slot)),
+                 "r"(ncols)
+                 : "memory");
+    __syncwarp();
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;\n" ::: "memory");
+}
+__device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols) {
+    __syncwarp();  // .sync.aligned: the whole warp, converged
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;\n" ::"r"(taddr), "r"(ncols) : "memory");
+}
+__device__ __forceinline__ void mma_f16_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                             uint32_t accumulate) {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+__device__ __forceinline__ void mma_f8_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                            uint32_t accumulate) {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// Arrive on the mbarrier at this offset in both CTAs once every pair operation this thread issued so
+// far completes.
+__device__ __forceinline__ void tc_commit_pair(uint64_t* bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n" ::"r"(
+            smem_u32(bar)),
+        "h"((uint16_t)3)
+        : "memory");
 }
 
 // Waits for the phase with the given parity, bounded, ignoring any abort flag

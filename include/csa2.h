@@ -671,6 +671,43 @@ int csa2_paged_attn(const csa2_params* p, const csa2_pages* c, int layer, int B,
                     const int32_t* seq, const int32_t* n_tokens, int window, int n_first,
                     void* out, void* workspace, size_t ws_bytes, int32_t* dev_status, void* stream);
 
+/* Bytes of scratch csa2_paged_attn_shared needs on the current device (for any B). */
+size_t csa2_paged_attn_shared_workspace_size(const csa2_params* p, const csa2_pages* c, int B);
+
+/*
+ * csa2_paged_attn_shared — csa2_paged_attn (without a window) for a batch in which groups of
+ * sequences share their leading positions: those are read once for the whole group. Groups are
+ * what csa2_prefix_groups finds, or the caller's own, by slots i = 0 .. B-1 of an order:
+ *   order  [B] int32, device: the sequences of the call (indices of q, seq, n_tokens and out), group
+ *          after group, each once;
+ *   first  [B] int32, device: the slot where the group of slot i begins;
+ *   shared [B] int32, device: positions the group of slot i has in common (read at its first slot).
+ * Positions t < shared are read through the table row of the group's first sequence, whatever the
+ * others' rows hold there, positions from shared on through each sequence's own row. A sequence sees
+ * its positions t < n_tokens[b], also where that is less than shared. Of an order that does not name
+ * every sequence once, the missing ones' outputs are undefined.
+ *   Arguments, masking and limits are otherwise those of csa2_paged_attn, as are the roundings of
+ *   weights and output; with E4M3 pages a query is the sum of two E4M3 values under a power of two
+ *   per head: exact down to 2^-10 of the head's largest value, to 2^-18 of it below. An infinity in a
+ *   row of a page counts only through the logits: it makes the outputs that see it NaN, unless its
+ *   logit is -infinity, which takes the row out. What sequences do not see does not reach them, NaN in
+ *   another sequence's positions among it.
+ *   A slot with first outside [0, i] counts as a group of its own, one with order outside [0, B) as
+ *   padding (both CSA2_DEV_BAD_INDEX); a shared below 0 or beyond max_pages pages sets
+ *   CSA2_DEV_BAD_LENGTH (none, or the first max_pages pages).
+ *   workspace: csa2_paged_attn_shared_workspace_size bytes, 256-byte aligned, contents
+ *   arbitrary; calls that share it must be ordered (one stream or events).
+ * On the 5th-generation tensor cores, by pairs of CTAs (one CTA per SM, or p->max_ctas, at least
+ * two): up to 128 rows (heads of a group's sequences) meet a position together. The tiles of the
+ * batch are cut into equal ranges; a second kernel joins what was cut, in order, so results do not
+ * vary from run to run.
+ */
+int csa2_paged_attn_shared(const csa2_params* p, const csa2_pages* c, int layer, int B,
+                           const void* q, int64_t q_seq, int64_t q_head, const float* sink,
+                           const int32_t* seq, const int32_t* n_tokens, const int32_t* order,
+                           const int32_t* first, const int32_t* shared, void* out, void* workspace,
+                           size_t ws_bytes, int32_t* dev_status, void* stream);
+
 /*
  * csa2_fp4_mma_peak — measurement aid, no counterpart in the pages: the rate of
  * the block-scaled FP4 tensor-core MMA that csa2_index_scores_shared issues, so
