@@ -44,7 +44,8 @@ struct Args {
     int32_t* dev_status;
     float scale_log2;
     int pairs;
-    int box_rows;     // rows of a copied box: a power of two, divides 64 and the page size
+    int box_rows;     // rows of a copied box, 2^box_shift: divides 64 and the page size
+    int box_shift;
 };
 
 // How a pair's range ends: its last unit goes on behind it; is its only one; and began before it.
@@ -203,7 +204,7 @@ struct Walk {
     int64_t left;
     int i, j, base;
     Slot mine, s;  // of lane's slot, of slot i
-    int pre, items;
+    int pre, items, u0;
     __device__ __forceinline__ Walk(const Args& a, const Range& r)
         : a(a), left(r.items), i(r.i), j(r.j), base(-1) {
         if (left > 0) enter();
@@ -220,7 +221,8 @@ struct Walk {
         s.f = __shfl_sync(0xffffffffu, mine.f, l);
         s.sh = __shfl_sync(0xffffffffu, mine.sh, l);
         s.prow = __shfl_sync(0xffffffffu, mine.prow, l);
-        pre = prefix_tiles(a, s, i);
+        u0 = unit_of(a, i, s.f);
+        pre = u0 == i ? tiles_of(s.sh) : 0;
         items = pre + own_tiles(s);
     }
     __device__ __forceinline__ bool next(Tile& t) {
@@ -231,13 +233,13 @@ struct Walk {
             enter();
         }
         const bool own = j >= pre;
-        t.u0 = unit_of(a, i, s.f);
+        t.u0 = u0;
         t.f = s.f;
         t.t0 = kTile * (own ? s.sh / kTile + j - pre : j);
         t.lo = own ? s.sh : 0;
         t.hi = own ? s.T : s.sh;
         t.row = own ? s.row : s.prow;
-        t.k = own ? i - t.u0 : -1;
+        t.k = own ? i - u0 : -1;
         ++j;
         --left;
         return true;
@@ -274,11 +276,11 @@ __device__ __forceinline__ Row row_info(const Args& a, int u0, int f, int r) {
 template <bool kBf16>
 struct Shape {
     static constexpr int kSoftWarps = 8;
-    static constexpr int kMmaWarp = 8, kTmaWarp = 9, kHelp0 = 10, kHelpWarps = 4;
+    static constexpr int kMmaWarp = 8, kKeyWarp = 9, kValueWarp = 10, kPlanWarp = 11, kHelp0 = 12, kHelpWarps = 4;
     static constexpr int kThreads = 32 * (kHelp0 + kHelpWarps);
     static constexpr uint32_t kChunk = kMine * 128;            // 64 rows x 128 bytes, 128-byte swizzle
     static constexpr uint32_t kPlace = kBf16 ? 2 * kChunk : kChunk;  // 64 positions x 128 channels
-    static constexpr int kPlaces = kBf16 ? 8 : 16;
+    static constexpr int kKeys = kBf16 ? 4 : 8, kValues = kBf16 ? 4 : 8;  // places; a tile takes four of each
     static constexpr uint32_t kIdesc = (1u << 4) | ((128u >> 4) << 24);  // D fp32, M = 128 over the pair
     // N = 128 positions, both K-major; N = 256 channels, B MN-major. Types: bf16 1, E4M3 0, E5M2 1
     static constexpr uint32_t kIdescS = kIdesc | ((128u >> 3) << 17) | (kBf16 ? (1u << 7) | (1u << 10) : 0u);
@@ -305,21 +307,22 @@ struct alignas(16) Info {
     };
     int t0, lo, hi, k, u0, f, flags, pad;
     uint32_t ok[4];  // the positions whose page exists
+    int y[16];       // the pool's row where each box of the tile begins
 };
 
 template <bool kBf16>
 struct Shared {
     using S = Shape<kBf16>;
-    uint8_t ring[S::kPlaces][S::kPlace];
+    uint8_t keys[S::kKeys][S::kPlace], values[S::kValues][S::kPlace];
     uint8_t q[8 * S::kChunk];
     uint8_t p[(kBf16 ? 2 : 3) * S::kChunk];  // bf16: 64 positions each; E4M3: 128, a part each
     float red_max[2][4][kMine];
     float red_sum[4][kMine];
     float row_scale[2][kMine];  // E4M3: logit factor, by run parity
     Info info[kInfos];
-    uint64_t full[S::kPlaces], empty[S::kPlaces];
-    uint64_t peer_full[S::kPlaces];  // the even CTA's: the odd one's place is full
-    uint64_t info_full[kInfos];
+    uint64_t key_full[S::kKeys], key_empty[S::kKeys], value_full[S::kValues], value_empty[S::kValues];
+    uint64_t key_peer[S::kKeys], value_peer[S::kValues];  // the even CTA's: the odd one's place is full
+    uint64_t info_full[kInfos], info_empty[kInfos];
     uint64_t s_full[2], p_full, pv_done;
     uint64_t q_full[2];   // the even CTA's: both CTAs' rows are staged; by run parity
     uint64_t q_here[2];   // this CTA's are
@@ -334,124 +337,149 @@ struct Shared {
 // An arrive on the even CTA's barrier, from either CTA of the pair.
 __device__ __forceinline__ void arrive_lead(uint64_t* bar, uint32_t rank) {
     if (rank == 0) mbar_arrive(bar);
-    else mbar_arrive_cluster(mapa_shared(smem_u32(bar), 0));
+    else mbar_arrive_peer(mapa_shared(smem_u32(bar), 0));
 }
 
-// ---------------------------------------------------------------- copies
-// One warp walks the range, tells the other roles of each tile, and copies it box by box (rows of
-// one page). Boxes that hold nothing seen are copied from behind the pool's last row, which reads
-// as zeros: P is zero for them, and 0 x whatever the place held before might be NaN.
-// The places in order: K of a run's first tile; then, for each tile, K of the next one and V of it.
+// ---------------------------------------------------------------- tiles
+// One warp walks the range and tells the other roles of each tile. Boxes (rows of one page) that hold
+// nothing seen are copied from behind the pool's last row, which reads as zeros: P is zero for them,
+// and 0 x whatever the place held before might be NaN.
 template <bool kBf16>
-__device__ void tma_role(Shared<kBf16>& sh, const Args& a, const CUtensorMap* tmap, int lane, int rank, int pair,
-                         volatile int* abort) {
+__device__ void plan_role(Shared<kBf16>& sh, const Args& a, int lane, int rank, int pair, volatile int* abort) {
     using S = Shape<kBf16>;
-    const int br = a.box_rows, ps = a.g.page_size, behind = a.g.n_pages * ps;
-    const int pos = lane * br;  // of this lane's box in the tile
+    const int br = a.box_rows, shift = a.box_shift, ps = a.g.page_size;
+    const int pos = lane << shift;  // of this lane's box in the tile
     const Range range = sh.plan.range;
     Walk walk(a, range);
-    Tile cur = {}, nxt = {};
-    bool has = walk.next(cur), has_nx = has && walk.next(nxt);
-    int gt = 0, g = 0;  // tiles told of, places filled
     int run = 0, runs = 0, pieces = 0;
-    auto tell = [&](const Tile& t, bool more) {  // returns the pool's row where this lane's box begins
-        const bool ends = !more || nxt.u0 != t.u0 || nxt.f != t.f;
-        const bool last = ends || run == S::kRun - 1;
-        int y = behind;
-        bool there = false;
+    // this lane's box: its page's entry is on its way while the tile before is told
+    struct Box {
+        int nth, page;  // of the row of the table, and its entry; nth < 0: not seen
+    };
+    auto look = [&](const Tile& t) {
+        Box b = {-1, -1};
         if (pos < kTile && t.t0 + pos < t.hi && t.t0 + pos + br > t.lo) {
-            const int at = t.t0 + pos, page = t.row < 0 ? -1 : a.g.table[(int64_t)t.row * a.g.max_pages + at / ps];
-            there = page >= 0 && page < a.g.n_pages;
-            if (there) y = page * ps + at % ps;
-            else if (rank == 0) raise_status(a.dev_status, CSA2_DEV_BAD_INDEX);
+            b.nth = (int)((uint32_t)(t.t0 + pos) / (uint32_t)ps);
+            b.page = t.row < 0 ? -1 : a.g.table[(int64_t)t.row * a.g.max_pages + b.nth];
         }
+        return b;
+    };
+    Tile cur = {}, nxt = {};
+    Box box = {}, box_nx = {};
+    bool has = walk.next(cur);
+    if (has) box = look(cur);
+    int gt = 0;
+    for (; has; ++gt) {
+        const bool more = walk.next(nxt);
+        if (more) box_nx = look(nxt);
+        const bool ends = !more || nxt.u0 != cur.u0 || nxt.f != cur.f;
+        const bool last = ends || run == S::kRun - 1;
+        if (gt >= kInfos && !mbar_wait_warp(&sh.info_empty[gt % kInfos], (uint32_t)((gt / kInfos - 1) & 1), abort)) return;
+        const bool there = box.nth >= 0 && box.page >= 0 && box.page < a.g.n_pages;
+        if (box.nth >= 0 && !there && rank == 0) raise_status(a.dev_status, CSA2_DEV_BAD_INDEX);
         const uint32_t held = __ballot_sync(0xffffffffu, there);
         Info& o = sh.info[gt % kInfos];
+        if (pos < kTile) o.y[lane] = there ? box.page * ps + cur.t0 + pos - box.nth * ps : a.g.n_pages * ps;
         if (lane < 4) {
             uint32_t ok = 0;
+#pragma unroll
             for (int p = 0; p < 32; p += 8)  // (a box has at least eight rows)
-                if ((held >> ((32 * lane + p) / br)) & 1u) ok |= 0xffu << p;
+                if ((held >> ((32 * lane + p) >> shift)) & 1u) ok |= 0xffu << p;
             o.ok[lane] = ok;
         }
         if (lane == 0) {
-            o.t0 = t.t0;
-            o.lo = t.lo;
-            o.hi = t.hi;
-            o.k = t.k;
-            o.u0 = t.u0;
-            o.f = t.f;
+            o.t0 = cur.t0;
+            o.lo = cur.lo;
+            o.hi = cur.hi;
+            o.k = cur.k;
+            o.u0 = cur.u0;
+            o.f = cur.f;
             o.flags = (run == 0 ? Info::kFirst : 0) | (last ? Info::kLast : 0) | (runs == 0 ? Info::kBegins : 0) |
                       (ends ? Info::kEnds : 0) | (pieces == 0 ? Info::kOpens : 0) |
                       (ends && !(pieces == 0 && range.cont) && !(!more && range.cut) ? Info::kWhole : 0);
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.info_full[gt % kInfos]);
-        ++gt;
         ++run;
         if (last) run = 0, ++runs;
         if (ends) runs = 0, ++pieces;
-        return y;
-    };
-    const uint32_t ring = smem_u32(sh.ring[0]);
-    auto fill = [&](int y, int first, int x) {  // 64 positions from `first` of the tile, 128 channels from x
-        const int slot = g % S::kPlaces;
-        if (g >= S::kPlaces && !mbar_wait_warp(&sh.empty[slot], (uint32_t)((g / S::kPlaces - 1) & 1), abort)) return false;
-        if (lane == 0) mbar_arrive_expect_tx(&sh.full[slot], S::kPlace);
-        __syncwarp();
-        if (pos >= first && pos < first + kMine) {
-            const uint32_t dst = ring + slot * S::kPlace + (pos - first) * 128;
-            tma_g2s_2d(dst, tmap, x, y, &sh.full[slot]);
-            if constexpr (kBf16) tma_g2s_2d(dst + S::kChunk, tmap, x + 64, y, &sh.full[slot]);
-        }
-        ++g;
-        return true;
-    };
-    auto keys = [&](int y) {
-        for (int d = 0; d < 4; ++d)
-            if (!fill(y, kMine * rank, 128 * d)) return false;
-        return true;
-    };
-    auto values = [&](int y) {
-        for (int h = 0; h < 2; ++h)
-            for (int p = 0; p < 2; ++p)
-                if (!fill(y, kMine * p, 256 * h + 128 * rank)) return false;
-        return true;
-    };
-    int y = 0, y_nx = 0;
-    bool good = true, last = false;
-    Tile end = {};
-    if (has) {
-        y = tell(cur, has_nx);
-        last = run == 0;
-        good = keys(y);
-    }
-    while (has && good) {
-        const bool was_last = last, more = has_nx;
-        end = cur;
-        if (more) {
-            cur = nxt;
-            has_nx = walk.next(nxt);
-            y_nx = tell(cur, has_nx);
-            last = run == 0;
-        }
-        good = (was_last || keys(y_nx)) && values(y) && (!was_last || !more || keys(y_nx));
-        y = y_nx;
         has = more;
+        // for the join: the unit that the range ends with, and whether it is cut there and before
+        if (!more && lane == 0 && rank == 0)
+            a.ends[pair] = make_int4((range.cut ? kCut : 0) | (pieces == 1 ? kSingle : 0) |
+                                     (pieces == 1 && range.cont ? kThrough : 0), cur.u0, cur.f, 0);
+        cur = nxt;
+        box = box_nx;
     }
+    if (range.items <= 0 && lane == 0 && rank == 0) a.ends[pair] = make_int4(0, 0, 0, 0);
+    if (gt >= kInfos && !mbar_wait_warp(&sh.info_empty[gt % kInfos], (uint32_t)((gt / kInfos - 1) & 1), abort)) return;
     if (lane == 0) {
         sh.info[gt % kInfos].flags = Info::kStop;
         mbar_arrive(&sh.info_full[gt % kInfos]);
-        // for the join: the unit that the range ends with, and whether it is cut there and before
-        if (rank == 0) {
-            const bool any = range.items > 0;
-            a.ends[pair] = make_int4(any ? (range.cut ? kCut : 0) | (pieces == 1 ? kSingle : 0) |
-                                               (pieces == 1 && range.cont ? kThrough : 0) : 0, end.u0, end.f, 0);
-        }
     }
+}
+
+// The tile's entry, as a warp reads it; false: the wait gave up.
+template <bool kBf16>
+__device__ __forceinline__ bool info_wait(Shared<kBf16>& sh, int gt, volatile int* abort) {
+    return mbar_wait_warp(&sh.info_full[gt % kInfos], (uint32_t)((gt / kInfos) & 1), abort);
+}
+template <bool kBf16>
+__device__ __forceinline__ void info_done(Shared<kBf16>& sh, int gt, int lane) {
     __syncwarp();
+    if (lane == 0) mbar_arrive(&sh.info_empty[gt % kInfos]);
+}
+
+// ---------------------------------------------------------------- copies
+// One warp copies the keys, one the values, box by box. One elected lane issues, from values of the
+// whole warp.
+template <bool kBf16, bool kKeys>
+__device__ void load_role(Shared<kBf16>& sh, const Args& a, const CUtensorMap* tmap, int lane, int rank,
+                          volatile int* abort) {
+    using S = Shape<kBf16>;
+    constexpr int kPlaces = kKeys ? S::kKeys : S::kValues;
+    uint64_t* const full = kKeys ? sh.key_full : sh.value_full;
+    uint64_t* const empty = kKeys ? sh.key_empty : sh.value_empty;
+    const uint32_t ring = smem_u32(kKeys ? sh.keys[0] : sh.values[0]);
+    const int shift = a.box_shift;
+    int slot = 0, g = 0;
+    uint32_t phase = 1;  // of a place that is free
+    for (int gt = 0;; ++gt) {
+        if (!info_wait(sh, gt, abort)) break;
+        const Info& in = sh.info[gt % kInfos];
+        if (in.flags & Info::kStop) break;
+        const int y = in.y[lane & 15];
+        info_done(sh, gt, lane);
+        bool good = true;
+#pragma unroll
+        for (int i = 0; i < 4 && good; ++i) {
+            // 64 positions from `first` of the tile, 128 channels from x
+            const int first = kKeys ? kMine * rank : kMine * (i & 1);
+            const int x = kKeys ? 128 * i : 256 * (i >> 1) + 128 * rank;
+            good = g < kPlaces || mbar_wait_warp(&empty[slot], phase, abort);
+            if (!good) break;
+            const uint32_t at = ring + (uint32_t)__shfl_sync(0xffffffffu, slot, 0) * S::kPlace;
+            const int y0 = __shfl_sync(0xffffffffu, y, first >> shift);
+            if (elect_one()) {
+                mbar_arrive_expect_tx(&full[slot], S::kPlace);
+                tma_g2s_2d(at, tmap, x, y0, &full[slot]);
+                if constexpr (kBf16) tma_g2s_2d(at + S::kChunk, tmap, x + 64, y0, &full[slot]);
+            }
+            for (int b = a.box_rows; b < kMine; b += a.box_rows) {
+                const int yb = __shfl_sync(0xffffffffu, y, (first + b) >> shift);
+                if (elect_one()) {
+                    tma_g2s_2d(at + b * 128, tmap, x, yb, &full[slot]);
+                    if constexpr (kBf16) tma_g2s_2d(at + b * 128 + S::kChunk, tmap, x + 64, yb, &full[slot]);
+                }
+            }
+            __syncwarp();
+            ++g;
+            if (++slot == kPlaces) slot = 0, phase ^= 1u;
+        }
+        if (!good) break;
+    }
     // whatever ended the loop, no copy of this CTA outlives it
-    for (int s = max(0, g - S::kPlaces); s < g; ++s)
-        mbar_wait_drain(&sh.full[s % S::kPlaces], (uint32_t)((s / S::kPlaces) & 1));
+    for (int s = max(0, g - kPlaces); s < g; ++s) mbar_wait_drain(&full[s % kPlaces], (uint32_t)((s / kPlaces) & 1));
 }
 
 // ---------------------------------------------------------------- queries
@@ -531,118 +559,140 @@ __device__ void query_role(Shared<kBf16>& sh, const Args& a, int warp, int lane,
 // The even CTA's warp issues the pair's MMAs: S of a tile, then S of the next one before PV of this,
 // so that the tensor cores work while the softmax runs. The odd CTA's passes on that its places are
 // full.
+//
+// What a warp does between MMAs costs as much as they do: a look at a barrier 200 cycles and more. So
+// the lanes look at a product's barriers together, and its MMAs are issued in one go.
+template <int kPlaces>
+struct Ring {
+    int slot = 0;
+    uint32_t phase = 0;
+    __device__ __forceinline__ int nth(int i) const { return slot + i < kPlaces ? slot + i : slot + i - kPlaces; }
+    __device__ __forceinline__ uint32_t parity(int i) const { return slot + i < kPlaces ? phase : phase ^ 1u; }
+    __device__ __forceinline__ void step(int n) {
+        if ((slot += n) >= kPlaces) slot -= kPlaces, phase ^= 1u;
+    }
+};
+
 template <bool kBf16>
-__device__ void mma_role(Shared<kBf16>& sh, uint32_t tmem, volatile int* abort) {
+__device__ void mma_role(Shared<kBf16>& sh, uint32_t tmem, int lane, volatile int* abort) {
     using S = Shape<kBf16>;
     const uint64_t dQ = smem_desc(smem_u32(sh.q), 16, 1024, kLayoutSw128);
     const uint64_t dP = smem_desc(smem_u32(sh.p), 16, 1024, kLayoutSw128);
-    const uint64_t dK = smem_desc(smem_u32(sh.ring[0]), 16, 1024, kLayoutSw128);
-    const uint64_t dV = smem_desc(smem_u32(sh.ring[0]), S::kChunk, 1024, kLayoutSw128);
-    int slot = 0, it = 0;
-    uint32_t phase = 0;
-    auto landed = [&]() {
-        if (!mbar_wait_warp(&sh.full[slot], phase, abort)) return false;
-        if (!mbar_wait_cluster_warp(&sh.peer_full[slot], phase, abort)) return false;
+    const uint64_t dK = smem_desc(smem_u32(sh.keys[0]), 16, 1024, kLayoutSw128);
+    const uint64_t dV = smem_desc(smem_u32(sh.values[0]), S::kChunk, 1024, kLayoutSw128);
+    Ring<S::kKeys> keys;
+    Ring<S::kValues> values;
+    int it = 0;
+    auto step = [](int slot) { return (uint64_t)__shfl_sync(0xffffffffu, (uint32_t)slot * (S::kPlace >> 4), 0); };
+    // S of tile gt; returns its flags, -1: gave up
+    auto scores = [&](int gt) -> int {
+        const int i = lane & 3;
+        uint64_t* const bar = lane < 4 ? &sh.key_full[keys.nth(i)] : lane < 8 ? &sh.key_peer[keys.nth(i)] : &sh.info_full[gt % kInfos];
+        if (!mbar_wait_warp(bar, lane < 8 ? keys.parity(i) : (uint32_t)((gt / kInfos) & 1), abort)) return -1;
         tc_fence_after();
-        return true;
-    };
-    auto place = [&]() { return (uint64_t)__shfl_sync(0xffffffffu, (uint32_t)slot * (S::kPlace >> 4), 0); };
-    auto used = [&]() {
-        if (++slot == S::kPlaces) slot = 0, phase ^= 1u;
-    };
-    auto scores = [&](int gt, bool last) {
+        const int flags = *(volatile int*)&sh.info[gt % kInfos].flags;
+        info_done(sh, gt, lane);
         const uint32_t at = tmem + kColS + (uint32_t)__shfl_sync(0xffffffffu, gt & 1, 0) * 64u;
+        const uint64_t k[4] = {dK + step(keys.nth(0)), dK + step(keys.nth(1)), dK + step(keys.nth(2)), dK + step(keys.nth(3))};
+        if (elect_one()) {
 #pragma unroll
-        for (int d = 0; d < 4; ++d) {
-            if (!landed()) return false;
-            const uint64_t k = dK + place();
-            if (elect_one()) {
+            for (int d = 0; d < 4; ++d) {
                 if constexpr (kBf16) {
 #pragma unroll
                     for (int c = 0; c < 2; ++c)
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
                             mma_f16_pair(at, dQ + (((2 * d + c) * S::kChunk + 32 * i) >> 4),
-                                         k + ((c * S::kChunk + 32 * i) >> 4), S::kIdescS, (d | c | i) != 0);
+                                         k[d] + ((c * S::kChunk + 32 * i) >> 4), S::kIdescS, (d | c | i) != 0);
                 } else {
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
 #pragma unroll
                         for (int part = 0; part < 2; ++part)
-                            mma_f8_pair(at, dQ + (((4 * part + d) * S::kChunk + 32 * i) >> 4), k + ((32 * i) >> 4),
+                            mma_f8_pair(at, dQ + (((4 * part + d) * S::kChunk + 32 * i) >> 4), k[d] + ((32 * i) >> 4),
                                         S::kIdescS, (d | i | part) != 0);
                 }
-                tc_commit_pair(&sh.empty[slot]);
-                if (d == 3) tc_commit_pair(&sh.s_full[gt & 1]);
-                if (d == 3 && last) tc_commit_pair(&sh.q_empty);
+                tc_commit_pair(&sh.key_empty[keys.nth(d)]);
             }
-            __syncwarp();
-            used();
+            tc_commit_pair(&sh.s_full[gt & 1]);
+            if (flags & Info::kLast) tc_commit_pair(&sh.q_empty);
         }
+        __syncwarp();
+        keys.step(4);
+        return flags;
+    };
+    auto output = [&](int gt, bool first) {
+        const int i = lane & 3;
+        uint64_t* const bar = lane < 4 ? &sh.value_full[values.nth(i)] : lane < 8 ? &sh.value_peer[values.nth(i)] : &sh.p_full;
+        if (!mbar_wait_warp(bar, lane < 8 ? values.parity(i) : (uint32_t)(gt & 1), abort)) return false;
+        tc_fence_after();
+        const uint32_t more = __shfl_sync(0xffffffffu, first ? 0u : 1u, 0);
+        const uint64_t v[4] = {dV + step(values.nth(0)), dV + step(values.nth(1)), dV + step(values.nth(2)), dV + step(values.nth(3))};
+        if (elect_one()) {
+#pragma unroll
+            for (int n = 0; n < 4; ++n) {
+                const int h = n >> 1, p = n & 1;
+                if constexpr (kBf16) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        mma_f16_pair(tmem + kColO + 128 * h, dP + ((p * S::kChunk + 32 * i) >> 4), v[n] + ((2048 * i) >> 4),
+                                     S::kIdescPV, (p | i) == 0 ? more : 1u);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+#pragma unroll
+                        for (int part = 0; part < 3; ++part)
+                            mma_f8_pair(tmem + kColO + 128 * h, dP + ((part * S::kChunk + 64 * p + 32 * i) >> 4),
+                                        v[n] + ((4096 * i) >> 4), S::kIdescPV, (p | i | part) == 0 ? more : 1u);
+                }
+                tc_commit_pair(&sh.value_empty[values.nth(n)]);
+            }
+            tc_commit_pair(&sh.pv_done);
+        }
+        __syncwarp();
+        values.step(4);
         return true;
     };
-    auto flags_of = [&](int gt) -> int {  // -1: gave up
-        if (!mbar_wait_warp(&sh.info_full[gt % kInfos], (uint32_t)((gt / kInfos) & 1), abort)) return -1;
-        return *(volatile int*)&sh.info[gt % kInfos].flags;
-    };
-    int flags = flags_of(0);
-    for (int gt = 0; flags >= 0 && !(flags & Info::kStop); ++gt) {
-        if (flags & Info::kFirst) {
-            if (!mbar_wait_cluster_warp(&sh.q_full[it & 1], (uint32_t)((it >> 1) & 1), abort)) return;
-            tc_fence_after();
-            ++it;
-            if (!scores(gt, flags & Info::kLast)) return;
+    for (int gt = 0;;) {
+        // a run's first tile, or the range's end
+        if (!info_wait(sh, gt, abort)) return;
+        if (*(volatile int*)&sh.info[gt % kInfos].flags & Info::kStop) return;
+        if (!mbar_wait_warp(&sh.q_full[it & 1], (uint32_t)((it >> 1) & 1), abort)) return;
+        ++it;
+        int flags = scores(gt);
+        for (bool first = true; flags >= 0; first = false, ++gt) {
+            const bool last = flags & Info::kLast;
+            if (!last && (flags = scores(gt + 1)) < 0) return;
+            if (!output(gt, first)) return;
+            if (last) break;
         }
-        const int next = flags_of(gt + 1);
-        if (next < 0) return;
-        if (!(flags & Info::kLast) && !scores(gt + 1, next & Info::kLast)) return;
-        if (!mbar_wait_cluster_warp(&sh.p_full, (uint32_t)(gt & 1), abort)) return;
-        tc_fence_after();
-        const uint32_t more = __shfl_sync(0xffffffffu, flags & Info::kFirst ? 0u : 1u, 0);
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int p = 0; p < 2; ++p) {
-                if (!landed()) return;
-                const uint64_t v = dV + place();
-                if (elect_one()) {
-                    if constexpr (kBf16) {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            mma_f16_pair(tmem + kColO + 128 * h, dP + ((p * S::kChunk + 32 * i) >> 4),
-                                         v + ((2048 * i) >> 4), S::kIdescPV, (p | i) == 0 ? more : 1u);
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 2; ++i)
-#pragma unroll
-                            for (int part = 0; part < 3; ++part)
-                                mma_f8_pair(tmem + kColO + 128 * h, dP + ((part * S::kChunk + 64 * p + 32 * i) >> 4),
-                                            v + ((4096 * i) >> 4), S::kIdescPV, (p | i | part) == 0 ? more : 1u);
-                    }
-                    tc_commit_pair(&sh.empty[slot]);
-                    if ((h & p) == 1) tc_commit_pair(&sh.pv_done);
-                }
-                __syncwarp();
-                used();
-            }
-        flags = next;
+        if (flags < 0) return;
+        ++gt;
     }
 }
 
 template <bool kBf16>
 __device__ void relay_role(Shared<kBf16>& sh, int lane, volatile int* abort) {
     using S = Shape<kBf16>;
-    int slot = 0;
-    uint32_t phase = 0;
-    for (int gt = 0;; ++gt) {
-        if (!mbar_wait_warp(&sh.info_full[gt % kInfos], (uint32_t)((gt / kInfos) & 1), abort)) return;
-        if (*(volatile int*)&sh.info[gt % kInfos].flags & Info::kStop) return;
-        for (int i = 0; i < 8; ++i) {  // (a tile has eight places)
-            if (!mbar_wait_warp(&sh.full[slot], phase, abort)) return;
-            fence_proxy_async_smem();
-            if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&sh.peer_full[slot]), 0));
-            __syncwarp();
-            if (++slot == S::kPlaces) slot = 0, phase ^= 1u;
+    Ring<S::kKeys> keys;
+    Ring<S::kValues> values;
+    const int i = lane & 3;
+    auto pass = [&](uint64_t* full, uint64_t* peer, uint32_t parity) {
+        if (!mbar_wait_warp(full, parity, abort)) return false;
+        if (lane < 4) mbar_arrive_peer(mapa_shared(smem_u32(peer), 0));
+        __syncwarp();
+        return true;
+    };
+    bool more = true;
+    for (int gt = 0; more; ++gt) {  // the values of a tile behind the keys of the next
+        if (!info_wait(sh, gt, abort)) return;
+        more = !(*(volatile int*)&sh.info[gt % kInfos].flags & Info::kStop);
+        info_done(sh, gt, lane);
+        if (more && !pass(&sh.key_full[keys.nth(i)], &sh.key_peer[keys.nth(i)], keys.parity(i))) return;
+        keys.step(4);
+        if (gt > 0) {
+            if (!pass(&sh.value_full[values.nth(i)], &sh.value_peer[values.nth(i)], values.parity(i))) return;
+            values.step(4);
         }
     }
 }
@@ -651,17 +701,15 @@ __device__ void relay_role(Shared<kBf16>& sh, int lane, volatile int* abort) {
 // Makes zeros of what is not finite of positions 32 quarter + (the bits of `which`) in this CTA's
 // places of V of tile gt. Called by a warp when PV of the tile before is done.
 template <bool kBf16>
-__device__ __noinline__ bool finite_values(Shared<kBf16>& sh, uint32_t which, int gt, int flags, int quarter, int lane,
+__device__ __noinline__ bool finite_values(Shared<kBf16>& sh, uint32_t which, int gt, int quarter, int lane,
                                            volatile int* abort) {
     using S = Shape<kBf16>;
-    // places filled before them: four a tile for V and for K, K of the next tile of the run among them
-    const int v0 = 8 * gt + (flags & Info::kLast ? 4 : 8);
     uint8_t* at[2];
     for (int h = 0; h < 2; ++h) {
-        const int g = v0 + 2 * h + (quarter >> 1), slot = g % S::kPlaces;
+        const int g = 4 * gt + 2 * h + (quarter >> 1), slot = g % S::kValues;
         // (what the place held before has been used: this is the phase that its barrier is in)
-        if (!mbar_wait_warp(&sh.full[slot], (uint32_t)((g / S::kPlaces) & 1), abort)) return false;
-        at[h] = sh.ring[slot];
+        if (!mbar_wait_warp(&sh.value_full[slot], (uint32_t)((g / S::kValues) & 1), abort)) return false;
+        at[h] = sh.values[slot];
     }
     constexpr int kUnits = kBf16 ? 32 : 16;  // of 16 bytes: 128 channels in each half
     if (lane < kUnits) {
@@ -704,7 +752,7 @@ __device__ void softmax_role(Shared<kBf16>& sh, const Args& a, uint32_t tmem, in
     Row row = {-1, 0, 0, 0};
     int runs = 0;
     for (int gt = 0;; ++gt) {
-        if (!mbar_wait_warp(&sh.info_full[gt % kInfos], (uint32_t)((gt / kInfos) & 1), abort)) return;
+        if (!info_wait(sh, gt, abort)) return;
         const Info& in = sh.info[gt % kInfos];
         const int flags = in.flags;
         if (flags & Info::kStop) return;
@@ -726,6 +774,7 @@ __device__ void softmax_role(Shared<kBf16>& sh, const Args& a, uint32_t tmem, in
             seen = in.ok[quarter] & (hi == 32 ? ~0u : (1u << hi) - 1u) & (lo == 32 ? 0u : ~0u << lo);
         }
         const bool all = __all_sync(0xffffffffu, seen == ~0u);
+        info_done(sh, gt, lane);
         if (!mbar_wait_warp(&sh.s_full[gt & 1], (uint32_t)((gt >> 1) & 1), abort)) return;
         tc_fence_after();
         uint32_t sv[32];
@@ -834,7 +883,7 @@ __device__ void softmax_role(Shared<kBf16>& sh, const Args& a, uint32_t tmem, in
         // A weight of zero takes nothing from a position, unless that is not finite: rows that do not see
         // a position must not notice what it holds. Its products with the queries tell. What is not finite
         // of it becomes zero for PV; the rows that see it have NaN (or, of -infinity, zero) weights.
-        if (which && !finite_values(sh, which, gt, flags, quarter, lane, abort)) return;
+        if (which && !finite_values(sh, which, gt, quarter, lane, abort)) return;
         fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
@@ -931,12 +980,20 @@ k_paged_shared(const __grid_constant__ Args a, const __grid_constant__ CUtensorM
     const int rank = (int)cluster_ctarank(), pair = blockIdx.x >> 1;
     volatile int* abort = &sh.abort;
     if (tid == 0) {
-        for (int i = 0; i < S::kPlaces; ++i) {
-            mbar_init(&sh.full[i], 1);
-            mbar_init(&sh.empty[i], 1);
-            mbar_init(&sh.peer_full[i], 1);
+        for (int i = 0; i < S::kKeys; ++i) {
+            mbar_init(&sh.key_full[i], 1);
+            mbar_init(&sh.key_empty[i], 1);
+            mbar_init(&sh.key_peer[i], 1);
         }
-        for (int i = 0; i < kInfos; ++i) mbar_init(&sh.info_full[i], 1);
+        for (int i = 0; i < S::kValues; ++i) {
+            mbar_init(&sh.value_full[i], 1);
+            mbar_init(&sh.value_empty[i], 1);
+            mbar_init(&sh.value_peer[i], 1);
+        }
+        for (int i = 0; i < kInfos; ++i) {
+            mbar_init(&sh.info_full[i], 1);
+            mbar_init(&sh.info_empty[i], S::kSoftWarps + 3);  // the softmax warps, the MMA warp, two loaders
+        }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sh.s_full[i], 1);
             mbar_init(&sh.q_full[i], 2 * S::kHelpWarps);
@@ -965,7 +1022,7 @@ k_paged_shared(const __grid_constant__ Args a, const __grid_constant__ CUtensorM
         softmax_role<kBf16>(sh, a, tmem, warp, lane, rank, pair, abort);
     } else if (warp == S::kMmaWarp) {
         if (rank == 0) {
-            mma_role<kBf16>(sh, tmem, abort);
+            mma_role<kBf16>(sh, tmem, lane, abort);
             // every MMA issued must finish before TMEM and shared memory are released
             __syncwarp();
             if (elect_one()) tc_commit_pair(&sh.drain);
@@ -973,8 +1030,12 @@ k_paged_shared(const __grid_constant__ Args a, const __grid_constant__ CUtensorM
         } else {
             relay_role<kBf16>(sh, lane, abort);
         }
-    } else if (warp == S::kTmaWarp) {
-        tma_role<kBf16>(sh, a, &tmap, lane, rank, pair, abort);
+    } else if (warp == S::kKeyWarp) {
+        load_role<kBf16, true>(sh, a, &tmap, lane, rank, abort);
+    } else if (warp == S::kValueWarp) {
+        load_role<kBf16, false>(sh, a, &tmap, lane, rank, abort);
+    } else if (warp == S::kPlanWarp) {
+        plan_role<kBf16>(sh, a, lane, rank, pair, abort);
     } else {
         query_role<kBf16>(sh, a, warp - S::kHelp0, lane, rank, abort);
     }
@@ -1154,6 +1215,7 @@ extern "C" int csa2_paged_attn_shared(const csa2_params* p, const csa2_pages* c,
     a.pairs = pairs;
     a.box_rows = a.g.page_size & -a.g.page_size;
     if (a.box_rows > kMine) a.box_rows = kMine;
+    while ((1 << a.box_shift) < a.box_rows) ++a.box_shift;
     CUtensorMap rows = {};
     if (const int rc = encode_rows("paged_attn_shared", a.g, a.base, a.box_rows, &rows)) return rc;
     const bool bf16 = p->kv_format == CSA2_BF16;

@@ -184,6 +184,13 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];\n" ::"r"(cluster_addr)
                  : "memory");
 }
+// The same for what another proxy reads: the MMAs of a pair read shared memory that this thread has
+// put behind a proxy fence, or that a bulk copy has filled, so the arrive need not order memory for
+// the threads of the other CTA. (k_paged_shared, 38 sequences of 64 heads behind 65,536 positions: 667 us
+// with the form above, whose release took 800 to 1,000 cycles each time.)
+__device__ __forceinline__ void mbar_arrive_peer(uint32_t cluster_addr) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];\n" ::"r"(cluster_addr) : "memory");
+}
 __device__ __forceinline__ bool mbar_try_wait_acq_cluster(uint64_t* bar, uint32_t parity) {
     uint32_t ok;
     asm volatile(
@@ -193,15 +200,6 @@ __device__ __forceinline__ bool mbar_try_wait_acq_cluster(uint64_t* bar, uint32_
         : "r"(smem_u32(bar)), "r"(parity)
         : "memory");
     return ok != 0;
-}
-// mbar_wait_warp for such a phase.
-__device__ __forceinline__ bool mbar_wait_cluster_warp(uint64_t* bar, uint32_t parity, volatile int* abort) {
-    for (uint32_t i = 0; i < kSpinLimit; ++i) {
-        if (__all_sync(0xffffffffu, mbar_try_wait_acq_cluster(bar, parity))) return true;
-        if ((i & 255u) == 255u && __any_sync(0xffffffffu, *abort != 0)) return false;
-    }
-    *abort = 1;
-    return false;
 }
 // Bounded wait for a phase whose arrivals come from other CTAs of the cluster.
 __device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity) {
