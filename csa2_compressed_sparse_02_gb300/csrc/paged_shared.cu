@@ -334,6 +334,20 @@ struct Shared {
     int abort;
 };
 
+// mbar_wait_warp with the loop out of line: the roles' code runs side by side, and together it has to
+// fit the instruction cache (see the note at the kernel).
+__device__ __noinline__ bool wait_on(uint32_t bar, uint32_t parity, volatile int* abort) {
+    for (uint32_t i = 0; i < kSpinLimit; ++i) {
+        if (__all_sync(0xffffffffu, mbar_try_wait_at(bar, parity))) return true;
+        if ((i & 255u) == 255u && __any_sync(0xffffffffu, *abort != 0)) return false;
+    }
+    *abort = 1;
+    return false;
+}
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
+    return __all_sync(0xffffffffu, mbar_try_wait_at(smem_u32(bar), parity)) || wait_on(smem_u32(bar), parity, abort);
+}
+
 // An arrive on the even CTA's barrier, from either CTA of the pair.
 __device__ __forceinline__ void arrive_lead(uint64_t* bar, uint32_t rank) {
     if (rank == 0) mbar_arrive(bar);
@@ -374,7 +388,7 @@ __device__ void plan_role(Shared<kBf16>& sh, const Args& a, int lane, int rank, 
         if (more) box_nx = look(nxt);
         const bool ends = !more || nxt.u0 != cur.u0 || nxt.f != cur.f;
         const bool last = ends || run == S::kRun - 1;
-        if (gt >= kInfos && !mbar_wait_warp(&sh.info_empty[gt % kInfos], (uint32_t)((gt / kInfos - 1) & 1), abort)) return;
+        if (gt >= kInfos && !wait(&sh.info_empty[gt % kInfos], (uint32_t)((gt / kInfos - 1) & 1), abort)) return;
         const bool there = box.nth >= 0 && box.page >= 0 && box.page < a.g.n_pages;
         if (box.nth >= 0 && !there && rank == 0) raise_status(a.dev_status, CSA2_DEV_BAD_INDEX);
         const uint32_t held = __ballot_sync(0xffffffffu, there);
@@ -412,7 +426,7 @@ __device__ void plan_role(Shared<kBf16>& sh, const Args& a, int lane, int rank, 
         box = box_nx;
     }
     if (range.items <= 0 && lane == 0 && rank == 0) a.ends[pair] = make_int4(0, 0, 0, 0);
-    if (gt >= kInfos && !mbar_wait_warp(&sh.info_empty[gt % kInfos], (uint32_t)((gt / kInfos - 1) & 1), abort)) return;
+    if (gt >= kInfos && !wait(&sh.info_empty[gt % kInfos], (uint32_t)((gt / kInfos - 1) & 1), abort)) return;
     if (lane == 0) {
         sh.info[gt % kInfos].flags = Info::kStop;
         mbar_arrive(&sh.info_full[gt % kInfos]);
@@ -422,7 +436,7 @@ __device__ void plan_role(Shared<kBf16>& sh, const Args& a, int lane, int rank, 
 // The tile's entry, as a warp reads it; false: the wait gave up.
 template <bool kBf16>
 __device__ __forceinline__ bool info_wait(Shared<kBf16>& sh, int gt, volatile int* abort) {
-    return mbar_wait_warp(&sh.info_full[gt % kInfos], (uint32_t)((gt / kInfos) & 1), abort);
+    return wait(&sh.info_full[gt % kInfos], (uint32_t)((gt / kInfos) & 1), abort);
 }
 template <bool kBf16>
 __device__ __forceinline__ void info_done(Shared<kBf16>& sh, int gt, int lane) {
@@ -433,14 +447,14 @@ __device__ __forceinline__ void info_done(Shared<kBf16>& sh, int gt, int lane) {
 // ---------------------------------------------------------------- copies
 // One warp copies the keys, one the values, box by box. One elected lane issues, from values of the
 // whole warp.
-template <bool kBf16, bool kKeys>
-__device__ void load_role(Shared<kBf16>& sh, const Args& a, const CUtensorMap* tmap, int lane, int rank,
-                          volatile int* abort) {
+template <bool kBf16>
+__device__ __noinline__ void load_role(Shared<kBf16>& sh, const Args& a, const CUtensorMap* tmap, bool keys, int lane,
+                                       int rank, volatile int* abort) {
     using S = Shape<kBf16>;
-    constexpr int kPlaces = kKeys ? S::kKeys : S::kValues;
-    uint64_t* const full = kKeys ? sh.key_full : sh.value_full;
-    uint64_t* const empty = kKeys ? sh.key_empty : sh.value_empty;
-    const uint32_t ring = smem_u32(kKeys ? sh.keys[0] : sh.values[0]);
+    const int places = keys ? S::kKeys : S::kValues;
+    uint64_t* const full = keys ? sh.key_full : sh.value_full;
+    uint64_t* const empty = keys ? sh.key_empty : sh.value_empty;
+    const uint32_t ring = smem_u32(keys ? sh.keys[0] : sh.values[0]);
     const int shift = a.box_shift;
     int slot = 0, g = 0;
     uint32_t phase = 1;  // of a place that is free
@@ -450,22 +464,17 @@ __device__ void load_role(Shared<kBf16>& sh, const Args& a, const CUtensorMap* t
         if (in.flags & Info::kStop) break;
         const int y = in.y[lane & 15];
         info_done(sh, gt, lane);
-        bool good = true;
-#pragma unroll
-        for (int i = 0; i < 4 && good; ++i) {
+        int i = 0;
+#pragma unroll 1
+        for (; i < 4; ++i) {
             // 64 positions from `first` of the tile, 128 channels from x
-            const int first = kKeys ? kMine * rank : kMine * (i & 1);
-            const int x = kKeys ? 128 * i : 256 * (i >> 1) + 128 * rank;
-            good = g < kPlaces || mbar_wait_warp(&empty[slot], phase, abort);
-            if (!good) break;
+            const int first = keys ? kMine * rank : kMine * (i & 1);
+            const int x = keys ? 128 * i : 256 * (i >> 1) + 128 * rank;
+            if (g >= places && !wait(&empty[slot], phase, abort)) break;
             const uint32_t at = ring + (uint32_t)__shfl_sync(0xffffffffu, slot, 0) * S::kPlace;
-            const int y0 = __shfl_sync(0xffffffffu, y, first >> shift);
-            if (elect_one()) {
-                mbar_arrive_expect_tx(&full[slot], S::kPlace);
-                tma_g2s_2d(at, tmap, x, y0, &full[slot]);
-                if constexpr (kBf16) tma_g2s_2d(at + S::kChunk, tmap, x + 64, y0, &full[slot]);
-            }
-            for (int b = a.box_rows; b < kMine; b += a.box_rows) {
+            if (elect_one()) mbar_arrive_expect_tx(&full[slot], S::kPlace);
+#pragma unroll 1
+            for (int b = 0; b < kMine; b += a.box_rows) {
                 const int yb = __shfl_sync(0xffffffffu, y, (first + b) >> shift);
                 if (elect_one()) {
                     tma_g2s_2d(at + b * 128, tmap, x, yb, &full[slot]);
@@ -474,12 +483,12 @@ __device__ void load_role(Shared<kBf16>& sh, const Args& a, const CUtensorMap* t
             }
             __syncwarp();
             ++g;
-            if (++slot == kPlaces) slot = 0, phase ^= 1u;
+            if (++slot == places) slot = 0, phase ^= 1u;
         }
-        if (!good) break;
+        if (i < 4) break;
     }
     // whatever ended the loop, no copy of this CTA outlives it
-    for (int s = max(0, g - kPlaces); s < g; ++s) mbar_wait_drain(&full[s % kPlaces], (uint32_t)((s / kPlaces) & 1));
+    for (int s = max(0, g - places); s < g; ++s) mbar_wait_drain(&full[s % places], (uint32_t)((s / places) & 1));
 }
 
 // ---------------------------------------------------------------- queries
@@ -499,7 +508,7 @@ __device__ void query_role(Shared<kBf16>& sh, const Args& a, int warp, int lane,
         u0 = t.u0;
         f = t.f;
         run = 1;
-        if (it > 0 && !mbar_wait_warp(&sh.q_empty, (uint32_t)((it - 1) & 1), abort)) return;
+        if (it > 0 && !wait(&sh.q_empty, (uint32_t)((it - 1) & 1), abort)) return;
         const Row mine = row_info(a, u0, f, kMine * rank + kEach * warp + (lane & (kEach - 1)));
 #pragma unroll 4
         for (int i = 0; i < kEach; ++i) {
@@ -568,7 +577,7 @@ struct Ring {
     uint32_t phase = 0;
     __device__ __forceinline__ int nth(int i) const { return slot + i < kPlaces ? slot + i : slot + i - kPlaces; }
     __device__ __forceinline__ uint32_t parity(int i) const { return slot + i < kPlaces ? phase : phase ^ 1u; }
-    __device__ __forceinline__ void step(int n) {
+    __device__ __forceinline__ void step(int n = 1) {
         if ((slot += n) >= kPlaces) slot -= kPlaces, phase ^= 1u;
     }
 };
@@ -576,98 +585,105 @@ struct Ring {
 template <bool kBf16>
 __device__ void mma_role(Shared<kBf16>& sh, uint32_t tmem, int lane, volatile int* abort) {
     using S = Shape<kBf16>;
-    const uint64_t dQ = smem_desc(smem_u32(sh.q), 16, 1024, kLayoutSw128);
-    const uint64_t dP = smem_desc(smem_u32(sh.p), 16, 1024, kLayoutSw128);
-    const uint64_t dK = smem_desc(smem_u32(sh.keys[0]), 16, 1024, kLayoutSw128);
-    const uint64_t dV = smem_desc(smem_u32(sh.values[0]), S::kChunk, 1024, kLayoutSw128);
+    // (the leading offset of V is in the low word)
+    constexpr uint32_t kHigh = (1024u >> 4) | (1u << 14) | (kLayoutSw128 << 29);
+    const uint32_t dQ = (uint32_t)smem_desc(smem_u32(sh.q), 16, 1024, kLayoutSw128);
+    const uint32_t dP = (uint32_t)smem_desc(smem_u32(sh.p), 16, 1024, kLayoutSw128);
+    const uint32_t dK = (uint32_t)smem_desc(smem_u32(sh.keys[0]), 16, 1024, kLayoutSw128);
+    const uint32_t dV = (uint32_t)smem_desc(smem_u32(sh.values[0]), S::kChunk, 1024, kLayoutSw128);
     Ring<S::kKeys> keys;
     Ring<S::kValues> values;
     int it = 0;
-    auto step = [](int slot) { return (uint64_t)__shfl_sync(0xffffffffu, (uint32_t)slot * (S::kPlace >> 4), 0); };
+    auto step = [](int slot) { return __shfl_sync(0xffffffffu, (uint32_t)slot * (S::kPlace >> 4), 0); };
     // S of tile gt; returns its flags, -1: gave up
     auto scores = [&](int gt) -> int {
         const int i = lane & 3;
         uint64_t* const bar = lane < 4 ? &sh.key_full[keys.nth(i)] : lane < 8 ? &sh.key_peer[keys.nth(i)] : &sh.info_full[gt % kInfos];
-        if (!mbar_wait_warp(bar, lane < 8 ? keys.parity(i) : (uint32_t)((gt / kInfos) & 1), abort)) return -1;
+        if (!wait(bar, lane < 8 ? keys.parity(i) : (uint32_t)((gt / kInfos) & 1), abort)) return -1;
         tc_fence_after();
         const int flags = *(volatile int*)&sh.info[gt % kInfos].flags;
         info_done(sh, gt, lane);
         const uint32_t at = tmem + kColS + (uint32_t)__shfl_sync(0xffffffffu, gt & 1, 0) * 64u;
-        const uint64_t k[4] = {dK + step(keys.nth(0)), dK + step(keys.nth(1)), dK + step(keys.nth(2)), dK + step(keys.nth(3))};
-        if (elect_one()) {
-#pragma unroll
-            for (int d = 0; d < 4; ++d) {
+#pragma unroll 1
+        for (int d = 0; d < 4; ++d) {
+            const uint32_t k = dK + step(keys.slot), q = dQ + d * ((kBf16 ? 2 * S::kChunk : S::kChunk) >> 4);
+            if (elect_one()) {
                 if constexpr (kBf16) {
 #pragma unroll
                     for (int c = 0; c < 2; ++c)
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
-                            mma_f16_pair(at, dQ + (((2 * d + c) * S::kChunk + 32 * i) >> 4),
-                                         k[d] + ((c * S::kChunk + 32 * i) >> 4), S::kIdescS, (d | c | i) != 0);
+                            mma_f16_pair(at, q + ((c * S::kChunk + 32 * i) >> 4), kHigh, k + ((c * S::kChunk + 32 * i) >> 4),
+                                         kHigh, S::kIdescS, (c | i) != 0 ? 1u : (uint32_t)(d != 0));
                 } else {
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
 #pragma unroll
                         for (int part = 0; part < 2; ++part)
-                            mma_f8_pair(at, dQ + (((4 * part + d) * S::kChunk + 32 * i) >> 4), k[d] + ((32 * i) >> 4),
-                                        S::kIdescS, (d | i | part) != 0);
+                            mma_f8_pair(at, q + ((4 * part * S::kChunk + 32 * i) >> 4), kHigh, k + ((32 * i) >> 4), kHigh,
+                                        S::kIdescS, (i | part) != 0 ? 1u : (uint32_t)(d != 0));
                 }
-                tc_commit_pair(&sh.key_empty[keys.nth(d)]);
+                tc_commit_pair(&sh.key_empty[keys.slot]);
             }
+            __syncwarp();
+            keys.step();
+        }
+        if (elect_one()) {
             tc_commit_pair(&sh.s_full[gt & 1]);
             if (flags & Info::kLast) tc_commit_pair(&sh.q_empty);
         }
         __syncwarp();
-        keys.step(4);
         return flags;
     };
     auto output = [&](int gt, bool first) {
         const int i = lane & 3;
         uint64_t* const bar = lane < 4 ? &sh.value_full[values.nth(i)] : lane < 8 ? &sh.value_peer[values.nth(i)] : &sh.p_full;
-        if (!mbar_wait_warp(bar, lane < 8 ? values.parity(i) : (uint32_t)(gt & 1), abort)) return false;
+        if (!wait(bar, lane < 8 ? values.parity(i) : (uint32_t)(gt & 1), abort)) return false;
         tc_fence_after();
-        const uint32_t more = __shfl_sync(0xffffffffu, first ? 0u : 1u, 0);
-        const uint64_t v[4] = {dV + step(values.nth(0)), dV + step(values.nth(1)), dV + step(values.nth(2)), dV + step(values.nth(3))};
-        if (elect_one()) {
-#pragma unroll
-            for (int n = 0; n < 4; ++n) {
-                const int h = n >> 1, p = n & 1;
+#pragma unroll 1
+        for (int n = 0; n < 4; ++n) {
+            const uint32_t v = dV + step(values.slot), p = dP + (n & 1) * ((kBf16 ? S::kChunk : 64u) >> 4);
+            const uint32_t o = tmem + kColO + 128 * (n >> 1), more = (n & 1) || !first;
+            if (elect_one()) {
                 if constexpr (kBf16) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        mma_f16_pair(tmem + kColO + 128 * h, dP + ((p * S::kChunk + 32 * i) >> 4), v[n] + ((2048 * i) >> 4),
-                                     S::kIdescPV, (p | i) == 0 ? more : 1u);
+                        mma_f16_pair(o, p + ((32 * i) >> 4), kHigh, v + ((2048 * i) >> 4), kHigh, S::kIdescPV, i == 0 ? more : 1u);
                 } else {
 #pragma unroll
                     for (int i = 0; i < 2; ++i)
 #pragma unroll
                         for (int part = 0; part < 3; ++part)
-                            mma_f8_pair(tmem + kColO + 128 * h, dP + ((part * S::kChunk + 64 * p + 32 * i) >> 4),
-                                        v[n] + ((4096 * i) >> 4), S::kIdescPV, (p | i | part) == 0 ? more : 1u);
+                            mma_f8_pair(o, p + ((part * S::kChunk + 32 * i) >> 4), kHigh, v + ((4096 * i) >> 4), kHigh,
+                                        S::kIdescPV, (i | part) == 0 ? more : 1u);
                 }
-                tc_commit_pair(&sh.value_empty[values.nth(n)]);
+                tc_commit_pair(&sh.value_empty[values.slot]);
+                if (n == 3) tc_commit_pair(&sh.pv_done);
             }
-            tc_commit_pair(&sh.pv_done);
+            __syncwarp();
+            values.step();
         }
-        __syncwarp();
-        values.step(4);
         return true;
     };
-    for (int gt = 0;;) {
-        // a run's first tile, or the range's end
-        if (!info_wait(sh, gt, abort)) return;
-        if (*(volatile int*)&sh.info[gt % kInfos].flags & Info::kStop) return;
-        if (!mbar_wait_warp(&sh.q_full[it & 1], (uint32_t)((it >> 1) & 1), abort)) return;
-        ++it;
-        int flags = scores(gt);
-        for (bool first = true; flags >= 0; first = false, ++gt) {
-            const bool last = flags & Info::kLast;
-            if (!last && (flags = scores(gt + 1)) < 0) return;
-            if (!output(gt, first)) return;
-            if (last) break;
+    // S of tile n, one tile ahead of PV of tile o within a run (the next run's query comes after this
+    // one's last S)
+    bool first = true, last = true;  // o is a run's first tile, n - 1 its last
+    for (int n = 0, o = 0;;) {
+        if (n == o || !last) {
+            if (n == o && last) {  // a run begins, or the range is done
+                if (!info_wait(sh, n, abort)) return;
+                if (*(volatile int*)&sh.info[n % kInfos].flags & Info::kStop) return;
+                if (!wait(&sh.q_full[it & 1], (uint32_t)((it >> 1) & 1), abort)) return;
+                ++it;
+                first = true;
+            }
+            const int flags = scores(n);
+            if (flags < 0) return;
+            last = flags & Info::kLast;
+            if (n++ == o && !last) continue;
         }
-        if (flags < 0) return;
-        ++gt;
+        if (!output(o++, first)) return;
+        first = false;
     }
 }
 
@@ -678,7 +694,7 @@ __device__ void relay_role(Shared<kBf16>& sh, int lane, volatile int* abort) {
     Ring<S::kValues> values;
     const int i = lane & 3;
     auto pass = [&](uint64_t* full, uint64_t* peer, uint32_t parity) {
-        if (!mbar_wait_warp(full, parity, abort)) return false;
+        if (!wait(full, parity, abort)) return false;
         if (lane < 4) mbar_arrive_peer(mapa_shared(smem_u32(peer), 0));
         __syncwarp();
         return true;
@@ -708,7 +724,7 @@ __device__ __noinline__ bool finite_values(Shared<kBf16>& sh, uint32_t which, in
     for (int h = 0; h < 2; ++h) {
         const int g = 4 * gt + 2 * h + (quarter >> 1), slot = g % S::kValues;
         // (what the place held before has been used: this is the phase that its barrier is in)
-        if (!mbar_wait_warp(&sh.value_full[slot], (uint32_t)((g / S::kValues) & 1), abort)) return false;
+        if (!wait(&sh.value_full[slot], (uint32_t)((g / S::kValues) & 1), abort)) return false;
         at[h] = sh.values[slot];
     }
     constexpr int kUnits = kBf16 ? 32 : 16;  // of 16 bytes: 128 channels in each half
@@ -761,7 +777,7 @@ __device__ void softmax_role(Shared<kBf16>& sh, const Args& a, uint32_t tmem, in
             m = -INFINITY;
             l = 0.f;
             if constexpr (!kBf16) {
-                if (!mbar_wait_warp(&sh.q_here[runs & 1], (uint32_t)((runs >> 1) & 1), abort)) return;
+                if (!wait(&sh.q_here[runs & 1], (uint32_t)((runs >> 1) & 1), abort)) return;
                 c = sh.row_scale[runs & 1][r];
             }
             ++runs;
@@ -775,7 +791,7 @@ __device__ void softmax_role(Shared<kBf16>& sh, const Args& a, uint32_t tmem, in
         }
         const bool all = __all_sync(0xffffffffu, seen == ~0u);
         info_done(sh, gt, lane);
-        if (!mbar_wait_warp(&sh.s_full[gt & 1], (uint32_t)((gt >> 1) & 1), abort)) return;
+        if (!wait(&sh.s_full[gt & 1], (uint32_t)((gt >> 1) & 1), abort)) return;
         tc_fence_after();
         uint32_t sv[32];
         tmem_ld_32x32b_x32(tl + kColS + 64 * (gt & 1) + 32 * ch, sv);
@@ -804,7 +820,7 @@ __device__ void softmax_role(Shared<kBf16>& sh, const Args& a, uint32_t tmem, in
         sh.red_max[gt & 1][quarter][r] = top;
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.max_bar[grp]);
-        if (!mbar_wait_warp(&sh.max_bar[grp], (uint32_t)(gt & 1), abort)) return;
+        if (!wait(&sh.max_bar[grp], (uint32_t)(gt & 1), abort)) return;
         top = fmaxf(fmaxf(sh.red_max[gt & 1][0][r], sh.red_max[gt & 1][1][r]),
                     fmaxf(sh.red_max[gt & 1][2][r], sh.red_max[gt & 1][3][r]));
         float alpha = 1.f;
@@ -854,7 +870,7 @@ __device__ void softmax_role(Shared<kBf16>& sh, const Args& a, uint32_t tmem, in
         }
         l = fmaf(l, alpha, sum + sum2);
         // after PV of the tile before P may be written again, and O rescaled
-        if (!(flags & Info::kFirst) && !mbar_wait_warp(&sh.pv_done, (uint32_t)((gt - 1) & 1), abort)) return;
+        if (!(flags & Info::kFirst) && !wait(&sh.pv_done, (uint32_t)((gt - 1) & 1), abort)) return;
         if (__any_sync(0xffffffffu, alpha != 1.f)) {
             tc_fence_after();
 #pragma unroll 1
@@ -891,12 +907,12 @@ __device__ void softmax_role(Shared<kBf16>& sh, const Args& a, uint32_t tmem, in
         if (!(flags & Info::kLast)) continue;
 
         // ---- the run's end: this thread has 128 channels of its row, 256 ch + 128 (qd >> 1) and on
-        if (!mbar_wait_warp(&sh.pv_done, (uint32_t)(gt & 1), abort)) return;
+        if (!wait(&sh.pv_done, (uint32_t)(gt & 1), abort)) return;
         tc_fence_after();
         sh.red_sum[quarter][r] = l;
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.sum_bar[grp]);
-        if (!mbar_wait_warp(&sh.sum_bar[grp], (uint32_t)((runs - 1) & 1), abort)) return;
+        if (!wait(&sh.sum_bar[grp], (uint32_t)((runs - 1) & 1), abort)) return;
         float total = (sh.red_sum[0][r] + sh.red_sum[1][r]) + (sh.red_sum[2][r] + sh.red_sum[3][r]);
         float top_of = m - S::kLift;  // what P and O are relative to
         float was = 0.f, now = 1.f;
@@ -1030,10 +1046,8 @@ k_paged_shared(const __grid_constant__ Args a, const __grid_constant__ CUtensorM
         } else {
             relay_role<kBf16>(sh, lane, abort);
         }
-    } else if (warp == S::kKeyWarp) {
-        load_role<kBf16, true>(sh, a, &tmap, lane, rank, abort);
-    } else if (warp == S::kValueWarp) {
-        load_role<kBf16, false>(sh, a, &tmap, lane, rank, abort);
+    } else if (warp == S::kKeyWarp || warp == S::kValueWarp) {
+        load_role<kBf16>(sh, a, &tmap, warp == S::kKeyWarp, lane, rank, abort);
     } else if (warp == S::kPlanWarp) {
         plan_role<kBf16>(sh, a, lane, rank, pair, abort);
     } else {

@@ -39,6 +39,17 @@ __device__ __forceinline__ bool mbar_try_wait(uint64_t* bar, uint32_t parity) {
     return ok != 0;
 }
 
+__device__ __forceinline__ bool mbar_try_wait_at(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+        " selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
 // Each try_wait suspends for a hardware-chosen slice; 2^22 of them is well over
 // a second on any load this library generates.
 constexpr uint32_t kSpinLimit = 1u << 22;
@@ -543,22 +554,20 @@ __device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols
     __syncwarp();  // .sync.aligned: the whole warp, converged
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;\n" ::"r"(taddr), "r"(ncols) : "memory");
 }
-__device__ __forceinline__ void mma_f16_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
-                                             uint32_t accumulate) {
-    asm volatile(
-        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-        " tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
-        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
-        : "memory");
-}
-__device__ __forceinline__ void mma_f8_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
-                                            uint32_t accumulate) {
-    asm volatile(
-        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-        " tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
-        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
-        : "memory");
-}
+// A descriptor comes as its low word, which holds the address, and its high word, the same for all
+// steps of an operand: 32-bit sums, which stay in the warp's uniform registers.
+#define CSA2_MMA_PAIR(name, kind)                                                                                  \
+    __device__ __forceinline__ void name(uint32_t d_tmem, uint32_t a, uint32_t a_high, uint32_t b, uint32_t b_high, \
+                                         uint32_t idesc, uint32_t accumulate) {                                    \
+        asm volatile(                                                                                              \
+            "{\n .reg .pred p;\n .reg .b64 da, db;\n mov.b64 da, {%1, %2};\n mov.b64 db, {%3, %4};\n"               \
+            " setp.ne.b32 p, %6, 0;\n tcgen05.mma.cta_group::2.kind::" kind " [%0], da, db, %5, p;\n}\n" ::"r"(d_tmem), \
+            "r"(a), "r"(a_high), "r"(b), "r"(b_high), "r"(idesc), "r"(accumulate)                                  \
+            : "memory");                                                                                           \
+    }
+CSA2_MMA_PAIR(mma_f16_pair, "f16")
+CSA2_MMA_PAIR(mma_f8_pair, "f8f6f4")
+#undef CSA2_MMA_PAIR
 // Arrive on the mbarrier at this offset in both CTAs once every pair operation this thread issued so
 // far completes.
 __device__ __forceinline__ void tc_commit_pair(uint64_t* bar) {
