@@ -39,7 +39,7 @@ struct Args {
     const float* sink;
     const int32_t *seq, *n_tokens, *order, *first, *shared;
     __nv_bfloat16* out;
-    int4* ends;       // workspace: of each pair, how its range ends and with which unit [pairs]
+    int32_t* ends;    // workspace: of each pair, how its range ends [pairs]
     float* part;      // workspace: two partial results per pair
     int32_t* dev_status;
     float scale_log2;
@@ -51,30 +51,32 @@ struct Args {
 // How a pair's range ends: its last unit goes on behind it; is its only one; and began before it.
 enum { kCut = 1, kSingle = 2, kThrough = 4 };
 
-// A partial result: O as [512 / 4][128 rows] float4, then m [128] and l [128].
-constexpr int kPartFloats = kRows * (kD + 2);
+// A partial result: O as [512 / 4][128 rows] float4, then m [128], l [128] and the rows' places in the
+// output [128] (sequence x heads + head, -1: none).
+constexpr int kPartFloats = kRows * (kD + 3);
 
 __device__ __forceinline__ float* part_of(const Args& a, int pair, int slot) {
     return a.part + (2 * (int64_t)pair + slot) * kPartFloats;
 }
 
 // ---------------------------------------------------------------- the batch
-// Slot i of the order: sequence b of the call with T positions in row `row` of the table (T = 0:
-// nothing to see), in the group that begins at slot f and shares `sh` positions, which are read
-// through row `prow`.
+// Slot i of the order: sequence b of the call (-1: padding, whose output is left as it is) with T
+// positions in row `row` of the table (T = 0: nothing to see), in the group that begins at slot f and
+// shares `sh` positions, which are read through row `prow`.
 struct Slot {
     int b, T, row, f, sh, prow;
 };
 
+// Sequence b's row of the table: -1 padding, INT_MAX out of range.
 __device__ __forceinline__ int row_of(const Args& a, int b, bool report) {
     if (b < 0 || b >= a.B) {
         if (report) raise_status(a.dev_status, CSA2_DEV_BAD_INDEX);
         return -1;
     }
     const int row = a.seq ? a.seq[b] : b;
-    if (row < a.g.max_seqs) return row;
+    if (row < a.g.max_seqs) return max(row, -1);
     if (report) raise_status(a.dev_status, CSA2_DEV_BAD_INDEX);
-    return -1;
+    return INT_MAX;
 }
 
 __device__ __forceinline__ int length_of(const Args& a, int64_t n, bool report) {
@@ -97,8 +99,11 @@ __device__ __forceinline__ Slot slot_of(const Args& a, int i, bool report) {
     s.f = first_of(a, i, report);
     s.sh = length_of(a, a.shared[s.f], report && s.f == i);
     s.row = row_of(a, s.b, report);
+    if (s.row < 0) s.b = -1;
+    if (s.row == INT_MAX) s.row = -1;
     s.T = s.row < 0 ? 0 : length_of(a, a.n_tokens[s.b], report);
     s.prow = row_of(a, a.order[s.f], false);
+    if (s.prow == INT_MAX) s.prow = -1;
     return s;
 }
 
@@ -121,7 +126,10 @@ struct Range {
     bool cont, cut;    // its first unit began before it; its last one ends behind it
 };
 
+constexpr int kKept = 192;  // slots that stay in shared memory
+
 struct PlanShared {
+    Slot slots[kKept];
     int64_t warp_sum[32];
     long long begin, end;  // where the first tile's unit begins, and the last one's ends
     Range range;
@@ -150,6 +158,7 @@ __device__ void plan(const Args& a, PlanShared& sh, int pair) {
         *head = false;
         if (i >= a.B) return 0;
         const Slot s = slot_of(a, i, report);
+        if (i < kKept) sh.slots[i] = s;
         *head = unit_of(a, i, s.f) == i;
         return (uint32_t)prefix_tiles(a, s, i) + own_tiles(s);
     };
@@ -192,7 +201,7 @@ __device__ void plan(const Args& a, PlanShared& sh, int pair) {
     __syncthreads();
 }
 
-// A range tile by tile, by a whole warp: each lane holds one of 32 neighbouring slots.
+// A range tile by tile.
 struct Tile {
     int t0, lo, hi;  // positions t0 .. t0 + 127, of which [lo, hi) are seen
     int row;         // of the table
@@ -201,26 +210,17 @@ struct Tile {
 };
 struct Walk {
     const Args& a;
+    const PlanShared& plan;
     int64_t left;
-    int i, j, base;
-    Slot mine, s;  // of lane's slot, of slot i
+    int i, j;
+    Slot s;  // of slot i
     int pre, items, u0;
-    __device__ __forceinline__ Walk(const Args& a, const Range& r)
-        : a(a), left(r.items), i(r.i), j(r.j), base(-1) {
+    __device__ __forceinline__ Walk(const Args& a, const PlanShared& plan)
+        : a(a), plan(plan), left(plan.range.items), i(plan.range.i), j(plan.range.j) {
         if (left > 0) enter();
     }
     __device__ __forceinline__ void enter() {
-        if ((i & ~31) != base) {
-            base = i & ~31;
-            const int at = base + (threadIdx.x & 31);
-            mine = at < a.B ? slot_of(a, at, false) : Slot{0, 0, -1, at, 0, -1};
-        }
-        const int l = i & 31;
-        s.T = __shfl_sync(0xffffffffu, mine.T, l);
-        s.row = __shfl_sync(0xffffffffu, mine.row, l);
-        s.f = __shfl_sync(0xffffffffu, mine.f, l);
-        s.sh = __shfl_sync(0xffffffffu, mine.sh, l);
-        s.prow = __shfl_sync(0xffffffffu, mine.prow, l);
+        s = i < kKept ? plan.slots[i] : slot_of(a, i, false);
         u0 = unit_of(a, i, s.f);
         pre = u0 == i ? tiles_of(s.sh) : 0;
         items = pre + own_tiles(s);
@@ -250,20 +250,18 @@ struct Walk {
 struct Row {
     int b, h, k, T;
 };
-__device__ __forceinline__ Row row_info(const Args& a, int u0, int f, int r) {
+__device__ __noinline__ Row row_info(const Args& a, const PlanShared& plan, int u0, int f, int r) {
     Row x;
     x.k = r / a.heads;
     x.h = r - x.k * a.heads;
     x.b = -1;
     x.T = 0;
     const int i = u0 + x.k;
-    if (x.k >= a.members || i >= a.B || first_of(a, i, false) != f) return x;
-    const int b = a.order[i];
-    if (b < 0 || b >= a.B) return x;
-    const int row = a.seq ? a.seq[b] : b;
-    if (row < 0) return x;  // padding: its output is left as it is
-    x.b = b;
-    if (row < a.g.max_seqs) x.T = length_of(a, a.n_tokens[b], false);
+    if (x.k >= a.members || i >= a.B) return x;
+    const Slot s = i < kKept ? plan.slots[i] : slot_of(a, i, false);
+    if (s.f != f) return x;
+    x.b = s.b;
+    x.T = s.T;
     return x;
 }
 
@@ -364,7 +362,7 @@ __device__ void plan_role(Shared<kBf16>& sh, const Args& a, int lane, int rank, 
     const int br = a.box_rows, shift = a.box_shift, ps = a.g.page_size;
     const int pos = lane << shift;  // of this lane's box in the tile
     const Range range = sh.plan.range;
-    Walk walk(a, range);
+    Walk walk(a, sh.plan);
     int run = 0, runs = 0, pieces = 0;
     // this lane's box: its page's entry is on its way while the tile before is told
     struct Box {
@@ -418,14 +416,13 @@ __device__ void plan_role(Shared<kBf16>& sh, const Args& a, int lane, int rank, 
         if (last) run = 0, ++runs;
         if (ends) runs = 0, ++pieces;
         has = more;
-        // for the join: the unit that the range ends with, and whether it is cut there and before
+        // for the join
         if (!more && lane == 0 && rank == 0)
-            a.ends[pair] = make_int4((range.cut ? kCut : 0) | (pieces == 1 ? kSingle : 0) |
-                                     (pieces == 1 && range.cont ? kThrough : 0), cur.u0, cur.f, 0);
+            a.ends[pair] = (range.cut ? kCut : 0) | (pieces == 1 ? kSingle : 0) | (pieces == 1 && range.cont ? kThrough : 0);
         cur = nxt;
         box = box_nx;
     }
-    if (range.items <= 0 && lane == 0 && rank == 0) a.ends[pair] = make_int4(0, 0, 0, 0);
+    if (range.items <= 0 && lane == 0 && rank == 0) a.ends[pair] = 0;
     if (gt >= kInfos && !wait(&sh.info_empty[gt % kInfos], (uint32_t)((gt / kInfos - 1) & 1), abort)) return;
     if (lane == 0) {
         sh.info[gt % kInfos].flags = Info::kStop;
@@ -497,7 +494,7 @@ template <bool kBf16>
 __device__ void query_role(Shared<kBf16>& sh, const Args& a, int warp, int lane, int rank, volatile int* abort) {
     using S = Shape<kBf16>;
     constexpr int kEach = kMine / S::kHelpWarps;
-    Walk walk(a, sh.plan.range);
+    Walk walk(a, sh.plan);
     Tile t;
     int it = 0, run = 0, u0 = -1, f = -1;
     while (walk.next(t)) {
@@ -508,8 +505,8 @@ __device__ void query_role(Shared<kBf16>& sh, const Args& a, int warp, int lane,
         u0 = t.u0;
         f = t.f;
         run = 1;
+        const Row mine = row_info(a, sh.plan, u0, f, kMine * rank + kEach * warp + (lane & (kEach - 1)));
         if (it > 0 && !wait(&sh.q_empty, (uint32_t)((it - 1) & 1), abort)) return;
-        const Row mine = row_info(a, u0, f, kMine * rank + kEach * warp + (lane & (kEach - 1)));
 #pragma unroll 4
         for (int i = 0; i < kEach; ++i) {
             const int r = kEach * warp + i;
@@ -773,7 +770,7 @@ __device__ void softmax_role(Shared<kBf16>& sh, const Args& a, uint32_t tmem, in
         const int flags = in.flags;
         if (flags & Info::kStop) return;
         if (flags & Info::kFirst) {
-            row = row_info(a, in.u0, in.f, kMine * rank + r);
+            row = row_info(a, sh.plan, in.u0, in.f, kMine * rank + r);
             m = -INFINITY;
             l = 0.f;
             if constexpr (!kBf16) {
@@ -978,9 +975,10 @@ __device__ void softmax_role(Shared<kBf16>& sh, const Args& a, uint32_t tmem, in
                     kept[(n / 4 + i) * kRows] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
             }
         }
-        if (!done && quarter == 0 && row.b >= 0) {
+        if (!done && quarter == 0) {
             slot[kRows * kD + R] = top_of;
             slot[kRows * (kD + 1) + R] = total;
+            slot[kRows * (kD + 2) + R] = __int_as_float(row.b < 0 ? -1 : row.b * a.heads + row.h);
         }
         tc_fence_before();
     }
@@ -1073,79 +1071,125 @@ static_assert(smem_bytes<true>() <= 227 * 1024 && smem_bytes<false>() <= 227 * 1
 
 // ---------------------------------------------------------------- join
 // The units that the ranges cut: o = sum_i O_i 2^(m_i - M) / (2^(sink - M) + sum_i l_i 2^(m_i - M)) over the
-// pairs' partial results in order. A thread has four channels of a row; an item is 8 channels of a
-// unit's 128 rows. What sees nothing and had no unit gets its zeros here.
+// pairs' partial results in order, by batches. A thread has a row and kEach groups of four channels;
+// the values of a batch of pieces are requested together with their maxima. What sees nothing gets its
+// zeros here.
 constexpr int kJoinThreads = 256;
-constexpr int kJoinItems = kD / 8;  // of a unit
-constexpr int kJoinBatch = 8;
+constexpr int kJoinLoads = 8;  // in flight a thread, 16 bytes each
+
+template <int kEach>
+__device__ __forceinline__ void join_rows(const Args& a, int c0, int slot0, int n, int item) {
+    constexpr int kBatch = kJoinLoads / kEach;
+    const int R = threadIdx.x & (kRows - 1), cg = kEach * (2 * item + (threadIdx.x >> 7));
+    auto piece = [&](int i) { return part_of(a, c0 + i, i == 0 ? slot0 : 0); };
+    const int place = __float_as_int(__ldcg(piece(0) + kRows * (kD + 2) + R));
+    const int h = max(place, 0) % a.heads;
+    float4 acc[kEach];
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+    float den = 0.f, M = -INFINITY;
+    for (int i0 = 0; i0 < n; i0 += kBatch) {
+        float4 v[kBatch][kEach];
+        float m[kBatch], l[kBatch], top = M;
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            m[i] = -INFINITY;
+            if (i0 + i >= n) continue;
+            const float* p = piece(i0 + i);
+#pragma unroll
+            for (int e = 0; e < kEach; ++e) v[i][e] = __ldcg(reinterpret_cast<const float4*>(p) + (cg + e) * kRows + R);
+            m[i] = __ldcg(p + kRows * kD + R);
+            l[i] = __ldcg(p + kRows * (kD + 1) + R);
+        }
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) top = fmaxf(top, m[i]);
+        if (top != M) {
+            const float w = M == -INFINITY ? 0.f : ex2(M - top);
+            den *= w;
+#pragma unroll
+            for (int e = 0; e < kEach; ++e) acc[e] = make_float4(acc[e].x * w, acc[e].y * w, acc[e].z * w, acc[e].w * w);
+            M = top;
+        }
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            if (m[i] == -INFINITY) continue;  // (nothing, or nothing seen)
+            const float w = ex2(m[i] - M);
+            den = fmaf(l[i], w, den);
+#pragma unroll
+            for (int e = 0; e < kEach; ++e) {
+                acc[e].x = fmaf(v[i][e].x, w, acc[e].x);
+                acc[e].y = fmaf(v[i][e].y, w, acc[e].y);
+                acc[e].z = fmaf(v[i][e].z, w, acc[e].z);
+                acc[e].w = fmaf(v[i][e].w, w, acc[e].w);
+            }
+        }
+    }
+    if (place < 0) return;
+    const float s2 = a.sink ? a.sink[h] * kLog2e : -INFINITY, top = fmaxf(M, s2);
+    const float f = M == -INFINITY ? 0.f : ex2(M - top);
+    den = den * f + (s2 == -INFINITY ? 0.f : ex2(s2 - top));
+    const float inv = den == 0.f ? 0.f : f / den;
+    uint32_t o[2 * kEach];
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) {
+        const __nv_bfloat162 x = __floats2bfloat162_rn(inv == 0.f ? 0.f : acc[e].x * inv, inv == 0.f ? 0.f : acc[e].y * inv);
+        const __nv_bfloat162 y = __floats2bfloat162_rn(inv == 0.f ? 0.f : acc[e].z * inv, inv == 0.f ? 0.f : acc[e].w * inv);
+        o[2 * e] = *reinterpret_cast<const uint32_t*>(&x);
+        o[2 * e + 1] = *reinterpret_cast<const uint32_t*>(&y);
+    }
+    __nv_bfloat16* const out = a.out + (int64_t)place * kD + 4 * cg;
+    if constexpr (kEach == 1) {
+        *reinterpret_cast<uint2*>(out) = make_uint2(o[0], o[1]);
+    } else {
+#pragma unroll
+        for (int e = 0; e < kEach; e += 2)
+            *reinterpret_cast<uint4*>(out + 4 * e) = make_uint4(o[2 * e], o[2 * e + 1], o[2 * e + 2], o[2 * e + 3]);
+    }
+}
 
 __global__ void __launch_bounds__(kJoinThreads) k_shared_join(const __grid_constant__ Args a) {
-    __shared__ int4 ends[kMaxPairs];
-    __shared__ int starts[kMaxPairs], units;
+    __shared__ uint32_t cut_s[kMaxPairs / 32], through_s[kMaxPairs / 32], single_s[kMaxPairs / 32];
     grid_dep_wait();
     const int tid = threadIdx.x, lane = tid & 31;
-    for (int c = tid; c < a.pairs; c += kJoinThreads) ends[c] = a.ends[c];
+    if (tid < kMaxPairs) {
+        const int e = tid < a.pairs ? a.ends[tid] : 0;
+        const uint32_t cut = __ballot_sync(0xffffffffu, e & kCut), through = __ballot_sync(0xffffffffu, e & kThrough);
+        const uint32_t single = __ballot_sync(0xffffffffu, e & kSingle);
+        if (lane == 0) {
+            cut_s[tid >> 5] = cut;
+            through_s[tid >> 5] = through;
+            single_s[tid >> 5] = single;
+        }
+    }
+    __syncthreads();
+    int units = 0;  // that begin in a pair's range and end behind it
+#pragma unroll
+    for (int w = 0; w < kMaxPairs / 32; ++w) units += __popc(cut_s[w] & ~through_s[w]);
+    // few units are cut into many pieces each, by few threads: those take less each
+    const bool few = units * 16 < (int)gridDim.x;
+    const int each = few ? kD / 8 : kD / 32;
+    for (int item = blockIdx.x; item < units * each; item += gridDim.x) {
+        int nth = item / each, w = 0;
+        uint32_t bits = cut_s[0] & ~through_s[0];
+        while (nth >= __popc(bits)) {
+            nth -= __popc(bits);
+            ++w;
+            bits = cut_s[w] & ~through_s[w];
+        }
+        for (; nth > 0; --nth) bits &= bits - 1;
+        const int c0 = 32 * w + __ffs(bits) - 1;
+        auto has = [](const uint32_t* s, int c) { return (s[c >> 5] >> (c & 31)) & 1u; };
+        int n = 2;  // pieces: c0's last one, then the others' first ones
+        while (c0 + n < a.pairs && has(cut_s, c0 + n - 1) && has(through_s, c0 + n - 1)) ++n;
+        const int slot0 = has(single_s, c0) ? 0 : 1;
+        if (few) join_rows<1>(a, c0, slot0, n, item % each);
+        else join_rows<4>(a, c0, slot0, n, item % each);
+    }
     for (int b = blockIdx.x * (kJoinThreads / 32) + (tid >> 5); b < a.B; b += gridDim.x * (kJoinThreads / 32)) {
         const int row = a.seq ? a.seq[b] : b;
         if (row < 0 || (row < a.g.max_seqs && length_of(a, a.n_tokens[b], false) > 0)) continue;
         uint4* out = reinterpret_cast<uint4*>(a.out + (int64_t)b * a.heads * kD);
         for (int u = lane; u < a.heads * (kD / 8); u += 32) out[u] = make_uint4(0u, 0u, 0u, 0u);
-    }
-    __syncthreads();
-    if (tid == 0) {
-        int n = 0;
-        for (int c = 0; c + 1 < a.pairs; ++c)
-            if ((ends[c].x & kCut) && !(ends[c].x & kThrough)) starts[n++] = c;
-        units = n;
-    }
-    __syncthreads();
-    const int R = tid & (kRows - 1);
-    for (int item = blockIdx.x; item < units * kJoinItems; item += gridDim.x) {
-        const int c0 = starts[item / kJoinItems], cg = 2 * (item % kJoinItems) + (tid >> 7);
-        const int4 u = ends[c0];
-        const Row row = row_info(a, u.y, u.z, R);
-        if (row.b < 0) continue;
-        int n = 2;  // pieces: c0's last one, then the others' first ones
-        while (c0 + n < a.pairs && (ends[c0 + n - 1].x & (kCut | kThrough)) == (kCut | kThrough)) ++n;
-        auto piece = [&](int i) { return part_of(a, c0 + i, i == 0 && !(u.x & kSingle) ? 1 : 0); };
-        const float s2 = a.sink ? a.sink[row.h] * kLog2e : -INFINITY;
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        float den = 0.f, M = s2;
-        for (int i0 = 0; i0 < n; i0 += kJoinBatch) {
-            float m[kJoinBatch];
-#pragma unroll
-            for (int i = 0; i < kJoinBatch; ++i) m[i] = i0 + i < n ? __ldcg(piece(i0 + i) + kRows * kD + R) : -INFINITY;
-#pragma unroll
-            for (int i = 0; i < kJoinBatch; ++i) M = fmaxf(M, m[i]);
-        }
-        for (int i0 = 0; i0 < n; i0 += kJoinBatch) {
-            float4 v[kJoinBatch];
-            float m[kJoinBatch], l[kJoinBatch];
-#pragma unroll
-            for (int i = 0; i < kJoinBatch; ++i) {
-                if (i0 + i >= n) continue;
-                const float* p = piece(i0 + i);
-                v[i] = __ldcg(reinterpret_cast<const float4*>(p) + cg * kRows + R);
-                m[i] = __ldcg(p + kRows * kD + R);
-                l[i] = __ldcg(p + kRows * (kD + 1) + R);
-            }
-#pragma unroll
-            for (int i = 0; i < kJoinBatch; ++i) {
-                if (i0 + i >= n) continue;
-                const float w = m[i] == -INFINITY ? 0.f : ex2(m[i] - M);
-                den = fmaf(l[i], w, den);
-                acc.x = fmaf(v[i].x, w, acc.x);
-                acc.y = fmaf(v[i].y, w, acc.y);
-                acc.z = fmaf(v[i].z, w, acc.z);
-                acc.w = fmaf(v[i].w, w, acc.w);
-            }
-        }
-        den += s2 == -INFINITY ? 0.f : ex2(s2 - M);
-        const float inv = den == 0.f ? 0.f : 1.f / den;
-        const __nv_bfloat162 x = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
-        const __nv_bfloat162 y = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
-        *reinterpret_cast<uint2*>(a.out + ((int64_t)row.b * a.heads + row.h) * kD + 4 * cg) =
-            make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
     }
 }
 
@@ -1157,7 +1201,7 @@ int pairs_of(const csa2_params* p) {
     return n < 2 ? 1 : n / 2 < kMaxPairs ? n / 2 : kMaxPairs;
 }
 
-int64_t ends_bytes(int pairs) { return ((int64_t)pairs * (int)sizeof(int4) + 255) & ~(int64_t)255; }
+int64_t ends_bytes(int pairs) { return ((int64_t)pairs * 4 + 255) & ~(int64_t)255; }
 int64_t ws_need(int pairs) { return ends_bytes(pairs) + 2 * (int64_t)pairs * kPartFloats * 4; }
 
 }  // namespace
@@ -1222,7 +1266,7 @@ extern "C" int csa2_paged_attn_shared(const csa2_params* p, const csa2_pages* c,
     a.first = first;
     a.shared = shared;
     a.out = static_cast<__nv_bfloat16*>(out);
-    a.ends = static_cast<int4*>(workspace);
+    a.ends = static_cast<int32_t*>(workspace);
     a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + ends_bytes(pairs));
     a.dev_status = dev_status;
     a.scale_log2 = p->softmax_scale * kLog2e;
