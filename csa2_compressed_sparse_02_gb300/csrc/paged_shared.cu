@@ -126,11 +126,12 @@ struct Range {
     bool cont, cut;    // its first unit began before it; its last one ends behind it
 };
 
-constexpr int kKept = 192;  // slots that stay in shared memory
+constexpr int kKept = 40;  // slots from the range's first unit on that stay in shared memory
 
 struct PlanShared {
     Slot slots[kKept];
-    int64_t warp_sum[32];
+    int base;  // the first of them
+    int64_t warp_sum[16];
     long long begin, end;  // where the first tile's unit begins, and the last one's ends
     Range range;
 };
@@ -154,20 +155,21 @@ __device__ void plan(const Args& a, PlanShared& sh, int pair) {
         *all = sum;
         return warps_before + before;
     };
+    Slot s = {};
     auto items_of = [&](int i, bool report, bool* head) -> uint32_t {
         *head = false;
         if (i >= a.B) return 0;
-        const Slot s = slot_of(a, i, report);
-        if (i < kKept) sh.slots[i] = s;
+        s = slot_of(a, i, report);
         *head = unit_of(a, i, s.f) == i;
         return (uint32_t)prefix_tiles(a, s, i) + own_tiles(s);
     };
-    int64_t total = 0, all;
+    const bool once = a.B <= (int)blockDim.x;  // a slot a thread: one scan
+    int64_t total = 0, all, here = 0;
     uint32_t n = 0;
     bool head = false;
     for (int i0 = 0; i0 < a.B; i0 += blockDim.x) {
         n = items_of(i0 + tid, blockIdx.x == 0, &head);
-        scan(n, &all);
+        here = scan(n, &all);
         total += all;
     }
     const Cut ranges(total, a.pairs);
@@ -176,6 +178,7 @@ __device__ void plan(const Args& a, PlanShared& sh, int pair) {
     if (tid == 0) {
         sh.range.items = end - at;
         sh.range.i = sh.range.j = 0;
+        sh.base = 0;
         sh.begin = 0;
         sh.end = total;
     }
@@ -183,12 +186,15 @@ __device__ void plan(const Args& a, PlanShared& sh, int pair) {
     int64_t before = 0;
     for (int i0 = 0; i0 < a.B; i0 += blockDim.x) {
         const int i = i0 + tid;
-        if (a.B > (int)blockDim.x) n = items_of(i, false, &head);
-        const int64_t here = before + scan(n, &all);
-        before += all;
+        if (!once) {
+            n = items_of(i, false, &head);
+            here = before + scan(n, &all);
+            before += all;
+        }
         if (at >= here && at < here + n) {
             sh.range.i = i;
             sh.range.j = (int)(at - here);
+            sh.base = unit_of(a, i, s.f);
         }
         if (head && here <= at) atomicMax(&sh.begin, (long long)here);
         if (head && here >= end) atomicMin(&sh.end, (long long)here);
@@ -198,7 +204,17 @@ __device__ void plan(const Args& a, PlanShared& sh, int pair) {
         sh.range.cont = sh.begin < at;
         sh.range.cut = sh.end > end;
     }
+    if (once) {
+        if (tid >= sh.base && tid < min(sh.base + kKept, a.B)) sh.slots[tid - sh.base] = s;
+    } else if (tid < kKept && sh.base + tid < a.B) {
+        sh.slots[tid] = slot_of(a, sh.base + tid, false);
+    }
     __syncthreads();
+}
+
+// Slot i, which is not before the range's first unit.
+__device__ __forceinline__ Slot slot_at(const Args& a, const PlanShared& plan, int i) {
+    return i - plan.base < kKept ? plan.slots[i - plan.base] : slot_of(a, i, false);
 }
 
 // A range tile by tile.
@@ -220,7 +236,7 @@ struct Walk {
         if (left > 0) enter();
     }
     __device__ __forceinline__ void enter() {
-        s = i < kKept ? plan.slots[i] : slot_of(a, i, false);
+        s = slot_at(a, plan, i);
         u0 = unit_of(a, i, s.f);
         pre = u0 == i ? tiles_of(s.sh) : 0;
         items = pre + own_tiles(s);
@@ -258,7 +274,7 @@ __device__ __noinline__ Row row_info(const Args& a, const PlanShared& plan, int 
     x.T = 0;
     const int i = u0 + x.k;
     if (x.k >= a.members || i >= a.B) return x;
-    const Slot s = i < kKept ? plan.slots[i] : slot_of(a, i, false);
+    const Slot s = slot_at(a, plan, i);
     if (s.f != f) return x;
     x.b = s.b;
     x.T = s.T;
@@ -274,11 +290,13 @@ __device__ __noinline__ Row row_info(const Args& a, const PlanShared& plan, int 
 template <bool kBf16>
 struct Shape {
     static constexpr int kSoftWarps = 8;
-    static constexpr int kMmaWarp = 8, kKeyWarp = 9, kValueWarp = 10, kPlanWarp = 11, kHelp0 = 12, kHelpWarps = 4;
+    static constexpr int kScoreWarp = 8, kOutputWarp = 9, kKeyWarp = 10, kValueWarp = 11, kPlanWarp = 12;
+    static constexpr int kHelp0 = 13, kHelpWarps = 3;  // (16 warps: 128 registers a thread)
     static constexpr int kThreads = 32 * (kHelp0 + kHelpWarps);
     static constexpr uint32_t kChunk = kMine * 128;            // 64 rows x 128 bytes, 128-byte swizzle
     static constexpr uint32_t kPlace = kBf16 ? 2 * kChunk : kChunk;  // 64 positions x 128 channels
-    static constexpr int kKeys = kBf16 ? 4 : 8, kValues = kBf16 ? 4 : 8;  // places; a tile takes four of each
+    static constexpr int kKeys = kBf16 ? 4 : 8, kValues = 4;  // places; a tile takes four of each
+    static constexpr uint32_t kWeights = (kBf16 ? 2 : 3) * kChunk;  // P: 64 positions a chunk; E4M3: 128, a part each
     static constexpr uint32_t kIdesc = (1u << 4) | ((128u >> 4) << 24);  // D fp32, M = 128 over the pair
     // N = 128 positions, both K-major; N = 256 channels, B MN-major. Types: bf16 1, E4M3 0, E5M2 1
     static constexpr uint32_t kIdescS = kIdesc | ((128u >> 3) << 17) | (kBf16 ? (1u << 7) | (1u << 10) : 0u);
@@ -294,7 +312,7 @@ struct Shape {
 constexpr uint32_t kColO = 0, kColS = 256;  // TMEM: O 2 x 128 columns, S 2 x 64
 constexpr uint32_t kTmemCols = 512;         // one CTA an SM, so it takes them all
 
-constexpr int kInfos = 8;
+constexpr int kInfos = 4;
 struct alignas(16) Info {
     enum {
         kFirst = 1, kLast = 2,    // of a run of at most kRun tiles
@@ -313,15 +331,15 @@ struct Shared {
     using S = Shape<kBf16>;
     uint8_t keys[S::kKeys][S::kPlace], values[S::kValues][S::kPlace];
     uint8_t q[8 * S::kChunk];
-    uint8_t p[(kBf16 ? 2 : 3) * S::kChunk];  // bf16: 64 positions each; E4M3: 128, a part each
-    float red_max[2][4][kMine];
-    float red_sum[4][kMine];
-    float row_scale[2][kMine];  // E4M3: logit factor, by run parity
+    uint8_t p[2][S::kWeights];  // by tile parity
+    __nv_bfloat16 red_max[2][4][kMine];  // rounded up: what it bounds need not be close
+    float row_scale[kBf16 ? 0 : 2][kMine];  // E4M3: logit factor, by run parity
     Info info[kInfos];
-    uint64_t key_full[S::kKeys], key_empty[S::kKeys], value_full[S::kValues], value_empty[S::kValues];
-    uint64_t key_peer[S::kKeys], value_peer[S::kValues];  // the even CTA's: the odd one's place is full
+    uint64_t key_full[S::kKeys];  // the even CTA's: the place is full in both
+    uint64_t key_empty[S::kKeys], value_full[S::kValues], value_empty[S::kValues];
+    uint64_t value_peer[S::kValues];  // the even CTA's: the odd one's place is full
     uint64_t info_full[kInfos], info_empty[kInfos];
-    uint64_t s_full[2], p_full, pv_done;
+    uint64_t s_full[2], s_empty[2], p_full[2], pv_done[2];  // by tile parity; s_empty, p_full: the even CTA's
     uint64_t q_full[2];   // the even CTA's: both CTAs' rows are staged; by run parity
     uint64_t q_here[2];   // this CTA's are
     uint64_t q_empty;
@@ -443,7 +461,8 @@ __device__ __forceinline__ void info_done(Shared<kBf16>& sh, int gt, int lane) {
 
 // ---------------------------------------------------------------- copies
 // One warp copies the keys, one the values, box by box. One elected lane issues, from values of the
-// whole warp.
+// whole warp. Keys of both CTAs count on the even one's barrier, where the MMAs wait; values on each
+// CTA's own, which its softmax warps look at too (finite_values).
 template <bool kBf16>
 __device__ __noinline__ void load_role(Shared<kBf16>& sh, const Args& a, const CUtensorMap* tmap, bool keys, int lane,
                                        int rank, volatile int* abort) {
@@ -469,13 +488,14 @@ __device__ __noinline__ void load_role(Shared<kBf16>& sh, const Args& a, const C
             const int x = keys ? 128 * i : 256 * (i >> 1) + 128 * rank;
             if (g >= places && !wait(&empty[slot], phase, abort)) break;
             const uint32_t at = ring + (uint32_t)__shfl_sync(0xffffffffu, slot, 0) * S::kPlace;
-            if (elect_one()) mbar_arrive_expect_tx(&full[slot], S::kPlace);
+            const uint32_t bar = keys ? mapa_shared(smem_u32(&full[slot]), 0) : smem_u32(&full[slot]);
+            if ((!keys || rank == 0) && elect_one()) mbar_arrive_expect_tx(&full[slot], keys ? 2 * S::kPlace : S::kPlace);
 #pragma unroll 1
             for (int b = 0; b < kMine; b += a.box_rows) {
                 const int yb = __shfl_sync(0xffffffffu, y, (first + b) >> shift);
                 if (elect_one()) {
-                    tma_g2s_2d(at + b * 128, tmap, x, yb, &full[slot]);
-                    if constexpr (kBf16) tma_g2s_2d(at + b * 128 + S::kChunk, tmap, x + 64, yb, &full[slot]);
+                    tma_g2s_2d_pair(at + b * 128, tmap, x, yb, bar);
+                    if constexpr (kBf16) tma_g2s_2d_pair(at + b * 128 + S::kChunk, tmap, x + 64, yb, bar);
                 }
             }
             __syncwarp();
@@ -484,16 +504,18 @@ __device__ __noinline__ void load_role(Shared<kBf16>& sh, const Args& a, const C
         }
         if (i < 4) break;
     }
-    // whatever ended the loop, no copy of this CTA outlives it
-    for (int s = max(0, g - places); s < g; ++s) mbar_wait_drain(&full[s % places], (uint32_t)((s / places) & 1));
+    // Whatever ended the loop, no copy outlives the pair, which ends together. (Where a wait has given
+    // up, the even CTA may have armed less than the odd one has asked for: a copy takes a microsecond.)
+    if (!keys || rank == 0)
+        for (int s = max(0, g - places); s < g; ++s) mbar_wait_drain(&full[s % places], (uint32_t)((s / places) & 1));
+    if (*abort) __nanosleep(200000);
 }
 
 // ---------------------------------------------------------------- queries
-// Four warps stage this CTA's rows of the unit, once a run: warp w rows 16 w .. 16 w + 15.
+// Three warps stage this CTA's rows of the unit, once a run: warp w rows w, w + 3 and so on.
 template <bool kBf16>
 __device__ void query_role(Shared<kBf16>& sh, const Args& a, int warp, int lane, int rank, volatile int* abort) {
     using S = Shape<kBf16>;
-    constexpr int kEach = kMine / S::kHelpWarps;
     Walk walk(a, sh.plan);
     Tile t;
     int it = 0, run = 0, u0 = -1, f = -1;
@@ -505,11 +527,10 @@ __device__ void query_role(Shared<kBf16>& sh, const Args& a, int warp, int lane,
         u0 = t.u0;
         f = t.f;
         run = 1;
-        const Row mine = row_info(a, sh.plan, u0, f, kMine * rank + kEach * warp + (lane & (kEach - 1)));
+        const Row mine = row_info(a, sh.plan, u0, f, kMine * rank + min(warp + S::kHelpWarps * lane, kMine - 1));
         if (it > 0 && !wait(&sh.q_empty, (uint32_t)((it - 1) & 1), abort)) return;
 #pragma unroll 4
-        for (int i = 0; i < kEach; ++i) {
-            const int r = kEach * warp + i;
+        for (int i = 0, r = warp; r < kMine; ++i, r += S::kHelpWarps) {
             const int b = __shfl_sync(0xffffffffu, mine.b, i), h = __shfl_sync(0xffffffffu, mine.h, i);
             const __nv_bfloat16* src = a.q + (b < 0 ? 0 : b * a.q_seq + h * a.q_head);
             if constexpr (kBf16) {
@@ -562,12 +583,10 @@ __device__ void query_role(Shared<kBf16>& sh, const Args& a, int warp, int lane,
 }
 
 // ---------------------------------------------------------------- MMAs
-// The even CTA's warp issues the pair's MMAs: S of a tile, then S of the next one before PV of this,
-// so that the tensor cores work while the softmax runs. The odd CTA's passes on that its places are
-// full.
-//
-// What a warp does between MMAs costs as much as they do: a look at a barrier 200 cycles and more. So
-// the lanes look at a product's barriers together, and its MMAs are issued in one go.
+// Two warps of the even CTA issue the pair's MMAs, one S, one PV: what a warp does between its MMAs
+// (a look at a barrier takes 200 cycles and more) then falls into the other's. The lanes look at a
+// product's barriers together, and it is issued in one go. S is up to two tiles ahead of the softmax.
+// In the odd CTA a warp passes on that the places of V are full.
 template <int kPlaces>
 struct Ring {
     int slot = 0;
@@ -579,31 +598,44 @@ struct Ring {
     }
 };
 
+// (the leading offset of V is in a descriptor's low word)
+constexpr uint32_t kHigh = (1024u >> 4) | (1u << 14) | (kLayoutSw128 << 29);
+
 template <bool kBf16>
-__device__ void mma_role(Shared<kBf16>& sh, uint32_t tmem, int lane, volatile int* abort) {
+__device__ void score_role(Shared<kBf16>& sh, uint32_t tmem, int lane, volatile int* abort) {
     using S = Shape<kBf16>;
-    // (the leading offset of V is in the low word)
-    constexpr uint32_t kHigh = (1024u >> 4) | (1u << 14) | (kLayoutSw128 << 29);
     const uint32_t dQ = (uint32_t)smem_desc(smem_u32(sh.q), 16, 1024, kLayoutSw128);
-    const uint32_t dP = (uint32_t)smem_desc(smem_u32(sh.p), 16, 1024, kLayoutSw128);
     const uint32_t dK = (uint32_t)smem_desc(smem_u32(sh.keys[0]), 16, 1024, kLayoutSw128);
-    const uint32_t dV = (uint32_t)smem_desc(smem_u32(sh.values[0]), S::kChunk, 1024, kLayoutSw128);
     Ring<S::kKeys> keys;
-    Ring<S::kValues> values;
     int it = 0;
-    auto step = [](int slot) { return __shfl_sync(0xffffffffu, (uint32_t)slot * (S::kPlace >> 4), 0); };
-    // S of tile gt; returns its flags, -1: gave up
-    auto scores = [&](int gt) -> int {
-        const int i = lane & 3;
-        uint64_t* const bar = lane < 4 ? &sh.key_full[keys.nth(i)] : lane < 8 ? &sh.key_peer[keys.nth(i)] : &sh.info_full[gt % kInfos];
-        if (!wait(bar, lane < 8 ? keys.parity(i) : (uint32_t)((gt / kInfos) & 1), abort)) return -1;
-        tc_fence_after();
-        const int flags = *(volatile int*)&sh.info[gt % kInfos].flags;
-        info_done(sh, gt, lane);
+    bool last = true;  // the tile before was a run's last
+    for (int gt = 0;; ++gt) {
+        if (last) {  // a run begins, or the range is done
+            if (!info_wait(sh, gt, abort)) return;
+            if (*(volatile int*)&sh.info[gt % kInfos].flags & Info::kStop) return;
+            if (!wait(&sh.q_full[it & 1], (uint32_t)((it >> 1) & 1), abort)) return;
+            ++it;
+        }
         const uint32_t at = tmem + kColS + (uint32_t)__shfl_sync(0xffffffffu, gt & 1, 0) * 64u;
 #pragma unroll 1
         for (int d = 0; d < 4; ++d) {
-            const uint32_t k = dK + step(keys.slot), q = dQ + d * ((kBf16 ? 2 * S::kChunk : S::kChunk) >> 4);
+            if (!(d & 1)) {  // half of the tile's places at a look: the rest is on its way behind S of the tile before
+                uint64_t* bar = &sh.key_full[keys.nth(lane & 1)];
+                uint32_t parity = keys.parity(lane & 1);
+                if (d == 0 && lane >= 8) {
+                    const bool read = lane >= 16 && gt >= 2;  // S of two tiles before
+                    bar = read ? &sh.s_empty[gt & 1] : &sh.info_full[gt % kInfos];
+                    parity = (uint32_t)(read ? (gt >> 1) - 1 : gt / kInfos) & 1u;
+                }
+                if (!wait(bar, parity, abort)) return;
+                tc_fence_after();
+                if (d == 0) {
+                    last = *(volatile int*)&sh.info[gt % kInfos].flags & Info::kLast;
+                    info_done(sh, gt, lane);
+                }
+            }
+            const uint32_t k = dK + __shfl_sync(0xffffffffu, (uint32_t)keys.slot * (S::kPlace >> 4), 0);
+            const uint32_t q = dQ + d * ((kBf16 ? 2 * S::kChunk : S::kChunk) >> 4);
             if (elect_one()) {
                 if constexpr (kBf16) {
 #pragma unroll
@@ -621,26 +653,36 @@ __device__ void mma_role(Shared<kBf16>& sh, uint32_t tmem, int lane, volatile in
                                         S::kIdescS, (i | part) != 0 ? 1u : (uint32_t)(d != 0));
                 }
                 tc_commit_pair(&sh.key_empty[keys.slot]);
+                if (d == 3) tc_commit_pair(&sh.s_full[gt & 1]);
+                if (d == 3 && last) tc_commit_pair(&sh.q_empty);
             }
             __syncwarp();
             keys.step();
         }
-        if (elect_one()) {
-            tc_commit_pair(&sh.s_full[gt & 1]);
-            if (flags & Info::kLast) tc_commit_pair(&sh.q_empty);
-        }
-        __syncwarp();
-        return flags;
-    };
-    auto output = [&](int gt, bool first) {
+    }
+}
+
+template <bool kBf16>
+__device__ void output_role(Shared<kBf16>& sh, uint32_t tmem, int lane, volatile int* abort) {
+    using S = Shape<kBf16>;
+    const uint32_t dP = (uint32_t)smem_desc(smem_u32(sh.p[0]), 16, 1024, kLayoutSw128);
+    const uint32_t dV = (uint32_t)smem_desc(smem_u32(sh.values[0]), S::kChunk, 1024, kLayoutSw128);
+    Ring<S::kValues> values;
+    for (int gt = 0;; ++gt) {
+        if (!info_wait(sh, gt, abort)) return;
+        const int flags = *(volatile int*)&sh.info[gt % kInfos].flags;
+        if (flags & Info::kStop) return;
+        info_done(sh, gt, lane);
         const int i = lane & 3;
-        uint64_t* const bar = lane < 4 ? &sh.value_full[values.nth(i)] : lane < 8 ? &sh.value_peer[values.nth(i)] : &sh.p_full;
-        if (!wait(bar, lane < 8 ? values.parity(i) : (uint32_t)(gt & 1), abort)) return false;
+        uint64_t* const bar = lane < 4 ? &sh.value_full[values.nth(i)] : lane < 8 ? &sh.value_peer[values.nth(i)] : &sh.p_full[gt & 1];
+        if (!wait(bar, lane < 8 ? values.parity(i) : (uint32_t)((gt >> 1) & 1), abort)) return;
         tc_fence_after();
+        const uint32_t weights = dP + __shfl_sync(0xffffffffu, (uint32_t)(gt & 1) * (S::kWeights >> 4), 0);
 #pragma unroll 1
         for (int n = 0; n < 4; ++n) {
-            const uint32_t v = dV + step(values.slot), p = dP + (n & 1) * ((kBf16 ? S::kChunk : 64u) >> 4);
-            const uint32_t o = tmem + kColO + 128 * (n >> 1), more = (n & 1) || !first;
+            const uint32_t v = dV + __shfl_sync(0xffffffffu, (uint32_t)values.slot * (S::kPlace >> 4), 0);
+            const uint32_t p = weights + (n & 1) * ((kBf16 ? S::kChunk : 64u) >> 4);
+            const uint32_t o = tmem + kColO + 128 * (n >> 1), more = (n & 1) || !(flags & Info::kFirst);
             if (elect_one()) {
                 if constexpr (kBf16) {
 #pragma unroll
@@ -655,72 +697,71 @@ __device__ void mma_role(Shared<kBf16>& sh, uint32_t tmem, int lane, volatile in
                                         S::kIdescPV, (i | part) == 0 ? more : 1u);
                 }
                 tc_commit_pair(&sh.value_empty[values.slot]);
-                if (n == 3) tc_commit_pair(&sh.pv_done);
+                if (n == 3) tc_commit_pair(&sh.pv_done[gt & 1]);
             }
             __syncwarp();
             values.step();
         }
-        return true;
-    };
-    // S of tile n, one tile ahead of PV of tile o within a run (the next run's query comes after this
-    // one's last S)
-    bool first = true, last = true;  // o is a run's first tile, n - 1 its last
-    for (int n = 0, o = 0;;) {
-        if (n == o || !last) {
-            if (n == o && last) {  // a run begins, or the range is done
-                if (!info_wait(sh, n, abort)) return;
-                if (*(volatile int*)&sh.info[n % kInfos].flags & Info::kStop) return;
-                if (!wait(&sh.q_full[it & 1], (uint32_t)((it >> 1) & 1), abort)) return;
-                ++it;
-                first = true;
-            }
-            const int flags = scores(n);
-            if (flags < 0) return;
-            last = flags & Info::kLast;
-            if (n++ == o && !last) continue;
-        }
-        if (!output(o++, first)) return;
-        first = false;
     }
 }
 
 template <bool kBf16>
 __device__ void relay_role(Shared<kBf16>& sh, int lane, volatile int* abort) {
     using S = Shape<kBf16>;
-    Ring<S::kKeys> keys;
-    Ring<S::kValues> values;
-    const int i = lane & 3;
-    auto pass = [&](uint64_t* full, uint64_t* peer, uint32_t parity) {
-        if (!wait(full, parity, abort)) return false;
-        if (lane < 4) mbar_arrive_peer(mapa_shared(smem_u32(peer), 0));
-        __syncwarp();
-        return true;
-    };
-    bool more = true;
-    for (int gt = 0; more; ++gt) {  // the values of a tile behind the keys of the next
+    static_assert(S::kValues % 4 == 0, "a tile's places do not wrap");
+    int slot = lane & 3;
+    uint32_t phase = 0;
+    for (int gt = 0;; ++gt) {
         if (!info_wait(sh, gt, abort)) return;
-        more = !(*(volatile int*)&sh.info[gt % kInfos].flags & Info::kStop);
+        if (*(volatile int*)&sh.info[gt % kInfos].flags & Info::kStop) return;
         info_done(sh, gt, lane);
-        if (more && !pass(&sh.key_full[keys.nth(i)], &sh.key_peer[keys.nth(i)], keys.parity(i))) return;
-        keys.step(4);
-        if (gt > 0) {
-            if (!pass(&sh.value_full[values.nth(i)], &sh.value_peer[values.nth(i)], values.parity(i))) return;
-            values.step(4);
-        }
+        if (!wait(&sh.value_full[slot], phase, abort)) return;
+        if (lane < 4) mbar_arrive_peer(mapa_shared(smem_u32(&sh.value_peer[slot]), 0));
+        __syncwarp();
+        if ((slot += 4) >= S::kValues) slot -= S::kValues, phase ^= 1u;
     }
 }
 
 // ---------------------------------------------------------------- softmax and epilogue
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 r;
+    asm("{\n .reg .b64 x, y, z;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n mul.rn.f32x2 z, x, y;\n"
+        " mov.b64 {%0, %1}, z;\n}" : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 r;
+    asm("{\n .reg .b64 x, y, z;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n add.rn.f32x2 z, x, y;\n"
+        " mov.b64 {%0, %1}, z;\n}" : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 r;
+    asm("{\n .reg .b64 x, y, z, w;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n mov.b64 w, {%6, %7};\n"
+        " fma.rn.f32x2 z, x, y, w;\n mov.b64 {%0, %1}, z;\n}"
+        : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return r;
+}
+
+// The positions that are not finite in any row of the warp.
+__device__ __forceinline__ uint32_t not_finite(const uint32_t (&sv)[32]) {
+    uint32_t which = 0;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) which |= (uint32_t)((sv[i] & 0x7f800000u) == 0x7f800000u) << i;
+    return __reduce_or_sync(0xffffffffu, which);
+}
+
 // Makes zeros of what is not finite of positions 32 quarter + (the bits of `which`) in this CTA's
-// places of V of tile gt. Called by a warp when PV of the tile before is done.
+// places of V of tile gt.
 template <bool kBf16>
 __device__ __noinline__ bool finite_values(Shared<kBf16>& sh, uint32_t which, int gt, int quarter, int lane,
                                            volatile int* abort) {
     using S = Shape<kBf16>;
+    if (gt > 0 && !wait(&sh.pv_done[(gt - 1) & 1], (uint32_t)((gt - 1) >> 1) & 1u, abort)) return false;
     uint8_t* at[2];
     for (int h = 0; h < 2; ++h) {
         const int g = 4 * gt + 2 * h + (quarter >> 1), slot = g % S::kValues;
-        // (what the place held before has been used: this is the phase that its barrier is in)
+        // PV of the tile before has used what the place held: this is the phase that its barrier is in
         if (!wait(&sh.value_full[slot], (uint32_t)((g / S::kValues) & 1), abort)) return false;
         at[h] = sh.values[slot];
     }
@@ -760,16 +801,17 @@ __device__ void softmax_role(Shared<kBf16>& sh, const Args& a, uint32_t tmem, in
     const int r = 32 * grp + lane;                 // of this CTA's rows
     const int p0 = 32 * quarter;                   // first position
     const uint32_t tl = tmem + ((uint32_t)(32 * qd) << 16);
-    float m = -INFINITY, l = 0.f, c = a.scale_log2;
+    float m = -INFINITY, l = 0.f, c = a.scale_log2;  // maximum and sum (this thread's share), logit factor
     float m_was = -INFINITY, l_was = 0.f;          // of the piece up to this run
+    const float2 c0 = make_float2(0.f, 0.f);
     Row row = {-1, 0, 0, 0};
     int runs = 0;
+    bool last = true;  // the tile before was a run's last
     for (int gt = 0;; ++gt) {
-        if (!info_wait(sh, gt, abort)) return;
-        const Info& in = sh.info[gt % kInfos];
-        const int flags = in.flags;
-        if (flags & Info::kStop) return;
-        if (flags & Info::kFirst) {
+        if (last) {  // a run begins, or the range is done
+            if (!info_wait(sh, gt, abort)) return;
+            const Info& in = sh.info[gt % kInfos];
+            if (in.flags & Info::kStop) return;
             row = row_info(a, sh.plan, in.u0, in.f, kMine * rank + r);
             m = -INFINITY;
             l = 0.f;
@@ -779,68 +821,86 @@ __device__ void softmax_role(Shared<kBf16>& sh, const Args& a, uint32_t tmem, in
             }
             ++runs;
         }
-        // the positions of this thread that its row sees; rows that stand for nothing see everything
-        uint32_t seen = ~0u;
-        if (row.b >= 0) {
-            const int lo = max(0, min(32, in.lo - in.t0 - p0));
-            const int hi = in.k >= 0 && in.k != row.k ? 0 : max(0, min(32, min(in.hi, row.T) - in.t0 - p0));
-            seen = in.ok[quarter] & (hi == 32 ? ~0u : (1u << hi) - 1u) & (lo == 32 ? 0u : ~0u << lo);
-        }
-        const bool all = __all_sync(0xffffffffu, seen == ~0u);
-        info_done(sh, gt, lane);
-        if (!wait(&sh.s_full[gt & 1], (uint32_t)((gt >> 1) & 1), abort)) return;
+        if (!wait(lane < 16 ? &sh.s_full[gt & 1] : &sh.info_full[gt % kInfos],
+                  (uint32_t)(lane < 16 ? gt >> 1 : gt / kInfos) & 1u, abort))
+            return;
         tc_fence_after();
         uint32_t sv[32];
-        tmem_ld_32x32b_x32(tl + kColS + 64 * (gt & 1) + 32 * ch, sv);
-        float x[32], odd = 0.f, odd2 = 0.f;  // 0, or NaN where a product is not finite
-#pragma unroll
-        for (int i = 0; i < 32; i += 2) {
-            odd = fmaf(__uint_as_float(sv[i]), 0.f, odd);
-            odd2 = fmaf(__uint_as_float(sv[i + 1]), 0.f, odd2);
+        tmem_ld_32x32b_x32_nowait(tl + kColS + 64 * (gt & 1) + 32 * ch, sv);
+        const Info& in = sh.info[gt % kInfos];
+        const int flags = in.flags;
+        last = flags & Info::kLast;
+        // whether this thread's row sees all its positions; rows that stand for nothing see everything
+        const int reach = row.b < 0 ? kTile : min(in.hi, row.T) - in.t0;
+        const bool all = __all_sync(0xffffffffu, in.k < 0 && in.ok[quarter] == ~0u && reach >= kTile);
+        uint32_t seen = ~0u;
+        if (!all && row.b >= 0) {
+            const int lo = max(0, min(32, in.lo - in.t0 - p0));
+            const int hi = in.k >= 0 && in.k != row.k ? 0 : max(0, min(32, reach - p0));
+            seen = in.ok[quarter] & (hi == 32 ? ~0u : (1u << hi) - 1u) & (lo == 32 ? 0u : ~0u << lo);
         }
-        const bool bad = __any_sync(0xffffffffu, !(odd + odd2 == 0.f));
-        uint32_t which = 0;  // positions whose products are not finite
-        if (bad) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) which |= (uint32_t)((sv[i] & 0x7f800000u) == 0x7f800000u) << i;
-            which = __reduce_or_sync(0xffffffffu, which);
-        }
-#pragma unroll
-        for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(sv[i]) * c;
-        if (!all) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) x[i] = (seen >> i) & 1u ? x[i] : -INFINITY;
-        }
-        float top = x[0];
-#pragma unroll
-        for (int i = 1; i < 32; ++i) top = fmaxf(top, x[i]);
-        sh.red_max[gt & 1][quarter][r] = top;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.max_bar[grp]);
-        if (!wait(&sh.max_bar[grp], (uint32_t)(gt & 1), abort)) return;
-        top = fmaxf(fmaxf(sh.red_max[gt & 1][0][r], sh.red_max[gt & 1][1][r]),
-                    fmaxf(sh.red_max[gt & 1][2][r], sh.red_max[gt & 1][3][r]));
-        float alpha = 1.f;
-        if (top > m + S::kLazyMax || (flags & Info::kFirst)) {
-            if (m != -INFINITY) alpha = ex2(m - top);
-            m = top;
-        }
-        const float sub = m == -INFINITY ? 0.f : m - S::kLift;
-        // P, rounded; the sum takes the values that the product multiplies
-        uint32_t w[16], part[kBf16 ? 1 : 3][8];
-        float sum = 0.f, sum2 = 0.f;
+        tmem_wait_ld_regs32(sv);
+        tc_fence_before();
+        info_done(sh, gt, lane);
+        if (lane == 0) arrive_lead(&sh.s_empty[gt & 1], rank);
+        float2 x[16], odd = c0;  // odd: 0, or NaN where a product is not finite
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-            const float e0 = ex2(x[2 * i] - sub), e1 = ex2(x[2 * i + 1] - sub);
-            if constexpr (kBf16) {
-                const __nv_bfloat162 v = __floats2bfloat162_rn(e0, e1);
-                w[i] = *reinterpret_cast<const uint32_t*>(&v);
-                sum += __uint_as_float(w[i] << 16);
-                sum2 += __uint_as_float(w[i] & 0xffff0000u);
-            } else {
-                const __half2 v = __floats2half2_rn(e0, e1);
-                w[i] = *reinterpret_cast<const uint32_t*>(&v);
+            x[i] = make_float2(__uint_as_float(sv[2 * i]), __uint_as_float(sv[2 * i + 1]));
+            odd = fma2(x[i], c0, odd);
+            x[i] = mul2(x[i], make_float2(c, c));
+        }
+        uint32_t which = 0;  // positions whose products are not finite
+        if (__any_sync(0xffffffffu, !(odd.x + odd.y == 0.f))) which = not_finite(sv);
+        if (!all) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                x[i].x = (seen >> (2 * i)) & 1u ? x[i].x : -INFINITY;
+                x[i].y = (seen >> (2 * i + 1)) & 1u ? x[i].y : -INFINITY;
             }
+        }
+        float top = fmaxf(x[0].x, x[0].y);
+#pragma unroll
+        for (int i = 1; i < 16; ++i) top = fmaxf(top, fmaxf(x[i].x, x[i].y));
+        sh.red_max[gt & 1][quarter][r] = __float2bfloat16_ru(top);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.max_bar[grp]);
+        // P under the maximum so far, while the others' maxima are on their way; again in the few tiles
+        // where the maximum moves. Rounded; the sum takes the values that the product multiplies.
+        uint32_t w[16], part[kBf16 ? 1 : 3][8];
+        float2 sum = c0;
+        float alpha = 1.f;
+        bool fresh = flags & Info::kFirst, known = false;
+        for (;;) {
+            if (!fresh) {
+                const float sub = m == -INFINITY ? 0.f : S::kLift - m;
+                sum = c0;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const float2 e = add2(x[i], make_float2(sub, sub));
+                    if constexpr (kBf16) {
+                        const __nv_bfloat162 v = __floats2bfloat162_rn(ex2(e.x), ex2(e.y));
+                        w[i] = *reinterpret_cast<const uint32_t*>(&v);
+                        sum = add2(sum, make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u)));
+                    } else {
+                        const __half2 v = __floats2half2_rn(ex2(e.x), ex2(e.y));
+                        w[i] = *reinterpret_cast<const uint32_t*>(&v);
+                    }
+                }
+            }
+            if (known) break;
+            if (!wait(&sh.max_bar[grp], (uint32_t)(gt & 1), abort)) return;
+            known = true;
+            const auto* all4 = sh.red_max[gt & 1];
+            top = fmaxf(fmaxf(__bfloat162float(all4[0][r]), __bfloat162float(all4[1][r])),
+                        fmaxf(__bfloat162float(all4[2][r]), __bfloat162float(all4[3][r])));
+            const bool move = fresh || top > m + S::kLazyMax;
+            if (!__any_sync(0xffffffffu, move)) break;
+            if (move) {
+                if (m != -INFINITY) alpha = ex2(m - top);
+                m = top;
+            }
+            fresh = false;
         }
         if constexpr (!kBf16) {
             // A NaN loses itself in the first two parts' rounding and stays what is left of them, so the
@@ -859,16 +919,15 @@ __device__ void softmax_role(Shared<kBf16>& sh, const Args& a, uint32_t tmem, in
                 part[2][k] = h2x2_to_e5m2x4(x0, x1);
                 const uint32_t v0 = h2_sub(w[2 * k], h2_sub(x0, __byte_perm(part[2][k], 0u, 0x1404)));
                 const uint32_t v1 = h2_sub(w[2 * k + 1], h2_sub(x1, __byte_perm(part[2][k], 0u, 0x3424)));
-                const float2 f0 = __half22float2(*reinterpret_cast<const __half2*>(&v0));
-                const float2 f1 = __half22float2(*reinterpret_cast<const __half2*>(&v1));
-                sum += f0.x + f0.y;
-                sum2 += f1.x + f1.y;
+                sum = add2(sum, __half22float2(*reinterpret_cast<const __half2*>(&v0)));
+                sum = add2(sum, __half22float2(*reinterpret_cast<const __half2*>(&v1)));
             }
         }
-        l = fmaf(l, alpha, sum + sum2);
-        // after PV of the tile before P may be written again, and O rescaled
-        if (!(flags & Info::kFirst) && !wait(&sh.pv_done, (uint32_t)((gt - 1) & 1), abort)) return;
-        if (__any_sync(0xffffffffu, alpha != 1.f)) {
+        l = fmaf(l, alpha, sum.x + sum.y);
+        // PV of two tiles before: P may be written again
+        if (gt > 1 && !wait(&sh.pv_done[gt & 1], (uint32_t)((gt >> 1) - 1) & 1u, abort)) return;
+        if (__any_sync(0xffffffffu, alpha != 1.f)) {  // (not in a run's first tile)
+            if (!wait(&sh.pv_done[(gt - 1) & 1], (uint32_t)((gt - 1) >> 1) & 1u, abort)) return;  // O is that of the tile before
             tc_fence_after();
 #pragma unroll 1
             for (int n = 0; n < 128; n += 32) {
@@ -881,7 +940,7 @@ __device__ void softmax_role(Shared<kBf16>& sh, const Args& a, uint32_t tmem, in
             tmem_wait_st();
         }
         if constexpr (kBf16) {
-            uint8_t* dst = sh.p + (qd >> 1) * S::kChunk;
+            uint8_t* dst = sh.p[gt & 1] + (qd >> 1) * S::kChunk;
 #pragma unroll
             for (int u = 0; u < 4; ++u)
                 *reinterpret_cast<uint4*>(dst + sw128(r, 4 * ch + u)) = make_uint4(w[4 * u], w[4 * u + 1], w[4 * u + 2], w[4 * u + 3]);
@@ -890,7 +949,7 @@ __device__ void softmax_role(Shared<kBf16>& sh, const Args& a, uint32_t tmem, in
             for (int i = 0; i < 3; ++i)
 #pragma unroll
                 for (int u = 0; u < 2; ++u)
-                    *reinterpret_cast<uint4*>(sh.p + i * S::kChunk + sw128(r, 2 * quarter + u)) =
+                    *reinterpret_cast<uint4*>(sh.p[gt & 1] + i * S::kChunk + sw128(r, 2 * quarter + u)) =
                         make_uint4(part[i][4 * u], part[i][4 * u + 1], part[i][4 * u + 2], part[i][4 * u + 3]);
         }
         // A weight of zero takes nothing from a position, unless that is not finite: rows that do not see
@@ -900,17 +959,20 @@ __device__ void softmax_role(Shared<kBf16>& sh, const Args& a, uint32_t tmem, in
         fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) arrive_lead(&sh.p_full, rank);
+        if (lane == 0) arrive_lead(&sh.p_full[gt & 1], rank);
         if (!(flags & Info::kLast)) continue;
 
         // ---- the run's end: this thread has 128 channels of its row, 256 ch + 128 (qd >> 1) and on
-        if (!wait(&sh.pv_done, (uint32_t)(gt & 1), abort)) return;
+        if (!wait(&sh.pv_done[gt & 1], (uint32_t)(gt >> 1) & 1u, abort)) return;
         tc_fence_after();
-        sh.red_sum[quarter][r] = l;
+        // (in these rows of this tile's P: only the four warps that have them write there, in two tiles'
+        // time, when all of them have come past here)
+        float* const sums = reinterpret_cast<float*>(sh.p[gt & 1] + 32 * grp * 128);
+        sums[32 * quarter + lane] = l;
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.sum_bar[grp]);
         if (!wait(&sh.sum_bar[grp], (uint32_t)((runs - 1) & 1), abort)) return;
-        float total = (sh.red_sum[0][r] + sh.red_sum[1][r]) + (sh.red_sum[2][r] + sh.red_sum[3][r]);
+        float total = (sums[lane] + sums[32 + lane]) + (sums[64 + lane] + sums[96 + lane]);
         float top_of = m - S::kLift;  // what P and O are relative to
         float was = 0.f, now = 1.f;
         if (!(flags & Info::kBegins)) {
@@ -936,43 +998,38 @@ __device__ void softmax_role(Shared<kBf16>& sh, const Args& a, uint32_t tmem, in
         float4* const kept = reinterpret_cast<float4*>(slot) + (d0 / 4) * kRows + R;
         __nv_bfloat16* const out = a.out + ((int64_t)max(row.b, 0) * a.heads + row.h) * kD + d0;
 #pragma unroll 1
-        for (int n = 0; n < 128; n += 32) {
-            float4 before[8];
-            if (!(flags & Info::kBegins)) {
+        for (int n = 0; n < 128; n += 16) {
+            uint32_t ov[16];
+            tmem_ld_32x32b_x16(tl + kColO + 128 * ch + n, ov);
+            float4 o[4];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) before[i] = row.b >= 0 ? kept[(n / 4 + i) * kRows] : make_float4(0.f, 0.f, 0.f, 0.f);
-            }
-            uint32_t ov[32];
-            tmem_ld_32x32b_x32(tl + kColO + 128 * ch + n, ov);
-            float o[32];
-#pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] = __uint_as_float(ov[i]);
-            if (!(flags & Info::kBegins)) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    o[4 * i] = fmaf(before[i].x, was, o[4 * i] * now);
-                    o[4 * i + 1] = fmaf(before[i].y, was, o[4 * i + 1] * now);
-                    o[4 * i + 2] = fmaf(before[i].z, was, o[4 * i + 2] * now);
-                    o[4 * i + 3] = fmaf(before[i].w, was, o[4 * i + 3] * now);
-                }
-            }
+            for (int i = 0; i < 4; ++i)
+                o[i] = make_float4(__uint_as_float(ov[4 * i]), __uint_as_float(ov[4 * i + 1]),
+                                   __uint_as_float(ov[4 * i + 2]), __uint_as_float(ov[4 * i + 3]));
             if (row.b < 0) continue;
-            if (done) {
+            if (!(flags & Info::kBegins)) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    uint32_t v[4];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const float2 y = make_float2(o[8 * i + 2 * k], o[8 * i + 2 * k + 1]);
-                        const __nv_bfloat162 b2 = __floats2bfloat162_rn(scale == 0.f ? 0.f : y.x * scale, scale == 0.f ? 0.f : y.y * scale);
-                        v[k] = *reinterpret_cast<const uint32_t*>(&b2);
-                    }
-                    *reinterpret_cast<uint4*>(out + n + 8 * i) = make_uint4(v[0], v[1], v[2], v[3]);
+                    const float4 b = kept[(n / 4 + i) * kRows];
+                    o[i] = make_float4(fmaf(b.x, was, o[i].x * now), fmaf(b.y, was, o[i].y * now),
+                                       fmaf(b.z, was, o[i].z * now), fmaf(b.w, was, o[i].w * now));
                 }
+            }
+            if (done) {
+                uint32_t v[8];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const bool none = scale == 0.f;
+                    const __nv_bfloat162 y = __floats2bfloat162_rn(none ? 0.f : o[i].x * scale, none ? 0.f : o[i].y * scale);
+                    const __nv_bfloat162 z = __floats2bfloat162_rn(none ? 0.f : o[i].z * scale, none ? 0.f : o[i].w * scale);
+                    v[2 * i] = *reinterpret_cast<const uint32_t*>(&y);
+                    v[2 * i + 1] = *reinterpret_cast<const uint32_t*>(&z);
+                }
+                *reinterpret_cast<uint4*>(out + n) = make_uint4(v[0], v[1], v[2], v[3]);
+                *reinterpret_cast<uint4*>(out + n + 8) = make_uint4(v[4], v[5], v[6], v[7]);
             } else {
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    kept[(n / 4 + i) * kRows] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                for (int i = 0; i < 4; ++i) kept[(n / 4 + i) * kRows] = o[i];
             }
         }
         if (!done && quarter == 0) {
@@ -988,8 +1045,12 @@ template <bool kBf16>
 __global__ void __launch_bounds__(Shape<kBf16>::kThreads, 1)
 k_paged_shared(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap tmap) {
     using S = Shape<kBf16>;
-    extern __shared__ uint8_t raw[];
-    auto& sh = *reinterpret_cast<Shared<kBf16>*>(raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u));
+    extern __shared__ __align__(1024) uint8_t raw[];
+    auto& sh = *reinterpret_cast<Shared<kBf16>*>(raw);
+    if (smem_u32(raw) & 1023u) {  // (the operands' layout needs it, and there is no room to move up)
+        if (threadIdx.x == 0) raise_status(a.dev_status, CSA2_DEV_TIMEOUT);
+        return;
+    }
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const int rank = (int)cluster_ctarank(), pair = blockIdx.x >> 1;
     volatile int* abort = &sh.abort;
@@ -997,7 +1058,6 @@ k_paged_shared(const __grid_constant__ Args a, const __grid_constant__ CUtensorM
         for (int i = 0; i < S::kKeys; ++i) {
             mbar_init(&sh.key_full[i], 1);
             mbar_init(&sh.key_empty[i], 1);
-            mbar_init(&sh.key_peer[i], 1);
         }
         for (int i = 0; i < S::kValues; ++i) {
             mbar_init(&sh.value_full[i], 1);
@@ -1006,23 +1066,24 @@ k_paged_shared(const __grid_constant__ Args a, const __grid_constant__ CUtensorM
         }
         for (int i = 0; i < kInfos; ++i) {
             mbar_init(&sh.info_full[i], 1);
-            mbar_init(&sh.info_empty[i], S::kSoftWarps + 3);  // the softmax warps, the MMA warp, two loaders
+            mbar_init(&sh.info_empty[i], S::kSoftWarps + (rank ? 3 : 4));  // the softmax and MMA warps, the loaders
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sh.s_full[i], 1);
+            mbar_init(&sh.p_full[i], 2 * S::kSoftWarps);
+            mbar_init(&sh.pv_done[i], 1);
+            mbar_init(&sh.s_empty[i], 2 * S::kSoftWarps);
             mbar_init(&sh.q_full[i], 2 * S::kHelpWarps);
             mbar_init(&sh.q_here[i], S::kHelpWarps);
             mbar_init(&sh.max_bar[i], 4);
             mbar_init(&sh.sum_bar[i], 4);
         }
-        mbar_init(&sh.p_full, 2 * S::kSoftWarps);
-        mbar_init(&sh.pv_done, 1);
         mbar_init(&sh.q_empty, 1);
-        mbar_init(&sh.drain, 1);
+        mbar_init(&sh.drain, 2);
         sh.abort = 0;
         fence_mbar_init();
     }
-    if (warp == S::kMmaWarp) tmem_alloc_pair(&sh.tmem_base, kTmemCols);
+    if (warp == S::kScoreWarp) tmem_alloc_pair(&sh.tmem_base, kTmemCols);
     // a programmatic launch: only the setup above may overlap the kernel ahead
     grid_dep_launch_dependents();
     tc_fence_before();
@@ -1034,14 +1095,15 @@ k_paged_shared(const __grid_constant__ Args a, const __grid_constant__ CUtensorM
     const uint32_t tmem = __shfl_sync(0xffffffffu, sh.tmem_base, 0);
     if (warp < S::kSoftWarps) {
         softmax_role<kBf16>(sh, a, tmem, warp, lane, rank, pair, abort);
-    } else if (warp == S::kMmaWarp) {
+    } else if (warp == S::kScoreWarp || warp == S::kOutputWarp) {
         if (rank == 0) {
-            mma_role<kBf16>(sh, tmem, lane, abort);
+            if (warp == S::kScoreWarp) score_role<kBf16>(sh, tmem, lane, abort);
+            else output_role<kBf16>(sh, tmem, lane, abort);
             // every MMA issued must finish before TMEM and shared memory are released
             __syncwarp();
             if (elect_one()) tc_commit_pair(&sh.drain);
             if (!mbar_wait_drain(&sh.drain, 0)) *abort = 1;
-        } else {
+        } else if (warp == S::kOutputWarp) {
             relay_role<kBf16>(sh, lane, abort);
         }
     } else if (warp == S::kKeyWarp || warp == S::kValueWarp) {
@@ -1055,7 +1117,7 @@ k_paged_shared(const __grid_constant__ Args a, const __grid_constant__ CUtensorM
     __syncthreads();
     cluster_sync_all();  // nothing of the pair is in flight
     if (tid == 0 && sh.abort) raise_status(a.dev_status, CSA2_DEV_TIMEOUT);
-    if (warp == S::kMmaWarp) {
+    if (warp == S::kScoreWarp) {
         __syncwarp();
         tc_fence_after();
         tmem_dealloc_pair(tmem, kTmemCols);
@@ -1065,7 +1127,7 @@ k_paged_shared(const __grid_constant__ Args a, const __grid_constant__ CUtensorM
 
 template <bool kBf16>
 constexpr int smem_bytes() {
-    return (int)sizeof(Shared<kBf16>) + 1024;
+    return (int)sizeof(Shared<kBf16>);
 }
 static_assert(smem_bytes<true>() <= 227 * 1024 && smem_bytes<false>() <= 227 * 1024, "shared memory of a CTA");
 

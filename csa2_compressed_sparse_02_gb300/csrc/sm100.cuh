@@ -568,6 +568,15 @@ __device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols
 CSA2_MMA_PAIR(mma_f16_pair, "f16")
 CSA2_MMA_PAIR(mma_f8_pair, "f8f6f4")
 #undef CSA2_MMA_PAIR
+// A tiled copy into this CTA's shared memory that counts on a barrier of either CTA of the pair (its
+// address as mapa_shared gives it).
+__device__ __forceinline__ void tma_g2s_2d_pair(uint32_t smem_dst, const void* tmap, int x, int y, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], "
+        "[%1, {%2, %3}], [%4];\n" ::"r"(smem_dst),
+        "l"(tmap), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+}
 // Arrive on the mbarrier at this offset in both CTAs once every pair operation this thread issued so
 // far completes.
 __device__ __forceinline__ void tc_commit_pair(uint64_t* bar) {
