@@ -295,7 +295,7 @@ struct Shape {
     static constexpr int kThreads = 32 * (kHelp0 + kHelpWarps);
     static constexpr uint32_t kChunk = kMine * 128;            // 64 rows x 128 bytes, 128-byte swizzle
     static constexpr uint32_t kPlace = kBf16 ? 2 * kChunk : kChunk;  // 64 positions x 128 channels
-    static constexpr int kKeys = kBf16 ? 4 : 8, kValues = 4;  // places; a tile takes four of each
+    static constexpr int kKeys = kBf16 ? 4 : 7, kValues = kBf16 ? 4 : 6;  // places; a tile takes four of each
     static constexpr uint32_t kWeights = (kBf16 ? 2 : 3) * kChunk;  // P: 64 positions a chunk; E4M3: 128, a part each
     static constexpr uint32_t kIdesc = (1u << 4) | ((128u >> 4) << 24);  // D fp32, M = 128 over the pair
     // N = 128 positions, both K-major; N = 256 channels, B MN-major. Types: bf16 1, E4M3 0, E5M2 1
@@ -319,7 +319,8 @@ struct alignas(16) Info {
         kBegins = 4, kEnds = 8,   // the run begins, ends what this pair has of the unit
         kOpens = 16,              // which opens the pair's range
         kWhole = 32,              // and is all of the unit (set with kEnds)
-        kStop = 64                // no tile: the range is done
+        kStop = 64,               // no tile: the range is done
+        kSeen = 128               // every row of the unit sees every position of the tile
     };
     int t0, lo, hi, k, u0, f, flags, pad;
     uint32_t ok[4];  // the positions whose page exists
@@ -335,9 +336,9 @@ struct Shared {
     __nv_bfloat16 red_max[2][4][kMine];  // rounded up: what it bounds need not be close
     float row_scale[kBf16 ? 0 : 2][kMine];  // E4M3: logit factor, by run parity
     Info info[kInfos];
-    uint64_t key_full[S::kKeys];  // the even CTA's: the place is full in both
-    uint64_t key_empty[S::kKeys], value_full[S::kValues], value_empty[S::kValues];
-    uint64_t value_peer[S::kValues];  // the even CTA's: the odd one's place is full
+    uint64_t key_full[S::kKeys], value_full[S::kValues];  // the even CTA's: the place is full in both
+    uint64_t key_empty[S::kKeys], value_empty[S::kValues];
+    uint64_t value_here;  // the odd CTA's: V of a tile that not all rows see has landed
     uint64_t info_full[kInfos], info_empty[kInfos];
     uint64_t s_full[2], s_empty[2], p_full[2], pv_done[2];  // by tile parity; s_empty, p_full: the even CTA's
     uint64_t q_full[2];   // the even CTA's: both CTAs' rows are staged; by run parity
@@ -394,20 +395,32 @@ __device__ void plan_role(Shared<kBf16>& sh, const Args& a, int lane, int rank, 
         }
         return b;
     };
+    // positions that every sequence of the unit sees, of the shared ones
+    auto seen_by_all = [&](int u0, int f) {
+        int n = INT_MAX;
+        for (int k = lane; k < a.members && u0 + k < a.B; k += 32) {
+            const Slot s = slot_at(a, sh.plan, u0 + k);
+            if (s.f == f && s.b >= 0) n = min(n, s.T);
+        }
+        return __reduce_min_sync(0xffffffffu, n);
+    };
     Tile cur = {}, nxt = {};
     Box box = {}, box_nx = {};
+    int reach = 0;
     bool has = walk.next(cur);
     if (has) box = look(cur);
     int gt = 0;
     for (; has; ++gt) {
         const bool more = walk.next(nxt);
         if (more) box_nx = look(nxt);
+        if (runs == 0 && run == 0) reach = seen_by_all(cur.u0, cur.f);
         const bool ends = !more || nxt.u0 != cur.u0 || nxt.f != cur.f;
         const bool last = ends || run == S::kRun - 1;
         if (gt >= kInfos && !wait(&sh.info_empty[gt % kInfos], (uint32_t)((gt / kInfos - 1) & 1), abort)) return;
         const bool there = box.nth >= 0 && box.page >= 0 && box.page < a.g.n_pages;
         if (box.nth >= 0 && !there && rank == 0) raise_status(a.dev_status, CSA2_DEV_BAD_INDEX);
         const uint32_t held = __ballot_sync(0xffffffffu, there);
+        const bool seen = cur.k < 0 && min(cur.hi, reach) - cur.t0 >= kTile && __all_sync(0xffffffffu, there || pos >= kTile);
         Info& o = sh.info[gt % kInfos];
         if (pos < kTile) o.y[lane] = there ? box.page * ps + cur.t0 + pos - box.nth * ps : a.g.n_pages * ps;
         if (lane < 4) {
@@ -426,7 +439,8 @@ __device__ void plan_role(Shared<kBf16>& sh, const Args& a, int lane, int rank, 
             o.f = cur.f;
             o.flags = (run == 0 ? Info::kFirst : 0) | (last ? Info::kLast : 0) | (runs == 0 ? Info::kBegins : 0) |
                       (ends ? Info::kEnds : 0) | (pieces == 0 ? Info::kOpens : 0) |
-                      (ends && !(pieces == 0 && range.cont) && !(!more && range.cut) ? Info::kWhole : 0);
+                      (ends && !(pieces == 0 && range.cont) && !(!more && range.cut) ? Info::kWhole : 0) |
+                      (seen ? Info::kSeen : 0);
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.info_full[gt % kInfos]);
@@ -461,8 +475,8 @@ __device__ __forceinline__ void info_done(Shared<kBf16>& sh, int gt, int lane) {
 
 // ---------------------------------------------------------------- copies
 // One warp copies the keys, one the values, box by box. One elected lane issues, from values of the
-// whole warp. Keys of both CTAs count on the even one's barrier, where the MMAs wait; values on each
-// CTA's own, which its softmax warps look at too (finite_values).
+// whole warp. Both CTAs' copies count on the even one's barrier, where the MMAs
+// wait (a warp of the odd one that passed on that its places were full: 500 cycles later).
 template <bool kBf16>
 __device__ __noinline__ void load_role(Shared<kBf16>& sh, const Args& a, const CUtensorMap* tmap, bool keys, int lane,
                                        int rank, volatile int* abort) {
@@ -471,31 +485,33 @@ __device__ __noinline__ void load_role(Shared<kBf16>& sh, const Args& a, const C
     uint64_t* const full = keys ? sh.key_full : sh.value_full;
     uint64_t* const empty = keys ? sh.key_empty : sh.value_empty;
     const uint32_t ring = smem_u32(keys ? sh.keys[0] : sh.values[0]);
+    const uint32_t lead = mapa_shared(smem_u32(full), 0);
     const int shift = a.box_shift;
     int slot = 0, g = 0;
     uint32_t phase = 1;  // of a place that is free
     for (int gt = 0;; ++gt) {
         if (!info_wait(sh, gt, abort)) break;
         const Info& in = sh.info[gt % kInfos];
-        if (in.flags & Info::kStop) break;
-        const int y = in.y[lane & 15];
+        const int flags = in.flags, y = in.y[lane & 15];
+        if (flags & Info::kStop) break;
         info_done(sh, gt, lane);
         int i = 0;
 #pragma unroll 1
         for (; i < 4; ++i) {
+            // (a place that has not been in use: its barrier's phase before the first reads as complete)
+            if (!wait(&empty[slot], phase, abort)) break;
             // 64 positions from `first` of the tile, 128 channels from x
             const int first = keys ? kMine * rank : kMine * (i & 1);
             const int x = keys ? 128 * i : 256 * (i >> 1) + 128 * rank;
-            if (g >= places && !wait(&empty[slot], phase, abort)) break;
-            const uint32_t at = ring + (uint32_t)__shfl_sync(0xffffffffu, slot, 0) * S::kPlace;
-            const uint32_t bar = keys ? mapa_shared(smem_u32(&full[slot]), 0) : smem_u32(&full[slot]);
-            if ((!keys || rank == 0) && elect_one()) mbar_arrive_expect_tx(&full[slot], keys ? 2 * S::kPlace : S::kPlace);
+            const uint32_t at = __shfl_sync(0xffffffffu, slot, 0);
+            if (rank == 0 && elect_one()) mbar_arrive_expect_tx(&full[at], 2 * S::kPlace);
 #pragma unroll 1
             for (int b = 0; b < kMine; b += a.box_rows) {
                 const int yb = __shfl_sync(0xffffffffu, y, (first + b) >> shift);
                 if (elect_one()) {
-                    tma_g2s_2d_pair(at + b * 128, tmap, x, yb, bar);
-                    if constexpr (kBf16) tma_g2s_2d_pair(at + b * 128 + S::kChunk, tmap, x + 64, yb, bar);
+                    const uint32_t dst = ring + at * S::kPlace + b * 128;
+                    tma_g2s_2d_pair(dst, tmap, x, yb, lead + 8 * at);
+                    if constexpr (kBf16) tma_g2s_2d_pair(dst + S::kChunk, tmap, x + 64, yb, lead + 8 * at);
                 }
             }
             __syncwarp();
@@ -503,10 +519,16 @@ __device__ __noinline__ void load_role(Shared<kBf16>& sh, const Args& a, const C
             if (++slot == places) slot = 0, phase ^= 1u;
         }
         if (i < 4) break;
+        if (!keys && rank == 0 && !(flags & Info::kSeen)) {  // the odd CTA's softmax may have to know (finite_values)
+            const int of = g - 4 + (lane & 3);
+            if (!wait(&full[of % places], (uint32_t)((of / places) & 1), abort)) break;
+            if (lane == 0) mbar_arrive_peer(mapa_shared(smem_u32(&sh.value_here), 1));
+            __syncwarp();
+        }
     }
     // Whatever ended the loop, no copy outlives the pair, which ends together. (Where a wait has given
     // up, the even CTA may have armed less than the odd one has asked for: a copy takes a microsecond.)
-    if (!keys || rank == 0)
+    if (rank == 0)
         for (int s = max(0, g - places); s < g; ++s) mbar_wait_drain(&full[s % places], (uint32_t)((s / places) & 1));
     if (*abort) __nanosleep(200000);
 }
@@ -586,7 +608,6 @@ __device__ void query_role(Shared<kBf16>& sh, const Args& a, int warp, int lane,
 // Two warps of the even CTA issue the pair's MMAs, one S, one PV: what a warp does between its MMAs
 // (a look at a barrier takes 200 cycles and more) then falls into the other's. The lanes look at a
 // product's barriers together, and it is issued in one go. S is up to two tiles ahead of the softmax.
-// In the odd CTA a warp passes on that the places of V are full.
 template <int kPlaces>
 struct Ring {
     int slot = 0;
@@ -673,13 +694,16 @@ __device__ void output_role(Shared<kBf16>& sh, uint32_t tmem, int lane, volatile
         const int flags = *(volatile int*)&sh.info[gt % kInfos].flags;
         if (flags & Info::kStop) return;
         info_done(sh, gt, lane);
-        const int i = lane & 3;
-        uint64_t* const bar = lane < 4 ? &sh.value_full[values.nth(i)] : lane < 8 ? &sh.value_peer[values.nth(i)] : &sh.p_full[gt & 1];
-        if (!wait(bar, lane < 8 ? values.parity(i) : (uint32_t)((gt >> 1) & 1), abort)) return;
-        tc_fence_after();
         const uint32_t weights = dP + __shfl_sync(0xffffffffu, (uint32_t)(gt & 1) * (S::kWeights >> 4), 0);
 #pragma unroll 1
         for (int n = 0; n < 4; ++n) {
+            if (!(n & 1)) {  // half of the tile's places at a look, as in score_role
+                const bool weights_too = n == 0 && lane >= 16;
+                if (!wait(weights_too ? &sh.p_full[gt & 1] : &sh.value_full[values.nth(lane & 1)],
+                          weights_too ? (uint32_t)((gt >> 1) & 1) : values.parity(lane & 1), abort))
+                    return;
+                tc_fence_after();
+            }
             const uint32_t v = dV + __shfl_sync(0xffffffffu, (uint32_t)values.slot * (S::kPlace >> 4), 0);
             const uint32_t p = weights + (n & 1) * ((kBf16 ? S::kChunk : 64u) >> 4);
             const uint32_t o = tmem + kColO + 128 * (n >> 1), more = (n & 1) || !(flags & Info::kFirst);
@@ -705,23 +729,6 @@ __device__ void output_role(Shared<kBf16>& sh, uint32_t tmem, int lane, volatile
     }
 }
 
-template <bool kBf16>
-__device__ void relay_role(Shared<kBf16>& sh, int lane, volatile int* abort) {
-    using S = Shape<kBf16>;
-    static_assert(S::kValues % 4 == 0, "a tile's places do not wrap");
-    int slot = lane & 3;
-    uint32_t phase = 0;
-    for (int gt = 0;; ++gt) {
-        if (!info_wait(sh, gt, abort)) return;
-        if (*(volatile int*)&sh.info[gt % kInfos].flags & Info::kStop) return;
-        info_done(sh, gt, lane);
-        if (!wait(&sh.value_full[slot], phase, abort)) return;
-        if (lane < 4) mbar_arrive_peer(mapa_shared(smem_u32(&sh.value_peer[slot]), 0));
-        __syncwarp();
-        if ((slot += 4) >= S::kValues) slot -= S::kValues, phase ^= 1u;
-    }
-}
-
 // ---------------------------------------------------------------- softmax and epilogue
 __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
     float2 r;
@@ -735,14 +742,6 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
         " mov.b64 {%0, %1}, z;\n}" : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
     return r;
 }
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-    float2 r;
-    asm("{\n .reg .b64 x, y, z, w;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n mov.b64 w, {%6, %7};\n"
-        " fma.rn.f32x2 z, x, y, w;\n mov.b64 {%0, %1}, z;\n}"
-        : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-    return r;
-}
-
 // The positions that are not finite in any row of the warp.
 __device__ __forceinline__ uint32_t not_finite(const uint32_t (&sv)[32]) {
     uint32_t which = 0;
@@ -751,20 +750,24 @@ __device__ __forceinline__ uint32_t not_finite(const uint32_t (&sv)[32]) {
     return __reduce_or_sync(0xffffffffu, which);
 }
 
+// (nth: tiles that not all rows see before this one.)
 // Makes zeros of what is not finite of positions 32 quarter + (the bits of `which`) in this CTA's
 // places of V of tile gt.
 template <bool kBf16>
-__device__ __noinline__ bool finite_values(Shared<kBf16>& sh, uint32_t which, int gt, int quarter, int lane,
+__device__ __noinline__ bool finite_values(Shared<kBf16>& sh, uint32_t which, int gt, int nth, int quarter, int lane, int rank,
                                            volatile int* abort) {
     using S = Shape<kBf16>;
+    // The tile's V has landed (once PV of the tile before has used what the places held, the phase that
+    // their barriers are in is this tile's).
     if (gt > 0 && !wait(&sh.pv_done[(gt - 1) & 1], (uint32_t)((gt - 1) >> 1) & 1u, abort)) return false;
+    if (rank && !wait(&sh.value_here, (uint32_t)nth & 1u, abort)) return false;
     uint8_t* at[2];
     for (int h = 0; h < 2; ++h) {
         const int g = 4 * gt + 2 * h + (quarter >> 1), slot = g % S::kValues;
-        // PV of the tile before has used what the place held: this is the phase that its barrier is in
-        if (!wait(&sh.value_full[slot], (uint32_t)((g / S::kValues) & 1), abort)) return false;
+        if (!rank && !wait(&sh.value_full[slot], (uint32_t)((g / S::kValues) & 1), abort)) return false;
         at[h] = sh.values[slot];
     }
+    fence_proxy_async_smem();
     constexpr int kUnits = kBf16 ? 32 : 16;  // of 16 bytes: 128 channels in each half
     if (lane < kUnits) {
         const int h = lane / (kUnits / 2), u = lane % (kUnits / 2);
@@ -805,7 +808,7 @@ __device__ void softmax_role(Shared<kBf16>& sh, const Args& a, uint32_t tmem, in
     float m_was = -INFINITY, l_was = 0.f;          // of the piece up to this run
     const float2 c0 = make_float2(0.f, 0.f);
     Row row = {-1, 0, 0, 0};
-    int runs = 0;
+    int runs = 0, partly = 0;  // tiles that not all rows see
     bool last = true;  // the tile before was a run's last
     for (int gt = 0;; ++gt) {
         if (last) {  // a run begins, or the range is done
@@ -821,38 +824,38 @@ __device__ void softmax_role(Shared<kBf16>& sh, const Args& a, uint32_t tmem, in
             }
             ++runs;
         }
-        if (!wait(lane < 16 ? &sh.s_full[gt & 1] : &sh.info_full[gt % kInfos],
-                  (uint32_t)(lane < 16 ? gt >> 1 : gt / kInfos) & 1u, abort))
-            return;
+        {  // S, the tile's entry, and PV of two tiles before: P may be written again
+            uint64_t* bar = lane < 8 ? &sh.s_full[gt & 1] : &sh.info_full[gt % kInfos];
+            uint32_t parity = lane < 8 ? gt >> 1 : gt / kInfos;
+            if (lane >= 16 && gt > 1) {
+                bar = &sh.pv_done[gt & 1];
+                parity = (gt >> 1) - 1;
+            }
+            if (!wait(bar, parity & 1u, abort)) return;
+        }
         tc_fence_after();
         uint32_t sv[32];
         tmem_ld_32x32b_x32_nowait(tl + kColS + 64 * (gt & 1) + 32 * ch, sv);
         const Info& in = sh.info[gt % kInfos];
         const int flags = in.flags;
         last = flags & Info::kLast;
-        // whether this thread's row sees all its positions; rows that stand for nothing see everything
-        const int reach = row.b < 0 ? kTile : min(in.hi, row.T) - in.t0;
-        const bool all = __all_sync(0xffffffffu, in.k < 0 && in.ok[quarter] == ~0u && reach >= kTile);
-        uint32_t seen = ~0u;
-        if (!all && row.b >= 0) {
+        uint32_t seen = ~0u;  // of this thread's positions; rows that stand for nothing see everything
+        if (!(flags & Info::kSeen) && row.b >= 0) {
             const int lo = max(0, min(32, in.lo - in.t0 - p0));
-            const int hi = in.k >= 0 && in.k != row.k ? 0 : max(0, min(32, reach - p0));
+            const int hi = in.k >= 0 && in.k != row.k ? 0 : max(0, min(32, min(in.hi, row.T) - in.t0 - p0));
             seen = in.ok[quarter] & (hi == 32 ? ~0u : (1u << hi) - 1u) & (lo == 32 ? 0u : ~0u << lo);
         }
         tmem_wait_ld_regs32(sv);
         tc_fence_before();
         info_done(sh, gt, lane);
         if (lane == 0) arrive_lead(&sh.s_empty[gt & 1], rank);
-        float2 x[16], odd = c0;  // odd: 0, or NaN where a product is not finite
+        float2 x[16];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            x[i] = make_float2(__uint_as_float(sv[2 * i]), __uint_as_float(sv[2 * i + 1]));
-            odd = fma2(x[i], c0, odd);
-            x[i] = mul2(x[i], make_float2(c, c));
-        }
-        uint32_t which = 0;  // positions whose products are not finite
-        if (__any_sync(0xffffffffu, !(odd.x + odd.y == 0.f))) which = not_finite(sv);
-        if (!all) {
+        for (int i = 0; i < 16; ++i)
+            x[i] = mul2(make_float2(__uint_as_float(sv[2 * i]), __uint_as_float(sv[2 * i + 1])), make_float2(c, c));
+        uint32_t which = 0;  // positions whose products are not finite, where some row may not see them
+        if (!(flags & Info::kSeen)) {
+            which = not_finite(sv);
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
                 x[i].x = (seen >> (2 * i)) & 1u ? x[i].x : -INFINITY;
@@ -924,8 +927,6 @@ __device__ void softmax_role(Shared<kBf16>& sh, const Args& a, uint32_t tmem, in
             }
         }
         l = fmaf(l, alpha, sum.x + sum.y);
-        // PV of two tiles before: P may be written again
-        if (gt > 1 && !wait(&sh.pv_done[gt & 1], (uint32_t)((gt >> 1) - 1) & 1u, abort)) return;
         if (__any_sync(0xffffffffu, alpha != 1.f)) {  // (not in a run's first tile)
             if (!wait(&sh.pv_done[(gt - 1) & 1], (uint32_t)((gt - 1) >> 1) & 1u, abort)) return;  // O is that of the tile before
             tc_fence_after();
@@ -955,7 +956,8 @@ __device__ void softmax_role(Shared<kBf16>& sh, const Args& a, uint32_t tmem, in
         // A weight of zero takes nothing from a position, unless that is not finite: rows that do not see
         // a position must not notice what it holds. Its products with the queries tell. What is not finite
         // of it becomes zero for PV; the rows that see it have NaN (or, of -infinity, zero) weights.
-        if (which && !finite_values(sh, which, gt, quarter, lane, abort)) return;
+        if (which && !finite_values(sh, which, gt, partly, quarter, lane, rank, abort)) return;
+        partly += !(flags & Info::kSeen);
         fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
@@ -1062,11 +1064,10 @@ k_paged_shared(const __grid_constant__ Args a, const __grid_constant__ CUtensorM
         for (int i = 0; i < S::kValues; ++i) {
             mbar_init(&sh.value_full[i], 1);
             mbar_init(&sh.value_empty[i], 1);
-            mbar_init(&sh.value_peer[i], 1);
         }
         for (int i = 0; i < kInfos; ++i) {
             mbar_init(&sh.info_full[i], 1);
-            mbar_init(&sh.info_empty[i], S::kSoftWarps + (rank ? 3 : 4));  // the softmax and MMA warps, the loaders
+            mbar_init(&sh.info_empty[i], S::kSoftWarps + (rank ? 2 : 4));  // the softmax and MMA warps, the loaders
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sh.s_full[i], 1);
@@ -1079,6 +1080,7 @@ k_paged_shared(const __grid_constant__ Args a, const __grid_constant__ CUtensorM
             mbar_init(&sh.sum_bar[i], 4);
         }
         mbar_init(&sh.q_empty, 1);
+        mbar_init(&sh.value_here, 1);
         mbar_init(&sh.drain, 2);
         sh.abort = 0;
         fence_mbar_init();
@@ -1103,8 +1105,6 @@ k_paged_shared(const __grid_constant__ Args a, const __grid_constant__ CUtensorM
             __syncwarp();
             if (elect_one()) tc_commit_pair(&sh.drain);
             if (!mbar_wait_drain(&sh.drain, 0)) *abort = 1;
-        } else if (warp == S::kOutputWarp) {
-            relay_role<kBf16>(sh, lane, abort);
         }
     } else if (warp == S::kKeyWarp || warp == S::kValueWarp) {
         load_role<kBf16>(sh, a, &tmap, warp == S::kKeyWarp, lane, rank, abort);
