@@ -119,32 +119,42 @@ __device__ __forceinline__ int prefix_tiles(const Args& a, const Slot& s, int i)
 __device__ __forceinline__ int own_tiles(const Slot& s) { return s.T > s.sh ? tiles_of(s.T) - s.sh / kTile : 0; }
 
 // ---------------------------------------------------------------- schedule
-// The batch's tiles, unit after unit, are cut into one contiguous range of equal length a pair.
+// The batch's tiles, unit after unit, are cut into one contiguous range a pair.
+//  - As a rule of equal length: most pairs then have the end of one unit and the beginning of another.
+//  - Where there are at most as many units as pairs, a unit may be cut into ceil(tiles / L) equal pieces, one a
+//    pair, with the smallest L whose pieces fit the pairs: the longest range is longer, but a pair has one
+//    piece. kSecondPiece says what the second one costs.
 struct Range {
     int64_t items;
     int i, j;          // it begins with tile j of slot i
     bool cont, cut;    // its first unit began before it; its last one ends behind it
 };
 
-constexpr int kKept = 40;  // slots from the range's first unit on that stay in shared memory
+// In tiles: its queries, its first tile's way through an empty pipeline and its partial result.
+constexpr int kSecondPiece = 4;
 
+constexpr int kKept = 40;  // slots from the range's first unit on that stay in shared memory
 struct PlanShared {
     Slot slots[kKept];
     int base;  // the first of them
-    int64_t warp_sum[16];
-    long long begin, end;  // where the first tile's unit begins, and the last one's ends
     Range range;
+};
+struct PlanScratch {  // (where P comes later)
+    int64_t warp_sum[32], starts[kMaxPairs];  // starts, tiles: of the units
+    uint32_t tiles[kMaxPairs];
+    int fits[32];
+    long long at, end, first, last;  // the range; where the unit that it begins in begins, and the last one ends
 };
 
 // Called by the whole CTA.
-__device__ void plan(const Args& a, PlanShared& sh, int pair) {
+__device__ void plan(const Args& a, PlanShared& sh, PlanScratch& x, int pair) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
     // Exclusive sum over the CTA of n < 2^26, and the sum of all.
     auto scan = [&](uint32_t n, int64_t* all) {
         const uint32_t before = warp_scan(n, lane);
-        if (lane == 31) sh.warp_sum[warp] = (int64_t)before + n;
+        if (lane == 31) x.warp_sum[warp] = (int64_t)before + n;
         __syncthreads();
-        const int64_t w = lane < warps ? sh.warp_sum[lane] : 0;
+        const int64_t w = lane < warps ? x.warp_sum[lane] : 0;
         int64_t warps_before = lane < warp ? w : 0, sum = w;
 #pragma unroll
         for (int o = 16; o >= 1; o >>= 1) {
@@ -163,7 +173,7 @@ __device__ void plan(const Args& a, PlanShared& sh, int pair) {
         *head = unit_of(a, i, s.f) == i;
         return (uint32_t)prefix_tiles(a, s, i) + own_tiles(s);
     };
-    const bool once = a.B <= (int)blockDim.x;  // a slot a thread: one scan
+    const bool once = a.B <= (int)blockDim.x;  // a slot a thread
     int64_t total = 0, all, here = 0;
     uint32_t n = 0;
     bool head = false;
@@ -173,16 +183,49 @@ __device__ void plan(const Args& a, PlanShared& sh, int pair) {
         total += all;
     }
     const Cut ranges(total, a.pairs);
-    const int c = min(pair, ranges.n);
-    const int64_t at = ranges.at(c), end = ranges.at(min(c + 1, ranges.n));
     if (tid == 0) {
-        sh.range.items = end - at;
+        const int c = min(pair, ranges.n);
+        x.at = ranges.at(c);
+        x.end = ranges.at(min(c + 1, ranges.n));
         sh.range.i = sh.range.j = 0;
         sh.base = 0;
-        sh.begin = 0;
-        sh.end = total;
+        x.first = 0;
+        x.last = total;
+    }
+    if (once && total > 0) {
+        int64_t units;
+        const int unit = (int)scan(head ? 1u : 0u, &units) + head - 1;
+        if (units <= a.pairs) {
+            if (tid < kMaxPairs) x.tiles[tid] = 0;
+            __syncthreads();
+            if (n) atomicAdd(&x.tiles[max(unit, 0)], n);
+            if (head) x.starts[unit] = here;
+            __syncthreads();
+            uint32_t lo = (uint32_t)((total + a.pairs - 1) / a.pairs), hi = lo + kSecondPiece + 1;
+            const uint32_t t = tid < units ? x.tiles[tid] : 0;
+            // The smallest L of lo .. hi - 1 with sum ceil(tiles / L) <= pairs, a value a warp; hi: none
+            if (warp <= kSecondPiece) {
+                uint32_t k = 0;
+                for (int u = lane; u < (int)units; u += 32) k += (x.tiles[u] + lo + warp - 1) / (lo + warp);
+                k = __reduce_add_sync(0xffffffffu, k);
+                if (lane == 0) x.fits[warp] = k <= (uint32_t)a.pairs;
+            }
+            __syncthreads();
+            const uint32_t good = __ballot_sync(0xffffffffu, lane <= kSecondPiece && x.fits[lane]);
+            const uint32_t L = good ? lo + __ffs(good) - 1 : hi;
+            if (L < hi) {
+                const uint32_t k = (t + L - 1) / L;
+                if (tid == 0) x.at = x.end = total;
+                const int64_t c = pair - scan(k, &all);
+                if (c >= 0 && c < k) {
+                    x.at = x.starts[tid] + t * c / k;
+                    x.end = x.starts[tid] + t * (c + 1) / k;
+                }
+            }
+        }
     }
     __syncthreads();
+    const int64_t at = x.at, end = x.end;
     int64_t before = 0;
     for (int i0 = 0; i0 < a.B; i0 += blockDim.x) {
         const int i = i0 + tid;
@@ -196,13 +239,14 @@ __device__ void plan(const Args& a, PlanShared& sh, int pair) {
             sh.range.j = (int)(at - here);
             sh.base = unit_of(a, i, s.f);
         }
-        if (head && here <= at) atomicMax(&sh.begin, (long long)here);
-        if (head && here >= end) atomicMin(&sh.end, (long long)here);
+        if (head && here <= at) atomicMax(&x.first, (long long)here);
+        if (head && here >= end) atomicMin(&x.last, (long long)here);
     }
     __syncthreads();
     if (tid == 0) {
-        sh.range.cont = sh.begin < at;
-        sh.range.cut = sh.end > end;
+        sh.range.items = end - at;
+        sh.range.cont = x.first < at;
+        sh.range.cut = x.last > end;
     }
     if (once) {
         if (tid >= sh.base && tid < min(sh.base + kKept, a.B)) sh.slots[tid - sh.base] = s;
@@ -307,7 +351,7 @@ struct Shape {
     static constexpr float kLift = kBf16 ? 0.f : 9.f;
     // Tiles that add up in TMEM under one maximum (see csa2_paged_attn: of a long tail less than 2^-9
     // of the weight is lost); what came before is added in fp32.
-    static constexpr int kRun = 128;
+    static constexpr int kRun = kBf16 ? 192 : 128;
 };
 constexpr uint32_t kColO = 0, kColS = 256;  // TMEM: O 2 x 128 columns, S 2 x 64
 constexpr uint32_t kTmemCols = 512;         // one CTA an SM, so it takes them all
@@ -550,47 +594,67 @@ __device__ void query_role(Shared<kBf16>& sh, const Args& a, int warp, int lane,
         f = t.f;
         run = 1;
         const Row mine = row_info(a, sh.plan, u0, f, kMine * rank + min(warp + S::kHelpWarps * lane, kMine - 1));
-        if (it > 0 && !wait(&sh.q_empty, (uint32_t)((it - 1) & 1), abort)) return;
+        if (it > 0) {
+            // the rows into L2 while the run before still needs its own
+            for (int i = 0, r = warp; r < kMine; ++i, r += S::kHelpWarps) {
+                const int b = __shfl_sync(0xffffffffu, mine.b, i), h = __shfl_sync(0xffffffffu, mine.h, i);
+                if (lane < 8 && b >= 0) prefetch_l2(a.q + b * a.q_seq + h * a.q_head + 64 * lane);
+            }
+            if (!wait(&sh.q_empty, (uint32_t)((it - 1) & 1), abort)) return;
+        }
+        if constexpr (kBf16) {
 #pragma unroll 4
-        for (int i = 0, r = warp; r < kMine; ++i, r += S::kHelpWarps) {
-            const int b = __shfl_sync(0xffffffffu, mine.b, i), h = __shfl_sync(0xffffffffu, mine.h, i);
-            const __nv_bfloat16* src = a.q + (b < 0 ? 0 : b * a.q_seq + h * a.q_head);
-            if constexpr (kBf16) {
+            for (int i = 0, r = warp; r < kMine; ++i, r += S::kHelpWarps) {
+                const int b = __shfl_sync(0xffffffffu, mine.b, i), h = __shfl_sync(0xffffffffu, mine.h, i);
+                const __nv_bfloat16* src = a.q + (b < 0 ? 0 : b * a.q_seq + h * a.q_head);
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
                     const int u = lane + 32 * x;
                     cp_async_16(smem_u32(sh.q) + (u >> 3) * S::kChunk + sw128(r, u & 7), src + 8 * u, b >= 0);
                 }
-            } else {
-                uint4 w2[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
-                if (b >= 0) {
-                    w2[0] = __ldg(reinterpret_cast<const uint4*>(src) + 2 * lane);
-                    w2[1] = __ldg(reinterpret_cast<const uint4*>(src) + 2 * lane + 1);
-                }
-                const uint32_t w[8] = {w2[0].x, w2[0].y, w2[0].z, w2[0].w, w2[1].x, w2[1].y, w2[1].z, w2[1].w};
-                float mx = 0.f;
+            }
+        } else {
+            constexpr int kAtOnce = 4;  // rows whose loads are in flight together
+#pragma unroll 1
+            for (int i0 = 0; warp + S::kHelpWarps * i0 < kMine; i0 += kAtOnce) {
+                uint4 w2[kAtOnce][2];
 #pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(w[k] << 16)), fabsf(__uint_as_float(w[k] & 0xffff0000u))));
-                mx = warp_max(mx);
-                int s = 7 - ((int)((__float_as_uint(mx) >> 23) & 0xffu) - 127);
-                s = max(-126, min(126, s));
-                const float two_s = __uint_as_float((uint32_t)(s + 127) << 23);
-                uint32_t hi[4] = {}, lo[4] = {};
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    float x = __uint_as_float(w[k] << 16) * two_s, y = __uint_as_float(w[k] & 0xffff0000u) * two_s;
-                    x = fmaf(x, 0.f, x);  // infinity to NaN: E4M3 has none
-                    y = fmaf(y, 0.f, y);
-                    const uint32_t xy = e4m3x2(x, y);
-                    const float2 got = e4m3x2_to_float2(xy);
-                    hi[k >> 1] |= xy << (16 * (k & 1));
-                    lo[k >> 1] |= e4m3x2(x - got.x, y - got.y) << (16 * (k & 1));
+                for (int i = 0; i < kAtOnce; ++i) {
+                    const int b = __shfl_sync(0xffffffffu, mine.b, i0 + i), h = __shfl_sync(0xffffffffu, mine.h, i0 + i);
+                    const uint4* src = reinterpret_cast<const uint4*>(a.q + (b < 0 ? 0 : b * a.q_seq + h * a.q_head)) + 2 * lane;
+                    w2[i][0] = w2[i][1] = make_uint4(0u, 0u, 0u, 0u);
+                    if (b >= 0) w2[i][0] = __ldg(src), w2[i][1] = __ldg(src + 1);
                 }
-                uint8_t* q = sh.q + (lane >> 3) * S::kChunk + sw128(r, lane & 7);
-                *reinterpret_cast<uint4*>(q) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                *reinterpret_cast<uint4*>(q + 4 * S::kChunk) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-                if (lane == 0) sh.row_scale[it & 1][r] = a.scale_log2 * __uint_as_float((uint32_t)(127 - s) << 23);
+#pragma unroll
+                for (int i = 0; i < kAtOnce; ++i) {
+                    const int r = warp + S::kHelpWarps * (i0 + i);
+                    if (r >= kMine) break;
+                    const uint32_t w[8] = {w2[i][0].x, w2[i][0].y, w2[i][0].z, w2[i][0].w,
+                                           w2[i][1].x, w2[i][1].y, w2[i][1].z, w2[i][1].w};
+                    float mx = 0.f;
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(w[k] << 16)), fabsf(__uint_as_float(w[k] & 0xffff0000u))));
+                    mx = warp_max(mx);
+                    int s = 7 - ((int)((__float_as_uint(mx) >> 23) & 0xffu) - 127);
+                    s = max(-126, min(126, s));
+                    const float two_s = __uint_as_float((uint32_t)(s + 127) << 23);
+                    uint32_t hi[4] = {}, lo[4] = {};
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        float x = __uint_as_float(w[k] << 16) * two_s, y = __uint_as_float(w[k] & 0xffff0000u) * two_s;
+                        x = fmaf(x, 0.f, x);  // infinity to NaN: E4M3 has none
+                        y = fmaf(y, 0.f, y);
+                        const uint32_t xy = e4m3x2(x, y);
+                        const float2 got = e4m3x2_to_float2(xy);
+                        hi[k >> 1] |= xy << (16 * (k & 1));
+                        lo[k >> 1] |= e4m3x2(x - got.x, y - got.y) << (16 * (k & 1));
+                    }
+                    uint8_t* q = sh.q + (lane >> 3) * S::kChunk + sw128(r, lane & 7);
+                    *reinterpret_cast<uint4*>(q) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                    *reinterpret_cast<uint4*>(q + 4 * S::kChunk) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                    if (lane == 0) sh.row_scale[it & 1][r] = a.scale_log2 * __uint_as_float((uint32_t)(127 - s) << 23);
+                }
             }
         }
         if constexpr (kBf16) cp_async_wait_all();
@@ -1093,7 +1157,7 @@ k_paged_shared(const __grid_constant__ Args a, const __grid_constant__ CUtensorM
     cluster_sync_all();  // the other CTA's barriers are there
     tc_fence_after();
     grid_dep_wait();
-    plan(a, sh.plan, pair);  // ends with a CTA barrier
+    plan(a, sh.plan, *reinterpret_cast<PlanScratch*>(sh.p), pair);  // ends with a CTA barrier
     const uint32_t tmem = __shfl_sync(0xffffffffu, sh.tmem_base, 0);
     if (warp < S::kSoftWarps) {
         softmax_role<kBf16>(sh, a, tmem, warp, lane, rank, pair, abort);

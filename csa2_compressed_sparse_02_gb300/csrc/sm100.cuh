@@ -278,6 +278,9 @@ __device__ __forceinline__ void bulk_prefetch_l2(const void* gsrc, uint32_t byte
     asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;\n" ::"l"(gsrc), "r"(bytes) : "memory");
 }
 
+// The line of an address into L2.
+__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];\n" ::"l"(p)); }
+
 // 16 bytes global -> shared by the calling thread, zeros when !pred (nothing is read then).
 __device__ __forceinline__ void cp_async_16(uint32_t smem_dst, const void* gsrc, bool pred) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(smem_dst), "l"(gsrc),
