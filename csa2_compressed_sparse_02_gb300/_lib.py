@@ -68,12 +68,15 @@ SIGNATURES = {
     "csa2_rope": (I32, [PP, I32, I32, I64, I32, I32, I32, I32, P, I64, I64, P, I64, I64, P, P]),
     "csa2_page_workspace_size": (SZ, [GP]),
     "csa2_page_reserve": (I32, [PP, GP, I32, P, P, P, P, SZ, P, P]),
+    "csa2_page_slots": (I32, [PP, GP, I32, P, P, P, I32, P, P, P, P, P, P, SZ, P, P]),
     "csa2_page_release": (I32, [PP, GP, I32, P, P, I32, I32, P, P]),
     "csa2_page_fork": (I32, [PP, GP, I32, P, P, P, P, SZ, P, P]),
     "csa2_page_compact": (I32, [PP, GP, P, P, SZ, P, P]),
     "csa2_page_write": (I32, [PP, GP, I32, I64, P, I32, I64, P, P, P, P]),
     "csa2_paged_attn_workspace_size": (SZ, [PP, GP, I32]),
     "csa2_paged_attn": (I32, [PP, GP, I32, I32, P, I64, I64, P, P, P, I32, I32, P, P, SZ, P, P]),
+    "csa2_prefix_groups_workspace_size": (SZ, [I32]),
+    "csa2_prefix_groups": (I32, [PP, GP, I32, P, P, I32, P, P, P, P, SZ, P, P]),
     "csa2_paged_attn_shared_workspace_size": (SZ, [PP, GP, I32]),
     "csa2_paged_attn_shared": (I32, [PP, GP, I32, I32, P, I64, I64, P, P, P, P, P, P, P, P, SZ, P, P]),
     "csa2_fp4_mma_peak": (I32, [I32, I32, P, P]),

@@ -317,6 +317,20 @@ def page_reserve(params, cache, seq, n_from, n_to, dev_status=None, stream=None)
          cache.ws_ptr, cache.ws_bytes, _status(dev_status, dev))
 
 
+def page_slots(params, cache, seq, n_tokens, n_new, slots, dev_status=None, stream=None):
+    """The block tables and slot maps of a step (csa2_page_slots): request i brings n_new [B] rows to
+    the n_tokens [B] positions of sequence seq [B]; their pages are reserved, and `slots` (SlotMap)
+    receives every row's place and the lengths behind the step."""
+    B, dev = seq.numel(), cache.index
+    if slots.n_tokens.numel() != B:
+        _fail("page_slots: slots are for %d requests, not %d" % (slots.n_tokens.numel(), B))
+    N = slots.seq.numel()
+    _run("page_slots", dev, stream, lib().csa2_page_slots, params, cache.c, B, _i32("seq", seq, B, dev),
+         _i32("n_tokens", n_tokens, B, dev), _i32("n_new", n_new, B, dev), N, _at("slots", slots.n_tokens, dev),
+         slots.start.data_ptr(), slots.seq.data_ptr(), slots.pos.data_ptr(), slots.slot.data_ptr(),
+         cache.ws_ptr, cache.ws_bytes, _status(dev_status, dev))
+
+
 def page_release(params, cache, seq, n_tokens=None, window=0, n_first=0, dev_status=None, stream=None):
     """Let go of every page of sequences seq [N], or with n_tokens [N] of those that no later
     token sees through window and n_first (csa2_page_release)."""
@@ -389,6 +403,18 @@ def paged_attn(params, cache, layer, q, sink, seq, n_tokens, out, workspace, win
          _at("q", q, dev), q.stride(0), q.stride(1), None if sink is None else _at("sink", sink, dev),
          None if seq is None else _i32("seq", seq, B, dev), _i32("n_tokens", n_tokens, B, dev),
          window, n_first, _at("out", out, dev), _at("workspace", workspace, dev), workspace.nbytes,
+         _status(dev_status, dev))
+
+
+def prefix_groups(params, cache, seq, n_tokens, groups, least=1, dev_status=None, stream=None):
+    """Find which sequences of a batch share at least `least` leading positions (csa2_prefix_groups):
+    seq [B] int32 or None (row b of the table), n_tokens [B] int32; `groups` (PrefixGroups) receives
+    order, first and shared."""
+    B, dev = n_tokens.numel(), cache.index
+    _run("prefix_groups", dev, stream, lib().csa2_prefix_groups, params, cache.c, B,
+         None if seq is None else _i32("seq", seq, B, dev), _i32("n_tokens", n_tokens, B, dev), least,
+         _i32("groups.order", groups.order, B, dev), _i32("groups.first", groups.first, B, dev),
+         _i32("groups.shared", groups.shared, B, dev), groups.workspace.data_ptr(), groups.workspace.numel(),
          _status(dev_status, dev))
 
 
@@ -544,6 +570,18 @@ class PagedCache:
         self.ws_ptr, self.ws_bytes = self.workspace.data_ptr(), self.workspace.numel()
 
 
+class SlotMap:
+    """Where the rows of a step of B requests and N rows go (csa2_page_slots): n_tokens [B] (behind the
+    step), start [B + 1], seq and pos [N] int32, slot [N] int64. page_slots writes all of them; rows
+    behind the last one are -1, which rope and page_write skip, so a captured step of N rows takes fewer."""
+
+    def __init__(self, B, N, device="cuda"):
+        self.n_tokens = torch.empty(B, dtype=torch.int32, device=device)
+        self.start = torch.empty(B + 1, dtype=torch.int32, device=device)
+        self.seq, self.pos = torch.empty(2, N, dtype=torch.int32, device=device).unbind(0)
+        self.slot = torch.empty(N, dtype=torch.int64, device=device)
+
+
 class PrefixGroups:
     """Which sequences of a batch share leading positions (csa2_prefix_groups): order, first and
     shared [B] int32, allocated here for B sequences or the caller's own. Slot i of the batch's
@@ -558,6 +596,8 @@ class PrefixGroups:
         for name, t in (("order", order), ("first", first), ("shared", shared)):
             _i32(name, t, order.numel(), order.get_device())
         self.order, self.first, self.shared = order, first, shared
+        n = lib().csa2_prefix_groups_workspace_size(order.numel())
+        self.workspace = torch.empty(max(int(n), 256), dtype=torch.uint8, device=order.device)
 
 
 def n_blocks(n: int) -> int:

@@ -33,7 +33,7 @@ int ensure_loaded() {
     cudaError_t (*lists[])() = {preload_compress, preload_index, preload_index_shared,
                                 preload_select, preload_attn, preload_attn_tc, preload_peak,
                                 preload_rope, preload_pages, preload_paged_attn,
-                                preload_paged_shared};
+                                preload_paged_shared, preload_groups};
     for (auto f : lists) {
         const cudaError_t e = f();
         if (e != cudaSuccess) {

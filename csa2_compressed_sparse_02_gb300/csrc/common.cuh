@@ -59,6 +59,7 @@ cudaError_t preload_rope();
 cudaError_t preload_pages();
 cudaError_t preload_paged_attn();
 cudaError_t preload_paged_shared();
+cudaError_t preload_groups();
 
 // Single-layer sparse attention (csa2_sparse_attn, quantised formats) on the
 // tcgen05 kernel of sparse_attn_tc.cu with the even split schedule; the

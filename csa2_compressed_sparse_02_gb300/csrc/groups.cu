@@ -1,0 +1,263 @@
+// csa2_prefix_groups: which sequences of a batch hold the same leading pages, and how many positions
+// they have in common, for csa2_paged_attn_shared.
+//
+// Pages that are shared are shared from the first on (a fork shares its parent's full pages), so
+// sequences with the same page at position least - 1 are candidates; the lowest-numbered one of them
+// leads, and the others' rows of the table are compared with its entry by entry. The first kernel does that with a warp a
+// sequence; the second one, a CTA, puts the sequences in order. Both are chains of round trips.
+#include <climits>
+
+#include "pages.cuh"
+#include "sm100.cuh"
+
+namespace csa2 {
+namespace {
+
+constexpr int kWarps = 8;      // sequences a CTA of the first kernel takes
+constexpr int kKeys = 2048;    // of the batch's keys at a time
+constexpr int kOrder = 1024;   // threads of the second one
+
+// Scratch: of each sequence of the call its leader and what they have in common, and by leader the
+// members, their first slot and the least of what they have in common; and the members so far.
+struct Scratch {
+    int32_t *lead, *common, *count, *start, *least, *seen;
+};
+int64_t scratch_bytes(int64_t B) { return 6 * 4 * B; }
+Scratch scratch_of(void* ws, int B) {
+    int32_t* p = static_cast<int32_t*>(ws);
+    return {p, p + B, p + 2 * (int64_t)B, p + 3 * (int64_t)B, p + 4 * (int64_t)B, p + 5 * (int64_t)B};
+}
+
+struct Args {
+    Pages g;
+    int B, least;
+    const int32_t *seq, *n_tokens;
+    int32_t *order, *first, *shared;
+    Scratch ws;
+    int32_t* dev_status;
+};
+
+__device__ __forceinline__ int row_of(const Args& a, int b) { return a.seq ? a.seq[b] : b; }
+
+// Positions that sequence b has (0: it takes no part).
+__device__ __forceinline__ int length_of(const Args& a, int b, int row) {
+    const int64_t T = a.n_tokens[b];
+    return row < 0 || row >= a.g.max_seqs || T < 0 ? 0 : (int)min(T, a.g.max_len());
+}
+
+__device__ __forceinline__ bool real(const Args& a, int page) { return page >= 0 && page < a.g.n_pages; }
+
+// The page of position least - 1, or a number that no other sequence has.
+__device__ __forceinline__ int key_of(const Args& a, int b) {
+    const int row = row_of(a, b), at = (a.least - 1) / a.g.page_size;
+    if (length_of(a, b, row) < a.least || at >= a.g.max_pages) return -1 - b;
+    const int page = a.g.table[(int64_t)row * a.g.max_pages + at];
+    return real(a, page) ? page : -1 - b;
+}
+
+__global__ void __launch_bounds__(32 * kWarps) k_groups_compare(const __grid_constant__ Args a) {
+    __shared__ int32_t keys[kKeys];
+    __shared__ int left;
+    sm100::grid_dep_wait();
+    sm100::grid_dep_launch_dependents();
+    const int lane = threadIdx.x & 31, b = blockIdx.x * kWarps + (threadIdx.x >> 5);
+    const int mine = b < a.B ? key_of(a, b) : 0;
+    int lead = b < a.B && mine >= 0 ? -1 : b;  // -1: not found yet
+    if (b < a.B && lane == 0) {
+        const int row = row_of(a, b), T = a.n_tokens[b];
+        if (row >= a.g.max_seqs) raise_status(a.dev_status, CSA2_DEV_BAD_INDEX);
+        else if (row >= 0 && (T < 0 || T > a.g.max_len())) raise_status(a.dev_status, CSA2_DEV_BAD_LENGTH);
+    }
+    for (int j0 = 0; j0 < a.B; j0 += kKeys) {
+        if (threadIdx.x == 0) left = 0;
+        const int n = min(kKeys, a.B - j0);
+        __syncthreads();
+        for (int j = threadIdx.x; j < n; j += 32 * kWarps) keys[j] = key_of(a, j0 + j);
+        if (lead < 0 && lane == 0) left = 1;
+        __syncthreads();
+        if (!left) break;
+        for (int j = 0; j < n && lead < 0; j += 32) {
+            const uint32_t same = __ballot_sync(0xffffffffu, j + lane < n && keys[j + lane] == mine);
+            if (same) lead = j0 + j + __ffs(same) - 1;
+        }
+        __syncthreads();
+    }
+    if (b >= a.B) return;
+    int common = 0;
+    if (lead != b) {
+        const int r0 = row_of(a, b), r1 = row_of(a, lead);
+        const int n = min(length_of(a, b, r0), length_of(a, lead, r1));
+        const int32_t *x = a.g.table + (int64_t)r0 * a.g.max_pages, *y = a.g.table + (int64_t)r1 * a.g.max_pages;
+        const int pages = (int)(((int64_t)n + a.g.page_size - 1) / a.g.page_size);
+        int same = pages;
+        constexpr int kAtOnce = 4;  // entries a lane whose loads are in flight together
+        for (int k0 = 0; k0 < pages; k0 += 32 * kAtOnce) {
+            int u[kAtOnce], v[kAtOnce];
+#pragma unroll
+            for (int i = 0; i < kAtOnce; ++i) {
+                const int k = k0 + 32 * i + lane;
+                u[i] = k < pages ? x[k] : 0;
+                v[i] = k < pages ? y[k] : 0;
+            }
+            bool found = false;
+#pragma unroll
+            for (int i = 0; i < kAtOnce; ++i) {
+                const uint32_t other = __ballot_sync(0xffffffffu, u[i] != v[i] || !real(a, u[i]));
+                if (other && !found) {
+                    same = min(same, k0 + 32 * i + __ffs(other) - 1);
+                    found = true;
+                }
+            }
+            if (found) break;
+        }
+        common = (int)min((int64_t)n, (int64_t)same * a.g.page_size);
+        if (common < a.least) lead = b;
+    }
+    if (lane == 0) {
+        a.ws.lead[b] = lead;
+        a.ws.common[b] = common;
+    }
+}
+
+// Exclusive sum over the CTA; *total gets the sum. Two CTA barriers.
+__device__ __forceinline__ int scan(int v, int* total) {
+    __shared__ int warp_sum[kOrder / 32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int inc = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int up = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += up;
+    }
+    if (lane == 31) warp_sum[warp] = inc;
+    __syncthreads();
+    const int w = warp_sum[lane];
+    int before = lane < warp ? w : 0, all = w;
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) {
+        before += __shfl_xor_sync(0xffffffffu, before, o);
+        all += __shfl_xor_sync(0xffffffffu, all, o);
+    }
+    __syncthreads();
+    *total = all;
+    return before + inc - v;
+}
+
+// Groups in the order of their leaders, members ascending, padding behind them. Batches of up to
+// kOrder sequences are counted in shared memory, others in the scratch, kOrder at a time.
+__global__ void __launch_bounds__(kOrder) k_groups_order(const __grid_constant__ Args a) {
+    __shared__ int32_t leads[kOrder], count_s[kOrder], start_s[kOrder], least_s[kOrder], seen_s[kOrder];
+    sm100::grid_dep_wait();
+    const int tid = threadIdx.x;
+    const bool small = a.B <= kOrder;
+    int32_t *count = small ? count_s : a.ws.count, *start = small ? start_s : a.ws.start;
+    int32_t *least = small ? least_s : a.ws.least, *seen = small ? seen_s : a.ws.seen;
+    for (int b = tid; b < a.B; b += kOrder) {
+        count[b] = seen[b] = 0;
+        least[b] = INT_MAX;
+    }
+    __syncthreads();
+    for (int b = tid; b < a.B; b += kOrder) {
+        if (row_of(a, b) < 0) continue;
+        const int l = a.ws.lead[b];
+        atomicAdd(&count[l], 1);
+        if (l != b) atomicMin(&least[l], a.ws.common[b]);
+    }
+    __syncthreads();
+    int slots = 0, total;
+    for (int b0 = 0; b0 < a.B; b0 += kOrder) {
+        const int b = b0 + tid;
+        const int at = slots + scan(b < a.B ? count[b] : 0, &total);
+        if (b < a.B) start[b] = at;
+        slots += total;
+    }
+    int padding = slots;
+    for (int b0 = 0; b0 < a.B; b0 += kOrder) {
+        const int b = b0 + tid;
+        const bool pad = b < a.B && row_of(a, b) < 0;
+        const int l = b < a.B && !pad ? a.ws.lead[b] : -1;
+        leads[tid] = l;
+        const int at = padding + scan(pad ? 1 : 0, &total);  // (a barrier between leads' writes and reads)
+        padding += total;
+        if (pad) {
+            a.order[at] = b;
+            a.first[at] = at;
+            a.shared[at] = 0;
+        }
+        int rank = 0;
+        if (l >= 0) {
+            // members before this one: those of earlier rounds, then this round's
+            rank = seen[l];
+            const int from = l >= b0 ? l - b0 : 0;
+            if (l != b)
+                for (int j = from; j < tid; ++j) rank += leads[j] == l;
+            const int slot = start[l] + rank;
+            a.order[slot] = b;
+            a.first[slot] = start[l];
+            a.shared[slot] = least[l] == INT_MAX ? 0 : least[l];
+        }
+        __syncthreads();
+        if (l >= 0) atomicAdd(&seen[l], 1);
+        __syncthreads();
+    }
+}
+
+template <typename K>
+int launch(K* k, dim3 grid, int threads, void* stream, const Args& a) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.stream = static_cast<cudaStream_t>(stream);
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cudaLaunchKernelEx(&cfg, k, a);
+    return check_launch("prefix_groups");
+}
+
+}  // namespace
+
+cudaError_t preload_groups() {
+    if (const cudaError_t e = preload_kernel(k_groups_compare)) return e;
+    return preload_kernel(k_groups_order);
+}
+
+}  // namespace csa2
+
+using namespace csa2;
+
+extern "C" size_t csa2_prefix_groups_workspace_size(int B) {
+    return B > 0 ? ((size_t)scratch_bytes(B) + 255) & ~(size_t)255 : 0;
+}
+
+extern "C" int csa2_prefix_groups(const csa2_params* p, const csa2_pages* c, int B, const int32_t* seq,
+                                  const int32_t* n_tokens, int least, int32_t* order, int32_t* first,
+                                  int32_t* shared, void* workspace, size_t ws_bytes, int32_t* dev_status,
+                                  void* stream) {
+    Args a = {};
+    if (const int rc = check_pages("prefix_groups", p, c, &a.g)) return rc;
+    if (B < 0 || least < 1) return fail(CSA2_ERR_INVALID_ARG, "prefix_groups: negative size, or least below 1");
+    if (B > 65535) return fail(CSA2_ERR_UNSUPPORTED, "prefix_groups: at most 65535 sequences");
+    if (B == 0) return CSA2_OK;
+    if (!seq && B > a.g.max_seqs) return fail(CSA2_ERR_INVALID_ARG, "prefix_groups: B beyond max_seqs needs seq");
+    if (!n_tokens || !order || !first || !shared || !workspace)
+        return fail(CSA2_ERR_INVALID_ARG, "prefix_groups: NULL buffer");
+    if (reinterpret_cast<uintptr_t>(workspace) & 255u)
+        return fail(CSA2_ERR_ALIGN, "prefix_groups: workspace must be 256-byte aligned");
+    if ((int64_t)ws_bytes < scratch_bytes(B))
+        return fail(CSA2_ERR_SHAPE, "prefix_groups: workspace smaller than csa2_prefix_groups_workspace_size");
+    if (const int rc = ensure_loaded()) return rc;
+    a.B = B;
+    a.least = least;
+    a.seq = seq;
+    a.n_tokens = n_tokens;
+    a.order = order;
+    a.first = first;
+    a.shared = shared;
+    a.ws = scratch_of(workspace, B);
+    a.dev_status = dev_status;
+    if (const int rc = launch(k_groups_compare, dim3((B + kWarps - 1) / kWarps), 32 * kWarps, stream, a)) return rc;
+    return launch(k_groups_order, dim3(1), kOrder, stream, a);
+}

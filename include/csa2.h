@@ -575,6 +575,29 @@ int csa2_page_reserve(const csa2_params* p, const csa2_pages* c, int N, const in
                       int32_t* dev_status, void* stream);
 
 /*
+ * csa2_page_slots — a step's block tables and slot maps from the lengths of its requests: request
+ * i holds n_tokens[i] positions of sequence seq[i] and brings n_new[i] rows. Reserves the pages of
+ * the new positions as csa2_page_reserve does (the lowest-numbered free ones, in the order of
+ * (i, position)) and writes, for the rows of all requests in a list of N,
+ *   n_after   [B] int32: n_tokens[i] + n_new[i]
+ *   row_start [B + 1] int32: the first row of request i; at B, the rows in all
+ *   row_seq, row_pos [N] int32: each row's sequence and position (what csa2_page_write and csa2_rope
+ *             take); -1 behind the last row
+ *   row_slot  [N] int64: its row in a layer of the pool, page * page_size + position % page_size; -1
+ *             where there is no page, and behind the last row
+ *   seq, n_tokens, n_new [B] int32, device. seq[i] < 0 is padding: no rows. A sequence past max_seqs or
+ *   listed before sets CSA2_DEV_BAD_INDEX; a length below 0 or beyond max_pages pages
+ *   CSA2_DEV_BAD_LENGTH, as does the first request whose rows do not fit into N, and every one with rows
+ *   behind it. Such a request has no rows and takes no pages, and its n_after is n_tokens[i].
+ *   CSA2_DEV_NO_PAGE as in csa2_page_reserve. n_after may be n_tokens itself.
+ *   workspace: that of the page calls. B <= max(max_seqs, 1024).
+ */
+int csa2_page_slots(const csa2_params* p, const csa2_pages* c, int B, const int32_t* seq,
+                    const int32_t* n_tokens, const int32_t* n_new, int N, int32_t* n_after,
+                    int32_t* row_start, int32_t* row_seq, int32_t* row_pos, int64_t* row_slot,
+                    void* workspace, size_t ws_bytes, int32_t* dev_status, void* stream);
+
+/*
  * csa2_page_release — let go of pages of N sequences: their entries become -1 and the
  * pages' counts fall by one (a page with count 0 is free).
  *   n_tokens NULL: every page. Else the pages that no later token of a sequence with
@@ -670,6 +693,28 @@ int csa2_paged_attn(const csa2_params* p, const csa2_pages* c, int layer, int B,
                     const void* q, int64_t q_seq, int64_t q_head, const float* sink,
                     const int32_t* seq, const int32_t* n_tokens, int window, int n_first,
                     void* out, void* workspace, size_t ws_bytes, int32_t* dev_status, void* stream);
+
+/* Bytes of scratch csa2_prefix_groups needs for B sequences. */
+size_t csa2_prefix_groups_workspace_size(int B);
+
+/*
+ * csa2_prefix_groups — the groups of a batch for csa2_paged_attn_shared, from the page table.
+ * Sequences that have the same page at position least - 1 are compared with the first one of them in the
+ * call: positions are common as long as both rows of the table name the same page of the pool and
+ * both sequences reach there. Those with at least `least` in common form a group with it, whose
+ * shared positions are the least that any of them has in common; every other sequence is a group
+ * of its own, which shares 0.
+ *   seq [B] int32, device (NULL: row b), n_tokens [B] int32, device, as in csa2_paged_attn; the same
+ *   sequence may appear often.
+ *   order, first, shared [B] int32 out, device (csa2_paged_attn_shared): groups in the order of their
+ *   first sequences, sequences of a group in that of the call; seq[b] < 0 (padding) behind them.
+ *   A sequence out of range sets CSA2_DEV_BAD_INDEX, a length out of range CSA2_DEV_BAD_LENGTH.
+ *   least >= 1: fewer are not worth a group. B <= 65535.
+ *   workspace: csa2_prefix_groups_workspace_size(B) bytes, 256-byte aligned, contents arbitrary.
+ */
+int csa2_prefix_groups(const csa2_params* p, const csa2_pages* c, int B, const int32_t* seq,
+                       const int32_t* n_tokens, int least, int32_t* order, int32_t* first,
+                       int32_t* shared, void* workspace, size_t ws_bytes, int32_t* dev_status, void* stream);
 
 /* Bytes of scratch csa2_paged_attn_shared needs on the current device (for any B). */
 size_t csa2_paged_attn_shared_workspace_size(const csa2_params* p, const csa2_pages* c, int B);
