@@ -14,6 +14,7 @@
 // between the two products), so a CTA streams 1,024 bytes a position in bf16, and each place of the
 // ring comes free as soon as its own product has read it.
 #include <climits>
+#include <type_traits>
 
 #include "attn.cuh"
 #include "pages.cuh"
@@ -103,7 +104,7 @@ __device__ __forceinline__ Slot slot_of(const Args& a, int i, bool report) {
     if (s.row == INT_MAX) s.row = -1;
     s.T = s.row < 0 ? 0 : length_of(a, a.n_tokens[s.b], report);
     s.prow = row_of(a, a.order[s.f], false);
-    if (s.prow == INT_MAX) s.prow = -1;
+    if (s.prow < 0 || s.prow == INT_MAX) s.sh = 0;  // no sequence to read them through
     return s;
 }
 
@@ -329,7 +330,7 @@ __device__ __noinline__ Row row_info(const Args& a, const PlanShared& plan, int 
 // kBf16: bf16 pages, the products in bf16. Else E4M3 pages, whose bytes are the operand as they
 // are; what meets them is split into 8-bit parts that add up to it:
 //   q 2^s = hi + lo, both E4M3, with the largest |q| 2^s of a row in [2^7, 2^8): bf16's 8 bits
-//   down to 2^-10 of the largest, to 2^-18 of it below; both products into the same S;
+//   down to 2^-10 of the largest, to 2^-17 of it below; both products into the same S;
 //   P in f16 = three parts in E5M2, each the nearest three bits of what is left.
 template <bool kBf16>
 struct Shape {
@@ -349,6 +350,9 @@ struct Shape {
     // 1.75 x 2^15 and holds small values as multiples of 2^-16.
     static constexpr float kLazyMax = kBf16 ? 8.f : 6.f;
     static constexpr float kLift = kBf16 ? 0.f : 9.f;
+    // A row's maximum as its threads exchange it. In bf16, rounded up, where room is short: what it bounds
+    // need not be close, as bf16 weights are as exact at any scale.
+    using Bound = std::conditional_t<kBf16, __nv_bfloat16, float>;
     // Tiles that add up in TMEM under one maximum (see csa2_paged_attn: of a long tail less than 2^-9
     // of the weight is lost); what came before is added in fp32.
     static constexpr int kRun = kBf16 ? 192 : 128;
@@ -377,7 +381,7 @@ struct Shared {
     uint8_t keys[S::kKeys][S::kPlace], values[S::kValues][S::kPlace];
     uint8_t q[8 * S::kChunk];
     uint8_t p[2][S::kWeights];  // by tile parity
-    __nv_bfloat16 red_max[2][4][kMine];  // rounded up: what it bounds need not be close
+    typename S::Bound red_max[2][4][kMine];
     float row_scale[kBf16 ? 0 : 2][kMine];  // E4M3: logit factor, by run parity
     Info info[kInfos];
     uint64_t key_full[S::kKeys], value_full[S::kValues];  // the even CTA's: the place is full in both
@@ -929,7 +933,8 @@ __device__ void softmax_role(Shared<kBf16>& sh, const Args& a, uint32_t tmem, in
         float top = fmaxf(x[0].x, x[0].y);
 #pragma unroll
         for (int i = 1; i < 16; ++i) top = fmaxf(top, fmaxf(x[i].x, x[i].y));
-        sh.red_max[gt & 1][quarter][r] = __float2bfloat16_ru(top);
+        if constexpr (kBf16) sh.red_max[gt & 1][quarter][r] = __float2bfloat16_ru(top);
+        else sh.red_max[gt & 1][quarter][r] = top;
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.max_bar[grp]);
         // P under the maximum so far, while the others' maxima are on their way; again in the few tiles
@@ -958,9 +963,8 @@ __device__ void softmax_role(Shared<kBf16>& sh, const Args& a, uint32_t tmem, in
             if (known) break;
             if (!wait(&sh.max_bar[grp], (uint32_t)(gt & 1), abort)) return;
             known = true;
-            const auto* all4 = sh.red_max[gt & 1];
-            top = fmaxf(fmaxf(__bfloat162float(all4[0][r]), __bfloat162float(all4[1][r])),
-                        fmaxf(__bfloat162float(all4[2][r]), __bfloat162float(all4[3][r])));
+            const auto* four = sh.red_max[gt & 1];
+            top = fmaxf(fmaxf((float)four[0][r], (float)four[1][r]), fmaxf((float)four[2][r], (float)four[3][r]));
             const bool move = fresh || top > m + S::kLazyMax;
             if (!__any_sync(0xffffffffu, move)) break;
             if (move) {

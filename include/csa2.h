@@ -728,12 +728,13 @@ size_t csa2_paged_attn_shared_workspace_size(const csa2_params* p, const csa2_pa
  *   first  [B] int32, device: the slot where the group of slot i begins;
  *   shared [B] int32, device: positions the group of slot i has in common (read at its first slot).
  * Positions t < shared are read through the table row of the group's first sequence, whatever the
- * others' rows hold there, positions from shared on through each sequence's own row. A sequence sees
+ * others' rows hold there, positions from shared on through each sequence's own row. (Behind a
+ * first sequence that is padding or out of range a group shares nothing.) A sequence sees
  * its positions t < n_tokens[b], also where that is less than shared. Of an order that does not name
  * every sequence once, the missing ones' outputs are undefined.
  *   Arguments, masking and limits are otherwise those of csa2_paged_attn, as are the roundings of
  *   weights and output; with E4M3 pages a query is the sum of two E4M3 values under a power of two
- *   per head: exact down to 2^-10 of the head's largest value, to 2^-18 of it below. An infinity in a
+ *   per head: exact down to 2^-10 of the head's largest value, to 2^-17 of it below. An infinity in a
  *   row of a page counts only through the logits: it makes the outputs that see it NaN, unless its
  *   logit is -infinity, which takes the row out. What sequences do not see does not reach them, NaN in
  *   another sequence's positions among it.
