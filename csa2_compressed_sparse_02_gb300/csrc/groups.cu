@@ -3,8 +3,10 @@
 //
 // Pages that are shared are shared from the first on (a fork shares its parent's full pages), so
 // sequences with the same page at position least - 1 are candidates; the lowest-numbered one of them
-// leads, and the others' rows of the table are compared with its entry by entry. The first kernel does that with a warp a
-// sequence; the second one, a CTA, puts the sequences in order. Both are chains of round trips.
+// leads, and the others' rows of the table are compared with its entry by entry. The first kernel does
+// that with a warp a sequence; in the second one a warp counts what stands before its sequence, which
+// needs no order of arrival. Both are chains of round trips; 4 million comparisons for 2,000 sequences
+// are nothing to 152 SMs (one CTA that counted by leaders took 40 us for them).
 #include <climits>
 
 #include "pages.cuh"
@@ -13,19 +15,17 @@
 namespace csa2 {
 namespace {
 
-constexpr int kWarps = 8;      // sequences a CTA of the first kernel takes
-constexpr int kKeys = 2048;    // of the batch's keys at a time
-constexpr int kOrder = 1024;   // threads of the second one
+constexpr int kWarps = 32;     // sequences a CTA takes
+constexpr int kKeys = 4096;    // of the batch that it looks at together
 
-// Scratch: of each sequence of the call its leader and what they have in common, and by leader the
-// members, their first slot and the least of what they have in common; and the members so far.
+// Scratch: of each sequence of the call its leader (INT_MAX: padding) and what they have in common.
 struct Scratch {
-    int32_t *lead, *common, *count, *start, *least, *seen;
+    int32_t *lead, *common;
 };
-int64_t scratch_bytes(int64_t B) { return 6 * 4 * B; }
+int64_t scratch_bytes(int64_t B) { return 2 * 4 * B; }
 Scratch scratch_of(void* ws, int B) {
     int32_t* p = static_cast<int32_t*>(ws);
-    return {p, p + B, p + 2 * (int64_t)B, p + 3 * (int64_t)B, p + 4 * (int64_t)B, p + 5 * (int64_t)B};
+    return {p, p + B};
 }
 
 struct Args {
@@ -55,7 +55,7 @@ __device__ __forceinline__ int key_of(const Args& a, int b) {
     return real(a, page) ? page : -1 - b;
 }
 
-__global__ void __launch_bounds__(32 * kWarps) k_groups_compare(const __grid_constant__ Args a) {
+__global__ void __launch_bounds__(32 * kWarps, 1) k_groups_compare(const __grid_constant__ Args a) {
     __shared__ int32_t keys[kKeys];
     __shared__ int left;
     sm100::grid_dep_wait();
@@ -90,7 +90,7 @@ __global__ void __launch_bounds__(32 * kWarps) k_groups_compare(const __grid_con
         const int32_t *x = a.g.table + (int64_t)r0 * a.g.max_pages, *y = a.g.table + (int64_t)r1 * a.g.max_pages;
         const int pages = (int)(((int64_t)n + a.g.page_size - 1) / a.g.page_size);
         int same = pages;
-        constexpr int kAtOnce = 4;  // entries a lane whose loads are in flight together
+        constexpr int kAtOnce = 8;  // entries a lane whose loads are in flight together
         for (int k0 = 0; k0 < pages; k0 += 32 * kAtOnce) {
             int u[kAtOnce], v[kAtOnce];
 #pragma unroll
@@ -114,91 +114,41 @@ __global__ void __launch_bounds__(32 * kWarps) k_groups_compare(const __grid_con
         if (common < a.least) lead = b;
     }
     if (lane == 0) {
-        a.ws.lead[b] = lead;
+        a.ws.lead[b] = row_of(a, b) < 0 ? INT_MAX : lead;
         a.ws.common[b] = common;
     }
 }
 
-// Exclusive sum over the CTA; *total gets the sum. Two CTA barriers.
-__device__ __forceinline__ int scan(int v, int* total) {
-    __shared__ int warp_sum[kOrder / 32];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int inc = v;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int up = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += up;
-    }
-    if (lane == 31) warp_sum[warp] = inc;
-    __syncthreads();
-    const int w = warp_sum[lane];
-    int before = lane < warp ? w : 0, all = w;
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) {
-        before += __shfl_xor_sync(0xffffffffu, before, o);
-        all += __shfl_xor_sync(0xffffffffu, all, o);
-    }
-    __syncthreads();
-    *total = all;
-    return before + inc - v;
-}
-
-// Groups in the order of their leaders, members ascending, padding behind them. Batches of up to
-// kOrder sequences are counted in shared memory, others in the scratch, kOrder at a time.
-__global__ void __launch_bounds__(kOrder) k_groups_order(const __grid_constant__ Args a) {
-    __shared__ int32_t leads[kOrder], count_s[kOrder], start_s[kOrder], least_s[kOrder], seen_s[kOrder];
+// Groups in the order of their leaders, members ascending, padding behind them: a sequence's slot is
+// the number of those with a lower leader, and of those with the same one before it.
+__global__ void __launch_bounds__(32 * kWarps, 1) k_groups_order(const __grid_constant__ Args a) {
+    __shared__ int32_t leads[kKeys];
     sm100::grid_dep_wait();
-    const int tid = threadIdx.x;
-    const bool small = a.B <= kOrder;
-    int32_t *count = small ? count_s : a.ws.count, *start = small ? start_s : a.ws.start;
-    int32_t *least = small ? least_s : a.ws.least, *seen = small ? seen_s : a.ws.seen;
-    for (int b = tid; b < a.B; b += kOrder) {
-        count[b] = seen[b] = 0;
-        least[b] = INT_MAX;
-    }
-    __syncthreads();
-    for (int b = tid; b < a.B; b += kOrder) {
-        if (row_of(a, b) < 0) continue;
-        const int l = a.ws.lead[b];
-        atomicAdd(&count[l], 1);
-        if (l != b) atomicMin(&least[l], a.ws.common[b]);
-    }
-    __syncthreads();
-    int slots = 0, total;
-    for (int b0 = 0; b0 < a.B; b0 += kOrder) {
-        const int b = b0 + tid;
-        const int at = slots + scan(b < a.B ? count[b] : 0, &total);
-        if (b < a.B) start[b] = at;
-        slots += total;
-    }
-    int padding = slots;
-    for (int b0 = 0; b0 < a.B; b0 += kOrder) {
-        const int b = b0 + tid;
-        const bool pad = b < a.B && row_of(a, b) < 0;
-        const int l = b < a.B && !pad ? a.ws.lead[b] : -1;
-        leads[tid] = l;
-        const int at = padding + scan(pad ? 1 : 0, &total);  // (a barrier between leads' writes and reads)
-        padding += total;
-        if (pad) {
-            a.order[at] = b;
-            a.first[at] = at;
-            a.shared[at] = 0;
-        }
-        int rank = 0;
-        if (l >= 0) {
-            // members before this one: those of earlier rounds, then this round's
-            rank = seen[l];
-            const int from = l >= b0 ? l - b0 : 0;
-            if (l != b)
-                for (int j = from; j < tid; ++j) rank += leads[j] == l;
-            const int slot = start[l] + rank;
-            a.order[slot] = b;
-            a.first[slot] = start[l];
-            a.shared[slot] = least[l] == INT_MAX ? 0 : least[l];
-        }
+    const int lane = threadIdx.x & 31, b = blockIdx.x * kWarps + (threadIdx.x >> 5);
+    const int mine = b < a.B ? a.ws.lead[b] : 0;
+    int lower = 0, before = 0, least = INT_MAX;
+    for (int j0 = 0; j0 < a.B; j0 += kKeys) {
+        const int n = min(kKeys, a.B - j0);
         __syncthreads();
-        if (l >= 0) atomicAdd(&seen[l], 1);
+        for (int j = threadIdx.x; j < n; j += 32 * kWarps) leads[j] = a.ws.lead[j0 + j];
         __syncthreads();
+        for (int j = lane; j < n; j += 32) {
+            const int l = leads[j];
+            lower += l < mine;
+            if (l != mine) continue;
+            before += j0 + j < b;
+            if (j0 + j != mine) least = min(least, a.ws.common[j0 + j]);
+        }
+    }
+    if (b >= a.B) return;
+    lower = __reduce_add_sync(0xffffffffu, lower);
+    before = __reduce_add_sync(0xffffffffu, before);
+    least = __reduce_min_sync(0xffffffffu, least);
+    if (lane == 0) {
+        const int slot = lower + before;
+        a.order[slot] = b;
+        a.first[slot] = mine == INT_MAX ? slot : lower;
+        a.shared[slot] = mine == INT_MAX || least == INT_MAX ? 0 : least;
     }
 }
 
@@ -259,5 +209,5 @@ extern "C" int csa2_prefix_groups(const csa2_params* p, const csa2_pages* c, int
     a.ws = scratch_of(workspace, B);
     a.dev_status = dev_status;
     if (const int rc = launch(k_groups_compare, dim3((B + kWarps - 1) / kWarps), 32 * kWarps, stream, a)) return rc;
-    return launch(k_groups_order, dim3(1), kOrder, stream, a);
+    return launch(k_groups_order, dim3((B + kWarps - 1) / kWarps), 32 * kWarps, stream, a);
 }

@@ -301,10 +301,11 @@ k_slots_plan(Pages g, int B, const int32_t* seq, const int32_t* n_tokens, const 
     }
     int32_t* list = entries <= kFresh ? list_s : ws.list;
     const int free = lowest_free(g, entries, list, first_ref);  // ends with a CTA barrier
+    // Four neighbouring entries a thread: a step of prompts has thousands, and a round takes a microsecond.
     int taken = 0;
-    for (int64_t e0 = 0; e0 < entries; e0 += kPlan) {
-        const int64_t e = e0 + tid;
-        int32_t* entry = nullptr;
+    for (int64_t e0 = 0; e0 < entries; e0 += 4 * kPlan) {
+        const int64_t e = e0 + 4 * (int64_t)tid;
+        int32_t* entry[4] = {};
         if (e < entries) {
             int lo = 0, hi = B;  // off[lo] <= e < off[hi]
             while (hi - lo > 1) {
@@ -312,19 +313,31 @@ k_slots_plan(Pages g, int B, const int32_t* seq, const int32_t* n_tokens, const 
                 if (off[mid] <= e) lo = mid;
                 else hi = mid;
             }
-            entry = g.table + (int64_t)seq[lo] * g.max_pages + held_before(out, out.start, lo) / g.page_size + (e - off[lo]);
-            if (*entry >= 0) entry = nullptr;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                if (e + k >= entries) break;
+                while (off[lo + 1] <= e + k) ++lo;
+                entry[k] = g.table + (int64_t)seq[lo] * g.max_pages + held_before(out, out.start, lo) / g.page_size + (e + k - off[lo]);
+            }
         }
+        int have[4], n = 0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) have[k] = entry[k] ? *entry[k] : 0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) n += have[k] < 0;
         int total;
-        const int k = taken + block_scan(entry ? 1 : 0, &total);
-        if (entry) {
-            if (k < free) {
-                const int32_t page = list[k];
-                *entry = page;
+        int at = taken + block_scan(n, &total);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            if (have[k] >= 0) continue;
+            if (at < free) {
+                const int32_t page = list[at];
+                *entry[k] = page;
                 g.ref[page] = 1;
             } else {
                 raise_status(dev_status, CSA2_DEV_NO_PAGE);
             }
+            ++at;
         }
         taken += total;
     }
