@@ -15,7 +15,7 @@
 namespace csa2 {
 namespace {
 
-constexpr int kWarps = 32;     // sequences a CTA takes
+constexpr int kWarps = 16;     // sequences a CTA takes
 constexpr int kKeys = 4096;    // of the batch that it looks at together
 
 // Scratch: of each sequence of the call its leader (INT_MAX: padding) and what they have in common.
@@ -72,7 +72,15 @@ __global__ void __launch_bounds__(32 * kWarps, 1) k_groups_compare(const __grid_
         if (threadIdx.x == 0) left = 0;
         const int n = min(kKeys, a.B - j0);
         __syncthreads();
-        for (int j = threadIdx.x; j < n; j += 32 * kWarps) keys[j] = key_of(a, j0 + j);
+        constexpr int kLoads = 4;  // keys a thread, whose three round trips overlap
+        for (int j = threadIdx.x; j < n; j += 32 * kWarps * kLoads) {
+            int key[kLoads];
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i) key[i] = j0 + j + 32 * kWarps * i < a.B ? key_of(a, j0 + j + 32 * kWarps * i) : -1;
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i)
+                if (j + 32 * kWarps * i < n) keys[j + 32 * kWarps * i] = key[i];
+        }
         if (lead < 0 && lane == 0) left = 1;
         __syncthreads();
         if (!left) break;

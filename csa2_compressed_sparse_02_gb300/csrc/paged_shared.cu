@@ -147,8 +147,58 @@ struct PlanScratch {  // (where P comes later)
     long long at, end, first, last;  // the range; where the unit that it begins in begins, and the last one ends
 };
 
+// Up to 32 slots: by one warp, a slot a lane.
+__device__ void plan_few(const Args& a, PlanShared& sh, int pair) {
+    const int lane = threadIdx.x & 31;
+    Slot s = {-1, 0, -1, lane, 0, -1};
+    if (lane < a.B) s = slot_of(a, lane, blockIdx.x == 0);
+    const bool head = lane < a.B && unit_of(a, lane, s.f) == lane;
+    const uint32_t n = lane < a.B ? (uint32_t)prefix_tiles(a, s, lane) + own_tiles(s) : 0;  // (below 2^26)
+    const uint32_t here = warp_scan(n, lane), total = __shfl_sync(0xffffffffu, here + n, 31);
+    const uint32_t heads = __ballot_sync(0xffffffffu, head), behind = lane < 31 ? heads & (~0u << (lane + 1)) : 0u;
+    const uint32_t next = __shfl_sync(0xffffffffu, here, behind ? __ffs(behind) - 1 : 0);
+    const uint32_t t = head ? (behind ? next : total) - here : 0;  // of the unit
+    const Cut ranges(total, a.pairs);
+    const int c = min(pair, ranges.n);
+    int64_t at = ranges.at(c), end = ranges.at(min(c + 1, ranges.n));
+    if (__popc(heads) <= a.pairs && total > 0) {
+        const uint32_t lo = (total + a.pairs - 1) / a.pairs;
+        for (uint32_t L = lo; L <= lo + kSecondPiece; ++L) {
+            const uint32_t k = (t + L - 1) / L;
+            if (__reduce_add_sync(0xffffffffu, k) > (uint32_t)a.pairs) continue;
+            const int i = pair - (int)warp_scan(k, lane);
+            const uint32_t mine = __ballot_sync(0xffffffffu, i >= 0 && i < (int)k);
+            at = end = total;
+            if (mine) {
+                const int l = __ffs(mine) - 1;
+                at = __shfl_sync(0xffffffffu, here + (uint32_t)((uint64_t)t * max(i, 0) / max(k, 1u)), l);
+                end = __shfl_sync(0xffffffffu, here + (uint32_t)((uint64_t)t * (max(i, 0) + 1) / max(k, 1u)), l);
+            }
+            break;
+        }
+    }
+    // (units of no tiles begin where the next one does)
+    const uint32_t first = __reduce_max_sync(0xffffffffu, head && here <= at ? here : 0u);
+    const uint32_t last = __reduce_min_sync(0xffffffffu, head && here >= end ? here : total);
+    const uint32_t begins = __ballot_sync(0xffffffffu, at >= here && at < (int64_t)here + n);
+    const int l = begins ? __ffs(begins) - 1 : 0;
+    const int base = __shfl_sync(0xffffffffu, unit_of(a, lane, s.f), l);
+    const uint32_t before = __shfl_sync(0xffffffffu, here, l);
+    if (lane == 0) {
+        sh.base = begins ? base : 0;
+        sh.range = {end - at, l, begins ? (int)(at - before) : 0, first < at, last > end};
+    }
+    if (lane >= (begins ? base : 0) && lane < a.B) sh.slots[lane - (begins ? base : 0)] = s;
+}
+
 // Called by the whole CTA.
 __device__ void plan(const Args& a, PlanShared& sh, PlanScratch& x, int pair) {
+    static_assert(kKept >= 32, "plan_few keeps its slots");
+    if (a.B <= 32) {  // 3.9 against 2.3 us
+        if (threadIdx.x < 32) plan_few(a, sh, pair);
+        __syncthreads();
+        return;
+    }
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
     // Exclusive sum over the CTA of n < 2^26, and the sum of all.
     auto scan = [&](uint32_t n, int64_t* all) {
@@ -1068,38 +1118,44 @@ __device__ void softmax_role(Shared<kBf16>& sh, const Args& a, uint32_t tmem, in
         float4* const kept = reinterpret_cast<float4*>(slot) + (d0 / 4) * kRows + R;
         __nv_bfloat16* const out = a.out + ((int64_t)max(row.b, 0) * a.heads + row.h) * kD + d0;
 #pragma unroll 1
-        for (int n = 0; n < 128; n += 16) {
-            uint32_t ov[16];
-            tmem_ld_32x32b_x16(tl + kColO + 128 * ch + n, ov);
-            float4 o[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                o[i] = make_float4(__uint_as_float(ov[4 * i]), __uint_as_float(ov[4 * i + 1]),
-                                   __uint_as_float(ov[4 * i + 2]), __uint_as_float(ov[4 * i + 3]));
+        for (int n = 0; n < 128; n += 64) {
+            uint32_t ov[2][32];
+            tmem_ld_32x32b_x32_nowait(tl + kColO + 128 * ch + n, ov[0]);
+            tmem_ld_32x32b_x32_nowait(tl + kColO + 128 * ch + n + 32, ov[1]);
+            tmem_wait_ld_regs32(ov[0]);
+            tmem_wait_ld_regs32(ov[1]);
             if (row.b < 0) continue;
-            if (!(flags & Info::kBegins)) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float4 b = kept[(n / 4 + i) * kRows];
-                    o[i] = make_float4(fmaf(b.x, was, o[i].x * now), fmaf(b.y, was, o[i].y * now),
-                                       fmaf(b.z, was, o[i].z * now), fmaf(b.w, was, o[i].w * now));
+            for (int i = 0; i < 16; i += 2) {
+                float4 o[2];
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const uint32_t* v = &ov[(i + k) >> 3][4 * ((i + k) & 7)];
+                    o[k] = make_float4(__uint_as_float(v[0]), __uint_as_float(v[1]), __uint_as_float(v[2]), __uint_as_float(v[3]));
                 }
-            }
-            if (done) {
-                uint32_t v[8];
+                if (!(flags & Info::kBegins)) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
+                    for (int k = 0; k < 2; ++k) {
+                        const float4 b = kept[(n / 4 + i + k) * kRows];
+                        o[k] = make_float4(fmaf(b.x, was, o[k].x * now), fmaf(b.y, was, o[k].y * now),
+                                           fmaf(b.z, was, o[k].z * now), fmaf(b.w, was, o[k].w * now));
+                    }
+                }
+                if (done) {
                     const bool none = scale == 0.f;
-                    const __nv_bfloat162 y = __floats2bfloat162_rn(none ? 0.f : o[i].x * scale, none ? 0.f : o[i].y * scale);
-                    const __nv_bfloat162 z = __floats2bfloat162_rn(none ? 0.f : o[i].z * scale, none ? 0.f : o[i].w * scale);
-                    v[2 * i] = *reinterpret_cast<const uint32_t*>(&y);
-                    v[2 * i + 1] = *reinterpret_cast<const uint32_t*>(&z);
-                }
-                *reinterpret_cast<uint4*>(out + n) = make_uint4(v[0], v[1], v[2], v[3]);
-                *reinterpret_cast<uint4*>(out + n + 8) = make_uint4(v[4], v[5], v[6], v[7]);
-            } else {
+                    uint32_t v[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) kept[(n / 4 + i) * kRows] = o[i];
+                    for (int k = 0; k < 2; ++k) {
+                        const __nv_bfloat162 y = __floats2bfloat162_rn(none ? 0.f : o[k].x * scale, none ? 0.f : o[k].y * scale);
+                        const __nv_bfloat162 z = __floats2bfloat162_rn(none ? 0.f : o[k].z * scale, none ? 0.f : o[k].w * scale);
+                        v[2 * k] = *reinterpret_cast<const uint32_t*>(&y);
+                        v[2 * k + 1] = *reinterpret_cast<const uint32_t*>(&z);
+                    }
+                    *reinterpret_cast<uint4*>(out + n + 4 * i) = make_uint4(v[0], v[1], v[2], v[3]);
+                } else {
+                    kept[(n / 4 + i) * kRows] = o[0];
+                    kept[(n / 4 + i + 1) * kRows] = o[1];
+                }
             }
         }
         if (!done && quarter == 0) {
@@ -1157,11 +1213,12 @@ k_paged_shared(const __grid_constant__ Args a, const __grid_constant__ CUtensorM
     // a programmatic launch: only the setup above may overlap the kernel ahead
     grid_dep_launch_dependents();
     tc_fence_before();
-    __syncthreads();
-    cluster_sync_all();  // the other CTA's barriers are there
-    tc_fence_after();
+    cluster_arrive();
+    if (tid == 0) prefetch_tmap(&tmap);
     grid_dep_wait();
     plan(a, sh.plan, *reinterpret_cast<PlanScratch*>(sh.p), pair);  // ends with a CTA barrier
+    cluster_wait();  // the other CTA's barriers are there
+    tc_fence_after();
     const uint32_t tmem = __shfl_sync(0xffffffffu, sh.tmem_base, 0);
     if (warp < S::kSoftWarps) {
         softmax_role<kBf16>(sh, a, tmem, warp, lane, rank, pair, abort);
@@ -1204,40 +1261,47 @@ static_assert(smem_bytes<true>() <= 227 * 1024 && smem_bytes<false>() <= 227 * 1
 // pairs' partial results in order, by batches. A thread has a row and kEach groups of four channels;
 // the values of a batch of pieces are requested together with their maxima. What sees nothing gets its
 // zeros here.
-constexpr int kJoinThreads = 256;
-constexpr int kJoinLoads = 8;  // in flight a thread, 16 bytes each
+// Many units: a CTA takes 32 channels of one, a thread 8 of them. Few units, which are cut into many pieces
+// each: four channels, and every group of threads takes every fourth piece.
+constexpr int kJoinGroups = 4, kJoinThreads = kRows * kJoinGroups;
 
-template <int kEach>
-__device__ __forceinline__ void join_rows(const Args& a, int c0, int slot0, int n, int item) {
-    constexpr int kBatch = kJoinLoads / kEach;
-    const int R = threadIdx.x & (kRows - 1), cg = kEach * (2 * item + (threadIdx.x >> 7));
-    auto piece = [&](int i) { return part_of(a, c0 + i, i == 0 ? slot0 : 0); };
-    const int place = __float_as_int(__ldcg(piece(0) + kRows * (kD + 2) + R));
-    const int h = max(place, 0) % a.heads;
-    float4 acc[kEach];
+template <bool kFew>
+__device__ __forceinline__ void join_item(const Args& a, int item, uint32_t s0, int n, float4 (*sums)[kRows],
+                                          float2 (*tops)[kRows]) {
+    constexpr int E = kFew ? 1 : 2, kBatch = kFew ? 4 : 2, kStep = kFew ? kJoinGroups : 1;
+    const int R = threadIdx.x & (kRows - 1), group = threadIdx.x / kRows;
+    const int cg = kFew ? item : 2 * (kJoinGroups * item + group);  // four channels each
+    // slots of the pieces: the first, and two further on each time from the pair behind it
+    const float* const first = part_of(a, 0, 0) + (int64_t)s0 * kPartFloats;
+    const float* const rest = part_of(a, 0, 0) + (int64_t)(s0 & ~1u) * kPartFloats;
+    const int place = __float_as_int(__ldcg(first + kRows * (kD + 2) + R));
+    float4 acc[E];
 #pragma unroll
-    for (int e = 0; e < kEach; ++e) acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int e = 0; e < E; ++e) acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
     float den = 0.f, M = -INFINITY;
-    for (int i0 = 0; i0 < n; i0 += kBatch) {
-        float4 v[kBatch][kEach];
+#pragma unroll 1
+    for (int i0 = kFew ? group : 0; i0 < n; i0 += kStep * kBatch) {
+        float4 v[kBatch][E];
         float m[kBatch], l[kBatch], top = M;
 #pragma unroll
         for (int i = 0; i < kBatch; ++i) {
-            m[i] = -INFINITY;
-            if (i0 + i >= n) continue;
-            const float* p = piece(i0 + i);
+            const int p = min(i0 + kStep * i, n - 1);  // (again the last one, for nothing)
+            const float* const at = p ? rest + (int64_t)p * (2 * kPartFloats) : first;
 #pragma unroll
-            for (int e = 0; e < kEach; ++e) v[i][e] = __ldcg(reinterpret_cast<const float4*>(p) + (cg + e) * kRows + R);
-            m[i] = __ldcg(p + kRows * kD + R);
-            l[i] = __ldcg(p + kRows * (kD + 1) + R);
+            for (int e = 0; e < E; ++e) v[i][e] = __ldcg(reinterpret_cast<const float4*>(at) + (cg + e) * kRows + R);
+            m[i] = __ldcg(at + kRows * kD + R);
+            l[i] = __ldcg(at + kRows * (kD + 1) + R);
         }
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i) top = fmaxf(top, m[i]);
+        for (int i = 0; i < kBatch; ++i) {
+            if (i0 + kStep * i >= n) m[i] = -INFINITY;
+            top = fmaxf(top, m[i]);
+        }
         if (top != M) {
             const float w = M == -INFINITY ? 0.f : ex2(M - top);
             den *= w;
 #pragma unroll
-            for (int e = 0; e < kEach; ++e) acc[e] = make_float4(acc[e].x * w, acc[e].y * w, acc[e].z * w, acc[e].w * w);
+            for (int e = 0; e < E; ++e) acc[e] = make_float4(acc[e].x * w, acc[e].y * w, acc[e].z * w, acc[e].w * w);
             M = top;
         }
 #pragma unroll
@@ -1246,80 +1310,90 @@ __device__ __forceinline__ void join_rows(const Args& a, int c0, int slot0, int 
             const float w = ex2(m[i] - M);
             den = fmaf(l[i], w, den);
 #pragma unroll
-            for (int e = 0; e < kEach; ++e) {
-                acc[e].x = fmaf(v[i][e].x, w, acc[e].x);
-                acc[e].y = fmaf(v[i][e].y, w, acc[e].y);
-                acc[e].z = fmaf(v[i][e].z, w, acc[e].z);
-                acc[e].w = fmaf(v[i][e].w, w, acc[e].w);
-            }
+            for (int e = 0; e < E; ++e)
+                acc[e] = make_float4(fmaf(v[i][e].x, w, acc[e].x), fmaf(v[i][e].y, w, acc[e].y),
+                                     fmaf(v[i][e].z, w, acc[e].z), fmaf(v[i][e].w, w, acc[e].w));
+        }
+    }
+    if constexpr (kFew) {
+        __syncthreads();  // (the item before has read them)
+        if (group) {
+            sums[group - 1][R] = acc[0];
+            tops[group - 1][R] = make_float2(M, den);
+        }
+        __syncthreads();
+        if (group) return;
+#pragma unroll 1
+        for (int g = 0; g < kJoinGroups - 1; ++g) {
+            const float2 o = tops[g][R];
+            const float4 b = sums[g][R];
+            const float top = fmaxf(M, o.x), u = M == -INFINITY ? 0.f : ex2(M - top), w = o.x == -INFINITY ? 0.f : ex2(o.x - top);
+            den = fmaf(o.y, w, den * u);
+            acc[0] = make_float4(fmaf(b.x, w, acc[0].x * u), fmaf(b.y, w, acc[0].y * u), fmaf(b.z, w, acc[0].z * u),
+                                 fmaf(b.w, w, acc[0].w * u));
+            M = top;
         }
     }
     if (place < 0) return;
-    const float s2 = a.sink ? a.sink[h] * kLog2e : -INFINITY, top = fmaxf(M, s2);
+    const float s2 = a.sink ? a.sink[place % a.heads] * kLog2e : -INFINITY, top = fmaxf(M, s2);
     const float f = M == -INFINITY ? 0.f : ex2(M - top);
     den = den * f + (s2 == -INFINITY ? 0.f : ex2(s2 - top));
     const float inv = den == 0.f ? 0.f : f / den;
-    uint32_t o[2 * kEach];
+    uint32_t o[2 * E];
 #pragma unroll
-    for (int e = 0; e < kEach; ++e) {
+    for (int e = 0; e < E; ++e) {
         const __nv_bfloat162 x = __floats2bfloat162_rn(inv == 0.f ? 0.f : acc[e].x * inv, inv == 0.f ? 0.f : acc[e].y * inv);
         const __nv_bfloat162 y = __floats2bfloat162_rn(inv == 0.f ? 0.f : acc[e].z * inv, inv == 0.f ? 0.f : acc[e].w * inv);
         o[2 * e] = *reinterpret_cast<const uint32_t*>(&x);
         o[2 * e + 1] = *reinterpret_cast<const uint32_t*>(&y);
     }
     __nv_bfloat16* const out = a.out + (int64_t)place * kD + 4 * cg;
-    if constexpr (kEach == 1) {
-        *reinterpret_cast<uint2*>(out) = make_uint2(o[0], o[1]);
-    } else {
-#pragma unroll
-        for (int e = 0; e < kEach; e += 2)
-            *reinterpret_cast<uint4*>(out + 4 * e) = make_uint4(o[2 * e], o[2 * e + 1], o[2 * e + 2], o[2 * e + 3]);
-    }
+    if constexpr (kFew) *reinterpret_cast<uint2*>(out) = make_uint2(o[0], o[1]);
+    else *reinterpret_cast<uint4*>(out) = make_uint4(o[0], o[1], o[2], o[3]);
 }
 
-__global__ void __launch_bounds__(kJoinThreads) k_shared_join(const __grid_constant__ Args a) {
-    __shared__ uint32_t cut_s[kMaxPairs / 32], through_s[kMaxPairs / 32], single_s[kMaxPairs / 32];
+__global__ void __launch_bounds__(kJoinThreads, 2) k_shared_join(const __grid_constant__ Args a) {
+    __shared__ int first_s[kMaxPairs], pieces_s[kMaxPairs], units_s;  // of the units that are cut
     grid_dep_wait();
-    const int tid = threadIdx.x, lane = tid & 31;
-    if (tid < kMaxPairs) {
-        const int e = tid < a.pairs ? a.ends[tid] : 0;
-        const uint32_t cut = __ballot_sync(0xffffffffu, e & kCut), through = __ballot_sync(0xffffffffu, e & kThrough);
-        const uint32_t single = __ballot_sync(0xffffffffu, e & kSingle);
-        if (lane == 0) {
-            cut_s[tid >> 5] = cut;
-            through_s[tid >> 5] = through;
-            single_s[tid >> 5] = single;
+    const int tid = threadIdx.x;
+    if (tid < 32) {  // 32 pairs at a time: the units that begin in a pair's range and end behind it
+        int units = 0;
+        uint32_t through[kMaxPairs / 32];
+        for (int w = kMaxPairs / 32 - 1; w >= 0; --w) {
+            const int c = 32 * w + tid;
+            through[w] = __ballot_sync(0xffffffffu, c < a.pairs && (a.ends[c] & (kCut | kThrough)) == (kCut | kThrough));
         }
+#pragma unroll
+        for (int w = 0; w < kMaxPairs / 32; ++w) {
+            const int c = 32 * w + tid, e = c < a.pairs ? a.ends[c] : 0;
+            const bool begins = (e & kCut) && !(e & kThrough);
+            const uint32_t all = __ballot_sync(0xffffffffu, begins);
+            if (begins) {
+                int n = 2;  // the unit's last pair is the first one behind that does not go through
+                for (int k = c + 1; k + 1 < a.pairs && ((through[k >> 5] >> (k & 31)) & 1u); ++k) ++n;
+                const int at = units + __popc(all & ((1u << tid) - 1u));
+                first_s[at] = 2 * c + (e & kSingle ? 0 : 1);  // its slot, counted over all pairs
+                pieces_s[at] = n;
+            }
+            units += __popc(all);
+        }
+        if (tid == 0) units_s = units;
     }
     __syncthreads();
-    int units = 0;  // that begin in a pair's range and end behind it
-#pragma unroll
-    for (int w = 0; w < kMaxPairs / 32; ++w) units += __popc(cut_s[w] & ~through_s[w]);
-    // few units are cut into many pieces each, by few threads: those take less each
-    const bool few = units * 16 < (int)gridDim.x;
-    const int each = few ? kD / 8 : kD / 32;
-    for (int item = blockIdx.x; item < units * each; item += gridDim.x) {
-        int nth = item / each, w = 0;
-        uint32_t bits = cut_s[0] & ~through_s[0];
-        while (nth >= __popc(bits)) {
-            nth -= __popc(bits);
-            ++w;
-            bits = cut_s[w] & ~through_s[w];
-        }
-        for (; nth > 0; --nth) bits &= bits - 1;
-        const int c0 = 32 * w + __ffs(bits) - 1;
-        auto has = [](const uint32_t* s, int c) { return (s[c >> 5] >> (c & 31)) & 1u; };
-        int n = 2;  // pieces: c0's last one, then the others' first ones
-        while (c0 + n < a.pairs && has(cut_s, c0 + n - 1) && has(through_s, c0 + n - 1)) ++n;
-        const int slot0 = has(single_s, c0) ? 0 : 1;
-        if (few) join_rows<1>(a, c0, slot0, n, item % each);
-        else join_rows<4>(a, c0, slot0, n, item % each);
+    __shared__ float4 sums[kJoinGroups - 1][kRows];
+    __shared__ float2 tops[kJoinGroups - 1][kRows];
+    const bool few = units_s * (kD / 4) <= 2 * (int)gridDim.x;
+    const int each = few ? kD / 4 : kD / 32;
+    for (int item = blockIdx.x; item < units_s * each; item += gridDim.x) {
+        const int unit = item / each;
+        if (few) join_item<true>(a, item % each, first_s[unit], pieces_s[unit], sums, tops);
+        else join_item<false>(a, item % each, first_s[unit], pieces_s[unit], sums, tops);
     }
     for (int b = blockIdx.x * (kJoinThreads / 32) + (tid >> 5); b < a.B; b += gridDim.x * (kJoinThreads / 32)) {
         const int row = a.seq ? a.seq[b] : b;
         if (row < 0 || (row < a.g.max_seqs && length_of(a, a.n_tokens[b], false) > 0)) continue;
         uint4* out = reinterpret_cast<uint4*>(a.out + (int64_t)b * a.heads * kD);
-        for (int u = lane; u < a.heads * (kD / 8); u += 32) out[u] = make_uint4(0u, 0u, 0u, 0u);
+        for (int u = tid & 31; u < a.heads * (kD / 8); u += 32) out[u] = make_uint4(0u, 0u, 0u, 0u);
     }
 }
 
@@ -1424,7 +1498,7 @@ extern "C" int csa2_paged_attn_shared(const csa2_params* p, const csa2_pages* c,
     else cudaLaunchKernelEx(&cfg, k_paged_shared<false>, a, rows);
     if (const int rc = check_launch("paged_attn_shared")) return rc;
     cfg.numAttrs = 1;
-    cfg.gridDim = dim3(pairs > 1 ? 16 * pairs : 8);
+    cfg.gridDim = dim3(8 * pairs);  // four CTAs an SM
     cfg.blockDim = dim3(kJoinThreads);
     cfg.dynamicSmemBytes = 0;
     cudaLaunchKernelEx(&cfg, k_shared_join, a);

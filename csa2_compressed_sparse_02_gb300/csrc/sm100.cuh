@@ -225,6 +225,10 @@ __device__ __forceinline__ void cluster_sync_all() {
                      "memory");
 }
 
+// The two halves of cluster_sync_all: what stands between them runs while the others come.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;\n" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;\n" ::: "memory"); }
+
 // ---- bulk copy global -> shared, completion counted on an mbarrier ----
 __device__ __forceinline__ void bulk_g2s(void* smem_dst, const void* gsrc, uint32_t bytes,
                                          uint64_t* bar) {
@@ -262,6 +266,11 @@ __device__ __forceinline__ void tma_g2s_2d_hint(uint32_t smem_dst, const void* t
         "[%1, {%2, %3}], [%4], %5;\n" ::"r"(smem_dst),
         "l"(tmap), "r"(x), "r"(y), "r"(smem_u32(bar)), "l"(policy)
         : "memory");
+}
+
+// A tensor map (an address in the kernel's parameters) on its way before the first copy needs it.
+__device__ __forceinline__ void prefetch_tmap(const void* tmap) {
+    asm volatile("prefetch.tensormap [%0];\n" ::"l"(tmap) : "memory");
 }
 
 // The same without a policy.

@@ -525,7 +525,7 @@ def test_attention_flags_and_skips_what_is_out_of_range(kv):
         b.c.pool.copy_(torch.where(raw, torch.zeros((), device=DEV), b.c.pool.float()).to(b.c.pool.dtype))
         return b
     b = fresh()
-    base = b.check()
+    base, ref = b.check(), b.ref()
     most = b.c.table.shape[1] * 16
     for T, bit in ((most + 5, 2), (-3, 2)):  # cut, or nothing seen
         b = fresh()
@@ -535,12 +535,13 @@ def test_attention_flags_and_skips_what_is_out_of_range(kv):
         out = b.run(st=st)
         b.T[4] = min(max(T, 0), most)
         assert_attn(out, b.ref(), kv)
-        assert torch.equal(out[:4], base[:4]) and st.item() & bit
+        assert st.item() & bit
     b = fresh()
     b.seq[1] = 5  # out of range: nothing seen
     st = status()
     out = b.run(st=st)
-    assert st.item() == 1 and torch.all(out[1] == 0) and torch.equal(out[[0, 2, 3, 4]], base[[0, 2, 3, 4]])
+    assert st.item() == 1 and torch.all(out[1] == 0)
+    assert_attn(out, b.ref(), kv)
     b = fresh()
     b.c.table[0, 3], b.c.table[2, 12], b.c.table[3, 1] = -1, b.c.pool.shape[1], 1 << 30
     st = status()
@@ -552,9 +553,11 @@ def test_attention_flags_and_skips_what_is_out_of_range(kv):
         getattr(b, name)[at] = v
         st = status()
         out = b.run(st=st)
-        keep = [i for i in range(5) if i not in lost]
-        assert st.item() == 1 and torch.equal(out[keep], base[keep]), (name, v)
+        assert st.item() == 1, (name, v)
         assert all(torch.all(out[i] == 9) for i in lost)
+        keep = [i for i in range(5) if i not in lost]
+        o, A, dz, F = ref
+        assert_attn(out[keep], (o[keep], A[keep], dz, F[keep]), kv)
     for v in (-1, most + 1):
         b = fresh()
         b.shared[3] = v
