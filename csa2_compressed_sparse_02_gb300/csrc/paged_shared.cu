@@ -1258,137 +1258,132 @@ static_assert(smem_bytes<true>() <= 227 * 1024 && smem_bytes<false>() <= 227 * 1
 
 // ---------------------------------------------------------------- join
 // The units that the ranges cut: o = sum_i O_i 2^(m_i - M) / (2^(sink - M) + sum_i l_i 2^(m_i - M)) over the
-// pairs' partial results in order, by batches. A thread has a row and kEach groups of four channels;
-// the values of a batch of pieces are requested together with their maxima. What sees nothing gets its
-// zeros here.
-// Many units: a CTA takes 32 channels of one, a thread 8 of them. Few units, which are cut into many pieces
-// each: four channels, and every group of threads takes every fourth piece.
+// pairs' partial results in order. What sees nothing gets its zeros here. A thread has a row and four
+// channels and asks for four pieces at once. Many units: the four groups of a CTA have 16 channels of one,
+// whose rows are then written 32 bytes at a time. Few units, which are cut into many pieces each: all have
+// the same channels, and every group takes every fourth piece.
 constexpr int kJoinGroups = 4, kJoinThreads = kRows * kJoinGroups;
+constexpr int kBatch = 4;  // pieces
 
-template <bool kFew>
-__device__ __forceinline__ void join_item(const Args& a, int item, uint32_t s0, int n, float4 (*sums)[kRows],
-                                          float2 (*tops)[kRows]) {
-    constexpr int E = kFew ? 1 : 2, kBatch = kFew ? 4 : 2, kStep = kFew ? kJoinGroups : 1;
+struct JoinShared {
+    int first[kMaxPairs], pieces[kMaxPairs], units;  // of the units that are cut
+    float4 sums[kJoinGroups][kRows];  // (many units: the result, 48 bytes a row)
+    float2 tops[kJoinGroups][kRows];
+};
+
+__device__ __forceinline__ void join_item(const Args& a, JoinShared& sh, bool few, int unit, int item) {
     const int R = threadIdx.x & (kRows - 1), group = threadIdx.x / kRows;
-    const int cg = kFew ? item : 2 * (kJoinGroups * item + group);  // four channels each
+    const int cg = few ? item : kJoinGroups * item + group, step = few ? kJoinGroups : 1, n = sh.pieces[unit];
+    const uint32_t s0 = sh.first[unit];
     // slots of the pieces: the first, and two further on each time from the pair behind it
     const float* const first = part_of(a, 0, 0) + (int64_t)s0 * kPartFloats;
     const float* const rest = part_of(a, 0, 0) + (int64_t)(s0 & ~1u) * kPartFloats;
     const int place = __float_as_int(__ldcg(first + kRows * (kD + 2) + R));
-    float4 acc[E];
-#pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+    const int place_out = __float_as_int(__ldcg(first + kRows * (kD + 2) + (threadIdx.x >> 1 & (kRows - 1))));
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     float den = 0.f, M = -INFINITY;
+    auto add = [&](float4 v, float m, float l) {  // under the maximum M of both
+        if (m == -INFINITY) return;               // (nothing, or nothing seen)
+        const float w = ex2(m - M);
+        den = fmaf(l, w, den);
+        acc = make_float4(fmaf(v.x, w, acc.x), fmaf(v.y, w, acc.y), fmaf(v.z, w, acc.z), fmaf(v.w, w, acc.w));
+    };
+    auto raise = [&](float top) {
+        if (top == M) return;
+        const float w = M == -INFINITY ? 0.f : ex2(M - top);
+        den *= w;
+        acc = make_float4(acc.x * w, acc.y * w, acc.z * w, acc.w * w);
+        M = top;
+    };
 #pragma unroll 1
-    for (int i0 = kFew ? group : 0; i0 < n; i0 += kStep * kBatch) {
-        float4 v[kBatch][E];
+    for (int i0 = few ? group : 0; i0 < n; i0 += step * kBatch) {
+        float4 v[kBatch];
         float m[kBatch], l[kBatch], top = M;
 #pragma unroll
         for (int i = 0; i < kBatch; ++i) {
-            const int p = min(i0 + kStep * i, n - 1);  // (again the last one, for nothing)
-            const float* const at = p ? rest + (int64_t)p * (2 * kPartFloats) : first;
-#pragma unroll
-            for (int e = 0; e < E; ++e) v[i][e] = __ldcg(reinterpret_cast<const float4*>(at) + (cg + e) * kRows + R);
-            m[i] = __ldcg(at + kRows * kD + R);
-            l[i] = __ldcg(at + kRows * (kD + 1) + R);
+            const int p = i0 + step * i;
+            v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+            m[i] = -INFINITY;
+            l[i] = 0.f;
+            if (p < n) {
+                const float* const at = p ? rest + (int64_t)p * (2 * kPartFloats) : first;
+                v[i] = __ldcg(reinterpret_cast<const float4*>(at) + cg * kRows + R);
+                m[i] = __ldcg(at + kRows * kD + R);
+                l[i] = __ldcg(at + kRows * (kD + 1) + R);
+            }
         }
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-            if (i0 + kStep * i >= n) m[i] = -INFINITY;
-            top = fmaxf(top, m[i]);
-        }
-        if (top != M) {
-            const float w = M == -INFINITY ? 0.f : ex2(M - top);
-            den *= w;
+        for (int i = 0; i < kBatch; ++i) top = fmaxf(top, m[i]);
+        raise(top);
 #pragma unroll
-            for (int e = 0; e < E; ++e) acc[e] = make_float4(acc[e].x * w, acc[e].y * w, acc[e].z * w, acc[e].w * w);
-            M = top;
-        }
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-            if (m[i] == -INFINITY) continue;  // (nothing, or nothing seen)
-            const float w = ex2(m[i] - M);
-            den = fmaf(l[i], w, den);
-#pragma unroll
-            for (int e = 0; e < E; ++e)
-                acc[e] = make_float4(fmaf(v[i][e].x, w, acc[e].x), fmaf(v[i][e].y, w, acc[e].y),
-                                     fmaf(v[i][e].z, w, acc[e].z), fmaf(v[i][e].w, w, acc[e].w));
-        }
+        for (int i = 0; i < kBatch; ++i) add(v[i], m[i], l[i]);
     }
-    if constexpr (kFew) {
+    if (few) {
         __syncthreads();  // (the item before has read them)
-        if (group) {
-            sums[group - 1][R] = acc[0];
-            tops[group - 1][R] = make_float2(M, den);
-        }
+        sh.sums[group][R] = acc;
+        sh.tops[group][R] = make_float2(M, den);
         __syncthreads();
         if (group) return;
 #pragma unroll 1
-        for (int g = 0; g < kJoinGroups - 1; ++g) {
-            const float2 o = tops[g][R];
-            const float4 b = sums[g][R];
-            const float top = fmaxf(M, o.x), u = M == -INFINITY ? 0.f : ex2(M - top), w = o.x == -INFINITY ? 0.f : ex2(o.x - top);
-            den = fmaf(o.y, w, den * u);
-            acc[0] = make_float4(fmaf(b.x, w, acc[0].x * u), fmaf(b.y, w, acc[0].y * u), fmaf(b.z, w, acc[0].z * u),
-                                 fmaf(b.w, w, acc[0].w * u));
-            M = top;
+        for (int g = 1; g < kJoinGroups; ++g) {
+            const float2 o = sh.tops[g][R];
+            raise(fmaxf(M, o.x));
+            add(sh.sums[g][R], o.x, o.y);
         }
     }
-    if (place < 0) return;
-    const float s2 = a.sink ? a.sink[place % a.heads] * kLog2e : -INFINITY, top = fmaxf(M, s2);
+    const float s2 = a.sink && place >= 0 ? a.sink[place % a.heads] * kLog2e : -INFINITY, top = fmaxf(M, s2);
     const float f = M == -INFINITY ? 0.f : ex2(M - top);
     den = den * f + (s2 == -INFINITY ? 0.f : ex2(s2 - top));
     const float inv = den == 0.f ? 0.f : f / den;
-    uint32_t o[2 * E];
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-        const __nv_bfloat162 x = __floats2bfloat162_rn(inv == 0.f ? 0.f : acc[e].x * inv, inv == 0.f ? 0.f : acc[e].y * inv);
-        const __nv_bfloat162 y = __floats2bfloat162_rn(inv == 0.f ? 0.f : acc[e].z * inv, inv == 0.f ? 0.f : acc[e].w * inv);
-        o[2 * e] = *reinterpret_cast<const uint32_t*>(&x);
-        o[2 * e + 1] = *reinterpret_cast<const uint32_t*>(&y);
+    const __nv_bfloat162 x = __floats2bfloat162_rn(inv == 0.f ? 0.f : acc.x * inv, inv == 0.f ? 0.f : acc.y * inv);
+    const __nv_bfloat162 y = __floats2bfloat162_rn(inv == 0.f ? 0.f : acc.z * inv, inv == 0.f ? 0.f : acc.w * inv);
+    const uint2 o = make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
+    if (few) {
+        if (place >= 0) *reinterpret_cast<uint2*>(a.out + (int64_t)place * kD + 4 * cg) = o;
+        return;
     }
-    __nv_bfloat16* const out = a.out + (int64_t)place * kD + 4 * cg;
-    if constexpr (kFew) *reinterpret_cast<uint2*>(out) = make_uint2(o[0], o[1]);
-    else *reinterpret_cast<uint4*>(out) = make_uint4(o[0], o[1], o[2], o[3]);
+    uint8_t* const rows = reinterpret_cast<uint8_t*>(sh.sums);
+    __syncthreads();
+    *reinterpret_cast<uint2*>(rows + 48 * R + 8 * group) = o;
+    __syncthreads();
+    if (threadIdx.x < 2 * kRows && place_out >= 0)
+        *reinterpret_cast<uint4*>(a.out + (int64_t)place_out * kD + 16 * item + 8 * (threadIdx.x & 1)) =
+            *reinterpret_cast<const uint4*>(rows + 48 * (threadIdx.x >> 1) + 16 * (threadIdx.x & 1));
 }
 
 __global__ void __launch_bounds__(kJoinThreads, 2) k_shared_join(const __grid_constant__ Args a) {
-    __shared__ int first_s[kMaxPairs], pieces_s[kMaxPairs], units_s;  // of the units that are cut
+    __shared__ JoinShared sh;
     grid_dep_wait();
     const int tid = threadIdx.x;
     if (tid < 32) {  // 32 pairs at a time: the units that begin in a pair's range and end behind it
-        int units = 0;
-        uint32_t through[kMaxPairs / 32];
-        for (int w = kMaxPairs / 32 - 1; w >= 0; --w) {
-            const int c = 32 * w + tid;
-            through[w] = __ballot_sync(0xffffffffu, c < a.pairs && (a.ends[c] & (kCut | kThrough)) == (kCut | kThrough));
-        }
+        constexpr int kWords = kMaxPairs / 32;
+        int units = 0, ends[kWords];
+        uint32_t through[kWords];
 #pragma unroll
-        for (int w = 0; w < kMaxPairs / 32; ++w) {
-            const int c = 32 * w + tid, e = c < a.pairs ? a.ends[c] : 0;
+        for (int w = 0; w < kWords; ++w) ends[w] = 32 * w + tid < a.pairs ? __ldcg(a.ends + 32 * w + tid) : 0;
+#pragma unroll
+        for (int w = 0; w < kWords; ++w) through[w] = __ballot_sync(0xffffffffu, (ends[w] & (kCut | kThrough)) == (kCut | kThrough));
+#pragma unroll
+        for (int w = 0; w < kWords; ++w) {
+            const int c = 32 * w + tid, e = ends[w];
             const bool begins = (e & kCut) && !(e & kThrough);
             const uint32_t all = __ballot_sync(0xffffffffu, begins);
             if (begins) {
                 int n = 2;  // the unit's last pair is the first one behind that does not go through
                 for (int k = c + 1; k + 1 < a.pairs && ((through[k >> 5] >> (k & 31)) & 1u); ++k) ++n;
                 const int at = units + __popc(all & ((1u << tid) - 1u));
-                first_s[at] = 2 * c + (e & kSingle ? 0 : 1);  // its slot, counted over all pairs
-                pieces_s[at] = n;
+                sh.first[at] = 2 * c + (e & kSingle ? 0 : 1);  // its slot, counted over all pairs
+                sh.pieces[at] = n;
             }
             units += __popc(all);
         }
-        if (tid == 0) units_s = units;
+        if (tid == 0) sh.units = units;
     }
     __syncthreads();
-    __shared__ float4 sums[kJoinGroups - 1][kRows];
-    __shared__ float2 tops[kJoinGroups - 1][kRows];
-    const bool few = units_s * (kD / 4) <= 2 * (int)gridDim.x;
-    const int each = few ? kD / 4 : kD / 32;
-    for (int item = blockIdx.x; item < units_s * each; item += gridDim.x) {
-        const int unit = item / each;
-        if (few) join_item<true>(a, item % each, first_s[unit], pieces_s[unit], sums, tops);
-        else join_item<false>(a, item % each, first_s[unit], pieces_s[unit], sums, tops);
-    }
+    const bool few = sh.units * (kD / 4) <= (int)gridDim.x;
+    const int each = few ? kD / 4 : kD / 4 / kJoinGroups;
+    for (int item = blockIdx.x; item < sh.units * each; item += gridDim.x)
+        join_item(a, sh, few, item / each, item % each);
     for (int b = blockIdx.x * (kJoinThreads / 32) + (tid >> 5); b < a.B; b += gridDim.x * (kJoinThreads / 32)) {
         const int row = a.seq ? a.seq[b] : b;
         if (row < 0 || (row < a.g.max_seqs && length_of(a, a.n_tokens[b], false) > 0)) continue;
@@ -1498,7 +1493,7 @@ extern "C" int csa2_paged_attn_shared(const csa2_params* p, const csa2_pages* c,
     else cudaLaunchKernelEx(&cfg, k_paged_shared<false>, a, rows);
     if (const int rc = check_launch("paged_attn_shared")) return rc;
     cfg.numAttrs = 1;
-    cfg.gridDim = dim3(8 * pairs);  // four CTAs an SM
+    cfg.gridDim = dim3(4 * pairs);  // as many as run at once
     cfg.blockDim = dim3(kJoinThreads);
     cfg.dynamicSmemBytes = 0;
     cudaLaunchKernelEx(&cfg, k_shared_join, a);
