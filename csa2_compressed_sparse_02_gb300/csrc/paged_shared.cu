@@ -860,6 +860,13 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
         " mov.b64 {%0, %1}, z;\n}" : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
     return r;
 }
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 r;
+    asm("{\n .reg .b64 x, y, z;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n mov.b64 z, {%6, %7};\n"
+        " fma.rn.f32x2 z, x, y, z;\n mov.b64 {%0, %1}, z;\n}"
+        : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return r;
+}
 // The positions that are not finite in any row of the warp.
 __device__ __forceinline__ uint32_t not_finite(const uint32_t (&sv)[32]) {
     uint32_t which = 0;
@@ -973,11 +980,16 @@ __device__ void softmax_role(Shared<kBf16>& sh, const Args& a, uint32_t tmem, in
             x[i] = mul2(make_float2(__uint_as_float(sv[2 * i]), __uint_as_float(sv[2 * i + 1])), make_float2(c, c));
         uint32_t which = 0;  // positions whose products are not finite, where some row may not see them
         if (!(flags & Info::kSeen)) {
-            which = not_finite(sv);
+            float2 t = c0;  // (a NaN as soon as one is not finite)
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                x[i].x = (seen >> (2 * i)) & 1u ? x[i].x : -INFINITY;
-                x[i].y = (seen >> (2 * i + 1)) & 1u ? x[i].y : -INFINITY;
+            for (int i = 0; i < 16; ++i) t = fma2(x[i], c0, t);
+            if (__any_sync(0xffffffffu, t.x + t.y != 0.f)) which = not_finite(sv);
+            if (!__all_sync(0xffffffffu, seen == ~0u)) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    x[i].x = (seen >> (2 * i)) & 1u ? x[i].x : -INFINITY;
+                    x[i].y = (seen >> (2 * i + 1)) & 1u ? x[i].y : -INFINITY;
+                }
             }
         }
         float top = fmaxf(x[0].x, x[0].y);
