@@ -647,7 +647,8 @@ __device__ void query_role(Shared<kBf16>& sh, const Args& a, int warp, int lane,
         u0 = t.u0;
         f = t.f;
         run = 1;
-        const Row mine = row_info(a, sh.plan, u0, f, kMine * rank + min(warp + S::kHelpWarps * lane, kMine - 1));
+        Row mine = row_info(a, sh.plan, u0, f, kMine * rank + min(warp + S::kHelpWarps * lane, kMine - 1));
+        if (warp + S::kHelpWarps * lane >= kMine) mine.b = -1;  // (no row)
         if (it > 0) {
             // the rows into L2 while the run before still needs its own
             for (int i = 0, r = warp; r < kMine; ++i, r += S::kHelpWarps) {
@@ -656,62 +657,56 @@ __device__ void query_role(Shared<kBf16>& sh, const Args& a, int warp, int lane,
             }
             if (!wait(&sh.q_empty, (uint32_t)((it - 1) & 1), abort)) return;
         }
-        if constexpr (kBf16) {
-#pragma unroll 4
-            for (int i = 0, r = warp; r < kMine; ++i, r += S::kHelpWarps) {
-                const int b = __shfl_sync(0xffffffffu, mine.b, i), h = __shfl_sync(0xffffffffu, mine.h, i);
-                const __nv_bfloat16* src = a.q + (b < 0 ? 0 : b * a.q_seq + h * a.q_head);
+        const __nv_bfloat16* const from = mine.b < 0 ? nullptr : a.q + mine.b * a.q_seq + mine.h * a.q_head;
+        // 16-byte unit u of a row as it is read: in bf16 its place in the operand; else channels 16 l .. + 7 come where
+        // hi of 16 l .. + 15 will be, the next eight where lo will
+        auto place = [&](int r, int u) {
+            if constexpr (kBf16) return smem_u32(sh.q) + (u >> 3) * S::kChunk + sw128(r, u & 7);
+            else return smem_u32(sh.q) + ((u & 1) * 4 + (u >> 4)) * S::kChunk + sw128(r, (u >> 1) & 7);
+        };
+#pragma unroll 2
+        for (int i = 0, r = warp; r < kMine; ++i, r += S::kHelpWarps) {
+            const auto* const row = reinterpret_cast<const __nv_bfloat16*>(
+                __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(from), i));
 #pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    const int u = lane + 32 * x;
-                    cp_async_16(smem_u32(sh.q) + (u >> 3) * S::kChunk + sw128(r, u & 7), src + 8 * u, b >= 0);
-                }
-            }
-        } else {
-            constexpr int kAtOnce = 4;  // rows whose loads are in flight together
-#pragma unroll 1
-            for (int i0 = 0; warp + S::kHelpWarps * i0 < kMine; i0 += kAtOnce) {
-                uint4 w2[kAtOnce][2];
-#pragma unroll
-                for (int i = 0; i < kAtOnce; ++i) {
-                    const int b = __shfl_sync(0xffffffffu, mine.b, i0 + i), h = __shfl_sync(0xffffffffu, mine.h, i0 + i);
-                    const uint4* src = reinterpret_cast<const uint4*>(a.q + (b < 0 ? 0 : b * a.q_seq + h * a.q_head)) + 2 * lane;
-                    w2[i][0] = w2[i][1] = make_uint4(0u, 0u, 0u, 0u);
-                    if (b >= 0) w2[i][0] = __ldg(src), w2[i][1] = __ldg(src + 1);
-                }
-#pragma unroll
-                for (int i = 0; i < kAtOnce; ++i) {
-                    const int r = warp + S::kHelpWarps * (i0 + i);
-                    if (r >= kMine) break;
-                    const uint32_t w[8] = {w2[i][0].x, w2[i][0].y, w2[i][0].z, w2[i][0].w,
-                                           w2[i][1].x, w2[i][1].y, w2[i][1].z, w2[i][1].w};
-                    float mx = 0.f;
-#pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(w[k] << 16)), fabsf(__uint_as_float(w[k] & 0xffff0000u))));
-                    mx = warp_max(mx);
-                    int s = 7 - ((int)((__float_as_uint(mx) >> 23) & 0xffu) - 127);
-                    s = max(-126, min(126, s));
-                    const float two_s = __uint_as_float((uint32_t)(s + 127) << 23);
-                    uint32_t hi[4] = {}, lo[4] = {};
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        float x = __uint_as_float(w[k] << 16) * two_s, y = __uint_as_float(w[k] & 0xffff0000u) * two_s;
-                        x = fmaf(x, 0.f, x);  // infinity to NaN: E4M3 has none
-                        y = fmaf(y, 0.f, y);
-                        const uint32_t xy = e4m3x2(x, y);
-                        const float2 got = e4m3x2_to_float2(xy);
-                        hi[k >> 1] |= xy << (16 * (k & 1));
-                        lo[k >> 1] |= e4m3x2(x - got.x, y - got.y) << (16 * (k & 1));
-                    }
-                    uint8_t* q = sh.q + (lane >> 3) * S::kChunk + sw128(r, lane & 7);
-                    *reinterpret_cast<uint4*>(q) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                    *reinterpret_cast<uint4*>(q + 4 * S::kChunk) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-                    if (lane == 0) sh.row_scale[it & 1][r] = a.scale_log2 * __uint_as_float((uint32_t)(127 - s) << 23);
-                }
+            for (int x = 0; x < 2; ++x) {
+                const int u = kBf16 ? lane + 32 * x : 2 * lane + x;
+                cp_async_16(place(r, u), row ? row + 8 * u : a.q, row != nullptr);
             }
         }
-        if constexpr (kBf16) cp_async_wait_all();
+        cp_async_wait_all();
+        if constexpr (!kBf16) {  // (in 4,000 cycles; by conversion instructions 10,000; unrolled, as much again for the code)
+#pragma unroll 1
+            for (int r = warp; r < kMine; r += S::kHelpWarps) {
+                uint8_t* const q = sh.q + (lane >> 3) * S::kChunk + sw128(r, lane & 7);
+                uint4 *const hi = reinterpret_cast<uint4*>(q), *const lo = reinterpret_cast<uint4*>(q + 4 * S::kChunk);
+                const uint4 v0 = *hi, v1 = *lo;
+                const uint32_t w[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
+                uint32_t mx = 0;  // largest magnitude
+#pragma unroll
+                for (int k = 0; k < 8; ++k) mx = __vmaxu2(mx, w[k] & 0x7fff7fffu);
+                mx = __reduce_max_sync(0xffffffffu, max(mx >> 16, mx & 0xffffu)) << 16;
+                const int s = min(126, 7 - ((int)(mx >> 23) - 127));  // -121 and up
+                // E4M3 is the upper part of f16, 2^8 times as large: x 2^(s - 8) < 1 in f16, rounded to three bits
+                // of mantissa, and so what is left.
+                const float scale = __uint_as_float(s >= -118 ? (uint32_t)(s + 119) << 23 : 1u << max(0, s + 141));
+                uint32_t h[8], l[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const __half2 x = __floats2half2_rn(__uint_as_float(w[k] << 16) * scale,
+                                                        __uint_as_float(w[k] & 0xffff0000u) * scale);
+                    const uint32_t x0 = *reinterpret_cast<const uint32_t*>(&x), x1 = (x0 + 0x00400040u) & 0xff80ff80u;
+                    const uint32_t y = h2_sub(x0, x1) + 0x00400040u;
+                    h[k] = (x1 & 0x80008000u) | ((x1 << 1) & ~0x80008000u);  // (the upper byte)
+                    l[k] = (y & 0x80008000u) | ((y << 1) & ~0x80008000u);
+                }
+                const bool finite = mx < 0x7f800000u;  // else the row is NaN: every score of it is
+                auto pack = [&](uint32_t p, uint32_t q) { return finite ? __byte_perm(p, q, 0x7531) : 0x7f7f7f7fu; };
+                *hi = make_uint4(pack(h[0], h[1]), pack(h[2], h[3]), pack(h[4], h[5]), pack(h[6], h[7]));
+                *lo = make_uint4(pack(l[0], l[1]), pack(l[2], l[3]), pack(l[4], l[5]), pack(l[6], l[7]));
+                if (lane == 0) sh.row_scale[it & 1][r] = a.scale_log2 * __uint_as_float((uint32_t)(127 - s) << 23);
+            }
+        }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
