@@ -632,7 +632,84 @@ __device__ __noinline__ void load_role(Shared<kBf16>& sh, const Args& a, const C
 }
 
 // ---------------------------------------------------------------- queries
-// Three warps stage this CTA's rows of the unit, once a run: warp w rows w, w + 3 and so on.
+// Three warps stage this CTA's rows of the unit, once a run. For the first one of a range the softmax's
+// warps, which have nothing to do yet, take their share of the rows.
+template <bool kBf16>
+struct Stagers {
+    static constexpr int kAll = Shape<kBf16>::kSoftWarps + Shape<kBf16>::kHelpWarps;
+};
+
+// Warp w of n: rows w, w + n and so on, which lane i knows as the warp's row i.
+template <bool kBf16>
+__device__ __noinline__ void stage_queries(Shared<kBf16>& sh, const Args& a, Row mine, int w, int n, int it, int lane, int rank) {
+    using S = Shape<kBf16>;
+    const __nv_bfloat16* const from = mine.b < 0 ? nullptr : a.q + mine.b * a.q_seq + mine.h * a.q_head;
+    // 16-byte unit u of a row as it is read: in bf16 its place in the operand; else channels 16 l .. + 7 come where
+    // hi of 16 l .. + 15 will be, the next eight where lo will
+    auto place = [&](int r, int u) {
+        if constexpr (kBf16) return smem_u32(sh.q) + (u >> 3) * S::kChunk + sw128(r, u & 7);
+        else return smem_u32(sh.q) + ((u & 1) * 4 + (u >> 4)) * S::kChunk + sw128(r, (u >> 1) & 7);
+    };
+#pragma unroll 2
+    for (int i = 0, r = w; r < kMine; ++i, r += n) {
+        const auto* const row = reinterpret_cast<const __nv_bfloat16*>(
+            __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(from), i));
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            const int u = lane + 32 * x;
+            cp_async_16(place(r, u), row ? row + 8 * u : a.q, row != nullptr);
+        }
+    }
+    cp_async_wait_all();
+    __syncwarp();
+    if constexpr (!kBf16) {  // (in 4,000 cycles; by conversion instructions 10,000; unrolled, as much again for the code)
+#pragma unroll 1
+        for (int r = w; r < kMine; r += n) {
+            uint8_t* const q = sh.q + (lane >> 3) * S::kChunk + sw128(r, lane & 7);
+            uint4 *const hi = reinterpret_cast<uint4*>(q), *const lo = reinterpret_cast<uint4*>(q + 4 * S::kChunk);
+            const uint4 v0 = *hi, v1 = *lo;
+            const uint32_t w[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
+            uint32_t mx = 0;  // largest magnitude
+#pragma unroll
+            for (int k = 0; k < 8; ++k) mx = __vmaxu2(mx, w[k] & 0x7fff7fffu);
+            mx = __reduce_max_sync(0xffffffffu, max(mx >> 16, mx & 0xffffu)) << 16;
+            const int s = min(126, 7 - ((int)(mx >> 23) - 127));  // -121 and up
+            // E4M3 is the upper part of f16, 2^8 times as large: x 2^(s - 8) < 1 in f16, rounded to three bits
+            // of mantissa, and so what is left.
+            const float scale = __uint_as_float(s >= -118 ? (uint32_t)(s + 119) << 23 : 1u << max(0, s + 141));
+            uint32_t h[8], l[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const __half2 x = __floats2half2_rn(__uint_as_float(w[k] << 16) * scale,
+                                                    __uint_as_float(w[k] & 0xffff0000u) * scale);
+                const uint32_t x0 = *reinterpret_cast<const uint32_t*>(&x), x1 = (x0 + 0x00400040u) & 0xff80ff80u;
+                const uint32_t y = h2_sub(x0, x1) + 0x00400040u;
+                h[k] = (x1 & 0x80008000u) | ((x1 << 1) & ~0x80008000u);  // (the upper byte)
+                l[k] = (y & 0x80008000u) | ((y << 1) & ~0x80008000u);
+            }
+            const bool finite = mx < 0x7f800000u;  // else the row is NaN: every score of it is
+            auto pack = [&](uint32_t p, uint32_t q) { return finite ? __byte_perm(p, q, 0x7531) : 0x7f7f7f7fu; };
+            *hi = make_uint4(pack(h[0], h[1]), pack(h[2], h[3]), pack(h[4], h[5]), pack(h[6], h[7]));
+            *lo = make_uint4(pack(l[0], l[1]), pack(l[2], l[3]), pack(l[4], l[5]), pack(l[6], l[7]));
+            if (lane == 0) sh.row_scale[it & 1][r] = a.scale_log2 * __uint_as_float((uint32_t)(127 - s) << 23);
+        }
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+    // (of kAll arrivals; warp 0 makes those of the warps that took no part)
+    if (lane < (w == 0 ? 1 + Stagers<kBf16>::kAll - n : 1)) {
+        mbar_arrive(&sh.q_here[it & 1]);
+        arrive_lead(&sh.q_full[it & 1], rank);
+    }
+}
+
+template <bool kBf16>
+__device__ __forceinline__ Row staged_row(const Args& a, const PlanShared& plan, int u0, int f, int w, int n, int lane, int rank) {
+    Row mine = row_info(a, plan, u0, f, kMine * rank + min(w + n * lane, kMine - 1));
+    if (w + n * lane >= kMine) mine.b = -1;  // (no row)
+    return mine;
+}
+
 template <bool kBf16>
 __device__ void query_role(Shared<kBf16>& sh, const Args& a, int warp, int lane, int rank, volatile int* abort) {
     using S = Shape<kBf16>;
@@ -647,72 +724,17 @@ __device__ void query_role(Shared<kBf16>& sh, const Args& a, int warp, int lane,
         u0 = t.u0;
         f = t.f;
         run = 1;
-        Row mine = row_info(a, sh.plan, u0, f, kMine * rank + min(warp + S::kHelpWarps * lane, kMine - 1));
-        if (warp + S::kHelpWarps * lane >= kMine) mine.b = -1;  // (no row)
+        const int n = it ? S::kHelpWarps : Stagers<kBf16>::kAll;
+        const Row mine = staged_row<kBf16>(a, sh.plan, u0, f, warp, n, lane, rank);
         if (it > 0) {
             // the rows into L2 while the run before still needs its own
-            for (int i = 0, r = warp; r < kMine; ++i, r += S::kHelpWarps) {
+            for (int i = 0, r = warp; r < kMine; ++i, r += n) {
                 const int b = __shfl_sync(0xffffffffu, mine.b, i), h = __shfl_sync(0xffffffffu, mine.h, i);
                 if (lane < 8 && b >= 0) prefetch_l2(a.q + b * a.q_seq + h * a.q_head + 64 * lane);
             }
             if (!wait(&sh.q_empty, (uint32_t)((it - 1) & 1), abort)) return;
         }
-        const __nv_bfloat16* const from = mine.b < 0 ? nullptr : a.q + mine.b * a.q_seq + mine.h * a.q_head;
-        // 16-byte unit u of a row as it is read: in bf16 its place in the operand; else channels 16 l .. + 7 come where
-        // hi of 16 l .. + 15 will be, the next eight where lo will
-        auto place = [&](int r, int u) {
-            if constexpr (kBf16) return smem_u32(sh.q) + (u >> 3) * S::kChunk + sw128(r, u & 7);
-            else return smem_u32(sh.q) + ((u & 1) * 4 + (u >> 4)) * S::kChunk + sw128(r, (u >> 1) & 7);
-        };
-#pragma unroll 2
-        for (int i = 0, r = warp; r < kMine; ++i, r += S::kHelpWarps) {
-            const auto* const row = reinterpret_cast<const __nv_bfloat16*>(
-                __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(from), i));
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                const int u = kBf16 ? lane + 32 * x : 2 * lane + x;
-                cp_async_16(place(r, u), row ? row + 8 * u : a.q, row != nullptr);
-            }
-        }
-        cp_async_wait_all();
-        if constexpr (!kBf16) {  // (in 4,000 cycles; by conversion instructions 10,000; unrolled, as much again for the code)
-#pragma unroll 1
-            for (int r = warp; r < kMine; r += S::kHelpWarps) {
-                uint8_t* const q = sh.q + (lane >> 3) * S::kChunk + sw128(r, lane & 7);
-                uint4 *const hi = reinterpret_cast<uint4*>(q), *const lo = reinterpret_cast<uint4*>(q + 4 * S::kChunk);
-                const uint4 v0 = *hi, v1 = *lo;
-                const uint32_t w[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
-                uint32_t mx = 0;  // largest magnitude
-#pragma unroll
-                for (int k = 0; k < 8; ++k) mx = __vmaxu2(mx, w[k] & 0x7fff7fffu);
-                mx = __reduce_max_sync(0xffffffffu, max(mx >> 16, mx & 0xffffu)) << 16;
-                const int s = min(126, 7 - ((int)(mx >> 23) - 127));  // -121 and up
-                // E4M3 is the upper part of f16, 2^8 times as large: x 2^(s - 8) < 1 in f16, rounded to three bits
-                // of mantissa, and so what is left.
-                const float scale = __uint_as_float(s >= -118 ? (uint32_t)(s + 119) << 23 : 1u << max(0, s + 141));
-                uint32_t h[8], l[8];
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const __half2 x = __floats2half2_rn(__uint_as_float(w[k] << 16) * scale,
-                                                        __uint_as_float(w[k] & 0xffff0000u) * scale);
-                    const uint32_t x0 = *reinterpret_cast<const uint32_t*>(&x), x1 = (x0 + 0x00400040u) & 0xff80ff80u;
-                    const uint32_t y = h2_sub(x0, x1) + 0x00400040u;
-                    h[k] = (x1 & 0x80008000u) | ((x1 << 1) & ~0x80008000u);  // (the upper byte)
-                    l[k] = (y & 0x80008000u) | ((y << 1) & ~0x80008000u);
-                }
-                const bool finite = mx < 0x7f800000u;  // else the row is NaN: every score of it is
-                auto pack = [&](uint32_t p, uint32_t q) { return finite ? __byte_perm(p, q, 0x7531) : 0x7f7f7f7fu; };
-                *hi = make_uint4(pack(h[0], h[1]), pack(h[2], h[3]), pack(h[4], h[5]), pack(h[6], h[7]));
-                *lo = make_uint4(pack(l[0], l[1]), pack(l[2], l[3]), pack(l[4], l[5]), pack(l[6], l[7]));
-                if (lane == 0) sh.row_scale[it & 1][r] = a.scale_log2 * __uint_as_float((uint32_t)(127 - s) << 23);
-            }
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-            mbar_arrive(&sh.q_here[it & 1]);
-            arrive_lead(&sh.q_full[it & 1], rank);
-        }
+        stage_queries(sh, a, mine, warp, n, it, lane, rank);
         ++it;
     }
 }
@@ -930,6 +952,11 @@ __device__ void softmax_role(Shared<kBf16>& sh, const Args& a, uint32_t tmem, in
     Row row = {-1, 0, 0, 0};
     int runs = 0, partly = 0;  // tiles that not all rows see
     bool last = true;  // the tile before was a run's last
+    if (sh.plan.range.items > 0) {
+        const int n = Stagers<kBf16>::kAll, w = S::kHelpWarps + warp;
+        const int f = slot_at(a, sh.plan, sh.plan.range.i).f;
+        stage_queries(sh, a, staged_row<kBf16>(a, sh.plan, sh.plan.base, f, w, n, lane, rank), w, n, 0, lane, rank);
+    }
     for (int gt = 0;; ++gt) {
         if (last) {  // a run begins, or the range is done
             if (!info_wait(sh, gt, abort)) return;
@@ -1205,8 +1232,8 @@ k_paged_shared(const __grid_constant__ Args a, const __grid_constant__ CUtensorM
             mbar_init(&sh.p_full[i], 2 * S::kSoftWarps);
             mbar_init(&sh.pv_done[i], 1);
             mbar_init(&sh.s_empty[i], 2 * S::kSoftWarps);
-            mbar_init(&sh.q_full[i], 2 * S::kHelpWarps);
-            mbar_init(&sh.q_here[i], S::kHelpWarps);
+            mbar_init(&sh.q_full[i], 2 * Stagers<kBf16>::kAll);
+            mbar_init(&sh.q_here[i], Stagers<kBf16>::kAll);
             mbar_init(&sh.max_bar[i], 4);
             mbar_init(&sh.sum_bar[i], 4);
         }
