@@ -158,9 +158,9 @@ __device__ void plan_few(const Args& a, PlanShared& sh, int pair) {
     const uint32_t heads = __ballot_sync(0xffffffffu, head), behind = lane < 31 ? heads & (~0u << (lane + 1)) : 0u;
     const uint32_t next = __shfl_sync(0xffffffffu, here, behind ? __ffs(behind) - 1 : 0);
     const uint32_t t = head ? (behind ? next : total) - here : 0;  // of the unit
-    const Cut ranges(total, a.pairs);
-    const int c = min(pair, ranges.n);
-    int64_t at = ranges.at(c), end = ranges.at(min(c + 1, ranges.n));
+    // piece c of k of x tiles, as in Cut: 32 bits hold all of it
+    auto piece = [](uint32_t x, uint32_t k, uint32_t c) { return x / k * c + min(c, x % k); };
+    uint32_t at = piece(total, a.pairs, pair), end = piece(total, a.pairs, pair + 1);
     if (__popc(heads) <= a.pairs && total > 0) {
         const uint32_t lo = (total + a.pairs - 1) / a.pairs;
         for (uint32_t L = lo; L <= lo + kSecondPiece; ++L) {
@@ -171,8 +171,8 @@ __device__ void plan_few(const Args& a, PlanShared& sh, int pair) {
             at = end = total;
             if (mine) {
                 const int l = __ffs(mine) - 1;
-                at = __shfl_sync(0xffffffffu, here + (uint32_t)((uint64_t)t * max(i, 0) / max(k, 1u)), l);
-                end = __shfl_sync(0xffffffffu, here + (uint32_t)((uint64_t)t * (max(i, 0) + 1) / max(k, 1u)), l);
+                at = __shfl_sync(0xffffffffu, here + piece(t, max(k, 1u), i), l);
+                end = __shfl_sync(0xffffffffu, here + piece(t, max(k, 1u), i + 1), l);
             }
             break;
         }
@@ -180,13 +180,13 @@ __device__ void plan_few(const Args& a, PlanShared& sh, int pair) {
     // (units of no tiles begin where the next one does)
     const uint32_t first = __reduce_max_sync(0xffffffffu, head && here <= at ? here : 0u);
     const uint32_t last = __reduce_min_sync(0xffffffffu, head && here >= end ? here : total);
-    const uint32_t begins = __ballot_sync(0xffffffffu, at >= here && at < (int64_t)here + n);
+    const uint32_t begins = __ballot_sync(0xffffffffu, at >= here && at - here < n);
     const int l = begins ? __ffs(begins) - 1 : 0;
     const int base = __shfl_sync(0xffffffffu, unit_of(a, lane, s.f), l);
     const uint32_t before = __shfl_sync(0xffffffffu, here, l);
     if (lane == 0) {
         sh.base = begins ? base : 0;
-        sh.range = {end - at, l, begins ? (int)(at - before) : 0, first < at, last > end};
+        sh.range = {(int64_t)(end - at), l, begins ? (int)(at - before) : 0, first < at, last > end};
     }
     if (lane >= (begins ? base : 0) && lane < a.B) sh.slots[lane - (begins ? base : 0)] = s;
 }
@@ -391,6 +391,7 @@ struct Shape {
     static constexpr uint32_t kChunk = kMine * 128;            // 64 rows x 128 bytes, 128-byte swizzle
     static constexpr uint32_t kPlace = kBf16 ? 2 * kChunk : kChunk;  // 64 positions x 128 channels
     static constexpr int kKeys = kBf16 ? 4 : 7, kValues = kBf16 ? 4 : 6;  // places; a tile takes four of each
+    static_assert(kValues >= 4, "finite_values finds a tile's values all in place");
     static constexpr uint32_t kWeights = (kBf16 ? 2 : 3) * kChunk;  // P: 64 positions a chunk; E4M3: 128, a part each
     static constexpr uint32_t kIdesc = (1u << 4) | ((128u >> 4) << 24);  // D fp32, M = 128 over the pair
     // N = 128 positions, both K-major; N = 256 channels, B MN-major. Types: bf16 1, E4M3 0, E5M2 1
