@@ -426,6 +426,10 @@ struct alignas(16) Info {
     int y[16];       // the pool's row where each box of the tile begins
 };
 
+// E4M3: S is at most two tiles ahead of the softmax, so up to three runs of one tile each are staged whose factors
+// it has not taken yet.
+constexpr int kHeres = 4;
+
 template <bool kBf16>
 struct Shared {
     using S = Shape<kBf16>;
@@ -433,20 +437,20 @@ struct Shared {
     uint8_t q[8 * S::kChunk];
     uint8_t p[2][S::kWeights];  // by tile parity
     typename S::Bound red_max[2][4][kMine];
-    float row_scale[kBf16 ? 0 : 2][kMine];  // E4M3: logit factor, by run parity
+    float row_scale[kBf16 ? 0 : kHeres][kMine];  // E4M3: logit factor, by run
     Info info[kInfos];
     uint64_t key_full[S::kKeys], value_full[S::kValues];  // the even CTA's: the place is full in both
     uint64_t key_empty[S::kKeys], value_empty[S::kValues];
-    uint64_t value_here;  // the odd CTA's: V of a tile that not all rows see has landed
     uint64_t info_full[kInfos], info_empty[kInfos];
     uint64_t s_full[2], s_empty[2], p_full[2], pv_done[2];  // by tile parity; s_empty, p_full: the even CTA's
     uint64_t q_full[2];   // the even CTA's: both CTAs' rows are staged; by run parity
-    uint64_t q_here[2];   // this CTA's are
+    uint64_t q_here[kHeres];  // this CTA's are; by run
     uint64_t q_empty;
     uint64_t max_bar[2], sum_bar[2];
     uint64_t drain;
     PlanShared plan;
     uint32_t tmem_base;
+    int value_here;  // the odd CTA's: V of the tiles before this one that not all rows see has landed
     int abort;
 };
 
@@ -621,7 +625,7 @@ __device__ __noinline__ void load_role(Shared<kBf16>& sh, const Args& a, const C
         if (!keys && rank == 0 && !(flags & Info::kSeen)) {  // the odd CTA's softmax may have to know (finite_values)
             const int of = g - 4 + (lane & 3);
             if (!wait(&full[of % places], (uint32_t)((of / places) & 1), abort)) break;
-            if (lane == 0) mbar_arrive_peer(mapa_shared(smem_u32(&sh.value_here), 1));
+            if (lane == 0) st_cluster(mapa_shared(smem_u32(&sh.value_here), 1), gt + 1);
             __syncwarp();
         }
     }
@@ -692,14 +696,14 @@ __device__ __noinline__ void stage_queries(Shared<kBf16>& sh, const Args& a, Row
             auto pack = [&](uint32_t p, uint32_t q) { return finite ? __byte_perm(p, q, 0x7531) : 0x7f7f7f7fu; };
             *hi = make_uint4(pack(h[0], h[1]), pack(h[2], h[3]), pack(h[4], h[5]), pack(h[6], h[7]));
             *lo = make_uint4(pack(l[0], l[1]), pack(l[2], l[3]), pack(l[4], l[5]), pack(l[6], l[7]));
-            if (lane == 0) sh.row_scale[it & 1][r] = a.scale_log2 * __uint_as_float((uint32_t)(127 - s) << 23);
+            if (lane == 0) sh.row_scale[it % kHeres][r] = a.scale_log2 * __uint_as_float((uint32_t)(127 - s) << 23);
         }
     }
     fence_proxy_async_smem();
     __syncwarp();
     // (of kAll arrivals; warp 0 makes those of the warps that took no part)
     if (lane < (w == 0 ? 1 + Stagers<kBf16>::kAll - n : 1)) {
-        mbar_arrive(&sh.q_here[it & 1]);
+        mbar_arrive(&sh.q_here[it % kHeres]);
         arrive_lead(&sh.q_full[it & 1], rank);
     }
 }
@@ -893,17 +897,22 @@ __device__ __forceinline__ uint32_t not_finite(const uint32_t (&sv)[32]) {
     return __reduce_or_sync(0xffffffffu, which);
 }
 
-// (nth: tiles that not all rows see before this one.)
 // Makes zeros of what is not finite of positions 32 quarter + (the bits of `which`) in this CTA's
 // places of V of tile gt.
 template <bool kBf16>
-__device__ __noinline__ bool finite_values(Shared<kBf16>& sh, uint32_t which, int gt, int nth, int quarter, int lane, int rank,
+__device__ __noinline__ bool finite_values(Shared<kBf16>& sh, uint32_t which, int gt, int quarter, int lane, int rank,
                                            volatile int* abort) {
     using S = Shape<kBf16>;
     // The tile's V has landed (once PV of the tile before has used what the places held, the phase that
     // their barriers are in is this tile's).
     if (gt > 0 && !wait(&sh.pv_done[(gt - 1) & 1], (uint32_t)((gt - 1) >> 1) & 1u, abort)) return false;
-    if (rank && !wait(&sh.value_here, (uint32_t)nth & 1u, abort)) return false;
+    if (rank) {  // (a count, as not every tile's is waited for)
+        for (uint32_t i = 0; __any_sync(0xffffffffu, ld_acquire_cluster(smem_u32(&sh.value_here)) <= gt); ++i) {
+            if (i < kSpinLimit && !__any_sync(0xffffffffu, *abort)) continue;
+            *abort = 1;
+            return false;
+        }
+    }
     uint8_t* at[2];
     for (int h = 0; h < 2; ++h) {
         const int g = 4 * gt + 2 * h + (quarter >> 1), slot = g % S::kValues;
@@ -951,7 +960,7 @@ __device__ void softmax_role(Shared<kBf16>& sh, const Args& a, uint32_t tmem, in
     float m_was = -INFINITY, l_was = 0.f;          // of the piece up to this run
     const float2 c0 = make_float2(0.f, 0.f);
     Row row = {-1, 0, 0, 0};
-    int runs = 0, partly = 0;  // tiles that not all rows see
+    int runs = 0;
     bool last = true;  // the tile before was a run's last
     if (sh.plan.range.items > 0) {
         const int n = Stagers<kBf16>::kAll, w = S::kHelpWarps + warp;
@@ -967,8 +976,8 @@ __device__ void softmax_role(Shared<kBf16>& sh, const Args& a, uint32_t tmem, in
             m = -INFINITY;
             l = 0.f;
             if constexpr (!kBf16) {
-                if (!wait(&sh.q_here[runs & 1], (uint32_t)((runs >> 1) & 1), abort)) return;
-                c = sh.row_scale[runs & 1][r];
+                if (!wait(&sh.q_here[runs % kHeres], (uint32_t)(runs / kHeres) & 1u, abort)) return;
+                c = sh.row_scale[runs % kHeres][r];
             }
             ++runs;
         }
@@ -1109,8 +1118,7 @@ __device__ void softmax_role(Shared<kBf16>& sh, const Args& a, uint32_t tmem, in
         // A weight of zero takes nothing from a position, unless that is not finite: rows that do not see
         // a position must not notice what it holds. Its products with the queries tell. What is not finite
         // of it becomes zero for PV; the rows that see it have NaN (or, of -infinity, zero) weights.
-        if (which && !finite_values(sh, which, gt, partly, quarter, lane, rank, abort)) return;
-        partly += !(flags & Info::kSeen);
+        if (which && !finite_values(sh, which, gt, quarter, lane, rank, abort)) return;
         fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
@@ -1234,12 +1242,12 @@ k_paged_shared(const __grid_constant__ Args a, const __grid_constant__ CUtensorM
             mbar_init(&sh.pv_done[i], 1);
             mbar_init(&sh.s_empty[i], 2 * S::kSoftWarps);
             mbar_init(&sh.q_full[i], 2 * Stagers<kBf16>::kAll);
-            mbar_init(&sh.q_here[i], Stagers<kBf16>::kAll);
             mbar_init(&sh.max_bar[i], 4);
             mbar_init(&sh.sum_bar[i], 4);
         }
+        for (int i = 0; i < kHeres; ++i) mbar_init(&sh.q_here[i], Stagers<kBf16>::kAll);
         mbar_init(&sh.q_empty, 1);
-        mbar_init(&sh.value_here, 1);
+        sh.value_here = 0;
         mbar_init(&sh.drain, 2);
         sh.abort = 0;
         fence_mbar_init();

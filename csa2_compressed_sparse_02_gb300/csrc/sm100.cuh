@@ -202,6 +202,16 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
 __device__ __forceinline__ void mbar_arrive_peer(uint32_t cluster_addr) {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];\n" ::"r"(cluster_addr) : "memory");
 }
+// A word of another CTA's shared memory (cluster address), and this CTA's one that another has written. The
+// store tells of what a bulk copy has put there, so it need not wait for this thread's own.
+__device__ __forceinline__ void st_cluster(uint32_t cluster_addr, int v) {
+    asm volatile("st.relaxed.cluster.shared::cluster.s32 [%0], %1;\n" ::"r"(cluster_addr), "r"(v) : "memory");
+}
+__device__ __forceinline__ int ld_acquire_cluster(uint32_t addr) {
+    int v;
+    asm volatile("ld.acquire.cluster.shared::cta.s32 %0, [%1];\n" : "=r"(v) : "r"(addr) : "memory");
+    return v;
+}
 __device__ __forceinline__ bool mbar_try_wait_acq_cluster(uint64_t* bar, uint32_t parity) {
     uint32_t ok;
     asm volatile(
@@ -271,15 +281,6 @@ __device__ __forceinline__ void tma_g2s_2d_hint(uint32_t smem_dst, const void* t
 // A tensor map (an address in the kernel's parameters) on its way before the first copy needs it.
 __device__ __forceinline__ void prefetch_tmap(const void* tmap) {
     asm volatile("prefetch.tensormap [%0];\n" ::"l"(tmap) : "memory");
-}
-
-// The same without a policy.
-__device__ __forceinline__ void tma_g2s_2d(uint32_t smem_dst, const void* tmap, int x, int y, uint64_t* bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];\n" ::"r"(
-            smem_dst),
-        "l"(tmap), "r"(x), "r"(y), "r"(smem_u32(bar))
-        : "memory");
 }
 
 // Consecutive bytes into L2 only; address and size are multiples of 16.

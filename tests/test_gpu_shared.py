@@ -409,6 +409,20 @@ def test_attention_of_as_many_units_as_pairs(kv, ctas, n):
 
 
 @BOTH
+@pytest.mark.parametrize("heads", [64, 7])
+def test_attention_of_many_units_of_one_tile(kv, heads):
+    """Units that are done before the ones behind them are staged, a hundred to a pair, with rows and
+    positions around each that no other may notice."""
+    rng = np.random.default_rng(heads)
+    b = Batch(kv, heads, [(0, [int(rng.integers(1, 129)) for _ in range(int(rng.integers(1, 128 // heads + 1)))])
+                          for _ in range(400)], 32, seed=heads)
+    b.p.max_ctas = 8
+    out = b.check()
+    for _ in range(3):
+        assert torch.equal(b.run(), out)
+
+
+@BOTH
 def test_attention_of_single_sequences_agrees_with_paged_attn(kv):
     T = [1, 700, 129, 0, 64, 3000]
     b = Batch(kv, 32, [(0, [t]) for t in T], 32, seed=7)
