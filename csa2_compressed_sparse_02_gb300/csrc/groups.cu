@@ -6,7 +6,7 @@
 // leads, and the others' rows of the table are compared with its entry by entry. The first kernel does
 // that with a warp a sequence; in the second one a warp counts what stands before its sequence, which
 // needs no order of arrival. Both are chains of round trips; 4 million comparisons for 2,000 sequences
-// are nothing to 152 SMs (one CTA that counted by leaders took 40 us for them).
+// are nothing to 152 SMs.
 #include <climits>
 
 #include "pages.cuh"
@@ -84,9 +84,17 @@ __global__ void __launch_bounds__(32 * kWarps, 1) k_groups_compare(const __grid_
         if (lead < 0 && lane == 0) left = 1;
         __syncthreads();
         if (!left) break;
-        for (int j = 0; j < n && lead < 0; j += 32) {
-            const uint32_t same = __ballot_sync(0xffffffffu, j + lane < n && keys[j + lane] == mine);
-            if (same) lead = j0 + j + __ffs(same) - 1;
+        constexpr int kLook = 4;  // words of 32 keys at a look
+        for (int j = 0; j < n && lead < 0; j += 32 * kLook) {
+            uint32_t same[kLook];
+#pragma unroll
+            for (int i = 0; i < kLook; ++i) {
+                const int at = j + 32 * i + lane;
+                same[i] = __ballot_sync(0xffffffffu, at < n && keys[min(at, kKeys - 1)] == mine);
+            }
+#pragma unroll
+            for (int i = kLook - 1; i >= 0; --i)
+                if (same[i]) lead = j0 + j + 32 * i + __ffs(same[i]) - 1;
         }
         __syncthreads();
     }
@@ -130,7 +138,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) k_groups_compare(const __grid_
 // Groups in the order of their leaders, members ascending, padding behind them: a sequence's slot is
 // the number of those with a lower leader, and of those with the same one before it.
 __global__ void __launch_bounds__(32 * kWarps, 1) k_groups_order(const __grid_constant__ Args a) {
-    __shared__ int32_t leads[kKeys];
+    __shared__ int32_t leads[kKeys], commons[kKeys];
     sm100::grid_dep_wait();
     const int lane = threadIdx.x & 31, b = blockIdx.x * kWarps + (threadIdx.x >> 5);
     const int mine = b < a.B ? a.ws.lead[b] : 0;
@@ -138,14 +146,18 @@ __global__ void __launch_bounds__(32 * kWarps, 1) k_groups_order(const __grid_co
     for (int j0 = 0; j0 < a.B; j0 += kKeys) {
         const int n = min(kKeys, a.B - j0);
         __syncthreads();
-        for (int j = threadIdx.x; j < n; j += 32 * kWarps) leads[j] = a.ws.lead[j0 + j];
+#pragma unroll 4
+        for (int j = threadIdx.x; j < n; j += 32 * kWarps) {
+            leads[j] = a.ws.lead[j0 + j];
+            commons[j] = a.ws.common[j0 + j];
+        }
         __syncthreads();
+#pragma unroll 8
         for (int j = lane; j < n; j += 32) {
-            const int l = leads[j];
+            const int l = leads[j], c = commons[j];
             lower += l < mine;
-            if (l != mine) continue;
-            before += j0 + j < b;
-            if (j0 + j != mine) least = min(least, a.ws.common[j0 + j]);
+            before += l == mine && j0 + j < b;
+            least = min(least, l == mine && j0 + j != mine ? c : INT_MAX);
         }
     }
     if (b >= a.B) return;
