@@ -13,6 +13,18 @@
 // operand's place in shared memory holds the same positions or channels in both CTAs, which differ
 // between the two products), so a CTA streams 1,024 bytes a position in bf16, and each place of the
 // ring comes free as soon as its own product has read it.
+//
+// Why a pair: O of 64 rows is 256 of a CTA's 512 TMEM columns, which leaves room for two S, so that the
+// products of one tile run beside the softmax of another; 128 rows in one CTA would be all of it. And Q of
+// 64 rows (64 KB) leaves shared memory for the rings.
+//
+// What bounds it. A tile's products take 2,048 cycles of the tensor pipe in bf16; in E4M3, whose S takes two
+// products and PV three at twice the rate, 2,560. E4M3: one in 2,900 to 3,300 cycles, the pipe busy 88 % of the time
+// (24 sequences of 64 heads behind 262,144 positions: 559 us). bf16: one in 3,000 to 3,300, the pipe busy 70 % (24 behind
+// 131,072: 273 us, 1,510 TFLOP/s): a CTA reads 128 KB a tile (43 bytes a cycle, of the 57 that copies alone
+// reach), and its MMAs read 224 KB of shared memory beside them (S of two tiles as one product with N = 256, which
+// reads Q half as often, but needs twice the keys at a time: 305 us against 295). Around the tiles: 11,000 cycles
+// until the first S, 6,000 at the end of a unit, and a join of 6 to 13 us.
 #include <climits>
 #include <type_traits>
 
@@ -194,7 +206,7 @@ __device__ void plan_few(const Args& a, PlanShared& sh, int pair) {
 // Called by the whole CTA.
 __device__ void plan(const Args& a, PlanShared& sh, PlanScratch& x, int pair) {
     static_assert(kKept >= 32, "plan_few keeps its slots");
-    if (a.B <= 32) {  // 3.9 against 2.3 us
+    if (a.B <= 32) {  // 2.4 us (32 sequences; 80 take 4.1 the other way)
         if (threadIdx.x < 32) plan_few(a, sh, pair);
         __syncthreads();
         return;
@@ -455,7 +467,7 @@ struct Shared {
 };
 
 // mbar_wait_warp with the loop out of line: the roles' code runs side by side, and together it has to
-// fit the instruction cache (see the note at the kernel).
+// fit the instruction cache (see k_paged_shared).
 __device__ __noinline__ bool wait_on(uint32_t bar, uint32_t parity, volatile int* abort) {
     for (uint32_t i = 0; i < kSpinLimit; ++i) {
         if (__all_sync(0xffffffffu, mbar_try_wait_at(bar, parity))) return true;
@@ -1210,6 +1222,9 @@ __device__ void softmax_role(Shared<kBf16>& sh, const Args& a, uint32_t tmem, in
     }
 }
 
+// Sixteen warps in seven roles, whose code runs side by side and competes for the instruction cache: with
+// unrolled loops and every wait in line only 54 % of the fetches hit, and a tile took 1.5 times as long. So what a
+// role repeats is short, and what is rare stands out of line.
 template <bool kBf16>
 __global__ void __launch_bounds__(Shape<kBf16>::kThreads, 1)
 k_paged_shared(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap tmap) {
