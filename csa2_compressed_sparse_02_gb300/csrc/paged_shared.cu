@@ -54,6 +54,8 @@ struct Args {
     __nv_bfloat16* out;
     int32_t* ends;    // workspace: of each pair, how its range ends [pairs]
     float* part;      // workspace: two partial results per pair
+    uint8_t* q8;      // workspace, E4M3: the queries as their two parts [B][heads][2][512], and the logits'
+    float* q_scale;   // factors [B][heads]
     int32_t* dev_status;
     float scale_log2;
     int pairs;
@@ -438,10 +440,6 @@ struct alignas(16) Info {
     int y[16];       // the pool's row where each box of the tile begins
 };
 
-// E4M3: S is at most two tiles ahead of the softmax, so up to three runs of one tile each are staged whose factors
-// it has not taken yet.
-constexpr int kHeres = 4;
-
 template <bool kBf16>
 struct Shared {
     using S = Shape<kBf16>;
@@ -449,14 +447,12 @@ struct Shared {
     uint8_t q[8 * S::kChunk];
     uint8_t p[2][S::kWeights];  // by tile parity
     typename S::Bound red_max[2][4][kMine];
-    float row_scale[kBf16 ? 0 : kHeres][kMine];  // E4M3: logit factor, by run
     Info info[kInfos];
     uint64_t key_full[S::kKeys], value_full[S::kValues];  // the even CTA's: the place is full in both
     uint64_t key_empty[S::kKeys], value_empty[S::kValues];
     uint64_t info_full[kInfos], info_empty[kInfos];
     uint64_t s_full[2], s_empty[2], p_full[2], pv_done[2];  // by tile parity; s_empty, p_full: the even CTA's
-    uint64_t q_full[2];   // the even CTA's: both CTAs' rows are staged; by run parity
-    uint64_t q_here[kHeres];  // this CTA's are; by run
+    uint64_t q_full[2];  // the even CTA's: both CTAs' rows are staged; by run parity
     uint64_t q_empty;
     uint64_t max_bar[2], sum_bar[2];
     uint64_t drain;
@@ -656,68 +652,34 @@ struct Stagers {
     static constexpr int kAll = Shape<kBf16>::kSoftWarps + Shape<kBf16>::kHelpWarps;
 };
 
+// A row's operand: 1,024 bytes, in E4M3 hi and lo.
+template <bool kBf16>
+__device__ __forceinline__ const uint8_t* row_bytes(const Args& a, int b, int h) {
+    if constexpr (kBf16) return reinterpret_cast<const uint8_t*>(a.q + b * a.q_seq + h * a.q_head);
+    else return a.q8 + ((int64_t)b * a.heads + h) * (2 * kD);
+}
+
 // Warp w of n: rows w, w + n and so on, which lane i knows as the warp's row i.
 template <bool kBf16>
 __device__ __noinline__ void stage_queries(Shared<kBf16>& sh, const Args& a, Row mine, int w, int n, int it, int lane, int rank) {
     using S = Shape<kBf16>;
-    const __nv_bfloat16* const from = mine.b < 0 ? nullptr : a.q + mine.b * a.q_seq + mine.h * a.q_head;
-    // 16-byte unit u of a row as it is read: in bf16 its place in the operand; else channels 16 l .. + 7 come where
-    // hi of 16 l .. + 15 will be, the next eight where lo will
-    auto place = [&](int r, int u) {
-        if constexpr (kBf16) return smem_u32(sh.q) + (u >> 3) * S::kChunk + sw128(r, u & 7);
-        else return smem_u32(sh.q) + ((u & 1) * 4 + (u >> 4)) * S::kChunk + sw128(r, (u >> 1) & 7);
-    };
+    const uint8_t* const from = mine.b < 0 ? nullptr : row_bytes<kBf16>(a, mine.b, mine.h);
 #pragma unroll 2
     for (int i = 0, r = w; r < kMine; ++i, r += n) {
-        const auto* const row = reinterpret_cast<const __nv_bfloat16*>(
+        const auto* const row = reinterpret_cast<const uint8_t*>(
             __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(from), i));
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
             const int u = lane + 32 * x;
-            cp_async_16(place(r, u), row ? row + 8 * u : a.q, row != nullptr);
+            cp_async_16(smem_u32(sh.q) + (u >> 3) * S::kChunk + sw128(r, u & 7),
+                        row ? row + 16 * u : reinterpret_cast<const uint8_t*>(a.q), row != nullptr);
         }
     }
     cp_async_wait_all();
-    __syncwarp();
-    if constexpr (!kBf16) {  // (in 4,000 cycles; by conversion instructions 10,000; unrolled, as much again for the code)
-#pragma unroll 1
-        for (int r = w; r < kMine; r += n) {
-            uint8_t* const q = sh.q + (lane >> 3) * S::kChunk + sw128(r, lane & 7);
-            uint4 *const hi = reinterpret_cast<uint4*>(q), *const lo = reinterpret_cast<uint4*>(q + 4 * S::kChunk);
-            const uint4 v0 = *hi, v1 = *lo;
-            const uint32_t w[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
-            uint32_t mx = 0;  // largest magnitude
-#pragma unroll
-            for (int k = 0; k < 8; ++k) mx = __vmaxu2(mx, w[k] & 0x7fff7fffu);
-            mx = __reduce_max_sync(0xffffffffu, max(mx >> 16, mx & 0xffffu)) << 16;
-            const int s = min(126, 7 - ((int)(mx >> 23) - 127));  // -121 and up
-            // E4M3 is the upper part of f16, 2^8 times as large: x 2^(s - 8) < 1 in f16, rounded to three bits
-            // of mantissa, and so what is left.
-            const float scale = __uint_as_float(s >= -118 ? (uint32_t)(s + 119) << 23 : 1u << max(0, s + 141));
-            uint32_t h[8], l[8];
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const __half2 x = __floats2half2_rn(__uint_as_float(w[k] << 16) * scale,
-                                                    __uint_as_float(w[k] & 0xffff0000u) * scale);
-                const uint32_t x0 = *reinterpret_cast<const uint32_t*>(&x), x1 = (x0 + 0x00400040u) & 0xff80ff80u;
-                const uint32_t y = h2_sub(x0, x1) + 0x00400040u;
-                h[k] = (x1 & 0x80008000u) | ((x1 << 1) & ~0x80008000u);  // (the upper byte)
-                l[k] = (y & 0x80008000u) | ((y << 1) & ~0x80008000u);
-            }
-            const bool finite = mx < 0x7f800000u;  // else the row is NaN: every score of it is
-            auto pack = [&](uint32_t p, uint32_t q) { return finite ? __byte_perm(p, q, 0x7531) : 0x7f7f7f7fu; };
-            *hi = make_uint4(pack(h[0], h[1]), pack(h[2], h[3]), pack(h[4], h[5]), pack(h[6], h[7]));
-            *lo = make_uint4(pack(l[0], l[1]), pack(l[2], l[3]), pack(l[4], l[5]), pack(l[6], l[7]));
-            if (lane == 0) sh.row_scale[it % kHeres][r] = a.scale_log2 * __uint_as_float((uint32_t)(127 - s) << 23);
-        }
-    }
     fence_proxy_async_smem();
     __syncwarp();
     // (of kAll arrivals; warp 0 makes those of the warps that took no part)
-    if (lane < (w == 0 ? 1 + Stagers<kBf16>::kAll - n : 1)) {
-        mbar_arrive(&sh.q_here[it % kHeres]);
-        arrive_lead(&sh.q_full[it & 1], rank);
-    }
+    if (lane < (w == 0 ? 1 + Stagers<kBf16>::kAll - n : 1)) arrive_lead(&sh.q_full[it & 1], rank);
 }
 
 template <bool kBf16>
@@ -747,7 +709,7 @@ __device__ void query_role(Shared<kBf16>& sh, const Args& a, int warp, int lane,
             // the rows into L2 while the run before still needs its own
             for (int i = 0, r = warp; r < kMine; ++i, r += n) {
                 const int b = __shfl_sync(0xffffffffu, mine.b, i), h = __shfl_sync(0xffffffffu, mine.h, i);
-                if (lane < 8 && b >= 0) prefetch_l2(a.q + b * a.q_seq + h * a.q_head + 64 * lane);
+                if (lane < 8 && b >= 0) prefetch_l2(row_bytes<kBf16>(a, b, h) + 128 * lane);
             }
             if (!wait(&sh.q_empty, (uint32_t)((it - 1) & 1), abort)) return;
         }
@@ -987,10 +949,7 @@ __device__ void softmax_role(Shared<kBf16>& sh, const Args& a, uint32_t tmem, in
             row = row_info(a, sh.plan, in.u0, in.f, kMine * rank + r);
             m = -INFINITY;
             l = 0.f;
-            if constexpr (!kBf16) {
-                if (!wait(&sh.q_here[runs % kHeres], (uint32_t)(runs / kHeres) & 1u, abort)) return;
-                c = sh.row_scale[runs % kHeres][r];
-            }
+            if constexpr (!kBf16) c = row.b < 0 ? 0.f : a.q_scale[(int64_t)row.b * a.heads + row.h];
             ++runs;
         }
         {  // S, the tile's entry, and PV of two tiles before: P may be written again
@@ -1260,7 +1219,6 @@ k_paged_shared(const __grid_constant__ Args a, const __grid_constant__ CUtensorM
             mbar_init(&sh.max_bar[i], 4);
             mbar_init(&sh.sum_bar[i], 4);
         }
-        for (int i = 0; i < kHeres; ++i) mbar_init(&sh.q_here[i], Stagers<kBf16>::kAll);
         mbar_init(&sh.q_empty, 1);
         sh.value_here = 0;
         mbar_init(&sh.drain, 2);
@@ -1313,6 +1271,46 @@ constexpr int smem_bytes() {
     return (int)sizeof(Shared<kBf16>);
 }
 static_assert(smem_bytes<true>() <= 227 * 1024 && smem_bytes<false>() <= 227 * 1024, "shared memory of a CTA");
+
+// ---------------------------------------------------------------- queries for E4M3 pages
+// A warp a row: hi and lo and the logits' factor, in a kernel of its own, as the staging warps took 10,000 cycles
+// for the conversions of 64 rows (four short sequences 19.7 us against 22; 80 drafts 80 against 89; 80 sequences of
+// 18 families 135 against 146).
+constexpr int kQueryWarps = 8;
+
+__global__ void __launch_bounds__(32 * kQueryWarps) k_shared_queries(const __grid_constant__ Args a) {
+    grid_dep_wait();
+    grid_dep_launch_dependents();
+    const int64_t row = (int64_t)blockIdx.x * kQueryWarps + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31;
+    if (row >= (int64_t)a.B * a.heads) return;
+    const int b = (int)(row / a.heads), h = (int)(row - (int64_t)b * a.heads);
+    const uint4* const src = reinterpret_cast<const uint4*>(row_bytes<true>(a, b, h)) + 2 * lane;
+    const uint4 v0 = __ldg(src), v1 = __ldg(src + 1);
+    const uint32_t w[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
+    float mx = 0.f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+        mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(w[k] << 16)), fabsf(__uint_as_float(w[k] & 0xffff0000u))));
+    mx = warp_max(mx);
+    const int s = max(-126, min(126, 7 - ((int)((__float_as_uint(mx) >> 23) & 0xffu) - 127)));
+    const float two_s = __uint_as_float((uint32_t)(s + 127) << 23);
+    uint32_t hi[4] = {}, lo[4] = {};
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        float x = __uint_as_float(w[k] << 16) * two_s, y = __uint_as_float(w[k] & 0xffff0000u) * two_s;
+        x = fmaf(x, 0.f, x);  // infinity to NaN: E4M3 has none
+        y = fmaf(y, 0.f, y);
+        const uint32_t xy = e4m3x2(x, y);
+        const float2 got = e4m3x2_to_float2(xy);
+        hi[k >> 1] |= xy << (16 * (k & 1));
+        lo[k >> 1] |= e4m3x2(x - got.x, y - got.y) << (16 * (k & 1));
+    }
+    uint4* const to = reinterpret_cast<uint4*>(a.q8 + row * (2 * kD)) + lane;
+    to[0] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+    to[kD / 16] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    if (lane == 0) a.q_scale[row] = a.scale_log2 * __uint_as_float((uint32_t)(127 - s) << 23);
+}
 
 // ---------------------------------------------------------------- join
 // The units that the ranges cut: o = sum_i O_i 2^(m_i - M) / (2^(sink - M) + sum_i l_i 2^(m_i - M)) over the
@@ -1459,14 +1457,20 @@ int pairs_of(const csa2_params* p) {
 }
 
 int64_t ends_bytes(int pairs) { return ((int64_t)pairs * 4 + 255) & ~(int64_t)255; }
-int64_t ws_need(int pairs) { return ends_bytes(pairs) + 2 * (int64_t)pairs * kPartFloats * 4; }
+int64_t part_bytes(int pairs) { return 2 * (int64_t)pairs * kPartFloats * 4; }
+int64_t query_bytes(const csa2_params* p, int B) {
+    return p->kv_format == CSA2_BF16 ? 0 : (int64_t)B * p->heads * (2 * kD + 4);
+}
+int64_t ws_need(const csa2_params* p, int pairs, int B) {
+    return ends_bytes(pairs) + part_bytes(pairs) + query_bytes(p, B);
+}
 
 }  // namespace
 
 cudaError_t preload_paged_shared() {
     cudaError_t (*l[])() = {[] { return preload_kernel(k_paged_shared<true>, smem_bytes<true>()); },
                             [] { return preload_kernel(k_paged_shared<false>, smem_bytes<false>()); },
-                            [] { return preload_kernel(k_shared_join); }};
+                            [] { return preload_kernel(k_shared_queries); }, [] { return preload_kernel(k_shared_join); }};
     for (auto f : l)
         if (const cudaError_t e = f()) return e;
     return cudaSuccess;
@@ -1479,7 +1483,7 @@ using namespace csa2;
 extern "C" size_t csa2_paged_attn_shared_workspace_size(const csa2_params* p, const csa2_pages* c, int B) {
     if (!p || !c || B <= 0 || p->heads < 1 || p->heads > kMaxHeads) return 0;
     const int pairs = pairs_of(p);
-    return pairs > 0 ? (size_t)ws_need(pairs) : 0;
+    return pairs > 0 ? (size_t)ws_need(p, pairs, B) : 0;
 }
 
 extern "C" int csa2_paged_attn_shared(const csa2_params* p, const csa2_pages* c, int layer, int B, const void* q,
@@ -1507,7 +1511,7 @@ extern "C" int csa2_paged_attn_shared(const csa2_params* p, const csa2_pages* c,
     if (const int rc = ensure_loaded()) return rc;
     const int pairs = pairs_of(p);
     if (pairs <= 0) return check_launch("paged_attn_shared: device");
-    if ((int64_t)ws_bytes < ws_need(pairs))
+    if ((int64_t)ws_bytes < ws_need(p, pairs, B))
         return fail(CSA2_ERR_SHAPE, "paged_attn_shared: workspace smaller than csa2_paged_attn_shared_workspace_size");
     a.base = a.g.pool + layer * a.g.layer_bytes;
     a.B = B;
@@ -1525,6 +1529,8 @@ extern "C" int csa2_paged_attn_shared(const csa2_params* p, const csa2_pages* c,
     a.out = static_cast<__nv_bfloat16*>(out);
     a.ends = static_cast<int32_t*>(workspace);
     a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + ends_bytes(pairs));
+    a.q8 = static_cast<uint8_t*>(workspace) + ends_bytes(pairs) + part_bytes(pairs);
+    a.q_scale = reinterpret_cast<float*>(a.q8 + (int64_t)B * p->heads * (2 * kD));
     a.dev_status = dev_status;
     a.scale_log2 = p->softmax_scale * kLog2e;
     a.pairs = pairs;
@@ -1543,6 +1549,13 @@ extern "C" int csa2_paged_attn_shared(const csa2_params* p, const csa2_pages* c,
     attr[1].val.clusterDim.x = 2;
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
+    if (!bf16) {
+        cfg.numAttrs = 1;
+        cfg.gridDim = dim3((unsigned)(((int64_t)B * p->heads + kQueryWarps - 1) / kQueryWarps));
+        cfg.blockDim = dim3(32 * kQueryWarps);
+        cudaLaunchKernelEx(&cfg, k_shared_queries, a);
+        if (const int rc = check_launch("paged_attn_shared: queries")) return rc;
+    }
     cfg.numAttrs = 2;
     cfg.gridDim = dim3(2 * pairs);
     cfg.blockDim = dim3(bf16 ? Shape<true>::kThreads : Shape<false>::kThreads);

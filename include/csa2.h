@@ -716,7 +716,7 @@ int csa2_prefix_groups(const csa2_params* p, const csa2_pages* c, int B, const i
                        const int32_t* n_tokens, int least, int32_t* order, int32_t* first,
                        int32_t* shared, void* workspace, size_t ws_bytes, int32_t* dev_status, void* stream);
 
-/* Bytes of scratch csa2_paged_attn_shared needs on the current device (for any B). */
+/* Bytes of scratch csa2_paged_attn_shared needs on the current device for up to B sequences. */
 size_t csa2_paged_attn_shared_workspace_size(const csa2_params* p, const csa2_pages* c, int B);
 
 /*
