@@ -19,12 +19,12 @@
 // 64 rows (64 KB) leaves shared memory for the rings.
 //
 // What bounds it. A tile's products take 2,048 cycles of the tensor pipe in bf16; in E4M3, whose S takes two
-// products and PV three at twice the rate, 2,560. E4M3: one in 2,900 to 3,300 cycles, the pipe busy 88 % of the time
-// (24 sequences of 64 heads behind 262,144 positions: 559 us). bf16: one in 3,000 to 3,300, the pipe busy 70 % (24 behind
-// 131,072: 273 us, 1,510 TFLOP/s): a CTA reads 128 KB a tile (43 bytes a cycle, of the 57 that copies alone
-// reach), and its MMAs read 224 KB of shared memory beside them (S of two tiles as one product with N = 256, which
-// reads Q half as often, but needs twice the keys at a time: 305 us against 295). Around the tiles: 11,000 cycles
-// until the first S, 6,000 at the end of a unit, and a join of 6 to 13 us.
+// products and PV three at twice the rate, 2,560. E4M3: a tile in 2,900 to 3,300 cycles, the pipe busy 88 % of the
+// time (24 sequences of 64 heads behind 262,144 positions: 559 us). bf16: 3,000 to 3,300, the pipe busy 70 % (24 behind
+// 131,072: 273 us, 1,510 TFLOP/s). There it is shared memory: the MMAs read 128 + 96 KB a tile and CTA, the copies
+// write 128 and the softmax 16, which at 128 bytes a cycle is 2,944 cycles. (S of two tiles as one product with
+// N = 256 reads Q half as often, 2,688 cycles, but holds twice the keys at a time: 305 us against 295.) Around the
+// tiles: 11,000 cycles until the first S, 6,000 at the end of a unit, and a join of 6 to 13 us.
 #include <climits>
 #include <type_traits>
 
@@ -158,7 +158,8 @@ struct PlanScratch {  // (where P comes later)
     int64_t warp_sum[32], starts[kMaxPairs];  // starts, tiles: of the units
     uint32_t tiles[kMaxPairs];
     int fits[32];
-    long long at, end, first, last;  // the range; where the unit that it begins in begins, and the last one ends
+    long long at, end;        // the range
+    int begins, ends;         // whether a unit begins at `at`, and one at `end`
 };
 
 // Up to 32 slots: by one warp, a slot a lane.
@@ -254,8 +255,7 @@ __device__ void plan(const Args& a, PlanShared& sh, PlanScratch& x, int pair) {
         x.end = ranges.at(min(c + 1, ranges.n));
         sh.range.i = sh.range.j = 0;
         sh.base = 0;
-        x.first = 0;
-        x.last = total;
+        x.begins = x.ends = 0;
     }
     if (once && total > 0) {
         int64_t units;
@@ -304,14 +304,14 @@ __device__ void plan(const Args& a, PlanShared& sh, PlanScratch& x, int pair) {
             sh.range.j = (int)(at - here);
             sh.base = unit_of(a, i, s.f);
         }
-        if (head && here <= at) atomicMax(&x.first, (long long)here);
-        if (head && here >= end) atomicMin(&x.last, (long long)here);
+        if (head && here == at) x.begins = 1;
+        if (head && here == end) x.ends = 1;
     }
     __syncthreads();
     if (tid == 0) {
         sh.range.items = end - at;
-        sh.range.cont = x.first < at;
-        sh.range.cut = x.last > end;
+        sh.range.cont = !x.begins;
+        sh.range.cut = end < total && !x.ends;
     }
     if (once) {
         if (tid >= sh.base && tid < min(sh.base + kKept, a.B)) sh.slots[tid - sh.base] = s;
