@@ -506,32 +506,37 @@ __device__ void plan_role(Shared<kBf16>& sh, const Args& a, int lane, int rank, 
         }
         return b;
     };
-    // positions that every sequence of the unit sees, of the shared ones
-    auto seen_by_all = [&](int u0, int f) {
-        int n = INT_MAX;
+    // positions that every sequence of the unit sees, of the shared ones, and whether there is but one
+    int reach = 0;
+    bool alone = false;
+    auto look_at_unit = [&](int u0, int f) {
+        int n = INT_MAX, live = 0;
         for (int k = lane; k < a.members && u0 + k < a.B; k += 32) {
             const Slot s = slot_at(a, sh.plan, u0 + k);
-            if (s.f == f && s.b >= 0) n = min(n, s.T);
+            if (s.f != f || s.b < 0) continue;
+            n = min(n, s.T);
+            ++live;
         }
-        return __reduce_min_sync(0xffffffffu, n);
+        reach = __reduce_min_sync(0xffffffffu, n);
+        alone = __reduce_add_sync(0xffffffffu, live) == 1;
     };
     Tile cur = {}, nxt = {};
     Box box = {}, box_nx = {};
-    int reach = 0;
     bool has = walk.next(cur);
     if (has) box = look(cur);
     int gt = 0;
     for (; has; ++gt) {
         const bool more = walk.next(nxt);
         if (more) box_nx = look(nxt);
-        if (runs == 0 && run == 0) reach = seen_by_all(cur.u0, cur.f);
+        if (runs == 0 && run == 0) look_at_unit(cur.u0, cur.f);
         const bool ends = !more || nxt.u0 != cur.u0 || nxt.f != cur.f;
         const bool last = ends || run == S::kRun - 1;
         if (gt >= kInfos && !wait(&sh.info_empty[gt % kInfos], (uint32_t)((gt / kInfos - 1) & 1), abort)) return;
         const bool there = box.nth >= 0 && box.page >= 0 && box.page < a.g.n_pages;
         if (box.nth >= 0 && !there && rank == 0) raise_status(a.dev_status, CSA2_DEV_BAD_INDEX);
         const uint32_t held = __ballot_sync(0xffffffffu, there);
-        const bool seen = cur.k < 0 && min(cur.hi, reach) - cur.t0 >= kTile && __all_sync(0xffffffffu, there || pos >= kTile);
+        const bool seen = (cur.k < 0 || alone) && cur.lo <= cur.t0 && min(cur.hi, reach) - cur.t0 >= kTile &&
+                          __all_sync(0xffffffffu, there || pos >= kTile);
         Info& o = sh.info[gt % kInfos];
         if (pos < kTile) o.y[lane] = there ? box.page * ps + cur.t0 + pos - box.nth * ps : a.g.n_pages * ps;
         if (lane < 4) {
