@@ -1145,16 +1145,16 @@ __device__ void softmax_role(Shared<kBf16>& sh, const Args& a, uint32_t tmem, in
             tmem_wait_ld_regs32(ov[1]);
             if (row.b < 0) continue;
 #pragma unroll
-            for (int i = 0; i < 16; i += 2) {
-                float4 o[2];
+            for (int i = 0; i < 16; i += 4) {
+                float4 o[4];
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
+                for (int k = 0; k < 4; ++k) {
                     const uint32_t* v = &ov[(i + k) >> 3][4 * ((i + k) & 7)];
                     o[k] = make_float4(__uint_as_float(v[0]), __uint_as_float(v[1]), __uint_as_float(v[2]), __uint_as_float(v[3]));
                 }
                 if (!(flags & Info::kBegins)) {
 #pragma unroll
-                    for (int k = 0; k < 2; ++k) {
+                    for (int k = 0; k < 4; ++k) {
                         const float4 b = kept[(n / 4 + i + k) * kRows];
                         o[k] = make_float4(fmaf(b.x, was, o[k].x * now), fmaf(b.y, was, o[k].y * now),
                                            fmaf(b.z, was, o[k].z * now), fmaf(b.w, was, o[k].w * now));
@@ -1162,18 +1162,23 @@ __device__ void softmax_role(Shared<kBf16>& sh, const Args& a, uint32_t tmem, in
                 }
                 if (done) {
                     const bool none = scale == 0.f;
-                    uint32_t v[4];
+                    uint32_t v[8];
 #pragma unroll
-                    for (int k = 0; k < 2; ++k) {
+                    for (int k = 0; k < 4; ++k) {
                         const __nv_bfloat162 y = __floats2bfloat162_rn(none ? 0.f : o[k].x * scale, none ? 0.f : o[k].y * scale);
                         const __nv_bfloat162 z = __floats2bfloat162_rn(none ? 0.f : o[k].z * scale, none ? 0.f : o[k].w * scale);
                         v[2 * k] = *reinterpret_cast<const uint32_t*>(&y);
                         v[2 * k + 1] = *reinterpret_cast<const uint32_t*>(&z);
                     }
-                    *reinterpret_cast<uint4*>(out + n + 4 * i) = make_uint4(v[0], v[1], v[2], v[3]);
+                    if (reinterpret_cast<uintptr_t>(a.out) & 31u) {
+                        *reinterpret_cast<uint4*>(out + n + 4 * i) = make_uint4(v[0], v[1], v[2], v[3]);
+                        *reinterpret_cast<uint4*>(out + n + 4 * i + 8) = make_uint4(v[4], v[5], v[6], v[7]);
+                    } else {
+                        st_global_32(out + n + 4 * i, v);  // a whole sector of the row
+                    }
                 } else {
-                    kept[(n / 4 + i) * kRows] = o[0];
-                    kept[(n / 4 + i + 1) * kRows] = o[1];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) kept[(n / 4 + i + k) * kRows] = o[k];
                 }
             }
         }
@@ -1439,18 +1444,20 @@ __global__ void __launch_bounds__(kJoinThreads, 2) k_shared_join(const __grid_co
             units += __popc(all);
         }
         if (tid == 0) sh.units = units;
+    } else {  // meanwhile, what sees nothing
+        constexpr int kWarps = kJoinThreads / 32 - 1;
+        for (int b = blockIdx.x * kWarps + (tid >> 5) - 1; b < a.B; b += gridDim.x * kWarps) {
+            const int row = a.seq ? a.seq[b] : b;
+            if (row < 0 || (row < a.g.max_seqs && length_of(a, a.n_tokens[b], false) > 0)) continue;
+            uint4* out = reinterpret_cast<uint4*>(a.out + (int64_t)b * a.heads * kD);
+            for (int u = tid & 31; u < a.heads * (kD / 8); u += 32) out[u] = make_uint4(0u, 0u, 0u, 0u);
+        }
     }
     __syncthreads();
     const bool few = sh.units * (kD / 4) <= (int)gridDim.x;
     const int each = few ? kD / 4 : kD / 4 / kJoinGroups;
     for (int item = blockIdx.x; item < sh.units * each; item += gridDim.x)
         join_item(a, sh, few, item / each, item % each);
-    for (int b = blockIdx.x * (kJoinThreads / 32) + (tid >> 5); b < a.B; b += gridDim.x * (kJoinThreads / 32)) {
-        const int row = a.seq ? a.seq[b] : b;
-        if (row < 0 || (row < a.g.max_seqs && length_of(a, a.n_tokens[b], false) > 0)) continue;
-        uint4* out = reinterpret_cast<uint4*>(a.out + (int64_t)b * a.heads * kD);
-        for (int u = tid & 31; u < a.heads * (kD / 8); u += 32) out[u] = make_uint4(0u, 0u, 0u, 0u);
-    }
 }
 
 // CTA pairs on the current device: one CTA per SM, at most max_ctas (but one pair). 0: no device.

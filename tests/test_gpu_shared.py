@@ -530,6 +530,18 @@ def test_attention_padding_strides_and_rows_of_the_table(kv):
 
 
 @BOTH
+def test_attention_of_an_output_at_any_16_bytes(kv):
+    b = Batch(kv, 40, [(100, [130, 101, 128]), (0, [60])], 16, seed=31)
+    base = b.check()
+    flat = torch.full((b.q.numel() + 16,), 9.0, dtype=torch.bfloat16, device=DEV)
+    out = flat[8:-8].view(b.q.shape)
+    assert out.data_ptr() % 32 == 16
+    api.paged_attn_shared(b.p, b.c, 0, b.q, b.sink, i32(b.seq), i32(b.T), b.groups(), out,
+                          api.paged_attn_shared_workspace(b.p, b.c, len(b.T)))
+    assert torch.equal(out, base) and torch.all(flat[:8] == 9) and torch.all(flat[-8:] == 9)
+
+
+@BOTH
 def test_attention_flags_and_skips_what_is_out_of_range(kv):
     """Lengths, sequences, pages and groups outside their ranges: the call ends, flags them and leaves
     what they name unseen; the other sequences are what they were."""
