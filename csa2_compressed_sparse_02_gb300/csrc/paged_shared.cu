@@ -162,11 +162,31 @@ struct PlanScratch {  // (where P comes later)
     int begins, ends;         // whether a unit begins at `at`, and one at `end`
 };
 
+// slot_of of all slots, a lane each (32 at most), which look at a group's first slot where its lane has it.
+__device__ __forceinline__ Slot slots_of(const Args& a, int lane, bool report) {
+    Slot s = {-1, 0, -1, lane, 0, -1};
+    int shared = 0;
+    if (lane < a.B) {
+        s.b = a.order[lane];
+        s.f = first_of(a, lane, report);
+        shared = a.shared[lane];
+        s.row = row_of(a, s.b, report);
+    }
+    s.prow = __shfl_sync(0xffffffffu, s.row, s.f);
+    shared = __shfl_sync(0xffffffffu, shared, s.f);
+    if (lane >= a.B) return s;
+    s.sh = length_of(a, shared, report && s.f == lane);
+    if (s.row < 0) s.b = -1;
+    if (s.row == INT_MAX) s.row = -1;
+    s.T = s.row < 0 ? 0 : length_of(a, a.n_tokens[s.b], report);
+    if (s.prow < 0 || s.prow == INT_MAX) s.sh = 0;
+    return s;
+}
+
 // Up to 32 slots: by one warp, a slot a lane.
 __device__ void plan_few(const Args& a, PlanShared& sh, int pair) {
     const int lane = threadIdx.x & 31;
-    Slot s = {-1, 0, -1, lane, 0, -1};
-    if (lane < a.B) s = slot_of(a, lane, blockIdx.x == 0);
+    const Slot s = slots_of(a, lane, blockIdx.x == 0);
     const bool head = lane < a.B && unit_of(a, lane, s.f) == lane;
     const uint32_t n = lane < a.B ? (uint32_t)prefix_tiles(a, s, lane) + own_tiles(s) : 0;  // (below 2^26)
     const uint32_t here = warp_scan(n, lane), total = __shfl_sync(0xffffffffu, here + n, 31);
@@ -1243,6 +1263,7 @@ k_paged_shared(const __grid_constant__ Args a, const __grid_constant__ CUtensorM
     if (tid == 0) prefetch_tmap(&tmap);
     grid_dep_wait();
     plan(a, sh.plan, *reinterpret_cast<PlanScratch*>(sh.p), pair);  // ends with a CTA barrier
+    if (warp == S::kPlanWarp) plan_role<kBf16>(sh, a, lane, rank, pair, abort);  // (only with this CTA's barriers)
     cluster_wait();  // the other CTA's barriers are there
     tc_fence_after();
     const uint32_t tmem = __shfl_sync(0xffffffffu, sh.tmem_base, 0);
@@ -1259,9 +1280,7 @@ k_paged_shared(const __grid_constant__ Args a, const __grid_constant__ CUtensorM
         }
     } else if (warp == S::kKeyWarp || warp == S::kValueWarp) {
         load_role<kBf16>(sh, a, &tmap, warp == S::kKeyWarp, lane, rank, abort);
-    } else if (warp == S::kPlanWarp) {
-        plan_role<kBf16>(sh, a, lane, rank, pair, abort);
-    } else {
+    } else if (warp != S::kPlanWarp) {
         query_role<kBf16>(sh, a, warp - S::kHelp0, lane, rank, abort);
     }
     tc_fence_before();
