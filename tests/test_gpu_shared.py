@@ -434,6 +434,33 @@ def test_attention_of_single_sequences_agrees_with_paged_attn(kv):
 
 
 @BOTH
+@pytest.mark.parametrize("heads,B", [(1, 65535), (5, 6000)])
+def test_attention_of_large_batches_agrees_with_paged_attn(kv, heads, B):
+    """Groups as prefix_groups finds them among forks of many short prompts. Each call is off by its rounding of
+    the output (2^-8 of it) and of the weights, in numerator and denominator (2^-8 or 2^-11 of the largest value)."""
+    g = torch.Generator(device=DEV).manual_seed(heads)
+    p, S, ps = api.default_params(kv_format=kv, heads=heads), 2048, 8
+    c = api.PagedCache(p, n_pages=6 * S, page_size=ps, max_seqs=S, max_pages=6, device=DEV)
+    c.pool.copy_(torch.randn(c.pool.shape, generator=g, device=DEV).to(c.pool.dtype))
+    table = torch.randperm(6 * S, generator=g, device=DEV).view(S, 6).to(torch.int32)
+    table[:, :2] = table[torch.arange(S, device=DEV) // 8 * 8][:, :2]
+    c.table.copy_(table)
+    seq = torch.randint(-1, S, (B,), generator=g, device=DEV).to(torch.int32)
+    T = torch.randint(0, 6 * ps + 1, (B,), generator=g, device=DEV).to(torch.int32)
+    st, groups = status(), api.PrefixGroups(B, device=DEV)
+    api.prefix_groups(p, c, seq, T, groups, least=9, dev_status=st)
+    q = torch.randn(B, heads, D, generator=g, device=DEV).bfloat16()
+    sink = torch.randn(heads, generator=g, device=DEV)
+    one, two = torch.full_like(q, 9), torch.full_like(q, 9)
+    api.paged_attn_shared(p, c, 0, q, sink, seq, T, groups, one, api.paged_attn_shared_workspace(p, c, B), dev_status=st)
+    api.paged_attn(p, c, 0, q, sink, seq, T, two, api.paged_attn_workspace(p, c, B), dev_status=st)
+    u_p = 2.0 ** -8 if kv == api.BF16 else 2.0 ** -11
+    tol = 2 * (2.0 ** -8 + 2 * u_p + 2.0 ** -15) * c.pool.float().abs().max()
+    assert st.item() == 0 and (one.float() - two.float()).abs().max() <= tol
+    assert torch.all(one[seq < 0] == 9) and torch.all(one[(seq >= 0) & (T == 0)] == 0)
+
+
+@BOTH
 def test_attention_sinks_and_large_logits(kv):
     b = Batch(kv, 64, [(300, [301, 400, 1200]), (0, [5, 0])], 32, seed=11)
     b.q = (b.q.float() * 20).bfloat16()  # logits to +-200: the running maximum moves
