@@ -745,8 +745,8 @@ size_t csa2_paged_attn_shared_workspace_size(const csa2_params* p, const csa2_pa
  *   arbitrary; calls that share it must be ordered (one stream or events).
  * On the 5th-generation tensor cores, by pairs of CTAs (one CTA per SM, or p->max_ctas, at least
  * two): up to 128 rows (heads of a group's sequences) meet a position together. The tiles of the
- * batch are cut into equal ranges; a second kernel joins what was cut, in order, so results do not
- * vary from run to run.
+ * batch are cut into equal ranges, or, where there are no more sets of rows than pairs, each set's into
+ * equal pieces; another kernel joins what was cut, in order, so results do not vary from run to run.
  */
 int csa2_paged_attn_shared(const csa2_params* p, const csa2_pages* c, int layer, int B,
                            const void* q, int64_t q_seq, int64_t q_head, const float* sink,
