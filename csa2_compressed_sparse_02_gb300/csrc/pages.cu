@@ -217,13 +217,17 @@ struct SlotOut {
 };
 
 // Positions that request i held before the step (n_after may be n_tokens itself).
-__device__ __forceinline__ int held_before(const SlotOut& out, const int32_t* start, int i) {
-    return out.n_after[i] - (start[i + 1] - start[i]);
-}
+__device__ __forceinline__ int held_before(const SlotOut& out, int i) { return out.n_after[i] - (out.start[i + 1] - out.start[i]); }
+
+// The requests of a step, at hand for a CTA that looks at them often.
+struct Requests {
+    int32_t start[kOffsets + 1], seq[kOffsets], held[kOffsets], page[kOffsets];  // page: of the first new position
+};
 
 // Row r of the step belongs to the request whose range [start[i], start[i + 1]) holds it.
-__device__ __forceinline__ void map_row(const Pages& g, int B, const int32_t* seq, const int32_t* start, int r,
+__device__ __forceinline__ void map_row(const Pages& g, int B, const int32_t* seq, const Requests* near, int r,
                                         const SlotOut& out, int32_t* dev_status) {
+    const int32_t* const start = near ? near->start : out.start;
     int s = -1, pos = -1;
     int64_t slot = -1;
     if (r < start[B]) {
@@ -233,8 +237,8 @@ __device__ __forceinline__ void map_row(const Pages& g, int B, const int32_t* se
             if (start[mid] <= r) lo = mid;
             else hi = mid;
         }
-        s = seq[lo];
-        pos = held_before(out, start, lo) + r - start[lo];
+        s = near ? near->seq[lo] : seq[lo];
+        pos = (near ? near->held[lo] : held_before(out, lo)) + r - start[lo];
         const int page = g.table[(int64_t)s * g.max_pages + pos / g.page_size];
         if (page >= 0 && page < g.n_pages) slot = (int64_t)page * g.page_size + pos % g.page_size;
         else if (page >= 0) raise_status(dev_status, CSA2_DEV_BAD_INDEX);
@@ -244,68 +248,97 @@ __device__ __forceinline__ void map_row(const Pages& g, int B, const int32_t* se
     out.row_slot[r] = slot;
 }
 
-// Rows that the planning CTA maps itself: 64 rows 7.0 us against 8.4 with the second kernel, 4,096 7.8 against 8.5.
-constexpr int kMapHere = 4096;
+// block_scan of two values at once.
+__device__ __forceinline__ void block_scan2(int64_t& x, int64_t& y, int64_t* all_x, int64_t* all_y) {
+    __shared__ int64_t sums[2][kPlan / 32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    auto scan = [&](int64_t& u, int64_t& v) {
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t a = __shfl_up_sync(0xffffffffu, u, o), b = __shfl_up_sync(0xffffffffu, v, o);
+            if (lane >= o) u += a, v += b;
+        }
+    };
+    int64_t u = x, v = y;
+    scan(u, v);
+    if (lane == 31) sums[0][warp] = u, sums[1][warp] = v;
+    __syncthreads();
+    int64_t p = sums[0][lane], q = sums[1][lane];
+    scan(p, q);
+    const int64_t bx = __shfl_sync(0xffffffffu, p, max(warp - 1, 0)), by = __shfl_sync(0xffffffffu, q, max(warp - 1, 0));
+    *all_x = __shfl_sync(0xffffffffu, p, 31);
+    *all_y = __shfl_sync(0xffffffffu, q, 31);
+    __syncthreads();  // sums is free for the next call
+    x = u - x + (warp ? bx : 0);
+    y = v - y + (warp ? by : 0);
+}
 
-__global__ void __launch_bounds__(kPlan)
-k_slots_plan(Pages g, int B, const int32_t* seq, const int32_t* n_tokens, const int32_t* n_new, int N, SlotOut out,
-             Scratch ws, int32_t* dev_status) {
-    __shared__ int64_t off_s[kOffsets + 1];
-    __shared__ int32_t owner_s[kOwners], list_s[kFresh];
-    __shared__ int rows_fit;
-    sm100::grid_dep_wait();
-    sm100::grid_dep_launch_dependents();
-    const int tid = threadIdx.x;
-    const int4 first_ref = ref4(g, 4 * (int64_t)tid);
-    int32_t* owner = g.max_seqs <= kOwners ? owner_s : ws.owner;
-    for (int i = tid; i < B; i += kPlan)
-        if (seq[i] >= 0 && seq[i] < g.max_seqs) owner[seq[i]] = INT_MAX;
-    if (tid == 0) rows_fit = INT_MAX;
-    __syncthreads();
-    for (int i = tid; i < B; i += kPlan)
-        if (seq[i] >= 0 && seq[i] < g.max_seqs) atomicMin(&owner[seq[i]], i);
-    __syncthreads();
-    int64_t* off = B <= kOffsets ? off_s : ws.offset;
-    int64_t rows = 0, entries = 0;
-    for (int i0 = 0; i0 < B; i0 += kPlan) {
-        const int i = i0 + tid;
-        int64_t n = 0, T = 0;
-        if (i < B) {
-            const int s = seq[i];
-            T = n_tokens[i];
-            const int64_t want = n_new[i];
-            if (s >= g.max_seqs || (s >= 0 && owner[s] != i)) raise_status(dev_status, CSA2_DEV_BAD_INDEX);
-            else if (s >= 0 && (T < 0 || want < 0 || T + want > g.max_len())) raise_status(dev_status, CSA2_DEV_BAD_LENGTH);
-            else if (s >= 0) n = want;
-        }
-        int64_t total;
-        const int64_t at = rows + block_scan(n, &total);
-        rows += total;
-        if (n > 0 && at + n > N) {  // neither this request nor any behind it has room
-            raise_status(dev_status, CSA2_DEV_BAD_LENGTH);
-            atomicMin(&rows_fit, (int)min(at, (int64_t)N));
-            n = 0;
-        }
-        const int64_t pages = n > 0 ? (T + n + g.page_size - 1) / g.page_size - T / g.page_size : 0;
-        const int64_t before = block_scan(pages, &total);  // (its barriers are between rows_fit's writes and reads)
-        if (i < B) {
-            off[i] = entries + before;
-            out.start[i] = (int)min(at, (int64_t)min(rows_fit, N));
-            out.n_after[i] = (int)(T + n);
-        }
-        entries += total;
+// lowest_free for long lists: behind the first round, 16 counts a thread and round (a round takes a
+// microsecond), as four words of a warp's 128 pages each, so that what it lists lies together.
+__device__ int lowest_free_wide(const Pages& g, int64_t want, int32_t* list, int4 first) {
+    constexpr int kWords = 4;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int64_t have = 0;
+    auto bits = [](int4 v) { return (uint32_t)(v.x <= 0) | (v.y <= 0) << 1 | (v.z <= 0) << 2 | (v.w <= 0) << 3; };
+    auto put = [&](uint32_t free, int64_t at, int64_t k) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if ((free >> i) & 1u) {
+                if (k < want) list[k] = (int32_t)at + i;
+                ++k;
+            }
+    };
+    if (want > 0) {
+        const uint32_t free = bits(first);
+        int total;
+        const int before = block_scan(__popc(free), &total);
+        put(free, 4 * (int64_t)threadIdx.x, before);
+        have = total;
     }
-    if (tid == 0) {
-        off[B] = entries;
-        out.start[B] = (int)min(rows, (int64_t)min(rows_fit, N));
+    for (int64_t base = 4 * kPlan; base < g.n_pages && have < want; base += 4 * kWords * kPlan) {
+        const int64_t at = base + 128 * (kWords * warp) + 4 * lane;
+        int4 v[kWords];
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) v[i] = ref4(g, at + 128 * i);
+        uint32_t free[kWords], counts = 0;  // of each word, a byte each: at most 128 in a warp
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) {
+            free[i] = bits(v[i]);
+            counts |= __popc(free[i]) << (8 * i);
+        }
+        uint32_t sum = counts;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t up = __shfl_up_sync(0xffffffffu, sum, o);
+            if (lane >= o) sum += up;
+        }
+        const uint32_t all = __shfl_sync(0xffffffffu, sum, 31);
+        sum -= counts;
+        int n = 0, total;
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) n += (all >> (8 * i)) & 0xffu;
+        int64_t k = have + __shfl_sync(0xffffffffu, block_scan(lane ? 0 : n, &total), 0);
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) {
+            put(free[i], at + 128 * i, k + ((sum >> (8 * i)) & 0xffu));
+            k += (all >> (8 * i)) & 0xffu;
+        }
+        have += total;
     }
-    int32_t* list = entries <= kFresh ? list_s : ws.list;
-    const int free = lowest_free(g, entries, list, first_ref);  // ends with a CTA barrier
-    // Four neighbouring entries a thread: a step of prompts has thousands, and a round takes a microsecond.
+    __syncthreads();
+    return (int)min(have, want);
+}
+
+// Pages list[0 .. free - 1] to the entries without one, which are in the order of the requests: kEach
+// neighbouring ones a thread and round.
+template <int kEach>
+__device__ __forceinline__ void give_pages(const Pages& g, int B, const int32_t* seq, const Requests* near,
+                                           const int64_t* off, int64_t entries, const SlotOut& out, const int32_t* list,
+                                           int free, int32_t* dev_status) {
     int taken = 0;
-    for (int64_t e0 = 0; e0 < entries; e0 += 4 * kPlan) {
-        const int64_t e = e0 + 4 * (int64_t)tid;
-        int32_t* entry[4] = {};
+    for (int64_t e0 = 0; e0 < entries; e0 += kEach * kPlan) {
+        const int64_t e = e0 + kEach * (int64_t)threadIdx.x;
+        int32_t* entry[kEach] = {};
         if (e < entries) {
             int lo = 0, hi = B;  // off[lo] <= e < off[hi]
             while (hi - lo > 1) {
@@ -314,21 +347,22 @@ k_slots_plan(Pages g, int B, const int32_t* seq, const int32_t* n_tokens, const 
                 else hi = mid;
             }
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
+            for (int k = 0; k < kEach; ++k) {
                 if (e + k >= entries) break;
                 while (off[lo + 1] <= e + k) ++lo;
-                entry[k] = g.table + (int64_t)seq[lo] * g.max_pages + held_before(out, out.start, lo) / g.page_size + (e + k - off[lo]);
+                const int s = near ? near->seq[lo] : seq[lo], page = near ? near->page[lo] : held_before(out, lo) / g.page_size;
+                entry[k] = g.table + (int64_t)s * g.max_pages + page + (e + k - off[lo]);
             }
         }
-        int have[4], n = 0;
+        int have[kEach], n = 0;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) have[k] = entry[k] ? *entry[k] : 0;
+        for (int k = 0; k < kEach; ++k) have[k] = entry[k] ? *entry[k] : 0;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) n += have[k] < 0;
+        for (int k = 0; k < kEach; ++k) n += have[k] < 0;
         int total;
         int at = taken + block_scan(n, &total);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
+        for (int k = 0; k < kEach; ++k) {
             if (have[k] >= 0) continue;
             if (at < free) {
                 const int32_t page = list[at];
@@ -341,23 +375,111 @@ k_slots_plan(Pages g, int B, const int32_t* seq, const int32_t* n_tokens, const 
         }
         taken += total;
     }
+}
+
+// Rows that the planning CTA maps itself: 4,096 in 7.0 us, one more by the second kernel 8.2; 8,192 are slower here.
+constexpr int kMapHere = 4096;
+
+__global__ void __launch_bounds__(kPlan)
+k_slots_plan(Pages g, int B, const int32_t* seq, const int32_t* n_tokens, const int32_t* n_new, int N, SlotOut out,
+             Scratch ws, int32_t* dev_status) {
+    __shared__ int64_t off_s[kOffsets + 1], pages_fit;
+    __shared__ int32_t owner_s[kOwners], list_s[kFresh];
+    __shared__ Requests near;
+    __shared__ int rows_fit;
+    sm100::grid_dep_wait();
+    sm100::grid_dep_launch_dependents();
+    const int tid = threadIdx.x;
+    const int4 first_ref = ref4(g, 4 * (int64_t)tid);
+    // the first kPlan requests
+    const int s0 = tid < B ? seq[tid] : -1, T0 = tid < B ? n_tokens[tid] : 0, new0 = tid < B ? n_new[tid] : 0;
+    int32_t* owner = g.max_seqs <= kOwners ? owner_s : ws.owner;
+    for (int i = tid; i < B; i += kPlan) {
+        const int s = i < kPlan ? s0 : seq[i];
+        if (s >= 0 && s < g.max_seqs) owner[s] = INT_MAX;
+    }
+    if (tid == 0) {
+        rows_fit = INT_MAX;
+        pages_fit = INT64_MAX;
+    }
+    __syncthreads();
+    for (int i = tid; i < B; i += kPlan) {
+        const int s = i < kPlan ? s0 : seq[i];
+        if (s >= 0 && s < g.max_seqs) atomicMin(&owner[s], i);
+    }
+    __syncthreads();
+    const bool few = B <= kOffsets;
+    int64_t* off = few ? off_s : ws.offset;
+    int64_t rows = 0, entries = 0;
+    for (int i0 = 0; i0 < B; i0 += kPlan) {
+        const int i = i0 + tid, s = i0 == 0 ? s0 : i < B ? seq[i] : -1;
+        const int64_t T = i0 == 0 ? T0 : i < B ? n_tokens[i] : 0, want = i0 == 0 ? new0 : i < B ? n_new[i] : 0;
+        int64_t n = 0;
+        if (s >= g.max_seqs || (s >= 0 && owner[s] != i)) raise_status(dev_status, CSA2_DEV_BAD_INDEX);
+        else if (s >= 0 && (T < 0 || want < 0 || T + want > g.max_len())) raise_status(dev_status, CSA2_DEV_BAD_LENGTH);
+        else if (s >= 0) n = want;
+        const int first = n > 0 ? (int)T / g.page_size : 0;
+        int64_t at = n, before = n > 0 ? (uint32_t)(T + n - 1) / (uint32_t)g.page_size + 1u - first : 0, all_rows, all_pages;
+        block_scan2(at, before, &all_rows, &all_pages);
+        at += rows;
+        before += entries;
+        if (n > 0 && at + n > N) {  // neither this request nor any behind it has room
+            raise_status(dev_status, CSA2_DEV_BAD_LENGTH);
+            if (at <= N) {  // the first of them
+                rows_fit = (int)at;
+                pages_fit = before;
+            }
+            n = 0;
+        }
+        rows += all_rows;
+        entries += all_pages;
+        __syncthreads();
+        if (i < B) {
+            const int start = (int)min(at, (int64_t)min(rows_fit, N));
+            off[i] = min(before, pages_fit);
+            out.start[i] = start;
+            out.n_after[i] = (int)(T + n);
+            if (few) {
+                near.start[i] = start;
+                near.seq[i] = s;
+                near.held[i] = (int)T;
+                near.page[i] = first;
+            }
+        }
+    }
+    if (tid == 0) {
+        const int all = (int)min(rows, (int64_t)min(rows_fit, N));
+        off[B] = min(entries, pages_fit);
+        out.start[B] = all;
+        if (few) near.start[B] = all;
+    }
+    entries = min(entries, pages_fit);
+    int32_t* list = entries <= kFresh ? list_s : ws.list;
+    const int free = lowest_free_wide(g, entries, list, first_ref);  // ends with a CTA barrier
+    // Decoding requests bring an entry each at most; a step of prompts has thousands, and a round takes a microsecond.
+    if (entries <= kPlan) give_pages<1>(g, B, seq, few ? &near : nullptr, off, entries, out, list, free, dev_status);
+    else give_pages<4>(g, B, seq, few ? &near : nullptr, off, entries, out, list, free, dev_status);
     if (N > kMapHere) return;
     __syncthreads();
-    for (int r = tid; r < N; r += kPlan) map_row(g, B, seq, out.start, r, out, dev_status);
+    for (int r = tid; r < N; r += kPlan) map_row(g, B, seq, few ? &near : nullptr, r, out, dev_status);
 }
 
 __global__ void __launch_bounds__(kCopy)
 k_slots_map(Pages g, int B, const int32_t* seq, int N, SlotOut out, int32_t* dev_status) {
-    __shared__ int32_t start_s[kOffsets + 1];
+    __shared__ Requests near;
     sm100::grid_dep_wait();
-    const int32_t* start = out.start;
-    if (B <= kOffsets) {
-        for (int i = threadIdx.x; i <= B; i += kCopy) start_s[i] = out.start[i];
+    const bool few = B <= kOffsets;
+    if (few) {
+        for (int i = threadIdx.x; i <= B; i += kCopy) {
+            near.start[i] = out.start[i];
+            if (i == B) break;
+            near.seq[i] = seq[i];
+            near.held[i] = held_before(out, i);
+        }
         __syncthreads();
-        start = start_s;
     }
     for (int r = blockIdx.x * kCopy + threadIdx.x; r < N; r += gridDim.x * kCopy)
-        map_row(g, B, seq, start, r, out, dev_status);
+        map_row(g, B, seq, few ? &near : nullptr, r, out, dev_status);
 }
 
 // ---------------------------------------------------------------- release

@@ -125,6 +125,22 @@ def test_slots_of_many_requests_and_rows(N):
         assert np.array_equal(g, w)
 
 
+@pytest.mark.parametrize("spare", [40_000, 9_000, 3_000])
+def test_slots_of_prompts(spare):
+    """A thousand requests of several pages each, free pages here and there in a large pool, or too few of them."""
+    rng = np.random.default_rng(spare)
+    seqs, ps, wide = 1000, 8, 30
+    held = rng.integers(0, 100, seqs)
+    table, ref = random_table(rng, seqs, wide, ps, held, spare)
+    seq = rng.permutation(seqs)
+    new = rng.integers(0, 130, seqs)
+    total = int(new.sum())
+    for N in (total + 5, total - 300):
+        got = slots_of(api.E4M3, table, ref, ps, seq, held[seq], new, N)
+        for g, w in zip(got, model_slots(table, ref, ps, seq, held[seq], new, N)):
+            assert np.array_equal(g, w)
+
+
 def test_slots_without_requests_or_pages():
     table, ref = np.full((3, 4), -1), np.zeros(5, np.int64)
     none = np.zeros(0, np.int64)
