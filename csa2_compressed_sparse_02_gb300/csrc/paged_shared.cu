@@ -145,8 +145,19 @@ struct Range {
     bool cont, cut;    // its first unit began before it; its last one ends behind it
 };
 
-// In tiles: its queries, its first tile's way through an empty pipeline and its partial result.
+// In tiles: its queries, its first tile's way through an empty pipeline and its partial result. In bf16 also a 16th
+// of all: equal pieces of a group's units are at the same positions at the same time, so rows that L2 does not
+// hold are read from HBM once (24 sequences of 64 heads behind 131,072 positions, 6 % more tiles a pair: 271 us
+// against 291; 128 of 16 heads behind 32,768, which it holds, 112 both; E4M3, bound by the tensor pipe, 33 behind
+// 32,768: 124 against 117).
 constexpr int kSecondPiece = 4;
+template <bool kBf16>
+constexpr int kSecondShare = kBf16 ? 16 : INT_MAX;
+constexpr int kTries = 8;  // values of L, from ceil(tiles / pairs) on
+template <bool kBf16>
+__device__ __forceinline__ uint32_t longest_piece(uint32_t lo, int i) {
+    return lo + (kSecondPiece + lo / kSecondShare<kBf16>) * i / (kTries - 1);
+}
 
 constexpr int kKept = 40;  // slots from the range's first unit on that stay in shared memory
 struct PlanShared {
@@ -184,6 +195,7 @@ __device__ __forceinline__ Slot slots_of(const Args& a, int lane, bool report) {
 }
 
 // Up to 32 slots: by one warp, a slot a lane.
+template <bool kBf16>
 __device__ void plan_few(const Args& a, PlanShared& sh, int pair) {
     const int lane = threadIdx.x & 31;
     const Slot s = slots_of(a, lane, blockIdx.x == 0);
@@ -198,7 +210,8 @@ __device__ void plan_few(const Args& a, PlanShared& sh, int pair) {
     uint32_t at = piece(total, a.pairs, pair), end = piece(total, a.pairs, pair + 1);
     if (__popc(heads) <= a.pairs && total > 0) {
         const uint32_t lo = (total + a.pairs - 1) / a.pairs;
-        for (uint32_t L = lo; L <= lo + kSecondPiece; ++L) {
+        for (int tried = 0; tried < kTries; ++tried) {
+            const uint32_t L = longest_piece<kBf16>(lo, tried);
             const uint32_t k = (t + L - 1) / L;
             if (__reduce_add_sync(0xffffffffu, k) > (uint32_t)a.pairs) continue;
             const int i = pair - (int)warp_scan(k, lane);
@@ -227,10 +240,11 @@ __device__ void plan_few(const Args& a, PlanShared& sh, int pair) {
 }
 
 // Called by the whole CTA.
+template <bool kBf16>
 __device__ void plan(const Args& a, PlanShared& sh, PlanScratch& x, int pair) {
     static_assert(kKept >= 32, "plan_few keeps its slots");
     if (a.B <= 32) {  // 2.4 us (32 sequences; 80 take 4.1 the other way)
-        if (threadIdx.x < 32) plan_few(a, sh, pair);
+        if (threadIdx.x < 32) plan_few<kBf16>(a, sh, pair);
         __syncthreads();
         return;
     }
@@ -286,19 +300,19 @@ __device__ void plan(const Args& a, PlanShared& sh, PlanScratch& x, int pair) {
             if (n) atomicAdd(&x.tiles[max(unit, 0)], n);
             if (head) x.starts[unit] = here;
             __syncthreads();
-            uint32_t lo = (uint32_t)((total + a.pairs - 1) / a.pairs), hi = lo + kSecondPiece + 1;
-            const uint32_t t = tid < units ? x.tiles[tid] : 0;
-            // The smallest L of lo .. hi - 1 with sum ceil(tiles / L) <= pairs, a value a warp; hi: none
-            if (warp <= kSecondPiece) {
+            const uint32_t lo = (uint32_t)((total + a.pairs - 1) / a.pairs), t = tid < units ? x.tiles[tid] : 0;
+            // The smallest L that is tried with sum ceil(tiles / L) <= pairs, a value a warp
+            if (warp < kTries) {
+                const uint32_t L = longest_piece<kBf16>(lo, warp);
                 uint32_t k = 0;
-                for (int u = lane; u < (int)units; u += 32) k += (x.tiles[u] + lo + warp - 1) / (lo + warp);
+                for (int u = lane; u < (int)units; u += 32) k += (x.tiles[u] + L - 1) / L;
                 k = __reduce_add_sync(0xffffffffu, k);
                 if (lane == 0) x.fits[warp] = k <= (uint32_t)a.pairs;
             }
             __syncthreads();
-            const uint32_t good = __ballot_sync(0xffffffffu, lane <= kSecondPiece && x.fits[lane]);
-            const uint32_t L = good ? lo + __ffs(good) - 1 : hi;
-            if (L < hi) {
+            const uint32_t good = __ballot_sync(0xffffffffu, lane < kTries && x.fits[lane]);
+            if (good) {
+                const uint32_t L = longest_piece<kBf16>(lo, __ffs(good) - 1);
                 const uint32_t k = (t + L - 1) / L;
                 if (tid == 0) x.at = x.end = total;
                 const int64_t c = pair - scan(k, &all);
@@ -1262,7 +1276,7 @@ k_paged_shared(const __grid_constant__ Args a, const __grid_constant__ CUtensorM
     cluster_arrive();
     if (tid == 0) prefetch_tmap(&tmap);
     grid_dep_wait();
-    plan(a, sh.plan, *reinterpret_cast<PlanScratch*>(sh.p), pair);  // ends with a CTA barrier
+    plan<kBf16>(a, sh.plan, *reinterpret_cast<PlanScratch*>(sh.p), pair);  // ends with a CTA barrier
     if (warp == S::kPlanWarp) plan_role<kBf16>(sh, a, lane, rank, pair, abort);  // (only with this CTA's barriers)
     cluster_wait();  // the other CTA's barriers are there
     tc_fence_after();
