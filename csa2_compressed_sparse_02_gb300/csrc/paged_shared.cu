@@ -20,11 +20,12 @@
 //
 // What bounds it. A tile's products take 2,048 cycles of the tensor pipe in bf16; in E4M3, whose S takes two
 // products and PV three at twice the rate, 2,560. E4M3: a tile in 2,900 to 3,300 cycles, the pipe busy 88 % of the
-// time (24 sequences of 64 heads behind 262,144 positions: 559 us). bf16: 3,000 to 3,300, the pipe busy 70 % (24 behind
-// 131,072: 273 us, 1,510 TFLOP/s). There it is shared memory: the MMAs read 128 + 96 KB a tile and CTA, the copies
-// write 128 and the softmax 16, which at 128 bytes a cycle is 2,944 cycles. (S of two tiles as one product with
-// N = 256 reads Q half as often, 2,688 cycles, but holds twice the keys at a time: 305 us against 295.) Around the
-// tiles: 11,000 cycles until the first S, 6,000 at the end of a unit, and a join of 6 to 13 us.
+// time (24 sequences of 64 heads behind 262,144 positions: 559 us). bf16: the copies, 128 KB a tile and CTA, which by
+// themselves reach 57 bytes a cycle (2,300 cycles), through rings of half a tile. A tile takes 2,400 where all pairs
+// read the same rows at a time (76 units of 152 sequences behind 16,384), 2,850 where a few of them do (24 behind
+// 131,072: 272 us, 1,510 TFLOP/s), 3,060 where each is at a place of its own. (S of two tiles as one product with N =
+// 256 reads Q half as often, but needs the keys of both at a time: 305 us against 295.) Around the tiles: 11,000
+// cycles until the first S, 6,000 at the end of a unit, and a join of 6 to 13 us.
 #include <climits>
 #include <type_traits>
 
@@ -143,21 +144,12 @@ struct Range {
     int64_t items;
     int i, j;          // it begins with tile j of slot i
     bool cont, cut;    // its first unit began before it; its last one ends behind it
+    int wave;          // ranges of equal length: it; else 0
 };
 
-// In tiles: its queries, its first tile's way through an empty pipeline and its partial result. In bf16 also a 16th
-// of all: equal pieces of a group's units are at the same positions at the same time, so rows that L2 does not
-// hold are read from HBM once (24 sequences of 64 heads behind 131,072 positions, 6 % more tiles a pair: 271 us
-// against 291; 128 of 16 heads behind 32,768, which it holds, 112 both; E4M3, bound by the tensor pipe, 33 behind
-// 32,768: 124 against 117).
+// In tiles: its queries, its first tile's way through an empty pipeline and its partial result.
 constexpr int kSecondPiece = 4;
-template <bool kBf16>
-constexpr int kSecondShare = kBf16 ? 16 : INT_MAX;
-constexpr int kTries = 8;  // values of L, from ceil(tiles / pairs) on
-template <bool kBf16>
-__device__ __forceinline__ uint32_t longest_piece(uint32_t lo, int i) {
-    return lo + (kSecondPiece + lo / kSecondShare<kBf16>) * i / (kTries - 1);
-}
+constexpr int kTries = kSecondPiece + 1;  // values of L, from ceil(tiles / pairs) on
 
 constexpr int kKept = 40;  // slots from the range's first unit on that stay in shared memory
 struct PlanShared {
@@ -195,7 +187,6 @@ __device__ __forceinline__ Slot slots_of(const Args& a, int lane, bool report) {
 }
 
 // Up to 32 slots: by one warp, a slot a lane.
-template <bool kBf16>
 __device__ void plan_few(const Args& a, PlanShared& sh, int pair) {
     const int lane = threadIdx.x & 31;
     const Slot s = slots_of(a, lane, blockIdx.x == 0);
@@ -208,15 +199,17 @@ __device__ void plan_few(const Args& a, PlanShared& sh, int pair) {
     // piece c of k of x tiles, as in Cut: 32 bits hold all of it
     auto piece = [](uint32_t x, uint32_t k, uint32_t c) { return x / k * c + min(c, x % k); };
     uint32_t at = piece(total, a.pairs, pair), end = piece(total, a.pairs, pair + 1);
+    int wave = (int)(total / a.pairs);
     if (__popc(heads) <= a.pairs && total > 0) {
         const uint32_t lo = (total + a.pairs - 1) / a.pairs;
         for (int tried = 0; tried < kTries; ++tried) {
-            const uint32_t L = longest_piece<kBf16>(lo, tried);
+            const uint32_t L = lo + tried;
             const uint32_t k = (t + L - 1) / L;
             if (__reduce_add_sync(0xffffffffu, k) > (uint32_t)a.pairs) continue;
             const int i = pair - (int)warp_scan(k, lane);
             const uint32_t mine = __ballot_sync(0xffffffffu, i >= 0 && i < (int)k);
             at = end = total;
+            wave = 0;
             if (mine) {
                 const int l = __ffs(mine) - 1;
                 at = __shfl_sync(0xffffffffu, here + piece(t, max(k, 1u), i), l);
@@ -234,17 +227,16 @@ __device__ void plan_few(const Args& a, PlanShared& sh, int pair) {
     const uint32_t before = __shfl_sync(0xffffffffu, here, l);
     if (lane == 0) {
         sh.base = begins ? base : 0;
-        sh.range = {(int64_t)(end - at), l, begins ? (int)(at - before) : 0, first < at, last > end};
+        sh.range = {(int64_t)(end - at), l, begins ? (int)(at - before) : 0, first < at, last > end, wave};
     }
     if (lane >= (begins ? base : 0) && lane < a.B) sh.slots[lane - (begins ? base : 0)] = s;
 }
 
 // Called by the whole CTA.
-template <bool kBf16>
 __device__ void plan(const Args& a, PlanShared& sh, PlanScratch& x, int pair) {
     static_assert(kKept >= 32, "plan_few keeps its slots");
     if (a.B <= 32) {  // 2.4 us (32 sequences; 80 take 4.1 the other way)
-        if (threadIdx.x < 32) plan_few<kBf16>(a, sh, pair);
+        if (threadIdx.x < 32) plan_few(a, sh, pair);
         __syncthreads();
         return;
     }
@@ -288,6 +280,7 @@ __device__ void plan(const Args& a, PlanShared& sh, PlanScratch& x, int pair) {
         x.at = ranges.at(c);
         x.end = ranges.at(min(c + 1, ranges.n));
         sh.range.i = sh.range.j = 0;
+        sh.range.wave = (int)min(ranges.base, (int64_t)INT_MAX);
         sh.base = 0;
         x.begins = x.ends = 0;
     }
@@ -303,7 +296,7 @@ __device__ void plan(const Args& a, PlanShared& sh, PlanScratch& x, int pair) {
             const uint32_t lo = (uint32_t)((total + a.pairs - 1) / a.pairs), t = tid < units ? x.tiles[tid] : 0;
             // The smallest L that is tried with sum ceil(tiles / L) <= pairs, a value a warp
             if (warp < kTries) {
-                const uint32_t L = longest_piece<kBf16>(lo, warp);
+                const uint32_t L = lo + warp;
                 uint32_t k = 0;
                 for (int u = lane; u < (int)units; u += 32) k += (x.tiles[u] + L - 1) / L;
                 k = __reduce_add_sync(0xffffffffu, k);
@@ -312,9 +305,9 @@ __device__ void plan(const Args& a, PlanShared& sh, PlanScratch& x, int pair) {
             __syncthreads();
             const uint32_t good = __ballot_sync(0xffffffffu, lane < kTries && x.fits[lane]);
             if (good) {
-                const uint32_t L = longest_piece<kBf16>(lo, __ffs(good) - 1);
+                const uint32_t L = lo + __ffs(good) - 1;
                 const uint32_t k = (t + L - 1) / L;
-                if (tid == 0) x.at = x.end = total;
+                if (tid == 0) x.at = x.end = total, sh.range.wave = 0;
                 const int64_t c = pair - scan(k, &all);
                 if (c >= 0 && c < k) {
                     x.at = x.starts[tid] + t * c / k;
@@ -374,6 +367,7 @@ struct Walk {
     int i, j;
     Slot s;  // of slot i
     int pre, items, u0;
+    int first, len, ahead;  // of the prefix's tiles the range has `len` from `first` on, and begins `ahead` of it
     __device__ __forceinline__ Walk(const Args& a, const PlanShared& plan)
         : a(a), plan(plan), left(plan.range.items), i(plan.range.i), j(plan.range.j) {
         if (left > 0) enter();
@@ -383,6 +377,16 @@ struct Walk {
         u0 = unit_of(a, i, s.f);
         pre = u0 == i ? tiles_of(s.sh) : 0;
         items = pre + own_tiles(s);
+        // Ranges of equal length begin anywhere in a prefix. Each goes round its part of it so that the tile, modulo
+        // that length, is the same for all at a time: pairs that read the same rows then do so together (44 sequences
+        // of 64 heads behind 131,072 bf16 positions 452 us against 519, 24 272 against 291; 64 in E4M3 715 against 736).
+        first = j;
+        len = (int)min((int64_t)max(pre - j, 0), left);
+        ahead = 0;
+        if (const int wave = plan.range.wave; wave > 1 && len > 1) {
+            const int at = (int)((plan.range.items - left + wave - j % wave) % wave);
+            if (at < len) ahead = at;
+        }
     }
     __device__ __forceinline__ bool next(Tile& t) {
         if (left <= 0) return false;
@@ -394,7 +398,9 @@ struct Walk {
         const bool own = j >= pre;
         t.u0 = u0;
         t.f = s.f;
-        t.t0 = kTile * (own ? s.sh / kTile + j - pre : j);
+        int tile = j + ahead;
+        if (tile >= first + len) tile -= len;
+        t.t0 = kTile * (own ? s.sh / kTile + j - pre : tile);
         t.lo = own ? s.sh : 0;
         t.hi = own ? s.T : s.sh;
         t.row = own ? s.row : s.prow;
@@ -1276,7 +1282,7 @@ k_paged_shared(const __grid_constant__ Args a, const __grid_constant__ CUtensorM
     cluster_arrive();
     if (tid == 0) prefetch_tmap(&tmap);
     grid_dep_wait();
-    plan<kBf16>(a, sh.plan, *reinterpret_cast<PlanScratch*>(sh.p), pair);  // ends with a CTA barrier
+    plan(a, sh.plan, *reinterpret_cast<PlanScratch*>(sh.p), pair);  // ends with a CTA barrier
     if (warp == S::kPlanWarp) plan_role<kBf16>(sh, a, lane, rank, pair, abort);  // (only with this CTA's barriers)
     cluster_wait();  // the other CTA's barriers are there
     tc_fence_after();
