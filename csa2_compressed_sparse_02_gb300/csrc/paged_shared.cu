@@ -1312,6 +1312,7 @@ k_paged_shared(const __grid_constant__ Args a, const __grid_constant__ CUtensorM
         tc_fence_after();
         tmem_dealloc_pair(tmem, kTmemCols);
     }
+    __syncwarp();
     cluster_sync_all();
 }
 
