@@ -498,7 +498,8 @@ struct Shared {
     uint64_t drain;
     PlanShared plan;
     uint32_t tmem_base;
-    int value_here;  // the odd CTA's: V of the tiles before this one that not all rows see has landed
+    int value_asked, value_told;  // the even CTA's: the odd one's softmax waits for V of the tiles before this one; was told
+    int value_here;   // the odd CTA's: it has landed (finite_values)
     int abort;
 };
 
@@ -512,14 +513,46 @@ __device__ __noinline__ bool wait_on(uint32_t bar, uint32_t parity, volatile int
     *abort = 1;
     return false;
 }
+__device__ __forceinline__ bool ready(uint32_t bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, mbar_try_wait_at(bar, parity));
+}
 __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
-    return __all_sync(0xffffffffu, mbar_try_wait_at(smem_u32(bar), parity)) || wait_on(smem_u32(bar), parity, abort);
+    return ready(smem_u32(bar), parity) || wait_on(smem_u32(bar), parity, abort);
 }
 
 // An arrive on the even CTA's barrier, from either CTA of the pair.
 __device__ __forceinline__ void arrive_lead(uint64_t* bar, uint32_t rank) {
     if (rank == 0) mbar_arrive(bar);
     else mbar_arrive_peer(mapa_shared(smem_u32(bar), 0));
+}
+
+// What the odd CTA's softmax asks of the even one, on whose barriers both CTAs' copies count (finite_values): that
+// V of a tile has landed. The even CTA's plan warp answers while it waits for a barrier of its own, with a release
+// at the cluster's scope that covers the odd CTA's copies too. (The value loader, were it to look for requests between
+// its tries: 24 sequences of 64 heads behind 131,072 bf16 positions 345 us against 290.)
+template <bool kBf16>
+__device__ __noinline__ bool wait_answering(Shared<kBf16>& sh, uint64_t* bar, uint32_t parity, int lane, volatile int* abort) {
+    using S = Shape<kBf16>;
+    for (uint32_t i = 0; i < kSpinLimit; ++i) {
+        if (ready(smem_u32(bar), parity)) return true;
+        if ((i & 255u) == 255u && __any_sync(0xffffffffu, *abort != 0)) return false;
+        if (__shfl_sync(0xffffffffu, ld_relaxed_cluster(smem_u32(&sh.value_asked)), 0) <= sh.value_told) continue;
+        const int asked = __shfl_sync(0xffffffffu, ld_acquire_cluster(smem_u32(&sh.value_asked)), 0);
+        if (asked <= sh.value_told) continue;
+        // Its PV waits for the answer and that of the tile before is done, so the phases that the barriers of its
+        // places are in are this tile's.
+        const int of = 4 * (asked - 1) + (lane & 3);
+        const uint32_t phase = (uint32_t)((of / S::kValues) & 1);
+        if (!wait(&sh.value_full[of % S::kValues], phase, abort)) return false;
+        if (!__all_sync(0xffffffffu, acquire_phase_cluster(&sh.value_full[of % S::kValues], phase))) return false;
+        if (lane == 0) {
+            st_release_cluster(mapa_shared(smem_u32(&sh.value_here), 1), asked);
+            sh.value_told = asked;
+        }
+        __syncwarp();
+    }
+    *abort = 1;
+    return false;
 }
 
 // ---------------------------------------------------------------- tiles
@@ -571,7 +604,9 @@ __device__ void plan_role(Shared<kBf16>& sh, const Args& a, int lane, int rank, 
         if (runs == 0 && run == 0) look_at_unit(cur.u0, cur.f);
         const bool ends = !more || nxt.u0 != cur.u0 || nxt.f != cur.f;
         const bool last = ends || run == S::kRun - 1;
-        if (gt >= kInfos && !wait(&sh.info_empty[gt % kInfos], (uint32_t)((gt / kInfos - 1) & 1), abort)) return;
+        if (gt >= kInfos && !(rank == 0 ? wait_answering(sh, &sh.info_empty[gt % kInfos], (uint32_t)((gt / kInfos - 1) & 1), lane, abort)
+                                        : wait(&sh.info_empty[gt % kInfos], (uint32_t)((gt / kInfos - 1) & 1), abort)))
+            return;
         const bool there = box.nth >= 0 && box.page >= 0 && box.page < a.g.n_pages;
         if (box.nth >= 0 && !there && rank == 0) raise_status(a.dev_status, CSA2_DEV_BAD_INDEX);
         const uint32_t held = __ballot_sync(0xffffffffu, there);
@@ -611,11 +646,19 @@ __device__ void plan_role(Shared<kBf16>& sh, const Args& a, int lane, int rank, 
         box = box_nx;
     }
     if (range.items <= 0 && lane == 0 && rank == 0) a.ends[pair] = 0;
-    if (gt >= kInfos && !wait(&sh.info_empty[gt % kInfos], (uint32_t)((gt / kInfos - 1) & 1), abort)) return;
+    if (gt >= kInfos && !(rank == 0 ? wait_answering(sh, &sh.info_empty[gt % kInfos], (uint32_t)((gt / kInfos - 1) & 1), lane, abort)
+                                    : wait(&sh.info_empty[gt % kInfos], (uint32_t)((gt / kInfos - 1) & 1), abort)))
+        return;
     if (lane == 0) {
         sh.info[gt % kInfos].flags = Info::kStop;
         mbar_arrive(&sh.info_full[gt % kInfos]);
     }
+    __syncwarp();
+    // To the last tile's PV there may be questions. (Every phase in turn: the softmax had come past that of six tiles
+    // before the last one when it had read the entry whose place the end's took.)
+    if (rank == 0)
+        for (int t = max(0, gt - 5); t < gt; ++t)
+            if (!wait_answering(sh, &sh.pv_done[t & 1], (uint32_t)(t >> 1) & 1u, lane, abort)) return;
 }
 
 // The tile's entry, as a warp reads it; false: the wait gave up.
@@ -675,12 +718,6 @@ __device__ __noinline__ void load_role(Shared<kBf16>& sh, const Args& a, const C
             if (++slot == places) slot = 0, phase ^= 1u;
         }
         if (i < 4) break;
-        if (!keys && rank == 0 && !(flags & Info::kSeen)) {  // the odd CTA's softmax may have to know (finite_values)
-            const int of = g - 4 + (lane & 3);
-            if (!wait(&full[of % places], (uint32_t)((of / places) & 1), abort)) break;
-            if (lane == 0) st_cluster(mapa_shared(smem_u32(&sh.value_here), 1), gt + 1);
-            __syncwarp();
-        }
     }
     // Whatever ended the loop, no copy outlives the pair, which ends together. (Where a wait has given
     // up, the even CTA may have armed less than the odd one has asked for: a copy takes a microsecond.)
@@ -925,8 +962,10 @@ __device__ __noinline__ bool finite_values(Shared<kBf16>& sh, uint32_t which, in
     // The tile's V has landed (once PV of the tile before has used what the places held, the phase that
     // their barriers are in is this tile's).
     if (gt > 0 && !wait(&sh.pv_done[(gt - 1) & 1], (uint32_t)((gt - 1) >> 1) & 1u, abort)) return false;
-    if (rank) {  // (a count, as not every tile's is waited for)
+    if (rank) {  // (asked again and again: what another warp has asked for the tile before may come late)
+        const uint32_t asked = mapa_shared(smem_u32(&sh.value_asked), 0);
         for (uint32_t i = 0; __any_sync(0xffffffffu, ld_acquire_cluster(smem_u32(&sh.value_here)) <= gt); ++i) {
+            if (lane == 0 && i % 64 == 0) st_release_cluster(asked, gt + 1);
             if (i < kSpinLimit && !__any_sync(0xffffffffu, *abort)) continue;
             *abort = 1;
             return false;
@@ -1270,7 +1309,7 @@ k_paged_shared(const __grid_constant__ Args a, const __grid_constant__ CUtensorM
             mbar_init(&sh.sum_bar[i], 4);
         }
         mbar_init(&sh.q_empty, 1);
-        sh.value_here = 0;
+        sh.value_asked = sh.value_told = sh.value_here = 0;
         mbar_init(&sh.drain, 2);
         sh.abort = 0;
         fence_mbar_init();

@@ -202,10 +202,15 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
 __device__ __forceinline__ void mbar_arrive_peer(uint32_t cluster_addr) {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];\n" ::"r"(cluster_addr) : "memory");
 }
-// A word of another CTA's shared memory (cluster address), and this CTA's one that another has written. The
-// store tells of what a bulk copy has put there, so it need not wait for this thread's own.
-__device__ __forceinline__ void st_cluster(uint32_t cluster_addr, int v) {
-    asm volatile("st.relaxed.cluster.shared::cluster.s32 [%0], %1;\n" ::"r"(cluster_addr), "r"(v) : "memory");
+// A word of another CTA's shared memory (cluster address), behind what this thread knows of memory (which takes 800
+// to 1,000 cycles); and this CTA's one that another has written.
+__device__ __forceinline__ void st_release_cluster(uint32_t cluster_addr, int v) {
+    asm volatile("st.release.cluster.shared::cluster.s32 [%0], %1;\n" ::"r"(cluster_addr), "r"(v) : "memory");
+}
+__device__ __forceinline__ int ld_relaxed_cluster(uint32_t addr) {
+    int v;
+    asm volatile("ld.relaxed.cluster.shared::cta.s32 %0, [%1];\n" : "=r"(v) : "r"(addr) : "memory");
+    return v;
 }
 __device__ __forceinline__ int ld_acquire_cluster(uint32_t addr) {
     int v;
@@ -227,6 +232,11 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity
     for (uint32_t i = 0; i < kSpinLimit; ++i)
         if (mbar_try_wait_acq_cluster(bar, parity)) return true;
     return false;
+}
+// A phase that has completed, read once more so that what other CTAs' copies counted in it is ordered before
+// what this thread goes on to release.
+__device__ __forceinline__ bool acquire_phase_cluster(uint64_t* bar, uint32_t parity) {
+    return mbar_try_wait_acq_cluster(bar, parity);
 }
 // Every thread of every CTA of the cluster (all must arrive: no thread may leave
 // before it). Used once, right after the CTAs initialise their mbarriers.

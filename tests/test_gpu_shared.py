@@ -538,6 +538,34 @@ def test_attention_keeps_what_a_sequence_does_not_see_from_it(kv, heads, members
 
 
 @BOTH
+@pytest.mark.parametrize("heads,ctas", [(64, 2), (64, 0), (20, 2), (20, 6), (3, 4)])
+def test_attention_of_many_tiles_that_are_not_finite(kv, heads, ctas):
+    """Positions that are not finite in every tile of one sequence's own positions, first and last ones among them,
+    whichever CTA of the pair has its rows; then in every sequence's."""
+    T = [1700, 300, 900, 1290, 333, 257]
+    b = Batch(kv, heads, [(200, T)], 16, seed=81, mix=False)
+    b.p.max_ctas = ctas
+    clean, good = b.check(), b.c.pool.clone()
+    bits = b.c.pool.view(torch.int16 if kv == api.BF16 else torch.uint8)
+    def spoil(who):
+        at = torch.tensor(sorted({200, T[who] - 1, *range(230, T[who], 60)}), device=DEV)
+        bits[0, b.c.table[who].long()[at // 16], at % 16, 7 * who] = 0x7FC0 if kv == api.BF16 else 0x7F
+    for who in range(6):
+        spoil(who)
+        for _ in range(2):
+            out = b.run()
+            assert out[who].isnan().all()
+            others = [i for i in range(6) if i != who]
+            assert torch.equal(out[others], clean[others])
+        b.c.pool.copy_(good)
+    for who in range(6):
+        spoil(who)
+    assert b.run().isnan().all()
+    b.c.pool.copy_(good)
+    assert torch.equal(b.run(), clean)
+
+
+@BOTH
 def test_attention_of_a_query_that_is_not_finite(kv):
     b = Batch(kv, 24, [(200, [210, 260, 200, 333, 201])], 16, seed=17, mix=False)
     clean = b.check()
