@@ -654,11 +654,9 @@ __device__ void plan_role(Shared<kBf16>& sh, const Args& a, int lane, int rank, 
         mbar_arrive(&sh.info_full[gt % kInfos]);
     }
     __syncwarp();
-    // To the last tile's PV there may be questions. (Every phase in turn: the softmax had come past that of six tiles
-    // before the last one when it had read the entry whose place the end's took.)
-    if (rank == 0)
-        for (int t = max(0, gt - 5); t < gt; ++t)
-            if (!wait_answering(sh, &sh.pv_done[t & 1], (uint32_t)(t >> 1) & 1u, lane, abort)) return;
+    // Up to the last tile's PV there may be questions. (A barrier of one phase: those of pv_done go on while this warp
+    // is still busy with the last tiles' entries, and a phase that is two ahead reads as not complete.)
+    if (rank == 0) wait_answering(sh, &sh.drain, 0, lane, abort);
 }
 
 // The tile's entry, as a warp reads it; false: the wait gave up.
