@@ -101,10 +101,25 @@ __device__ __forceinline__ int length_of(const Args& a, int64_t n, bool report) 
     return n < 0 ? 0 : (int)a.g.max_len();
 }
 
-// The slot where i's group begins.
+// The slot where the unit of slot i begins.
+__device__ __forceinline__ int unit_of(const Args& a, int i, int f) { return i - (i - f) % a.members; }
+
+// The slot where i's group begins. What `first` says of i holds if that slot begins a group and all slots of i's unit
+// before i say the same; else i is a group of its own. So a unit's slots stand together, whatever `first` holds.
 __device__ __forceinline__ int first_of(const Args& a, int i, bool report) {
     const int f = a.first[i];
-    if (f >= 0 && f <= i) return f;
+    bool holds = f >= 0 && f <= i;
+    if (holds && f < i) {
+        holds = a.first[f] == f;
+        constexpr int kLook = 8;  // a unit of 16 heads in one round trip
+        int j = unit_of(a, i, f);
+        do {
+#pragma unroll
+            for (int k = 0; k < kLook; ++k) holds &= a.first[min(j + k, i)] == f;
+            j += kLook;
+        } while (holds && j < i);
+    }
+    if (holds) return f;
     if (report) raise_status(a.dev_status, CSA2_DEV_BAD_INDEX);
     return i;
 }
@@ -122,9 +137,6 @@ __device__ __forceinline__ Slot slot_of(const Args& a, int i, bool report) {
     if (s.prow < 0 || s.prow == INT_MAX) s.sh = 0;  // no sequence to read them through
     return s;
 }
-
-// The slot where the unit of slot i begins.
-__device__ __forceinline__ int unit_of(const Args& a, int i, int f) { return i - (i - f) % a.members; }
 
 __device__ __forceinline__ int tiles_of(int n) { return n / kTile + (n % kTile != 0); }
 
@@ -171,10 +183,17 @@ __device__ __forceinline__ Slot slots_of(const Args& a, int lane, bool report) {
     int shared = 0;
     if (lane < a.B) {
         s.b = a.order[lane];
-        s.f = first_of(a, lane, report);
+        s.f = a.first[lane];
         shared = a.shared[lane];
         s.row = row_of(a, s.b, report);
     }
+    // first_of, by votes: no slot of the unit names another than the one before it
+    bool holds = s.f >= 0 && s.f <= lane;
+    const int u0 = holds ? unit_of(a, lane, s.f) : lane, named = __shfl_sync(0xffffffffu, s.f, holds ? s.f : lane);
+    const uint32_t other = __ballot_sync(0xffffffffu, s.f != __shfl_up_sync(0xffffffffu, s.f, 1));
+    holds &= named == s.f && !(other & ((2u << lane) - (2u << u0)));
+    if (!holds) s.f = lane;
+    if (!holds && report) raise_status(a.dev_status, CSA2_DEV_BAD_INDEX);
     s.prow = __shfl_sync(0xffffffffu, s.row, s.f);
     shared = __shfl_sync(0xffffffffu, shared, s.f);
     if (lane >= a.B) return s;
@@ -348,9 +367,10 @@ __device__ void plan(const Args& a, PlanShared& sh, PlanScratch& x, int pair) {
     __syncthreads();
 }
 
-// Slot i, which is not before the range's first unit.
+// Slot i, which is not before the range's first unit: a slot's unit begins in it or behind it (first_of).
+__device__ __noinline__ Slot slot_far(const Args& a, int i) { return slot_of(a, i, false); }
 __device__ __forceinline__ Slot slot_at(const Args& a, const PlanShared& plan, int i) {
-    return i - plan.base < kKept ? plan.slots[i - plan.base] : slot_of(a, i, false);
+    return (uint32_t)(i - plan.base) < (uint32_t)kKept ? plan.slots[i - plan.base] : slot_far(a, i);
 }
 
 // A range tile by tile.

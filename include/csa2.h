@@ -738,8 +738,10 @@ size_t csa2_paged_attn_shared_workspace_size(const csa2_params* p, const csa2_pa
  *   row of a page counts only through the logits: it makes the outputs that see it NaN, unless its
  *   logit is -infinity, which takes the row out. What sequences do not see does not reach them, NaN in
  *   another sequence's positions among it.
- *   A slot with first outside [0, i] counts as a group of its own, one with order outside [0, B) as
- *   padding (both CSA2_DEV_BAD_INDEX); a shared below 0 or beyond max_pages pages sets
+ *   A slot whose first is outside [0, i] or names a slot that begins no group counts as a group of its own,
+ *   as does one that other groups' slots cut off from those of its group that its rows would meet
+ *   positions with (up to 128 / heads sequences); one with order outside [0, B) as padding (all
+ *   CSA2_DEV_BAD_INDEX); a shared below 0 or beyond max_pages pages sets
  *   CSA2_DEV_BAD_LENGTH (none, or the first max_pages pages).
  *   workspace: csa2_paged_attn_shared_workspace_size bytes, 256-byte aligned, contents
  *   arbitrary; calls that share it must be ordered (one stream or events).

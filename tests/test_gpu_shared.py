@@ -671,6 +671,46 @@ def test_attention_flags_and_skips_what_is_out_of_range(kv):
     assert torch.equal(fresh().run(), base)
 
 
+def groups_that_hold(first, members):
+    """What csa2_paged_attn_shared makes of any `first`: the slot where each slot's group begins."""
+    out = []
+    for i, f in enumerate(first):
+        good = 0 <= f <= i and first[f] == f and all(first[j] == f for j in range(i - (i - f) % members, i))
+        out.append(f if good else i)
+    return out
+
+
+@BOTH
+@pytest.mark.parametrize("heads,B,ctas", [(64, 20, 0), (1, 32, 0), (1, 33, 4), (16, 90, 0), (5, 200, 6), (40, 600, 0)])
+def test_attention_of_groups_that_contradict_themselves(kv, heads, B, ctas):
+    """Any `first` at all: a slot whose group does not hold together is one of its own, and the others stand."""
+    rng = np.random.default_rng(B)
+    ps, wide = 16, 20
+    p = api.default_params(kv_format=kv, heads=heads)
+    p.max_ctas = ctas
+    c = api.PagedCache(p, 60, ps, 12, wide, device=DEV)
+    c.pool.copy_(randn(*c.pool.shape, seed=B).to(c.pool.dtype))
+    c.table.copy_(i32(rng.integers(0, 60, (12, wide))))
+    q, sink = randn(B, heads, D, seed=B + 1, dtype=torch.bfloat16), randn(heads, seed=B + 2)
+    slot = np.arange(B)
+    families = np.sort(rng.integers(0, B, B))
+    families = np.searchsorted(families, families)
+    two = slot % 2
+    wrong = families.copy()
+    wrong[rng.integers(0, B, 3)] = rng.integers(0, B, 3)
+    for n, first in enumerate([rng.integers(-1, slot + 2), np.append(slot[:-1], 0), families, two, wrong,
+                               np.where(slot < 2, slot, rng.integers(0, 2, B)), np.maximum(slot - 1, 0)]):
+        seq, T, order = rng.integers(0, 12, B), rng.integers(0, wide * ps + 1, B), rng.permutation(B)
+        shared, st = rng.integers(0, wide * ps + 1, B), status()
+        out = torch.empty_like(q)
+        api.paged_attn_shared(p, c, 0, q, sink, i32(seq), i32(T),
+                              api.PrefixGroups(order=i32(order), first=i32(first), shared=i32(shared)), out,
+                              api.paged_attn_shared_workspace(p, c, B), dev_status=st)
+        held = groups_that_hold(first.tolist(), 128 // heads)
+        assert st.item() == (held != first.tolist()), n
+        assert_attn(out, shared64(p, c, 0, q, sink, seq, T, order, held, shared), kv)
+
+
 @pytest.mark.parametrize("heads", [5, 64])
 def test_attention_e4m3_queries_of_a_wide_range(heads):
     """The query's two E4M3 parts: channels down to 2^-18 of a head's largest, heads from 2^-40 on."""
