@@ -1434,6 +1434,13 @@ struct JoinShared {
     float2 tops[kJoinGroups][kRows];
 };
 
+// Where row R of a partial result goes, -1: nowhere. Where a wait of the kernel before gave up, the workspace may hold
+// anything there.
+__device__ __forceinline__ int place_of(const Args& a, const float* part, int R) {
+    const int place = __float_as_int(__ldcg(part + kRows * (kD + 2) + R));
+    return (uint32_t)place < (uint32_t)(a.B * a.heads) ? place : -1;
+}
+
 __device__ __forceinline__ void join_item(const Args& a, JoinShared& sh, bool few, int unit, int item) {
     const int R = threadIdx.x & (kRows - 1), group = threadIdx.x / kRows;
     const int cg = few ? item : kJoinGroups * item + group, step = few ? kJoinGroups : 1, n = sh.pieces[unit];
@@ -1441,8 +1448,7 @@ __device__ __forceinline__ void join_item(const Args& a, JoinShared& sh, bool fe
     // slots of the pieces: the first, and two further on each time from the pair behind it
     const float* const first = part_of(a, 0, 0) + (int64_t)s0 * kPartFloats;
     const float* const rest = part_of(a, 0, 0) + (int64_t)(s0 & ~1u) * kPartFloats;
-    const int place = __float_as_int(__ldcg(first + kRows * (kD + 2) + R));
-    const int place_out = __float_as_int(__ldcg(first + kRows * (kD + 2) + (threadIdx.x >> 1 & (kRows - 1))));
+    const int place = place_of(a, first, R), place_out = place_of(a, first, threadIdx.x >> 1 & (kRows - 1));
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     float den = 0.f, M = -INFINITY;
     auto add = [&](float4 v, float m, float l) {  // under the maximum M of both

@@ -711,6 +711,23 @@ def test_attention_of_groups_that_contradict_themselves(kv, heads, B, ctas):
         assert_attn(out, shared64(p, c, 0, q, sink, seq, T, order, held, shared), kv)
 
 
+@BOTH
+@pytest.mark.parametrize("ctas", [0, 6])
+def test_attention_whatever_the_workspace_holds(kv, ctas):
+    """Words that look like outputs, sums or ends of ranges; what lies around the output stays."""
+    b = Batch(kv, 20, [(1500, [1600, 1501, 1500]), (200, [0, 333]), (0, [700, 1])], 16, seed=91)
+    b.p.max_ctas = ctas
+    base, n = b.check(), b.q.numel()
+    flat = torch.full((3 * n,), 9.0, dtype=torch.bfloat16, device=DEV)
+    out, ws = flat[n:2 * n].view(b.q.shape), api.paged_attn_shared_workspace(b.p, b.c, len(b.T))
+    words = ws[:ws.numel() // 4 * 4].view(torch.int32)
+    g = torch.Generator(device=DEV).manual_seed(92)
+    for lo, hi in ((-5, 200), (0, 8), (-2 ** 31, 2 ** 31 - 1), (0x7F800000, 0x7FC00001)):
+        words.random_(lo, hi, generator=g)
+        api.paged_attn_shared(b.p, b.c, 0, b.q, b.sink, i32(b.seq), i32(b.T), b.groups(), out, ws)
+        assert torch.equal(out, base) and torch.all(flat[:n] == 9) and torch.all(flat[2 * n:] == 9)
+
+
 @pytest.mark.parametrize("heads", [5, 64])
 def test_attention_e4m3_queries_of_a_wide_range(heads):
     """The query's two E4M3 parts: channels down to 2^-18 of a head's largest, heads from 2^-40 on."""

@@ -162,3 +162,14 @@ def test_waits_of_the_kernel_are_decided_by_the_warp():
     loop = code.split("bool wait_on(", 1)[1].split("\n}\n", 1)[0]
     returns = [line for line in loop.split("\n") if "*abort" in line and "return" in line]
     assert returns and all("__any_sync(0xffffffffu" in line for line in returns)
+
+
+def test_outputs_of_the_join_lie_in_the_batch():
+    """Rows of a partial result name their outputs in the workspace, which holds anything where a wait gave up before
+    they were stored. By the source: they are read in one place, which bounds them by the batch's rows."""
+    path = os.path.join(os.path.dirname(_lib.LIB_PATH), "csrc", "paged_shared.cu")
+    code = re.sub(r"//[^\n]*", "", open(path).read())
+    reads = [line for line in code.split("\n") if "kD + 2" in line and "__ldcg" in line]
+    place_of = code.split("int place_of(", 1)[1].split("\n}\n", 1)[0]
+    assert len(reads) == 1 and reads[0] in place_of
+    assert "(uint32_t)place < (uint32_t)(a.B * a.heads) ? place : -1" in place_of
