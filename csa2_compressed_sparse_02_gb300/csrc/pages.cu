@@ -410,13 +410,14 @@ k_slots_plan(Pages g, int B, const int32_t* seq, const int32_t* n_tokens, const 
     __syncthreads();
     const bool few = B <= kOffsets;
     int64_t* off = few ? off_s : ws.offset;
+    const int64_t most = min(g.max_len(), (int64_t)INT_MAX);  // lengths and positions are 32-bit
     int64_t rows = 0, entries = 0;
     for (int i0 = 0; i0 < B; i0 += kPlan) {
         const int i = i0 + tid, s = i0 == 0 ? s0 : i < B ? seq[i] : -1;
         const int64_t T = i0 == 0 ? T0 : i < B ? n_tokens[i] : 0, want = i0 == 0 ? new0 : i < B ? n_new[i] : 0;
         int64_t n = 0;
         if (s >= g.max_seqs || (s >= 0 && owner[s] != i)) raise_status(dev_status, CSA2_DEV_BAD_INDEX);
-        else if (s >= 0 && (T < 0 || want < 0 || T + want > g.max_len())) raise_status(dev_status, CSA2_DEV_BAD_LENGTH);
+        else if (s >= 0 && (T < 0 || want < 0 || T + want > most)) raise_status(dev_status, CSA2_DEV_BAD_LENGTH);
         else if (s >= 0) n = want;
         const int first = n > 0 ? (int)T / g.page_size : 0;
         int64_t at = n, before = n > 0 ? (uint32_t)(T + n - 1) / (uint32_t)g.page_size + 1u - first : 0, all_rows, all_pages;

@@ -586,7 +586,7 @@ int csa2_page_reserve(const csa2_params* p, const csa2_pages* c, int N, const in
  *   row_slot  [N] int64: its row in a layer of the pool, page * page_size + position % page_size; -1
  *             where there is no page, and behind the last row
  *   seq, n_tokens, n_new [B] int32, device. seq[i] < 0 is padding: no rows. A sequence past max_seqs or
- *   listed before sets CSA2_DEV_BAD_INDEX; a length below 0 or beyond max_pages pages
+ *   listed before sets CSA2_DEV_BAD_INDEX; a length below 0 or beyond max_pages pages (or 2^31 - 1)
  *   CSA2_DEV_BAD_LENGTH, as does the first request whose rows do not fit into N, and every one with rows
  *   behind it. Such a request has no rows and takes no pages, and its n_after is n_tokens[i].
  *   CSA2_DEV_NO_PAGE as in csa2_page_reserve. n_after may be n_tokens itself.

@@ -141,6 +141,32 @@ def test_slots_of_prompts(spare):
             assert np.array_equal(g, w)
 
 
+def test_slots_of_lengths_that_reach_31_bits():
+    """A table whose rows hold more positions than 31 bits: a request up to the last of those is served, one
+    that passes it is refused, and the ones around it stand."""
+    most, ps, wide = 2 ** 31 - 1, 1024, 2_100_000
+    p = api.default_params(kv_format=api.E4M3)
+    pool = torch.zeros(1, 8, ps, D, dtype=torch.int8, device=DEV).view(dtype_of(api.E4M3))
+    for held, new, bits in (([most - 3, 5, 70], [3, 2, 1], 0), ([most - 3, 5, 70], [4, 2, 1], 2),
+                            ([most - 47, 5, 70], [100, 2, 1], 2), ([most, 5, 70], [1, 2, 1], 2),
+                            ([most, 5, 70], [0, 2, 1], 0), ([7, 5, 70], [most, 2, 1], 2)):
+        c = api.PagedCache(p, pool=pool, table=torch.full((3, wide), -1, dtype=torch.int32, device=DEV),
+                           ref=torch.zeros(8, dtype=torch.int32, device=DEV))
+        out, st, taken = api.SlotMap(3, 8, device=DEV), status(), new[0] if not bits else 0
+        api.page_slots(p, c, i32([1, 0, 2]), i32(held), i32(new), out, st)
+        assert st.item() == bits
+        assert out.n_tokens.tolist() == [held[0] + taken, 7, 71] and out.start.tolist() == [0, taken, taken + 2, taken + 3]
+        rest = 8 - taken - 3
+        assert out.seq.tolist() == [1] * taken + [0, 0, 2] + [-1] * rest
+        assert out.pos.tolist() == [held[0] + r for r in range(taken)] + [5, 6, 70] + [-1] * rest
+        page = 1 if taken else 0  # the lowest free pages, in the order of the call
+        first = [(held[0] + r) % ps for r in range(taken)]
+        assert out.slot.tolist() == first + [page * ps + 5, page * ps + 6, (page + 1) * ps + 70] + [-1] * rest
+        assert int((c.table >= 0).sum()) == page + 2 == int(c.ref.sum())
+        if taken:
+            assert c.table[1, (most - 3) // ps].item() == 0
+
+
 def test_slots_without_requests_or_pages():
     table, ref = np.full((3, 4), -1), np.zeros(5, np.int64)
     none = np.zeros(0, np.int64)
