@@ -476,7 +476,8 @@ struct Shape {
     static constexpr float kLazyMax = kBf16 ? 8.f : 6.f;
     static constexpr float kLift = kBf16 ? 0.f : 9.f;
     // A row's maximum as its threads exchange it. In bf16, rounded up, where room is short: what it bounds
-    // need not be close, as bf16 weights are as exact at any scale.
+    // need not be close, as bf16 weights are as exact at any scale, as long as they are normal numbers. From
+    // 2^13 on, where a step is 64 and more, its other bits follow (exact_max).
     using Bound = std::conditional_t<kBf16, __nv_bfloat16, float>;
     // Tiles that add up in TMEM under one maximum (see csa2_paged_attn: of a long tail less than 2^-9
     // of the weight is lost); what came before is added in fp32.
@@ -1020,6 +1021,28 @@ __device__ __noinline__ bool finite_values(Shared<kBf16>& sh, uint32_t which, in
     return true;
 }
 
+// Whether a maximum that was rounded up to bf16 may be 64 or more above the logits that it stands for.
+__device__ __forceinline__ bool wide_step(float top) { return fabsf(top) >= 8192.f && top != -INFINITY; }
+
+// The rows' maxima to their last bits, of bf16 pages: of what is left of `mine`, this thread's own, below the rounded one
+// `top`, two more words of 8 bits each, which the row's threads exchange as they did the first. (Truncated: what is left
+// has one sign; beyond bf16's largest number it counts from that.) Two more phases of max_bar, from `met` on; a wait
+// that gives up has set *abort.
+__device__ __noinline__ float exact_max(Shared<true>& sh, float top, float mine, int met, int quarter, int grp, int r, int lane,
+                                        volatile int* abort) {
+    float have = top == INFINITY ? __uint_as_float(0x7f7f0000u) : top;
+#pragma unroll 1
+    for (int k = met; k < met + 2; ++k) {
+        sh.red_max[k & 1][quarter][r] = __float2bfloat16_rz(mine - have);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.max_bar[grp]);
+        if (!wait(&sh.max_bar[grp], (uint32_t)(k & 1), abort)) break;
+        const auto* four = sh.red_max[k & 1];
+        have += fmaxf(fmaxf((float)four[0][r], (float)four[1][r]), fmaxf((float)four[2][r], (float)four[3][r]));
+    }
+    return wide_step(top) && have == have ? have : top;  // (an infinity stays one)
+}
+
 // Warp (qd, ch): rows 32 (qd & 1) + lane of this CTA, positions 64 (qd >> 1) + 32 ch .. + 31 of the
 // tile: lane quarter qd of TMEM, whose upper half holds the same rows' other 64 positions. Logits
 // are in the log2 domain. A row's four threads agree on its maximum through shared memory; it is
@@ -1037,6 +1060,7 @@ __device__ void softmax_role(Shared<kBf16>& sh, const Args& a, uint32_t tmem, in
     const float2 c0 = make_float2(0.f, 0.f);
     Row row = {-1, 0, 0, 0};
     int runs = 0;
+    int met = 0;       // phases of max_bar so far
     bool last = true;  // the tile before was a run's last
     if (sh.plan.range.items > 0) {
         const int n = Stagers<kBf16>::kAll, w = S::kHelpWarps + warp;
@@ -1100,8 +1124,9 @@ __device__ void softmax_role(Shared<kBf16>& sh, const Args& a, uint32_t tmem, in
         float top = fmaxf(x[0].x, x[0].y);
 #pragma unroll
         for (int i = 1; i < 16; ++i) top = fmaxf(top, fmaxf(x[i].x, x[i].y));
-        if constexpr (kBf16) sh.red_max[gt & 1][quarter][r] = __float2bfloat16_ru(top);
-        else sh.red_max[gt & 1][quarter][r] = top;
+        const float mine = top;
+        if constexpr (kBf16) sh.red_max[met & 1][quarter][r] = __float2bfloat16_ru(top);
+        else sh.red_max[met & 1][quarter][r] = top;
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.max_bar[grp]);
         // P under the maximum so far, while the others' maxima are on their way; again in the few tiles
@@ -1128,11 +1153,20 @@ __device__ void softmax_role(Shared<kBf16>& sh, const Args& a, uint32_t tmem, in
                 }
             }
             if (known) break;
-            if (!wait(&sh.max_bar[grp], (uint32_t)(gt & 1), abort)) return;
+            if (!wait(&sh.max_bar[grp], (uint32_t)(met & 1), abort)) return;
             known = true;
-            const auto* four = sh.red_max[gt & 1];
+            const auto* four = sh.red_max[met & 1];
+            ++met;
             top = fmaxf(fmaxf((float)four[0][r], (float)four[1][r]), fmaxf((float)four[2][r], (float)four[3][r]));
-            const bool move = fresh || top > m + S::kLazyMax;
+            bool move = fresh || top > m + S::kLazyMax;
+            if constexpr (kBf16) {  // (all four warps of these rows decide alike)
+                if (__any_sync(0xffffffffu, move && wide_step(top))) {
+                    top = exact_max(sh, top, mine, met, quarter, grp, r, lane, abort);
+                    if (__any_sync(0xffffffffu, *abort)) return;
+                    met += 2;
+                    move = fresh || top > m + S::kLazyMax;
+                }
+            }
             if (!__any_sync(0xffffffffu, move)) break;
             if (move) {
                 if (m != -INFINITY) alpha = ex2(m - top);

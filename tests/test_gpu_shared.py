@@ -517,6 +517,80 @@ def test_attention_sinks_and_large_logits(kv):
 
 
 @BOTH
+@pytest.mark.parametrize("ctas,families", [
+    (2, [(300, [301, 420])]), (0, [(300, [301, 420])]), (0, [(1500, [1500, 1600, 1501])] * 2 + [(0, [700])]),
+    (8, [(1500, [1500, 1600, 1501])] * 2 + [(0, [700])])])
+@pytest.mark.parametrize("sink", [False, True])
+def test_attention_of_logits_far_from_zero(kv, ctas, families, sink):
+    """Maxima from 0 to +-1e5 and beyond, heads of every size in one unit, in whole and in cut units. Products of
+    whole numbers, so that the logits are exact but for their rounding to 32 bits: 2^-24 of the largest, twice in the
+    ratio of two weights (of a weight and the sink's: as much again)."""
+    b = Batch(kv, 64, families, 64, seed=61)
+    b.p.max_ctas = ctas
+    hold = ~torch.isnan(b.c.pool.float()[0, :, :, 0])
+    g = torch.Generator(device=DEV).manual_seed(62)
+    whole = lambda lo, hi, *shape: torch.randint(lo, hi + 1, shape, generator=g, device=DEV).float()
+    rows = b.c.pool[0].float()
+    n = int(hold.sum())
+    some = torch.where(torch.rand(n, generator=g, device=DEV) < 0.1, 64.0, 60.0)  # the maximum moves to these
+    rows[hold] = torch.cat([some[:, None], whole(-4, 4, n, 4), rows[hold][:, 5:]], 1)
+    b.c.pool[0] = rows.to(b.c.pool.dtype)
+    b.p.softmax_scale = 0.125
+    size = torch.tensor([0, 1, 7, 33, 128, 182, 200, 256, 320, 480, 500, 800, 1000, 1600, 2944, 4000, 5120, 8128, 8256 - 64,
+                         10240, 12800, 11392 // 2, 64 * 177 // 2, 13056, 6016, 9984, 15104, 16128, 3008, 2000, 240, 60], device=DEV)
+    q = torch.zeros_like(b.q, dtype=torch.float32)
+    q[..., 0] = torch.cat([size, -size]).bfloat16().float()
+    q[..., 1:5] = whole(-1, 1, *q.shape[:2], 4)
+    b.q = q.bfloat16()
+    if sink:
+        top = torch.where(q[0, :, 0] > 0, 64 * q[0, :, 0], 60 * q[0, :, 0]) / 8
+        b.sink = top + randn(64, seed=63)
+    else:
+        b.sink = None
+    st = status()
+    out = torch.full(b.q.shape, 9.0, dtype=torch.bfloat16, device=DEV)
+    api.paged_attn_shared(b.p, b.c, 0, b.q, b.sink, i32(b.seq), i32(b.T), b.groups(), out,
+                          api.paged_attn_shared_workspace(b.p, b.c, len(b.T)), dev_status=st)
+    assert st.item() == 0
+    o, A, _, F = shared64(b.p, b.c, 0, b.q, b.sink, b.seq, b.T, b.order, b.first, b.shared)
+    z = (b.q[0, :, 0].double().abs() * 64 + 16).cpu().numpy()[:, None] / 8  # no logit of the head is larger
+    u = 2.0 ** -8 if kv == api.BF16 else 2.0 ** -11
+    # as assert_attn has it, with each head's own logits; those in the log2 domain are 1.45 times as large, and what
+    # is rounded there weighs 0.7 of it here: 1.01 x 2^-24 z, for a weight and for the largest
+    tol = 2.0 ** -8 * np.abs(o) + (2 * u + 4.1 * 2.0 ** -24 * z + 2.0 ** -20) * A + 2.0 ** -26 * F + 2.0 ** -109
+    over = np.abs(out.double().cpu().numpy() - o) - tol
+    assert over.max() <= 0, (over.max(), np.argwhere(over.max((0, 2)) > 0).ravel())
+
+
+@BOTH
+@pytest.mark.parametrize("ctas", [2, 0])
+def test_attention_of_the_largest_logits(kv, ctas):
+    """Logits up to 32 bits' end, of either sign, and halves of them: the outputs are the means of the rows whose
+    logit is the largest, each with the same weight."""
+    b = Batch(kv, 20, [(700, [700, 760, 701]), (0, [300])], 16, seed=65)
+    b.p.max_ctas, b.p.softmax_scale = ctas, math.log(2)
+    hold = ~torch.isnan(b.c.pool.float()[0, :, :, 0])
+    rows = b.c.pool[0].float()
+    rows[..., 0] = torch.where(torch.rand(hold.shape, generator=torch.Generator(device=DEV).manual_seed(66), device=DEV) < 0.5, 1.0, 0.5)
+    rows[~hold] = float("nan")
+    b.c.pool[0] = rows.to(b.c.pool.dtype)
+    size = torch.tensor([torch.finfo(torch.bfloat16).max, 1e38, 1e37, 1e30, 1e20, 1e10, 1e7, 1e6, 2.0 ** 17, 2.0 ** 14], device=DEV)
+    b.q = torch.zeros_like(b.q)
+    b.q[..., 0] = torch.cat([size, -size]).bfloat16()
+    out = b.run(sink=False).double().cpu().numpy()
+    pool, table = b.c.pool[0].double().cpu().numpy(), b.c.table.cpu().numpy()
+    u = 2.0 ** -8 if kv == api.BF16 else 2.0 ** -11
+    for i, s in enumerate(b.order):
+        lead = b.order[b.first[i]]
+        t = np.arange(b.T[s])
+        k = pool[table[np.where(t < b.shared[i], b.seq[lead], b.seq[s]), t // 16], t % 16]
+        for sign, heads in ((1, slice(0, 10)), (-1, slice(10, 20))):
+            v = k[k[:, 0] == (1.0 if sign > 0 else 0.5)]
+            o, A = v.mean(0), np.abs(v).mean(0)
+            assert (np.abs(out[s, heads] - o) <= 2.0 ** -8 * np.abs(o) + (2 * u + 2.0 ** -20) * A).all()
+
+
+@BOTH
 @pytest.mark.parametrize("scale", [1.0, -1.0])
 def test_attention_rising_logits_rescale(kv, scale):
     """Later tiles outweigh earlier ones by more each time, so every tile moves the maximum, in some
