@@ -1486,7 +1486,7 @@ __device__ __forceinline__ void join_item(const Args& a, JoinShared& sh, bool fe
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     float den = 0.f, M = -INFINITY;
     auto add = [&](float4 v, float m, float l) {  // under the maximum M of both
-        if (m == -INFINITY) return;               // (nothing, or nothing seen)
+        if (m == -INFINITY && l == 0.f) return;   // (nothing, or nothing seen; a sum of NaN is from logits that are)
         const float w = ex2(m - M);
         den = fmaf(l, w, den);
         acc = make_float4(fmaf(v.x, w, acc.x), fmaf(v.y, w, acc.y), fmaf(v.z, w, acc.z), fmaf(v.w, w, acc.w));

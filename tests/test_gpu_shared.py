@@ -666,6 +666,23 @@ def test_attention_of_many_tiles_that_are_not_finite(kv, heads, ctas):
 
 
 @BOTH
+@pytest.mark.parametrize("families", [1, 5])
+@pytest.mark.parametrize("ctas", [2, 4, 6, 30, 0])
+def test_attention_of_a_piece_without_a_finite_logit(kv, families, ctas):
+    """A sequence's only own position is NaN, in a tile by itself, which may be a piece by itself: its output is
+    NaN wherever the unit is cut, and the others' are what they were."""
+    b = Batch(kv, 64, [(640, [641, 700, 640])] * families, 64, seed=71, mix=False)
+    b.p.max_ctas = ctas
+    clean = b.check()
+    for who in range(0, 3 * families, 3):
+        page = b.c.table[who, 10].item()
+        b.c.pool[0, page, 0].view(torch.int16 if kv == api.BF16 else torch.uint8)[3] = 0x7FC0 if kv == api.BF16 else 0x7F
+    out = b.run()
+    bad = torch.arange(3 * families, device=DEV) % 3 == 0
+    assert out[bad].isnan().all() and torch.equal(out[~bad], clean[~bad])
+
+
+@BOTH
 def test_attention_of_a_query_that_is_not_finite(kv):
     b = Batch(kv, 24, [(200, [210, 260, 200, 333, 201])], 16, seed=17, mix=False)
     clean = b.check()
