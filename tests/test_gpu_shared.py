@@ -682,6 +682,32 @@ def test_attention_of_a_piece_without_a_finite_logit(kv, families, ctas):
     assert out[bad].isnan().all() and torch.equal(out[~bad], clean[~bad])
 
 
+@pytest.mark.parametrize("ctas", [2, 0])
+@pytest.mark.parametrize("heads", [64, 20, 1])
+@pytest.mark.parametrize("bad", [float("inf"), -float("inf")])
+@pytest.mark.parametrize("at", [40, 255, 300])
+def test_attention_of_an_infinity_that_all_rows_see(heads, ctas, bad, at):
+    """An infinity in a tile that every row of the unit sees (a shared one, or a sequence's by itself): a logit
+    of -infinity takes the position out, as in the other tiles, any other is NaN."""
+    for families in ([(384, [390, 400, 384])], [(0, [700])]):
+        b = Batch(api.BF16, heads, families, 16, seed=heads + at, mix=False)
+        b.p.max_ctas = ctas
+        clean, ref = b.check(), b.ref()
+        row = b.c.pool[0, b.c.table[0, at // 16].item(), at % 16]
+        was = row[300].item()
+        row[300] = bad
+        out = b.run().float()
+        down = (b.q[:, :, 300].float() * bad) < 0
+        assert out[~down].isnan().all()
+        row[300] = 1e30 if bad > 0 else -1e30  # weights of the heads with `down`: 0, so finite, and taken out in the definition
+        o, A, _, F = b.ref()
+        keep = down.cpu().numpy()
+        assert out[down].isfinite().all()
+        assert_attn(out[down], (o[keep], A[keep], ref[2], 0.0), api.BF16)
+        row[300] = was
+        assert torch.equal(b.run(), clean)
+
+
 @BOTH
 def test_attention_of_a_query_that_is_not_finite(kv):
     b = Batch(kv, 24, [(200, [210, 260, 200, 333, 201])], 16, seed=17, mix=False)
