@@ -419,7 +419,7 @@ def prefix_groups(params, cache, seq, n_tokens, groups, least=1, dev_status=None
 
 
 def paged_attn_shared_workspace(params, cache, B):
-    """Workspace tensor of paged_attn_shared, for batches of any size."""
+    """Workspace tensor of paged_attn_shared for batches of up to B sequences."""
     if cache.index < 0:
         _fail("expected a CUDA tensor")
     with torch.cuda.device(cache.index):

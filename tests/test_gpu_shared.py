@@ -1051,3 +1051,17 @@ def test_calls_name_what_they_refuse():
         api.prefix_groups(b.p, b.c, seq, T, b.groups(), least=0)
     with pytest.raises(api.Csa2Error, match="is on cpu"):
         api.page_slots(b.p, b.c, seq, T, T, api.SlotMap(2, 8, device="cpu"))
+
+
+@BOTH
+def test_a_workspace_is_for_batches_of_up_to_its_size(kv):
+    """A workspace for fewer sequences is refused where it is smaller (E4M3 pages: the queries' parts lie there), one for
+    more is not."""
+    b = Batch(kv, 64, [(100, [130, 101, 128]), (0, [60])], 16, seed=95)
+    out = b.check(ws=api.paged_attn_shared_workspace(b.p, b.c, 40))
+    small = api.paged_attn_shared_workspace(b.p, b.c, 3)
+    if kv == api.E4M3:
+        with pytest.raises(api.Csa2Error, match="workspace smaller"):
+            b.run(ws=small)
+    else:
+        assert torch.equal(b.run(ws=small), out)
