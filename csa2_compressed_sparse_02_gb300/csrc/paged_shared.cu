@@ -594,7 +594,7 @@ __device__ void plan_role(Shared<kBf16>& sh, const Args& a, int lane, int rank, 
     };
     auto look = [&](const Tile& t) {
         Box b = {-1, -1};
-        if (pos < kTile && t.t0 + pos < t.hi && t.t0 + pos + br > t.lo) {
+        if (pos < kTile && t.t0 + pos < t.hi && t.t0 + pos + (br - 1) >= t.lo) {  // (positions end at 2^31 - 2)
             b.nth = (int)((uint32_t)(t.t0 + pos) / (uint32_t)ps);
             b.page = t.row < 0 ? -1 : a.g.table[(int64_t)t.row * a.g.max_pages + b.nth];
         }
@@ -634,7 +634,7 @@ __device__ void plan_role(Shared<kBf16>& sh, const Args& a, int lane, int rank, 
         const bool seen = (cur.k < 0 || alone) && cur.lo <= cur.t0 && min(cur.hi, reach) - cur.t0 >= kTile &&
                           __all_sync(0xffffffffu, there || pos >= kTile);
         Info& o = sh.info[gt % kInfos];
-        if (pos < kTile) o.y[lane] = there ? box.page * ps + cur.t0 + pos - box.nth * ps : a.g.n_pages * ps;
+        if (pos < kTile) o.y[lane] = there ? box.page * ps + (cur.t0 + pos - box.nth * ps) : a.g.n_pages * ps;
         if (lane < 4) {
             uint32_t ok = 0;
 #pragma unroll

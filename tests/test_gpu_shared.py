@@ -921,6 +921,35 @@ def test_attention_long_tails(kv, drop):
     assert ((out.double() - o).abs() <= tol + 2.0 ** -8 * (o.abs() + tol)).all()
 
 
+@BOTH
+def test_attention_of_the_longest_sequence(kv):
+    """2^31 - 1 positions, all but the last 1,023 of them the same page, whose weights are 2^-64 of the others' (2^-33 in
+    all): the outputs are the mean of those, up to the last box of rows."""
+    T, ps, heads = 2 ** 31 - 1, 1024, 8
+    p = api.default_params(kv_format=kv, heads=heads)
+    p.softmax_scale = math.log(2) / 64
+    table = torch.zeros(1, -(-T // ps), dtype=torch.int32, device=DEV)
+    table[0, -1] = 1
+    rows = randn(2, ps, D, seed=97)
+    rows[0, :, 0], rows[1, :, 0] = -16, 0
+    rows[1, :, 5] = 0
+    rows[1, 960:, 5] = 16
+    rows[1, 1023] = float("nan")
+    c = api.PagedCache(p, pool=rows.to(dtype_of(kv))[None].contiguous(), table=table, ref=i32([T // ps, 1]))
+    q = torch.zeros(1, heads, D, dtype=torch.bfloat16, device=DEV)
+    q[..., 0] = 256
+    out, st, groups = torch.empty_like(q), status(), api.PrefixGroups(1, device=DEV)
+    api.prefix_groups(p, c, None, i32([T]), groups, dev_status=st)
+    assert groups.shared.tolist() == [0]
+    api.paged_attn_shared(p, c, 0, q, None, None, i32([T]), groups, out, api.paged_attn_shared_workspace(p, c, 1), dev_status=st)
+    assert st.item() == 0
+    v = c.pool[0, 1, :1023].double()
+    # the largest weights are alike, and added up in 64 steps that lose 2^-24 each at most; the others' share is 2^31 x
+    # 2^-64 / 1,023, of values of 16 at most
+    o, A = v.mean(0), v.abs().mean(0)
+    assert ((out.double() - o).abs() <= 2.0 ** -8 * o.abs() + 2.0 ** -17 * A + 2.0 ** -38).all()
+
+
 def test_offsets_past_32_bits():
     """Shared pages beyond 4 GB of a pool, in its second layer."""
     n_pages, ps = 70_001, 64
