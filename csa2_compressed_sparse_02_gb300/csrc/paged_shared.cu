@@ -964,12 +964,22 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
         : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
     return r;
 }
+// Zero if all logits are finite, else NaN.
+__device__ __forceinline__ float all_finite(const float2 (&x)[16]) {
+    float2 t[2] = {};
+#pragma unroll
+    for (int i = 0; i < 16; ++i) t[i & 1] = fma2(x[i], make_float2(0.f, 0.f), t[i & 1]);
+    return (t[0].x + t[0].y) + (t[1].x + t[1].y);
+}
 // The positions that are not finite in all rows of the warp, as what is not finite in a row of a page makes them (0 x
 // infinity is NaN); a query's own NaN does not.
-__device__ __forceinline__ uint32_t not_finite(const uint32_t (&sv)[32]) {
+__device__ __forceinline__ uint32_t not_finite(const float2 (&x)[16]) {
     uint32_t which = 0;
 #pragma unroll
-    for (int i = 0; i < 32; ++i) which |= (uint32_t)((sv[i] & 0x7f800000u) == 0x7f800000u) << i;
+    for (int i = 0; i < 16; ++i) {
+        which |= (uint32_t)((__float_as_uint(x[i].x) & 0x7f800000u) == 0x7f800000u) << (2 * i);
+        which |= (uint32_t)((__float_as_uint(x[i].y) & 0x7f800000u) == 0x7f800000u) << (2 * i + 1);
+    }
     return __reduce_and_sync(0xffffffffu, which);
 }
 
@@ -1108,17 +1118,14 @@ __device__ void softmax_role(Shared<kBf16>& sh, const Args& a, uint32_t tmem, in
 #pragma unroll
         for (int i = 0; i < 16; ++i)
             x[i] = mul2(make_float2(__uint_as_float(sv[2 * i]), __uint_as_float(sv[2 * i + 1])), make_float2(c, c));
-        // Positions whose products are not finite, where a row may take nothing from them: it does not see them, or
-        // (of bf16 pages) its logit is -infinity. (1 % of a long bf16 batch's time, 288 to 291 us. Such a tile waits for
-        // its values first: 24 sequences behind 65,536, of which one's 64 queries are NaN, 880 us instead of 145.)
+        // Positions whose logits are not finite, where a row may take nothing from them: it does not see them, or (of
+        // bf16 pages) its logit is -infinity. (1 to 2 % of a bf16 batch's time: 24 behind 131,072 287 to 290 us, 128 of
+        // 16 heads behind 32,768 115 to 117. Such a tile waits for its values first: 24 sequences behind 65,536, of which one's 64
+        // queries are NaN, 880 us instead of 145.)
         uint32_t which = 0;
-        if (kBf16 || !(flags & Info::kSeen)) {
-            float2 t = c0;  // (a NaN as soon as one is not finite)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) t = fma2(x[i], c0, t);
-            if (__any_sync(0xffffffffu, t.x + t.y != 0.f)) which = not_finite(sv);
-        }
+        float off = 0.f;  // not zero: such a position is in a tile that every row sees
         if (!(flags & Info::kSeen)) {
+            if (__any_sync(0xffffffffu, all_finite(x) != 0.f)) which = not_finite(x);
             if (!__all_sync(0xffffffffu, seen == ~0u)) {
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
@@ -1135,6 +1142,8 @@ __device__ void softmax_role(Shared<kBf16>& sh, const Args& a, uint32_t tmem, in
         else sh.red_max[met & 1][quarter][r] = top;
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.max_bar[grp]);
+        if constexpr (kBf16)
+            if (flags & Info::kSeen) off = all_finite(x);
         // P under the maximum so far, while the others' maxima are on their way; again in the few tiles
         // where the maximum moves. Rounded; the sum takes the values that the product multiplies.
         uint32_t w[16], part[kBf16 ? 1 : 3][8];
@@ -1180,6 +1189,8 @@ __device__ void softmax_role(Shared<kBf16>& sh, const Args& a, uint32_t tmem, in
             }
             fresh = false;
         }
+        if constexpr (kBf16)
+            if (__any_sync(0xffffffffu, off != 0.f)) which = not_finite(x);
         if constexpr (!kBf16) {
             // A NaN loses itself in the first two parts' rounding and stays what is left of them, so the
             // last part holds it. What that one leaves out is at most half its step, and what it leaves of
