@@ -19,13 +19,14 @@
 // 64 rows (64 KB) leaves shared memory for the rings.
 //
 // What bounds it. A tile's products take 2,048 cycles of the tensor pipe in bf16; in E4M3, whose S takes two
-// products and PV three at twice the rate, 2,560. E4M3: a tile in 2,900 to 3,300 cycles, the pipe busy 88 % of the
-// time (24 sequences of 64 heads behind 262,144 positions: 559 us). bf16: the copies, 128 KB a tile and CTA, which by
-// themselves reach 57 bytes a cycle (2,300 cycles), through rings of half a tile. A tile takes 2,400 where all pairs
-// read the same rows at a time (76 units of 152 sequences behind 16,384), 2,850 where a few of them do (24 behind
-// 131,072: 272 us, 1,510 TFLOP/s), 3,060 where each is at a place of its own. (S of two tiles as one product with N =
-// 256 reads Q half as often, but needs the keys of both at a time: 305 us against 295.) Around the tiles: 11,000
-// cycles until the first S, 6,000 at the end of a unit, and a join of 6 to 13 us.
+// products and PV three at twice the rate, 2,560. E4M3: the pipe is busy 90 % of the time (24 sequences of 64 heads
+// behind 262,144 positions: 528 us cold, 539 in short bursts). bf16: the copies, 128 KB a tile and CTA, which by
+// themselves reach 57 bytes a cycle (2,300 cycles), through rings of half a tile; the pipe is busy 71 % of the time where
+// few pairs read the same rows at a time (24 behind 131,072: 252 us cold, 264 in short bursts, 1,560 TFLOP/s), so a tile
+// takes 2,770 cycles there, and 2,450 where all do (152 behind 16,384: 186 us). Passes in a queue are 5 to 15 % slower, at
+// the power limit. (S of two tiles as one product with N = 256 reads Q half as often, but needs the keys of both at a
+// time: 305 us against 295.) Around the tiles: 11,000 cycles until the first S, 6,000 at the end of a unit, and a join of
+// 6 to 13 us.
 #include <climits>
 #include <type_traits>
 
